@@ -433,6 +433,122 @@ int mla_block_table_from_pages(const int32_t* req_to_page, int64_t pool_rows, in
                                const int32_t* req_pool_indices, int batch, int32_t* block_table,
                                int max_blocks, void* stream);
 
+/* ---- FP8 layer operators (the steps between the hidden state and the decode) ----
+ *
+ * What a layer does around the calls above: the norm before its projections,
+ * the quantisation of their inputs, and the projections and expert products
+ * themselves with e4m3 operands.  (No counterpart on the serving pages, whose
+ * layers run outside them; this library's own addition.)  Every call is one
+ * launch, asynchronous on `stream`, allocates nothing, needs no workspace and
+ * may be captured in a CUDA graph.
+ *
+ * Shared conventions.
+ *   - Matrices are row-major with a row stride in elements (>= the row's
+ *     width), so a slice of a wider row is passed as it is.  Offsets are
+ *     64-bit.
+ *   - A block is 128 consecutive columns, the last one of a row possibly
+ *     shorter.  An e4m3 matrix [rows, cols] has one fp32 scale per row and
+ *     block, stored block-major: scales[block * scale_stride + row],
+ *     scale_stride >= rows.  The values are code * scale.
+ *   - The quantiser: s = max(amax, 1e-10) / 448 with amax the largest |v| of
+ *     the block, code = e4m3(v * (1 / s)), rounded to nearest even; v is the
+ *     unrounded fp32 value.  A NaN in a block makes its scale and its codes
+ *     NaN; an infinity makes the scale infinite, its own code NaN and the
+ *     finite codes 0.
+ *   - num_tokens may be 0: nothing is launched and no pointer is looked at.
+ *   - Outputs must not overlap inputs, except where stated.
+ */
+#define MLA_OUT_BF16 0
+#define MLA_OUT_E4M3 1
+#define MLA_OUT_FP32 2
+#define MLA_ACT_NONE 0
+#define MLA_ACT_SILU_MUL 1
+#define MLA_NORM_MAX_DIM 32768
+#define MLA_GEMM_MAX_EXPERTS 1024
+
+/*
+ * Root-mean-square norm of each row, with the residual's addition before it:
+ *   h = x + residual_in (fp32; h = x without a residual)
+ *   residual_out = h, rounded to the residual's type
+ *   y = h * 1 / sqrt(mean(h^2) + eps) * weight, from the unrounded h
+ *
+ *   x             device bf16 [num_tokens, dim], row stride x_stride.
+ *   residual_in, residual_out
+ *                 device [num_tokens, dim] of residual_dtype (MLA_OUT_BF16 or
+ *                 MLA_OUT_FP32), both with row stride residual_stride; both
+ *                 NULL = no residual.  They may be the same array.
+ *   weight        device bf16 [dim].
+ *   dim           1 .. MLA_NORM_MAX_DIM.
+ *   eps           finite, >= 0.
+ *   y             device [num_tokens, dim], row stride y_stride: bf16
+ *                 (MLA_OUT_BF16) or quantised e4m3 (MLA_OUT_E4M3).
+ *   y_scales      MLA_OUT_E4M3: device fp32 [ceil(dim / 128)][scale_stride];
+ *                 unused (may be NULL) for bf16.
+ * Sums of squares are fp32 (a row holding |h| beyond 1.8e19 overflows them and
+ * normalises to 0).  Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
+ */
+int mla_add_rmsnorm(const void* x, int64_t x_stride, const void* residual_in, void* residual_out, int residual_dtype,
+                    int64_t residual_stride, const void* weight, int num_tokens, int dim, float eps, void* y,
+                    int y_dtype, int64_t y_stride, float* y_scales, int64_t scale_stride, void* stream);
+
+/*
+ * Quantisation of activations, with or without the gated unit before it:
+ *   MLA_ACT_NONE      v = x                        x bf16 [num_tokens, dim]
+ *   MLA_ACT_SILU_MUL  v = g / (1 + e^-g) * u       x bf16 [num_tokens, 2 dim] = [g | u]
+ * y, y_dtype, y_stride, y_scales and scale_stride as in mla_add_rmsnorm;
+ * MLA_OUT_BF16 only with MLA_ACT_SILU_MUL.  dim >= 1.
+ * Errors: MLA_ERR_ARG (also when num_tokens * ceil(dim / 128) exceeds
+ * 2^31 - 1), MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
+ */
+int mla_act_quantize(const void* x, int64_t x_stride, int act, int num_tokens, int dim, void* y, int y_dtype,
+                     int64_t y_stride, float* y_scales, int64_t scale_stride, void* stream);
+
+/*
+ * Matrix product of e4m3 operands with a scale for each block of 128:
+ *   out[m][n] = sum_b a_scales[b][m] * w_scales[n / 128][b]
+ *                     * sum_{k in block b} a[m][k] * w[n][k]
+ *
+ *   a             device e4m3 [num_tokens, k], row stride lda (bytes), as
+ *                 mla_add_rmsnorm and mla_act_quantize write it; a_scales fp32
+ *                 [ceil(k / 128)][a_scale_stride].
+ *   w             device e4m3 [n, k], row stride ldw; w_scales device fp32
+ *                 [ceil(n / 128)][ceil(k / 128)], contiguous: one scale for
+ *                 each 128 x 128 block.
+ *   n, k          n >= 1; k >= 16 and a multiple of 16, as are lda and ldw; a
+ *                 and w 16-byte aligned (the copy engine's rules).
+ *   out           device bf16 (MLA_OUT_BF16) or fp32 (MLA_OUT_FP32)
+ *                 [num_tokens, n], row stride ldo.
+ * Each 128-wide block is summed on the tensor cores into fp32, scaled in fp32
+ * and added in fp32; bf16 results are rounded once.  The order of every sum is
+ * fixed by the sizes: the same call gives the same bits.  NaN and infinite
+ * operands or scales reach the results that use them and no other.
+ * Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
+ */
+int mla_gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a_scale_stride, const void* w,
+                 int64_t ldw, const float* w_scales, int num_tokens, int n, int k, void* out, int out_dtype,
+                 int64_t ldo, void* stream);
+
+/*
+ * The same product grouped by expert: rows expert_offsets[e] ..
+ * expert_offsets[e+1] - 1 of a and out (a batch sorted by expert) use the
+ * weights of expert e.
+ *
+ *   w             device e4m3 [num_experts, n, k], every row at stride ldw
+ *                 (expert e starts at row e * n); w_scales fp32
+ *                 [num_experts][ceil(n / 128)][ceil(k / 128)].
+ *   expert_offsets  device int32 [num_experts + 1], nondecreasing, within
+ *                 [0, num_tokens].  It is read on the device: no host copy of
+ *                 the routing is needed.  An expert without rows costs
+ *                 nothing; rows that no expert owns are not written.  An entry
+ *                 that breaks the rule gives its expert no row and the error
+ *                 word of mla_decode_device_error reads 0x701.
+ *   num_experts   1 .. MLA_GEMM_MAX_EXPERTS, num_experts * n < 2^31.
+ *   the rest      as for mla_gemm_fp8.
+ */
+int mla_grouped_gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a_scale_stride, const void* w,
+                         int64_t ldw, const float* w_scales, const int32_t* expert_offsets, int num_experts,
+                         int num_tokens, int n, int k, void* out, int out_dtype, int64_t ldo, void* stream);
+
 /* ---- plan inspection (host only; used by tests and tools) ---- */
 
 /* Device workspace bytes the plan needs. */
@@ -459,7 +575,8 @@ void mla_planner_constants(int* tile_tokens, int* segment_overhead_tiles, int* m
  * bounded wait that timed out inside a decode kernel since the last reset
  * (the kernel then stopped early and its outputs are not valid); failing
  * that, the first out-of-range lookup of a block-table builder (0x30x) or of
- * the RoPE / cache-write step (0x60x).  Reading it
+ * the RoPE / cache-write step (0x60x), or a malformed expert offset (0x701) or
+ * a timed-out wait (0x71x) of a product.  Reading it
  * synchronises with the device; reset != 0 clears it.  Errors: MLA_ERR_ARG,
  * MLA_ERR_CUDA. */
 int mla_decode_device_error(int* code, int reset);

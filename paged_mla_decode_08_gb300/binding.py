@@ -27,6 +27,7 @@ MLA_KV_E4M3 = 1
 
 # Every symbol the header declares, with its ctypes signature.
 _c_int, _c_size, _vp, _i32p = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)
+_i64 = ctypes.c_int64
 _DECODE_ARGS = [_vp, _vp, _vp, _c_int, _c_int, _vp, _c_int, ctypes.c_int64, _c_int, _vp, _c_int, _vp,
                 ctypes.c_float, ctypes.c_float, _vp, _vp, _vp, _c_size, _vp]
 SIGNATURES = {
@@ -54,6 +55,12 @@ SIGNATURES = {
                                              _vp, _c_int, _vp]),
     "mla_block_table_from_pages": (_c_int, [_vp, ctypes.c_int64, ctypes.c_int64, _vp, _c_int, _vp, _c_int,
                                             _vp]),
+    "mla_add_rmsnorm": (_c_int, [_vp, _i64, _vp, _vp, _c_int, _i64, _vp, _c_int, _c_int, ctypes.c_float, _vp, _c_int,
+                                 _i64, _vp, _i64, _vp]),
+    "mla_act_quantize": (_c_int, [_vp, _i64, _c_int, _c_int, _c_int, _vp, _c_int, _i64, _vp, _i64, _vp]),
+    "mla_gemm_fp8": (_c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _i64, _vp]),
+    "mla_grouped_gemm_fp8": (_c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp,
+                                      _c_int, _i64, _vp]),
     "mla_plan_workspace_bytes": (_c_size, [_vp]),
     "mla_plan_num_workers": (_c_int, [_vp]),
     "mla_plan_num_segments": (_c_int, [_vp]),
@@ -315,6 +322,121 @@ def mla_block_table_from_pages(req_to_page, req_pool_indices, block_table, strea
     _check(load().mla_block_table_from_pages(_ptr(req_to_page), int(rows), int(cols), _ptr(req_pool_indices),
                                              int(block_table.shape[0]), _ptr(block_table),
                                              int(block_table.shape[1]), _stream(stream)))
+
+
+MLA_OUT_BF16 = 0
+MLA_OUT_E4M3 = 1
+MLA_OUT_FP32 = 2
+MLA_ACT_NONE = 0
+MLA_ACT_SILU_MUL = 1
+MLA_NORM_MAX_DIM = 32768
+MLA_GEMM_MAX_EXPERTS = 1024
+
+
+_dtypes_of: dict = {}
+
+
+def _dtypes(out_dtype: int):
+    """Tensor types that can hold elements of ``out_dtype`` (stored bits included)."""
+    if not _dtypes_of:
+        import torch
+        _dtypes_of.update({MLA_OUT_BF16: (torch.bfloat16, torch.int16, torch.uint16),
+                           MLA_OUT_E4M3: (torch.float8_e4m3fn, torch.uint8, torch.int8),
+                           MLA_OUT_FP32: (torch.float32,), "i32": (torch.int32,)})
+    return _dtypes_of.get(out_dtype, ())
+
+
+def _rows(x, name: str, shape, out_dtype) -> int:
+    """Row stride of a 2-D CUDA tensor of ``shape`` with contiguous columns."""
+    if tuple(x.shape) != shape:
+        raise MlaError(MLA_ERR_ARG, f"{name} has shape {tuple(x.shape)}, expected {shape}")
+    if x.dtype not in _dtypes(out_dtype):
+        raise MlaError(MLA_ERR_ARG, f"{name} has type {x.dtype}")
+    rows, cols = shape
+    if cols > 1 and x.stride(1) != 1 and rows:
+        raise MlaError(MLA_ERR_ARG, f"{name} must have contiguous columns")
+    if not x.is_cuda:
+        raise MlaError(MLA_ERR_ARG, f"{name} must be a CUDA tensor")
+    return x.stride(0) if rows > 1 else cols  # one row: any stride serves
+
+
+def _packed(x, name: str, shape, out_dtype):
+    """Check a contiguous CUDA tensor of ``shape``."""
+    if tuple(x.shape) != shape or x.dtype not in _dtypes(out_dtype) or not x.is_contiguous() or not x.is_cuda:
+        raise MlaError(MLA_ERR_ARG, f"{name} must be a contiguous CUDA tensor of shape {shape} and its type")
+
+
+def _matrix(x, name: str):
+    if x.dim() != 2:
+        raise MlaError(MLA_ERR_ARG, f"{name} must be 2-D")
+    return x.shape
+
+
+def mla_add_rmsnorm(x, residual, residual_out, residual_dtype: int, weight, eps: float, y, y_dtype: int,
+                    y_scales=None, stream=None):
+    """RMS norm of the rows of ``x`` (bf16) after adding ``residual`` (None =
+    none; the sum goes to ``residual_out``, which may be the same tensor) into
+    ``y``: bf16, or e4m3 with ``y_scales`` [ceil(dim / 128), tokens]."""
+    t, d = _matrix(x, "x")
+    xs = _rows(x, "x", (t, d), MLA_OUT_BF16)
+    rs = 0
+    if residual is not None and residual_out is not None:
+        rs = _rows(residual, "residual", (t, d), residual_dtype)
+        if _rows(residual_out, "residual_out", (t, d), residual_dtype) != rs:
+            raise MlaError(MLA_ERR_ARG, "residual and residual_out differ in their row stride")
+    _packed(weight, "weight", (d,), MLA_OUT_BF16)
+    ys = _rows(y, "y", (t, d), y_dtype)
+    ss = 0 if y_scales is None else _rows(y_scales, "y_scales", (-(-d // 128), t), MLA_OUT_FP32)
+    _check(load().mla_add_rmsnorm(_ptr(x), xs, _ptr(residual), _ptr(residual_out), residual_dtype, rs, _ptr(weight), t, d,
+                                  eps, _ptr(y), y_dtype, ys, _ptr(y_scales), ss, _stream(stream)))
+
+
+def mla_act_quantize(x, act: int, y, y_dtype: int, y_scales=None, stream=None):
+    """Quantise the bf16 rows of ``x`` (MLA_ACT_NONE), or silu(g) * u of rows
+    [g | u] (MLA_ACT_SILU_MUL), into ``y`` with ``y_scales`` [ceil(dim / 128),
+    tokens] (bf16 ``y``: the gated unit alone)."""
+    t, d = _matrix(y, "y")
+    xs = _rows(x, "x", (t, 2 * d if act == MLA_ACT_SILU_MUL else d), MLA_OUT_BF16)
+    ys = _rows(y, "y", (t, d), y_dtype)
+    ss = 0 if y_scales is None else _rows(y_scales, "y_scales", (-(-d // 128), t), MLA_OUT_FP32)
+    _check(load().mla_act_quantize(_ptr(x), xs, act, t, d, _ptr(y), y_dtype, ys, _ptr(y_scales), ss, _stream(stream)))
+
+
+def mla_gemm_fp8(a, a_scales, w, w_scales, out, out_dtype: int, stream=None):
+    """``out`` [T, N] = ``a`` [T, K] times ``w`` [N, K] transposed, e4m3 operands
+    with ``a_scales`` [ceil(K / 128), T] and ``w_scales`` [ceil(N / 128), ceil(K / 128)]."""
+    t, k = _matrix(a, "a")
+    n = _matrix(w, "w")[0]
+    gk = -(-k // 128)
+    lda, ldw = _rows(a, "a", (t, k), MLA_OUT_E4M3), _rows(w, "w", (n, k), MLA_OUT_E4M3)
+    ss = _rows(a_scales, "a_scales", (gk, t), MLA_OUT_FP32)
+    _packed(w_scales, "w_scales", (-(-n // 128), gk), MLA_OUT_FP32)
+    ldo = _rows(out, "out", (t, n), out_dtype)
+    _check(load().mla_gemm_fp8(_ptr(a), lda, _ptr(a_scales), ss, _ptr(w), ldw, _ptr(w_scales), t, n, k, _ptr(out),
+                               out_dtype, ldo, _stream(stream)))
+
+
+def mla_grouped_gemm_fp8(a, a_scales, w, w_scales, expert_offsets, out, out_dtype: int, stream=None):
+    """``mla_gemm_fp8`` by expert: rows expert_offsets[e] .. expert_offsets[e+1]-1
+    (int32 CUDA [E + 1]) use ``w[e]`` of ``w`` [E, N, K] with ``w_scales``
+    [E, ceil(N / 128), ceil(K / 128)]."""
+    t, k = _matrix(a, "a")
+    if w.dim() != 3:
+        raise MlaError(MLA_ERR_ARG, "w must be [experts, n, k]")
+    e, n = int(w.shape[0]), int(w.shape[1])
+    gk = -(-k // 128)
+    ldw = w.stride(1) if n > 1 else w.stride(0) if e > 1 else k  # every row of every expert, n rows apart
+    if w.shape[2] != k or w.stride(2) != 1 or (e > 1 and w.stride(0) != n * ldw):
+        raise MlaError(MLA_ERR_ARG, "w must be [experts, n, k] with contiguous columns and one row stride")
+    if w.dtype not in _dtypes(MLA_OUT_E4M3) or not w.is_cuda:
+        raise MlaError(MLA_ERR_ARG, "w must be an e4m3 CUDA tensor")
+    lda = _rows(a, "a", (t, k), MLA_OUT_E4M3)
+    ss = _rows(a_scales, "a_scales", (gk, t), MLA_OUT_FP32)
+    _packed(w_scales, "w_scales", (e, -(-n // 128), gk), MLA_OUT_FP32)
+    _packed(expert_offsets, "expert_offsets", (e + 1,), "i32")
+    ldo = _rows(out, "out", (t, n), out_dtype)
+    _check(load().mla_grouped_gemm_fp8(_ptr(a), lda, _ptr(a_scales), ss, _ptr(w), ldw, _ptr(w_scales),
+                                       _ptr(expert_offsets), e, t, n, k, _ptr(out), out_dtype, ldo, _stream(stream)))
 
 
 def mla_planner_constants():

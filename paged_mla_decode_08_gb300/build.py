@@ -25,7 +25,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmladecode.so")
 
 CUDA_SOURCES = ["mla_abi.cu", "mla_sm103.cu", "mla_combine.cu", "mla_noalloc.cu", "mla_block_table.cu",
-                "mla_plan_device.cu", "mla_kv_write.cu"]
+                "mla_plan_device.cu", "mla_kv_write.cu", "mla_norm_quant.cu", "mla_gemm_fp8.cu"]
 CXX_SOURCES = ["mla_plan.cpp"]
 HEADERS = ["mla_internal.h", "sm103_ptx.cuh"]
 

@@ -36,6 +36,17 @@ cudaError_t launch_rope_quantize_write(const void* q_nope, const void* q_rope, i
                                        int is_neox, void* kv_pages, int kv_dtype, int64_t num_pages, int page_size,
                                        const int64_t* out_cache_loc, cudaStream_t stream);
 cudaError_t kv_write_read_error(int* code, bool reset);
+cudaError_t launch_add_rmsnorm(const void* x, int64_t x_stride, const void* res_in, void* res_out, int residual_kind,
+                               int64_t res_stride, const void* weight, int num_tokens, int dim, float eps, void* y,
+                               int64_t y_stride, bool e4m3, float* y_scales, int64_t scale_stride,
+                               cudaStream_t stream);
+cudaError_t launch_act_quantize(const void* x, int64_t x_stride, int num_tokens, int dim, bool silu_mul, void* y,
+                                int64_t y_stride, bool e4m3, float* y_scales, int64_t scale_stride,
+                                cudaStream_t stream);
+cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda, int64_t a_scale_stride, const void* w,
+                            const float* w_scales, int64_t ldw, const int32_t* offsets, int m, int n, int k,
+                            int experts, void* out, bool fp32, int64_t ldo, int sms, cudaStream_t stream);
+cudaError_t gemm_read_error(int* code, bool reset);
 }  // namespace mla
 
 namespace {
@@ -430,13 +441,15 @@ const char* mla_decode_last_error_string(void) { return g_last_error.c_str(); }
 
 int mla_decode_device_error(int* code, int reset) {
   if (!code) return fail(MLA_ERR_ARG, "code is NULL");
-  int bt_code = 0, kw_code = 0;
+  int bt_code = 0, kw_code = 0, gm_code = 0;
   cudaError_t e = mla::sm103_read_error(code, reset != 0);
   if (e == cudaSuccess) e = mla::block_table_read_error(&bt_code, reset != 0);
   if (e == cudaSuccess) e = mla::kv_write_read_error(&kw_code, reset != 0);
+  if (e == cudaSuccess) e = mla::gemm_read_error(&gm_code, reset != 0);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("reading the kernel error word: ") + cudaGetErrorString(e));
   if (*code == 0) *code = bt_code;
   if (*code == 0) *code = kw_code;
+  if (*code == 0) *code = gm_code;
   return ok();
 }
 
@@ -511,6 +524,128 @@ int mla_block_table_from_pages(const int32_t* req_to_page, int64_t pool_rows, in
                                                      block_table, max_blocks, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("block-table launch: ") + cudaGetErrorString(e));
   return ok();
+}
+
+// Shared output checks of the two row operators.
+static int check_row_output(int num_tokens, int dim, const void* y, int y_dtype, int64_t y_stride,
+                            const float* y_scales, int64_t scale_stride) {
+  if (y_dtype != MLA_OUT_BF16 && y_dtype != MLA_OUT_E4M3) return fail(MLA_ERR_ARG, "y_dtype must be MLA_OUT_BF16 or MLA_OUT_E4M3");
+  if (!y) return fail(MLA_ERR_ARG, "a required device pointer is NULL");
+  if (y_stride < dim) return fail(MLA_ERR_ARG, "y_stride must be >= dim");
+  if (y_dtype == MLA_OUT_BF16 && !aligned(y, 2)) return fail(MLA_ERR_ARG, "y must be aligned to its elements");
+  if (y_dtype == MLA_OUT_E4M3) {
+    if (!y_scales || !aligned(y_scales, 4)) return fail(MLA_ERR_ARG, "an e4m3 output needs 4-byte aligned y_scales");
+    if (scale_stride < num_tokens) return fail(MLA_ERR_ARG, "scale_stride must be >= num_tokens");
+  }
+  return MLA_OK;
+}
+
+int mla_add_rmsnorm(const void* x, int64_t x_stride, const void* residual_in, void* residual_out, int residual_dtype,
+                    int64_t residual_stride, const void* weight, int num_tokens, int dim, float eps, void* y,
+                    int y_dtype, int64_t y_stride, float* y_scales, int64_t scale_stride, void* stream) {
+  if (num_tokens < 0) return fail(MLA_ERR_ARG, "num_tokens must be >= 0");
+  if (dim < 1 || dim > MLA_NORM_MAX_DIM) return fail(MLA_ERR_ARG, "dim must be in [1, MLA_NORM_MAX_DIM]");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(MLA_ERR_ARG, "eps must be finite and >= 0");
+  if (num_tokens == 0) return ok();
+  if (!x || !weight) return fail(MLA_ERR_ARG, "a required device pointer is NULL");
+  if (x_stride < dim) return fail(MLA_ERR_ARG, "x_stride must be >= dim");
+  if (!aligned(x, 2) || !aligned(weight, 2)) return fail(MLA_ERR_ARG, "x and weight must be aligned to their elements");
+  int kind = 0;
+  if (residual_in || residual_out) {
+    if (!residual_in || !residual_out) return fail(MLA_ERR_ARG, "residual_in and residual_out go together");
+    if (residual_dtype != MLA_OUT_BF16 && residual_dtype != MLA_OUT_FP32)
+      return fail(MLA_ERR_ARG, "residual_dtype must be MLA_OUT_BF16 or MLA_OUT_FP32");
+    if (residual_stride < dim) return fail(MLA_ERR_ARG, "residual_stride must be >= dim");
+    kind = residual_dtype == MLA_OUT_BF16 ? 1 : 2;
+    if (!aligned(residual_in, 2 * kind) || !aligned(residual_out, 2 * kind))
+      return fail(MLA_ERR_ARG, "the residual must be aligned to its elements");
+  }
+  int rc = check_row_output(num_tokens, dim, y, y_dtype, y_stride, y_scales, scale_stride);
+  if (rc != MLA_OK) return rc;
+  rc = check_device(nullptr);
+  if (rc != MLA_OK) return rc;
+  cudaError_t e = mla::launch_add_rmsnorm(x, x_stride, residual_in, residual_out, kind, residual_stride, weight,
+                                          num_tokens, dim, eps, y, y_stride, y_dtype == MLA_OUT_E4M3, y_scales,
+                                          scale_stride, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("norm launch: ") + cudaGetErrorString(e));
+  return ok();
+}
+
+int mla_act_quantize(const void* x, int64_t x_stride, int act, int num_tokens, int dim, void* y, int y_dtype,
+                     int64_t y_stride, float* y_scales, int64_t scale_stride, void* stream) {
+  if (act != MLA_ACT_NONE && act != MLA_ACT_SILU_MUL) return fail(MLA_ERR_ARG, "act must be MLA_ACT_NONE or MLA_ACT_SILU_MUL");
+  if (num_tokens < 0) return fail(MLA_ERR_ARG, "num_tokens must be >= 0");
+  if (dim < 1 || (act == MLA_ACT_SILU_MUL && dim > INT32_MAX / 2)) return fail(MLA_ERR_ARG, "dim must be >= 1, and 2 dim < 2^31 with a gate");
+  // a thread block covers 16 blocks of 128 columns
+  if ((int64_t)num_tokens * (((int64_t)dim + 127) / 128) > INT32_MAX)
+    return fail(MLA_ERR_ARG, "too many tokens x columns for one launch");
+  if (num_tokens == 0) return ok();
+  if (!x || !aligned(x, 2)) return fail(MLA_ERR_ARG, "x must be a device pointer aligned to its elements");
+  if (x_stride < (act == MLA_ACT_SILU_MUL ? 2 : 1) * (int64_t)dim) return fail(MLA_ERR_ARG, "x_stride is smaller than a row");
+  if (act == MLA_ACT_NONE && y_dtype == MLA_OUT_BF16) return fail(MLA_ERR_ARG, "MLA_ACT_NONE has an e4m3 output only");
+  int rc = check_row_output(num_tokens, dim, y, y_dtype, y_stride, y_scales, scale_stride);
+  if (rc != MLA_OK) return rc;
+  rc = check_device(nullptr);
+  if (rc != MLA_OK) return rc;
+  cudaError_t e = mla::launch_act_quantize(x, x_stride, num_tokens, dim, act == MLA_ACT_SILU_MUL, y, y_stride,
+                                           y_dtype == MLA_OUT_E4M3, y_scales, scale_stride,
+                                           static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("quantise launch: ") + cudaGetErrorString(e));
+  return ok();
+}
+
+// Both products; expert_offsets == nullptr: the dense one.
+static int gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a_scale_stride, const void* w,
+                    int64_t ldw, const float* w_scales, const int32_t* expert_offsets, int num_experts,
+                    int num_tokens, int n, int k, void* out, int out_dtype, int64_t ldo, void* stream) {
+  if (num_tokens < 0) return fail(MLA_ERR_ARG, "num_tokens must be >= 0");
+  if (n < 1) return fail(MLA_ERR_ARG, "n must be >= 1");
+  if (k < 16 || k % 16 != 0) return fail(MLA_ERR_ARG, "k must be a positive multiple of 16");
+  if (num_experts < 1 || num_experts > MLA_GEMM_MAX_EXPERTS)
+    return fail(MLA_ERR_ARG, "num_experts must be in [1, MLA_GEMM_MAX_EXPERTS]");
+  if ((int64_t)num_experts * n > INT32_MAX) return fail(MLA_ERR_ARG, "num_experts * n must be < 2^31");
+  if (num_tokens == 0) return ok();
+  if (!a || !a_scales || !w || !w_scales || !out) return fail(MLA_ERR_ARG, "a required device pointer is NULL");
+  if (lda < k || lda % 16 != 0 || ldw < k || ldw % 16 != 0)
+    return fail(MLA_ERR_ARG, "lda and ldw must be multiples of 16 and >= k");
+  // the copy engine's strides are 40 bits
+  if (lda >= ((int64_t)1 << 40) || ldw >= ((int64_t)1 << 40)) return fail(MLA_ERR_ARG, "lda and ldw must be < 2^40");
+  if (a_scale_stride < num_tokens) return fail(MLA_ERR_ARG, "a_scale_stride must be >= num_tokens");
+  if (ldo < n) return fail(MLA_ERR_ARG, "ldo must be >= n");
+  if (out_dtype != MLA_OUT_BF16 && out_dtype != MLA_OUT_FP32)
+    return fail(MLA_ERR_ARG, "out_dtype must be MLA_OUT_BF16 or MLA_OUT_FP32");
+  if (!aligned(a, 16) || !aligned(w, 16)) return fail(MLA_ERR_ARG, "a and w must be 16-byte aligned");
+  if (!aligned(a_scales, 4) || !aligned(w_scales, 4) || !aligned(expert_offsets, 4) ||
+      !aligned(out, out_dtype == MLA_OUT_FP32 ? 4 : 2))
+    return fail(MLA_ERR_ARG, "scales, offsets and out must be aligned to their elements");
+  // tiles are counted in 32 bits: at most (num_tokens / 16 + num_experts) x ceil(n / 128)
+  if (((int64_t)num_tokens / 16 + num_experts) * (((int64_t)n + 127) / 128) > INT32_MAX / 2)
+    return fail(MLA_ERR_ARG, "too many tiles for one launch");
+  int sms = 0;
+  int rc = check_device(&sms);
+  if (rc != MLA_OK) return rc;
+  cudaError_t e = mla::launch_gemm_fp8(a, a_scales, lda, a_scale_stride, w, w_scales, ldw, expert_offsets, num_tokens,
+                                       n, k, num_experts, out, out_dtype == MLA_OUT_FP32, ldo, sms,
+                                       static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported)
+    return fail(MLA_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled unavailable or rejected the operands");
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("product launch: ") + cudaGetErrorString(e));
+  return ok();
+}
+
+int mla_gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a_scale_stride, const void* w,
+                 int64_t ldw, const float* w_scales, int num_tokens, int n, int k, void* out, int out_dtype,
+                 int64_t ldo, void* stream) {
+  return gemm_fp8(a, lda, a_scales, a_scale_stride, w, ldw, w_scales, nullptr, 1, num_tokens, n, k, out, out_dtype,
+                  ldo, stream);
+}
+
+int mla_grouped_gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a_scale_stride, const void* w,
+                         int64_t ldw, const float* w_scales, const int32_t* expert_offsets, int num_experts,
+                         int num_tokens, int n, int k, void* out, int out_dtype, int64_t ldo, void* stream) {
+  if (!expert_offsets) return fail(MLA_ERR_ARG, "expert_offsets is NULL");
+  return gemm_fp8(a, lda, a_scales, a_scale_stride, w, ldw, w_scales, expert_offsets, num_experts, num_tokens, n, k,
+                  out, out_dtype, ldo, stream);
 }
 
 int mla_decode_version(void) { return 100; }

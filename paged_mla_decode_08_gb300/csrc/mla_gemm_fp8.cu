@@ -1,0 +1,477 @@
+// Matrix product of e4m3 operands with fp32 scales for blocks of 128:
+//
+//   out[m, n] = sum_b sa[b, m] * sw[n / 128, b] * sum_{k in block b} a[m, k] * w[n, k]
+//
+// dense (one weight matrix) or grouped by expert (rows offsets[e] ..
+// offsets[e+1]-1 use the weights of expert e).
+//
+// A tile is 128 weight rows x TN tokens.  The weights are the M operand of
+// tcgen05.mma (128 rows) and the tokens its N operand, so that a handful of
+// tokens wastes no tensor-core rows and streams the weights once.  One 128-wide
+// block of k is one 128-byte swizzled row of both operands: TMA fills a ring of
+// stages, four kind::f8f6f4 MMAs reduce the block into a TMEM buffer, and the
+// epilogue warps read the buffer and add it, times the block's scales, to fp32
+// sums in registers while the next block runs into the other buffer.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "mla_internal.h"
+#include "sm103_ptx.cuh"
+
+namespace mla {
+namespace gemm8 {
+
+using namespace ptx;
+
+__device__ int g_gemm_error;
+
+constexpr int kBlockK = 128;     // k columns per scale block = bytes of one swizzled operand row
+constexpr int kTileRows = 128;   // weight rows per tile = columns that share a weight scale
+constexpr int kMaxExperts = 1024;
+constexpr int kThreads = 224;    // warps: 0 TMA, 1 MMA, 2-5 epilogue, 6 scales
+constexpr long long kTimeoutCycles = 2000000000LL;  // about a second: a wait this long has failed
+
+struct Args {
+  const float* a_scales;  // [k blocks][a_scale_stride]
+  const float* w_scales;  // [experts][row blocks][k blocks]
+  const int32_t* offsets; // int32 [experts + 1], nullptr: one group of all rows
+  void* out;
+  int64_t a_scale_stride, ldo;
+  int m, n, k_blocks, row_blocks, experts;
+};
+
+template <int TN>
+struct Cfg {
+  static constexpr int kStageA = kTileRows * kBlockK;  // weights
+  static constexpr int kStageB = TN * kBlockK;         // tokens
+  static constexpr int kStage = kStageA + kStageB;
+  static constexpr int kStages = TN <= 64 ? 8 : 6;
+  static constexpr int kScaleStages = 8;
+  static constexpr int kBufs = 2;
+  static constexpr uint32_t kTmemCols = kBufs * TN < 32 ? 32 : kBufs * TN;
+  static constexpr int kOffScales = kStages * kStage;
+  static constexpr int kOffPrefix = kOffScales + kScaleStages * TN * 4;
+  static constexpr int kOffBars = kOffPrefix + (kMaxExperts + 8) * 4;
+  static constexpr int kSmem = kOffBars + 512 + 1024;  // + alignment slack
+};
+
+struct Bars {
+  uint32_t base;
+  __device__ uint32_t full(int s) const { return base + 8 * s; }
+  __device__ uint32_t empty(int s) const { return base + 8 * (16 + s); }
+  __device__ uint32_t sfull(int s) const { return base + 8 * (32 + s); }
+  __device__ uint32_t sempty(int s) const { return base + 8 * (40 + s); }
+  __device__ uint32_t tfull(int s) const { return base + 8 * (48 + s); }
+  __device__ uint32_t tempty(int s) const { return base + 8 * (52 + s); }
+  __device__ uint32_t fin() const { return base + 8 * 56; }
+};
+
+// Bounded wait; false: gave up here or elsewhere in the CTA.
+__device__ __forceinline__ bool wait_bar(volatile int* abort_flag, uint32_t bar, uint32_t parity, int code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kTimeoutCycles) {
+      *abort_flag = 1;
+      atomicCAS(&g_gemm_error, 0, code);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_bar_warp(volatile int* abort_flag, uint32_t bar, uint32_t parity, int code) {
+  const bool ok = wait_bar(abort_flag, bar, parity, code);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, 8-bit operands, K = 32
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// fp32 accumulator, e4m3 x e4m3, both K-major
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+// 4-byte asynchronous copy; bytes == 0 writes zeros and reads nothing
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// this thread's earlier cp.async copies arrive on `bar` when they have landed
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  union U { float2 f; uint64_t u; } x, y, z, d;
+  x.f = a; y.f = b; z.f = c;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.u) : "l"(x.u), "l"(y.u), "l"(z.u));
+  return d.f;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  union U { float2 f; uint64_t u; } x, y, d;
+  x.f = a; y.f = b;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(x.u), "l"(y.u));
+  return d.f;
+}
+// 32 lanes x 16 columns with the wait in the same statement
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Rows [lo, hi) of expert e.  Offsets outside 0 <= lo <= hi <= m own no row
+// (recorded), so no access leaves the arrays.
+__device__ __forceinline__ int2 expert_rows(const Args& a, int e) {
+  if (a.offsets == nullptr) return make_int2(0, a.m);
+  const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
+  if (lo < 0 || hi < lo || hi > a.m) {
+    atomicCAS(&g_gemm_error, 0, 0x701);
+    return make_int2(0, 0);
+  }
+  return make_int2(lo, hi);
+}
+
+struct Tile {
+  int expert, row_block, tok0, tok_end;
+};
+
+// Tile `idx`: experts in order; within an expert the token tiles of one block
+// of weight rows are neighbours, so concurrent CTAs read the same weights.
+template <int TN>
+__device__ __forceinline__ Tile find_tile(const Args& a, const int* prefix, int idx) {
+  int e = 0;
+  if (a.offsets != nullptr) {
+    const int p = idx / a.row_blocks;  // an expert owns prefix[e] .. prefix[e+1] token tiles
+    int lo = 0, hi = a.experts - 1;
+    while (lo < hi) {  // last e with prefix[e] <= p
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= p) lo = mid; else hi = mid - 1;
+    }
+    e = lo;
+  }
+  const int first = prefix[e], count = prefix[e + 1] - first;
+  const int rem = idx - first * a.row_blocks;
+  const int2 rows = expert_rows(a, e);
+  Tile t;
+  t.expert = e;
+  t.row_block = rem / count;
+  t.tok0 = rows.x + (rem - t.row_block * count) * TN;
+  t.tok_end = rows.y;
+  return t;
+}
+
+template <int TN, bool kFp32>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const Args a) {
+  using C = Cfg<TN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const Bars bars{sbase + C::kOffBars};
+  int* prefix = reinterpret_cast<int*>(smem + C::kOffPrefix);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(prefix + kMaxExperts + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(prefix + kMaxExperts + 5);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(bars.full(i), 1);
+      mbar_init(bars.empty(i), 1);
+    }
+    for (int i = 0; i < C::kScaleStages; ++i) {
+      mbar_init(bars.sfull(i), 32);
+      mbar_init(bars.sempty(i), 128);
+    }
+    for (int i = 0; i < C::kBufs; ++i) {
+      mbar_init(bars.tfull(i), 1);
+      mbar_init(bars.tempty(i), 128);
+    }
+    mbar_init(bars.fin(), 1);
+    fence_mbar_init();
+    prefetch_tensormap(&tm_w);
+    prefetch_tensormap(&tm_a);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 2) {
+    // token tiles of the experts before each expert
+    int run = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 32) {
+      const int e = e0 + lane;
+      int c = 0;
+      if (e < a.experts) {
+        const int2 r = expert_rows(a, e);
+        c = (int)(((int64_t)r.y - r.x + TN - 1) / TN);
+      }
+      int inc = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (e < a.experts) prefix[e] = run + inc - c;
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) prefix[a.experts] = run;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const int tiles = prefix[a.experts] * a.row_blocks;
+
+  if (warp == 0) {
+    // ---- TMA producer
+    if (lane == 0) {
+      int j = 0;
+      bool ok = true;
+      for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
+        const Tile t = find_tile<TN>(a, prefix, idx);
+        const int wrow = t.expert * a.n + t.row_block * kTileRows;
+        for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
+          const int s = j % C::kStages;
+          if (j >= C::kStages && !wait_bar(abort_flag, bars.empty(s), ((j / C::kStages) - 1) & 1, 0x711)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bars.full(s), C::kStage);
+          tma_load_2d(sbase + s * C::kStage, &tm_w, bars.full(s), kb * kBlockK, wrow);
+          tma_load_2d(sbase + s * C::kStage + C::kStageA, &tm_a, bars.full(s), kb * kBlockK, t.tok0);
+        }
+      }
+      // the copies in flight must have landed before the CTA leaves
+      for (int k = max(0, j - C::kStages); k < j; ++k) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bars.full(k % C::kStages), (k / C::kStages) & 1) && clock64() - t0 < kTimeoutCycles) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kIdesc = idesc_e4m3(kTileRows, TN);
+      int j = 0;
+      bool ok = true;
+      for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
+        for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
+          const int s = j % C::kStages, b = j % C::kBufs;
+          if (!wait_bar(abort_flag, bars.full(s), (j / C::kStages) & 1, 0x712) ||
+              (j >= C::kBufs && !wait_bar(abort_flag, bars.tempty(b), ((j / C::kBufs) - 1) & 1, 0x713))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t wa = sbase + s * C::kStage, ta = wa + C::kStageA;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f8(tmem + b * TN, smem_desc(wa + kk * 32, 16, 1024, kSwizzle128B),
+                   smem_desc(ta + kk * 32, 16, 1024, kSwizzle128B), kIdesc, kk > 0);
+          mma_commit(bars.empty(s));
+          mma_commit(bars.tfull(b));
+        }
+      }
+      mma_commit(bars.fin());  // everything issued is done before TMEM is released
+      const long long t0 = clock64();
+      while (!mbar_try_wait(bars.fin(), 0) && clock64() - t0 < kTimeoutCycles) {
+      }
+    }
+  } else if (warp == 6) {
+    // ---- token scales of each k block into their own ring
+    int j = 0;
+    bool ok = true;
+    for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
+      const Tile t = find_tile<TN>(a, prefix, idx);
+      for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
+        const int s = j % C::kScaleStages;
+        if (j >= C::kScaleStages &&
+            !wait_bar_warp(abort_flag, bars.sempty(s), ((j / C::kScaleStages) - 1) & 1, 0x714)) {
+          ok = false;
+          break;
+        }
+        const float* src = a.a_scales + kb * a.a_scale_stride + t.tok0;
+        for (int i = lane; i < TN; i += 32) {
+          const bool in = t.tok0 + i < t.tok_end;
+          cp_async4(sbase + C::kOffScales + (s * TN + i) * 4, in ? src + i : a.a_scales, in ? 4 : 0);
+        }
+        cp_async_arrive(bars.sfull(s));
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    // ---- epilogue: thread = weight row, registers = tokens
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    int j = 0;
+    bool ok = true;
+    for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
+      const Tile t = find_tile<TN>(a, prefix, idx);
+      float2 acc[TN / 2];
+#pragma unroll
+      for (int i = 0; i < TN / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      const float* sw = a.w_scales + ((int64_t)t.expert * a.row_blocks + t.row_block) * a.k_blocks;
+      float sw_next = __ldg(sw);
+      for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
+        const int s = j % C::kScaleStages, b = j % C::kBufs;
+        const float2 w2 = make_float2(sw_next, sw_next);
+        if (kb + 1 < a.k_blocks) sw_next = __ldg(sw + kb + 1);
+        if (!wait_bar_warp(abort_flag, bars.sfull(s), (j / C::kScaleStages) & 1, 0x715) ||
+            !wait_bar_warp(abort_flag, bars.tfull(b), (j / C::kBufs) & 1, 0x716)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffScales + s * TN * 4);
+#pragma unroll
+        for (int c = 0; c < TN; c += 16) {
+          uint32_t r[16];
+          tmem_ld16(taddr + b * TN + c, r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 s4 = sc[c / 4 + i];
+            const float2 s01 = mul2(make_float2(s4.x, s4.y), w2), s23 = mul2(make_float2(s4.z, s4.w), w2);
+            const float2 p01 = make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]));
+            const float2 p23 = make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+            acc[c / 2 + 2 * i] = fma2(p01, s01, acc[c / 2 + 2 * i]);
+            acc[c / 2 + 2 * i + 1] = fma2(p23, s23, acc[c / 2 + 2 * i + 1]);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(bars.tempty(b));
+        mbar_arrive(bars.sempty(s));
+      }
+      const int n = t.row_block * kTileRows + row;
+      if (ok && n < a.n) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+          const int m = t.tok0 + i;
+          const float v = (i & 1) ? acc[i / 2].y : acc[i / 2].x;
+          if (m < t.tok_end) {
+            if (kFp32)
+              static_cast<float*>(a.out)[m * a.ldo + n] = v;
+            else
+              static_cast<__nv_bfloat16*>(a.out)[m * a.ldo + n] = __float2bfloat16_rn(v);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// ------------------------------------------------------------------ host side
+
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// Rows of k bytes with a row pitch of ld bytes, read as 128-byte x box_rows
+// boxes in the 128-byte swizzle; bytes past k and rows past the end read as 0.
+static bool make_map(CUtensorMap* map, const void* p, int64_t k, int64_t rows, int64_t ld, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld};
+  cuuint32_t box[2] = {(cuuint32_t)kBlockK, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int TN, bool kFp32>
+static cudaError_t launch_tn(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, const Args& a,
+                             int sms, cudaStream_t stream) {
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(gemm_kernel<TN, kFp32>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<TN>::kSmem);
+  });
+  if (attr_err != cudaSuccess) return attr_err;
+  CUtensorMap tm_w, tm_a;
+  if (!make_map(&tm_w, w, k, (int64_t)a.experts * a.n, ldw, kTileRows) || !make_map(&tm_a, act, k, a.m, lda, TN))
+    return cudaErrorNotSupported;
+  // at most this many token tiles exist, whatever the offsets say
+  const int64_t tok_tiles = (int64_t)a.m / TN + std::min(a.experts, a.m);
+  const int64_t tiles = std::min<int64_t>(tok_tiles * a.row_blocks, sms);
+  gemm_kernel<TN, kFp32><<<(unsigned)tiles, kThreads, Cfg<TN>::kSmem, stream>>>(tm_w, tm_a, a);
+  return cudaGetLastError();
+}
+
+template <bool kFp32>
+static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, const Args& a,
+                              int sms, cudaStream_t stream) {
+  const int64_t per_expert = ((int64_t)a.m + a.experts - 1) / a.experts;
+  if (per_expert <= 16) return launch_tn<16, kFp32>(act, lda, w, ldw, k, a, sms, stream);
+  if (per_expert <= 32) return launch_tn<32, kFp32>(act, lda, w, ldw, k, a, sms, stream);
+  if (per_expert <= 64) return launch_tn<64, kFp32>(act, lda, w, ldw, k, a, sms, stream);
+  return launch_tn<128, kFp32>(act, lda, w, ldw, k, a, sms, stream);
+}
+
+}  // namespace gemm8
+
+// Arguments are checked by the caller; cudaErrorNotSupported: the tensor-map
+// encoder is unavailable or rejected the operands.
+cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda, int64_t a_scale_stride, const void* w,
+                            const float* w_scales, int64_t ldw, const int32_t* offsets, int m, int n, int k,
+                            int experts, void* out, bool fp32, int64_t ldo, int sms, cudaStream_t stream) {
+  gemm8::Args a;
+  a.a_scales = a_scales;
+  a.w_scales = w_scales;
+  a.offsets = offsets;
+  a.out = out;
+  a.a_scale_stride = a_scale_stride;
+  a.ldo = ldo;
+  a.m = m;
+  a.n = n;
+  a.k_blocks = (k + gemm8::kBlockK - 1) / gemm8::kBlockK;
+  a.row_blocks = (n + gemm8::kTileRows - 1) / gemm8::kTileRows;
+  a.experts = experts;
+  return fp32 ? gemm8::launch_out<true>(act, lda, w, ldw, k, a, sms, stream)
+              : gemm8::launch_out<false>(act, lda, w, ldw, k, a, sms, stream);
+}
+
+cudaError_t gemm_read_error(int* code, bool reset) {
+  cudaError_t e = cudaMemcpyFromSymbol(code, gemm8::g_gemm_error, sizeof(int));
+  if (e != cudaSuccess || !reset) return e;
+  const int zero = 0;
+  return cudaMemcpyToSymbol(gemm8::g_gemm_error, &zero, sizeof(int));
+}
+
+}  // namespace mla
