@@ -112,10 +112,18 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+_raw_stream = None  # current stream of a device as an integer, without building a Stream object
+
+
 def _stream(stream) -> Optional[int]:
+    global _raw_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            import torch
+            get, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+            torch.cuda.current_stream()  # initialises CUDA
+            _raw_stream = lambda: get(device())  # noqa: E731
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -333,36 +341,37 @@ MLA_NORM_MAX_DIM = 32768
 MLA_GEMM_MAX_EXPERTS = 1024
 
 
-_dtypes_of: dict = {}
+# Tensor types that hold each element type (stored bits included), filled by _dtypes()
+_BF16, _E4M3, _FP32, _I32 = MLA_OUT_BF16, MLA_OUT_E4M3, MLA_OUT_FP32, 3
+_held_by: dict = {}
 
 
-def _dtypes(out_dtype: int):
-    """Tensor types that can hold elements of ``out_dtype`` (stored bits included)."""
-    if not _dtypes_of:
+def _dtypes(kind: int):
+    if not _held_by:
         import torch
-        _dtypes_of.update({MLA_OUT_BF16: (torch.bfloat16, torch.int16, torch.uint16),
-                           MLA_OUT_E4M3: (torch.float8_e4m3fn, torch.uint8, torch.int8),
-                           MLA_OUT_FP32: (torch.float32,), "i32": (torch.int32,)})
-    return _dtypes_of.get(out_dtype, ())
+        _held_by.update({_BF16: (torch.bfloat16, torch.int16, torch.uint16),
+                         _E4M3: (torch.float8_e4m3fn, torch.uint8, torch.int8),
+                         _FP32: (torch.float32,), _I32: (torch.int32,)})
+    return _held_by.get(kind, ())
 
 
-def _rows(x, name: str, shape, out_dtype) -> int:
+def _rows(x, name: str, shape, kind: int) -> int:
     """Row stride of a 2-D CUDA tensor of ``shape`` with contiguous columns."""
-    if tuple(x.shape) != shape:
-        raise MlaError(MLA_ERR_ARG, f"{name} has shape {tuple(x.shape)}, expected {shape}")
-    if x.dtype not in _dtypes(out_dtype):
+    if x.shape != shape:
+        raise MlaError(MLA_ERR_ARG, f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if x.dtype not in (_held_by.get(kind) or _dtypes(kind)):
         raise MlaError(MLA_ERR_ARG, f"{name} has type {x.dtype}")
-    rows, cols = shape
-    if cols > 1 and x.stride(1) != 1 and rows:
+    row, col = x.stride()
+    if col != 1 and shape[1] > 1 and shape[0]:
         raise MlaError(MLA_ERR_ARG, f"{name} must have contiguous columns")
     if not x.is_cuda:
         raise MlaError(MLA_ERR_ARG, f"{name} must be a CUDA tensor")
-    return x.stride(0) if rows > 1 else cols  # one row: any stride serves
+    return row if shape[0] > 1 else shape[1]  # one row: any stride serves
 
 
-def _packed(x, name: str, shape, out_dtype):
+def _packed(x, name: str, shape, kind: int):
     """Check a contiguous CUDA tensor of ``shape``."""
-    if tuple(x.shape) != shape or x.dtype not in _dtypes(out_dtype) or not x.is_contiguous() or not x.is_cuda:
+    if x.shape != shape or x.dtype not in _dtypes(kind) or not x.is_contiguous() or not x.is_cuda:
         raise MlaError(MLA_ERR_ARG, f"{name} must be a contiguous CUDA tensor of shape {shape} and its type")
 
 
@@ -378,17 +387,17 @@ def mla_add_rmsnorm(x, residual, residual_out, residual_dtype: int, weight, eps:
     none; the sum goes to ``residual_out``, which may be the same tensor) into
     ``y``: bf16, or e4m3 with ``y_scales`` [ceil(dim / 128), tokens]."""
     t, d = _matrix(x, "x")
-    xs = _rows(x, "x", (t, d), MLA_OUT_BF16)
+    xs = _rows(x, "x", x.shape, _BF16)
     rs = 0
     if residual is not None and residual_out is not None:
         rs = _rows(residual, "residual", (t, d), residual_dtype)
         if _rows(residual_out, "residual_out", (t, d), residual_dtype) != rs:
             raise MlaError(MLA_ERR_ARG, "residual and residual_out differ in their row stride")
-    _packed(weight, "weight", (d,), MLA_OUT_BF16)
+    _packed(weight, "weight", (d,), _BF16)
     ys = _rows(y, "y", (t, d), y_dtype)
-    ss = 0 if y_scales is None else _rows(y_scales, "y_scales", (-(-d // 128), t), MLA_OUT_FP32)
-    _check(load().mla_add_rmsnorm(_ptr(x), xs, _ptr(residual), _ptr(residual_out), residual_dtype, rs, _ptr(weight), t, d,
-                                  eps, _ptr(y), y_dtype, ys, _ptr(y_scales), ss, _stream(stream)))
+    ss = 0 if y_scales is None else _rows(y_scales, "y_scales", (-(-d // 128), t), _FP32)
+    _check(load().mla_add_rmsnorm(x.data_ptr(), xs, _ptr(residual), _ptr(residual_out), residual_dtype, rs, weight.data_ptr(), t, d,
+                                  eps, y.data_ptr(), y_dtype, ys, _ptr(y_scales), ss, _stream(stream)))
 
 
 def mla_act_quantize(x, act: int, y, y_dtype: int, y_scales=None, stream=None):
@@ -396,10 +405,10 @@ def mla_act_quantize(x, act: int, y, y_dtype: int, y_scales=None, stream=None):
     [g | u] (MLA_ACT_SILU_MUL), into ``y`` with ``y_scales`` [ceil(dim / 128),
     tokens] (bf16 ``y``: the gated unit alone)."""
     t, d = _matrix(y, "y")
-    xs = _rows(x, "x", (t, 2 * d if act == MLA_ACT_SILU_MUL else d), MLA_OUT_BF16)
-    ys = _rows(y, "y", (t, d), y_dtype)
-    ss = 0 if y_scales is None else _rows(y_scales, "y_scales", (-(-d // 128), t), MLA_OUT_FP32)
-    _check(load().mla_act_quantize(_ptr(x), xs, act, t, d, _ptr(y), y_dtype, ys, _ptr(y_scales), ss, _stream(stream)))
+    xs = _rows(x, "x", (t, 2 * d if act == MLA_ACT_SILU_MUL else d), _BF16)
+    ys = _rows(y, "y", y.shape, y_dtype)
+    ss = 0 if y_scales is None else _rows(y_scales, "y_scales", (-(-d // 128), t), _FP32)
+    _check(load().mla_act_quantize(x.data_ptr(), xs, act, t, d, y.data_ptr(), y_dtype, ys, _ptr(y_scales), ss, _stream(stream)))
 
 
 def mla_gemm_fp8(a, a_scales, w, w_scales, out, out_dtype: int, stream=None):
@@ -408,11 +417,11 @@ def mla_gemm_fp8(a, a_scales, w, w_scales, out, out_dtype: int, stream=None):
     t, k = _matrix(a, "a")
     n = _matrix(w, "w")[0]
     gk = -(-k // 128)
-    lda, ldw = _rows(a, "a", (t, k), MLA_OUT_E4M3), _rows(w, "w", (n, k), MLA_OUT_E4M3)
-    ss = _rows(a_scales, "a_scales", (gk, t), MLA_OUT_FP32)
-    _packed(w_scales, "w_scales", (-(-n // 128), gk), MLA_OUT_FP32)
+    lda, ldw = _rows(a, "a", (t, k), _E4M3), _rows(w, "w", (n, k), _E4M3)
+    ss = _rows(a_scales, "a_scales", (gk, t), _FP32)
+    _packed(w_scales, "w_scales", (-(-n // 128), gk), _FP32)
     ldo = _rows(out, "out", (t, n), out_dtype)
-    _check(load().mla_gemm_fp8(_ptr(a), lda, _ptr(a_scales), ss, _ptr(w), ldw, _ptr(w_scales), t, n, k, _ptr(out),
+    _check(load().mla_gemm_fp8(a.data_ptr(), lda, a_scales.data_ptr(), ss, w.data_ptr(), ldw, w_scales.data_ptr(), t, n, k, out.data_ptr(),
                                out_dtype, ldo, _stream(stream)))
 
 
@@ -428,15 +437,15 @@ def mla_grouped_gemm_fp8(a, a_scales, w, w_scales, expert_offsets, out, out_dtyp
     ldw = w.stride(1) if n > 1 else w.stride(0) if e > 1 else k  # every row of every expert, n rows apart
     if w.shape[2] != k or w.stride(2) != 1 or (e > 1 and w.stride(0) != n * ldw):
         raise MlaError(MLA_ERR_ARG, "w must be [experts, n, k] with contiguous columns and one row stride")
-    if w.dtype not in _dtypes(MLA_OUT_E4M3) or not w.is_cuda:
+    if w.dtype not in _dtypes(_E4M3) or not w.is_cuda:
         raise MlaError(MLA_ERR_ARG, "w must be an e4m3 CUDA tensor")
-    lda = _rows(a, "a", (t, k), MLA_OUT_E4M3)
-    ss = _rows(a_scales, "a_scales", (gk, t), MLA_OUT_FP32)
-    _packed(w_scales, "w_scales", (e, -(-n // 128), gk), MLA_OUT_FP32)
-    _packed(expert_offsets, "expert_offsets", (e + 1,), "i32")
+    lda = _rows(a, "a", (t, k), _E4M3)
+    ss = _rows(a_scales, "a_scales", (gk, t), _FP32)
+    _packed(w_scales, "w_scales", (e, -(-n // 128), gk), _FP32)
+    _packed(expert_offsets, "expert_offsets", (e + 1,), _I32)
     ldo = _rows(out, "out", (t, n), out_dtype)
-    _check(load().mla_grouped_gemm_fp8(_ptr(a), lda, _ptr(a_scales), ss, _ptr(w), ldw, _ptr(w_scales),
-                                       _ptr(expert_offsets), e, t, n, k, _ptr(out), out_dtype, ldo, _stream(stream)))
+    _check(load().mla_grouped_gemm_fp8(a.data_ptr(), lda, a_scales.data_ptr(), ss, w.data_ptr(), ldw, w_scales.data_ptr(),
+                                       expert_offsets.data_ptr(), e, t, n, k, out.data_ptr(), out_dtype, ldo, _stream(stream)))
 
 
 def mla_planner_constants():

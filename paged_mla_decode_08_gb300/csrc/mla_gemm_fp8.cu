@@ -34,7 +34,6 @@ __device__ int g_gemm_error;
 constexpr int kBlockK = 128;     // k columns per scale block = bytes of one swizzled operand row
 constexpr int kTileRows = 128;   // weight rows per tile = columns that share a weight scale
 constexpr int kMaxExperts = 1024;
-constexpr int kThreads = 224;    // warps: 0 TMA, 1 MMA, 2-5 epilogue, 6 scales
 constexpr long long kTimeoutCycles = 2000000000LL;  // about a second: a wait this long has failed
 
 struct Args {
@@ -44,19 +43,28 @@ struct Args {
   void* out;
   int64_t a_scale_stride, ldo;
   int m, n, k_blocks, row_blocks, experts;
+  int splits;  // CTAs that share a tile's k blocks (a cluster); 1: none
 };
 
-template <int TN>
+template <int TN, bool kSplit>
 struct Cfg {
+  // warps: 0 TMA, 1 MMA, then 4 (one per TMEM lane quadrant) or 8 (two, each
+  // with half of the tokens) of the epilogue, then the scales
+  static constexpr int kEpiWarps = TN >= 32 ? 8 : 4;
+  static constexpr int kThreads = 32 * (kEpiWarps + 3);
   static constexpr int kStageA = kTileRows * kBlockK;  // weights
   static constexpr int kStageB = TN * kBlockK;         // tokens
   static constexpr int kStage = kStageA + kStageB;
-  static constexpr int kStages = TN <= 64 ? 8 : 6;
+  // partial sums received from the CTAs of a split tile: [source][row][token slice]
+  static constexpr int kRecv = kSplit ? kTileRows * TN * 4 : 0;
+  static constexpr int kStages = (200 * 1024 - kRecv) / kStage < 8 ? (200 * 1024 - kRecv) / kStage : 8;
   static constexpr int kScaleStages = 8;
-  static constexpr int kBufs = 2;
-  static constexpr uint32_t kTmemCols = kBufs * TN < 32 ? 32 : kBufs * TN;
-  static constexpr int kOffScales = kStages * kStage;
-  static constexpr int kOffPrefix = kOffScales + kScaleStages * TN * 4;
+  static constexpr int kScaleSlot = TN + 4;            // token scales, then the weights' scale
+  static constexpr int kBufs = 4;
+  static constexpr uint32_t kTmemCols = kBufs * TN;
+  static constexpr int kOffRecv = kStages * kStage;
+  static constexpr int kOffScales = kOffRecv + kRecv;
+  static constexpr int kOffPrefix = kOffScales + kScaleStages * kScaleSlot * 4;
   static constexpr int kOffBars = kOffPrefix + (kMaxExperts + 8) * 4;
   static constexpr int kSmem = kOffBars + 512 + 1024;  // + alignment slack
 };
@@ -70,14 +78,16 @@ struct Bars {
   __device__ uint32_t tfull(int s) const { return base + 8 * (48 + s); }
   __device__ uint32_t tempty(int s) const { return base + 8 * (52 + s); }
   __device__ uint32_t fin() const { return base + 8 * 56; }
+  __device__ uint32_t recv() const { return base + 8 * 57; }
 };
 
 // Bounded wait; false: gave up here or elsewhere in the CTA.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar(volatile int* abort_flag, uint32_t bar, uint32_t parity, int code) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > kTimeoutCycles) {
       *abort_flag = 1;
@@ -86,8 +96,9 @@ __device__ __forceinline__ bool wait_bar(volatile int* abort_flag, uint32_t bar,
     }
   }
 }
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar_warp(volatile int* abort_flag, uint32_t bar, uint32_t parity, int code) {
-  const bool ok = wait_bar(abort_flag, bar, parity, code);
+  const bool ok = wait_bar<kCluster>(abort_flag, bar, parity, code);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -108,6 +119,13 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
       : "memory");
+}
+// Shared memory of this CTA -> shared memory of a CTA of the cluster, completing
+// `bytes` on that CTA's barrier (remote addresses from mapa).
+__device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t mbar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(src), "r"(bytes), "r"(mbar)
+               : "memory");
 }
 // 4-byte asynchronous copy; bytes == 0 writes zeros and reads nothing
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
@@ -181,10 +199,21 @@ __device__ __forceinline__ Tile find_tile(const Args& a, const int* prefix, int 
   return t;
 }
 
-template <int TN, bool kFp32>
-__global__ void __launch_bounds__(kThreads, 1)
+__device__ __forceinline__ void store_out(const Args& a, bool fp32, int m, int n, float v) {
+  if (fp32)
+    static_cast<float*>(a.out)[m * a.ldo + n] = v;
+  else
+    static_cast<__nv_bfloat16*>(a.out)[m * a.ldo + n] = __float2bfloat16_rn(v);
+}
+
+// kSplit: the CTAs of a cluster share a tile, each summing its part of the k
+// blocks; the sums are then exchanged through distributed shared memory, each
+// CTA adding up and storing a slice of the tile's tokens in CTA order (the
+// grid holds one cluster per tile).
+template <int TN, bool kSplit, bool kFp32>
+__global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const Args a) {
-  using C = Cfg<TN>;
+  using C = Cfg<TN, kSplit>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -193,6 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(prefix + kMaxExperts + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(prefix + kMaxExperts + 5);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = kSplit ? a.splits : 1;
+  const int rank = kSplit ? (int)cluster_ctarank() : 0;
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -202,14 +233,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < C::kScaleStages; ++i) {
       mbar_init(bars.sfull(i), 32);
-      mbar_init(bars.sempty(i), 128);
+      mbar_init(bars.sempty(i), C::kEpiWarps);
     }
     for (int i = 0; i < C::kBufs; ++i) {
       mbar_init(bars.tfull(i), 1);
-      mbar_init(bars.tempty(i), 128);
+      mbar_init(bars.tempty(i), C::kEpiWarps);
     }
     mbar_init(bars.fin(), 1);
+    mbar_init(bars.recv(), 1);
     fence_mbar_init();
+    if (kSplit) mbar_arrive_expect_tx(bars.recv(), C::kRecv);
     prefetch_tensormap(&tm_w);
     prefetch_tensormap(&tm_a);
   }
@@ -240,19 +273,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (kSplit) cluster_sync();  // the peers' barriers are initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const int tiles = prefix[a.experts] * a.row_blocks;
+  const int first = kSplit ? (int)blockIdx.x / splits : (int)blockIdx.x;
+  const int step = kSplit ? tiles : (int)gridDim.x;  // a split grid has a cluster for every tile
+  const int kb0 = kSplit ? (int)((int64_t)a.k_blocks * rank / splits) : 0;
+  const int kb1 = kSplit ? (int)((int64_t)a.k_blocks * (rank + 1) / splits) : a.k_blocks;
 
   if (warp == 0) {
     // ---- TMA producer
     if (lane == 0) {
       int j = 0;
       bool ok = true;
-      for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
+      for (int idx = first; ok && idx < tiles; idx += step) {
         const Tile t = find_tile<TN>(a, prefix, idx);
         const int wrow = t.expert * a.n + t.row_block * kTileRows;
-        for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
+        for (int kb = kb0; kb < kb1; ++kb, ++j) {
           const int s = j % C::kStages;
           if (j >= C::kStages && !wait_bar(abort_flag, bars.empty(s), ((j / C::kStages) - 1) & 1, 0x711)) {
             ok = false;
@@ -276,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kIdesc = idesc_e4m3(kTileRows, TN);
       int j = 0;
       bool ok = true;
-      for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
-        for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
+      for (int idx = first; ok && idx < tiles; idx += step) {
+        for (int kb = kb0; kb < kb1; ++kb, ++j) {
           const int s = j % C::kStages, b = j % C::kBufs;
           if (!wait_bar(abort_flag, bars.full(s), (j / C::kStages) & 1, 0x712) ||
               (j >= C::kBufs && !wait_bar(abort_flag, bars.tempty(b), ((j / C::kBufs) - 1) & 1, 0x713))) {
@@ -299,13 +337,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (!mbar_try_wait(bars.fin(), 0) && clock64() - t0 < kTimeoutCycles) {
       }
     }
-  } else if (warp == 6) {
-    // ---- token scales of each k block into their own ring
+  } else if (warp == C::kEpiWarps + 2) {
+    // ---- scales of each k block into their own ring: a load per block on the
+    // epilogue's path would cost it a memory latency per block
     int j = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
+    for (int idx = first; ok && idx < tiles; idx += step) {
       const Tile t = find_tile<TN>(a, prefix, idx);
-      for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
+      const float* sw = a.w_scales + ((int64_t)t.expert * a.row_blocks + t.row_block) * a.k_blocks;
+      for (int kb = kb0; kb < kb1; ++kb, ++j) {
         const int s = j % C::kScaleStages;
         if (j >= C::kScaleStages &&
             !wait_bar_warp(abort_flag, bars.sempty(s), ((j / C::kScaleStages) - 1) & 1, 0x714)) {
@@ -313,10 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const float* src = a.a_scales + kb * a.a_scale_stride + t.tok0;
+        const uint32_t dst = sbase + C::kOffScales + s * C::kScaleSlot * 4;
         for (int i = lane; i < TN; i += 32) {
           const bool in = t.tok0 + i < t.tok_end;
-          cp_async4(sbase + C::kOffScales + (s * TN + i) * 4, in ? src + i : a.a_scales, in ? 4 : 0);
+          cp_async4(dst + i * 4, in ? src + i : a.a_scales, in ? 4 : 0);
         }
+        if (lane == 0) cp_async4(dst + TN * 4, sw + kb, 4);
         cp_async_arrive(bars.sfull(s));
       }
     }
@@ -325,57 +367,95 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- epilogue: thread = weight row, registers = tokens
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    constexpr int kCols = TN / (C::kEpiWarps / 4);  // tokens of this warp
+    const int half = (warp - 2) >> 2;
+    const int col0 = half * kCols;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col0;
     int j = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
+    for (int idx = first; ok && idx < tiles; idx += step) {
       const Tile t = find_tile<TN>(a, prefix, idx);
-      float2 acc[TN / 2];
+      float2 acc[kCols / 2];
 #pragma unroll
-      for (int i = 0; i < TN / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      const float* sw = a.w_scales + ((int64_t)t.expert * a.row_blocks + t.row_block) * a.k_blocks;
-      float sw_next = __ldg(sw);
-      for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
+      for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int kb = kb0; kb < kb1; ++kb, ++j) {
         const int s = j % C::kScaleStages, b = j % C::kBufs;
-        const float2 w2 = make_float2(sw_next, sw_next);
-        if (kb + 1 < a.k_blocks) sw_next = __ldg(sw + kb + 1);
         if (!wait_bar_warp(abort_flag, bars.sfull(s), (j / C::kScaleStages) & 1, 0x715) ||
             !wait_bar_warp(abort_flag, bars.tfull(b), (j / C::kBufs) & 1, 0x716)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffScales + s * TN * 4);
-#pragma unroll
-        for (int c = 0; c < TN; c += 16) {
+        const float* slot = reinterpret_cast<const float*>(smem + C::kOffScales) + s * C::kScaleSlot;
+        const float4* sc = reinterpret_cast<const float4*>(slot + col0);
+        const float2 w2 = make_float2(slot[TN], slot[TN]);
+        auto add4 = [&](int c, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+          const float4 s4 = sc[c / 4];
+          const float2 s01 = mul2(make_float2(s4.x, s4.y), w2), s23 = mul2(make_float2(s4.z, s4.w), w2);
+          acc[c / 2] = fma2(make_float2(__uint_as_float(r0), __uint_as_float(r1)), s01, acc[c / 2]);
+          acc[c / 2 + 1] = fma2(make_float2(__uint_as_float(r2), __uint_as_float(r3)), s23, acc[c / 2 + 1]);
+        };
+        if (kCols == 16) {
           uint32_t r[16];
-          tmem_ld16(taddr + b * TN + c, r);
+          tmem_ld16(taddr + b * TN, r);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 s4 = sc[c / 4 + i];
-            const float2 s01 = mul2(make_float2(s4.x, s4.y), w2), s23 = mul2(make_float2(s4.z, s4.w), w2);
-            const float2 p01 = make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]));
-            const float2 p23 = make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
-            acc[c / 2 + 2 * i] = fma2(p01, s01, acc[c / 2 + 2 * i]);
-            acc[c / 2 + 2 * i + 1] = fma2(p23, s23, acc[c / 2 + 2 * i + 1]);
-          }
+          for (int i = 0; i < 16; i += 4) add4(i, r[i], r[i + 1], r[i + 2], r[i + 3]);
+        } else if (kCols == 32) {
+          uint32_t r[32];
+          tmem_ld32(taddr + b * TN, r);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) add4(i, r[i], r[i + 1], r[i + 2], r[i + 3]);
+        } else {
+          uint32_t r[64];
+          tmem_ld64(taddr + b * TN, r);
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) add4(i, r[i], r[i + 1], r[i + 2], r[i + 3]);
         }
         tc_fence_before();
-        mbar_arrive(bars.tempty(b));
-        mbar_arrive(bars.sempty(s));
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bars.tempty(b));
+          mbar_arrive(bars.sempty(s));
+        }
       }
+      if (!ok) break;
       const int n = t.row_block * kTileRows + row;
-      if (ok && n < a.n) {
+      if (kSplit) {
+        // tokens [p * slice, (p + 1) * slice) go to CTA p of the cluster: staged
+        // as [token][row] in the ring (idle: the tile's last product has been
+        // read) and moved by the copy engine, one contiguous piece per CTA
+        const int slice = TN / splits;
+        float* stage = reinterpret_cast<float*>(smem) + col0 * kTileRows + row;
 #pragma unroll
-        for (int i = 0; i < TN; ++i) {
-          const int m = t.tok0 + i;
-          const float v = (i & 1) ? acc[i / 2].y : acc[i / 2].x;
-          if (m < t.tok_end) {
-            if (kFp32)
-              static_cast<float*>(a.out)[m * a.ldo + n] = v;
-            else
-              static_cast<__nv_bfloat16*>(a.out)[m * a.ldo + n] = __float2bfloat16_rn(v);
+        for (int i = 0; i < kCols; ++i) stage[i * kTileRows] = (i & 1) ? acc[i / 2].y : acc[i / 2].x;
+        fence_proxy_async_smem();
+        named_bar_sync(1, 32 * C::kEpiWarps);
+        if (warp == 2 && lane < splits) {
+          const uint32_t bytes = (uint32_t)slice * kTileRows * 4;
+          bulk_copy_cluster(mapa(sbase + C::kOffRecv + rank * bytes, lane), sbase + lane * bytes, bytes,
+                            mapa(bars.recv(), lane));
+        }
+        if (!wait_bar_warp<true>(abort_flag, bars.recv(), 0, 0x717)) {
+          ok = false;
+          break;
+        }
+        const float* recv = reinterpret_cast<const float*>(smem + C::kOffRecv) + row;
+        for (int i0 = half * 2; i0 < slice; i0 += 2 * C::kEpiWarps / 4) {  // slices are even
+          float v0 = 0.f, v1 = 0.f;
+#pragma unroll 4
+          for (int p = 0; p < splits; ++p) {
+            v0 += recv[(p * slice + i0) * kTileRows];
+            v1 += recv[(p * slice + i0 + 1) * kTileRows];
           }
+          const int m = t.tok0 + rank * slice + i0;
+          if (n < a.n && m < t.tok_end) store_out(a, kFp32, m, n, v0);
+          if (n < a.n && m + 1 < t.tok_end) store_out(a, kFp32, m + 1, n, v1);
+        }
+      } else if (n < a.n) {
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+          const int m = t.tok0 + col0 + i;
+          if (m < t.tok_end) store_out(a, kFp32, m, n, (i & 1) ? acc[i / 2].y : acc[i / 2].x);
         }
       }
     }
@@ -384,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+  if (kSplit) cluster_sync();  // no peer may still address this CTA's shared memory
 }
 
 // ------------------------------------------------------------------ host side
@@ -415,23 +496,46 @@ static bool make_map(CUtensorMap* map, const void* p, int64_t k, int64_t rows, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int TN, bool kFp32>
-static cudaError_t launch_tn(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, const Args& a,
-                             int sms, cudaStream_t stream) {
+template <int TN, bool kSplit, bool kFp32>
+static cudaError_t launch_kernel(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const Args& a, int64_t grid,
+                                 cudaStream_t stream) {
+  using C = Cfg<TN, kSplit>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(gemm_kernel<TN, kFp32>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<TN>::kSmem);
+    attr_err = cudaFuncSetAttribute(gemm_kernel<TN, kSplit, kFp32>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (attr_err != cudaSuccess) return attr_err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  if (kSplit) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = a.splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<TN, kSplit, kFp32>, tm_w, tm_a, a);
+}
+
+template <int TN, bool kFp32>
+static cudaError_t launch_tn(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, Args a, int sms,
+                             cudaStream_t stream) {
   CUtensorMap tm_w, tm_a;
   if (!make_map(&tm_w, w, k, (int64_t)a.experts * a.n, ldw, kTileRows) || !make_map(&tm_a, act, k, a.m, lda, TN))
     return cudaErrorNotSupported;
-  // at most this many token tiles exist, whatever the offsets say
-  const int64_t tok_tiles = (int64_t)a.m / TN + std::min(a.experts, a.m);
-  const int64_t tiles = std::min<int64_t>(tok_tiles * a.row_blocks, sms);
-  gemm_kernel<TN, kFp32><<<(unsigned)tiles, kThreads, Cfg<TN>::kSmem, stream>>>(tm_w, tm_a, a);
-  return cudaGetLastError();
+  // at most this many tiles exist, whatever the offsets say
+  const int64_t tok_tiles = a.offsets ? (int64_t)a.m / TN + std::min(a.experts, a.m) : ((int64_t)a.m + TN - 1) / TN;
+  const int64_t tiles = tok_tiles * a.row_blocks;
+  a.splits = 1;
+  while (a.splits < 8 && a.splits * 2 * tiles <= sms && a.k_blocks >= a.splits * 4) a.splits *= 2;
+  if (a.splits > 1) return launch_kernel<TN, true, kFp32>(tm_w, tm_a, a, tiles * a.splits, stream);
+  return launch_kernel<TN, false, kFp32>(tm_w, tm_a, a, std::min<int64_t>(tiles, sms), stream);
 }
 
 template <bool kFp32>
@@ -463,6 +567,7 @@ cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda,
   a.k_blocks = (k + gemm8::kBlockK - 1) / gemm8::kBlockK;
   a.row_blocks = (n + gemm8::kTileRows - 1) / gemm8::kTileRows;
   a.experts = experts;
+  a.splits = 1;
   return fp32 ? gemm8::launch_out<true>(act, lda, w, ldw, k, a, sms, stream)
               : gemm8::launch_out<false>(act, lda, w, ldw, k, a, sms, stream);
 }
