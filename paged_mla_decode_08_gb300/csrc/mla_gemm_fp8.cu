@@ -57,7 +57,12 @@ struct Cfg {
   static constexpr int kStage = kStageA + kStageB;
   // partial sums received from the CTAs of a split tile: [source][row][token slice]
   static constexpr int kRecv = kSplit ? kTileRows * TN * 4 : 0;
-  static constexpr int kStages = (200 * 1024 - kRecv) / kStage < 8 ? (200 * 1024 - kRecv) / kStage : 8;
+  // Up to 64 tokens the weights' stream bounds the tile and two CTAs share an
+  // SM: twice the places for clusters (36 of 8 fit instead of 15) and one CTA
+  // loads while the other exchanges.  Wider tiles need the SM's TMEM.
+  static constexpr int kCtasPerSm = TN <= 64 ? 2 : 1;
+  static constexpr int kRing = (kCtasPerSm == 2 ? 106 : 200) * 1024 - kRecv;
+  static constexpr int kStages = kRing / kStage < 8 ? kRing / kStage : 8;
   static constexpr int kScaleStages = 8;
   static constexpr int kScaleSlot = TN + 4;            // token scales, then the weights' scale
   static constexpr int kBufs = 4;
@@ -158,6 +163,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
+// Programmatic dependent launch: wait for the kernels before this one in the
+// stream to be complete; let the next one start its prologue.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Rows [lo, hi) of expert e.  Offsets outside 0 <= lo <= hi <= m own no row
 // (recorded), so no access leaves the arrays.
 __device__ __forceinline__ int2 expert_rows(const Args& a, int e) {
@@ -211,7 +223,7 @@ __device__ __forceinline__ void store_out(const Args& a, bool fp32, int m, int n
 // CTA adding up and storing a slice of the tile's tokens in CTA order (the
 // grid holds one cluster per tile).
 template <int TN, bool kSplit, bool kFp32>
-__global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kCtasPerSm)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const Args a) {
   using C = Cfg<TN, kSplit>;
   extern __shared__ uint8_t smem_raw[];
@@ -250,6 +262,10 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }
+  // all of the above overlaps the kernel before; nothing of its results, or of
+  // what it still reads, is touched before this returns
+  pdl_wait();
+  pdl_launch_dependents();
   if (warp == 2) {
     // token tiles of the experts before each expert
     int run = 0;
@@ -395,16 +411,14 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, 1)
           acc[c / 2] = fma2(make_float2(__uint_as_float(r0), __uint_as_float(r1)), s01, acc[c / 2]);
           acc[c / 2 + 1] = fma2(make_float2(__uint_as_float(r2), __uint_as_float(r3)), s23, acc[c / 2 + 1]);
         };
-        if (kCols == 16) {
-          uint32_t r[16];
-          tmem_ld16(taddr + b * TN, r);
+        if (kCols <= 32) {  // 16 at a time: two CTAs share the register file
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) add4(i, r[i], r[i + 1], r[i + 2], r[i + 3]);
-        } else if (kCols == 32) {
-          uint32_t r[32];
-          tmem_ld32(taddr + b * TN, r);
+          for (int c = 0; c < kCols; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(taddr + b * TN + c, r);
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) add4(i, r[i], r[i + 1], r[i + 2], r[i + 3]);
+            for (int i = 0; i < 16; i += 4) add4(c + i, r[i], r[i + 1], r[i + 2], r[i + 3]);
+          }
         } else {
           uint32_t r[64];
           tmem_ld64(taddr + b * TN, r);
@@ -496,46 +510,88 @@ static bool make_map(CUtensorMap* map, const void* p, int64_t k, int64_t rows, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// One kernel form on one device: its attributes, and how many clusters of 2, 4
+// and 8 CTAs the device holds at once (GPCs of unequal size hold fewer than the
+// SM count suggests).
 template <int TN, bool kSplit, bool kFp32>
-static cudaError_t launch_kernel(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const Args& a, int64_t grid,
-                                 cudaStream_t stream) {
+struct Form {
   using C = Cfg<TN, kSplit>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(gemm_kernel<TN, kSplit, kFp32>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  });
-  if (attr_err != cudaSuccess) return attr_err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  if (kSplit) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = a.splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+  static constexpr auto kKernel = gemm_kernel<TN, kSplit, kFp32>;
+
+  static void config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int64_t grid, int cluster,
+                     cudaStream_t stream) {
+    *cfg = cudaLaunchConfig_t{};
+    cfg->gridDim = dim3((unsigned)grid);
+    cfg->blockDim = dim3(C::kThreads);
+    cfg->dynamicSmemBytes = C::kSmem;
+    cfg->stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg->attrs = attr;
+    cfg->numAttrs = cluster > 1 ? 2 : 1;
   }
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<TN, kSplit, kFp32>, tm_w, tm_a, a);
-}
+  static cudaError_t set_attributes() {
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [] {
+      err = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    });
+    return err;
+  }
+  // clusters of `size` (2, 4, 8) CTAs that run at once; 0 when unknown
+  static int active_clusters(int size) {
+    static std::once_flag once;
+    static int count[3];
+    std::call_once(once, [] {
+      for (int i = 0; i < 3; ++i) {
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        config(&cfg, attr, 2 << i, 2 << i, nullptr);
+        cfg.attrs = attr + 1;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&count[i], kKernel, &cfg) != cudaSuccess) {
+          cudaGetLastError();
+          count[i] = 0;
+        }
+      }
+    });
+    return count[size == 2 ? 0 : size == 4 ? 1 : 2];
+  }
+  static cudaError_t launch(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const Args& a, int64_t grid,
+                            cudaStream_t stream) {
+    const cudaError_t e = set_attributes();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    config(&cfg, attr, grid, a.splits, stream);
+    return cudaLaunchKernelEx(&cfg, kKernel, tm_w, tm_a, a);
+  }
+};
 
 template <int TN, bool kFp32>
 static cudaError_t launch_tn(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, Args a, int sms,
                              cudaStream_t stream) {
+  using Split = Form<TN, true, kFp32>;
+  using Whole = Form<TN, false, kFp32>;
   CUtensorMap tm_w, tm_a;
   if (!make_map(&tm_w, w, k, (int64_t)a.experts * a.n, ldw, kTileRows) || !make_map(&tm_a, act, k, a.m, lda, TN))
     return cudaErrorNotSupported;
   // at most this many tiles exist, whatever the offsets say
   const int64_t tok_tiles = a.offsets ? (int64_t)a.m / TN + std::min(a.experts, a.m) : ((int64_t)a.m + TN - 1) / TN;
   const int64_t tiles = tok_tiles * a.row_blocks;
+  // Split k as long as every cluster runs at once and a CTA keeps two blocks.
   a.splits = 1;
-  while (a.splits < 8 && a.splits * 2 * tiles <= sms && a.k_blocks >= a.splits * 4) a.splits *= 2;
-  if (a.splits > 1) return launch_kernel<TN, true, kFp32>(tm_w, tm_a, a, tiles * a.splits, stream);
-  return launch_kernel<TN, false, kFp32>(tm_w, tm_a, a, std::min<int64_t>(tiles, sms), stream);
+  if (tiles * 2 <= (int64_t)sms * Whole::C::kCtasPerSm) {
+    const cudaError_t e = Split::set_attributes();
+    if (e != cudaSuccess) return e;
+    for (int s = 2; s <= 8 && a.k_blocks >= 2 * s && tiles <= Split::active_clusters(s); s *= 2) a.splits = s;
+  }
+  if (a.splits > 1) return Split::launch(tm_w, tm_a, a, tiles * a.splits, stream);
+  return Whole::launch(tm_w, tm_a, a, std::min<int64_t>(tiles, (int64_t)sms * Whole::C::kCtasPerSm), stream);
 }
 
 template <bool kFp32>

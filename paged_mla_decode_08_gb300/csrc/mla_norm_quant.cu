@@ -44,6 +44,14 @@ __device__ __forceinline__ float silu(float g) {
   return g * (g < 0.f ? e : 1.0f) / (1.0f + e);
 }
 
+// Programmatic dependent launch: this kernel may be scheduled while the one
+// before it in the stream drains; it touches memory only after that one is
+// complete, and lets the next one be scheduled in the same way.
+__device__ __forceinline__ void pdl_sync() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // 8 consecutive columns of a row.  kVec: 16-byte accesses (all 8 present);
 // otherwise element by element, the columns past n reading as 0 and not stored.
 template <bool kVec>
@@ -134,6 +142,7 @@ struct NormArgs {
 // kRes: 0 none, 1 bf16, 2 fp32.
 template <int kChunks, bool kVec, int kRes, bool kE4m3>
 __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
+  pdl_sync();
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ float part[32];
@@ -209,6 +218,7 @@ constexpr int kActThreads = 256;
 // a block's 16 items are 16 neighbouring lanes.
 template <bool kVec, bool kSiluMul, bool kE4m3>
 __global__ void __launch_bounds__(kActThreads) act_quantize_kernel(const ActArgs a) {
+  pdl_sync();
   const int64_t item = (int64_t)blockIdx.x * kActThreads + threadIdx.x;
   const bool live = item < a.items;  // whole half warps: items is a multiple of 16
   const int64_t t = live ? item / a.items_per_row : 0;
@@ -233,14 +243,28 @@ __global__ void __launch_bounds__(kActThreads) act_quantize_kernel(const ActArgs
     store_bf16<kVec>(static_cast<uint16_t*>(a.y) + t * a.y_stride + col, n, v);
 }
 
+template <class Kernel, class A>
+static void launch_pdl(Kernel kernel, unsigned blocks, unsigned threads, cudaStream_t stream, const A& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, a);  // an error is read with cudaGetLastError
+}
+
 static bool multiple(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 template <int kChunks, bool kVec, int kRes>
 static void launch_norm_out(const NormArgs& a, int threads, bool e4m3, cudaStream_t stream) {
   if (e4m3)
-    add_rmsnorm_kernel<kChunks, kVec, kRes, true><<<a.num_tokens, threads, 0, stream>>>(a);
+    launch_pdl(add_rmsnorm_kernel<kChunks, kVec, kRes, true>, a.num_tokens, threads, stream, a);
   else
-    add_rmsnorm_kernel<kChunks, kVec, kRes, false><<<a.num_tokens, threads, 0, stream>>>(a);
+    launch_pdl(add_rmsnorm_kernel<kChunks, kVec, kRes, false>, a.num_tokens, threads, stream, a);
 }
 
 template <int kChunks, bool kVec>
@@ -315,14 +339,14 @@ cudaError_t launch_act_quantize(const void* x, int64_t x_stride, int num_tokens,
   const bool vec = dim % 8 == 0 && x_stride % 8 == 0 && y_stride % 8 == 0 && multiple(x, 16) && multiple(y, e4m3 ? 8 : 16);
   const unsigned blocks = (unsigned)((a.items + kActThreads - 1) / kActThreads);
   if (silu_mul && e4m3)
-    vec ? act_quantize_kernel<true, true, true><<<blocks, kActThreads, 0, stream>>>(a)
-        : act_quantize_kernel<false, true, true><<<blocks, kActThreads, 0, stream>>>(a);
+    vec ? launch_pdl(act_quantize_kernel<true, true, true>, blocks, kActThreads, stream, a)
+        : launch_pdl(act_quantize_kernel<false, true, true>, blocks, kActThreads, stream, a);
   else if (silu_mul)
-    vec ? act_quantize_kernel<true, true, false><<<blocks, kActThreads, 0, stream>>>(a)
-        : act_quantize_kernel<false, true, false><<<blocks, kActThreads, 0, stream>>>(a);
+    vec ? launch_pdl(act_quantize_kernel<true, true, false>, blocks, kActThreads, stream, a)
+        : launch_pdl(act_quantize_kernel<false, true, false>, blocks, kActThreads, stream, a);
   else
-    vec ? act_quantize_kernel<true, false, true><<<blocks, kActThreads, 0, stream>>>(a)
-        : act_quantize_kernel<false, false, true><<<blocks, kActThreads, 0, stream>>>(a);
+    vec ? launch_pdl(act_quantize_kernel<true, false, true>, blocks, kActThreads, stream, a)
+        : launch_pdl(act_quantize_kernel<false, false, true>, blocks, kActThreads, stream, a);
   return cudaGetLastError();
 }
 
