@@ -125,6 +125,11 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
 // Shared memory of this CTA -> shared memory of a CTA of the cluster, completing
 // `bytes` on that CTA's barrier (remote addresses from mapa).
 __device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t mbar) {
@@ -234,8 +239,6 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
   volatile int* abort_flag = reinterpret_cast<volatile int*>(prefix + kMaxExperts + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(prefix + kMaxExperts + 5);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int splits = kSplit ? a.splits : 1;
-  const int rank = kSplit ? (int)cluster_ctarank() : 0;
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -261,6 +264,17 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tmem_relinquish();
+  }
+  const int splits = kSplit ? a.splits : 1;
+  const int rank = kSplit ? (int)cluster_ctarank() : 0;
+  const int first = kSplit ? (int)blockIdx.x / splits : (int)blockIdx.x;
+  const int kb0 = kSplit ? (int)((int64_t)a.k_blocks * rank / splits) : 0;
+  const int kb1 = kSplit ? (int)((int64_t)a.k_blocks * (rank + 1) / splits) : a.k_blocks;
+  if (warp == 0 && lane == 0 && a.offsets == nullptr) {
+    // pull the first weights into L2 while the kernel before this one drains
+    // (a hint: the loads that follow the wait below read what is there then)
+    const int wrow = first / ((a.m + TN - 1) / TN) * kTileRows;
+    for (int kb = kb0; kb < min(kb0 + C::kStages, kb1); ++kb) tma_prefetch_2d(&tm_w, kb * kBlockK, wrow);
   }
   // all of the above overlaps the kernel before; nothing of its results, or of
   // what it still reads, is touched before this returns
@@ -293,10 +307,7 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const int tiles = prefix[a.experts] * a.row_blocks;
-  const int first = kSplit ? (int)blockIdx.x / splits : (int)blockIdx.x;
   const int step = kSplit ? tiles : (int)gridDim.x;  // a split grid has a cluster for every tile
-  const int kb0 = kSplit ? (int)((int64_t)a.k_blocks * rank / splits) : 0;
-  const int kb1 = kSplit ? (int)((int64_t)a.k_blocks * (rank + 1) / splits) : a.k_blocks;
 
   if (warp == 0) {
     // ---- TMA producer
@@ -478,7 +489,11 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
-  if (kSplit) cluster_sync();  // no peer may still address this CTA's shared memory
+  if (kSplit) {
+    // no peer may still address this CTA's shared memory; nothing is published
+    // here, so the arrival need not wait for the output's stores
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -509,6 +524,12 @@ static bool make_map(CUtensorMap* map, const void* p, int64_t k, int64_t rows, i
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+// Stands in for gemm_kernel in the occupancy query, which answers one CTA per SM
+// for any kernel that allocates TMEM (two are resident, by their columns and in
+// fact): same threads and shared memory, no TMEM.
+template <int kThreads, int kCtasPerSm>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) places_kernel() {}
 
 // One kernel form on one device: its attributes, and how many clusters of 2, 4
 // and 8 CTAs the device holds at once (GPCs of unequal size hold fewer than the
@@ -547,13 +568,15 @@ struct Form {
     static std::once_flag once;
     static int count[3];
     std::call_once(once, [] {
+      constexpr auto kPlaces = places_kernel<C::kThreads, C::kCtasPerSm>;
+      const bool ok = cudaFuncSetAttribute(kPlaces, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) == cudaSuccess;
       for (int i = 0; i < 3; ++i) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         config(&cfg, attr, 2 << i, 2 << i, nullptr);
         cfg.attrs = attr + 1;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&count[i], kKernel, &cfg) != cudaSuccess) {
+        if (!ok || cudaOccupancyMaxActiveClusters(&count[i], kPlaces, &cfg) != cudaSuccess) {
           cudaGetLastError();
           count[i] = 0;
         }
