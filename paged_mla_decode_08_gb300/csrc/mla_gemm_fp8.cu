@@ -42,7 +42,8 @@ struct Args {
   const int32_t* offsets; // int32 [experts + 1], nullptr: one group of all rows
   void* out;
   int64_t a_scale_stride, ldo;
-  int m, n, k_blocks, row_blocks, experts;
+  int m, n, k_blocks, row_blocks, experts;  // row_blocks: tiles along the weight rows
+  int scale_rows;  // 128-row blocks of the weights' scales
   int splits;  // CTAs that share a tile's k blocks (a cluster); 1: none
 };
 
@@ -187,6 +188,29 @@ __device__ __forceinline__ int2 expert_rows(const Args& a, int e) {
   return make_int2(lo, hi);
 }
 
+// prefix[e] = token tiles of the experts before e, by one warp
+template <int TN>
+__device__ __forceinline__ void scan_experts(const Args& a, int* prefix, int lane) {
+  int run = 0;
+  for (int e0 = 0; e0 < a.experts; e0 += 32) {
+    const int e = e0 + lane;
+    int c = 0;
+    if (e < a.experts) {
+      const int2 r = expert_rows(a, e);
+      c = (int)(((int64_t)r.y - r.x + TN - 1) / TN);
+    }
+    int inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (e < a.experts) prefix[e] = run + inc - c;
+    run += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) prefix[a.experts] = run;
+}
+
 struct Tile {
   int expert, row_block, tok0, tok_end;
 };
@@ -280,27 +304,7 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
   // what it still reads, is touched before this returns
   pdl_wait();
   pdl_launch_dependents();
-  if (warp == 2) {
-    // token tiles of the experts before each expert
-    int run = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 32) {
-      const int e = e0 + lane;
-      int c = 0;
-      if (e < a.experts) {
-        const int2 r = expert_rows(a, e);
-        c = (int)(((int64_t)r.y - r.x + TN - 1) / TN);
-      }
-      int inc = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (e < a.experts) prefix[e] = run + inc - c;
-      run += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) prefix[a.experts] = run;
-  }
+  if (warp == 2) scan_experts<TN>(a, prefix, lane);
   tc_fence_before();
   __syncthreads();
   if (kSplit) cluster_sync();  // the peers' barriers are initialised before any remote arrival
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
     bool ok = true;
     for (int idx = first; ok && idx < tiles; idx += step) {
       const Tile t = find_tile<TN>(a, prefix, idx);
-      const float* sw = a.w_scales + ((int64_t)t.expert * a.row_blocks + t.row_block) * a.k_blocks;
+      const float* sw = a.w_scales + ((int64_t)t.expert * a.scale_rows + t.row_block) * a.k_blocks;
       for (int kb = kb0; kb < kb1; ++kb, ++j) {
         const int s = j % C::kScaleStages;
         if (j >= C::kScaleStages &&
@@ -496,6 +500,314 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
   }
 }
 
+// ------------------------------------------------------------------ wide tiles
+
+// A pair of CTAs (cta_group::2) computes 256 tokens x 256 weight rows: here the
+// tokens are the M operand, 128 of them per CTA, so an epilogue thread owns one
+// token and 128 weight rows that share one weight scale -- its factor for a k
+// block is one register, not one per column.  Each CTA loads its own 128 tokens
+// and 128 of the weight rows; the pair's tensor cores read both halves, which
+// halves the shared-memory and L2 traffic of a 128 x 256 tile.
+namespace wide {
+
+constexpr int kTileTok = 256, kTileCol = 256;  // of the pair
+constexpr int kHalf = 128;
+constexpr int kStage = 2 * kHalf * kBlockK;    // per CTA: tokens, then weights
+constexpr int kStages = 6;
+constexpr int kScaleStages = 8;
+constexpr int kScaleSlot = kHalf + 4;          // token scales, then two weight scales
+constexpr int kBufs = 2;                       // 2 x 256 TMEM columns
+constexpr int kEpiWarps = 8;
+// warps 0-3: TMA, MMA, scales, idle; 4-11: epilogue (two per TMEM lane quadrant)
+constexpr int kThreads = 384;
+constexpr int kRegsLoad = 56, kRegsEpi = 224;  // 128 x 56 + 256 x 224 = 384 x 168, the launch's registers
+constexpr int kOffScales = kStages * kStage;
+constexpr int kOffPrefix = kOffScales + kScaleStages * kScaleSlot * 4;
+constexpr int kOffBars = kOffPrefix + (kMaxExperts + 8) * 4;
+constexpr int kSmem = kOffBars + 512 + 1024;
+
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Load into this CTA's shared memory, completing on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t cluster_bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+      "[%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs when the products issued so far are done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// Arrive on a barrier of either CTA of the pair (address from mapa).  Only a
+// TMEM buffer's reads precede it, which the tcgen05 fence orders; a release at
+// cluster scope would wait for every store in flight (measured: 1000 cycles).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// The tokens of `t` that this CTA holds start at tok0 + 128 * rank.
+__device__ __forceinline__ Tile find(const Args& a, const int* prefix, int idx) {
+  return find_tile<kTileTok>(a, prefix, idx);  // a.row_blocks counts 256-row tiles here
+}
+
+template <bool kFp32, bool kVec>
+__device__ __forceinline__ void store_row(const Args& a, int64_t m, int n0, const float2 (&acc)[64]) {
+  // 128 consecutive columns of one output row
+  if (kFp32) {
+    float* o = static_cast<float*>(a.out) + m * a.ldo + n0;
+    if (kVec && n0 + 128 <= a.n) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        reinterpret_cast<float4*>(o)[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        if (n0 + 2 * i < a.n) o[2 * i] = acc[i].x;
+        if (n0 + 2 * i + 1 < a.n) o[2 * i + 1] = acc[i].y;
+      }
+    }
+  } else {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + m * a.ldo + n0;
+    if (kVec && n0 + 128 <= a.n) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          __nv_bfloat162 v = __floats2bfloat162_rn(acc[4 * i + q].x, acc[4 * i + q].y);
+          w[q] = *reinterpret_cast<uint32_t*>(&v);
+        }
+        reinterpret_cast<uint4*>(o)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        if (n0 + 2 * i < a.n) o[2 * i] = __float2bfloat16_rn(acc[i].x);
+        if (n0 + 2 * i + 1 < a.n) o[2 * i + 1] = __float2bfloat16_rn(acc[i].y);
+      }
+    }
+  }
+}
+
+// a.row_blocks: 256-row tiles of the weights; a.scale_rows: 128-row blocks.
+template <bool kFp32, bool kVec>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gemm_wide_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const Bars bars{sbase + kOffBars};
+  int* prefix = reinterpret_cast<int*>(smem + kOffPrefix);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(prefix + kMaxExperts + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(prefix + kMaxExperts + 5);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bars.full(i), 1);
+      mbar_init(bars.empty(i), 1);
+    }
+    for (int i = 0; i < kScaleStages; ++i) {
+      mbar_init(bars.sfull(i), 32);
+      mbar_init(bars.sempty(i), kEpiWarps);
+    }
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(bars.tfull(i), 1);
+      mbar_init(bars.tempty(i), 2 * kEpiWarps);  // both CTAs' epilogues (the leader's barrier)
+    }
+    mbar_init(bars.fin(), 1);
+    fence_mbar_init();
+    prefetch_tensormap(&tm_w);
+    prefetch_tensormap(&tm_a);
+  }
+  if (warp == 1) {
+    tmem_alloc2(smem_u32(tmem_slot), kBufs * kTileCol);
+    tmem_relinquish2();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (warp == 2) scan_experts<kTileTok>(a, prefix, lane);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers are initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const int tiles = prefix[a.experts] * a.row_blocks;
+  const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
+    if (warp == 0 && lane == 0) {
+      // ---- TMA producer: both CTAs' copies complete on the leader's barrier
+      int j = 0;
+      bool ok = true;
+      for (int idx = first; ok && idx < tiles; idx += step) {
+        const Tile t = find(a, prefix, idx);
+        const int wrow = t.expert * a.n + t.row_block * kTileCol + rank * kHalf;
+        const int trow = t.tok0 + rank * kHalf;
+        for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
+          const int s = j % kStages;
+          if (j >= kStages && !wait_bar(abort_flag, bars.empty(s), ((j / kStages) - 1) & 1, 0x721)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(bars.full(s), 2 * kStage);
+          const uint32_t full = mapa(bars.full(s), 0);
+          tma_load_2d_pair(sbase + s * kStage, &tm_a, full, kb * kBlockK, trow);
+          tma_load_2d_pair(sbase + s * kStage + kHalf * kBlockK, &tm_w, full, kb * kBlockK, wrow);
+        }
+      }
+      if (rank == 0) {  // the copies in flight must have landed before the pair leaves
+        for (int k = max(0, j - kStages); k < j; ++k) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait(bars.full(k % kStages), (k / kStages) & 1) && clock64() - t0 < kTimeoutCycles) {
+          }
+        }
+      }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ---- MMA issuer (the leader, for the pair)
+      constexpr uint32_t kIdesc = idesc_e4m3(kTileTok, kTileCol);
+      int j = 0;
+      bool ok = true;
+      for (int idx = first; ok && idx < tiles; idx += step) {
+        for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
+          const int s = j % kStages, b = j % kBufs;
+          if (!wait_bar(abort_flag, bars.full(s), (j / kStages) & 1, 0x722) ||
+              (j >= kBufs && !wait_bar(abort_flag, bars.tempty(b), ((j / kBufs) - 1) & 1, 0x723))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ta = sbase + s * kStage, wa = ta + kHalf * kBlockK;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f8_pair(tmem + b * kTileCol, smem_desc(ta + kk * 32, 16, 1024, kSwizzle128B),
+                        smem_desc(wa + kk * 32, 16, 1024, kSwizzle128B), kIdesc, kk > 0);
+          mma_commit_pair(bars.empty(s));
+          mma_commit_pair(bars.tfull(b));
+        }
+      }
+      mma_commit_pair(bars.fin());
+      const long long t0 = clock64();
+      while (!mbar_try_wait(bars.fin(), 0) && clock64() - t0 < kTimeoutCycles) {
+      }
+    } else if (warp == 2) {
+      // ---- scales: this CTA's tokens and the tile's two weight blocks
+      int j = 0;
+      bool ok = true;
+      for (int idx = first; ok && idx < tiles; idx += step) {
+        const Tile t = find(a, prefix, idx);
+        const int trow = t.tok0 + rank * kHalf;
+        const int wb = min(2 * t.row_block + (lane & 1), a.scale_rows - 1);
+        const float* sw = a.w_scales + ((int64_t)t.expert * a.scale_rows + wb) * a.k_blocks;
+        for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
+          const int s = j % kScaleStages;
+          if (j >= kScaleStages && !wait_bar_warp(abort_flag, bars.sempty(s), ((j / kScaleStages) - 1) & 1, 0x724)) {
+            ok = false;
+            break;
+          }
+          const float* src = a.a_scales + kb * a.a_scale_stride + trow;
+          const uint32_t dst = sbase + kOffScales + s * kScaleSlot * 4;
+#pragma unroll
+          for (int i = 0; i < kHalf; i += 32) {
+            const bool in = trow + i + lane < t.tok_end;
+            cp_async4(dst + (i + lane) * 4, in ? src + i + lane : a.a_scales, in ? 4 : 0);
+          }
+          if (lane < 2) cp_async4(dst + (kHalf + lane) * 4, sw + kb, 4);
+          cp_async_arrive(bars.sfull(s));
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  } else {
+    // ---- epilogue: thread = token, registers = 128 weight rows
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kHalf;
+    const uint32_t tempty = mapa(bars.tempty(0), 0);  // the leader's; buffer b at + 8 b
+    int j = 0;
+    bool ok = true;
+    for (int idx = first; ok && idx < tiles; idx += step) {
+      const Tile t = find(a, prefix, idx);
+      float2 acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
+        const int s = j % kScaleStages, b = j % kBufs;
+        if (!wait_bar_warp(abort_flag, bars.sfull(s), (j / kScaleStages) & 1, 0x725) ||
+            !wait_bar_warp(abort_flag, bars.tfull(b), (j / kBufs) & 1, 0x726)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float* slot = reinterpret_cast<const float*>(smem + kOffScales) + s * kScaleSlot;
+        const float f = slot[quad * 32 + lane] * slot[kHalf + half];
+        const float2 f2 = make_float2(f, f);
+        // the next 32 columns are fetched while these are added
+        uint32_t r0[32], r1[32];
+        auto add = [&](int c, const uint32_t (&r)[32]) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            acc[c / 2 + i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[c / 2 + i]);
+        };
+        const uint32_t src = taddr + b * kTileCol;
+        tmem_ld32_async(src, r0);
+        tmem_wait_ld32(r0);
+        tmem_ld32_async(src + 32, r1);
+        add(0, r0);
+        tmem_wait_ld32(r1);
+        tmem_ld32_async(src + 64, r0);
+        add(32, r1);
+        tmem_wait_ld32(r0);
+        tmem_ld32_async(src + 96, r1);
+        add(64, r0);
+        tmem_wait_ld32(r1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_pair(tempty + 8 * b);
+          mbar_arrive(bars.sempty(s));
+        }
+        add(96, r1);
+      }
+      if (!ok) break;
+      const int m = t.tok0 + rank * kHalf + quad * 32 + lane;
+      const int n0 = t.row_block * kTileCol + half * kHalf;
+      if (m < t.tok_end && n0 < a.n) store_row<kFp32, kVec>(a, m, n0, acc);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // every product is read and no remote arrival is left
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc2(tmem, kBufs * kTileCol);
+  cluster_sync();
+}
+
+}  // namespace wide
+
 // ------------------------------------------------------------------ host side
 
 static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -617,10 +929,45 @@ static cudaError_t launch_tn(const void* act, int64_t lda, const void* w, int64_
   return Whole::launch(tm_w, tm_a, a, std::min<int64_t>(tiles, (int64_t)sms * Whole::C::kCtasPerSm), stream);
 }
 
+template <bool kFp32, bool kVec>
+static cudaError_t launch_wide(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, Args a, int sms,
+                               cudaStream_t stream) {
+  constexpr auto kernel = wide::gemm_wide_kernel<kFp32, kVec>;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wide::kSmem);
+  });
+  if (attr_err != cudaSuccess) return attr_err;
+  CUtensorMap tm_w, tm_a;
+  if (!make_map(&tm_w, w, k, (int64_t)a.experts * a.n, ldw, wide::kHalf) || !make_map(&tm_a, act, k, a.m, lda, wide::kHalf))
+    return cudaErrorNotSupported;
+  a.row_blocks = (a.n + wide::kTileCol - 1) / wide::kTileCol;
+  const int64_t tok_tiles = a.offsets ? (int64_t)a.m / wide::kTileTok + std::min(a.experts, a.m)
+                                      : ((int64_t)a.m + wide::kTileTok - 1) / wide::kTileTok;
+  const int64_t pairs = std::min<int64_t>(tok_tiles * a.row_blocks, sms / 2);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(wide::kThreads);
+  cfg.dynamicSmemBytes = wide::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, a);
+}
+
 template <bool kFp32>
 static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, const Args& a,
                               int sms, cudaStream_t stream) {
   const int64_t per_expert = ((int64_t)a.m + a.experts - 1) / a.experts;
+  if (per_expert >= 256) {
+    const bool vec = a.ldo % (kFp32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+    return vec ? launch_wide<kFp32, true>(act, lda, w, ldw, k, a, sms, stream)
+               : launch_wide<kFp32, false>(act, lda, w, ldw, k, a, sms, stream);
+  }
   if (per_expert <= 16) return launch_tn<16, kFp32>(act, lda, w, ldw, k, a, sms, stream);
   if (per_expert <= 32) return launch_tn<32, kFp32>(act, lda, w, ldw, k, a, sms, stream);
   if (per_expert <= 64) return launch_tn<64, kFp32>(act, lda, w, ldw, k, a, sms, stream);
@@ -645,6 +992,7 @@ cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda,
   a.n = n;
   a.k_blocks = (k + gemm8::kBlockK - 1) / gemm8::kBlockK;
   a.row_blocks = (n + gemm8::kTileRows - 1) / gemm8::kTileRows;
+  a.scale_rows = a.row_blocks;
   a.experts = experts;
   a.splits = 1;
   return fp32 ? gemm8::launch_out<true>(act, lda, w, ldw, k, a, sms, stream)
