@@ -87,6 +87,20 @@ struct Bars {
   __device__ uint32_t recv() const { return base + 8 * 57; }
 };
 
+// Position in a ring of N slots: the slot, and the parity of its current pass.
+// A barrier is waited for at `phase` by the reader of its slot, and at
+// `phase ^ 1` by the writer (which passes at once in the first pass).
+template <int N>
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 // Bounded wait; false: gave up here or elsewhere in the CTA.
 template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar(volatile int* abort_flag, uint32_t bar, uint32_t parity, int code) {
@@ -108,12 +122,37 @@ __device__ __forceinline__ bool wait_bar_warp(volatile int* abort_flag, uint32_t
   return __all_sync(0xffffffffu, ok);
 }
 
-// D[tmem] (+)= A[smem desc] * B[smem desc]^T, 8-bit operands, K = 32
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Wait at a role's end: limited, without a verdict.
+__device__ __forceinline__ void wait_limited(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity) && clock64() - t0 < kTimeoutCycles) {
+  }
+}
+// The last `issued` (at most N) uses of the producer's ring are released.
+template <int N>
+__device__ __forceinline__ void drain(Ring<N> ring, int issued, const Bars& bars) {
+  const long long t0 = clock64();
+  for (int k = 0; k < N; ++k, ring.next()) {  // from the oldest slot on
+    if (k < N - issued) continue;             // never used
+    while (!mbar_try_wait(bars.empty(ring.slot), ring.phase ^ 1) && clock64() - t0 < kTimeoutCycles) {
+    }
+  }
+}
+
+// Shared-memory operand descriptors here differ in the start address alone (the
+// low word): rows of 128 bytes in the 128-byte swizzle, groups of 8 rows 1 KB
+// apart.  The issuing thread adds to the low word instead of building each
+// descriptor, which is most of its work per k block.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (kSwizzle128B << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
+
+// D[tmem] (+)= A[smem] * B[smem]^T, 8-bit operands, K = 32; a, b: low words
+__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
       : "memory");
 }
 // fp32 accumulator, e4m3 x e4m3, both K-major
@@ -317,13 +356,14 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
     // ---- TMA producer
     if (lane == 0) {
       int j = 0;
+      Ring<C::kStages> ring;
       bool ok = true;
       for (int idx = first; ok && idx < tiles; idx += step) {
         const Tile t = find_tile<TN>(a, prefix, idx);
         const int wrow = t.expert * a.n + t.row_block * kTileRows;
-        for (int kb = kb0; kb < kb1; ++kb, ++j) {
-          const int s = j % C::kStages;
-          if (j >= C::kStages && !wait_bar(abort_flag, bars.empty(s), ((j / C::kStages) - 1) & 1, 0x711)) {
+        for (int kb = kb0; kb < kb1; ++kb, ++j, ring.next()) {
+          const uint32_t s = ring.slot;
+          if (!wait_bar(abort_flag, bars.empty(s), ring.phase ^ 1, 0x711)) {
             ok = false;
             break;
           }
@@ -332,54 +372,48 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
           tma_load_2d(sbase + s * C::kStage + C::kStageA, &tm_a, bars.full(s), kb * kBlockK, t.tok0);
         }
       }
-      // the copies in flight must have landed before the CTA leaves
-      for (int k = max(0, j - C::kStages); k < j; ++k) {
-        const long long t0 = clock64();
-        while (!mbar_try_wait(bars.full(k % C::kStages), (k / C::kStages) & 1) && clock64() - t0 < kTimeoutCycles) {
-        }
-      }
+      // the copies in flight, and the arrivals that release their stages, must
+      // have landed before the CTA leaves
+      drain<C::kStages>(ring, j, bars);
     }
   } else if (warp == 1) {
     // ---- MMA issuer
     if (lane == 0) {
       constexpr uint32_t kIdesc = idesc_e4m3(kTileRows, TN);
-      int j = 0;
+      const uint32_t wa0 = desc_low(sbase), ta0 = desc_low(sbase + C::kStageA);
+      Ring<C::kStages> ring;
+      Ring<C::kBufs> buf;
       bool ok = true;
       for (int idx = first; ok && idx < tiles; idx += step) {
-        for (int kb = kb0; kb < kb1; ++kb, ++j) {
-          const int s = j % C::kStages, b = j % C::kBufs;
-          if (!wait_bar(abort_flag, bars.full(s), (j / C::kStages) & 1, 0x712) ||
-              (j >= C::kBufs && !wait_bar(abort_flag, bars.tempty(b), ((j / C::kBufs) - 1) & 1, 0x713))) {
+        for (int kb = kb0; kb < kb1; ++kb, ring.next(), buf.next()) {
+          if (!wait_bar(abort_flag, bars.tempty(buf.slot), buf.phase ^ 1, 0x713) ||
+              !wait_bar(abort_flag, bars.full(ring.slot), ring.phase, 0x712)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t wa = sbase + s * C::kStage, ta = wa + C::kStageA;
+          const uint32_t wa = wa0 + ring.slot * (C::kStage >> 4), ta = ta0 + ring.slot * (C::kStage >> 4);
+          const uint32_t d = tmem + buf.slot * TN;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f8(tmem + b * TN, smem_desc(wa + kk * 32, 16, 1024, kSwizzle128B),
-                   smem_desc(ta + kk * 32, 16, 1024, kSwizzle128B), kIdesc, kk > 0);
-          mma_commit(bars.empty(s));
-          mma_commit(bars.tfull(b));
+          for (int kk = 0; kk < 4; ++kk) mma_f8(d, wa + 2 * kk, ta + 2 * kk, kIdesc, kk > 0);
+          mma_commit(bars.empty(ring.slot));
+          mma_commit(bars.tfull(buf.slot));
         }
       }
       mma_commit(bars.fin());  // everything issued is done before TMEM is released
-      const long long t0 = clock64();
-      while (!mbar_try_wait(bars.fin(), 0) && clock64() - t0 < kTimeoutCycles) {
-      }
+      wait_limited(bars.fin(), 0);
     }
   } else if (warp == C::kEpiWarps + 2) {
     // ---- scales of each k block into their own ring: a load per block on the
     // epilogue's path would cost it a memory latency per block
-    int j = 0;
+    Ring<C::kScaleStages> ring;
     bool ok = true;
     for (int idx = first; ok && idx < tiles; idx += step) {
       const Tile t = find_tile<TN>(a, prefix, idx);
       const float* sw = a.w_scales + ((int64_t)t.expert * a.scale_rows + t.row_block) * a.k_blocks;
-      for (int kb = kb0; kb < kb1; ++kb, ++j) {
-        const int s = j % C::kScaleStages;
-        if (j >= C::kScaleStages &&
-            !wait_bar_warp(abort_flag, bars.sempty(s), ((j / C::kScaleStages) - 1) & 1, 0x714)) {
+      for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+        const uint32_t s = ring.slot;
+        if (!wait_bar_warp(abort_flag, bars.sempty(s), ring.phase ^ 1, 0x714)) {
           ok = false;
           break;
         }
@@ -402,17 +436,18 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
     const int half = (warp - 2) >> 2;
     const int col0 = half * kCols;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col0;
-    int j = 0;
+    Ring<C::kScaleStages> ring;
+    Ring<C::kBufs> buf;
     bool ok = true;
     for (int idx = first; ok && idx < tiles; idx += step) {
       const Tile t = find_tile<TN>(a, prefix, idx);
       float2 acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      for (int kb = kb0; kb < kb1; ++kb, ++j) {
-        const int s = j % C::kScaleStages, b = j % C::kBufs;
-        if (!wait_bar_warp(abort_flag, bars.sfull(s), (j / C::kScaleStages) & 1, 0x715) ||
-            !wait_bar_warp(abort_flag, bars.tfull(b), (j / C::kBufs) & 1, 0x716)) {
+      for (int kb = kb0; kb < kb1; ++kb, ring.next(), buf.next()) {
+        const uint32_t s = ring.slot, b = buf.slot;
+        if (!wait_bar_warp(abort_flag, bars.sfull(s), ring.phase, 0x715) ||
+            !wait_bar_warp(abort_flag, bars.tfull(b), buf.phase, 0x716)) {
           ok = false;
           break;
         }
@@ -513,15 +548,20 @@ namespace wide {
 constexpr int kTileTok = 256, kTileCol = 256;  // of the pair
 constexpr int kHalf = 128;
 constexpr int kStage = 2 * kHalf * kBlockK;    // per CTA: tokens, then weights
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kScaleStages = 8;
 constexpr int kScaleSlot = kHalf + 4;          // token scales, then two weight scales
 constexpr int kBufs = 2;                       // 2 x 256 TMEM columns
-constexpr int kEpiWarps = 8;
-// warps 0-3: TMA, MMA, scales, idle; 4-11: epilogue (two per TMEM lane quadrant)
-constexpr int kThreads = 384;
-constexpr int kRegsLoad = 56, kRegsEpi = 224;  // 128 x 56 + 256 x 224 = 384 x 168, the launch's registers
-constexpr int kOffScales = kStages * kStage;
+// warps 0-3: TMA, MMA, scales, idle; 4-19: epilogue, four per TMEM lane quadrant
+// with 64 columns each.  A k block costs an epilogue warp a chain of latencies
+// (barriers, TMEM reads, the buffer's release) of about twice the pair's 512 MMA
+// cycles; four warps per scheduler overlap theirs (two took 1000 cycles a block).
+constexpr int kEpiWarps = 16;
+constexpr int kCols = kTileCol / (kEpiWarps / 4);
+constexpr int kThreads = 32 * (4 + kEpiWarps);
+constexpr int kStaging = 32 * 64;              // per epilogue warp: 64 bytes of each of its 32 output rows
+constexpr int kOffStaging = kStages * kStage;
+constexpr int kOffScales = kOffStaging + kEpiWarps * kStaging;
 constexpr int kOffPrefix = kOffScales + kScaleStages * kScaleSlot * 4;
 constexpr int kOffBars = kOffPrefix + (kMaxExperts + 8) * 4;
 constexpr int kSmem = kOffBars + 512 + 1024;
@@ -543,11 +583,12 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y)
       : "memory");
 }
-__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
       : "memory");
 }
 // Arrive on the barrier at this offset in both CTAs when the products issued so far are done.
@@ -570,42 +611,66 @@ __device__ __forceinline__ Tile find(const Args& a, const int* prefix, int idx) 
   return find_tile<kTileTok>(a, prefix, idx);  // a.row_blocks counts 256-row tiles here
 }
 
+// The warp's 32 rows x kCols columns of results, through shared memory in
+// pieces of 64 bytes a row: stored straight from the registers, every
+// instruction would touch 32 rows (measured: 3400 cycles a tile).
 template <bool kFp32, bool kVec>
-__device__ __forceinline__ void store_row(const Args& a, int64_t m, int n0, const float2 (&acc)[64]) {
-  // 128 consecutive columns of one output row
-  if (kFp32) {
-    float* o = static_cast<float*>(a.out) + m * a.ldo + n0;
-    if (kVec && n0 + 128 <= a.n) {
+__device__ __forceinline__ void store_rows(const Args& a, uint32_t staging, int m0, int tok_end, int n0, int lane,
+                                           const float2 (&acc)[kCols / 2]) {
+  constexpr int kPiece = kFp32 ? 16 : 32;  // columns of a piece
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        reinterpret_cast<float4*>(o)[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
-    } else {
+  for (int p = 0; p < kCols / kPiece; ++p) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        if (n0 + 2 * i < a.n) o[2 * i] = acc[i].x;
-        if (n0 + 2 * i + 1 < a.n) o[2 * i + 1] = acc[i].y;
-      }
-    }
-  } else {
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + m * a.ldo + n0;
-    if (kVec && n0 + 128 <= a.n) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
+    for (int q = 0; q < 4; ++q) {
+      uint4 v;
+      if (kFp32) {
+        const float2 x = acc[(p * kPiece + 4 * q) / 2], y = acc[(p * kPiece + 4 * q) / 2 + 1];
+        v = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+      } else {
         uint32_t w[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          __nv_bfloat162 v = __floats2bfloat162_rn(acc[4 * i + q].x, acc[4 * i + q].y);
-          w[q] = *reinterpret_cast<uint32_t*>(&v);
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = acc[(p * kPiece + 8 * q) / 2 + i];
+          __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+          w[i] = *reinterpret_cast<uint32_t*>(&b);
         }
-        reinterpret_cast<uint4*>(o)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      st_shared_v4(staging + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), v);
+    }
+    __syncwarp();
+    const int n = n0 + p * kPiece;
+    if (kVec && n + kPiece <= a.n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2), q = lane & 3;
+        const uint4 v = ld_shared_v4(staging + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+        if (m0 + r < tok_end) {
+          const int64_t at = (m0 + r) * a.ldo + n + q * (kFp32 ? 4 : 8);
+          if (kFp32)
+            *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + at) = v;
+          else
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at) = v;
+        }
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        if (n0 + 2 * i < a.n) o[2 * i] = __float2bfloat16_rn(acc[i].x);
-        if (n0 + 2 * i + 1 < a.n) o[2 * i + 1] = __float2bfloat16_rn(acc[i].y);
+      const int c = lane & (kPiece - 1);
+      for (int r = lane / kPiece; r < 32; r += 32 / kPiece) {
+        const uint32_t at = staging + r * 64 + (((c / (kFp32 ? 4 : 8)) ^ ((r >> 1) & 3)) << 4);
+        if (m0 + r < tok_end && n + c < a.n) {
+          if (kFp32) {
+            uint32_t v;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at + (c & 3) * 4) : "memory");
+            static_cast<float*>(a.out)[(m0 + r) * a.ldo + n + c] = __uint_as_float(v);
+          } else {
+            uint16_t v;
+            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(at + (c & 7) * 2) : "memory");
+            static_cast<uint16_t*>(a.out)[(m0 + r) * a.ldo + n + c] = v;
+          }
+        }
       }
     }
+    __syncwarp();
   }
 }
 
@@ -658,73 +723,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
     if (warp == 0 && lane == 0) {
       // ---- TMA producer: both CTAs' copies complete on the leader's barrier
       int j = 0;
+      Ring<kStages> ring;
+      const uint32_t full0 = mapa(bars.full(0), 0);
       bool ok = true;
       for (int idx = first; ok && idx < tiles; idx += step) {
         const Tile t = find(a, prefix, idx);
         const int wrow = t.expert * a.n + t.row_block * kTileCol + rank * kHalf;
         const int trow = t.tok0 + rank * kHalf;
-        for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
-          const int s = j % kStages;
-          if (j >= kStages && !wait_bar(abort_flag, bars.empty(s), ((j / kStages) - 1) & 1, 0x721)) {
+        for (int kb = 0; kb < a.k_blocks; ++kb, ++j, ring.next()) {
+          const uint32_t s = ring.slot;
+          if (!wait_bar(abort_flag, bars.empty(s), ring.phase ^ 1, 0x721)) {
             ok = false;
             break;
           }
           if (rank == 0) mbar_arrive_expect_tx(bars.full(s), 2 * kStage);
-          const uint32_t full = mapa(bars.full(s), 0);
+          const uint32_t full = full0 + 8 * s;
           tma_load_2d_pair(sbase + s * kStage, &tm_a, full, kb * kBlockK, trow);
           tma_load_2d_pair(sbase + s * kStage + kHalf * kBlockK, &tm_w, full, kb * kBlockK, wrow);
         }
       }
-      if (rank == 0) {  // the copies in flight must have landed before the pair leaves
-        for (int k = max(0, j - kStages); k < j; ++k) {
-          const long long t0 = clock64();
-          while (!mbar_try_wait(bars.full(k % kStages), (k / kStages) & 1) && clock64() - t0 < kTimeoutCycles) {
-          }
-        }
-      }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // The pair's products release the stages by arrivals in both CTAs: a CTA
+      // that left before the last ones came in would have them land in the
+      // shared memory of whoever runs there next.  (They also follow the copies.)
+      drain<kStages>(ring, j, bars);
+    } else if (warp == 1 && lane == 0 && rank == 1) {
+      wait_limited(bars.fin(), 0);  // the leader's last arrival here
+    } else if (warp == 1 && lane == 0) {
       // ---- MMA issuer (the leader, for the pair)
       constexpr uint32_t kIdesc = idesc_e4m3(kTileTok, kTileCol);
-      int j = 0;
+      const uint32_t ta0 = desc_low(sbase), wa0 = desc_low(sbase + kHalf * kBlockK);
+      Ring<kStages> ring;
+      Ring<kBufs> buf;
       bool ok = true;
       for (int idx = first; ok && idx < tiles; idx += step) {
-        for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
-          const int s = j % kStages, b = j % kBufs;
-          if (!wait_bar(abort_flag, bars.full(s), (j / kStages) & 1, 0x722) ||
-              (j >= kBufs && !wait_bar(abort_flag, bars.tempty(b), ((j / kBufs) - 1) & 1, 0x723))) {
+        for (int kb = 0; kb < a.k_blocks; ++kb, ring.next(), buf.next()) {
+          if (!wait_bar(abort_flag, bars.tempty(buf.slot), buf.phase ^ 1, 0x723) ||
+              !wait_bar(abort_flag, bars.full(ring.slot), ring.phase, 0x722)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t ta = sbase + s * kStage, wa = ta + kHalf * kBlockK;
+          const uint32_t ta = ta0 + ring.slot * (kStage >> 4), wa = wa0 + ring.slot * (kStage >> 4);
+          const uint32_t d = tmem + buf.slot * kTileCol;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f8_pair(tmem + b * kTileCol, smem_desc(ta + kk * 32, 16, 1024, kSwizzle128B),
-                        smem_desc(wa + kk * 32, 16, 1024, kSwizzle128B), kIdesc, kk > 0);
-          mma_commit_pair(bars.empty(s));
-          mma_commit_pair(bars.tfull(b));
+          for (int kk = 0; kk < 4; ++kk) mma_f8_pair(d, ta + 2 * kk, wa + 2 * kk, kIdesc, kk > 0);
+          mma_commit_pair(bars.empty(ring.slot));
+          mma_commit_pair(bars.tfull(buf.slot));
         }
       }
       mma_commit_pair(bars.fin());
-      const long long t0 = clock64();
-      while (!mbar_try_wait(bars.fin(), 0) && clock64() - t0 < kTimeoutCycles) {
-      }
+      wait_limited(bars.fin(), 0);
     } else if (warp == 2) {
       // ---- scales: this CTA's tokens and the tile's two weight blocks
-      int j = 0;
+      Ring<kScaleStages> ring;
       bool ok = true;
       for (int idx = first; ok && idx < tiles; idx += step) {
         const Tile t = find(a, prefix, idx);
         const int trow = t.tok0 + rank * kHalf;
         const int wb = min(2 * t.row_block + (lane & 1), a.scale_rows - 1);
         const float* sw = a.w_scales + ((int64_t)t.expert * a.scale_rows + wb) * a.k_blocks;
-        for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
-          const int s = j % kScaleStages;
-          if (j >= kScaleStages && !wait_bar_warp(abort_flag, bars.sempty(s), ((j / kScaleStages) - 1) & 1, 0x724)) {
+        for (int kb = 0; kb < a.k_blocks; ++kb, ring.next()) {
+          const uint32_t s = ring.slot;
+          if (!wait_bar_warp(abort_flag, bars.sempty(s), ring.phase ^ 1, 0x724)) {
             ok = false;
             break;
           }
@@ -742,60 +805,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
-    // ---- epilogue: thread = token, registers = 128 weight rows
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
-    const int quad = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kHalf;
+    // ---- epilogue: thread = token, registers = 64 weight rows
+    const int quad = warp & 3, part = (warp - 4) >> 2;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * kCols;
     const uint32_t tempty = mapa(bars.tempty(0), 0);  // the leader's; buffer b at + 8 b
-    int j = 0;
+    const uint32_t staging = sbase + kOffStaging + (warp - 4) * kStaging;
+    Ring<kScaleStages> ring;
+    Ring<kBufs> buf;
     bool ok = true;
+    // factor of this thread's token and weight block for the next k block
+    auto factor = [&](float* f) {
+      const uint32_t s = ring.slot;
+      if (!wait_bar_warp(abort_flag, bars.sfull(s), ring.phase, 0x725)) return false;
+      const float* slot = reinterpret_cast<const float*>(smem + kOffScales) + s * kScaleSlot;
+      *f = slot[quad * 32 + lane] * slot[kHalf + (part >> 1)];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars.sempty(s));
+      return true;
+    };
     for (int idx = first; ok && idx < tiles; idx += step) {
       const Tile t = find(a, prefix, idx);
-      float2 acc[64];
+      float2 acc[kCols / 2];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
-        const int s = j % kScaleStages, b = j % kBufs;
-        if (!wait_bar_warp(abort_flag, bars.sfull(s), (j / kScaleStages) & 1, 0x725) ||
-            !wait_bar_warp(abort_flag, bars.tfull(b), (j / kBufs) & 1, 0x726)) {
+      for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int kb = 0; kb < a.k_blocks; ++kb, ring.next(), buf.next()) {
+        const uint32_t b = buf.slot;
+        float f;
+        if (!factor(&f) || !wait_bar_warp(abort_flag, bars.tfull(b), buf.phase, 0x726)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const float* slot = reinterpret_cast<const float*>(smem + kOffScales) + s * kScaleSlot;
-        const float f = slot[quad * 32 + lane] * slot[kHalf + half];
         const float2 f2 = make_float2(f, f);
-        // the next 32 columns are fetched while these are added
-        uint32_t r0[32], r1[32];
-        auto add = [&](int c, const uint32_t (&r)[32]) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            acc[c / 2 + i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[c / 2 + i]);
-        };
         const uint32_t src = taddr + b * kTileCol;
-        tmem_ld32_async(src, r0);
-        tmem_wait_ld32(r0);
-        tmem_ld32_async(src + 32, r1);
-        add(0, r0);
-        tmem_wait_ld32(r1);
-        tmem_ld32_async(src + 64, r0);
-        add(32, r1);
-        tmem_wait_ld32(r0);
-        tmem_ld32_async(src + 96, r1);
-        add(64, r0);
-        tmem_wait_ld32(r1);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_pair(tempty + 8 * b);
-          mbar_arrive(bars.sempty(s));
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {  // 16 at a time: 96 registers a thread
+          uint32_t r[16];
+          tmem_ld16(src + c, r);
+          if (c + 16 == kCols) {  // the buffer is read: release it before the last additions
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(tempty + 8 * b);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            acc[c / 2 + i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[c / 2 + i]);
         }
-        add(96, r1);
       }
       if (!ok) break;
-      const int m = t.tok0 + rank * kHalf + quad * 32 + lane;
-      const int n0 = t.row_block * kTileCol + half * kHalf;
-      if (m < t.tok_end && n0 < a.n) store_row<kFp32, kVec>(a, m, n0, acc);
+      store_rows<kFp32, kVec>(a, staging, t.tok0 + rank * kHalf + quad * 32, t.tok_end,
+                              t.row_block * kTileCol + part * kCols, lane, acc);
     }
   }
   tc_fence_before();
