@@ -197,8 +197,16 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(x.u), "l"(y.u));
   return d.f;
 }
-// 32 lanes x 16 columns with the wait in the same statement
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+// 32 lanes x 8 or 16 columns with the wait in the same statement
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
       "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
@@ -324,6 +332,7 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
     prefetch_tensormap(&tm_w);
     prefetch_tensormap(&tm_a);
   }
+  __syncwarp();
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tmem_relinquish();
@@ -344,6 +353,9 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
   pdl_wait();
   pdl_launch_dependents();
   if (warp == 2) scan_experts<TN>(a, prefix, lane);
+  // every warp whole again before each .aligned instruction (the barriers, the
+  // TMEM calls): executed by parts of a warp they are undefined
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (kSplit) cluster_sync();  // the peers' barriers are initialised before any remote arrival
@@ -461,13 +473,14 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
           acc[c / 2] = fma2(make_float2(__uint_as_float(r0), __uint_as_float(r1)), s01, acc[c / 2]);
           acc[c / 2 + 1] = fma2(make_float2(__uint_as_float(r2), __uint_as_float(r3)), s23, acc[c / 2 + 1]);
         };
-        if (kCols <= 32) {  // 16 at a time: two CTAs share the register file
+        if (kCols <= 32) {  // few at a time: two CTAs share the register file
+          constexpr int kChunk = kSplit && kCols == 32 ? 8 : 16;
 #pragma unroll
-          for (int c = 0; c < kCols; c += 16) {
-            uint32_t r[16];
-            tmem_ld16(taddr + b * TN + c, r);
+          for (int c = 0; c < kCols; c += kChunk) {
+            uint32_t r[kChunk];
+            tmem_ld(taddr + b * TN + c, r);
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) add4(c + i, r[i], r[i + 1], r[i + 2], r[i + 3]);
+            for (int i = 0; i < kChunk; i += 4) add4(c + i, r[i], r[i + 1], r[i + 2], r[i + 3]);
           }
         } else {
           uint32_t r[64];
@@ -493,6 +506,7 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
 #pragma unroll
         for (int i = 0; i < kCols; ++i) stage[i * kTileRows] = (i & 1) ? acc[i / 2].y : acc[i / 2].x;
         fence_proxy_async_smem();
+        __syncwarp();
         named_bar_sync(1, 32 * C::kEpiWarps);
         if (warp == 2 && lane < splits) {
           const uint32_t bytes = (uint32_t)slice * kTileRows * 4;
@@ -524,6 +538,7 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
       }
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -622,10 +637,13 @@ __device__ __forceinline__ void store_rows(const Args& a, uint32_t staging, int 
   for (int p = 0; p < kCols / kPiece; ++p) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      uint4 v;
-      if (kFp32) {
-        const float2 x = acc[(p * kPiece + 4 * q) / 2], y = acc[(p * kPiece + 4 * q) / 2 + 1];
-        v = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+      const uint32_t at = staging + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
+      if (kFp32) {  // pairs, as the sums are held
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 x = acc[(p * kPiece + 4 * q) / 2 + i];
+          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at + 8 * i), "f"(x.x), "f"(x.y) : "memory");
+        }
       } else {
         uint32_t w[4];
 #pragma unroll
@@ -634,14 +652,13 @@ __device__ __forceinline__ void store_rows(const Args& a, uint32_t staging, int 
           __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
           w[i] = *reinterpret_cast<uint32_t*>(&b);
         }
-        v = make_uint4(w[0], w[1], w[2], w[3]);
+        st_shared_v4(at, make_uint4(w[0], w[1], w[2], w[3]));
       }
-      st_shared_v4(staging + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), v);
     }
     __syncwarp();
     const int n = n0 + p * kPiece;
     if (kVec && n + kPiece <= a.n) {
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < 4; ++i) {
         const int r = 8 * i + (lane >> 2), q = lane & 3;
         const uint4 v = ld_shared_v4(staging + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
@@ -655,6 +672,7 @@ __device__ __forceinline__ void store_rows(const Args& a, uint32_t staging, int 
       }
     } else {
       const int c = lane & (kPiece - 1);
+#pragma unroll 1
       for (int r = lane / kPiece; r < 32; r += 32 / kPiece) {
         const uint32_t at = staging + r * 64 + (((c / (kFp32 ? 4 : 8)) ^ ((r >> 1) & 3)) << 4);
         if (m0 + r < tok_end && n + c < a.n) {
@@ -707,6 +725,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tm_w);
     prefetch_tensormap(&tm_a);
   }
+  __syncwarp();
   if (warp == 1) {
     tmem_alloc2(smem_u32(tmem_slot), kBufs * kTileCol);
     tmem_relinquish2();
@@ -714,6 +733,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
   if (warp == 2) scan_experts<kTileTok>(a, prefix, lane);
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the peer's barriers are initialised before any remote arrival
@@ -841,7 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kCols; c += 16) {  // 16 at a time: 96 registers a thread
           uint32_t r[16];
-          tmem_ld16(src + c, r);
+          tmem_ld(src + c, r);
           if (c + 16 == kCols) {  // the buffer is read: release it before the last additions
             tc_fence_before();
             __syncwarp();
@@ -857,6 +877,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                               t.row_block * kTileCol + part * kCols, lane, acc);
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // every product is read and no remote arrival is left
