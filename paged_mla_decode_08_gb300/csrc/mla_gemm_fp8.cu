@@ -122,6 +122,33 @@ __device__ __forceinline__ bool wait_bar_warp(volatile int* abort_flag, uint32_t
   return __all_sync(0xffffffffu, ok);
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+// wait_bar_warp for the issuing warp.  The first tries loop inside one
+// statement and the verdict is a vote, so the compiler sees no divergence and
+// keeps the ring's state, the descriptors and the branch in uniform registers:
+// the loop around a product's issue is then a handful of instructions (by one
+// lane under `if (lane == 0)` it took 1000 cycles per k block, twice the
+// product's own time).
+__device__ __forceinline__ bool wait_bar_uniform(volatile int* abort_flag, uint32_t bar, uint32_t parity, int code) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+      "TRY:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+      "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 64;\n\t@q bra TRY;\n"
+      "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (__all_sync(0xffffffffu, ok)) return true;
+  return wait_bar_warp(abort_flag, bar, parity, code);
+}
+
 // Wait at a role's end: limited, without a verdict.
 __device__ __forceinline__ void wait_limited(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -309,7 +336,7 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
   int* prefix = reinterpret_cast<int*>(smem + C::kOffPrefix);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(prefix + kMaxExperts + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(prefix + kMaxExperts + 5);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -389,29 +416,33 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
       drain<C::kStages>(ring, j, bars);
     }
   } else if (warp == 1) {
-    // ---- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kIdesc = idesc_e4m3(kTileRows, TN);
-      const uint32_t wa0 = desc_low(sbase), ta0 = desc_low(sbase + C::kStageA);
-      Ring<C::kStages> ring;
-      Ring<C::kBufs> buf;
-      bool ok = true;
-      for (int idx = first; ok && idx < tiles; idx += step) {
-        for (int kb = kb0; kb < kb1; ++kb, ring.next(), buf.next()) {
-          if (!wait_bar(abort_flag, bars.tempty(buf.slot), buf.phase ^ 1, 0x713) ||
-              !wait_bar(abort_flag, bars.full(ring.slot), ring.phase, 0x712)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t wa = wa0 + ring.slot * (C::kStage >> 4), ta = ta0 + ring.slot * (C::kStage >> 4);
-          const uint32_t d = tmem + buf.slot * TN;
+    // ---- MMA issuer: the whole warp runs the loop, one lane issues
+    constexpr uint32_t kIdesc = idesc_e4m3(kTileRows, TN);
+    const uint32_t wa0 = desc_low(sbase), ta0 = desc_low(sbase + C::kStageA);
+    const bool issuer = elect_one();
+    Ring<C::kStages> ring;
+    Ring<C::kBufs> buf;
+    bool ok = true;
+    for (int idx = first; ok && idx < tiles; idx += step) {
+      for (int kb = kb0; kb < kb1; ++kb, ring.next(), buf.next()) {
+        if (!wait_bar_uniform(abort_flag, bars.full(ring.slot), ring.phase, 0x712) ||
+            !wait_bar_uniform(abort_flag, bars.tempty(buf.slot), buf.phase ^ 1, 0x713)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t wa = wa0 + ring.slot * (C::kStage >> 4), ta = ta0 + ring.slot * (C::kStage >> 4);
+        const uint32_t d = tmem + buf.slot * TN;
+        if (issuer) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_f8(d, wa + 2 * kk, ta + 2 * kk, kIdesc, kk > 0);
           mma_commit(bars.empty(ring.slot));
           mma_commit(bars.tfull(buf.slot));
         }
+        __syncwarp();
       }
+    }
+    if (issuer) {
       mma_commit(bars.fin());  // everything issued is done before TMEM is released
       wait_limited(bars.fin(), 0);
     }
@@ -563,17 +594,18 @@ namespace wide {
 constexpr int kTileTok = 256, kTileCol = 256;  // of the pair
 constexpr int kHalf = 128;
 constexpr int kStage = 2 * kHalf * kBlockK;    // per CTA: tokens, then weights
-constexpr int kStages = 5;
-constexpr int kScaleStages = 8;
-constexpr int kScaleSlot = kHalf + 4;          // token scales, then two weight scales
+constexpr int kStages = 6;
+constexpr int kScaleGroup = 4;                 // k blocks whose scales share a slot (and a wait)
+constexpr int kScaleStages = 4;
+constexpr int kScaleRow = kHalf + 4;           // token scales, then two weight scales
+constexpr int kScaleSlot = kScaleGroup * kScaleRow;
 constexpr int kBufs = 2;                       // 2 x 256 TMEM columns
-// warps 0-3: TMA, MMA, scales, idle; 4-19: epilogue, four per TMEM lane quadrant
-// with 64 columns each.  A k block costs an epilogue warp a chain of latencies
-// (barriers, TMEM reads, the buffer's release) of about twice the pair's 512 MMA
-// cycles; four warps per scheduler overlap theirs (two took 1000 cycles a block).
-constexpr int kEpiWarps = 16;
+// warps 0-3: TMA, MMA, scales, idle; 4-11: epilogue, two per TMEM lane quadrant with
+// 128 columns each
+constexpr int kEpiWarps = 8;
 constexpr int kCols = kTileCol / (kEpiWarps / 4);
 constexpr int kThreads = 32 * (4 + kEpiWarps);
+constexpr int kRegsLoad = 56, kRegsEpi = 224;  // 128 x 56 + 256 x 224 = 384 x 168, the launch's registers
 constexpr int kStaging = 32 * 64;              // per epilogue warp: 64 bytes of each of its 32 output rows
 constexpr int kOffStaging = kStages * kStage;
 constexpr int kOffScales = kOffStaging + kEpiWarps * kStaging;
@@ -703,7 +735,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int* prefix = reinterpret_cast<int*>(smem + kOffPrefix);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(prefix + kMaxExperts + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(prefix + kMaxExperts + 5);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
 
   if (threadIdx.x == 0) {
@@ -743,6 +775,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
 
   if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
     if (warp == 0 && lane == 0) {
       // ---- TMA producer: both CTAs' copies complete on the leader's barrier
       int j = 0;
@@ -769,33 +802,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // that left before the last ones came in would have them land in the
       // shared memory of whoever runs there next.  (They also follow the copies.)
       drain<kStages>(ring, j, bars);
-    } else if (warp == 1 && lane == 0 && rank == 1) {
-      wait_limited(bars.fin(), 0);  // the leader's last arrival here
-    } else if (warp == 1 && lane == 0) {
-      // ---- MMA issuer (the leader, for the pair)
+    } else if (warp == 1 && rank == 1) {
+      if (lane == 0) wait_limited(bars.fin(), 0);  // the leader's last arrival here
+    } else if (warp == 1) {
+      // ---- MMA issuer (the leader, for the pair): the whole warp runs the
+      // loop, one lane issues
       constexpr uint32_t kIdesc = idesc_e4m3(kTileTok, kTileCol);
       const uint32_t ta0 = desc_low(sbase), wa0 = desc_low(sbase + kHalf * kBlockK);
+      const bool issuer = elect_one();
       Ring<kStages> ring;
       Ring<kBufs> buf;
       bool ok = true;
       for (int idx = first; ok && idx < tiles; idx += step) {
         for (int kb = 0; kb < a.k_blocks; ++kb, ring.next(), buf.next()) {
-          if (!wait_bar(abort_flag, bars.tempty(buf.slot), buf.phase ^ 1, 0x723) ||
-              !wait_bar(abort_flag, bars.full(ring.slot), ring.phase, 0x722)) {
+          if (!wait_bar_uniform(abort_flag, bars.full(ring.slot), ring.phase, 0x722) ||
+              !wait_bar_uniform(abort_flag, bars.tempty(buf.slot), buf.phase ^ 1, 0x723)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t ta = ta0 + ring.slot * (kStage >> 4), wa = wa0 + ring.slot * (kStage >> 4);
           const uint32_t d = tmem + buf.slot * kTileCol;
+          if (issuer) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_f8_pair(d, ta + 2 * kk, wa + 2 * kk, kIdesc, kk > 0);
-          mma_commit_pair(bars.empty(ring.slot));
-          mma_commit_pair(bars.tfull(buf.slot));
+            for (int kk = 0; kk < 4; ++kk) mma_f8_pair(d, ta + 2 * kk, wa + 2 * kk, kIdesc, kk > 0);
+            mma_commit_pair(bars.empty(ring.slot));
+            mma_commit_pair(bars.tfull(buf.slot));
+          }
+          __syncwarp();
         }
       }
-      mma_commit_pair(bars.fin());
-      wait_limited(bars.fin(), 0);
+      if (issuer) {
+        mma_commit_pair(bars.fin());
+        wait_limited(bars.fin(), 0);
+      }
     } else if (warp == 2) {
       // ---- scales: this CTA's tokens and the tile's two weight blocks
       Ring<kScaleStages> ring;
@@ -805,76 +845,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int trow = t.tok0 + rank * kHalf;
         const int wb = min(2 * t.row_block + (lane & 1), a.scale_rows - 1);
         const float* sw = a.w_scales + ((int64_t)t.expert * a.scale_rows + wb) * a.k_blocks;
-        for (int kb = 0; kb < a.k_blocks; ++kb, ring.next()) {
-          const uint32_t s = ring.slot;
-          if (!wait_bar_warp(abort_flag, bars.sempty(s), ring.phase ^ 1, 0x724)) {
+        for (int kb = 0; kb < a.k_blocks; kb += kScaleGroup, ring.next()) {
+          if (!wait_bar_warp(abort_flag, bars.sempty(ring.slot), ring.phase ^ 1, 0x724)) {
             ok = false;
             break;
           }
-          const float* src = a.a_scales + kb * a.a_scale_stride + trow;
-          const uint32_t dst = sbase + kOffScales + s * kScaleSlot * 4;
+          for (int g = kb; g < min(kb + kScaleGroup, a.k_blocks); ++g) {
+            const float* src = a.a_scales + g * a.a_scale_stride + trow;
+            const uint32_t dst = sbase + kOffScales + (ring.slot * kScaleSlot + (g - kb) * kScaleRow) * 4;
 #pragma unroll
-          for (int i = 0; i < kHalf; i += 32) {
-            const bool in = trow + i + lane < t.tok_end;
-            cp_async4(dst + (i + lane) * 4, in ? src + i + lane : a.a_scales, in ? 4 : 0);
+            for (int i = 0; i < kHalf; i += 32) {
+              const bool in = trow + i + lane < t.tok_end;
+              cp_async4(dst + (i + lane) * 4, in ? src + i + lane : a.a_scales, in ? 4 : 0);
+            }
+            if (lane < 2) cp_async4(dst + (kHalf + lane) * 4, sw + g, 4);
           }
-          if (lane < 2) cp_async4(dst + (kHalf + lane) * 4, sw + kb, 4);
-          cp_async_arrive(bars.sfull(s));
+          cp_async_arrive(bars.sfull(ring.slot));
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
-    // ---- epilogue: thread = token, registers = 64 weight rows
+    // ---- epilogue: thread = token, registers = 128 weight rows.  A block's
+    // release is on the path from product to product, so little is on it: one
+    // wait, two TMEM reads with the additions of the first half between them.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
     const int quad = warp & 3, part = (warp - 4) >> 2;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * kCols;
     const uint32_t tempty = mapa(bars.tempty(0), 0);  // the leader's; buffer b at + 8 b
     const uint32_t staging = sbase + kOffStaging + (warp - 4) * kStaging;
+    const float* slots = reinterpret_cast<const float*>(smem + kOffScales);
     Ring<kScaleStages> ring;
     Ring<kBufs> buf;
     bool ok = true;
-    // factor of this thread's token and weight block for the next k block
-    auto factor = [&](float* f) {
-      const uint32_t s = ring.slot;
-      if (!wait_bar_warp(abort_flag, bars.sfull(s), ring.phase, 0x725)) return false;
-      const float* slot = reinterpret_cast<const float*>(smem + kOffScales) + s * kScaleSlot;
-      *f = slot[quad * 32 + lane] * slot[kHalf + (part >> 1)];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars.sempty(s));
-      return true;
-    };
     for (int idx = first; ok && idx < tiles; idx += step) {
       const Tile t = find(a, prefix, idx);
+      const int m0 = t.tok0 + rank * kHalf + quad * 32;
       float2 acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      for (int kb = 0; kb < a.k_blocks; ++kb, ring.next(), buf.next()) {
-        const uint32_t b = buf.slot;
-        float f;
-        if (!factor(&f) || !wait_bar_warp(abort_flag, bars.tfull(b), buf.phase, 0x726)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const float2 f2 = make_float2(f, f);
-        const uint32_t src = taddr + b * kTileCol;
-#pragma unroll
-        for (int c = 0; c < kCols; c += 16) {  // 16 at a time: 96 registers a thread
-          uint32_t r[16];
-          tmem_ld(src + c, r);
-          if (c + 16 == kCols) {  // the buffer is read: release it before the last additions
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_pair(tempty + 8 * b);
+      for (int kb0 = 0; ok && kb0 < a.k_blocks; kb0 += kScaleGroup, ring.next()) {
+        ok = wait_bar_warp(abort_flag, bars.sfull(ring.slot), ring.phase, 0x725);
+        const float* slot = slots + ring.slot * kScaleSlot;
+        const int blocks = min(kScaleGroup, a.k_blocks - kb0);
+        for (int g = 0; ok && g < blocks; ++g, buf.next(), slot += kScaleRow) {
+          const float f = slot[quad * 32 + lane] * slot[kHalf + part];
+          if (!wait_bar_warp(abort_flag, bars.tfull(buf.slot), buf.phase, 0x726)) {
+            ok = false;
+            break;
           }
+          tc_fence_after();
+          const float2 f2 = make_float2(f, f);
+          const uint32_t src = taddr + buf.slot * kTileCol;
+          uint32_t r[64];
+          tmem_ld64(src, r);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            acc[c / 2 + i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[c / 2 + i]);
+          for (int i = 0; i < 32; ++i)
+            acc[i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[i]);
+          tmem_ld64(src + 64, r);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_pair(tempty + 8 * buf.slot);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            acc[32 + i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[32 + i]);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.sempty(ring.slot));
       }
       if (!ok) break;
-      store_rows<kFp32, kVec>(a, staging, t.tok0 + rank * kHalf + quad * 32, t.tok_end,
-                              t.row_block * kTileCol + part * kCols, lane, acc);
+      store_rows<kFp32, kVec>(a, staging, m0, t.tok_end, t.row_block * kTileCol + part * kCols, lane, acc);
     }
   }
   __syncwarp();
@@ -915,6 +955,11 @@ static bool make_map(CUtensorMap* map, const void* p, int64_t k, int64_t rows, i
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Token tiles of TN rows: at most this many exist, whatever the offsets say.
+static int64_t most_token_tiles(const Args& a, int tn) {
+  return a.offsets ? (int64_t)a.m / tn + std::min(a.experts, a.m) : ((int64_t)a.m + tn - 1) / tn;
 }
 
 // Stands in for gemm_kernel in the occupancy query, which answers one CTA per SM
@@ -988,24 +1033,16 @@ struct Form {
 };
 
 template <int TN, bool kFp32>
-static cudaError_t launch_tn(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, Args a, int sms,
-                             cudaStream_t stream) {
+static cudaError_t launch_tn(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, Args a, int splits,
+                             int sms, cudaStream_t stream) {
   using Split = Form<TN, true, kFp32>;
   using Whole = Form<TN, false, kFp32>;
   CUtensorMap tm_w, tm_a;
   if (!make_map(&tm_w, w, k, (int64_t)a.experts * a.n, ldw, kTileRows) || !make_map(&tm_a, act, k, a.m, lda, TN))
     return cudaErrorNotSupported;
-  // at most this many tiles exist, whatever the offsets say
-  const int64_t tok_tiles = a.offsets ? (int64_t)a.m / TN + std::min(a.experts, a.m) : ((int64_t)a.m + TN - 1) / TN;
-  const int64_t tiles = tok_tiles * a.row_blocks;
-  // Split k as long as every cluster runs at once and a CTA keeps two blocks.
-  a.splits = 1;
-  if (tiles * 2 <= (int64_t)sms * Whole::C::kCtasPerSm) {
-    const cudaError_t e = Split::set_attributes();
-    if (e != cudaSuccess) return e;
-    for (int s = 2; s <= 8 && a.k_blocks >= 2 * s && tiles <= Split::active_clusters(s); s *= 2) a.splits = s;
-  }
-  if (a.splits > 1) return Split::launch(tm_w, tm_a, a, tiles * a.splits, stream);
+  a.splits = splits;
+  const int64_t tiles = most_token_tiles(a, TN) * a.row_blocks;
+  if (splits > 1) return Split::launch(tm_w, tm_a, a, tiles * splits, stream);
   return Whole::launch(tm_w, tm_a, a, std::min<int64_t>(tiles, (int64_t)sms * Whole::C::kCtasPerSm), stream);
 }
 
@@ -1023,9 +1060,7 @@ static cudaError_t launch_wide(const void* act, int64_t lda, const void* w, int6
   if (!make_map(&tm_w, w, k, (int64_t)a.experts * a.n, ldw, wide::kHalf) || !make_map(&tm_a, act, k, a.m, lda, wide::kHalf))
     return cudaErrorNotSupported;
   a.row_blocks = (a.n + wide::kTileCol - 1) / wide::kTileCol;
-  const int64_t tok_tiles = a.offsets ? (int64_t)a.m / wide::kTileTok + std::min(a.experts, a.m)
-                                      : ((int64_t)a.m + wide::kTileTok - 1) / wide::kTileTok;
-  const int64_t pairs = std::min<int64_t>(tok_tiles * a.row_blocks, sms / 2);
+  const int64_t pairs = std::min<int64_t>(most_token_tiles(a, wide::kTileTok) * a.row_blocks, sms / 2);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
   cfg.blockDim = dim3(wide::kThreads);
@@ -1039,19 +1074,79 @@ static cudaError_t launch_wide(const void* act, int64_t lda, const void* w, int6
   return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, a);
 }
 
+// The form with the least estimated time.  The estimate's constants are times
+// in us, measured on one GB300 (152 SMs):
+//   a k block of a tile takes a CTA `alone` while it has its SM to itself and
+//   `shared` of the SM's time when two CTAs share it; the wide kernel's pairs
+//   take 0.54 for 256 x 256;
+//   the weights cannot come faster than 6.3 TB/s;
+//   a launch costs about 4.5, the exchange of split sums `exchange`, a wide
+//   tile's results 0.6.
+// Measured / estimated, n = k = 4096: 64 tokens 32 wide in 4 parts 9.5 / 9.5;
+// 128 tokens 64 in 4 12.3 / 11.6, 128 in 4 14.0 / 13.7; 256 tokens 64 whole 16.5 /
+// 16.3, in 2 17.1 / 16.4, wide 20.8 / 22.4; 512 tokens 128 whole 19.8 / 19.2, wide
+// 20.9 / 22.4; 1024 tokens wide 22 / 22.4, 128 whole 36 / 34.
+struct Choice {
+  int tn = 16, splits = 1;  // tn 256: the wide kernel
+};
+
+template <int TN, bool kFp32>
+static cudaError_t consider(const Args& a, int sms, double alone, double shared, double exchange, double* best,
+                            Choice* choice) {
+  const int per_sm = Cfg<TN, true>::kCtasPerSm;
+  // grouped rows: about half a tile of each expert is empty, and none shares one
+  const double tok_tiles =
+      a.offsets ? std::max((double)std::min(a.experts, a.m), (double)a.m / TN + 0.5 * std::min(a.experts, a.m))
+                : (double)most_token_tiles(a, TN);
+  const int64_t tiles = std::max<int64_t>(1, (int64_t)(tok_tiles * a.row_blocks));
+  for (int s = 1; s <= 8; s *= 2) {
+    if (s > 1) {
+      // every cluster runs at once, and a CTA keeps two blocks
+      if (a.k_blocks < 2 * s || most_token_tiles(a, TN) * a.row_blocks * s > (int64_t)sms * per_sm) break;
+      const cudaError_t e = Form<TN, true, kFp32>::set_attributes();
+      if (e != cudaSuccess) return e;
+      if (most_token_tiles(a, TN) * a.row_blocks > Form<TN, true, kFp32>::active_clusters(s)) break;
+    }
+    const int64_t on_sm = (tiles * s + sms - 1) / sms;  // CTAs of an SM, at once or one after the other
+    const double blocks = (double)((a.k_blocks + s - 1) / s);
+    const double chain = on_sm == 1 ? blocks * alone : on_sm * blocks * (per_sm == 2 ? shared : alone);
+    const double weights = (double)std::min(a.experts, a.m) * a.n * a.k_blocks * kBlockK / 6.3e6;
+    const double t = std::max(chain, weights) + 4.5 + (s > 1 ? exchange : 0.0);
+    if (t < *best) {
+      *best = t;
+      choice->tn = TN;
+      choice->splits = s;
+    }
+  }
+  return cudaSuccess;
+}
+
 template <bool kFp32>
 static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, const Args& a,
                               int sms, cudaStream_t stream) {
-  const int64_t per_expert = ((int64_t)a.m + a.experts - 1) / a.experts;
-  if (per_expert >= 256) {
-    const bool vec = a.ldo % (kFp32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
-    return vec ? launch_wide<kFp32, true>(act, lda, w, ldw, k, a, sms, stream)
-               : launch_wide<kFp32, false>(act, lda, w, ldw, k, a, sms, stream);
+  Choice c;
+  double best = 1e30;
+  cudaError_t e = consider<16, kFp32>(a, sms, 0.30, 0.18, 1.2, &best, &c);
+  if (e == cudaSuccess && a.m > 16) e = consider<32, kFp32>(a, sms, 0.33, 0.21, 1.6, &best, &c);
+  if (e == cudaSuccess && a.m > 32) e = consider<64, kFp32>(a, sms, 0.37, 0.30, 2.3, &best, &c);
+  if (e == cudaSuccess && a.m > 64) e = consider<128, kFp32>(a, sms, 0.46, 0.46, 5.5, &best, &c);
+  if (e != cudaSuccess) return e;
+  if (a.m > 128) {
+    const double tok_tiles = a.offsets ? std::max((double)std::min(a.experts, a.m), a.m / 256.0 + 0.5 * a.experts)
+                                       : (double)most_token_tiles(a, wide::kTileTok);
+    const int64_t tiles = std::max<int64_t>(1, (int64_t)(tok_tiles * ((a.n + wide::kTileCol - 1) / wide::kTileCol)));
+    const int64_t rounds = (tiles + sms / 2 - 1) / (sms / 2);
+    if (rounds * (a.k_blocks * 0.54 + 0.6) + 4.5 < best) c.tn = 256;
   }
-  if (per_expert <= 16) return launch_tn<16, kFp32>(act, lda, w, ldw, k, a, sms, stream);
-  if (per_expert <= 32) return launch_tn<32, kFp32>(act, lda, w, ldw, k, a, sms, stream);
-  if (per_expert <= 64) return launch_tn<64, kFp32>(act, lda, w, ldw, k, a, sms, stream);
-  return launch_tn<128, kFp32>(act, lda, w, ldw, k, a, sms, stream);
+  switch (c.tn) {
+    case 16: return launch_tn<16, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
+    case 32: return launch_tn<32, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
+    case 64: return launch_tn<64, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
+    case 128: return launch_tn<128, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
+  }
+  const bool vec = a.ldo % (kFp32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+  return vec ? launch_wide<kFp32, true>(act, lda, w, ldw, k, a, sms, stream)
+             : launch_wide<kFp32, false>(act, lda, w, ldw, k, a, sms, stream);
 }
 
 }  // namespace gemm8
