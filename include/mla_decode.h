@@ -496,7 +496,7 @@ int mla_add_rmsnorm(const void* x, int64_t x_stride, const void* residual_in, vo
  *   MLA_ACT_NONE      v = x                        x bf16 [num_tokens, dim]
  *   MLA_ACT_SILU_MUL  v = g / (1 + e^-g) * u       x bf16 [num_tokens, 2 dim] = [g | u]
  * y, y_dtype, y_stride, y_scales and scale_stride as in mla_add_rmsnorm;
- * MLA_OUT_BF16 only with MLA_ACT_SILU_MUL.  dim >= 1.
+ * MLA_OUT_BF16 only with MLA_ACT_SILU_MUL.  dim in [1, 65535 * 512].
  * Errors: MLA_ERR_ARG (also when num_tokens * ceil(dim / 128) exceeds
  * 2^31 - 1), MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
  */

@@ -38,7 +38,7 @@ cudaError_t launch_rope_quantize_write(const void* q_nope, const void* q_rope, i
 cudaError_t kv_write_read_error(int* code, bool reset);
 cudaError_t launch_add_rmsnorm(const void* x, int64_t x_stride, const void* res_in, void* res_out, int residual_kind,
                                int64_t res_stride, const void* weight, int num_tokens, int dim, float eps, void* y,
-                               int64_t y_stride, bool e4m3, float* y_scales, int64_t scale_stride,
+                               int64_t y_stride, bool e4m3, float* y_scales, int64_t scale_stride, int sms,
                                cudaStream_t stream);
 cudaError_t launch_act_quantize(const void* x, int64_t x_stride, int num_tokens, int dim, bool silu_mul, void* y,
                                 int64_t y_stride, bool e4m3, float* y_scales, int64_t scale_stride,
@@ -562,11 +562,12 @@ int mla_add_rmsnorm(const void* x, int64_t x_stride, const void* residual_in, vo
   }
   int rc = check_row_output(num_tokens, dim, y, y_dtype, y_stride, y_scales, scale_stride);
   if (rc != MLA_OK) return rc;
-  rc = check_device(nullptr);
+  int sms = 0;
+  rc = check_device(&sms);
   if (rc != MLA_OK) return rc;
   cudaError_t e = mla::launch_add_rmsnorm(x, x_stride, residual_in, residual_out, kind, residual_stride, weight,
                                           num_tokens, dim, eps, y, y_stride, y_dtype == MLA_OUT_E4M3, y_scales,
-                                          scale_stride, static_cast<cudaStream_t>(stream));
+                                          scale_stride, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("norm launch: ") + cudaGetErrorString(e));
   return ok();
 }
@@ -576,9 +577,9 @@ int mla_act_quantize(const void* x, int64_t x_stride, int act, int num_tokens, i
   if (act != MLA_ACT_NONE && act != MLA_ACT_SILU_MUL) return fail(MLA_ERR_ARG, "act must be MLA_ACT_NONE or MLA_ACT_SILU_MUL");
   if (num_tokens < 0) return fail(MLA_ERR_ARG, "num_tokens must be >= 0");
   if (dim < 1 || (act == MLA_ACT_SILU_MUL && dim > INT32_MAX / 2)) return fail(MLA_ERR_ARG, "dim must be >= 1, and 2 dim < 2^31 with a gate");
-  // a thread block covers 16 blocks of 128 columns
   if ((int64_t)num_tokens * (((int64_t)dim + 127) / 128) > INT32_MAX)
     return fail(MLA_ERR_ARG, "too many tokens x columns for one launch");
+  if (dim > 65535 * 512) return fail(MLA_ERR_ARG, "dim must be <= 65535 * 512");
   if (num_tokens == 0) return ok();
   if (!x || !aligned(x, 2)) return fail(MLA_ERR_ARG, "x must be a device pointer aligned to its elements");
   if (x_stride < (act == MLA_ACT_SILU_MUL ? 2 : 1) * (int64_t)dim) return fail(MLA_ERR_ARG, "x_stride is smaller than a row");

@@ -88,6 +88,30 @@ def test_norm(t, d, pad, y_dtype, residual):
     assert torch.all(yw[:, d:].float() == 7)
 
 
+@pytest.mark.parametrize("t,d,pad", [(700, 2048, 0), (613, 1544, 8), (1300, 8192, 0), (900, 1032, 16), (640, 700, 0),
+                                     (1000, 130, 0)])
+@pytest.mark.parametrize("residual", [None, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("y_dtype", [B.MLA_OUT_BF16, B.MLA_OUT_E4M3])
+def test_norm_many_rows(t, d, pad, residual, y_dtype):
+    """More rows than CTAs run at once: every row's own statistics, none left out."""
+    test_norm(t, d, pad, y_dtype, residual)
+
+
+def test_norm_many_rows_keep_apart():
+    """A NaN row among many leaves the rows before and after it (same CTA) alone."""
+    t, d = 2000, 2048
+    x = torch.ones(t, d, device="cuda", dtype=torch.bfloat16)
+    bad = torch.arange(7, t, 13, device="cuda")
+    x[bad, 100] = float("nan")
+    w = torch.ones(d, device="cuda", dtype=torch.bfloat16)
+    res = torch.zeros_like(x)
+    y = torch.empty_like(x)
+    B.mla_add_rmsnorm(x, res, res, B.MLA_OUT_BF16, w, 0.0, y, B.MLA_OUT_BF16)
+    rows = torch.ones(t, dtype=torch.bool, device="cuda")
+    rows[bad] = False
+    assert torch.all(y[rows] == 1) and torch.all(y[~rows].isnan())
+
+
 def test_norm_in_place_residual_and_stream():
     rng = np.random.default_rng(3)
     x, w, res = bf16(rng, (64, 1024)), bf16(rng, (1024,)), bf16(rng, (64, 1024))
@@ -225,6 +249,41 @@ def test_gemm_exact_integers(t, n, k, kind):
 @pytest.mark.parametrize("t,n,k", SIZES)
 def test_gemm(t, n, k, kind):
     run_gemm(np.random.default_rng(t * n + k), t, n, k, kind, False)
+
+
+LARGE = [(64, 4096, 4096), (100, 4100, 1040), (128, 8192, 2064), (200, 3000, 4096), (256, 8192, 1024), (300, 8200, 512),
+         (512, 4096, 1000 // 16 * 16), (777, 2500, 1024), (1025, 4097, 400), (2000, 2300, 1168)]
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("t,n,k", LARGE)
+def test_gemm_exact_integers_large(t, n, k, kind):
+    """Sizes at which every form of the kernel is the one chosen (whole and split
+    tiles of each width, pairs of CTAs), cut on all sides."""
+    a, sa, w, sw = operands(np.random.default_rng(t * 3 + n + k), t, n, k, integers=True)
+    for out_pad in (0, 3):
+        wide = torch.full((t, n + out_pad), 7.0, device="cuda", dtype=kind)
+        out = wide[:, :n]
+        B.mla_gemm_fp8(a, sa, w[0], sw[0], out, B.MLA_OUT_BF16 if kind == torch.bfloat16 else B.MLA_OUT_FP32)
+        assert B.mla_decode_device_error() == 0
+        ad = a.double() * sa.double().t().repeat_interleave(128, 1)[:, :k]
+        wd = w[0].double() * sw[0].double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+        assert torch.equal(out, (ad @ wd.t()).to(kind)) and torch.all(wide[:, n:] == 7)
+
+
+@pytest.mark.parametrize("counts,n,k", [([600, 0, 5, 411, 900, 33], 2100, 528), ([30] * 48, 1024, 1024),
+                                        ([0, 2000, 1, 0], 1290, 1040), ([7] * 64, 4096, 512)])
+def test_grouped_gemm_exact_integers_large(counts, n, k):
+    t = sum(counts)
+    a, sa, w, sw = operands(np.random.default_rng(t + n), t, n, k, len(counts), True)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    out = torch.full((t, n), 7.0, device="cuda")
+    B.mla_grouped_gemm_fp8(a, sa, w, sw, torch.from_numpy(off).cuda(), out, B.MLA_OUT_FP32)
+    assert B.mla_decode_device_error() == 0
+    ad = a.double() * sa.double().t().repeat_interleave(128, 1)[:, :k]
+    for e, (lo, hi) in enumerate(zip(off[:-1], off[1:])):
+        wd = w[e].double() * sw[e].double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+        assert torch.equal(out[lo:hi], (ad[lo:hi] @ wd.t()).float())
 
 
 def run_grouped(rng, counts, n, k, kind, integers, head=0, tail=0):
