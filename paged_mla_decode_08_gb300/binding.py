@@ -1,7 +1,8 @@
 """Thin ctypes binding of libmladecode.so (the C ABI in include/mla_decode.h).
 
 Argument marshalling only: every step of the decode runs in the library's
-CUDA kernels.  Torch tensors are accepted for convenience and are only used
+CUDA kernels.  (The FP8 layer operators' tensors are checked and passed on by the
+native module _mla_calls instead of ctypes.)  Torch tensors are accepted for convenience and are only used
 for their device pointers and the current CUDA stream.  There is no fallback:
 if the library is missing, loading fails loudly.
 """
@@ -9,12 +10,13 @@ if the library is missing, loading fails loudly.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
 import numpy as np
 
-from .build import LIB
+from .build import CALLS, LIB
 
 MLA_OK = 0
 MLA_ERR_ARG = -1
@@ -341,44 +343,23 @@ MLA_NORM_MAX_DIM = 32768
 MLA_GEMM_MAX_EXPERTS = 1024
 
 
-# Tensor types that hold each element type (stored bits included), filled by _dtypes()
-_BF16, _E4M3, _FP32, _I32 = MLA_OUT_BF16, MLA_OUT_E4M3, MLA_OUT_FP32, 3
-_held_by: dict = {}
+_calls = None
 
 
-def _dtypes(kind: int):
-    if not _held_by:
-        import torch
-        _held_by.update({_BF16: (torch.bfloat16, torch.int16, torch.uint16),
-                         _E4M3: (torch.float8_e4m3fn, torch.uint8, torch.int8),
-                         _FP32: (torch.float32,), _I32: (torch.int32,)})
-    return _held_by.get(kind, ())
-
-
-def _rows(x, name: str, shape, kind: int) -> int:
-    """Row stride of a 2-D CUDA tensor of ``shape`` with contiguous columns."""
-    if x.shape != shape:
-        raise MlaError(MLA_ERR_ARG, f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
-    if x.dtype not in (_held_by.get(kind) or _dtypes(kind)):
-        raise MlaError(MLA_ERR_ARG, f"{name} has type {x.dtype}")
-    row, col = x.stride()
-    if col != 1 and shape[1] > 1 and shape[0]:
-        raise MlaError(MLA_ERR_ARG, f"{name} must have contiguous columns")
-    if not x.is_cuda:
-        raise MlaError(MLA_ERR_ARG, f"{name} must be a CUDA tensor")
-    return row if shape[0] > 1 else shape[1]  # one row: any stride serves
-
-
-def _packed(x, name: str, shape, kind: int):
-    """Check a contiguous CUDA tensor of ``shape``."""
-    if x.shape != shape or x.dtype not in _dtypes(kind) or not x.is_contiguous() or not x.is_cuda:
-        raise MlaError(MLA_ERR_ARG, f"{name} must be a contiguous CUDA tensor of shape {shape} and its type")
-
-
-def _matrix(x, name: str):
-    if x.dim() != 2:
-        raise MlaError(MLA_ERR_ARG, f"{name} must be 2-D")
-    return x.shape
+def _load_calls():
+    """The module that checks tensors and makes the FP8 layer's calls (built by
+    build.build()); a Python check of their up to seven tensors takes longer than
+    the smallest kernels."""
+    global _calls
+    if not os.path.exists(CALLS):
+        raise RuntimeError(f"_mla_calls.so not built ({CALLS}); run __graft_entry__.build()")
+    import torch  # noqa: F401  (its libraries come first)
+    load()
+    spec = importlib.util.spec_from_file_location("_mla_calls", CALLS)
+    _calls = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(_calls)
+    _calls.set_error_type(MlaError)
+    return _calls
 
 
 def mla_add_rmsnorm(x, residual, residual_out, residual_dtype: int, weight, eps: float, y, y_dtype: int,
@@ -386,66 +367,30 @@ def mla_add_rmsnorm(x, residual, residual_out, residual_dtype: int, weight, eps:
     """RMS norm of the rows of ``x`` (bf16) after adding ``residual`` (None =
     none; the sum goes to ``residual_out``, which may be the same tensor) into
     ``y``: bf16, or e4m3 with ``y_scales`` [ceil(dim / 128), tokens]."""
-    t, d = _matrix(x, "x")
-    xs = _rows(x, "x", x.shape, _BF16)
-    rs = 0
-    if residual is not None and residual_out is not None:
-        rs = _rows(residual, "residual", (t, d), residual_dtype)
-        if _rows(residual_out, "residual_out", (t, d), residual_dtype) != rs:
-            raise MlaError(MLA_ERR_ARG, "residual and residual_out differ in their row stride")
-    _packed(weight, "weight", (d,), _BF16)
-    ys = _rows(y, "y", (t, d), y_dtype)
-    ss = 0 if y_scales is None else _rows(y_scales, "y_scales", (-(-d // 128), t), _FP32)
-    _check(load().mla_add_rmsnorm(x.data_ptr(), xs, _ptr(residual), _ptr(residual_out), residual_dtype, rs, weight.data_ptr(), t, d,
-                                  eps, y.data_ptr(), y_dtype, ys, _ptr(y_scales), ss, _stream(stream)))
+    (_calls or _load_calls()).add_rmsnorm(x, residual, residual_out, residual_dtype, weight, eps, y, y_dtype, y_scales,
+                                          None if stream is None else _stream(stream))
 
 
 def mla_act_quantize(x, act: int, y, y_dtype: int, y_scales=None, stream=None):
     """Quantise the bf16 rows of ``x`` (MLA_ACT_NONE), or silu(g) * u of rows
     [g | u] (MLA_ACT_SILU_MUL), into ``y`` with ``y_scales`` [ceil(dim / 128),
     tokens] (bf16 ``y``: the gated unit alone)."""
-    t, d = _matrix(y, "y")
-    xs = _rows(x, "x", (t, 2 * d if act == MLA_ACT_SILU_MUL else d), _BF16)
-    ys = _rows(y, "y", y.shape, y_dtype)
-    ss = 0 if y_scales is None else _rows(y_scales, "y_scales", (-(-d // 128), t), _FP32)
-    _check(load().mla_act_quantize(x.data_ptr(), xs, act, t, d, y.data_ptr(), y_dtype, ys, _ptr(y_scales), ss, _stream(stream)))
+    (_calls or _load_calls()).act_quantize(x, act, y, y_dtype, y_scales, None if stream is None else _stream(stream))
 
 
 def mla_gemm_fp8(a, a_scales, w, w_scales, out, out_dtype: int, stream=None):
     """``out`` [T, N] = ``a`` [T, K] times ``w`` [N, K] transposed, e4m3 operands
     with ``a_scales`` [ceil(K / 128), T] and ``w_scales`` [ceil(N / 128), ceil(K / 128)]."""
-    t, k = _matrix(a, "a")
-    n = _matrix(w, "w")[0]
-    gk = -(-k // 128)
-    lda, ldw = _rows(a, "a", (t, k), _E4M3), _rows(w, "w", (n, k), _E4M3)
-    ss = _rows(a_scales, "a_scales", (gk, t), _FP32)
-    _packed(w_scales, "w_scales", (-(-n // 128), gk), _FP32)
-    ldo = _rows(out, "out", (t, n), out_dtype)
-    _check(load().mla_gemm_fp8(a.data_ptr(), lda, a_scales.data_ptr(), ss, w.data_ptr(), ldw, w_scales.data_ptr(), t, n, k, out.data_ptr(),
-                               out_dtype, ldo, _stream(stream)))
+    (_calls or _load_calls()).gemm_fp8(a, a_scales, w, w_scales, out, out_dtype,
+                                       None if stream is None else _stream(stream))
 
 
 def mla_grouped_gemm_fp8(a, a_scales, w, w_scales, expert_offsets, out, out_dtype: int, stream=None):
     """``mla_gemm_fp8`` by expert: rows expert_offsets[e] .. expert_offsets[e+1]-1
     (int32 CUDA [E + 1]) use ``w[e]`` of ``w`` [E, N, K] with ``w_scales``
     [E, ceil(N / 128), ceil(K / 128)]."""
-    t, k = _matrix(a, "a")
-    if w.dim() != 3:
-        raise MlaError(MLA_ERR_ARG, "w must be [experts, n, k]")
-    e, n = int(w.shape[0]), int(w.shape[1])
-    gk = -(-k // 128)
-    ldw = w.stride(1) if n > 1 else w.stride(0) if e > 1 else k  # every row of every expert, n rows apart
-    if w.shape[2] != k or w.stride(2) != 1 or (e > 1 and w.stride(0) != n * ldw):
-        raise MlaError(MLA_ERR_ARG, "w must be [experts, n, k] with contiguous columns and one row stride")
-    if w.dtype not in _dtypes(_E4M3) or not w.is_cuda:
-        raise MlaError(MLA_ERR_ARG, "w must be an e4m3 CUDA tensor")
-    lda = _rows(a, "a", (t, k), _E4M3)
-    ss = _rows(a_scales, "a_scales", (gk, t), _FP32)
-    _packed(w_scales, "w_scales", (e, -(-n // 128), gk), _FP32)
-    _packed(expert_offsets, "expert_offsets", (e + 1,), _I32)
-    ldo = _rows(out, "out", (t, n), out_dtype)
-    _check(load().mla_grouped_gemm_fp8(a.data_ptr(), lda, a_scales.data_ptr(), ss, w.data_ptr(), ldw, w_scales.data_ptr(),
-                                       expert_offsets.data_ptr(), e, t, n, k, out.data_ptr(), out_dtype, ldo, _stream(stream)))
+    (_calls or _load_calls()).grouped_gemm_fp8(a, a_scales, w, w_scales, expert_offsets, out, out_dtype,
+                                               None if stream is None else _stream(stream))
 
 
 def mla_planner_constants():
