@@ -576,7 +576,7 @@ void mla_planner_constants(int* tile_tokens, int* segment_overhead_tiles, int* m
  * (the kernel then stopped early and its outputs are not valid); failing
  * that, the first out-of-range lookup of a block-table builder (0x30x) or of
  * the RoPE / cache-write step (0x60x), or a malformed expert offset (0x701) or
- * a timed-out wait (0x71x) of a product.  Reading it
+ * a timed-out wait (0x71x, 0x72x, 0x73x) of a product.  Reading it
  * synchronises with the device; reset != 0 clears it.  Errors: MLA_ERR_ARG,
  * MLA_ERR_CUDA. */
 int mla_decode_device_error(int* code, int reset);

@@ -5,13 +5,18 @@
 // dense (one weight matrix) or grouped by expert (rows offsets[e] ..
 // offsets[e+1]-1 use the weights of expert e).
 //
-// A tile is 128 weight rows x TN tokens.  The weights are the M operand of
-// tcgen05.mma (128 rows) and the tokens its N operand, so that a handful of
-// tokens wastes no tensor-core rows and streams the weights once.  One 128-wide
-// block of k is one 128-byte swizzled row of both operands: TMA fills a ring of
-// stages, four kind::f8f6f4 MMAs reduce the block into a TMEM buffer, and the
-// epilogue warps read the buffer and add it, times the block's scales, to fp32
-// sums in registers while the next block runs into the other buffer.
+// One 128-wide block of k is one 128-byte swizzled row of both operands: TMA fills
+// a ring of stages, four kind::f8f6f4 MMAs reduce the block into a TMEM buffer,
+// and the epilogue warps read the buffer and add it, times the block's scales, to
+// fp32 sums in registers while the next blocks run into the other buffers.
+//
+// Three forms of tile, chosen by an estimate of the time (at the end):
+//   swapped  128 weight rows x 16, 32 or 64 tokens, k split over a cluster where
+//            there are few tiles: the weights are the M operand of tcgen05.mma
+//            and the tokens its N operand, so that a handful of tokens wastes no
+//            tensor-core rows and streams the weights once;
+//   square   128 tokens x 128 weight rows, one CTA;
+//   paired   256 tokens x 256 weight rows, a pair of CTAs (cta_group::2).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -58,11 +63,10 @@ struct Cfg {
   static constexpr int kStage = kStageA + kStageB;
   // partial sums received from the CTAs of a split tile: [source][row][token slice]
   static constexpr int kRecv = kSplit ? kTileRows * TN * 4 : 0;
-  // Up to 64 tokens the weights' stream bounds the tile and two CTAs share an
-  // SM: twice the places for clusters (36 of 8 fit instead of 15) and one CTA
-  // loads while the other exchanges.  Wider tiles need the SM's TMEM.
-  static constexpr int kCtasPerSm = TN <= 64 ? 2 : 1;
-  static constexpr int kRing = (kCtasPerSm == 2 ? 106 : 200) * 1024 - kRecv;
+  // Two CTAs share an SM: twice the places for clusters (36 of 8 fit instead of
+  // 15), and one CTA loads while the other exchanges.
+  static constexpr int kCtasPerSm = 2;
+  static constexpr int kRing = 106 * 1024 - kRecv;
   static constexpr int kStages = kRing / kStage < 8 ? kRing / kStage : 8;
   static constexpr int kScaleStages = 8;
   static constexpr int kScaleSlot = TN + 4;            // token scales, then the weights' scale
@@ -101,23 +105,32 @@ struct Ring {
   }
 };
 
-// Bounded wait; false: gave up here or elsewhere in the CTA.
+__device__ __forceinline__ uint32_t flag_load(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void flag_store(uint32_t addr, uint32_t v) {
+  asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Bounded wait; false: gave up here or elsewhere in the CTA (the flag in shared memory).
 template <bool kCluster = false>
-__device__ __forceinline__ bool wait_bar(volatile int* abort_flag, uint32_t bar, uint32_t parity, int code) {
+__device__ __forceinline__ bool wait_bar(uint32_t abort_flag, uint32_t bar, uint32_t parity, int code) {
   if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
     if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
+    if (flag_load(abort_flag)) return false;
     if (clock64() - t0 > kTimeoutCycles) {
-      *abort_flag = 1;
+      flag_store(abort_flag, 1);
       atomicCAS(&g_gemm_error, 0, code);
       return false;
     }
   }
 }
 template <bool kCluster = false>
-__device__ __forceinline__ bool wait_bar_warp(volatile int* abort_flag, uint32_t bar, uint32_t parity, int code) {
+__device__ __forceinline__ bool wait_bar_warp(uint32_t abort_flag, uint32_t bar, uint32_t parity, int code) {
   const bool ok = wait_bar<kCluster>(abort_flag, bar, parity, code);
   return __all_sync(0xffffffffu, ok);
 }
@@ -129,13 +142,10 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
-// wait_bar_warp for the issuing warp.  The first tries loop inside one
+// wait_bar_warp for the issuing warps.  The first tries loop inside one
 // statement and the verdict is a vote, so the compiler sees no divergence and
-// keeps the ring's state, the descriptors and the branch in uniform registers:
-// the loop around a product's issue is then a handful of instructions (by one
-// lane under `if (lane == 0)` it took 1000 cycles per k block, twice the
-// product's own time).
-__device__ __forceinline__ bool wait_bar_uniform(volatile int* abort_flag, uint32_t bar, uint32_t parity, int code) {
+// keeps the ring's state, the descriptors and the branch in uniform registers.
+__device__ __forceinline__ bool wait_bar_uniform(uint32_t abort_flag, uint32_t bar, uint32_t parity, int code) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
@@ -173,13 +183,31 @@ __device__ __forceinline__ void drain(Ring<N> ring, int issued, const Bars& bars
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (kSwizzle128B << 29);
 __device__ __forceinline__ uint32_t desc_low(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, 8-bit operands, K = 32; a, b: low words
-__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+// The four K = 32 products of a 128-wide k block: D[tmem] = A[smem] * B[smem]^T,
+// 8-bit operands; a, b: low words.  Issued where `go` is nonzero: predicated
+// instructions, so that a whole warp runs through without a branch.
+__device__ __forceinline__ void mma_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t go) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred g, p;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\t"
+      "setp.ne.b32 g, %4, 0;\n\tsetp.ne.b32 p, 0, 0;\n\t"
       "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
+      "@g tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 da, {x, %5};\n\tmov.b64 db, {y, %5};\n\t"
+      "@g tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t"
+      "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 da, {x, %5};\n\tmov.b64 db, {y, %5};\n\t"
+      "@g tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t"
+      "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 da, {x, %5};\n\tmov.b64 db, {y, %5};\n\t"
+      "@g tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(go), "r"(kDescHigh)
+      : "memory");
+}
+// Arrive on `bar` when the products issued so far are done (where `go`).
+__device__ __forceinline__ void mma_commit_if(uint32_t bar, uint32_t go) {
+  asm volatile(
+      "{\n\t.reg .pred g;\n\tsetp.ne.b32 g, %1, 0;\n\t"
+      "@g tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(go)
       : "memory");
 }
 // fp32 accumulator, e4m3 x e4m3, both K-major
@@ -211,6 +239,11 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_
 // this thread's earlier cp.async copies arrive on `bar` when they have landed
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   union U { float2 f; uint64_t u; } x, y, z, d;
@@ -248,6 +281,59 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Announce `bytes` on `bar` and load a box that completes them, where `go`.
+__device__ __forceinline__ void tma_announce_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, uint32_t bytes, int x,
+                                                  int y, uint32_t go) {
+  asm volatile(
+      "{\n\t.reg .pred g;\n\tsetp.ne.b32 g, %6, 0;\n\t"
+      "@g mbarrier.arrive.expect_tx.shared::cta.b64 _, [%2], %5;\n\t"
+      "@g cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(bytes), "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_if(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, uint32_t go) {
+  asm volatile(
+      "{\n\t.reg .pred g;\n\tsetp.ne.b32 g, %5, 0;\n\t"
+      "@g cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(go)
+      : "memory");
+}
+
+// An issuing warp's way through its k blocks: of kTurns warps that take them in
+// turn, `id` has blocks id, id + kTurns, ... of `total`, and with them every
+// kTurns-th stage and buffer.  What it waits for is nearly always there, so its
+// own instructions set the pace: the whole warp runs the loop and a predicate
+// lets one lane issue, the next block's barriers are looked at while this one's
+// products go out, and one vote judges both (246 cycles per block alone on an
+// SM; 404 with two waits and a branch, 690 by one lane under a branch).
+template <int kTurns, int kStages, int kBufs>
+__device__ __forceinline__ bool issue_in_turn(uint32_t abort_flag, const Bars& bars, uint32_t a0, uint32_t b0,
+                                              uint32_t stage, uint32_t tmem, uint32_t cols, uint32_t idesc, int id,
+                                              int64_t total, uint32_t go, int code) {
+  static_assert(kStages % kTurns == 0 && kBufs % kTurns == 0, "whole shares");
+  Ring<kStages / kTurns> ring;
+  Ring<kBufs / kTurns> buf;
+  bool full = false, empty = false;
+  for (int64_t j = id; j < total; j += kTurns) {
+    const uint32_t s = ring.slot * kTurns + id, b = buf.slot * kTurns + id;
+    if (!__all_sync(0xffffffffu, full & empty)) {
+      // the buffer's release comes last: it is waited for last
+      if (!wait_bar_uniform(abort_flag, bars.full(s), ring.phase, code) ||
+          !wait_bar_uniform(abort_flag, bars.tempty(b), buf.phase ^ 1, code + 1))
+        return false;
+    }
+    tc_fence_after();
+    ring.next();
+    buf.next();
+    full = mbar_test_wait(bars.full(ring.slot * kTurns + id), ring.phase);
+    empty = mbar_test_wait(bars.tempty(buf.slot * kTurns + id), buf.phase ^ 1);
+    mma_block(tmem + b * cols, a0 + s * (stage >> 4), b0 + s * (stage >> 4), idesc, go);
+    mma_commit_if(bars.empty(s), go);
+    mma_commit_if(bars.tfull(b), go);
+  }
+  return true;
 }
 
 // Rows [lo, hi) of expert e.  Offsets outside 0 <= lo <= hi <= m own no row
@@ -334,12 +420,12 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
   const uint32_t sbase = smem_u32(smem);
   const Bars bars{sbase + C::kOffBars};
   int* prefix = reinterpret_cast<int*>(smem + C::kOffPrefix);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(prefix + kMaxExperts + 4);
+  const uint32_t abort_flag = sbase + C::kOffPrefix + (kMaxExperts + 4) * 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(prefix + kMaxExperts + 5);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    *abort_flag = 0;
+    flag_store(abort_flag, 0);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(bars.full(i), 1);
       mbar_init(bars.empty(i), 1);
@@ -416,36 +502,13 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
       drain<C::kStages>(ring, j, bars);
     }
   } else if (warp == 1) {
-    // ---- MMA issuer: the whole warp runs the loop, one lane issues
-    constexpr uint32_t kIdesc = idesc_e4m3(kTileRows, TN);
-    const uint32_t wa0 = desc_low(sbase), ta0 = desc_low(sbase + C::kStageA);
-    const bool issuer = elect_one();
-    Ring<C::kStages> ring;
-    Ring<C::kBufs> buf;
-    bool ok = true;
-    for (int idx = first; ok && idx < tiles; idx += step) {
-      for (int kb = kb0; kb < kb1; ++kb, ring.next(), buf.next()) {
-        if (!wait_bar_uniform(abort_flag, bars.full(ring.slot), ring.phase, 0x712) ||
-            !wait_bar_uniform(abort_flag, bars.tempty(buf.slot), buf.phase ^ 1, 0x713)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t wa = wa0 + ring.slot * (C::kStage >> 4), ta = ta0 + ring.slot * (C::kStage >> 4);
-        const uint32_t d = tmem + buf.slot * TN;
-        if (issuer) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_f8(d, wa + 2 * kk, ta + 2 * kk, kIdesc, kk > 0);
-          mma_commit(bars.empty(ring.slot));
-          mma_commit(bars.tfull(buf.slot));
-        }
-        __syncwarp();
-      }
-    }
-    if (issuer) {
-      mma_commit(bars.fin());  // everything issued is done before TMEM is released
-      wait_limited(bars.fin(), 0);
-    }
+    // ---- MMA issuer
+    const uint32_t go = elect_one();
+    const int64_t mine = tiles > first ? (tiles - first + step - 1) / step : 0;
+    issue_in_turn<1, C::kStages, C::kBufs>(abort_flag, bars, desc_low(sbase), desc_low(sbase + C::kStageA), C::kStage, tmem,
+                                           TN, idesc_e4m3(kTileRows, TN), 0, mine * (kb1 - kb0), go, 0x712);
+    mma_commit_if(bars.fin(), go);  // everything issued is done before TMEM is released
+    if (go) wait_limited(bars.fin(), 0);
   } else if (warp == C::kEpiWarps + 2) {
     // ---- scales of each k block into their own ring: a load per block on the
     // epilogue's path would cost it a memory latency per block
@@ -504,20 +567,13 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
           acc[c / 2] = fma2(make_float2(__uint_as_float(r0), __uint_as_float(r1)), s01, acc[c / 2]);
           acc[c / 2 + 1] = fma2(make_float2(__uint_as_float(r2), __uint_as_float(r3)), s23, acc[c / 2 + 1]);
         };
-        if (kCols <= 32) {  // few at a time: two CTAs share the register file
-          constexpr int kChunk = kSplit && kCols == 32 ? 8 : 16;
+        constexpr int kChunk = kSplit && kCols == 32 ? 8 : 16;  // few at a time: two CTAs share the register file
 #pragma unroll
-          for (int c = 0; c < kCols; c += kChunk) {
-            uint32_t r[kChunk];
-            tmem_ld(taddr + b * TN + c, r);
+        for (int c = 0; c < kCols; c += kChunk) {
+          uint32_t r[kChunk];
+          tmem_ld(taddr + b * TN + c, r);
 #pragma unroll
-            for (int i = 0; i < kChunk; i += 4) add4(c + i, r[i], r[i + 1], r[i + 2], r[i + 3]);
-          }
-        } else {
-          uint32_t r[64];
-          tmem_ld64(taddr + b * TN, r);
-#pragma unroll
-          for (int i = 0; i < 64; i += 4) add4(i, r[i], r[i + 1], r[i + 2], r[i + 3]);
+          for (int i = 0; i < kChunk; i += 4) add4(c + i, r[i], r[i + 1], r[i + 2], r[i + 3]);
         }
         tc_fence_before();
         __syncwarp();
@@ -581,87 +637,10 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
   }
 }
 
-// ------------------------------------------------------------------ wide tiles
-
-// A pair of CTAs (cta_group::2) computes 256 tokens x 256 weight rows: here the
-// tokens are the M operand, 128 of them per CTA, so an epilogue thread owns one
-// token and 128 weight rows that share one weight scale -- its factor for a k
-// block is one register, not one per column.  Each CTA loads its own 128 tokens
-// and 128 of the weight rows; the pair's tensor cores read both halves, which
-// halves the shared-memory and L2 traffic of a 128 x 256 tile.
-namespace wide {
-
-constexpr int kTileTok = 256, kTileCol = 256;  // of the pair
-constexpr int kHalf = 128;
-constexpr int kStage = 2 * kHalf * kBlockK;    // per CTA: tokens, then weights
-constexpr int kStages = 6;
-constexpr int kScaleGroup = 4;                 // k blocks whose scales share a slot (and a wait)
-constexpr int kScaleStages = 4;
-constexpr int kScaleRow = kHalf + 4;           // token scales, then two weight scales
-constexpr int kScaleSlot = kScaleGroup * kScaleRow;
-constexpr int kBufs = 2;                       // 2 x 256 TMEM columns
-// warps 0-3: TMA, MMA, scales, idle; 4-11: epilogue, two per TMEM lane quadrant with
-// 128 columns each
-constexpr int kEpiWarps = 8;
-constexpr int kCols = kTileCol / (kEpiWarps / 4);
-constexpr int kThreads = 32 * (4 + kEpiWarps);
-constexpr int kRegsLoad = 56, kRegsEpi = 224;  // 128 x 56 + 256 x 224 = 384 x 168, the launch's registers
-constexpr int kStaging = 32 * 64;              // per epilogue warp: 64 bytes of each of its 32 output rows
-constexpr int kOffStaging = kStages * kStage;
-constexpr int kOffScales = kOffStaging + kEpiWarps * kStaging;
-constexpr int kOffPrefix = kOffScales + kScaleStages * kScaleSlot * 4;
-constexpr int kOffBars = kOffPrefix + (kMaxExperts + 8) * 4;
-constexpr int kSmem = kOffBars + 512 + 1024;
-
-__device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish2() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-// Load into this CTA's shared memory, completing on a barrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t cluster_bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
-      "[%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y)
-      : "memory");
-}
-__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
-      : "memory");
-}
-// Arrive on the barrier at this offset in both CTAs when the products issued so far are done.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
-      : "memory");
-}
-
-// Arrive on a barrier of either CTA of the pair (address from mapa).  Only a
-// TMEM buffer's reads precede it, which the tcgen05 fence orders; a release at
-// cluster scope would wait for every store in flight (measured: 1000 cycles).
-__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-
-// The tokens of `t` that this CTA holds start at tok0 + 128 * rank.
-__device__ __forceinline__ Tile find(const Args& a, const int* prefix, int idx) {
-  return find_tile<kTileTok>(a, prefix, idx);  // a.row_blocks counts 256-row tiles here
-}
-
 // The warp's 32 rows x kCols columns of results, through shared memory in
 // pieces of 64 bytes a row: stored straight from the registers, every
 // instruction would touch 32 rows (measured: 3400 cycles a tile).
-template <bool kFp32, bool kVec>
+template <int kCols, bool kFp32, bool kVec>
 __device__ __forceinline__ void store_rows(const Args& a, uint32_t staging, int m0, int tok_end, int n0, int lane,
                                            const float2 (&acc)[kCols / 2]) {
   constexpr int kPiece = kFp32 ? 16 : 32;  // columns of a piece
@@ -724,22 +703,324 @@ __device__ __forceinline__ void store_rows(const Args& a, uint32_t staging, int 
   }
 }
 
-// a.row_blocks: 256-row tiles of the weights; a.scale_rows: 128-row blocks.
+// ------------------------------------------------------------------ square tiles
+
+// 128 tokens x 128 weight rows per CTA.  Here the tokens are the M operand, so an
+// epilogue thread owns one token and its factor for a k block is one register,
+// not one per column.  It reads its 64 columns of a block in two halves, the
+// second while the first is added and the next block's first while the second
+// is; a buffer is given back as soon as it is read, and four of them keep the
+// products ahead.  Two warps issue the products in turn: the instructions of one
+// block take an issuing warp about 550 cycles here, the products 256.
+// 256 x 8192 x 8192: 21.5 us (swapped tiles of 64 tokens 43 us, paired 37 us; the
+// weights alone 10.6 us); 256 x 4096 x 4096: 12.7 us (17.1, 21.0).
+namespace square {
+
+constexpr int kTileTok = 128, kTileCol = 128;
+constexpr int kStageTok = kTileTok * kBlockK;
+constexpr int kStage = kStageTok + kTileCol * kBlockK;
+constexpr int kStages = 6;
+constexpr int kScaleGroup = 4;                 // k blocks whose scales share a slot (and a wait)
+constexpr int kScaleStages = 4;
+constexpr int kScaleRow = kTileTok + 4;        // token scales, then the weights' scale
+constexpr int kScaleSlot = kScaleGroup * kScaleRow;
+constexpr int kBufs = 4;                       // of 128 TMEM columns
+// warps 0-3: copies, MMA, scales, MMA; 4-11: epilogue, two per TMEM lane quadrant
+// with 64 columns each
+constexpr int kEpiWarps = 8;
+constexpr int kCols = kTileCol / (kEpiWarps / 4);
+constexpr int kThreads = 32 * (4 + kEpiWarps);
+constexpr int kStaging = 32 * 64;              // per epilogue warp: 64 bytes of each of its 32 output rows
+constexpr int kOffStaging = kStages * kStage;
+constexpr int kOffScales = kOffStaging + kEpiWarps * kStaging;
+constexpr int kOffPrefix = kOffScales + kScaleStages * kScaleSlot * 4;
+constexpr int kOffBars = kOffPrefix + (kMaxExperts + 8) * 4;
+constexpr int kSmem = kOffBars + 512 + 1024;
+
+__device__ __forceinline__ Tile find(const Args& a, const int* prefix, int idx) {
+  return find_tile<kTileTok>(a, prefix, idx);
+}
+
 template <bool kFp32, bool kVec>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    gemm_wide_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const Args a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_square_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const Bars bars{sbase + kOffBars};
   int* prefix = reinterpret_cast<int*>(smem + kOffPrefix);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(prefix + kMaxExperts + 4);
+  const uint32_t abort_flag = sbase + kOffPrefix + (kMaxExperts + 4) * 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(prefix + kMaxExperts + 5);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    flag_store(abort_flag, 0);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bars.full(i), 1);
+      mbar_init(bars.empty(i), 1);
+    }
+    for (int i = 0; i < kScaleStages; ++i) {
+      mbar_init(bars.sfull(i), 32);
+      mbar_init(bars.sempty(i), kEpiWarps);
+    }
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(bars.tfull(i), 1);
+      mbar_init(bars.tempty(i), kEpiWarps);
+    }
+    mbar_init(bars.fin(), 1);
+    mbar_init(bars.fin() + 8, 1);
+    fence_mbar_init();
+    prefetch_tensormap(&tm_w);
+    prefetch_tensormap(&tm_a);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kBufs * kTileCol);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (warp == 2) scan_experts<kTileTok>(a, prefix, lane);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const int tiles = prefix[a.experts] * a.row_blocks;
+  const int first = (int)blockIdx.x, step = (int)gridDim.x;
+
+  if (warp < 4) {
+    if (warp == 0) {
+      // ---- TMA producer
+      const uint32_t go = elect_one();
+      int j = 0;
+      Ring<kStages> ring;
+      bool ok = true, free = false;  // the next stage, looked at ahead
+      for (int idx = first; ok && idx < tiles; idx += step) {
+        const Tile t = find(a, prefix, idx);
+        const int wrow = t.expert * a.n + t.row_block * kTileCol;
+        for (int kb = 0; kb < a.k_blocks; ++kb, ++j) {
+          if (!__all_sync(0xffffffffu, free) &&
+              !wait_bar_uniform(abort_flag, bars.empty(ring.slot), ring.phase ^ 1, 0x721)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = bars.full(ring.slot), dst = sbase + ring.slot * kStage;
+          ring.next();
+          free = mbar_test_wait(bars.empty(ring.slot), ring.phase ^ 1);
+          tma_announce_load(dst, &tm_a, full, kStage, kb * kBlockK, t.tok0, go);
+          tma_load_if(dst + kStageTok, &tm_w, full, kb * kBlockK, wrow, go);
+        }
+      }
+      if (go) drain<kStages>(ring, j, bars);
+    } else if (warp == 1 || warp == 3) {
+      // ---- MMA issuers
+      const uint32_t go = elect_one();
+      const int id = warp >> 1;
+      const int64_t mine = tiles > first ? (tiles - first + step - 1) / step : 0;
+      issue_in_turn<2, kStages, kBufs>(abort_flag, bars, desc_low(sbase), desc_low(sbase + kStageTok), kStage, tmem,
+                                       kTileCol, idesc_e4m3(kTileTok, kTileCol), id, mine * a.k_blocks, go, 0x722);
+      mma_commit_if(bars.fin() + 8 * id, go);
+      if (go) wait_limited(bars.fin() + 8 * id, 0);
+    } else {
+      // ---- scales: the tile's tokens and its block of weights
+      Ring<kScaleStages> ring;
+      bool ok = true;
+      for (int idx = first; ok && idx < tiles; idx += step) {
+        const Tile t = find(a, prefix, idx);
+        const float* sw = a.w_scales + ((int64_t)t.expert * a.scale_rows + t.row_block) * a.k_blocks;
+        for (int kb = 0; kb < a.k_blocks; kb += kScaleGroup, ring.next()) {
+          if (!wait_bar_warp(abort_flag, bars.sempty(ring.slot), ring.phase ^ 1, 0x724)) {
+            ok = false;
+            break;
+          }
+          for (int g = kb; g < min(kb + kScaleGroup, a.k_blocks); ++g) {
+            const float* src = a.a_scales + g * a.a_scale_stride + t.tok0;
+            const uint32_t dst = sbase + kOffScales + (ring.slot * kScaleSlot + (g - kb) * kScaleRow) * 4;
+#pragma unroll
+            for (int i = 0; i < kTileTok; i += 32) {
+              const bool in = t.tok0 + i + lane < t.tok_end;
+              cp_async4(dst + (i + lane) * 4, in ? src + i + lane : a.a_scales, in ? 4 : 0);
+            }
+            if (lane == 0) cp_async4(dst + kTileTok * 4, sw + g, 4);
+          }
+          cp_async_arrive(bars.sfull(ring.slot));
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  } else {
+    // ---- epilogue: thread = token, registers = 64 weight rows
+    const int quad = warp & 3, part = (warp - 4) >> 2;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * kCols;
+    const uint32_t staging = sbase + kOffStaging + (warp - 4) * kStaging;
+    const float* slots = reinterpret_cast<const float*>(smem + kOffScales);
+    Ring<kScaleStages> ring;
+    Ring<kBufs> buf;
+    bool ok = true;
+    for (int idx = first; ok && idx < tiles; idx += step) {
+      const Tile t = find(a, prefix, idx);
+      const int m0 = t.tok0 + quad * 32;
+      float2 acc[kCols / 2];
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      ok = wait_bar_warp(abort_flag, bars.sfull(ring.slot), ring.phase, 0x725) &&
+           wait_bar_warp(abort_flag, bars.tfull(buf.slot), buf.phase, 0x726);
+      if (!ok) break;
+      const float* slot = slots + ring.slot * kScaleSlot;
+      float f = slot[quad * 32 + lane] * slot[kTileTok];
+      uint32_t r0[32], r1[32];
+      tc_fence_after();
+      tmem_ld32_async(taddr + buf.slot * kTileCol, r0);
+      for (int kb = 0; kb < a.k_blocks; ++kb) {
+        float2 f2 = make_float2(f, f);
+        tmem_wait_ld32(r0);
+        tmem_ld32_async(taddr + buf.slot * kTileCol + 32, r1);
+        // the next block: its product, looked at, and its factor
+        const bool more = kb + 1 < a.k_blocks;
+        const uint32_t release = bars.tempty(buf.slot);
+        buf.next();
+        const bool there = mbar_test_wait(bars.tfull(buf.slot), buf.phase);
+        if ((kb & (kScaleGroup - 1)) == kScaleGroup - 1 || !more) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.sempty(ring.slot));
+          ring.next();
+          if (more && !wait_bar_warp(abort_flag, bars.sfull(ring.slot), ring.phase, 0x725)) ok = false;
+          slot = slots + ring.slot * kScaleSlot;
+        } else {
+          slot += kScaleRow;
+        }
+        f = slot[quad * 32 + lane] * slot[kTileTok];  // (past the last block: not used)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          acc[i] = fma2(make_float2(__uint_as_float(r0[2 * i]), __uint_as_float(r0[2 * i + 1])), f2, acc[i]);
+        tmem_wait_ld32(r1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(release);
+        if (!ok) break;
+        if (more) {
+          if (!__all_sync(0xffffffffu, there) && !wait_bar_warp(abort_flag, bars.tfull(buf.slot), buf.phase, 0x726)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          tmem_ld32_async(taddr + buf.slot * kTileCol, r0);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          acc[16 + i] = fma2(make_float2(__uint_as_float(r1[2 * i]), __uint_as_float(r1[2 * i + 1])), f2, acc[16 + i]);
+      }
+      if (!ok) break;
+      store_rows<kCols, kFp32, kVec>(a, staging, m0, t.tok_end, t.row_block * kTileCol + part * kCols, lane, acc);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kBufs * kTileCol);
+}
+
+}  // namespace square
+
+// ------------------------------------------------------------------ paired tiles
+
+// A pair of CTAs (cta_group::2) computes 256 tokens x 256 weight rows: the tokens
+// are the M operand, 128 of them per CTA, so an epilogue thread owns one token
+// and 128 weight rows that share one weight scale.  Each CTA loads its own 128
+// tokens and 128 of the weight rows; the pair's tensor cores read both halves,
+// which halves the shared-memory and L2 traffic of a 128 x 256 tile.
+// What bounds it is an epilogue warp's way through a block (wait, two reads, 128
+// additions, release to the leader): about 850 cycles, the products 512.  So it
+// spills nothing: 216 registers, state that is counted and not kept.  8192 tokens,
+// n = k = 8192: 440 us, 2.5 PFLOP/s (with spills in the loop 475 us, in square tiles
+// 485 us); the products in halves of 128 columns in four buffers: 537 us.
+namespace paired {
+
+constexpr int kTileTok = 256, kTileCol = 256;  // of the pair
+constexpr int kHalf = 128;
+constexpr int kStage = 2 * kHalf * kBlockK;    // per CTA: tokens, then weights
+constexpr int kStages = 6;
+constexpr int kScaleGroup = 4;                 // k blocks whose scales share a slot (and a wait)
+constexpr int kScaleStages = 4;
+constexpr int kScaleRow = kHalf + 4;           // token scales, then two weight scales
+constexpr int kScaleSlot = kScaleGroup * kScaleRow;
+constexpr int kBufs = 2;                       // 2 x 256 TMEM columns
+// warps 0-3: TMA, MMA, scales, idle; 4-11: epilogue, two per TMEM lane quadrant with
+// 128 columns each
+constexpr int kEpiWarps = 8;
+constexpr int kCols = kTileCol / (kEpiWarps / 4);
+constexpr int kThreads = 32 * (4 + kEpiWarps);
+constexpr int kRegsLoad = 72, kRegsEpi = 216;  // 128 x 72 + 256 x 216 = 384 x 168, the launch's registers
+constexpr int kStaging = 32 * 64;              // per epilogue warp: 64 bytes of each of its 32 output rows
+constexpr int kOffStaging = kStages * kStage;
+constexpr int kOffScales = kOffStaging + kEpiWarps * kStaging;
+constexpr int kOffPrefix = kOffScales + kScaleStages * kScaleSlot * 4;
+constexpr int kOffBars = kOffPrefix + (kMaxExperts + 8) * 4;
+constexpr int kSmem = kOffBars + 512 + 1024;
+
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Load into this CTA's shared memory, completing on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t cluster_bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+      "[%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
+      : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs when the products issued so far are done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// Arrive on a barrier of either CTA of the pair (address from mapa).  Only a
+// TMEM buffer's reads precede it, which the tcgen05 fence orders; a release at
+// cluster scope would wait for every store in flight (measured: 1000 cycles).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// The tokens of `t` that this CTA holds start at tok0 + 128 * rank.
+__device__ __forceinline__ Tile find(const Args& a, const int* prefix, int idx) {
+  return find_tile<kTileTok>(a, prefix, idx);  // a.row_blocks counts 256-row tiles here
+}
+
+// a.row_blocks: 256-row tiles of the weights; a.scale_rows: 128-row blocks.
+template <bool kFp32, bool kVec>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gemm_paired_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const Bars bars{sbase + kOffBars};
+  int* prefix = reinterpret_cast<int*>(smem + kOffPrefix);
+  const uint32_t abort_flag = sbase + kOffPrefix + (kMaxExperts + 4) * 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(prefix + kMaxExperts + 5);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
 
   if (threadIdx.x == 0) {
-    *abort_flag = 0;
+    flag_store(abort_flag, 0);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bars.full(i), 1);
       mbar_init(bars.empty(i), 1);
@@ -788,7 +1069,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int trow = t.tok0 + rank * kHalf;
         for (int kb = 0; kb < a.k_blocks; ++kb, ++j, ring.next()) {
           const uint32_t s = ring.slot;
-          if (!wait_bar(abort_flag, bars.empty(s), ring.phase ^ 1, 0x721)) {
+          if (!wait_bar(abort_flag, bars.empty(s), ring.phase ^ 1, 0x731)) {
             ok = false;
             break;
           }
@@ -815,8 +1096,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int idx = first; ok && idx < tiles; idx += step) {
         for (int kb = 0; kb < a.k_blocks; ++kb, ring.next(), buf.next()) {
-          if (!wait_bar_uniform(abort_flag, bars.full(ring.slot), ring.phase, 0x722) ||
-              !wait_bar_uniform(abort_flag, bars.tempty(buf.slot), buf.phase ^ 1, 0x723)) {
+          if (!wait_bar_uniform(abort_flag, bars.full(ring.slot), ring.phase, 0x732) ||
+              !wait_bar_uniform(abort_flag, bars.tempty(buf.slot), buf.phase ^ 1, 0x733)) {
             ok = false;
             break;
           }
@@ -846,7 +1127,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int wb = min(2 * t.row_block + (lane & 1), a.scale_rows - 1);
         const float* sw = a.w_scales + ((int64_t)t.expert * a.scale_rows + wb) * a.k_blocks;
         for (int kb = 0; kb < a.k_blocks; kb += kScaleGroup, ring.next()) {
-          if (!wait_bar_warp(abort_flag, bars.sempty(ring.slot), ring.phase ^ 1, 0x724)) {
+          if (!wait_bar_warp(abort_flag, bars.sempty(ring.slot), ring.phase ^ 1, 0x734)) {
             ok = false;
             break;
           }
@@ -873,48 +1154,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, part = (warp - 4) >> 2;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * kCols;
     const uint32_t tempty = mapa(bars.tempty(0), 0);  // the leader's; buffer b at + 8 b
-    const uint32_t staging = sbase + kOffStaging + (warp - 4) * kStaging;
-    const float* slots = reinterpret_cast<const float*>(smem + kOffScales);
-    Ring<kScaleStages> ring;
-    Ring<kBufs> buf;
+    const uint32_t slots = sbase + kOffScales, mine = (quad * 32 + lane) * 4, other = (kHalf + part) * 4;
+    uint32_t n = 0, group = 0;  // blocks and groups of scales so far
     bool ok = true;
     for (int idx = first; ok && idx < tiles; idx += step) {
-      const Tile t = find(a, prefix, idx);
-      const int m0 = t.tok0 + rank * kHalf + quad * 32;
       float2 acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      for (int kb0 = 0; ok && kb0 < a.k_blocks; kb0 += kScaleGroup, ring.next()) {
-        ok = wait_bar_warp(abort_flag, bars.sfull(ring.slot), ring.phase, 0x725);
-        const float* slot = slots + ring.slot * kScaleSlot;
-        const int blocks = min(kScaleGroup, a.k_blocks - kb0);
-        for (int g = 0; ok && g < blocks; ++g, buf.next(), slot += kScaleRow) {
-          const float f = slot[quad * 32 + lane] * slot[kHalf + part];
-          if (!wait_bar_warp(abort_flag, bars.tfull(buf.slot), buf.phase, 0x726)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const float2 f2 = make_float2(f, f);
-          const uint32_t src = taddr + buf.slot * kTileCol;
-          uint32_t r[64];
-          tmem_ld64(src, r);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            acc[i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[i]);
-          tmem_ld64(src + 64, r);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_pair(tempty + 8 * buf.slot);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            acc[32 + i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[32 + i]);
+#pragma unroll 1
+      for (int kb = 0; kb < a.k_blocks; ++kb, ++n) {
+        const uint32_t ring = group % kScaleStages, buf = n % kBufs;
+        if (kb % kScaleGroup == 0 && !wait_bar_warp(abort_flag, bars.sfull(ring), (group / kScaleStages) & 1, 0x735)) {
+          ok = false;
+          break;
         }
+        const uint32_t slot = slots + (ring * kScaleSlot + (kb % kScaleGroup) * kScaleRow) * 4;
+        const float f = ld_shared_f32(slot + mine) * ld_shared_f32(slot + other);
+        if (!wait_bar_warp(abort_flag, bars.tfull(buf), (n / kBufs) & 1, 0x736)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float2 f2 = make_float2(f, f);
+        const uint32_t src = taddr + buf * kTileCol;
+        uint32_t r[64];
+        tmem_ld64(src, r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          acc[i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[i]);
+        tmem_ld64(src + 64, r);
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars.sempty(ring.slot));
+        if (lane == 0) mbar_arrive_pair(tempty + 8 * buf);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          acc[32 + i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[32 + i]);
+        if (kb % kScaleGroup == kScaleGroup - 1 || kb + 1 == a.k_blocks) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.sempty(ring));
+          ++group;
+        }
       }
       if (!ok) break;
-      store_rows<kFp32, kVec>(a, staging, m0, t.tok_end, t.row_block * kTileCol + part * kCols, lane, acc);
+      const Tile t = find(a, prefix, idx);  // here, not before: nothing of it occupies registers while the sums do
+      store_rows<kCols, kFp32, kVec>(a, sbase + kOffStaging + (warp - 4) * kStaging, t.tok0 + rank * kHalf + quad * 32,
+                                     t.tok_end, t.row_block * kTileCol + part * kCols, lane, acc);
     }
   }
   __syncwarp();
@@ -926,7 +1210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
 }
 
-}  // namespace wide
+}  // namespace paired
 
 // ------------------------------------------------------------------ host side
 
@@ -1047,24 +1331,52 @@ static cudaError_t launch_tn(const void* act, int64_t lda, const void* w, int64_
 }
 
 template <bool kFp32, bool kVec>
-static cudaError_t launch_wide(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, Args a, int sms,
-                               cudaStream_t stream) {
-  constexpr auto kernel = wide::gemm_wide_kernel<kFp32, kVec>;
+static cudaError_t launch_square(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, const Args& a,
+                                 int sms, cudaStream_t stream) {
+  constexpr auto kernel = square::gemm_square_kernel<kFp32, kVec>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wide::kSmem);
+    attr_err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, square::kSmem);
   });
   if (attr_err != cudaSuccess) return attr_err;
   CUtensorMap tm_w, tm_a;
-  if (!make_map(&tm_w, w, k, (int64_t)a.experts * a.n, ldw, wide::kHalf) || !make_map(&tm_a, act, k, a.m, lda, wide::kHalf))
+  if (!make_map(&tm_w, w, k, (int64_t)a.experts * a.n, ldw, square::kTileCol) ||
+      !make_map(&tm_a, act, k, a.m, lda, square::kTileTok))
     return cudaErrorNotSupported;
-  a.row_blocks = (a.n + wide::kTileCol - 1) / wide::kTileCol;
-  const int64_t pairs = std::min<int64_t>(most_token_tiles(a, wide::kTileTok) * a.row_blocks, sms / 2);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(most_token_tiles(a, square::kTileTok) * a.row_blocks, sms));
+  cfg.blockDim = dim3(square::kThreads);
+  cfg.dynamicSmemBytes = square::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, a);
+}
+
+template <bool kFp32, bool kVec>
+static cudaError_t launch_paired(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, Args a, int sms,
+                               cudaStream_t stream) {
+  constexpr auto kernel = paired::gemm_paired_kernel<kFp32, kVec>;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, paired::kSmem);
+  });
+  if (attr_err != cudaSuccess) return attr_err;
+  CUtensorMap tm_w, tm_a;
+  if (!make_map(&tm_w, w, k, (int64_t)a.experts * a.n, ldw, paired::kHalf) ||
+      !make_map(&tm_a, act, k, a.m, lda, paired::kHalf))
+    return cudaErrorNotSupported;
+  a.row_blocks = (a.n + paired::kTileCol - 1) / paired::kTileCol;
+  const int64_t pairs = std::min<int64_t>(most_token_tiles(a, paired::kTileTok) * a.row_blocks, sms / 2);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
-  cfg.blockDim = dim3(wide::kThreads);
-  cfg.dynamicSmemBytes = wide::kSmem;
+  cfg.blockDim = dim3(paired::kThreads);
+  cfg.dynamicSmemBytes = paired::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1076,47 +1388,54 @@ static cudaError_t launch_wide(const void* act, int64_t lda, const void* w, int6
 
 // The form with the least estimated time.  The estimate's constants are times
 // in us, measured on one GB300 (152 SMs):
-//   a k block of a tile takes a CTA `alone` while it has its SM to itself and
-//   `shared` of the SM's time when two CTAs share it; the wide kernel's pairs
-//   take 0.54 for 256 x 256;
+//   a k block of a swapped tile takes a CTA `alone` while it has its SM to
+//   itself and `shared` of the SM's time when two CTAs share it; of a square
+//   tile 0.28, of a paired tile 0.455;
+//   the results of a tile cost 0.7 (square) or 2 (paired) more;
 //   the weights cannot come faster than 6.3 TB/s;
-//   a launch costs about 4.5, the exchange of split sums `exchange`, a wide
-//   tile's results 0.6.
-// Measured / estimated, n = k = 4096: 64 tokens 32 wide in 4 parts 9.5 / 9.5;
-// 128 tokens 64 in 4 12.3 / 11.6, 128 in 4 14.0 / 13.7; 256 tokens 64 whole 16.5 /
-// 16.3, in 2 17.1 / 16.4, wide 20.8 / 22.4; 512 tokens 128 whole 19.8 / 19.2, wide
-// 20.9 / 22.4; 1024 tokens wide 22 / 22.4, 128 whole 36 / 34.
+//   a launch costs about 4.5 and the exchange of split sums `exchange`.
+// Measured / estimated, n = k = 4096: 64 tokens 32 swapped in 4 parts 9.5 / 9.5;
+// 128 tokens 64 in 4 12.3 / 11.6, square 12.6 / 14.2; 256 tokens square 12.7 / 14.2,
+// 64 swapped 17.1 / 16.3, paired 20.3 / 21.1; 2048 tokens paired 36.4 / 37.6, square
+// 41 / 43; 8192 tokens, n = k = 8192: paired 440 / 440, square 485 / 507.
+enum Shape { kSwapped16 = 16, kSwapped32 = 32, kSwapped64 = 64, kSquare = 128, kPaired = 256 };
 struct Choice {
-  int tn = 16, splits = 1;  // tn 256: the wide kernel
+  double time = 1e30;
+  int shape = kSwapped16, splits = 1;
+  void offer(double t, int s, int parts) {
+    if (t < time) {
+      time = t;
+      shape = s;
+      splits = parts;
+    }
+  }
 };
 
+// Tiles to expect.  Grouped rows: about half a tile of each expert is empty, and
+// no tile serves two.
+static int64_t expected_tiles(const Args& a, int tokens, int64_t row_tiles) {
+  const int owners = std::min(a.experts, a.m);
+  const double tok_tiles = a.offsets ? std::max((double)owners, (double)a.m / tokens + 0.5 * owners)
+                                     : (double)most_token_tiles(a, tokens);
+  return std::max<int64_t>(1, (int64_t)(tok_tiles * row_tiles));
+}
+
 template <int TN, bool kFp32>
-static cudaError_t consider(const Args& a, int sms, double alone, double shared, double exchange, double* best,
+static cudaError_t consider(const Args& a, int sms, double alone, double shared, double exchange, double weights,
                             Choice* choice) {
-  const int per_sm = Cfg<TN, true>::kCtasPerSm;
-  // grouped rows: about half a tile of each expert is empty, and none shares one
-  const double tok_tiles =
-      a.offsets ? std::max((double)std::min(a.experts, a.m), (double)a.m / TN + 0.5 * std::min(a.experts, a.m))
-                : (double)most_token_tiles(a, TN);
-  const int64_t tiles = std::max<int64_t>(1, (int64_t)(tok_tiles * a.row_blocks));
+  constexpr int kPerSm = Cfg<TN, true>::kCtasPerSm;
+  const int64_t tiles = expected_tiles(a, TN, a.row_blocks), most = most_token_tiles(a, TN) * a.row_blocks;
   for (int s = 1; s <= 8; s *= 2) {
     if (s > 1) {
       // every cluster runs at once, and a CTA keeps two blocks
-      if (a.k_blocks < 2 * s || most_token_tiles(a, TN) * a.row_blocks * s > (int64_t)sms * per_sm) break;
+      if (a.k_blocks < 2 * s || most * s > (int64_t)sms * kPerSm) break;
       const cudaError_t e = Form<TN, true, kFp32>::set_attributes();
       if (e != cudaSuccess) return e;
-      if (most_token_tiles(a, TN) * a.row_blocks > Form<TN, true, kFp32>::active_clusters(s)) break;
+      if (most > Form<TN, true, kFp32>::active_clusters(s)) break;
     }
     const int64_t on_sm = (tiles * s + sms - 1) / sms;  // CTAs of an SM, at once or one after the other
-    const double blocks = (double)((a.k_blocks + s - 1) / s);
-    const double chain = on_sm == 1 ? blocks * alone : on_sm * blocks * (per_sm == 2 ? shared : alone);
-    const double weights = (double)std::min(a.experts, a.m) * a.n * a.k_blocks * kBlockK / 6.3e6;
-    const double t = std::max(chain, weights) + 4.5 + (s > 1 ? exchange : 0.0);
-    if (t < *best) {
-      *best = t;
-      choice->tn = TN;
-      choice->splits = s;
-    }
+    const double chain = on_sm * ((a.k_blocks + s - 1) / s) * (on_sm == 1 ? alone : shared);
+    choice->offer(std::max(chain, weights) + 4.5 + (s > 1 ? exchange : 0.0), TN, s);
   }
   return cudaSuccess;
 }
@@ -1125,28 +1444,31 @@ template <bool kFp32>
 static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, const Args& a,
                               int sms, cudaStream_t stream) {
   Choice c;
-  double best = 1e30;
-  cudaError_t e = consider<16, kFp32>(a, sms, 0.30, 0.18, 1.2, &best, &c);
-  if (e == cudaSuccess && a.m > 16) e = consider<32, kFp32>(a, sms, 0.33, 0.21, 1.6, &best, &c);
-  if (e == cudaSuccess && a.m > 32) e = consider<64, kFp32>(a, sms, 0.37, 0.30, 2.3, &best, &c);
-  if (e == cudaSuccess && a.m > 64) e = consider<128, kFp32>(a, sms, 0.46, 0.46, 5.5, &best, &c);
+  const double weights = (double)std::min(a.experts, a.m) * a.n * a.k_blocks * kBlockK / 6.3e6;
+  cudaError_t e = consider<16, kFp32>(a, sms, 0.30, 0.18, 1.2, weights, &c);
+  if (e == cudaSuccess && a.m > 16) e = consider<32, kFp32>(a, sms, 0.33, 0.21, 1.6, weights, &c);
+  if (e == cudaSuccess && a.m > 32) e = consider<64, kFp32>(a, sms, 0.37, 0.30, 2.3, weights, &c);
   if (e != cudaSuccess) return e;
-  if (a.m > 128) {
-    const double tok_tiles = a.offsets ? std::max((double)std::min(a.experts, a.m), a.m / 256.0 + 0.5 * a.experts)
-                                       : (double)most_token_tiles(a, wide::kTileTok);
-    const int64_t tiles = std::max<int64_t>(1, (int64_t)(tok_tiles * ((a.n + wide::kTileCol - 1) / wide::kTileCol)));
-    const int64_t rounds = (tiles + sms / 2 - 1) / (sms / 2);
-    if (rounds * (a.k_blocks * 0.54 + 0.6) + 4.5 < best) c.tn = 256;
+  if (a.m > 64) {
+    const int64_t rounds = (expected_tiles(a, square::kTileTok, a.row_blocks) + sms - 1) / sms;
+    c.offer(std::max(rounds * (a.k_blocks * 0.28 + 0.7), weights) + 4.5, kSquare, 1);
   }
-  switch (c.tn) {
-    case 16: return launch_tn<16, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
-    case 32: return launch_tn<32, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
-    case 64: return launch_tn<64, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
-    case 128: return launch_tn<128, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
+  if (a.m > 128) {
+    const int64_t row_tiles = (a.n + paired::kTileCol - 1) / paired::kTileCol;
+    const int64_t rounds = (expected_tiles(a, paired::kTileTok, row_tiles) + sms / 2 - 1) / (sms / 2);
+    c.offer(std::max(rounds * (a.k_blocks * 0.455 + 2.0), weights) + 4.5, kPaired, 1);
   }
   const bool vec = a.ldo % (kFp32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
-  return vec ? launch_wide<kFp32, true>(act, lda, w, ldw, k, a, sms, stream)
-             : launch_wide<kFp32, false>(act, lda, w, ldw, k, a, sms, stream);
+  switch (c.shape) {
+    case kSwapped16: return launch_tn<16, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
+    case kSwapped32: return launch_tn<32, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
+    case kSwapped64: return launch_tn<64, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
+    case kSquare:
+      return vec ? launch_square<kFp32, true>(act, lda, w, ldw, k, a, sms, stream)
+                 : launch_square<kFp32, false>(act, lda, w, ldw, k, a, sms, stream);
+  }
+  return vec ? launch_paired<kFp32, true>(act, lda, w, ldw, k, a, sms, stream)
+             : launch_paired<kFp32, false>(act, lda, w, ldw, k, a, sms, stream);
 }
 
 }  // namespace gemm8
