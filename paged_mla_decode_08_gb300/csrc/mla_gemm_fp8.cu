@@ -1386,18 +1386,18 @@ static cudaError_t launch_paired(const void* act, int64_t lda, const void* w, in
   return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, a);
 }
 
-// The form with the least estimated time.  The estimate's constants are times
-// in us, measured on one GB300 (152 SMs):
-//   a k block of a swapped tile takes a CTA `alone` while it has its SM to
-//   itself and `shared` of the SM's time when two CTAs share it; of a square
-//   tile 0.28, of a paired tile 0.455;
-//   the results of a tile cost 0.7 (square) or 2 (paired) more;
-//   the weights cannot come faster than 6.3 TB/s;
-//   a launch costs about 4.5 and the exchange of split sums `exchange`.
-// Measured / estimated, n = k = 4096: 64 tokens 32 swapped in 4 parts 9.5 / 9.5;
-// 128 tokens 64 in 4 12.3 / 11.6, square 12.6 / 14.2; 256 tokens square 12.7 / 14.2,
-// 64 swapped 17.1 / 16.3, paired 20.3 / 21.1; 2048 tokens paired 36.4 / 37.6, square
-// 41 / 43; 8192 tokens, n = k = 8192: paired 440 / 440, square 485 / 507.
+// The form with the least estimated time.  The estimate's constants are times in
+// us, fitted to 640 timings on one GB300 (152 SMs; 1 to 8192 tokens, k 512 to
+// 16384, every form):
+//   a k block of a swapped tile takes a CTA `alone` while it has its SM to itself
+//   and `shared` of the SM's time when two CTAs share it;
+//   the results of a tile cost `tile` more, the exchange of split sums `exchange`,
+//   the launch and the first loads `fixed`;
+//   the weights cannot come faster than 6.3 TB/s.
+// The chosen form is the fastest one within 1 % on average over those sizes, within
+// 15 % at worst.  Where forms meet (n = k = 4096): 64 tokens 32 swapped in 4 parts
+// 9.5, 64 in 4 9.8; 128 tokens 64 in 4 12.6, square 12.4; 512 tokens square 12.6,
+// paired 20.0; 1024 tokens square 21.8, paired 20.6.
 enum Shape { kSwapped16 = 16, kSwapped32 = 32, kSwapped64 = 64, kSquare = 128, kPaired = 256 };
 struct Choice {
   double time = 1e30;
@@ -1411,6 +1411,10 @@ struct Choice {
   }
 };
 
+struct Cost {
+  double alone, shared, tile, fixed, exchange;
+};
+
 // Tiles to expect.  Grouped rows: about half a tile of each expert is empty, and
 // no tile serves two.
 static int64_t expected_tiles(const Args& a, int tokens, int64_t row_tiles) {
@@ -1421,8 +1425,7 @@ static int64_t expected_tiles(const Args& a, int tokens, int64_t row_tiles) {
 }
 
 template <int TN, bool kFp32>
-static cudaError_t consider(const Args& a, int sms, double alone, double shared, double exchange, double weights,
-                            Choice* choice) {
+static cudaError_t consider(const Args& a, int sms, Cost c, double weights, Choice* choice) {
   constexpr int kPerSm = Cfg<TN, true>::kCtasPerSm;
   const int64_t tiles = expected_tiles(a, TN, a.row_blocks), most = most_token_tiles(a, TN) * a.row_blocks;
   for (int s = 1; s <= 8; s *= 2) {
@@ -1434,8 +1437,8 @@ static cudaError_t consider(const Args& a, int sms, double alone, double shared,
       if (most > Form<TN, true, kFp32>::active_clusters(s)) break;
     }
     const int64_t on_sm = (tiles * s + sms - 1) / sms;  // CTAs of an SM, at once or one after the other
-    const double chain = on_sm * ((a.k_blocks + s - 1) / s) * (on_sm == 1 ? alone : shared);
-    choice->offer(std::max(chain, weights) + 4.5 + (s > 1 ? exchange : 0.0), TN, s);
+    const double chain = on_sm * (((a.k_blocks + s - 1) / s) * (on_sm == 1 ? c.alone : c.shared) + c.tile);
+    choice->offer(std::max(chain, weights) + c.fixed + (s > 1 ? c.exchange : 0.0), TN, s);
   }
   return cudaSuccess;
 }
@@ -1445,18 +1448,18 @@ static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64
                               int sms, cudaStream_t stream) {
   Choice c;
   const double weights = (double)std::min(a.experts, a.m) * a.n * a.k_blocks * kBlockK / 6.3e6;
-  cudaError_t e = consider<16, kFp32>(a, sms, 0.30, 0.18, 1.2, weights, &c);
-  if (e == cudaSuccess && a.m > 16) e = consider<32, kFp32>(a, sms, 0.33, 0.21, 1.6, weights, &c);
-  if (e == cudaSuccess && a.m > 32) e = consider<64, kFp32>(a, sms, 0.37, 0.30, 2.3, weights, &c);
+  cudaError_t e = consider<16, kFp32>(a, sms, {0.244, 0.178, 0.5, 2.5, 1.2}, weights, &c);
+  if (e == cudaSuccess && a.m > 16) e = consider<32, kFp32>(a, sms, {0.276, 0.191, 0.8, 2.4, 1.8}, weights, &c);
+  if (e == cudaSuccess && a.m > 32) e = consider<64, kFp32>(a, sms, {0.395, 0.285, 1.4, 2.7, 2.2}, weights, &c);
   if (e != cudaSuccess) return e;
   if (a.m > 64) {
     const int64_t rounds = (expected_tiles(a, square::kTileTok, a.row_blocks) + sms - 1) / sms;
-    c.offer(std::max(rounds * (a.k_blocks * 0.28 + 0.7), weights) + 4.5, kSquare, 1);
+    c.offer(std::max(rounds * (a.k_blocks * 0.253 + 1.4), weights) + 2.6, kSquare, 1);
   }
   if (a.m > 128) {
     const int64_t row_tiles = (a.n + paired::kTileCol - 1) / paired::kTileCol;
     const int64_t rounds = (expected_tiles(a, paired::kTileTok, row_tiles) + sms / 2 - 1) / (sms / 2);
-    c.offer(std::max(rounds * (a.k_blocks * 0.455 + 2.0), weights) + 4.5, kPaired, 1);
+    c.offer(std::max(rounds * (a.k_blocks * 0.435 + 2.7), weights) + 3.3, kPaired, 1);
   }
   const bool vec = a.ldo % (kFp32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
   switch (c.shape) {
