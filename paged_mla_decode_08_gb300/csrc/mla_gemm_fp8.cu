@@ -927,15 +927,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ paired tiles
 
 // A pair of CTAs (cta_group::2) computes 256 tokens x 256 weight rows: the tokens
-// are the M operand, 128 of them per CTA, so an epilogue thread owns one token
-// and 128 weight rows that share one weight scale.  Each CTA loads its own 128
-// tokens and 128 of the weight rows; the pair's tensor cores read both halves,
-// which halves the shared-memory and L2 traffic of a 128 x 256 tile.
-// What bounds it is an epilogue warp's way through a block (wait, two reads, 128
-// additions, release to the leader): about 850 cycles, the products 512.  So it
-// spills nothing: 216 registers, state that is counted and not kept.  8192 tokens,
-// n = k = 8192: 440 us, 2.5 PFLOP/s (with spills in the loop 475 us, in square tiles
-// 485 us); the products in halves of 128 columns in four buffers: 537 us.
+// are the M operand, 128 of them per CTA, so an epilogue thread owns one token.
+// Each CTA loads its own 128 tokens and 128 of the weight rows; the pair's tensor
+// cores read both, which halves the shared-memory and L2 traffic of a 128 x 256
+// tile.
+// Additions (256 cycles a block on the FMA pipes) and TMEM reads have to overlap to
+// keep up with the products (512).  So the products of a block come in two halves,
+// of 64 of each CTA's weight rows, issued by a warp each into buffers of their own,
+// and half of the epilogue's warps take each half: they run out of step, and
+// within a warp 32 columns are read while 32 are added.  8192 tokens, n = k = 8192:
+// 423..450 us, 2.5 PFLOP/s (both halves in one product, all warps in step, reads and
+// additions in turn: 3 % more; in square tiles 475 us).  Spills in the epilogue's loop
+// cost 4 to 20 % and are kept out: 216 registers, state that is counted, not kept.
 namespace paired {
 
 constexpr int kTileTok = 256, kTileCol = 256;  // of the pair
@@ -946,9 +949,9 @@ constexpr int kScaleGroup = 4;                 // k blocks whose scales share a 
 constexpr int kScaleStages = 4;
 constexpr int kScaleRow = kHalf + 4;           // token scales, then two weight scales
 constexpr int kScaleSlot = kScaleGroup * kScaleRow;
-constexpr int kBufs = 2;                       // 2 x 256 TMEM columns
-// warps 0-3: TMA, MMA, scales, idle; 4-11: epilogue, two per TMEM lane quadrant with
-// 128 columns each
+constexpr int kBufs = 4;                       // of 128 TMEM columns: two for each half
+// warps 0-3: TMA, MMA of the first half, scales, MMA of the second; 4-11: epilogue,
+// one per TMEM lane quadrant and half
 constexpr int kEpiWarps = 8;
 constexpr int kCols = kTileCol / (kEpiWarps / 4);
 constexpr int kThreads = 32 * (4 + kEpiWarps);
@@ -1006,6 +1009,15 @@ __device__ __forceinline__ Tile find(const Args& a, const int* prefix, int idx) 
 }
 
 // a.row_blocks: 256-row tiles of the weights; a.scale_rows: 128-row blocks.
+// 32 columns of a block's products, times the block's scales, into the sums from kAt on
+template <int kAt>
+__device__ __forceinline__ void add32(float2 (&acc)[32], const uint32_t (&r)[32], float f) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    acc[kAt + i] =
+        fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), make_float2(f, f), acc[kAt + i]);
+}
+
 template <bool kFp32, bool kVec>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_paired_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const Args a) {
@@ -1023,7 +1035,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     flag_store(abort_flag, 0);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bars.full(i), 1);
-      mbar_init(bars.empty(i), 1);
+      mbar_init(bars.empty(i), 2);  // both halves of the products
     }
     for (int i = 0; i < kScaleStages; ++i) {
       mbar_init(bars.sfull(i), 32);
@@ -1031,16 +1043,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(bars.tfull(i), 1);
-      mbar_init(bars.tempty(i), 2 * kEpiWarps);  // both CTAs' epilogues (the leader's barrier)
+      mbar_init(bars.tempty(i), kEpiWarps);  // both CTAs' epilogues (the leader's barrier)
     }
     mbar_init(bars.fin(), 1);
+    mbar_init(bars.fin() + 8, 1);
     fence_mbar_init();
     prefetch_tensormap(&tm_w);
     prefetch_tensormap(&tm_a);
   }
   __syncwarp();
   if (warp == 1) {
-    tmem_alloc2(smem_u32(tmem_slot), kBufs * kTileCol);
+    tmem_alloc2(smem_u32(tmem_slot), kBufs * kHalf);
     tmem_relinquish2();
   }
   pdl_wait();
@@ -1083,39 +1096,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // that left before the last ones came in would have them land in the
       // shared memory of whoever runs there next.  (They also follow the copies.)
       drain<kStages>(ring, j, bars);
-    } else if (warp == 1 && rank == 1) {
-      if (lane == 0) wait_limited(bars.fin(), 0);  // the leader's last arrival here
-    } else if (warp == 1) {
-      // ---- MMA issuer (the leader, for the pair): the whole warp runs the
-      // loop, one lane issues
-      constexpr uint32_t kIdesc = idesc_e4m3(kTileTok, kTileCol);
-      const uint32_t ta0 = desc_low(sbase), wa0 = desc_low(sbase + kHalf * kBlockK);
+    } else if ((warp == 1 || warp == 3) && rank == 1) {
+      if (lane == 0) wait_limited(bars.fin() + 8 * (warp >> 1), 0);  // the leader's last arrival here
+    } else if (warp == 1 || warp == 3) {
+      // ---- MMA issuers (the leader's, for the pair), one for each half: the
+      // whole warp runs the loop, one lane issues
+      const uint32_t half = warp >> 1;
+      constexpr uint32_t kIdesc = idesc_e4m3(kTileTok, kHalf);
+      const uint32_t ta0 = desc_low(sbase), wa0 = desc_low(sbase + kHalf * kBlockK + half * (kHalf / 2) * kBlockK);
       const bool issuer = elect_one();
       Ring<kStages> ring;
-      Ring<kBufs> buf;
+      Ring<2> buf;
       bool ok = true;
       for (int idx = first; ok && idx < tiles; idx += step) {
-        for (int kb = 0; kb < a.k_blocks; ++kb, ring.next(), buf.next()) {
-          if (!wait_bar_uniform(abort_flag, bars.full(ring.slot), ring.phase, 0x732) ||
-              !wait_bar_uniform(abort_flag, bars.tempty(buf.slot), buf.phase ^ 1, 0x733)) {
+        for (int kb = 0; ok && kb < a.k_blocks; ++kb, ring.next(), buf.next()) {
+          if (!wait_bar_uniform(abort_flag, bars.full(ring.slot), ring.phase, 0x732)) {
+            ok = false;
+            break;
+          }
+          const uint32_t b = 2 * buf.slot + half;
+          if (!wait_bar_uniform(abort_flag, bars.tempty(b), buf.phase ^ 1, 0x733)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t ta = ta0 + ring.slot * (kStage >> 4), wa = wa0 + ring.slot * (kStage >> 4);
-          const uint32_t d = tmem + buf.slot * kTileCol;
           if (issuer) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mma_f8_pair(d, ta + 2 * kk, wa + 2 * kk, kIdesc, kk > 0);
+            for (int kk = 0; kk < 4; ++kk) mma_f8_pair(tmem + b * kHalf, ta + 2 * kk, wa + 2 * kk, kIdesc, kk > 0);
             mma_commit_pair(bars.empty(ring.slot));
-            mma_commit_pair(bars.tfull(buf.slot));
+            mma_commit_pair(bars.tfull(b));
           }
           __syncwarp();
         }
       }
       if (issuer) {
-        mma_commit_pair(bars.fin());
-        wait_limited(bars.fin(), 0);
+        mma_commit_pair(bars.fin() + 8 * half);
+        wait_limited(bars.fin() + 8 * half, 0);
       }
     } else if (warp == 2) {
       // ---- scales: this CTA's tokens and the tile's two weight blocks
@@ -1147,48 +1164,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
-    // ---- epilogue: thread = token, registers = 128 weight rows.  A block's
-    // release is on the path from product to product, so little is on it: one
-    // wait, two TMEM reads with the additions of the first half between them.
+    // ---- epilogue: thread = token, registers = 128 weight rows: 64 of the
+    // leader's and 64 of its peer's, which have a weight scale each
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
     const int quad = warp & 3, part = (warp - 4) >> 2;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * kCols;
-    const uint32_t tempty = mapa(bars.tempty(0), 0);  // the leader's; buffer b at + 8 b
-    const uint32_t slots = sbase + kOffScales, mine = (quad * 32 + lane) * 4, other = (kHalf + part) * 4;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * kHalf;
+    const uint32_t tempty = mapa(bars.tempty(part), 0);  // the leader's; this half's next buffer at + 16
+    const uint32_t slots = sbase + kOffScales, mine = (quad * 32 + lane) * 4;
     uint32_t n = 0, group = 0;  // blocks and groups of scales so far
     bool ok = true;
     for (int idx = first; ok && idx < tiles; idx += step) {
-      float2 acc[kCols / 2];
+      float2 acc0[kCols / 4], acc1[kCols / 4];
 #pragma unroll
-      for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < kCols / 4; ++i) acc0[i] = acc1[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int kb = 0; kb < a.k_blocks; ++kb, ++n) {
-        const uint32_t ring = group % kScaleStages, buf = n % kBufs;
+        const uint32_t ring = group % kScaleStages, buf = n % 2;
         if (kb % kScaleGroup == 0 && !wait_bar_warp(abort_flag, bars.sfull(ring), (group / kScaleStages) & 1, 0x735)) {
           ok = false;
           break;
         }
         const uint32_t slot = slots + (ring * kScaleSlot + (kb % kScaleGroup) * kScaleRow) * 4;
-        const float f = ld_shared_f32(slot + mine) * ld_shared_f32(slot + other);
-        if (!wait_bar_warp(abort_flag, bars.tfull(buf), (n / kBufs) & 1, 0x736)) {
+        const float f = ld_shared_f32(slot + mine);
+        const float f0 = f * ld_shared_f32(slot + kHalf * 4), f1 = f * ld_shared_f32(slot + kHalf * 4 + 4);
+        if (!wait_bar_warp(abort_flag, bars.tfull(2 * buf + part), (n / 2) & 1, 0x736)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const float2 f2 = make_float2(f, f);
-        const uint32_t src = taddr + buf * kTileCol;
-        uint32_t r[64];
-        tmem_ld64(src, r);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          acc[i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[i]);
-        tmem_ld64(src + 64, r);
+        const uint32_t src = taddr + buf * (2 * kHalf);
+        uint32_t r0[32], r1[32];
+        tmem_ld32_async(src, r0);
+        tmem_wait_ld32(r0);
+        tmem_ld32_async(src + 32, r1);
+        add32<0>(acc0, r0, f0);
+        tmem_wait_ld32(r1);
+        tmem_ld32_async(src + 64, r0);
+        add32<16>(acc0, r1, f0);
+        tmem_wait_ld32(r0);
+        tmem_ld32_async(src + 96, r1);
+        add32<0>(acc1, r0, f1);
+        tmem_wait_ld32(r1);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_pair(tempty + 8 * buf);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          acc[32 + i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[32 + i]);
+        if (lane == 0) mbar_arrive_pair(tempty + 16 * buf);
+        add32<16>(acc1, r1, f1);
         if (kb % kScaleGroup == kScaleGroup - 1 || kb + 1 == a.k_blocks) {
           __syncwarp();
           if (lane == 0) mbar_arrive(bars.sempty(ring));
@@ -1197,8 +1217,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       const Tile t = find(a, prefix, idx);  // here, not before: nothing of it occupies registers while the sums do
-      store_rows<kCols, kFp32, kVec>(a, sbase + kOffStaging + (warp - 4) * kStaging, t.tok0 + rank * kHalf + quad * 32,
-                                     t.tok_end, t.row_block * kTileCol + part * kCols, lane, acc);
+      const int m0 = t.tok0 + rank * kHalf + quad * 32, n0 = t.row_block * kTileCol + part * 64;
+      const uint32_t staging = sbase + kOffStaging + (warp - 4) * kStaging;
+      store_rows<kCols / 2, kFp32, kVec>(a, staging, m0, t.tok_end, n0, lane, acc0);
+      store_rows<kCols / 2, kFp32, kVec>(a, staging, m0, t.tok_end, n0 + kHalf, lane, acc1);
     }
   }
   __syncwarp();
@@ -1206,7 +1228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();  // every product is read and no remote arrival is left
   tc_fence_after();
-  if (warp == 1) tmem_dealloc2(tmem, kBufs * kTileCol);
+  if (warp == 1) tmem_dealloc2(tmem, kBufs * kHalf);
   cluster_sync();
 }
 
