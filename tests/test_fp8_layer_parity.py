@@ -192,6 +192,20 @@ def test_silu_mul(t, d, pad, y_dtype):
     assert torch.all(yw[:, d:].float() == 7)
 
 
+def test_silu_mul_of_infinities():
+    inf, nan, big = float("inf"), float("nan"), 2.0 ** 127
+    gate = [inf, inf, -inf, nan, big, -big, 0.0, -0.0, -80.0]
+    up = [2.0, -2.0, 1.0, 1.0, 1.0, 1.0, inf, 3.0, 1.0]
+    x = torch.tensor([gate + up], dtype=torch.bfloat16, device="cuda")
+    y = torch.empty(1, len(gate), dtype=torch.bfloat16, device="cuda")
+    B.mla_act_quantize(x, B.MLA_ACT_SILU_MUL, y, B.MLA_OUT_BF16, None)
+    got = y[0].float().tolist()
+    # g / (1 + e^-g): the gate itself, -inf / inf, and 0 times an infinity
+    assert got[:2] == [inf, -inf] and all(np.isnan(got[i]) for i in (2, 3, 6))
+    assert got[4] == big and got[5] == 0 and got[7] == 0
+    assert abs(got[8] + 80 * np.exp(-80.0)) <= (BF16_HALF + 2.0 ** -14) * 80 * np.exp(-80.0)
+
+
 # ------------------------------------------------------------------ products
 
 
