@@ -245,6 +245,23 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+// Copies from shared to global memory: a box, the commit of its group, and the
+// waits for the groups' reads and for their ends.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// threadIdx.x, read where it stands: what is computed from it is not moved out of loops
+__device__ __forceinline__ int thread_index() {
+  int v;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(v));
+  return v;
+}
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   union U { float2 f; uint64_t u; } x, y, z, d;
   x.f = a; y.f = b; z.f = c;
@@ -637,69 +654,72 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
   }
 }
 
-// The warp's 32 rows x kCols columns of results, through shared memory in
-// pieces of 64 bytes a row: stored straight from the registers, every
-// instruction would touch 32 rows (measured: 3400 cycles a tile).
-template <int kCols, bool kFp32, bool kVec>
-__device__ __forceinline__ void store_rows(const Args& a, uint32_t staging, int m0, int tok_end, int n0, int lane,
-                                           const float2 (&acc)[kCols / 2]) {
-  constexpr int kPiece = kFp32 ? 16 : 32;  // columns of a piece
+// The warp's 32 rows x 64 columns of results, kBytes of each row at a time through
+// shared memory (in the order of a TMA swizzle) and from there by TMA, which
+// drains while the next tile is computed.  Stored by the warps themselves they
+// cost a paired tile 1.9 us, since every SM stores at once: 8192 tokens, n 8192, k
+// 2048 134 us instead of 122.  A tile whose last rows are the next expert's is
+// stored row by row.
+template <int kBytes, bool kFp32, bool kVec>
+__device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap* tm_out, uint32_t staging, int m0, int tok_end,
+                                           int n0, int lane, const float2 (&acc)[32]) {
+  constexpr int kElt = kFp32 ? 4 : 2, kPiece = kBytes / kElt, kPer16 = 16 / kElt, kChunks = kBytes / 16;
+  auto swizzled = [&](int row, int c) {
+    return staging + row * kBytes + ((c ^ (kBytes == 128 ? row & 7 : (row >> 1) & 3)) << 4);
+  };
 #pragma unroll
-  for (int p = 0; p < kCols / kPiece; ++p) {
+  for (int p = 0; p < 64 / kPiece; ++p) {
+    if (kVec && lane == 0) bulk_wait_read();
+    __syncwarp();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t at = staging + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
+    for (int c = 0; c < kChunks; ++c) {
+      const uint32_t at = swizzled(lane, c);
       if (kFp32) {  // pairs, as the sums are held
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float2 x = acc[(p * kPiece + 4 * q) / 2 + i];
+          const float2 x = acc[(p * kPiece + 4 * c) / 2 + i];
           asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at + 8 * i), "f"(x.x), "f"(x.y) : "memory");
         }
       } else {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 x = acc[(p * kPiece + 8 * q) / 2 + i];
+          const float2 x = acc[(p * kPiece + 8 * c) / 2 + i];
           __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
           w[i] = *reinterpret_cast<uint32_t*>(&b);
         }
         st_shared_v4(at, make_uint4(w[0], w[1], w[2], w[3]));
       }
     }
-    __syncwarp();
     const int n = n0 + p * kPiece;
-    if (kVec && n + kPiece <= a.n) {
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2), q = lane & 3;
-        const uint4 v = ld_shared_v4(staging + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
-        if (m0 + r < tok_end) {
-          const int64_t at = (m0 + r) * a.ldo + n + q * (kFp32 ? 4 : 8);
-          if (kFp32)
-            *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + at) = v;
-          else
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at) = v;
-        }
-      }
+    // whole boxes, or cut at the array's end; along a row TMA cuts at 16 bytes
+    const bool rows = m0 + 32 <= tok_end || tok_end == a.m, cols = n + kPiece <= a.n || a.n % kPer16 == 0;
+    if (kVec && rows && cols) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && m0 < tok_end && n < a.n) tma_store_2d(tm_out, staging, n * kElt, m0);
     } else {
-      const int c = lane & (kPiece - 1);
+      __syncwarp();
+      const int chunk = lane % kChunks, col = n + chunk * kPer16;
 #pragma unroll 1
-      for (int r = lane / kPiece; r < 32; r += 32 / kPiece) {
-        const uint32_t at = staging + r * 64 + (((c / (kFp32 ? 4 : 8)) ^ ((r >> 1) & 3)) << 4);
-        if (m0 + r < tok_end && n + c < a.n) {
-          if (kFp32) {
-            uint32_t v;
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at + (c & 3) * 4) : "memory");
-            static_cast<float*>(a.out)[(m0 + r) * a.ldo + n + c] = __uint_as_float(v);
-          } else {
-            uint16_t v;
-            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(at + (c & 7) * 2) : "memory");
-            static_cast<uint16_t*>(a.out)[(m0 + r) * a.ldo + n + c] = v;
-          }
+      for (int row = lane / kChunks; row < min(32, tok_end - m0); row += 32 / kChunks) {
+        const uint4 v = ld_shared_v4(swizzled(row, chunk));
+        uint8_t* dst = static_cast<uint8_t*>(a.out) + ((m0 + row) * a.ldo + col) * kElt;
+        if (kVec && col + kPer16 <= a.n) {
+          *reinterpret_cast<uint4*>(dst) = v;
+        } else {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < kPer16; ++e)
+            if (col + e < a.n) {
+              if (kFp32)
+                reinterpret_cast<uint32_t*>(dst)[e] = w[e];
+              else
+                reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+            }
         }
       }
     }
-    __syncwarp();
   }
 }
 
@@ -712,8 +732,8 @@ __device__ __forceinline__ void store_rows(const Args& a, uint32_t staging, int 
 // is; a buffer is given back as soon as it is read, and four of them keep the
 // products ahead.  Two warps issue the products in turn: the instructions of one
 // block take an issuing warp about 550 cycles here, the products 256.
-// 256 x 8192 x 8192: 21.5 us (swapped tiles of 64 tokens 43 us, paired 37 us; the
-// weights alone 10.6 us); 256 x 4096 x 4096: 12.7 us (17.1, 21.0).
+// 256 x 8192 x 8192: 21.5 us (swapped tiles of 64 tokens 43 us, paired 35 us; the
+// weights alone 10.6 us); 256 x 4096 x 4096: 12.7 us (17.1, 19.9).
 namespace square {
 
 constexpr int kTileTok = 128, kTileCol = 128;
@@ -730,7 +750,7 @@ constexpr int kBufs = 4;                       // of 128 TMEM columns
 constexpr int kEpiWarps = 8;
 constexpr int kCols = kTileCol / (kEpiWarps / 4);
 constexpr int kThreads = 32 * (4 + kEpiWarps);
-constexpr int kStaging = 32 * 64;              // per epilogue warp: 64 bytes of each of its 32 output rows
+constexpr int kStaging = 32 * 64;              // per epilogue warp: 64 bytes of each of its 32 output rows, swizzled
 constexpr int kOffStaging = kStages * kStage;
 constexpr int kOffScales = kOffStaging + kEpiWarps * kStaging;
 constexpr int kOffPrefix = kOffScales + kScaleStages * kScaleSlot * 4;
@@ -743,7 +763,8 @@ __device__ __forceinline__ Tile find(const Args& a, const int* prefix, int idx) 
 
 template <bool kFp32, bool kVec>
 __global__ void __launch_bounds__(kThreads, 1)
-    gemm_square_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const Args a) {
+    gemm_square_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
+                       const __grid_constant__ CUtensorMap tm_out, const Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -912,8 +933,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc[16 + i] = fma2(make_float2(__uint_as_float(r1[2 * i]), __uint_as_float(r1[2 * i + 1])), f2, acc[16 + i]);
       }
       if (!ok) break;
-      store_rows<kCols, kFp32, kVec>(a, staging, m0, t.tok_end, t.row_block * kTileCol + part * kCols, lane, acc);
+      store_tile<64, kFp32, kVec>(a, &tm_out, staging, m0, t.tok_end, t.row_block * kTileCol + part * kCols, lane, acc);
     }
+    if (kVec && lane == 0) bulk_wait();
   }
   __syncwarp();
   tc_fence_before();
@@ -936,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of 64 of each CTA's weight rows, issued by a warp each into buffers of their own,
 // and half of the epilogue's warps take each half: they run out of step, and
 // within a warp 32 columns are read while 32 are added.  8192 tokens, n = k = 8192:
-// 423..450 us, 2.5 PFLOP/s (both halves in one product, all warps in step, reads and
+// 428..446 us, 2.5 PFLOP/s (both halves in one product, all warps in step, reads and
 // additions in turn: 3 % more; in square tiles 475 us).  Spills in the epilogue's loop
 // cost 4 to 20 % and are kept out: 216 registers, state that is counted, not kept.
 namespace paired {
@@ -944,7 +966,7 @@ namespace paired {
 constexpr int kTileTok = 256, kTileCol = 256;  // of the pair
 constexpr int kHalf = 128;
 constexpr int kStage = 2 * kHalf * kBlockK;    // per CTA: tokens, then weights
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kScaleGroup = 4;                 // k blocks whose scales share a slot (and a wait)
 constexpr int kScaleStages = 4;
 constexpr int kScaleRow = kHalf + 4;           // token scales, then two weight scales
@@ -956,7 +978,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kCols = kTileCol / (kEpiWarps / 4);
 constexpr int kThreads = 32 * (4 + kEpiWarps);
 constexpr int kRegsLoad = 72, kRegsEpi = 216;  // 128 x 72 + 256 x 216 = 384 x 168, the launch's registers
-constexpr int kStaging = 32 * 64;              // per epilogue warp: 64 bytes of each of its 32 output rows
+constexpr int kStaging = 32 * 128;             // per epilogue warp: 128 bytes of each of its 32 output rows, swizzled
 constexpr int kOffStaging = kStages * kStage;
 constexpr int kOffScales = kOffStaging + kEpiWarps * kStaging;
 constexpr int kOffPrefix = kOffScales + kScaleStages * kScaleSlot * 4;
@@ -1020,7 +1042,8 @@ __device__ __forceinline__ void add32(float2 (&acc)[32], const uint32_t (&r)[32]
 
 template <bool kFp32, bool kVec>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    gemm_paired_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const Args a) {
+    gemm_paired_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
+                       const __grid_constant__ CUtensorMap tm_out, const Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -1216,12 +1239,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      const Tile t = find(a, prefix, idx);  // here, not before: nothing of it occupies registers while the sums do
+      // The tile is looked up and the thread asked for its place here, not before:
+      // none of it occupies registers while the sums do.
+      const Tile t = find(a, prefix, idx);
+      const int tid = thread_index(), lane = tid & 31, quad = (tid >> 5) & 3, part = (tid >> 7) - 1;
       const int m0 = t.tok0 + rank * kHalf + quad * 32, n0 = t.row_block * kTileCol + part * 64;
-      const uint32_t staging = sbase + kOffStaging + (warp - 4) * kStaging;
-      store_rows<kCols / 2, kFp32, kVec>(a, staging, m0, t.tok_end, n0, lane, acc0);
-      store_rows<kCols / 2, kFp32, kVec>(a, staging, m0, t.tok_end, n0 + kHalf, lane, acc1);
+      const uint32_t staging = sbase + kOffStaging + ((tid >> 5) - 4) * kStaging;
+      store_tile<128, kFp32, kVec>(a, &tm_out, staging, m0, t.tok_end, n0, lane, acc0);
+      store_tile<128, kFp32, kVec>(a, &tm_out, staging, m0, t.tok_end, n0 + kHalf, lane, acc1);
     }
+    if (kVec && lane == 0) bulk_wait();
   }
   __syncwarp();
   tc_fence_before();
@@ -1251,16 +1278,27 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // Rows of k bytes with a row pitch of ld bytes, read as 128-byte x box_rows
 // boxes in the 128-byte swizzle; bytes past k and rows past the end read as 0.
-static bool make_map(CUtensorMap* map, const void* p, int64_t k, int64_t rows, int64_t ld, int box_rows) {
+static bool make_map(CUtensorMap* map, const void* p, int64_t k, int64_t rows, int64_t ld, int box_rows,
+                     int box_bytes = kBlockK) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)ld};
-  cuuint32_t box[2] = {(cuuint32_t)kBlockK, (cuuint32_t)box_rows};
+  cuuint32_t box[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The results' map for the stores of 32-row boxes; unused (zeros) where !kVec.
+template <bool kFp32, bool kVec>
+static bool make_out_map(CUtensorMap* map, const Args& a, int box_bytes) {
+  constexpr int64_t kElt = kFp32 ? 4 : 2;
+  if (kVec) return make_map(map, a.out, a.n * kElt, a.m, a.ldo * kElt, 32, box_bytes);
+  *map = CUtensorMap{};
+  return true;
 }
 
 // Token tiles of TN rows: at most this many exist, whatever the offsets say.
@@ -1362,10 +1400,11 @@ static cudaError_t launch_square(const void* act, int64_t lda, const void* w, in
     attr_err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, square::kSmem);
   });
   if (attr_err != cudaSuccess) return attr_err;
-  CUtensorMap tm_w, tm_a;
+  CUtensorMap tm_w, tm_a, tm_out;
   if (!make_map(&tm_w, w, k, (int64_t)a.experts * a.n, ldw, square::kTileCol) ||
       !make_map(&tm_a, act, k, a.m, lda, square::kTileTok))
     return cudaErrorNotSupported;
+  if (!make_out_map<kFp32, kVec>(&tm_out, a, 64)) return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<int64_t>(most_token_tiles(a, square::kTileTok) * a.row_blocks, sms));
   cfg.blockDim = dim3(square::kThreads);
@@ -1376,7 +1415,7 @@ static cudaError_t launch_square(const void* act, int64_t lda, const void* w, in
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, a);
+  return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, tm_out, a);
 }
 
 template <bool kFp32, bool kVec>
@@ -1389,10 +1428,11 @@ static cudaError_t launch_paired(const void* act, int64_t lda, const void* w, in
     attr_err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, paired::kSmem);
   });
   if (attr_err != cudaSuccess) return attr_err;
-  CUtensorMap tm_w, tm_a;
+  CUtensorMap tm_w, tm_a, tm_out;
   if (!make_map(&tm_w, w, k, (int64_t)a.experts * a.n, ldw, paired::kHalf) ||
       !make_map(&tm_a, act, k, a.m, lda, paired::kHalf))
     return cudaErrorNotSupported;
+  if (!make_out_map<kFp32, kVec>(&tm_out, a, 128)) return cudaErrorNotSupported;
   a.row_blocks = (a.n + paired::kTileCol - 1) / paired::kTileCol;
   const int64_t pairs = std::min<int64_t>(most_token_tiles(a, paired::kTileTok) * a.row_blocks, sms / 2);
   cudaLaunchConfig_t cfg = {};
@@ -1405,7 +1445,7 @@ static cudaError_t launch_paired(const void* act, int64_t lda, const void* w, in
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, a);
+  return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, tm_out, a);
 }
 
 // The form with the least estimated time.  The estimate's constants are times in
@@ -1418,8 +1458,8 @@ static cudaError_t launch_paired(const void* act, int64_t lda, const void* w, in
 //   the weights cannot come faster than 6.3 TB/s.
 // The chosen form is the fastest one within 1 % on average over those sizes, within
 // 15 % at worst.  Where forms meet (n = k = 4096): 64 tokens 32 swapped in 4 parts
-// 9.5, 64 in 4 9.8; 128 tokens 64 in 4 12.6, square 12.4; 512 tokens square 12.6,
-// paired 20.0; 1024 tokens square 21.8, paired 20.6.
+// 9.5, 64 in 4 9.8; 128 tokens 64 in 4 12.6, square 12.5; 512 tokens square 12.8,
+// paired 19.8; 1024 tokens square 21.8, paired 20.4; 4096 tokens square 66.9, paired 66.2.
 enum Shape { kSwapped16 = 16, kSwapped32 = 32, kSwapped64 = 64, kSquare = 128, kPaired = 256 };
 struct Choice {
   double time = 1e30;
@@ -1481,7 +1521,7 @@ static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64
   if (a.m > 128) {
     const int64_t row_tiles = (a.n + paired::kTileCol - 1) / paired::kTileCol;
     const int64_t rounds = (expected_tiles(a, paired::kTileTok, row_tiles) + sms / 2 - 1) / (sms / 2);
-    c.offer(std::max(rounds * (a.k_blocks * 0.435 + 2.7), weights) + 3.3, kPaired, 1);
+    c.offer(std::max(rounds * (a.k_blocks * 0.45 + 1.3), weights) + 3.3, kPaired, 1);
   }
   const bool vec = a.ldo % (kFp32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
   switch (c.shape) {

@@ -300,6 +300,43 @@ def test_grouped_gemm_exact_integers_large(counts, n, k):
         assert torch.equal(out[lo:hi], (ad[lo:hi] @ wd.t()).float())
 
 
+@pytest.mark.parametrize("kind,unit", [(torch.bfloat16, 8), (torch.float32, 4)])
+@pytest.mark.parametrize("n", [4095, 4097, 4100, 4104, 4160])
+@pytest.mark.parametrize("t", [300, 4097])
+def test_gemm_results_inside_wider_rows(t, n, kind, unit):
+    """Tiles cut at the right edge and below, in rows of 16-byte multiples: what
+    lies beside and below the results stays."""
+    k = 256
+    a, sa, w, sw = operands(np.random.default_rng(t + n), t, n, k, integers=True)
+    ad = a.double() * sa.double().t().repeat_interleave(128, 1)
+    wd = w[0].double() * sw[0].double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)
+    want = (ad @ wd.t()).to(kind)
+    for width in (-(-n // unit) * unit, -(-n // unit) * unit + unit):
+        wide = torch.full((t + 3, width), 7.0, device="cuda", dtype=kind)
+        B.mla_gemm_fp8(a, sa, w[0], sw[0], wide[:t, :n], B.MLA_OUT_BF16 if kind == torch.bfloat16 else B.MLA_OUT_FP32)
+        assert B.mla_decode_device_error() == 0
+        assert torch.equal(wide[:t, :n], want)
+        assert torch.all(wide[t:] == 7) and torch.all(wide[:, n:] == 7)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("counts,n", [([3000, 37, 0, 2100], 4104), ([130, 0, 129, 1, 300], 1096)])
+def test_grouped_gemm_large_unowned_rows(counts, n, kind):
+    k, head, tail = 256, 5, 70
+    t = head + sum(counts) + tail
+    a, sa, w, sw = operands(np.random.default_rng(t + n), t, n, k, len(counts), True)
+    off = (head + np.concatenate([[0], np.cumsum(counts)])).astype(np.int32)
+    out = torch.full((t, n), 7.0, device="cuda", dtype=kind)
+    B.mla_grouped_gemm_fp8(a, sa, w, sw, torch.from_numpy(off).cuda(), out,
+                           B.MLA_OUT_BF16 if kind == torch.bfloat16 else B.MLA_OUT_FP32)
+    assert B.mla_decode_device_error() == 0
+    ad = a.double() * sa.double().t().repeat_interleave(128, 1)
+    for e, (lo, hi) in enumerate(zip(off[:-1], off[1:])):
+        wd = w[e].double() * sw[e].double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)
+        assert torch.equal(out[lo:hi], (ad[lo:hi] @ wd.t()).to(kind))
+    assert torch.all(out[:head] == 7) and torch.all(out[off[-1]:] == 7)
+
+
 def run_grouped(rng, counts, n, k, kind, integers, head=0, tail=0):
     t = head + int(sum(counts)) + tail
     a, sa, w, sw = operands(rng, t, n, k, len(counts), integers)
