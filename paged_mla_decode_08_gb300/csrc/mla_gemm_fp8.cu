@@ -245,16 +245,19 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
-// Copies from shared to global memory: a box, the commit of its group, and the
-// waits for the groups' reads and for their ends.
+// Copies from shared to global memory: a box, the end of a group, the waits until
+// at most kPending groups still read and until all are done.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
-      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
       "r"(src), "r"(x), "r"(y)
       : "memory");
 }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
+}
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // threadIdx.x, read where it stands: what is computed from it is not moved out of loops
 __device__ __forceinline__ int thread_index() {
@@ -656,24 +659,24 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
 
 // The warp's 32 rows x 64 columns of results, kBytes of each row at a time through
 // shared memory (in the order of a TMA swizzle) and from there by TMA, which
-// drains while the next tile is computed.  Stored by the warps themselves they
-// cost a paired tile 1.9 us, since every SM stores at once: 8192 tokens, n 8192, k
-// 2048 134 us instead of 122.  A tile whose last rows are the next expert's is
-// stored row by row.
-template <int kBytes, bool kFp32, bool kVec>
-__device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap* tm_out, uint32_t staging, int m0, int tok_end,
+// drains while the next tile is computed.  kPart: which of a tile's calls; the
+// pieces go through the warp's buffers in turn.  Stored by the warps themselves
+// the results cost a paired tile 1.9 us, since every SM stores at once: 8192 tokens,
+// n 8192, k 2048 134 us, 122 with one buffer and five stages, 119 with two and four.
+// A tile whose last rows are the next expert's is stored row by row.
+template <int kBytes, int kBuffers, int kPart, bool kFp32, bool kVec>
+__device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap* tm_out, uint32_t buffers, int m0, int tok_end,
                                            int n0, int lane, const float2 (&acc)[32]) {
   constexpr int kElt = kFp32 ? 4 : 2, kPiece = kBytes / kElt, kPer16 = 16 / kElt, kChunks = kBytes / 16;
-  auto swizzled = [&](int row, int c) {
-    return staging + row * kBytes + ((c ^ (kBytes == 128 ? row & 7 : (row >> 1) & 3)) << 4);
-  };
+  auto swizzled = [](int row, int c) { return row * kBytes + ((c ^ (kBytes == 128 ? row & 7 : (row >> 1) & 3)) << 4); };
 #pragma unroll
   for (int p = 0; p < 64 / kPiece; ++p) {
-    if (kVec && lane == 0) bulk_wait_read();
+    const uint32_t staging = buffers + (kPart * (64 / kPiece) + p) % kBuffers * (32 * kBytes);
+    if (kVec && lane == 0) bulk_wait_read<kBuffers - 1>();
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      const uint32_t at = swizzled(lane, c);
+      const uint32_t at = staging + swizzled(lane, c);
       if (kFp32) {  // pairs, as the sums are held
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -703,7 +706,7 @@ __device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap* tm_
       const int chunk = lane % kChunks, col = n + chunk * kPer16;
 #pragma unroll 1
       for (int row = lane / kChunks; row < min(32, tok_end - m0); row += 32 / kChunks) {
-        const uint4 v = ld_shared_v4(swizzled(row, chunk));
+        const uint4 v = ld_shared_v4(staging + swizzled(row, chunk));
         uint8_t* dst = static_cast<uint8_t*>(a.out) + ((m0 + row) * a.ldo + col) * kElt;
         if (kVec && col + kPer16 <= a.n) {
           *reinterpret_cast<uint4*>(dst) = v;
@@ -720,6 +723,7 @@ __device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap* tm_
         }
       }
     }
+    if (kVec && lane == 0) bulk_commit();  // also of nothing: the wait counts pieces
   }
 }
 
@@ -933,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc[16 + i] = fma2(make_float2(__uint_as_float(r1[2 * i]), __uint_as_float(r1[2 * i + 1])), f2, acc[16 + i]);
       }
       if (!ok) break;
-      store_tile<64, kFp32, kVec>(a, &tm_out, staging, m0, t.tok_end, t.row_block * kTileCol + part * kCols, lane, acc);
+      store_tile<64, 1, 0, kFp32, kVec>(a, &tm_out, staging, m0, t.tok_end, t.row_block * kTileCol + part * kCols, lane, acc);
     }
     if (kVec && lane == 0) bulk_wait();
   }
@@ -958,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of 64 of each CTA's weight rows, issued by a warp each into buffers of their own,
 // and half of the epilogue's warps take each half: they run out of step, and
 // within a warp 32 columns are read while 32 are added.  8192 tokens, n = k = 8192:
-// 428..446 us, 2.5 PFLOP/s (both halves in one product, all warps in step, reads and
+// 423..440 us, 2.5 PFLOP/s (both halves in one product, all warps in step, reads and
 // additions in turn: 3 % more; in square tiles 475 us).  Spills in the epilogue's loop
 // cost 4 to 20 % and are kept out: 216 registers, state that is counted, not kept.
 namespace paired {
@@ -966,7 +970,7 @@ namespace paired {
 constexpr int kTileTok = 256, kTileCol = 256;  // of the pair
 constexpr int kHalf = 128;
 constexpr int kStage = 2 * kHalf * kBlockK;    // per CTA: tokens, then weights
-constexpr int kStages = 5;
+constexpr int kStages = 4;
 constexpr int kScaleGroup = 4;                 // k blocks whose scales share a slot (and a wait)
 constexpr int kScaleStages = 4;
 constexpr int kScaleRow = kHalf + 4;           // token scales, then two weight scales
@@ -978,7 +982,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kCols = kTileCol / (kEpiWarps / 4);
 constexpr int kThreads = 32 * (4 + kEpiWarps);
 constexpr int kRegsLoad = 72, kRegsEpi = 216;  // 128 x 72 + 256 x 216 = 384 x 168, the launch's registers
-constexpr int kStaging = 32 * 128;             // per epilogue warp: 128 bytes of each of its 32 output rows, swizzled
+constexpr int kStaging = 2 * 32 * 128;         // per epilogue warp: twice 128 bytes of each of its 32 output rows, swizzled
 constexpr int kOffStaging = kStages * kStage;
 constexpr int kOffScales = kOffStaging + kEpiWarps * kStaging;
 constexpr int kOffPrefix = kOffScales + kScaleStages * kScaleSlot * 4;
@@ -1245,8 +1249,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int tid = thread_index(), lane = tid & 31, quad = (tid >> 5) & 3, part = (tid >> 7) - 1;
       const int m0 = t.tok0 + rank * kHalf + quad * 32, n0 = t.row_block * kTileCol + part * 64;
       const uint32_t staging = sbase + kOffStaging + ((tid >> 5) - 4) * kStaging;
-      store_tile<128, kFp32, kVec>(a, &tm_out, staging, m0, t.tok_end, n0, lane, acc0);
-      store_tile<128, kFp32, kVec>(a, &tm_out, staging, m0, t.tok_end, n0 + kHalf, lane, acc1);
+      store_tile<128, 2, 0, kFp32, kVec>(a, &tm_out, staging, m0, t.tok_end, n0, lane, acc0);
+      store_tile<128, 2, 1, kFp32, kVec>(a, &tm_out, staging, m0, t.tok_end, n0 + kHalf, lane, acc1);
     }
     if (kVec && lane == 0) bulk_wait();
   }
@@ -1521,7 +1525,7 @@ static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64
   if (a.m > 128) {
     const int64_t row_tiles = (a.n + paired::kTileCol - 1) / paired::kTileCol;
     const int64_t rounds = (expected_tiles(a, paired::kTileTok, row_tiles) + sms / 2 - 1) / (sms / 2);
-    c.offer(std::max(rounds * (a.k_blocks * 0.45 + 1.3), weights) + 3.3, kPaired, 1);
+    c.offer(std::max(rounds * (a.k_blocks * 0.45 + 1.0), weights) + 3.3, kPaired, 1);
   }
   const bool vec = a.ldo % (kFp32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
   switch (c.shape) {
