@@ -964,7 +964,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // within a warp 32 columns are read while 32 are added.  8192 tokens, n = k = 8192:
 // 423..440 us, 2.5 PFLOP/s (both halves in one product, all warps in step, reads and
 // additions in turn: 3 % more; in square tiles 475 us).  Spills in the epilogue's loop
-// cost 4 to 20 % and are kept out: 216 registers, state that is counted, not kept.
+// cost 4 to 20 %, so it has 216 registers and its state is counted, not kept (8 bytes
+// are left with bf16 results, none with fp32).
 namespace paired {
 
 constexpr int kTileTok = 256, kTileCol = 256;  // of the pair
@@ -1197,7 +1198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, part = (warp - 4) >> 2;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * kHalf;
     const uint32_t tempty = mapa(bars.tempty(part), 0);  // the leader's; this half's next buffer at + 16
-    const uint32_t slots = sbase + kOffScales, mine = (quad * 32 + lane) * 4;
+    const uint32_t slots = sbase + kOffScales;
     uint32_t n = 0, group = 0;  // blocks and groups of scales so far
     bool ok = true;
     for (int idx = first; ok && idx < tiles; idx += step) {
@@ -1212,7 +1213,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         const uint32_t slot = slots + (ring * kScaleSlot + (kb % kScaleGroup) * kScaleRow) * 4;
-        const float f = ld_shared_f32(slot + mine);
+        const float f = ld_shared_f32(slot + (threadIdx.x & 127) * 4);  // this thread's token
         const float f0 = f * ld_shared_f32(slot + kHalf * 4), f1 = f * ld_shared_f32(slot + kHalf * 4 + 4);
         if (!wait_bar_warp(abort_flag, bars.tfull(2 * buf + part), (n / 2) & 1, 0x736)) {
           ok = false;
@@ -1234,11 +1235,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_wait_ld32(r1);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_pair(tempty + 16 * buf);
+        if (elect_one()) mbar_arrive_pair(tempty + 16 * buf);
         add32<16>(acc1, r1, f1);
         if (kb % kScaleGroup == kScaleGroup - 1 || kb + 1 == a.k_blocks) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(bars.sempty(ring));
+          if (elect_one()) mbar_arrive(bars.sempty(ring));
           ++group;
         }
       }
