@@ -265,6 +265,16 @@ __device__ __forceinline__ int thread_index() {
   asm volatile("mov.u32 %0, %%tid.x;" : "=r"(v));
   return v;
 }
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint16_t ld_shared_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   union U { float2 f; uint64_t u; } x, y, z, d;
   x.f = a; y.f = b; z.f = c;
@@ -663,7 +673,10 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
 // pieces go through the warp's buffers in turn.  Stored by the warps themselves
 // the results cost a paired tile 1.9 us, since every SM stores at once: 8192 tokens,
 // n 8192, k 2048 134 us, 122 with one buffer and five stages, 119 with two and four.
-// A tile whose last rows are the next expert's is stored row by row.
+// A piece that TMA cannot cut (its last rows are the next expert's, or rows that are
+// no multiple of 16 bytes) is read back along the rows, by the widest words that the
+// rows' alignment allows: 4096 x 4095 x 1024 31 us (4096 x 4096 23 us; 16 bytes of a row
+// per lane, stored one by one: 80 us).
 template <int kBytes, int kBuffers, int kPart, bool kFp32, bool kVec>
 __device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap* tm_out, uint32_t buffers, int m0, int tok_end,
                                            int n0, int lane, const float2 (&acc)[32]) {
@@ -703,24 +716,37 @@ __device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap* tm_
       if (lane == 0 && m0 < tok_end && n < a.n) tma_store_2d(tm_out, staging, n * kElt, m0);
     } else {
       __syncwarp();
-      const int chunk = lane % kChunks, col = n + chunk * kPer16;
-#pragma unroll 1
-      for (int row = lane / kChunks; row < min(32, tok_end - m0); row += 32 / kChunks) {
-        const uint4 v = ld_shared_v4(staging + swizzled(row, chunk));
-        uint8_t* dst = static_cast<uint8_t*>(a.out) + ((m0 + row) * a.ldo + col) * kElt;
-        if (kVec && col + kPer16 <= a.n) {
-          *reinterpret_cast<uint4*>(dst) = v;
-        } else {
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const int last = min(32, tok_end - m0), left = a.n - n;
+      uint8_t* dst = static_cast<uint8_t*>(a.out) + (m0 * a.ldo + n) * kElt;
+      const int64_t pitch = a.ldo * kElt;
+      if (kVec && cols) {
+        const int chunk = lane % kChunks;
+#pragma unroll 2
+        for (int row = lane / kChunks; row < last; row += 32 / kChunks)
+          if (chunk * kPer16 < left)
+            *reinterpret_cast<uint4*>(dst + row * pitch + chunk * 16) = ld_shared_v4(staging + swizzled(row, chunk));
+      } else if (kFp32 || (a.ldo % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0)) {
+        // neighbouring lanes store neighbouring 4 bytes: a value, or two
+        constexpr int kWords = kBytes / 4, kRows = 32 / kWords > 0 ? 32 / kWords : 1;
 #pragma unroll
-          for (int e = 0; e < kPer16; ++e)
-            if (col + e < a.n) {
-              if (kFp32)
-                reinterpret_cast<uint32_t*>(dst)[e] = w[e];
-              else
-                reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
-            }
-        }
+        for (int word = lane % kWords; word < kWords; word += 32)
+#pragma unroll 4
+          for (int row = lane / kWords; row < last; row += kRows) {
+            const uint32_t v = ld_shared_u32(staging + swizzled(row, word / 4) + word % 4 * 4);
+            uint8_t* at = dst + row * pitch + word * 4;
+            if ((word + 1) * (4 / kElt) <= left)
+              *reinterpret_cast<uint32_t*>(at) = v;
+            else if (!kFp32 && word * 2 < left)
+              *reinterpret_cast<uint16_t*>(at) = (uint16_t)v;
+          }
+      } else {
+#pragma unroll
+        for (int c = lane; c < kPiece; c += 32)
+          if (c < left)
+#pragma unroll 4
+            for (int row = 0; row < last; ++row)
+              *reinterpret_cast<uint16_t*>(dst + row * pitch + c * 2) =
+                  ld_shared_u16(staging + swizzled(row, c / 8) + c % 8 * 2);
       }
     }
     if (kVec && lane == 0) bulk_commit();  // also of nothing: the wait counts pieces
@@ -937,7 +963,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc[16 + i] = fma2(make_float2(__uint_as_float(r1[2 * i]), __uint_as_float(r1[2 * i + 1])), f2, acc[16 + i]);
       }
       if (!ok) break;
-      store_tile<64, 1, 0, kFp32, kVec>(a, &tm_out, staging, m0, t.tok_end, t.row_block * kTileCol + part * kCols, lane, acc);
+      store_tile<64, 1, 0, kFp32, kVec>(a, &tm_out, staging, m0, t.tok_end, t.row_block * kTileCol + part * kCols, lane,
+                                        acc);
     }
     if (kVec && lane == 0) bulk_wait();
   }
