@@ -549,6 +549,28 @@ int mla_grouped_gemm_fp8(const void* a, int64_t lda, const float* a_scales, int6
                          int64_t ldw, const float* w_scales, const int32_t* expert_offsets, int num_experts,
                          int num_tokens, int n, int k, void* out, int out_dtype, int64_t ldo, void* stream);
 
+/*
+ * Either product in a form of the caller's choice instead of the one the
+ * library estimates to be the fastest; for tests and tools, which cannot rely
+ * on an estimate to reach every form.  expert_offsets NULL (with num_experts 1)
+ * = mla_gemm_fp8, else mla_grouped_gemm_fp8.
+ *
+ *   tile_tokens   tokens of a tile: 16, 32, 64 (times 128 weight rows), 128 (times
+ *                 128), 256 (times 256, on a pair of CTAs).
+ *   k_parts       CTAs that share the k of a tile: 1; or 2, 4, 8 with up to 64
+ *                 tokens and at least two 128-wide blocks of k for each.
+ *   give_up_warp  -1.  Else, with up to 64 tokens, the warp 0 .. 7 (0 .. 3 with
+ *                 16 tokens) of the first CTA's epilogue that behaves as if its
+ *                 first wait had timed out: the call's results are not valid, the
+ *                 kernel ends within a few seconds and the error word reads 0x718
+ *                 or the code of a wait that timed out because of it.
+ * Errors: as the products.
+ */
+int mla_gemm_fp8_in_form(const void* a, int64_t lda, const float* a_scales, int64_t a_scale_stride, const void* w,
+                         int64_t ldw, const float* w_scales, const int32_t* expert_offsets, int num_experts,
+                         int num_tokens, int n, int k, void* out, int out_dtype, int64_t ldo, int tile_tokens,
+                         int k_parts, int give_up_warp, void* stream);
+
 /* ---- plan inspection (host only; used by tests and tools) ---- */
 
 /* Device workspace bytes the plan needs. */

@@ -45,7 +45,8 @@ cudaError_t launch_act_quantize(const void* x, int64_t x_stride, int num_tokens,
                                 cudaStream_t stream);
 cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda, int64_t a_scale_stride, const void* w,
                             const float* w_scales, int64_t ldw, const int32_t* offsets, int m, int n, int k,
-                            int experts, void* out, bool fp32, int64_t ldo, int sms, cudaStream_t stream);
+                            int experts, void* out, bool fp32, int64_t ldo, const GemmForm* form, int sms,
+                            cudaStream_t stream);
 cudaError_t gemm_read_error(int* code, bool reset);
 }  // namespace mla
 
@@ -595,10 +596,12 @@ int mla_act_quantize(const void* x, int64_t x_stride, int act, int num_tokens, i
   return ok();
 }
 
-// Both products; expert_offsets == nullptr: the dense one.
+// Both products; expert_offsets == nullptr: the dense one.  form: nullptr = the
+// library's choice.
 static int gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a_scale_stride, const void* w,
                     int64_t ldw, const float* w_scales, const int32_t* expert_offsets, int num_experts,
-                    int num_tokens, int n, int k, void* out, int out_dtype, int64_t ldo, void* stream) {
+                    int num_tokens, int n, int k, void* out, int out_dtype, int64_t ldo, const mla::GemmForm* form,
+                    void* stream) {
   if (num_tokens < 0) return fail(MLA_ERR_ARG, "num_tokens must be >= 0");
   if (n < 1) return fail(MLA_ERR_ARG, "n must be >= 1");
   if (k < 16 || k % 16 != 0) return fail(MLA_ERR_ARG, "k must be a positive multiple of 16");
@@ -626,7 +629,7 @@ static int gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a
   int rc = check_device(&sms);
   if (rc != MLA_OK) return rc;
   cudaError_t e = mla::launch_gemm_fp8(a, a_scales, lda, a_scale_stride, w, w_scales, ldw, expert_offsets, num_tokens,
-                                       n, k, num_experts, out, out_dtype == MLA_OUT_FP32, ldo, sms,
+                                       n, k, num_experts, out, out_dtype == MLA_OUT_FP32, ldo, form, sms,
                                        static_cast<cudaStream_t>(stream));
   if (e == cudaErrorNotSupported)
     return fail(MLA_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled unavailable or rejected the operands");
@@ -638,7 +641,7 @@ int mla_gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a_sc
                  int64_t ldw, const float* w_scales, int num_tokens, int n, int k, void* out, int out_dtype,
                  int64_t ldo, void* stream) {
   return gemm_fp8(a, lda, a_scales, a_scale_stride, w, ldw, w_scales, nullptr, 1, num_tokens, n, k, out, out_dtype,
-                  ldo, stream);
+                  ldo, nullptr, stream);
 }
 
 int mla_grouped_gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a_scale_stride, const void* w,
@@ -646,7 +649,28 @@ int mla_grouped_gemm_fp8(const void* a, int64_t lda, const float* a_scales, int6
                          int num_tokens, int n, int k, void* out, int out_dtype, int64_t ldo, void* stream) {
   if (!expert_offsets) return fail(MLA_ERR_ARG, "expert_offsets is NULL");
   return gemm_fp8(a, lda, a_scales, a_scale_stride, w, ldw, w_scales, expert_offsets, num_experts, num_tokens, n, k,
-                  out, out_dtype, ldo, stream);
+                  out, out_dtype, ldo, nullptr, stream);
+}
+
+int mla_gemm_fp8_in_form(const void* a, int64_t lda, const float* a_scales, int64_t a_scale_stride, const void* w,
+                         int64_t ldw, const float* w_scales, const int32_t* expert_offsets, int num_experts,
+                         int num_tokens, int n, int k, void* out, int out_dtype, int64_t ldo, int tile_tokens,
+                         int k_parts, int give_up_warp, void* stream) {
+  const bool swapped = tile_tokens == 16 || tile_tokens == 32 || tile_tokens == 64;
+  if (!swapped && tile_tokens != 128 && tile_tokens != 256)
+    return fail(MLA_ERR_ARG, "tile_tokens must be 16, 32, 64, 128 or 256");
+  if (k_parts != 1 && (!swapped || (k_parts != 2 && k_parts != 4 && k_parts != 8)))
+    return fail(MLA_ERR_ARG, "k_parts must be 1, or with tiles of up to 64 tokens 2, 4 or 8");
+  if (k_parts > 1 && ((int64_t)k + 127) / 128 < 2 * k_parts)
+    return fail(MLA_ERR_ARG, "every part of k must have two blocks of 128");
+  if (give_up_warp < -1 || give_up_warp >= (swapped ? (tile_tokens == 16 ? 4 : 8) : 0))
+    return fail(MLA_ERR_ARG, "give_up_warp must be -1, or an epilogue warp of a tile of up to 64 tokens");
+  if (!expert_offsets && num_experts != 1) return fail(MLA_ERR_ARG, "expert_offsets is NULL");
+  if (((int64_t)num_tokens / tile_tokens + num_experts) * (((int64_t)n + 127) / 128) > INT32_MAX / k_parts)
+    return fail(MLA_ERR_ARG, "too many tiles for one launch");
+  const mla::GemmForm form{tile_tokens, k_parts, give_up_warp};
+  return gemm_fp8(a, lda, a_scales, a_scale_stride, w, ldw, w_scales, expert_offsets, num_experts, num_tokens, n, k,
+                  out, out_dtype, ldo, &form, stream);
 }
 
 int mla_decode_version(void) { return 100; }

@@ -50,6 +50,7 @@ struct Args {
   int m, n, k_blocks, row_blocks, experts;  // row_blocks: tiles along the weight rows
   int scale_rows;  // 128-row blocks of the weights' scales
   int splits;  // CTAs that share a tile's k blocks (a cluster); 1: none
+  int give_up; // epilogue warp of CTA 0 that gives up at once (tests of the swapped form); -1: none
 };
 
 template <int TN, bool kSplit>
@@ -575,12 +576,18 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
     Ring<C::kScaleStages> ring;
     Ring<C::kBufs> buf;
     bool ok = true;
-    for (int idx = first; ok && idx < tiles; idx += step) {
+    if (blockIdx.x == 0 && warp - 2 == a.give_up) {
+      flag_store(abort_flag, 1);
+      atomicCAS(&g_gemm_error, 0, 0x718);
+      ok = false;
+    }
+    // a warp that has given up still goes through a split tile (there is one)
+    for (int idx = first; (ok || kSplit) && idx < tiles; idx += step) {
       const Tile t = find_tile<TN>(a, prefix, idx);
       float2 acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      for (int kb = kb0; kb < kb1; ++kb, ring.next(), buf.next()) {
+      for (int kb = kb0; ok && kb < kb1; ++kb, ring.next(), buf.next()) {
         const uint32_t s = ring.slot, b = buf.slot;
         if (!wait_bar_warp(abort_flag, bars.sfull(s), ring.phase, 0x715) ||
             !wait_bar_warp(abort_flag, bars.tfull(b), buf.phase, 0x716)) {
@@ -612,25 +619,32 @@ __global__ void __launch_bounds__(Cfg<TN, kSplit>::kThreads, Cfg<TN, kSplit>::kC
           mbar_arrive(bars.sempty(s));
         }
       }
-      if (!ok) break;
+      if (!kSplit && !ok) break;
       const int n = t.row_block * kTileRows + row;
       if (kSplit) {
         // tokens [p * slice, (p + 1) * slice) go to CTA p of the cluster: staged
         // as [token][row] in the ring (idle: the tile's last product has been
         // read) and moved by the copy engine, one contiguous piece per CTA
         const int slice = TN / splits;
-        float* stage = reinterpret_cast<float*>(smem) + col0 * kTileRows + row;
+        if (ok) {
+          float* stage = reinterpret_cast<float*>(smem) + col0 * kTileRows + row;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) stage[i * kTileRows] = (i & 1) ? acc[i / 2].y : acc[i / 2].x;
-        fence_proxy_async_smem();
+          for (int i = 0; i < kCols; ++i) stage[i * kTileRows] = (i & 1) ? acc[i / 2].y : acc[i / 2].x;
+          fence_proxy_async_smem();
+        }
         __syncwarp();
+        // The barrier has no time limit: every epilogue warp comes here once,
+        // whether its waits succeeded or not, and every CTA sends its pieces, so
+        // that no peer waits for one in vain (what they hold after a wait that
+        // timed out is of no use, which the error word says).
         named_bar_sync(1, 32 * C::kEpiWarps);
         if (warp == 2 && lane < splits) {
           const uint32_t bytes = (uint32_t)slice * kTileRows * 4;
           bulk_copy_cluster(mapa(sbase + C::kOffRecv + rank * bytes, lane), sbase + lane * bytes, bytes,
                             mapa(bars.recv(), lane));
         }
-        if (!wait_bar_warp<true>(abort_flag, bars.recv(), 0, 0x717)) {
+        if (!ok || !wait_bar_warp<true>(abort_flag, bars.recv(), 0, 0x717)) {
+          wait_limited(bars.recv(), 0);  // the peers' pieces land before the CTA leaves
           ok = false;
           break;
         }
@@ -1538,13 +1552,12 @@ static cudaError_t consider(const Args& a, int sms, Cost c, double weights, Choi
 }
 
 template <bool kFp32>
-static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, const Args& a,
-                              int sms, cudaStream_t stream) {
-  Choice c;
+static cudaError_t choose(const Args& a, int sms, Choice* choice) {
+  Choice& c = *choice;
   const double weights = (double)std::min(a.experts, a.m) * a.n * a.k_blocks * kBlockK / 6.3e6;
-  cudaError_t e = consider<16, kFp32>(a, sms, {0.244, 0.178, 0.5, 2.5, 1.2}, weights, &c);
-  if (e == cudaSuccess && a.m > 16) e = consider<32, kFp32>(a, sms, {0.276, 0.191, 0.8, 2.4, 1.8}, weights, &c);
-  if (e == cudaSuccess && a.m > 32) e = consider<64, kFp32>(a, sms, {0.395, 0.285, 1.4, 2.7, 2.2}, weights, &c);
+  cudaError_t e = consider<16, kFp32>(a, sms, {0.244, 0.178, 0.5, 2.5, 1.2}, weights, choice);
+  if (e == cudaSuccess && a.m > 16) e = consider<32, kFp32>(a, sms, {0.276, 0.191, 0.8, 2.4, 1.8}, weights, choice);
+  if (e == cudaSuccess && a.m > 32) e = consider<64, kFp32>(a, sms, {0.395, 0.285, 1.4, 2.7, 2.2}, weights, choice);
   if (e != cudaSuccess) return e;
   if (a.m > 64) {
     const int64_t rounds = (expected_tiles(a, square::kTileTok, a.row_blocks) + sms - 1) / sms;
@@ -1554,6 +1567,20 @@ static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64
     const int64_t row_tiles = (a.n + paired::kTileCol - 1) / paired::kTileCol;
     const int64_t rounds = (expected_tiles(a, paired::kTileTok, row_tiles) + sms / 2 - 1) / (sms / 2);
     c.offer(std::max(rounds * (a.k_blocks * 0.45 + 1.0), weights) + 3.3, kPaired, 1);
+  }
+  return cudaSuccess;
+}
+
+template <bool kFp32>
+static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, const Args& a,
+                              const GemmForm* form, int sms, cudaStream_t stream) {
+  Choice c;
+  if (form) {
+    c.shape = form->tile_tokens;
+    c.splits = form->k_parts;
+  } else {
+    const cudaError_t e = choose<kFp32>(a, sms, &c);
+    if (e != cudaSuccess) return e;
   }
   const bool vec = a.ldo % (kFp32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
   switch (c.shape) {
@@ -1571,10 +1598,12 @@ static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64
 }  // namespace gemm8
 
 // Arguments are checked by the caller; cudaErrorNotSupported: the tensor-map
-// encoder is unavailable or rejected the operands.
+// encoder is unavailable or rejected the operands.  form: nullptr = the one
+// with the least estimated time.
 cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda, int64_t a_scale_stride, const void* w,
                             const float* w_scales, int64_t ldw, const int32_t* offsets, int m, int n, int k,
-                            int experts, void* out, bool fp32, int64_t ldo, int sms, cudaStream_t stream) {
+                            int experts, void* out, bool fp32, int64_t ldo, const GemmForm* form, int sms,
+                            cudaStream_t stream) {
   gemm8::Args a;
   a.a_scales = a_scales;
   a.w_scales = w_scales;
@@ -1589,8 +1618,9 @@ cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda,
   a.scale_rows = a.row_blocks;
   a.experts = experts;
   a.splits = 1;
-  return fp32 ? gemm8::launch_out<true>(act, lda, w, ldw, k, a, sms, stream)
-              : gemm8::launch_out<false>(act, lda, w, ldw, k, a, sms, stream);
+  a.give_up = form ? form->give_up_warp : -1;
+  return fp32 ? gemm8::launch_out<true>(act, lda, w, ldw, k, a, form, sms, stream)
+              : gemm8::launch_out<false>(act, lda, w, ldw, k, a, form, sms, stream);
 }
 
 cudaError_t gemm_read_error(int* code, bool reset) {

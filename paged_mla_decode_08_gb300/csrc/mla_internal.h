@@ -94,6 +94,13 @@ struct DecodeArgs {
   int32_t q_e4m3;          // q_nope is the merged e4m3 query [T, H, 576] (q_pe unused)
 };
 
+// A form of the FP8 products that a caller asked for (mla_gemm_fp8_in_form).
+struct GemmForm {
+  int tile_tokens;   // 16, 32, 64: swapped; 128: square; 256: paired
+  int k_parts;       // CTAs that share a swapped tile's k blocks
+  int give_up_warp;  // epilogue warp that gives up, -1: none
+};
+
 #ifdef __CUDACC__
 // First query token and query-token count of request b: (b * q_len, q_len)
 // for a uniform batch; (cu_q[b], cu_q[b+1] - cu_q[b]) for a ragged one.  A

@@ -1,0 +1,62 @@
+"""The forms of the FP8 products, one by one, against the float64 definition.
+
+Operands are small integers and scales powers of two, so every sum is exact in
+fp32 and the result has to equal the rounded exact value, bit for bit."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8_layer_ref as L
+from paged_mla_decode_08_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def no_device_error():
+    B.mla_decode_device_error(reset=True)
+    yield
+    assert B.mla_decode_device_error(reset=True) == 0
+
+
+def operands(rng, t, n, k, experts=1):
+    """(a, sa, w, sw): codes -2 .. 2, scales 1/2, 1, 2."""
+    g = L.blocks(k)
+    dev = lambda v, kind: torch.from_numpy(v.astype(np.float32)).cuda().to(kind)  # noqa: E731
+    return (dev(rng.integers(-2, 3, (t, k)), torch.float8_e4m3fn), dev(2.0 ** rng.integers(-1, 2, (g, t)), torch.float32),
+            dev(rng.integers(-2, 3, (experts, n, k)), torch.float8_e4m3fn),
+            dev(2.0 ** rng.integers(-1, 2, (experts, L.blocks(n), g)), torch.float32))
+
+
+def exact(a, sa, w, sw):
+    """The product of one expert in float64 (exact here)."""
+    n, k = w.shape
+    a = a.double() * sa.double().t().repeat_interleave(128, 1)[:, :k]
+    w = w.double() * sw.double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    return a @ w.t()
+
+
+def in_form(a, sa, w, sw, off, out, tile, parts, give_up=-1):
+    """mla_gemm_fp8_in_form on contiguous operands and an `out` with contiguous columns."""
+    rc = B.load().mla_gemm_fp8_in_form(
+        a.data_ptr(), a.stride(0), sa.data_ptr(), sa.stride(0), w.data_ptr(), w.stride(-2), sw.data_ptr(),
+        None if off is None else off.data_ptr(), w.shape[0], a.shape[0], w.shape[1], a.shape[1], out.data_ptr(),
+        B.MLA_OUT_BF16 if out.dtype == torch.bfloat16 else B.MLA_OUT_FP32, out.stride(0), tile, parts, give_up,
+        torch.cuda.current_stream().cuda_stream)
+    assert rc == B.MLA_OK, B.load().mla_decode_last_error_string()
+
+
+@pytest.mark.parametrize("tile,parts,k,warp", [(16, 8, 2048, 0), (16, 8, 2048, 3), (16, 2, 4096, 1), (32, 4, 1024, 5),
+                                               (64, 8, 4096, 7), (64, 2, 512, 4), (16, 1, 1024, 2), (64, 1, 2048, 6)])
+def test_a_warp_that_gives_up_ends_the_kernel(tile, parts, k, warp):
+    """One epilogue warp of one CTA gives up while all others go on: the kernel
+    ends, says so, and the next call is right."""
+    t, n = min(tile, 40), 300
+    a, sa, w, sw = operands(np.random.default_rng(k + warp), t, n, k)
+    out = torch.empty(t, n, device="cuda")
+    in_form(a, sa, w, sw, None, out, tile, parts, warp)
+    assert B.mla_decode_device_error(reset=True) == 0x718
+    in_form(a, sa, w, sw, None, out, tile, parts)
+    assert B.mla_decode_device_error() == 0
+    assert torch.equal(out, exact(a, sa, w[0], sw[0]).float())
