@@ -514,7 +514,8 @@ int mla_act_quantize(const void* x, int64_t x_stride, int act, int num_tokens, i
  *   w             device e4m3 [n, k], row stride ldw; w_scales device fp32
  *                 [ceil(n / 128)][ceil(k / 128)], contiguous: one scale for
  *                 each 128 x 128 block.
- *   n, k          n >= 1; k >= 16 and a multiple of 16, as are lda and ldw; a
+ *   num_tokens    at most 2^31 - 256.
+ *   n, k          1 <= n <= 2^31 - 256; k >= 16 and a multiple of 16, as are lda and ldw; a
  *                 and w 16-byte aligned (the copy engine's rules).
  *   out           device bf16 (MLA_OUT_BF16) or fp32 (MLA_OUT_FP32)
  *                 [num_tokens, n], row stride ldo.
@@ -542,7 +543,7 @@ int mla_gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a_sc
  *                 nothing; rows that no expert owns are not written.  An entry
  *                 that breaks the rule gives its expert no row and the error
  *                 word of mla_decode_device_error reads 0x701.
- *   num_experts   1 .. MLA_GEMM_MAX_EXPERTS, num_experts * n < 2^31.
+ *   num_experts   1 .. MLA_GEMM_MAX_EXPERTS, num_experts * n <= 2^31 - 256.
  *   the rest      as for mla_gemm_fp8.
  */
 int mla_grouped_gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a_scale_stride, const void* w,

@@ -607,7 +607,9 @@ static int gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a
   if (k < 16 || k % 16 != 0) return fail(MLA_ERR_ARG, "k must be a positive multiple of 16");
   if (num_experts < 1 || num_experts > MLA_GEMM_MAX_EXPERTS)
     return fail(MLA_ERR_ARG, "num_experts must be in [1, MLA_GEMM_MAX_EXPERTS]");
-  if ((int64_t)num_experts * n > INT32_MAX) return fail(MLA_ERR_ARG, "num_experts * n must be < 2^31");
+  // rows are numbered in 32 bits, to the end of a tile that begins with the last one
+  if (num_tokens > INT32_MAX - 255) return fail(MLA_ERR_ARG, "num_tokens must be <= 2^31 - 256");
+  if ((int64_t)num_experts * n > INT32_MAX - 255) return fail(MLA_ERR_ARG, "num_experts * n must be <= 2^31 - 256");
   if (num_tokens == 0) return ok();
   if (!a || !a_scales || !w || !w_scales || !out) return fail(MLA_ERR_ARG, "a required device pointer is NULL");
   if (lda < k || lda % 16 != 0 || ldw < k || ldw % 16 != 0)

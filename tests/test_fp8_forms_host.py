@@ -28,6 +28,31 @@ def test_in_form_rejects(over):
     assert B.load().mla_decode_last_error_string()
 
 
+MOST = 2 ** 31 - 256  # rows are numbered in 32 bits, to the end of a tile of 256 that begins with the last one
+
+
+@pytest.mark.parametrize("over,fits", [
+    (dict(t=MOST, ss=MOST), True), (dict(t=MOST + 1, ss=MOST + 1), False), (dict(t=2 ** 31 - 1, ss=2 ** 31 - 1), False),
+    (dict(n=MOST, ldo=MOST, t=1), True), (dict(n=MOST + 1, ldo=MOST + 1, t=1), False),
+    (dict(e=8, n=MOST // 8), True), (dict(e=8, n=MOST // 8 + 1), False), (dict(e=1023, n=2 ** 31 // 1023), False),
+])
+def test_rows_that_32_bits_number(over, fits):
+    """Tiles of an expert may begin at any row: the last one's end, past the
+    rows, still has to be a positive 32-bit number."""
+    lib = B.load()
+    kw = dict(a=FAKE, lda=16, sa=FAKE, ss=4, w=FAKE, ldw=16, sw=FAKE, off=FAKE, e=1, t=4, n=8, k=16, out=FAKE,
+              od=B.MLA_OUT_FP32, ldo=1 << 32)
+    kw.update(over)
+    if fits and torch.cuda.is_available():
+        pytest.skip("valid arguments on fake pointers would launch on a GPU")
+    dense = {k: v for k, v in kw.items() if k not in ("off", "e")}
+    calls = [lib.mla_grouped_gemm_fp8(*kw.values(), None)]
+    if kw["e"] == 1:
+        calls.append(lib.mla_gemm_fp8(*dense.values(), None))
+    for rc in calls:
+        assert (rc in (B.MLA_ERR_CUDA, B.MLA_ERR_UNSUPPORTED)) if fits else rc == B.MLA_ERR_ARG
+
+
 def test_in_form_valid_arguments_reach_the_device_check():
     if torch.cuda.is_available():
         pytest.skip("valid arguments on fake pointers would launch on a GPU")
