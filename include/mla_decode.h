@@ -572,6 +572,20 @@ int mla_gemm_fp8_in_form(const void* a, int64_t lda, const float* a_scales, int6
                          int num_tokens, int n, int k, void* out, int out_dtype, int64_t ldo, int tile_tokens,
                          int k_parts, int give_up_warp, void* stream);
 
+/*
+ * The form that the products choose for a call of these sizes (host only, nothing
+ * is launched; used by tests and tools): tile_tokens and k_parts as above, and
+ * whether the copy engine stores the results (copied_results; tiles of 128 and 256
+ * tokens whose out and ldo are multiples of 16 bytes and whose rows have fewer than
+ * 2^31 bytes).  grouped != 0: mla_grouped_gemm_fp8.  num_sms 0 and clusters NULL:
+ * for the current device; else for one of num_sms SMs that runs clusters[0], [1], [2]
+ * clusters of 2, 4, 8 CTAs at once, two CTAs to an SM.
+ * Errors: MLA_ERR_ARG, and for the current device MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
+ */
+int mla_gemm_fp8_form(int num_tokens, int n, int k, int num_experts, int grouped, int out_dtype, const void* out,
+                      int64_t ldo, int num_sms, const int32_t* clusters, int* tile_tokens, int* k_parts,
+                      int* copied_results);
+
 /* ---- plan inspection (host only; used by tests and tools) ---- */
 
 /* Device workspace bytes the plan needs. */

@@ -65,6 +65,7 @@ SIGNATURES = {
                                       _c_int, _i64, _vp]),
     "mla_gemm_fp8_in_form": (_c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp,
                                       _c_int, _i64, _c_int, _c_int, _c_int, _vp]),
+    "mla_gemm_fp8_form": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _i64, _c_int, _vp, _vp, _vp, _vp]),
     "mla_plan_workspace_bytes": (_c_size, [_vp]),
     "mla_plan_num_workers": (_c_int, [_vp]),
     "mla_plan_num_segments": (_c_int, [_vp]),

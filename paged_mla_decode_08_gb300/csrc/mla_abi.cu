@@ -47,6 +47,8 @@ cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda,
                             const float* w_scales, int64_t ldw, const int32_t* offsets, int m, int n, int k,
                             int experts, void* out, bool fp32, int64_t ldo, const GemmForm* form, int sms,
                             cudaStream_t stream);
+void gemm_fp8_form(bool grouped, int m, int n, int k, int experts, const void* out, bool fp32, int64_t ldo, int sms,
+                   const int32_t* clusters, int* tile_tokens, int* k_parts, int* copied);
 cudaError_t gemm_read_error(int* code, bool reset);
 }  // namespace mla
 
@@ -596,12 +598,8 @@ int mla_act_quantize(const void* x, int64_t x_stride, int act, int num_tokens, i
   return ok();
 }
 
-// Both products; expert_offsets == nullptr: the dense one.  form: nullptr = the
-// library's choice.
-static int gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a_scale_stride, const void* w,
-                    int64_t ldw, const float* w_scales, const int32_t* expert_offsets, int num_experts,
-                    int num_tokens, int n, int k, void* out, int out_dtype, int64_t ldo, const mla::GemmForm* form,
-                    void* stream) {
+// The sizes of both products.
+static int check_product_sizes(int num_tokens, int n, int k, int num_experts) {
   if (num_tokens < 0) return fail(MLA_ERR_ARG, "num_tokens must be >= 0");
   if (n < 1) return fail(MLA_ERR_ARG, "n must be >= 1");
   if (k < 16 || k % 16 != 0) return fail(MLA_ERR_ARG, "k must be a positive multiple of 16");
@@ -610,6 +608,17 @@ static int gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a
   // rows are numbered in 32 bits, to the end of a tile that begins with the last one
   if (num_tokens > INT32_MAX - 255) return fail(MLA_ERR_ARG, "num_tokens must be <= 2^31 - 256");
   if ((int64_t)num_experts * n > INT32_MAX - 255) return fail(MLA_ERR_ARG, "num_experts * n must be <= 2^31 - 256");
+  return MLA_OK;
+}
+
+// Both products; expert_offsets == nullptr: the dense one.  form: nullptr = the
+// library's choice.
+static int gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a_scale_stride, const void* w,
+                    int64_t ldw, const float* w_scales, const int32_t* expert_offsets, int num_experts,
+                    int num_tokens, int n, int k, void* out, int out_dtype, int64_t ldo, const mla::GemmForm* form,
+                    void* stream) {
+  int rc = check_product_sizes(num_tokens, n, k, num_experts);
+  if (rc != MLA_OK) return rc;
   if (num_tokens == 0) return ok();
   if (!a || !a_scales || !w || !w_scales || !out) return fail(MLA_ERR_ARG, "a required device pointer is NULL");
   if (lda < k || lda % 16 != 0 || ldw < k || ldw % 16 != 0)
@@ -628,7 +637,7 @@ static int gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a
   if (((int64_t)num_tokens / 16 + num_experts) * (((int64_t)n + 127) / 128) > INT32_MAX / 2)
     return fail(MLA_ERR_ARG, "too many tiles for one launch");
   int sms = 0;
-  int rc = check_device(&sms);
+  rc = check_device(&sms);
   if (rc != MLA_OK) return rc;
   cudaError_t e = mla::launch_gemm_fp8(a, a_scales, lda, a_scale_stride, w, w_scales, ldw, expert_offsets, num_tokens,
                                        n, k, num_experts, out, out_dtype == MLA_OUT_FP32, ldo, form, sms,
@@ -673,6 +682,28 @@ int mla_gemm_fp8_in_form(const void* a, int64_t lda, const float* a_scales, int6
   const mla::GemmForm form{tile_tokens, k_parts, give_up_warp};
   return gemm_fp8(a, lda, a_scales, a_scale_stride, w, ldw, w_scales, expert_offsets, num_experts, num_tokens, n, k,
                   out, out_dtype, ldo, &form, stream);
+}
+
+int mla_gemm_fp8_form(int num_tokens, int n, int k, int num_experts, int grouped, int out_dtype, const void* out,
+                      int64_t ldo, int num_sms, const int32_t* clusters, int* tile_tokens, int* k_parts,
+                      int* copied_results) {
+  if (!tile_tokens || !k_parts || !copied_results) return fail(MLA_ERR_ARG, "a result pointer is NULL");
+  int rc = check_product_sizes(num_tokens, n, k, num_experts);
+  if (rc != MLA_OK) return rc;
+  if (num_tokens < 1) return fail(MLA_ERR_ARG, "num_tokens must be >= 1");
+  if (!grouped && num_experts != 1) return fail(MLA_ERR_ARG, "a dense product has one expert");
+  if (ldo < n) return fail(MLA_ERR_ARG, "ldo must be >= n");
+  if (out_dtype != MLA_OUT_BF16 && out_dtype != MLA_OUT_FP32)
+    return fail(MLA_ERR_ARG, "out_dtype must be MLA_OUT_BF16 or MLA_OUT_FP32");
+  if (num_sms < 0 || (num_sms > 0) != (clusters != nullptr))
+    return fail(MLA_ERR_ARG, "num_sms > 0 and clusters go together");
+  if (num_sms == 0) {
+    rc = check_device(&num_sms);
+    if (rc != MLA_OK) return rc;
+  }
+  mla::gemm_fp8_form(grouped != 0, num_tokens, n, k, num_experts, out, out_dtype == MLA_OUT_FP32, ldo, num_sms, clusters,
+                     tile_tokens, k_parts, copied_results);
+  return ok();
 }
 
 int mla_decode_version(void) { return 100; }

@@ -1532,33 +1532,30 @@ static int64_t expected_tiles(const Args& a, int tokens, int64_t row_tiles) {
   return std::max<int64_t>(1, (int64_t)(tok_tiles * row_tiles));
 }
 
+// `clusters`: how many clusters of 2, 4 and 8 CTAs run at once (nullptr: asked of the device).
 template <int TN, bool kFp32>
-static cudaError_t consider(const Args& a, int sms, Cost c, double weights, Choice* choice) {
+static void consider(const Args& a, int sms, const int32_t* clusters, Cost c, double weights, Choice* choice) {
   constexpr int kPerSm = Cfg<TN, true>::kCtasPerSm;
   const int64_t tiles = expected_tiles(a, TN, a.row_blocks), most = most_token_tiles(a, TN) * a.row_blocks;
-  for (int s = 1; s <= 8; s *= 2) {
+  for (int i = 0, s = 1; s <= 8; ++i, s *= 2) {
     if (s > 1) {
       // every cluster runs at once, and a CTA keeps two blocks
       if (a.k_blocks < 2 * s || most * s > (int64_t)sms * kPerSm) break;
-      const cudaError_t e = Form<TN, true, kFp32>::set_attributes();
-      if (e != cudaSuccess) return e;
-      if (most > Form<TN, true, kFp32>::active_clusters(s)) break;
+      if (most > (clusters ? clusters[i - 1] : Form<TN, true, kFp32>::active_clusters(s))) break;
     }
     const int64_t on_sm = (tiles * s + sms - 1) / sms;  // CTAs of an SM, at once or one after the other
     const double chain = on_sm * (((a.k_blocks + s - 1) / s) * (on_sm == 1 ? c.alone : c.shared) + c.tile);
     choice->offer(std::max(chain, weights) + c.fixed + (s > 1 ? c.exchange : 0.0), TN, s);
   }
-  return cudaSuccess;
 }
 
 template <bool kFp32>
-static cudaError_t choose(const Args& a, int sms, Choice* choice) {
-  Choice& c = *choice;
+static Choice choose(const Args& a, int sms, const int32_t* clusters) {
+  Choice c;
   const double weights = (double)std::min(a.experts, a.m) * a.n * a.k_blocks * kBlockK / 6.3e6;
-  cudaError_t e = consider<16, kFp32>(a, sms, {0.244, 0.178, 0.5, 2.5, 1.2}, weights, choice);
-  if (e == cudaSuccess && a.m > 16) e = consider<32, kFp32>(a, sms, {0.276, 0.191, 0.8, 2.4, 1.8}, weights, choice);
-  if (e == cudaSuccess && a.m > 32) e = consider<64, kFp32>(a, sms, {0.395, 0.285, 1.4, 2.7, 2.2}, weights, choice);
-  if (e != cudaSuccess) return e;
+  consider<16, kFp32>(a, sms, clusters, {0.244, 0.178, 0.5, 2.5, 1.2}, weights, &c);
+  if (a.m > 16) consider<32, kFp32>(a, sms, clusters, {0.276, 0.191, 0.8, 2.4, 1.8}, weights, &c);
+  if (a.m > 32) consider<64, kFp32>(a, sms, clusters, {0.395, 0.285, 1.4, 2.7, 2.2}, weights, &c);
   if (a.m > 64) {
     const int64_t rounds = (expected_tiles(a, square::kTileTok, a.row_blocks) + sms - 1) / sms;
     c.offer(std::max(rounds * (a.k_blocks * 0.253 + 1.4), weights) + 2.6, kSquare, 1);
@@ -1568,7 +1565,16 @@ static cudaError_t choose(const Args& a, int sms, Choice* choice) {
     const int64_t rounds = (expected_tiles(a, paired::kTileTok, row_tiles) + sms / 2 - 1) / (sms / 2);
     c.offer(std::max(rounds * (a.k_blocks * 0.45 + 1.0), weights) + 3.3, kPaired, 1);
   }
-  return cudaSuccess;
+  return c;
+}
+
+// Whether the copy engine can store the results: 16-byte rows, a row pitch of
+// fewer than 40 bits, and byte offsets within a row that its 32-bit coordinates hold.
+template <bool kFp32>
+static bool copied_results(const Args& a) {
+  constexpr int64_t kElt = kFp32 ? 4 : 2;
+  return a.ldo < (INT64_C(1) << 40) / kElt && a.ldo * kElt % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
+         a.n * kElt <= INT32_MAX;
 }
 
 template <bool kFp32>
@@ -1579,10 +1585,9 @@ static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64
     c.shape = form->tile_tokens;
     c.splits = form->k_parts;
   } else {
-    const cudaError_t e = choose<kFp32>(a, sms, &c);
-    if (e != cudaSuccess) return e;
+    c = choose<kFp32>(a, sms, nullptr);
   }
-  const bool vec = a.ldo % (kFp32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+  const bool vec = copied_results<kFp32>(a);
   switch (c.shape) {
     case kSwapped16: return launch_tn<16, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
     case kSwapped32: return launch_tn<32, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
@@ -1597,13 +1602,8 @@ static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64
 
 }  // namespace gemm8
 
-// Arguments are checked by the caller; cudaErrorNotSupported: the tensor-map
-// encoder is unavailable or rejected the operands.  form: nullptr = the one
-// with the least estimated time.
-cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda, int64_t a_scale_stride, const void* w,
-                            const float* w_scales, int64_t ldw, const int32_t* offsets, int m, int n, int k,
-                            int experts, void* out, bool fp32, int64_t ldo, const GemmForm* form, int sms,
-                            cudaStream_t stream) {
+static gemm8::Args gemm_args(const float* a_scales, int64_t a_scale_stride, const float* w_scales, const int32_t* offsets,
+                             int m, int n, int k, int experts, void* out, int64_t ldo) {
   gemm8::Args a;
   a.a_scales = a_scales;
   a.w_scales = w_scales;
@@ -1618,7 +1618,32 @@ cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda,
   a.scale_rows = a.row_blocks;
   a.experts = experts;
   a.splits = 1;
-  a.give_up = form ? form->give_up_warp : -1;
+  a.give_up = -1;
+  return a;
+}
+
+// The form that launch_gemm_fp8 chooses (`grouped`: offsets are given), and
+// whether the copy engine stores its results.
+void gemm_fp8_form(bool grouped, int m, int n, int k, int experts, const void* out, bool fp32, int64_t ldo, int sms,
+                   const int32_t* clusters, int* tile_tokens, int* k_parts, int* copied) {
+  static const int32_t some = 0;  // not read
+  const gemm8::Args a =
+      gemm_args(nullptr, 0, nullptr, grouped ? &some : nullptr, m, n, k, experts, const_cast<void*>(out), ldo);
+  const gemm8::Choice c = fp32 ? gemm8::choose<true>(a, sms, clusters) : gemm8::choose<false>(a, sms, clusters);
+  *tile_tokens = c.shape;
+  *k_parts = c.splits;
+  *copied = c.shape >= gemm8::kSquare && (fp32 ? gemm8::copied_results<true>(a) : gemm8::copied_results<false>(a));
+}
+
+// Arguments are checked by the caller; cudaErrorNotSupported: the tensor-map
+// encoder is unavailable or rejected the operands.  form: nullptr = the one
+// with the least estimated time.
+cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda, int64_t a_scale_stride, const void* w,
+                            const float* w_scales, int64_t ldw, const int32_t* offsets, int m, int n, int k,
+                            int experts, void* out, bool fp32, int64_t ldo, const GemmForm* form, int sms,
+                            cudaStream_t stream) {
+  gemm8::Args a = gemm_args(a_scales, a_scale_stride, w_scales, offsets, m, n, k, experts, out, ldo);
+  if (form) a.give_up = form->give_up_warp;
   return fp32 ? gemm8::launch_out<true>(act, lda, w, ldw, k, a, form, sms, stream)
               : gemm8::launch_out<false>(act, lda, w, ldw, k, a, form, sms, stream);
 }

@@ -1,5 +1,7 @@
-"""Refusals of the call that makes an FP8 product in a given form, on the host
-(no GPU is touched by these tests)."""
+"""The FP8 products' forms on the host: refusals of the call that makes a product
+in a given form, and the choice among them (no GPU is touched by these tests)."""
+
+import ctypes
 
 import pytest
 import torch
@@ -51,6 +53,39 @@ def test_rows_that_32_bits_number(over, fits):
         calls.append(lib.mla_gemm_fp8(*dense.values(), None))
     for rc in calls:
         assert (rc in (B.MLA_ERR_CUDA, B.MLA_ERR_UNSUPPORTED)) if fits else rc == B.MLA_ERR_ARG
+
+
+def chosen(t, n, k, experts=1, grouped=False, od=B.MLA_OUT_BF16, out=FAKE, ldo=None, sms=152, clusters=(150, 72, 36)):
+    """(tile_tokens, k_parts, copied_results) on a device of 152 SMs, or an error code."""
+    res = [ctypes.c_int(-1) for _ in range(3)]
+    places = (ctypes.c_int32 * 3)(*clusters) if clusters else None
+    rc = B.load().mla_gemm_fp8_form(t, n, k, experts, int(grouped), od, out, n if ldo is None else ldo, sms,
+                                    ctypes.addressof(places) if places else None, *[ctypes.byref(r) for r in res])
+    return rc if rc else tuple(r.value for r in res)
+
+
+@pytest.mark.parametrize("args", [
+    dict(t=0), dict(t=-1), dict(n=0), dict(k=8), dict(k=24), dict(experts=0, grouped=True), dict(experts=2), dict(ldo=7),
+    dict(od=B.MLA_OUT_E4M3), dict(sms=-1), dict(sms=0), dict(clusters=None), dict(t=MOST + 1),
+])
+def test_form_rejects(args):
+    assert chosen(**{**dict(t=4, n=8, k=16), **args}) == B.MLA_ERR_ARG
+
+
+@pytest.mark.parametrize("od,elt", [(B.MLA_OUT_BF16, 2), (B.MLA_OUT_FP32, 4)])
+def test_results_that_the_copy_engine_can_address(od, elt):
+    """Its coordinates are 32-bit byte offsets within a row, its row pitch has 40
+    bits, and every row starts on 16 bytes: else the warps store the results."""
+    def copied(n, **kw):
+        form = chosen(8192, n, 512, od=od, **{**dict(ldo=-(-n // 8) * 8), **kw})
+        assert form[0] >= 128
+        return form[2]
+
+    assert copied(1000) == 1 and copied(1000, out=FAKE + 8) == 0 and copied(1000, ldo=1000 + 8 // elt) == 0
+    most = (2 ** 31 - 1) // elt
+    assert copied(most) == 1 and copied(most + 1) == 0 and copied(MOST) == 0
+    assert copied(1000, ldo=(1 << 40) // elt - 8) == 1 and copied(1000, ldo=(1 << 40) // elt) == 0
+    assert chosen(8, 1000, 512, od=od, ldo=1000)[2] == 0  # small tiles are stored by the warps
 
 
 def test_in_form_valid_arguments_reach_the_device_check():
