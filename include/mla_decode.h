@@ -540,9 +540,10 @@ int mla_gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a_sc
  *   expert_offsets  device int32 [num_experts + 1], nondecreasing, within
  *                 [0, num_tokens].  It is read on the device: no host copy of
  *                 the routing is needed.  An expert without rows costs
- *                 nothing; rows that no expert owns are not written.  An entry
- *                 that breaks the rule gives its expert no row and the error
- *                 word of mla_decode_device_error reads 0x701.
+ *                 nothing; rows that no expert owns are not written.  An expert
+ *                 whose range breaks the rule, by itself or by beginning before
+ *                 the end of an earlier expert's, has no row, and the error word
+ *                 of mla_decode_device_error reads 0x701.
  *   num_experts   1 .. MLA_GEMM_MAX_EXPERTS, num_experts * n <= 2^31 - 256.
  *   the rest      as for mla_gemm_fp8.
  */

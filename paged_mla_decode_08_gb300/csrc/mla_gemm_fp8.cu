@@ -367,29 +367,43 @@ __device__ __forceinline__ bool issue_in_turn(uint32_t abort_flag, const Bars& b
   return true;
 }
 
-// Rows [lo, hi) of expert e.  Offsets outside 0 <= lo <= hi <= m own no row
-// (recorded), so no access leaves the arrays.
+// Rows [lo, hi) of expert e, as the offsets say.
 __device__ __forceinline__ int2 expert_rows(const Args& a, int e) {
   if (a.offsets == nullptr) return make_int2(0, a.m);
-  const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
-  if (lo < 0 || hi < lo || hi > a.m) {
-    atomicCAS(&g_gemm_error, 0, 0x701);
-    return make_int2(0, 0);
-  }
-  return make_int2(lo, hi);
+  return make_int2(__ldg(a.offsets + e), __ldg(a.offsets + e + 1));
 }
 
-// prefix[e] = token tiles of the experts before e, by one warp
+// prefix[e] = token tiles of the experts before e, by one warp.  An expert whose
+// range is not 0 <= lo <= hi <= m, or begins before the end of an earlier one,
+// owns no row (recorded): no access leaves the arrays, no row has two owners, and
+// there are no more tiles than most_token_tiles on the host.
 template <int TN>
 __device__ __forceinline__ void scan_experts(const Args& a, int* prefix, int lane) {
-  int run = 0;
+  int run = 0, end = 0;  // tiles, and the last row of a range, so far
   for (int e0 = 0; e0 < a.experts; e0 += 32) {
     const int e = e0 + lane;
-    int c = 0;
-    if (e < a.experts) {
-      const int2 r = expert_rows(a, e);
-      c = (int)(((int64_t)r.y - r.x + TN - 1) / TN);
+    int2 r = make_int2(end, end);
+    if (e < a.experts) r = expert_rows(a, e);
+    const bool range = r.x >= 0 && r.y >= r.x && r.y <= a.m;
+    // a range ends where the next begins: if every one is a range, they ascend
+    if (__all_sync(0xffffffffu, range && r.x >= end)) {
+      end = __shfl_sync(0xffffffffu, r.y, min(31, a.experts - 1 - e0));
+    } else {
+      int seen = range && r.y > r.x ? r.y : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, seen, o);
+        if (lane >= o) seen = max(seen, v);
+      }
+      int before = __shfl_up_sync(0xffffffffu, seen, 1);
+      before = lane == 0 ? end : max(end, before);
+      if (!range || (r.y > r.x && r.x < before)) {
+        atomicCAS(&g_gemm_error, 0, 0x701);
+        r = make_int2(0, 0);
+      }
+      end = max(end, __shfl_sync(0xffffffffu, seen, 31));
     }
+    const int c = (int)(((int64_t)r.y - r.x + TN - 1) / TN);
     int inc = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

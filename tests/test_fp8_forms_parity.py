@@ -47,6 +47,49 @@ def in_form(a, sa, w, sw, off, out, tile, parts, give_up=-1):
     assert rc == B.MLA_OK, B.load().mla_decode_last_error_string()
 
 
+FORMS = [(16, 1), (16, 2), (16, 4), (16, 8), (32, 1), (32, 2), (32, 4), (32, 8), (64, 1), (64, 2), (64, 4), (64, 8),
+         (128, 1), (256, 1)]
+
+
+def owned(off, t):
+    """Rows of each expert: its range, unless that is no range within [0, t] or
+    begins before the end of an earlier one."""
+    rows, end = [], 0
+    for lo, hi in zip(off[:-1], off[1:]):
+        ok = 0 <= lo <= hi <= t
+        rows.append(range(lo, hi) if ok and (lo >= end or lo == hi) else range(0))
+        if ok and hi > lo:
+            end = max(end, hi)
+    return rows
+
+
+def broken_offsets():
+    rng = np.random.default_rng(0)
+    many = np.sort(rng.integers(0, 201, 71))  # three groups of 32 experts
+    for i, v in [(5, -1), (30, 201), (31, 0), (33, 200), (50, 3), (64, 0)]:
+        many[i] = v
+    return [([0, 40, 0, 40], 40), ([0, 40, 0, 40, 0, 40, 0, 40], 40), ([0, 30, 20, 40], 40), ([10, 5, 20, 12, 25, 40], 40),
+            ([3, 3, 50, 40, 50, 60, 20, 64], 64), ([0] * 33 + [9, 4, 30], 30), (many.tolist(), 200)]
+
+
+@pytest.mark.parametrize("tile,parts", FORMS)
+@pytest.mark.parametrize("off,t", broken_offsets())
+def test_no_row_has_two_owners(off, t, tile, parts):
+    """Offsets that descend: overlapping ranges are refused on the device, and
+    the rows that are owned are right in every form."""
+    n, k, experts = 136, 2048, len(off) - 1
+    a, sa, w, sw = operands(np.random.default_rng(t + experts), t, n, k, experts)
+    out = torch.full((t, n), 7.0, device="cuda")
+    in_form(a, sa, w, sw, torch.tensor(off, dtype=torch.int32, device="cuda"), out, tile, parts)
+    assert B.mla_decode_device_error(reset=True) == 0x701
+    want = torch.full_like(out, 7.0)
+    for e, rows in enumerate(owned(off, t)):
+        if len(rows):
+            r = slice(rows.start, rows.stop)
+            want[r] = exact(a[r], sa[:, r], w[e], sw[e]).float()
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("tile,parts,k,warp", [(16, 8, 2048, 0), (16, 8, 2048, 3), (16, 2, 4096, 1), (32, 4, 1024, 5),
                                                (64, 8, 4096, 7), (64, 2, 512, 4), (16, 1, 1024, 2), (64, 1, 2048, 6)])
 def test_a_warp_that_gives_up_ends_the_kernel(tile, parts, k, warp):
