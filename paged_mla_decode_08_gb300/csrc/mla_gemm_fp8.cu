@@ -367,10 +367,12 @@ __device__ __forceinline__ bool issue_in_turn(uint32_t abort_flag, const Bars& b
   return true;
 }
 
-// Rows [lo, hi) of expert e, as the offsets say.
+// Rows [lo, hi) of expert e, as the offsets say.  Plain loads: the kernel before
+// this one may still be writing them while this one is resident, and a read-only
+// load may only be used on what nobody writes in a kernel's lifetime.
 __device__ __forceinline__ int2 expert_rows(const Args& a, int e) {
   if (a.offsets == nullptr) return make_int2(0, a.m);
-  return make_int2(__ldg(a.offsets + e), __ldg(a.offsets + e + 1));
+  return make_int2(a.offsets[e], a.offsets[e + 1]);
 }
 
 // prefix[e] = token tiles of the experts before e, by one warp.  An expert whose

@@ -90,6 +90,39 @@ def test_no_row_has_two_owners(off, t, tile, parts):
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("tile,parts", FORMS)
+def test_offsets_from_the_kernel_before(tile, parts):
+    """The offsets are results of a long kernel that is still running when the
+    product's CTAs become resident (a norm's residual output, whose last row they
+    are: 0 + bits, exact), call by call and replayed from a graph."""
+    experts, t, n, k, rows = 64, 192, 136, 2048, 20000
+    rng = np.random.default_rng(tile + parts)
+    a, sa, w, sw = operands(rng, t, n, k, experts)
+    x = torch.zeros(rows, experts + 1, dtype=torch.bfloat16, device="cuda")
+    weight, y = torch.ones(experts + 1, dtype=torch.bfloat16, device="cuda"), torch.empty_like(x)
+    source = torch.zeros(rows, experts + 1, device="cuda")
+    copied = torch.zeros_like(source)
+    off = copied[-1].view(torch.int32)
+    out = torch.empty(t, n, device="cuda")
+
+    def step():
+        B.mla_add_rmsnorm(x, source, copied, B.MLA_OUT_FP32, weight, 1.0, y, B.MLA_OUT_BF16)
+        in_form(a, sa, w, sw, off, out, tile, parts)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(6):
+        now = np.sort(np.concatenate([[0, t], rng.integers(0, t + 1, experts - 1)])).astype(np.int32)
+        source[-1].view(torch.int32).copy_(torch.from_numpy(now))
+        torch.cuda.synchronize()
+        graph.replay() if i % 2 else step()
+        want = torch.cat([exact(a[lo:hi], sa[:, lo:hi], w[e], sw[e]) for e, (lo, hi) in enumerate(zip(now[:-1], now[1:]))])
+        assert torch.equal(out, want.float())
+
+
 @pytest.mark.parametrize("tile,parts,k,warp", [(16, 8, 2048, 0), (16, 8, 2048, 3), (16, 2, 4096, 1), (32, 4, 1024, 5),
                                                (64, 8, 4096, 7), (64, 2, 512, 4), (16, 1, 1024, 2), (64, 1, 2048, 6)])
 def test_a_warp_that_gives_up_ends_the_kernel(tile, parts, k, warp):
