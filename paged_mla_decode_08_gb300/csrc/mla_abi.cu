@@ -56,7 +56,10 @@ namespace {
 
 thread_local std::string g_last_error;
 
+// A CUDA error is reported by the call that met it, once: the runtime keeps it for
+// cudaGetLastError, which the launches of the next call ask.
 int fail(int code, const std::string& msg) {
+  if (code == MLA_ERR_CUDA || code == MLA_ERR_UNSUPPORTED) cudaGetLastError();
   g_last_error = msg;
   return code;
 }

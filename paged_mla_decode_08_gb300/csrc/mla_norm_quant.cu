@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kActThreads) act_quantize_kernel(const ActArgs
 }
 
 template <class Kernel, class A>
-static void launch_pdl(Kernel kernel, dim3 blocks, unsigned threads, cudaStream_t stream, const A& a) {
+static cudaError_t launch_pdl(Kernel kernel, dim3 blocks, unsigned threads, cudaStream_t stream, const A& a) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = blocks;
   cfg.blockDim = dim3(threads);
@@ -376,47 +376,38 @@ static void launch_pdl(Kernel kernel, dim3 blocks, unsigned threads, cudaStream_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, a);  // an error is read with cudaGetLastError
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 static bool multiple(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 template <int kChunks, bool kVec, int kRes, bool kWarpRow>
-static void launch_norm_out(const NormArgs& a, int threads, bool e4m3, cudaStream_t stream) {
+static cudaError_t launch_norm_out(const NormArgs& a, int threads, bool e4m3, cudaStream_t stream) {
   const dim3 grid(kWarpRow ? (unsigned)(((int64_t)a.num_tokens + kRowsPerCta - 1) / kRowsPerCta) : a.num_tokens);
-  if (e4m3)
-    launch_pdl(add_rmsnorm_kernel<kChunks, kVec, kRes, true, kWarpRow>, grid, threads, stream, a);
-  else
-    launch_pdl(add_rmsnorm_kernel<kChunks, kVec, kRes, false, kWarpRow>, grid, threads, stream, a);
+  return e4m3 ? launch_pdl(add_rmsnorm_kernel<kChunks, kVec, kRes, true, kWarpRow>, grid, threads, stream, a)
+              : launch_pdl(add_rmsnorm_kernel<kChunks, kVec, kRes, false, kWarpRow>, grid, threads, stream, a);
 }
 
 template <int kChunks, bool kWarpRow, bool kVec>
-static void launch_norm_res(const NormArgs& a, int threads, int res, bool e4m3, cudaStream_t stream) {
-  if (res == 0)
-    launch_norm_out<kChunks, kVec, 0, kWarpRow>(a, threads, e4m3, stream);
-  else if (res == 1)
-    launch_norm_out<kChunks, kVec, 1, kWarpRow>(a, threads, e4m3, stream);
-  else
-    launch_norm_out<kChunks, kVec, 2, kWarpRow>(a, threads, e4m3, stream);
+static cudaError_t launch_norm_res(const NormArgs& a, int threads, int res, bool e4m3, cudaStream_t stream) {
+  if (res == 0) return launch_norm_out<kChunks, kVec, 0, kWarpRow>(a, threads, e4m3, stream);
+  if (res == 1) return launch_norm_out<kChunks, kVec, 1, kWarpRow>(a, threads, e4m3, stream);
+  return launch_norm_out<kChunks, kVec, 2, kWarpRow>(a, threads, e4m3, stream);
 }
 
 template <bool kRes>
-static void launch_norm_rows(const NormArgs& a, int items, bool e4m3, int sms, cudaStream_t stream) {
+static cudaError_t launch_norm_rows(const NormArgs& a, int items, bool e4m3, int sms, cudaStream_t stream) {
   const int threads = ((items + kRowsChunks - 1) / kRowsChunks + 31) / 32 * 32;
   const dim3 grid(std::min(a.num_tokens, sms * std::max(1, 2 * kRowsThreads / threads)));
-  if (e4m3)
-    launch_pdl(add_rmsnorm_rows_kernel<kRes, true>, grid, threads, stream, a);
-  else
-    launch_pdl(add_rmsnorm_rows_kernel<kRes, false>, grid, threads, stream, a);
+  return e4m3 ? launch_pdl(add_rmsnorm_rows_kernel<kRes, true>, grid, threads, stream, a)
+              : launch_pdl(add_rmsnorm_rows_kernel<kRes, false>, grid, threads, stream, a);
 }
 
 template <int kChunks, bool kWarpRow>
-static void launch_norm(const NormArgs& a, int items, bool vec, int res, bool e4m3, cudaStream_t stream) {
+static cudaError_t launch_norm(const NormArgs& a, int items, bool vec, int res, bool e4m3, cudaStream_t stream) {
   const int threads = kWarpRow ? 32 * kRowsPerCta : ((items + kChunks - 1) / kChunks + 31) / 32 * 32;
-  if (vec)
-    launch_norm_res<kChunks, kWarpRow, true>(a, threads, res, e4m3, stream);
-  else
-    launch_norm_res<kChunks, kWarpRow, false>(a, threads, res, e4m3, stream);
+  return vec ? launch_norm_res<kChunks, kWarpRow, true>(a, threads, res, e4m3, stream)
+             : launch_norm_res<kChunks, kWarpRow, false>(a, threads, res, e4m3, stream);
 }
 
 }  // namespace mla_nq
@@ -454,24 +445,15 @@ cudaError_t launch_add_rmsnorm(const void* x, int64_t x_stride, const void* res_
   // 153 us against 168 by a CTA per row, 16384 x 4096 without one 42 against 49).
   // Not with an fp32 residual, whose wider fetches cost more registers than they
   // win (130 against 107).
-  if (vec && residual_kind != 2 && items > 128 && items <= kRowsChunks * kRowsThreads && num_tokens >= 4 * sms) {
-    if (residual_kind == 0)
-      launch_norm_rows<false>(a, items, e4m3, sms, stream);
-    else
-      launch_norm_rows<true>(a, items, e4m3, sms, stream);
-  } else if (items <= 32)
-    launch_norm<1, true>(a, items, vec, residual_kind, e4m3, stream);
-  else if (items <= 64)
-    launch_norm<2, true>(a, items, vec, residual_kind, e4m3, stream);
-  else if (items <= 128)
-    launch_norm<4, true>(a, items, vec, residual_kind, e4m3, stream);
-  else if (items <= 1024)
-    launch_norm<1, false>(a, items, vec, residual_kind, e4m3, stream);
-  else if (items <= 2048)
-    launch_norm<2, false>(a, items, vec, residual_kind, e4m3, stream);
-  else
-    launch_norm<4, false>(a, items, vec, residual_kind, e4m3, stream);
-  return cudaGetLastError();
+  if (vec && residual_kind != 2 && items > 128 && items <= kRowsChunks * kRowsThreads && num_tokens >= 4 * sms)
+    return residual_kind == 0 ? launch_norm_rows<false>(a, items, e4m3, sms, stream)
+                              : launch_norm_rows<true>(a, items, e4m3, sms, stream);
+  if (items <= 32) return launch_norm<1, true>(a, items, vec, residual_kind, e4m3, stream);
+  if (items <= 64) return launch_norm<2, true>(a, items, vec, residual_kind, e4m3, stream);
+  if (items <= 128) return launch_norm<4, true>(a, items, vec, residual_kind, e4m3, stream);
+  if (items <= 1024) return launch_norm<1, false>(a, items, vec, residual_kind, e4m3, stream);
+  if (items <= 2048) return launch_norm<2, false>(a, items, vec, residual_kind, e4m3, stream);
+  return launch_norm<4, false>(a, items, vec, residual_kind, e4m3, stream);
 }
 
 cudaError_t launch_act_quantize(const void* x, int64_t x_stride, int num_tokens, int dim, bool silu_mul, void* y,
@@ -492,15 +474,13 @@ cudaError_t launch_act_quantize(const void* x, int64_t x_stride, int num_tokens,
   const int rows = kActThreads >> a.row_shift, cols = 16 << a.row_shift;
   const dim3 blocks((unsigned)(((int64_t)num_tokens + rows - 1) / rows), (unsigned)(((int64_t)dim + cols - 1) / cols));
   if (silu_mul && e4m3)
-    vec ? launch_pdl(act_quantize_kernel<true, true, true>, blocks, kActThreads, stream, a)
-        : launch_pdl(act_quantize_kernel<false, true, true>, blocks, kActThreads, stream, a);
-  else if (silu_mul)
-    vec ? launch_pdl(act_quantize_kernel<true, true, false>, blocks, kActThreads, stream, a)
-        : launch_pdl(act_quantize_kernel<false, true, false>, blocks, kActThreads, stream, a);
-  else
-    vec ? launch_pdl(act_quantize_kernel<true, false, true>, blocks, kActThreads, stream, a)
-        : launch_pdl(act_quantize_kernel<false, false, true>, blocks, kActThreads, stream, a);
-  return cudaGetLastError();
+    return vec ? launch_pdl(act_quantize_kernel<true, true, true>, blocks, kActThreads, stream, a)
+               : launch_pdl(act_quantize_kernel<false, true, true>, blocks, kActThreads, stream, a);
+  if (silu_mul)
+    return vec ? launch_pdl(act_quantize_kernel<true, true, false>, blocks, kActThreads, stream, a)
+               : launch_pdl(act_quantize_kernel<false, true, false>, blocks, kActThreads, stream, a);
+  return vec ? launch_pdl(act_quantize_kernel<true, false, true>, blocks, kActThreads, stream, a)
+             : launch_pdl(act_quantize_kernel<false, false, true>, blocks, kActThreads, stream, a);
 }
 
 }  // namespace mla
