@@ -33,7 +33,7 @@ CUDA_SOURCES = ["mla_abi.cu", "mla_sm103.cu", "mla_combine.cu", "mla_noalloc.cu"
                 "mla_plan_device.cu", "mla_kv_write.cu", "mla_norm_quant.cu", "mla_gemm_fp8.cu"]
 CXX_SOURCES = ["mla_plan.cpp"]
 CALLS_SOURCE = "mla_torch_calls.cpp"  # built against this machine's Python and torch
-HEADERS = ["mla_internal.h", "sm103_ptx.cuh"]
+HEADERS = ["mla_internal.h", "per_device.h", "sm103_ptx.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

@@ -13,6 +13,7 @@
 
 #include "../../include/mla_decode.h"
 #include "mla_internal.h"
+#include "per_device.h"
 
 namespace mla {
 cudaError_t launch_sm103(const mla_plan& p, const DecodeArgs& a, const void* workspace, cudaStream_t stream);
@@ -45,9 +46,9 @@ cudaError_t launch_act_quantize(const void* x, int64_t x_stride, int num_tokens,
                                 cudaStream_t stream);
 cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda, int64_t a_scale_stride, const void* w,
                             const float* w_scales, int64_t ldw, const int32_t* offsets, int m, int n, int k,
-                            int experts, void* out, bool fp32, int64_t ldo, const GemmForm* form, int sms,
+                            int experts, void* out, bool fp32, int64_t ldo, const GemmForm* form, Device dev,
                             cudaStream_t stream);
-void gemm_fp8_form(bool grouped, int m, int n, int k, int experts, const void* out, bool fp32, int64_t ldo, int sms,
+void gemm_fp8_form(bool grouped, int m, int n, int k, int experts, const void* out, bool fp32, int64_t ldo, Device dev,
                    const int32_t* clusters, int* tile_tokens, int* k_parts, int* copied);
 cudaError_t gemm_read_error(int* code, bool reset);
 }  // namespace mla
@@ -70,15 +71,15 @@ int ok() {
 }
 
 // Per-device capability cache: 1 = sm_103, -1 = other, 0 = unknown.
-int g_dev_ok[64];
-int g_dev_sms[64];
+int g_dev_ok[mla::kMaxDevices];
+int g_dev_sms[mla::kMaxDevices];
 std::mutex g_dev_mu;
 
-int check_device(int* sms_out) {
+int check_device(int* sms_out, int* device_out = nullptr) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("cudaGetDevice: ") + cudaGetErrorString(e));
-  if (dev < 0 || dev >= 64) return fail(MLA_ERR_UNSUPPORTED, "device index out of range");
+  if (dev < 0 || dev >= mla::kMaxDevices) return fail(MLA_ERR_UNSUPPORTED, "device index out of range");
   std::lock_guard<std::mutex> lk(g_dev_mu);
   if (g_dev_ok[dev] == 0) {
     int maj = 0, min = 0, sms = 0;
@@ -92,6 +93,7 @@ int check_device(int* sms_out) {
   if (g_dev_ok[dev] != 1)
     return fail(MLA_ERR_UNSUPPORTED, "this library holds sm_103a code only (GB300 class GPU required)");
   if (sms_out) *sms_out = g_dev_sms[dev];
+  if (device_out) *device_out = dev;
   return MLA_OK;
 }
 
@@ -639,11 +641,11 @@ static int gemm_fp8(const void* a, int64_t lda, const float* a_scales, int64_t a
   // tiles are counted in 32 bits: at most (num_tokens / 16 + num_experts) x ceil(n / 128)
   if (((int64_t)num_tokens / 16 + num_experts) * (((int64_t)n + 127) / 128) > INT32_MAX / 2)
     return fail(MLA_ERR_ARG, "too many tiles for one launch");
-  int sms = 0;
-  rc = check_device(&sms);
+  mla::Device dev{};
+  rc = check_device(&dev.sms, &dev.id);
   if (rc != MLA_OK) return rc;
   cudaError_t e = mla::launch_gemm_fp8(a, a_scales, lda, a_scale_stride, w, w_scales, ldw, expert_offsets, num_tokens,
-                                       n, k, num_experts, out, out_dtype == MLA_OUT_FP32, ldo, form, sms,
+                                       n, k, num_experts, out, out_dtype == MLA_OUT_FP32, ldo, form, dev,
                                        static_cast<cudaStream_t>(stream));
   if (e == cudaErrorNotSupported)
     return fail(MLA_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled unavailable or rejected the operands");
@@ -700,11 +702,12 @@ int mla_gemm_fp8_form(int num_tokens, int n, int k, int num_experts, int grouped
     return fail(MLA_ERR_ARG, "out_dtype must be MLA_OUT_BF16 or MLA_OUT_FP32");
   if (num_sms < 0 || (num_sms > 0) != (clusters != nullptr))
     return fail(MLA_ERR_ARG, "num_sms > 0 and clusters go together");
+  mla::Device dev{0, num_sms};
   if (num_sms == 0) {
-    rc = check_device(&num_sms);
+    rc = check_device(&dev.sms, &dev.id);
     if (rc != MLA_OK) return rc;
   }
-  mla::gemm_fp8_form(grouped != 0, num_tokens, n, k, num_experts, out, out_dtype == MLA_OUT_FP32, ldo, num_sms, clusters,
+  mla::gemm_fp8_form(grouped != 0, num_tokens, n, k, num_experts, out, out_dtype == MLA_OUT_FP32, ldo, dev, clusters,
                      tile_tokens, k_parts, copied_results);
   return ok();
 }

@@ -27,6 +27,7 @@
 #include <mutex>
 
 #include "mla_internal.h"
+#include "per_device.h"
 #include "sm103_ptx.cuh"
 
 namespace mla {
@@ -1398,38 +1399,34 @@ struct Form {
     cfg->attrs = attr;
     cfg->numAttrs = cluster > 1 ? 2 : 1;
   }
-  static cudaError_t set_attributes() {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] {
-      err = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    });
-    return err;
-  }
-  // clusters of `size` (2, 4, 8) CTAs that run at once; 0 when unknown
-  static int active_clusters(int size) {
-    static std::once_flag once;
-    static int count[3];
-    std::call_once(once, [] {
+  // clusters of `size` (2, 4, 8) CTAs that run at once on the device; 0 when unknown
+  static int active_clusters(int device, int size) {
+    static OncePerDevice once;
+    static int count[kMaxDevices][3];
+    const cudaError_t e = once.run(device, [&] {
       constexpr auto kPlaces = places_kernel<C::kThreads, C::kCtasPerSm>;
-      const bool ok = cudaFuncSetAttribute(kPlaces, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) == cudaSuccess;
-      for (int i = 0; i < 3; ++i) {
+      cudaError_t err = cudaFuncSetAttribute(kPlaces, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      for (int i = 0; i < 3 && err == cudaSuccess; ++i) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         config(&cfg, attr, 2 << i, 2 << i, nullptr);
         cfg.attrs = attr + 1;
         cfg.numAttrs = 1;
-        if (!ok || cudaOccupancyMaxActiveClusters(&count[i], kPlaces, &cfg) != cudaSuccess) {
-          cudaGetLastError();
-          count[i] = 0;
-        }
+        err = cudaOccupancyMaxActiveClusters(&count[device][i], kPlaces, &cfg);
       }
+      return err;
     });
-    return count[size == 2 ? 0 : size == 4 ? 1 : 2];
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    return count[device][size == 2 ? 0 : size == 4 ? 1 : 2];
   }
-  static cudaError_t launch(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const Args& a, int64_t grid,
+  static cudaError_t launch(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const Args& a, int64_t grid, int device,
                             cudaStream_t stream) {
-    const cudaError_t e = set_attributes();
+    static OncePerDevice once;
+    const cudaError_t e = once.run(
+        device, [] { return cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
@@ -1440,7 +1437,7 @@ struct Form {
 
 template <int TN, bool kFp32>
 static cudaError_t launch_tn(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, Args a, int splits,
-                             int sms, cudaStream_t stream) {
+                             Device dev, cudaStream_t stream) {
   using Split = Form<TN, true, kFp32>;
   using Whole = Form<TN, false, kFp32>;
   CUtensorMap tm_w, tm_a;
@@ -1448,27 +1445,25 @@ static cudaError_t launch_tn(const void* act, int64_t lda, const void* w, int64_
     return cudaErrorNotSupported;
   a.splits = splits;
   const int64_t tiles = most_token_tiles(a, TN) * a.row_blocks;
-  if (splits > 1) return Split::launch(tm_w, tm_a, a, tiles * splits, stream);
-  return Whole::launch(tm_w, tm_a, a, std::min<int64_t>(tiles, (int64_t)sms * Whole::C::kCtasPerSm), stream);
+  if (splits > 1) return Split::launch(tm_w, tm_a, a, tiles * splits, dev.id, stream);
+  return Whole::launch(tm_w, tm_a, a, std::min<int64_t>(tiles, (int64_t)dev.sms * Whole::C::kCtasPerSm), dev.id, stream);
 }
 
 template <bool kFp32, bool kVec>
 static cudaError_t launch_square(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, const Args& a,
-                                 int sms, cudaStream_t stream) {
+                                 Device dev, cudaStream_t stream) {
   constexpr auto kernel = square::gemm_square_kernel<kFp32, kVec>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, square::kSmem);
-  });
-  if (attr_err != cudaSuccess) return attr_err;
+  static OncePerDevice once;
+  const cudaError_t e = once.run(
+      dev.id, [] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, square::kSmem); });
+  if (e != cudaSuccess) return e;
   CUtensorMap tm_w, tm_a, tm_out;
   if (!make_map(&tm_w, w, k, (int64_t)a.experts * a.n, ldw, square::kTileCol) ||
       !make_map(&tm_a, act, k, a.m, lda, square::kTileTok))
     return cudaErrorNotSupported;
   if (!make_out_map<kFp32, kVec>(&tm_out, a, 64)) return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(most_token_tiles(a, square::kTileTok) * a.row_blocks, sms));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(most_token_tiles(a, square::kTileTok) * a.row_blocks, dev.sms));
   cfg.blockDim = dim3(square::kThreads);
   cfg.dynamicSmemBytes = square::kSmem;
   cfg.stream = stream;
@@ -1481,22 +1476,20 @@ static cudaError_t launch_square(const void* act, int64_t lda, const void* w, in
 }
 
 template <bool kFp32, bool kVec>
-static cudaError_t launch_paired(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, Args a, int sms,
-                               cudaStream_t stream) {
+static cudaError_t launch_paired(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, Args a, Device dev,
+                                 cudaStream_t stream) {
   constexpr auto kernel = paired::gemm_paired_kernel<kFp32, kVec>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, paired::kSmem);
-  });
-  if (attr_err != cudaSuccess) return attr_err;
+  static OncePerDevice once;
+  const cudaError_t e = once.run(
+      dev.id, [] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, paired::kSmem); });
+  if (e != cudaSuccess) return e;
   CUtensorMap tm_w, tm_a, tm_out;
   if (!make_map(&tm_w, w, k, (int64_t)a.experts * a.n, ldw, paired::kHalf) ||
       !make_map(&tm_a, act, k, a.m, lda, paired::kHalf))
     return cudaErrorNotSupported;
   if (!make_out_map<kFp32, kVec>(&tm_out, a, 128)) return cudaErrorNotSupported;
   a.row_blocks = (a.n + paired::kTileCol - 1) / paired::kTileCol;
-  const int64_t pairs = std::min<int64_t>(most_token_tiles(a, paired::kTileTok) * a.row_blocks, sms / 2);
+  const int64_t pairs = std::min<int64_t>(most_token_tiles(a, paired::kTileTok) * a.row_blocks, dev.sms / 2);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
   cfg.blockDim = dim3(paired::kThreads);
@@ -1550,14 +1543,15 @@ static int64_t expected_tiles(const Args& a, int tokens, int64_t row_tiles) {
 
 // `clusters`: how many clusters of 2, 4 and 8 CTAs run at once (nullptr: asked of the device).
 template <int TN, bool kFp32>
-static void consider(const Args& a, int sms, const int32_t* clusters, Cost c, double weights, Choice* choice) {
+static void consider(const Args& a, Device dev, const int32_t* clusters, Cost c, double weights, Choice* choice) {
   constexpr int kPerSm = Cfg<TN, true>::kCtasPerSm;
+  const int sms = dev.sms;
   const int64_t tiles = expected_tiles(a, TN, a.row_blocks), most = most_token_tiles(a, TN) * a.row_blocks;
   for (int i = 0, s = 1; s <= 8; ++i, s *= 2) {
     if (s > 1) {
       // every cluster runs at once, and a CTA keeps two blocks
       if (a.k_blocks < 2 * s || most * s > (int64_t)sms * kPerSm) break;
-      if (most > (clusters ? clusters[i - 1] : Form<TN, true, kFp32>::active_clusters(s))) break;
+      if (most > (clusters ? clusters[i - 1] : Form<TN, true, kFp32>::active_clusters(dev.id, s))) break;
     }
     const int64_t on_sm = (tiles * s + sms - 1) / sms;  // CTAs of an SM, at once or one after the other
     const double chain = on_sm * (((a.k_blocks + s - 1) / s) * (on_sm == 1 ? c.alone : c.shared) + c.tile);
@@ -1566,12 +1560,13 @@ static void consider(const Args& a, int sms, const int32_t* clusters, Cost c, do
 }
 
 template <bool kFp32>
-static Choice choose(const Args& a, int sms, const int32_t* clusters) {
+static Choice choose(const Args& a, Device dev, const int32_t* clusters) {
   Choice c;
+  const int sms = dev.sms;
   const double weights = (double)std::min(a.experts, a.m) * a.n * a.k_blocks * kBlockK / 6.3e6;
-  consider<16, kFp32>(a, sms, clusters, {0.244, 0.178, 0.5, 2.5, 1.2}, weights, &c);
-  if (a.m > 16) consider<32, kFp32>(a, sms, clusters, {0.276, 0.191, 0.8, 2.4, 1.8}, weights, &c);
-  if (a.m > 32) consider<64, kFp32>(a, sms, clusters, {0.395, 0.285, 1.4, 2.7, 2.2}, weights, &c);
+  consider<16, kFp32>(a, dev, clusters, {0.244, 0.178, 0.5, 2.5, 1.2}, weights, &c);
+  if (a.m > 16) consider<32, kFp32>(a, dev, clusters, {0.276, 0.191, 0.8, 2.4, 1.8}, weights, &c);
+  if (a.m > 32) consider<64, kFp32>(a, dev, clusters, {0.395, 0.285, 1.4, 2.7, 2.2}, weights, &c);
   if (a.m > 64) {
     const int64_t rounds = (expected_tiles(a, square::kTileTok, a.row_blocks) + sms - 1) / sms;
     c.offer(std::max(rounds * (a.k_blocks * 0.253 + 1.4), weights) + 2.6, kSquare, 1);
@@ -1595,25 +1590,25 @@ static bool copied_results(const Args& a) {
 
 template <bool kFp32>
 static cudaError_t launch_out(const void* act, int64_t lda, const void* w, int64_t ldw, int64_t k, const Args& a,
-                              const GemmForm* form, int sms, cudaStream_t stream) {
+                              const GemmForm* form, Device dev, cudaStream_t stream) {
   Choice c;
   if (form) {
     c.shape = form->tile_tokens;
     c.splits = form->k_parts;
   } else {
-    c = choose<kFp32>(a, sms, nullptr);
+    c = choose<kFp32>(a, dev, nullptr);
   }
   const bool vec = copied_results<kFp32>(a);
   switch (c.shape) {
-    case kSwapped16: return launch_tn<16, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
-    case kSwapped32: return launch_tn<32, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
-    case kSwapped64: return launch_tn<64, kFp32>(act, lda, w, ldw, k, a, c.splits, sms, stream);
+    case kSwapped16: return launch_tn<16, kFp32>(act, lda, w, ldw, k, a, c.splits, dev, stream);
+    case kSwapped32: return launch_tn<32, kFp32>(act, lda, w, ldw, k, a, c.splits, dev, stream);
+    case kSwapped64: return launch_tn<64, kFp32>(act, lda, w, ldw, k, a, c.splits, dev, stream);
     case kSquare:
-      return vec ? launch_square<kFp32, true>(act, lda, w, ldw, k, a, sms, stream)
-                 : launch_square<kFp32, false>(act, lda, w, ldw, k, a, sms, stream);
+      return vec ? launch_square<kFp32, true>(act, lda, w, ldw, k, a, dev, stream)
+                 : launch_square<kFp32, false>(act, lda, w, ldw, k, a, dev, stream);
   }
-  return vec ? launch_paired<kFp32, true>(act, lda, w, ldw, k, a, sms, stream)
-             : launch_paired<kFp32, false>(act, lda, w, ldw, k, a, sms, stream);
+  return vec ? launch_paired<kFp32, true>(act, lda, w, ldw, k, a, dev, stream)
+             : launch_paired<kFp32, false>(act, lda, w, ldw, k, a, dev, stream);
 }
 
 }  // namespace gemm8
@@ -1640,12 +1635,12 @@ static gemm8::Args gemm_args(const float* a_scales, int64_t a_scale_stride, cons
 
 // The form that launch_gemm_fp8 chooses (`grouped`: offsets are given), and
 // whether the copy engine stores its results.
-void gemm_fp8_form(bool grouped, int m, int n, int k, int experts, const void* out, bool fp32, int64_t ldo, int sms,
+void gemm_fp8_form(bool grouped, int m, int n, int k, int experts, const void* out, bool fp32, int64_t ldo, Device dev,
                    const int32_t* clusters, int* tile_tokens, int* k_parts, int* copied) {
   static const int32_t some = 0;  // not read
   const gemm8::Args a =
       gemm_args(nullptr, 0, nullptr, grouped ? &some : nullptr, m, n, k, experts, const_cast<void*>(out), ldo);
-  const gemm8::Choice c = fp32 ? gemm8::choose<true>(a, sms, clusters) : gemm8::choose<false>(a, sms, clusters);
+  const gemm8::Choice c = fp32 ? gemm8::choose<true>(a, dev, clusters) : gemm8::choose<false>(a, dev, clusters);
   *tile_tokens = c.shape;
   *k_parts = c.splits;
   *copied = c.shape >= gemm8::kSquare && (fp32 ? gemm8::copied_results<true>(a) : gemm8::copied_results<false>(a));
@@ -1656,12 +1651,12 @@ void gemm_fp8_form(bool grouped, int m, int n, int k, int experts, const void* o
 // with the least estimated time.
 cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda, int64_t a_scale_stride, const void* w,
                             const float* w_scales, int64_t ldw, const int32_t* offsets, int m, int n, int k,
-                            int experts, void* out, bool fp32, int64_t ldo, const GemmForm* form, int sms,
+                            int experts, void* out, bool fp32, int64_t ldo, const GemmForm* form, Device dev,
                             cudaStream_t stream) {
   gemm8::Args a = gemm_args(a_scales, a_scale_stride, w_scales, offsets, m, n, k, experts, out, ldo);
   if (form) a.give_up = form->give_up_warp;
-  return fp32 ? gemm8::launch_out<true>(act, lda, w, ldw, k, a, form, sms, stream)
-              : gemm8::launch_out<false>(act, lda, w, ldw, k, a, form, sms, stream);
+  return fp32 ? gemm8::launch_out<true>(act, lda, w, ldw, k, a, form, dev, stream)
+              : gemm8::launch_out<false>(act, lda, w, ldw, k, a, form, dev, stream);
 }
 
 cudaError_t gemm_read_error(int* code, bool reset) {

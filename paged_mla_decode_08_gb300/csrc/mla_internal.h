@@ -94,6 +94,11 @@ struct DecodeArgs {
   int32_t q_e4m3;          // q_nope is the merged e4m3 query [T, H, 576] (q_pe unused)
 };
 
+// The device a call runs on: its ordinal and its SMs.
+struct Device {
+  int id, sms;
+};
+
 // A form of the FP8 products that a caller asked for (mla_gemm_fp8_in_form).
 struct GemmForm {
   int tile_tokens;   // 16, 32, 64: swapped; 128: square; 256: paired

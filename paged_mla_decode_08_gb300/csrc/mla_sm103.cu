@@ -54,6 +54,7 @@
 
 #include "../../include/mla_decode.h"
 #include "mla_internal.h"
+#include "per_device.h"
 #include "sm103_ptx.cuh"
 
 namespace mla {
@@ -1222,16 +1223,22 @@ static bool make_map(CUtensorMap* m, const void* kv, int64_t rows, int box_cols,
   return r == CUDA_SUCCESS;
 }
 
+// The kernel's shared memory, allowed on the current device.
+template <class Kernel>
+static cudaError_t allow_smem(OncePerDevice& once, Kernel kernel) {
+  int device = 0;
+  const cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  return once.run(device,
+                  [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes); });
+}
+
 template <int CAP, bool F8, bool Q8>
 static cudaError_t launch_cap(const mla_plan& p, const DecodeArgs& a, const CUtensorMap& lat,
                               const CUtensorMap& rope, cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err =
-        cudaFuncSetAttribute(decode_kernel<CAP, F8, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  });
-  if (attr_err != cudaSuccess) return attr_err;
+  static OncePerDevice once;
+  const cudaError_t e = allow_smem(once, decode_kernel<CAP, F8, Q8>);
+  if (e != cudaSuccess) return e;
   Schedule<CAP> s;
   s.num_workers = p.num_workers;
   s.num_segments = (int32_t)p.segs.size();
@@ -1247,12 +1254,9 @@ static cudaError_t launch_cap(const mla_plan& p, const DecodeArgs& a, const CUte
 template <bool F8, bool Q8>
 static cudaError_t launch_dev(const mla_plan& p, const DecodeArgs& a, const CUtensorMap& lat,
                               const CUtensorMap& rope, const void* workspace, cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(decode_kernel_dev<F8, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  });
-  if (attr_err != cudaSuccess) return attr_err;
+  static OncePerDevice once;
+  const cudaError_t e = allow_smem(once, decode_kernel_dev<F8, Q8>);
+  if (e != cudaSuccess) return e;
   const auto* sched = reinterpret_cast<const Schedule<kSegCapLarge>*>(static_cast<const char*>(workspace) +
                                                                        kDevSchedOffset);
   cudaLaunchConfig_t cfg = {};
