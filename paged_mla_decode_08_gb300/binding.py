@@ -355,7 +355,8 @@ def _load_calls():
     the smallest kernels."""
     global _calls
     if not os.path.exists(CALLS):
-        raise RuntimeError(f"_mla_calls.so not built ({CALLS}); run __graft_entry__.build()")
+        raise RuntimeError(f"_mla_calls.so not built ({CALLS}); run __graft_entry__.build() where a CUDA build of torch "
+                           "and Python.h are installed")
     import torch  # noqa: F401  (its libraries come first)
     load()
     spec = importlib.util.spec_from_file_location("_mla_calls", CALLS)
