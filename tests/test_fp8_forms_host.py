@@ -88,6 +88,23 @@ def test_results_that_the_copy_engine_can_address(od, elt):
     assert chosen(8, 1000, 512, od=od, ldo=1000)[2] == 0  # small tiles are stored by the warps
 
 
+def test_every_choice_is_a_form_that_is_tested():
+    """Over the sizes a layer has, dense and grouped, for several cluster counts:
+    the choice is one of the forms that the GPU tests make one by one, and every
+    width of tile is somebody's choice."""
+    from tests.test_fp8_forms_parity import FORMS
+
+    seen = set()
+    for clusters in [(150, 72, 36), (152, 76, 32), (148, 60, 15), (0, 0, 0)]:
+        for t in (1, 7, 16, 17, 32, 33, 64, 65, 100, 128, 256, 500, 512, 1024, 4096, 16384):
+            for n in (64, 576, 2048, 4096, 7168, 36864):
+                for k in (128, 512, 2048, 7168, 16384):
+                    seen.add(chosen(t, n, k, clusters=clusters)[:2])
+                    for e in (2, 8, 256):
+                        seen.add(chosen(t, n, k, e, True, clusters=clusters)[:2])
+    assert seen <= set(FORMS) and {tile for tile, _ in seen} == {16, 32, 64, 128, 256}
+
+
 def test_in_form_valid_arguments_reach_the_device_check():
     if torch.cuda.is_available():
         pytest.skip("valid arguments on fake pointers would launch on a GPU")
