@@ -793,8 +793,8 @@ __device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap* tm_
 // is; a buffer is given back as soon as it is read, and four of them keep the
 // products ahead.  Two warps issue the products in turn: the instructions of one
 // block take an issuing warp about 550 cycles here, the products 256.
-// 256 x 8192 x 8192: 21.5 us (swapped tiles of 64 tokens 43 us, paired 35 us; the
-// weights alone 10.6 us); 256 x 4096 x 4096: 12.7 us (17.1, 19.9).
+// 256 x 8192 x 8192: 22.3 us (swapped tiles of 64 tokens 42 us, paired 35 us; the
+// weights alone 10.6 us); 256 x 4096 x 4096: 13.0 us (16.4, 20.1).
 namespace square {
 
 constexpr int kTileTok = 128, kTileCol = 128;
@@ -1020,10 +1020,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of 64 of each CTA's weight rows, issued by a warp each into buffers of their own,
 // and half of the epilogue's warps take each half: they run out of step, and
 // within a warp 32 columns are read while 32 are added.  8192 tokens, n = k = 8192:
-// 423..440 us, 2.5 PFLOP/s (both halves in one product, all warps in step, reads and
-// additions in turn: 3 % more; in square tiles 475 us).  Spills in the epilogue's loop
-// cost 4 to 20 %, so it has 216 registers and its state is counted, not kept (8 bytes
-// are left with bf16 results, none with fp32).
+// 429 us in a burst at 2070 MHz, 2.6 PFLOP/s; 476 in a steady loop, whose power limit
+// leaves 1720 MHz (both halves in one product, all warps in step, reads and additions
+// in turn: 3 % more; in square tiles 496 where these take 435).  Spills in the
+// epilogue's loop cost 4 to 20 %, so it has 216 registers and its state is counted, not
+// kept (8 bytes are left with bf16 results, 4 with unaligned fp32 ones, none with fp32
+// ones that the copy engine stores).
 namespace paired {
 
 constexpr int kTileTok = 256, kTileCol = 256;  // of the pair
@@ -1505,16 +1507,18 @@ static cudaError_t launch_paired(const void* act, int64_t lda, const void* w, in
 
 // The form with the least estimated time.  The estimate's constants are times in
 // us, fitted to 640 timings on one GB300 (152 SMs; 1 to 8192 tokens, k 512 to
-// 16384, every form):
+// 16384, every form), for the large tiles before their results left by TMA:
 //   a k block of a swapped tile takes a CTA `alone` while it has its SM to itself
 //   and `shared` of the SM's time when two CTAs share it;
 //   the results of a tile cost `tile` more, the exchange of split sums `exchange`,
 //   the launch and the first loads `fixed`;
 //   the weights cannot come faster than 6.3 TB/s.
-// The chosen form is the fastest one within 1 % on average over those sizes, within
-// 15 % at worst.  Where forms meet (n = k = 4096): 64 tokens 32 swapped in 4 parts
-// 9.5, 64 in 4 9.8; 128 tokens 64 in 4 12.6, square 12.5; 512 tokens square 12.8,
-// paired 19.8; 1024 tokens square 21.8, paired 20.4; 4096 tokens square 66.9, paired 66.2.
+// On the present kernels the chosen form is the fastest one within 1.8 % on average
+// over 90 dense sizes, 22 % at worst; grouped, with rows spread over all experts, 1 % and
+// 3 %; with all rows on an eighth of the experts 10 % and 28 %, since every expert's
+// weights are counted.  Where forms meet (n = k = 4096): 64 tokens 32 swapped in 4 parts
+// 9.2, 64 in 4 9.7; 128 tokens 64 in 4 12.2, square 12.8; 512 tokens square 13.3,
+// paired 20.2; 1024 tokens square 22.7, paired 20.9; 4096 tokens square 70.3, paired 66.9.
 enum Shape { kSwapped16 = 16, kSwapped32 = 32, kSwapped64 = 64, kSquare = 128, kPaired = 256 };
 struct Choice {
   double time = 1e30;
