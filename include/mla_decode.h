@@ -587,6 +587,187 @@ int mla_gemm_fp8_form(int num_tokens, int n, int k, int num_experts, int grouped
                       int64_t ldo, int num_sms, const int32_t* clusters, int* tile_tokens, int* k_parts,
                       int* copied_results);
 
+/* ---- prompts over the latent cache ----
+ *
+ * What a step with many new tokens a request does around the cache: rotary
+ * positions, attention in the expanded form (each head's keys and values made
+ * from the latent rows by a product of the caller's, or by mla_gemm_fp8), the
+ * gather of cached rows for the expansion of a prefix, and the merge of the
+ * prefix's and the new tokens' results.  (sglang trtllm_mla_backend.py,
+ * forward_extend: ragged attention of head dims 192 / 128 with lse, prefix chunks
+ * attended without a mask and merged; tokenspeed trtllm_mla.py, forward_extend.)
+ * Every call is asynchronous on `stream`, allocates nothing and may be captured in
+ * a CUDA graph.
+ *
+ * Shared conventions.
+ *   - [tokens, heads, columns] arrays are given by a pointer and the strides of a
+ *     token and a head in elements; columns are contiguous.  Offsets are 64-bit.
+ *   - num_tokens may be 0: nothing is launched and no pointer is looked at.
+ *   - Outputs must not overlap inputs, except where stated.
+ */
+#define MLA_ROPE_PLAIN 0
+#define MLA_ROPE_LINEAR 1
+#define MLA_ROPE_YARN 2
+#define MLA_ROPE_MAX_DIM 512
+#define MLA_MERGE_MAX_DIM 2048
+#define MLA_NOPE_DIM 128
+#define MLA_V_DIM 128
+
+/*
+ * The table of cosines and sines that mla_rope and mla_rope_quantize_cache_write
+ * read.  For pair i < rotary_dim / 2 and row p of the table (position
+ * first_position + p):
+ *   table[p][i]                  = magnitude * cos((first_position + p) * w_i)
+ *   table[p][rotary_dim / 2 + i] = magnitude * sin((first_position + p) * w_i)
+ * with f_i = base^(-2 i / rotary_dim) and
+ *   MLA_ROPE_PLAIN   w_i = f_i
+ *   MLA_ROPE_LINEAR  w_i = f_i / factor
+ *   MLA_ROPE_YARN    w_i = f_i / factor * g_i + f_i * (1 - g_i),
+ *                    g_i = clamp((i - lo) / (hi - lo), 0, 1),
+ *                    lo = max(floor(d(beta_fast)), 0), hi = min(ceil(d(beta_slow)), rotary_dim - 1)
+ *                    (hi + 0.001 if they are equal),
+ *                    d(beta) = rotary_dim * ln(original_max_position / (2 pi beta)) / (2 ln base):
+ *                    pairs that turn more than beta_fast times within the original
+ *                    context keep their frequency, those that turn less than
+ *                    beta_slow times are stretched.
+ * Angles are reduced exactly (to 2^-64 of a turn a position), so far positions
+ * lose nothing: the error is that of one fp32 sine, cosine and product.
+ *
+ *   table           device fp32 [num_positions, rotary_dim], contiguous.
+ *   first_position  >= 0, first_position + num_positions <= 2^31.
+ *   rotary_dim      even, 2 .. MLA_ROPE_MAX_DIM.
+ *   base            finite, > 1.  factor: finite, > 0 (unused with PLAIN).
+ *   original_max_position >= 1, beta_fast > beta_slow > 0, finite (YARN only).
+ *   magnitude       finite.
+ * Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
+ */
+int mla_rope_table(float* table, int64_t first_position, int64_t num_positions, int rotary_dim, double base,
+                   int scaling, double factor, int64_t original_max_position, double beta_fast, double beta_slow,
+                   double magnitude, void* stream);
+
+/*
+ * Rotation of the rotary columns of a query and of a key row that all heads share:
+ * a pair (a, b) becomes (a cos - b sin, b cos + a sin), in fp32 with every product
+ * and sum rounded on its own, then to bf16.
+ *
+ *   q, q_out      device bf16 [num_tokens, num_heads, rotary_dim]: the rotary
+ *                 part of each head, wherever it lies in the head (a slice); may
+ *                 be the same array.  num_heads 0: no query (NULL).
+ *   k, k_out      device bf16 [num_tokens, rotary_dim], row strides k_stride and
+ *                 k_out_stride; may be the same array.  NULL: no key.
+ *   positions     device int64 [num_tokens], rows of cos_sin_cache.
+ *   cos_sin_cache device fp32 [max_position, rotary_dim], contiguous (mla_rope_table).
+ *   rotary_dim    even, 2 .. MLA_ROPE_MAX_DIM.
+ *   is_neox       nonzero: element i pairs with i + rotary_dim / 2; zero: 2i with 2i + 1.
+ * Strides are at least rotary_dim.  Rows of 16-byte pieces (rotary_dim and strides
+ * multiples of 8, pointers of 16 bytes) are read and written in such pieces; others
+ * by element.  A position outside [0, max_position) leaves that token's rows
+ * unwritten and the error word of mla_decode_device_error reads 0x801.
+ * Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
+ */
+int mla_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
+             int num_tokens, int num_heads, int rotary_dim, const int64_t* positions, const float* cos_sin_cache,
+             int64_t max_position, int is_neox, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+             void* k_out, int64_t k_out_stride, void* stream);
+
+/*
+ * Gather rows of the paged cache into contiguous ones, for the expansion of a
+ * cached prefix: row cu_seqlens[b] + i takes cache token starts[b] + i of request b
+ * (through block_table[b]), for i < cu_seqlens[b + 1] - cu_seqlens[b].
+ *
+ *   kv_pages, kv_dtype, num_pages, page_size, block_table, bt_stride
+ *                 the cache and its block table, as mla_decode takes them.
+ *   starts        device int32 [batch]: first token of each request (a chunk of
+ *                 its prefix); NULL = 0.
+ *   cu_seqlens    device int32 [batch + 1], nondecreasing, within [0, num_tokens].
+ *   num_tokens    rows of the outputs; rows that no request owns are not written.
+ *   k_scale       scale of an e4m3 cache (finite, > 0); unused for a bf16 cache.
+ *   latent        device [num_tokens, 512] of latent_dtype, row stride latent_stride:
+ *                 MLA_OUT_BF16  value (times k_scale), rounded once;
+ *                 MLA_OUT_E4M3  codes with fp32 latent_scales [4][scale_stride], the
+ *                 operand that mla_gemm_fp8 takes: an e4m3 cache's own codes with
+ *                 k_scale, or a bf16 cache's values through the quantiser above.
+ *   k_pe          device bf16 [num_tokens, 64], row stride k_pe_stride: the rotary
+ *                 key (times k_scale, rounded once).
+ * Pointers and row pitches are multiples of 16 bytes (scales 4).  Device-side errors
+ * (mla_decode_device_error), each leaving the row unwritten: a token outside the
+ * block table's row (0x901), a page outside the pool (0x902).  Offsets that break
+ * their rule read 0x903; which rows are written is then not specified.
+ * Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
+ */
+int mla_cache_gather(const void* kv_pages, int kv_dtype, int64_t num_pages, int page_size, const int32_t* block_table,
+                     int64_t bt_stride, const int32_t* starts, const int32_t* cu_seqlens, int batch, int num_tokens,
+                     float k_scale, void* latent, int latent_dtype, int64_t latent_stride, float* latent_scales,
+                     int64_t scale_stride, void* k_pe, int64_t k_pe_stride, void* stream);
+
+/*
+ * Attention in the expanded form over a ragged batch.  Request b owns query rows
+ * cu_seqlens_q[b] .. cu_seqlens_q[b+1] - 1 and keys cu_seqlens_k[b] ..
+ * cu_seqlens_k[b+1] - 1; with n and L of them, query i < n and head h see
+ *   V = L - n + 1 + i keys (causal: the queries are the request's last tokens), or
+ *   V = L                  (not causal: a chunk of its prefix)
+ *   s_j = scale * (q_nope[t,h] . k_nope[j,h] + q_pe[t,h] . k_pe[j])
+ *   out[t,h,:] = sum_{j<V} softmax(s)_j v[j,h,:],   lse[t,h] = ln sum_{j<V} exp(s_j)
+ * Rows with V <= 0, or whose scores are all -inf, give out = 0 and lse = -inf.
+ *
+ *   q_nope, q_pe  device bf16 [num_tokens_q, num_heads, 128] and [.., 64]: two
+ *                 arrays, or two slices of 192-wide heads.
+ *   k_nope, v     device bf16 [num_tokens_k, num_heads, 128] each: two arrays, or
+ *                 two slices of the expansion's 256-wide heads.
+ *   k_pe          device bf16 [num_tokens_k, 64], row stride k_pe_stride: the rotary
+ *                 key that all heads share.
+ *   cu_seqlens_q, cu_seqlens_k
+ *                 device int32 [batch + 1], nondecreasing, within [0, num_tokens_q]
+ *                 and [0, num_tokens_k]; read on the device, so one captured graph
+ *                 serves any lengths.  A request whose query range breaks the rule, by
+ *                 itself or by beginning before the end of an earlier one's (0xA01 in
+ *                 mla_decode_device_error), or whose key range does (0xA02), has no
+ *                 query row.  Rows that no request owns are not written.
+ *   out           device bf16 [num_tokens_q, num_heads, 128].
+ *   lse           device fp32 [num_tokens_q, num_heads], contiguous.
+ *   scale         softmax scale, finite, > 0 (1/sqrt(192) for DeepSeek-V3 shapes).
+ *   workspace     device scratch of mla_prefill_workspace_bytes (same sizes), 256-byte
+ *                 aligned; may be NULL when that is 0.  No initial contents are needed
+ *                 and none are kept; calls that overlap on the GPU must not share it.
+ * Strides are multiples of 8 elements and at least the width, all pointers 16-byte
+ * aligned (offsets and lse 4), num_heads of a one-headed array any stride.
+ * Products run on the tensor cores with bf16 operands and fp32 accumulation;
+ * probabilities enter the second one as bf16, row sums and lse use them unrounded.
+ * Masked keys and values may hold anything (NaN, infinities); a value that is not
+ * finite reaches the rows that see it and no other.
+ * Errors: MLA_ERR_ARG, MLA_ERR_WORKSPACE, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.  A wait
+ * that timed out inside the kernel reads 0xA1x.
+ */
+int mla_prefill(const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_head_stride, const void* q_pe,
+                int64_t q_pe_token_stride, int64_t q_pe_head_stride, const void* k_nope, int64_t k_nope_token_stride,
+                int64_t k_nope_head_stride, const void* k_pe, int64_t k_pe_stride, const void* v,
+                int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_seqlens_q,
+                const int32_t* cu_seqlens_k, int batch, int num_tokens_q, int num_tokens_k, int num_heads, int causal,
+                float scale, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/* Device workspace that mla_prefill needs for these sizes on the current device
+ * (0: none).  Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA. */
+int mla_prefill_workspace_bytes(int num_tokens_q, int num_tokens_k, int batch, int num_heads, size_t* bytes_out);
+
+/*
+ * Merge two partial attention results of the same rows (over disjoint keys):
+ *   lse = ln(e^lse_a + e^lse_b),  out = e^(lse_a - lse) out_a + e^(lse_b - lse) out_b
+ * in fp32, rounded once.  A part with lse = -inf weighs nothing, whatever it
+ * holds; two of them give out = 0 and lse = -inf.
+ *
+ *   out_a, out_b, out  device bf16 [num_tokens, num_heads, dim] (mla_prefill's and
+ *                 mla_decode's), 16-byte aligned, strides multiples of 8.
+ *   lse_a, lse_b, lse  device fp32 [num_tokens, num_heads], contiguous.
+ *   dim           a multiple of 8, 8 .. MLA_MERGE_MAX_DIM.
+ * out and lse may be either part's own arrays.
+ * Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
+ */
+int mla_merge_states(const void* out_a, int64_t a_token_stride, int64_t a_head_stride, const float* lse_a,
+                     const void* out_b, int64_t b_token_stride, int64_t b_head_stride, const float* lse_b,
+                     int num_tokens, int num_heads, int dim, void* out, int64_t out_token_stride,
+                     int64_t out_head_stride, float* lse, void* stream);
+
 /* ---- plan inspection (host only; used by tests and tools) ---- */
 
 /* Device workspace bytes the plan needs. */
@@ -614,7 +795,9 @@ void mla_planner_constants(int* tile_tokens, int* segment_overhead_tiles, int* m
  * (the kernel then stopped early and its outputs are not valid); failing
  * that, the first out-of-range lookup of a block-table builder (0x30x) or of
  * the RoPE / cache-write step (0x60x), or a malformed expert offset (0x701) or
- * a timed-out wait (0x71x, 0x72x, 0x73x) of a product.  Reading it
+ * a timed-out wait (0x71x, 0x72x, 0x73x) of a product, or malformed offsets (0xA0x)
+ * or a timed-out wait (0xA1x) of mla_prefill, or an out-of-range lookup of
+ * mla_rope (0x801) or mla_cache_gather (0x90x).  Reading it
  * synchronises with the device; reset != 0 clears it.  Errors: MLA_ERR_ARG,
  * MLA_ERR_CUDA. */
 int mla_decode_device_error(int* code, int reset);

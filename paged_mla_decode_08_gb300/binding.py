@@ -1,8 +1,8 @@
 """Thin ctypes binding of libmladecode.so (the C ABI in include/mla_decode.h).
 
 Argument marshalling only: every step of the decode runs in the library's
-CUDA kernels.  (The FP8 layer operators' tensors are checked and passed on by the
-native module _mla_calls instead of ctypes.)  Torch tensors are accepted for convenience and are only used
+CUDA kernels.  (The tensors of the FP8 layer's and the prompt's operators are
+checked and passed on by the native module _mla_calls instead of ctypes.)  Torch tensors are accepted for convenience and are only used
 for their device pointers and the current CUDA stream.  There is no fallback:
 if the library is missing, loading fails loudly.
 """
@@ -66,6 +66,18 @@ SIGNATURES = {
     "mla_gemm_fp8_in_form": (_c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp,
                                       _c_int, _i64, _c_int, _c_int, _c_int, _vp]),
     "mla_gemm_fp8_form": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _i64, _c_int, _vp, _vp, _vp, _vp]),
+    "mla_rope_table": (_c_int, [_vp, _i64, _i64, _c_int, ctypes.c_double, _c_int, ctypes.c_double, _i64, ctypes.c_double,
+                                ctypes.c_double, ctypes.c_double, _vp]),
+    "mla_rope": (_c_int, [_vp, _i64, _i64, _vp, _i64, _c_int, _c_int, _c_int, _vp, _vp, _i64, _c_int, _vp, _i64, _i64, _vp,
+                          _i64, _vp]),
+    "mla_cache_gather": (_c_int, [_vp, _c_int, _i64, _c_int, _vp, _i64, _vp, _vp, _c_int, _c_int, ctypes.c_float, _vp,
+                                  _c_int, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "mla_prefill": (_c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp,
+                             _c_int, _c_int, _c_int, _c_int, _c_int, ctypes.c_float, _vp, _i64, _i64, _vp, _vp, _c_size,
+                             _vp]),
+    "mla_prefill_workspace_bytes": (_c_int, [_c_int, _c_int, _c_int, _c_int, ctypes.POINTER(_c_size)]),
+    "mla_merge_states": (_c_int, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _c_int, _c_int, _c_int, _vp, _i64, _i64, _vp,
+                                  _vp]),
     "mla_plan_workspace_bytes": (_c_size, [_vp]),
     "mla_plan_num_workers": (_c_int, [_vp]),
     "mla_plan_num_segments": (_c_int, [_vp]),
@@ -350,8 +362,8 @@ _calls = None
 
 
 def _load_calls():
-    """The module that checks tensors and makes the FP8 layer's calls (built by
-    build.build()); a Python check of their up to seven tensors takes longer than
+    """The module that checks tensors and makes the FP8 layer's and the prompt's calls
+    (built by build.build()); a Python check of their up to seven tensors takes longer than
     the smallest kernels."""
     global _calls
     if not os.path.exists(CALLS):
@@ -395,6 +407,73 @@ def mla_grouped_gemm_fp8(a, a_scales, w, w_scales, expert_offsets, out, out_dtyp
     [E, ceil(N / 128), ceil(K / 128)]."""
     (_calls or _load_calls()).grouped_gemm_fp8(a, a_scales, w, w_scales, expert_offsets, out, out_dtype,
                                                None if stream is None else _stream(stream))
+
+
+MLA_ROPE_PLAIN = 0
+MLA_ROPE_LINEAR = 1
+MLA_ROPE_YARN = 2
+MLA_ROPE_MAX_DIM = 512
+MLA_MERGE_MAX_DIM = 2048
+MLA_NOPE_DIM = 128
+MLA_V_DIM = 128
+
+
+def mla_rope_table(table, first_position: int = 0, base: float = 10000.0, scaling: int = MLA_ROPE_PLAIN,
+                   factor: float = 1.0, original_max_position: int = 4096, beta_fast: float = 32.0,
+                   beta_slow: float = 1.0, magnitude: float = 1.0, stream=None):
+    """Fill ``table`` (fp32 CUDA [positions, rotary_dim], contiguous) with the
+    cosines, then the sines, of positions first_position, first_position + 1, ...:
+    the cos_sin_cache of ``mla_rope`` and ``mla_rope_quantize_cache_write``."""
+    import torch
+    if table.dim() != 2 or table.dtype != torch.float32 or not table.is_contiguous() or not table.is_cuda:
+        raise MlaError(MLA_ERR_ARG, "table must be a contiguous fp32 CUDA tensor [positions, rotary_dim]")
+    if table.device.index != torch.cuda.current_device():
+        raise MlaError(MLA_ERR_ARG, "table is on another device than the current one")
+    rows, dim = table.shape
+    _check(load().mla_rope_table(_ptr(table), int(first_position), int(rows), int(dim), float(base), int(scaling),
+                                 float(factor), int(original_max_position), float(beta_fast), float(beta_slow),
+                                 float(magnitude), _stream(stream)))
+
+
+def mla_rope(q, k, positions, cos_sin_cache, is_neox: bool, q_out, k_out, stream=None):
+    """Rotate the rotary columns ``q`` [T, H, R] (a slice of wider heads, say) into
+    ``q_out`` and the shared key's ``k`` [T, R] into ``k_out`` (in place: pass the
+    same tensors; None: no query, or no key), at ``positions`` (int64 [T]) of
+    ``cos_sin_cache`` (fp32 [P, R])."""
+    (_calls or _load_calls()).rope(q, k, positions, cos_sin_cache, is_neox, q_out, k_out,
+                                   None if stream is None else _stream(stream))
+
+
+def mla_cache_gather(kv_pages, kv_dtype: int, block_table, starts, cu_seqlens, k_scale: float, latent,
+                     latent_dtype: int, latent_scales, k_pe, stream=None):
+    """Cache tokens starts[b] .. (None = 0) of each request, as many as
+    cu_seqlens[b + 1] - cu_seqlens[b], into rows cu_seqlens[b] .. of ``latent``
+    [T, 512] (bf16, or e4m3 with ``latent_scales`` [4, T]) and ``k_pe`` [T, 64]."""
+    (_calls or _load_calls()).cache_gather(kv_pages, kv_dtype, block_table, starts, cu_seqlens, k_scale, latent,
+                                           latent_dtype, latent_scales, k_pe, None if stream is None else _stream(stream))
+
+
+def mla_prefill_workspace_bytes(num_tokens_q: int, num_tokens_k: int, batch: int, num_heads: int) -> int:
+    """Device workspace that ``mla_prefill`` needs for these sizes (0: none)."""
+    need = _c_size()
+    _check(load().mla_prefill_workspace_bytes(num_tokens_q, num_tokens_k, batch, num_heads, ctypes.byref(need)))
+    return need.value
+
+
+def mla_prefill(q_nope, q_pe, k_nope, k_pe, v, cu_seqlens_q, cu_seqlens_k, causal: bool, scale: float, out, lse,
+                workspace=None, stream=None):
+    """Expanded attention over a ragged batch: queries ``q_nope`` [Tq, H, 128] and
+    ``q_pe`` [Tq, H, 64], keys ``k_nope`` [Tk, H, 128] and the heads' shared ``k_pe``
+    [Tk, 64], values ``v`` [Tk, H, 128], into ``out`` [Tq, H, 128] and ``lse`` [Tq, H]."""
+    (_calls or _load_calls()).prefill(q_nope, q_pe, k_nope, k_pe, v, cu_seqlens_q, cu_seqlens_k, causal, scale, out, lse,
+                                      workspace, None if stream is None else _stream(stream))
+
+
+def mla_merge_states(out_a, lse_a, out_b, lse_b, out, lse, stream=None):
+    """Merge two partial attention results of the same rows ([T, H, D] with [T, H]
+    lse) into ``out`` and ``lse`` (which may be either part's own tensors)."""
+    (_calls or _load_calls()).merge_states(out_a, lse_a, out_b, lse_b, out, lse,
+                                           None if stream is None else _stream(stream))
 
 
 def mla_planner_constants():

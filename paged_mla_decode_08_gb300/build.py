@@ -32,7 +32,8 @@ LIB = os.path.join(LIBDIR, "libmladecode.so")
 CALLS = os.path.join(LIBDIR, "_mla_calls.so")
 
 CUDA_SOURCES = ["mla_abi.cu", "mla_sm103.cu", "mla_combine.cu", "mla_noalloc.cu", "mla_block_table.cu",
-                "mla_plan_device.cu", "mla_kv_write.cu", "mla_norm_quant.cu", "mla_gemm_fp8.cu"]
+                "mla_plan_device.cu", "mla_kv_write.cu", "mla_norm_quant.cu", "mla_gemm_fp8.cu",
+                "mla_prefill.cu", "mla_prompt_rows.cu"]
 CXX_SOURCES = ["mla_plan.cpp"]
 CALLS_SOURCE = "mla_torch_calls.cpp"  # built against this machine's Python and torch
 HEADERS = ["mla_internal.h", "per_device.h", "sm103_ptx.cuh"]

@@ -51,6 +51,21 @@ cudaError_t launch_gemm_fp8(const void* act, const float* a_scales, int64_t lda,
 void gemm_fp8_form(bool grouped, int m, int n, int k, int experts, const void* out, bool fp32, int64_t ldo, Device dev,
                    const int32_t* clusters, int* tile_tokens, int* k_parts, int* copied);
 cudaError_t gemm_read_error(int* code, bool reset);
+cudaError_t launch_rope_table(float* table, int64_t first, int64_t positions, int half, const uint64_t* turns,
+                              float magnitude, cudaStream_t stream);
+cudaError_t launch_rope(HeadRows q, HeadRows k, HeadRows q_out, HeadRows k_out, const int64_t* positions,
+                        const float* table, int64_t max_position, int tokens, int heads, int half, bool neox,
+                        cudaStream_t stream);
+cudaError_t launch_cache_gather(const void* kv, bool kv_e4m3, int64_t num_pages, int page_size, const int32_t* block_table,
+                                int64_t bt_stride, const int32_t* starts, const int32_t* cu, int batch, int tokens,
+                                float k_scale, void* latent, bool latent_e4m3, int64_t latent_stride, float* scales,
+                                int64_t scale_stride, void* k_pe, int64_t k_pe_stride, cudaStream_t stream);
+cudaError_t launch_merge_states(HeadRows x, const float* lse_x, HeadRows y, const float* lse_y, HeadRows out, float* lse,
+                                int tokens, int heads, int dim, cudaStream_t stream);
+cudaError_t prompt_rows_read_error(int* code, bool reset);
+cudaError_t launch_prefill(const PrefillCall& p, Device dev, cudaStream_t stream);
+size_t prefill_workspace(int num_tokens_q, int num_tokens_k, int batch, int num_heads, Device dev);
+cudaError_t prefill_read_error(int* code, bool reset);
 }  // namespace mla
 
 namespace {
@@ -449,15 +464,19 @@ const char* mla_decode_last_error_string(void) { return g_last_error.c_str(); }
 
 int mla_decode_device_error(int* code, int reset) {
   if (!code) return fail(MLA_ERR_ARG, "code is NULL");
-  int bt_code = 0, kw_code = 0, gm_code = 0;
+  int bt_code = 0, kw_code = 0, gm_code = 0, pf_code = 0, pr_code = 0;
   cudaError_t e = mla::sm103_read_error(code, reset != 0);
   if (e == cudaSuccess) e = mla::block_table_read_error(&bt_code, reset != 0);
   if (e == cudaSuccess) e = mla::kv_write_read_error(&kw_code, reset != 0);
   if (e == cudaSuccess) e = mla::gemm_read_error(&gm_code, reset != 0);
+  if (e == cudaSuccess) e = mla::prefill_read_error(&pf_code, reset != 0);
+  if (e == cudaSuccess) e = mla::prompt_rows_read_error(&pr_code, reset != 0);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("reading the kernel error word: ") + cudaGetErrorString(e));
   if (*code == 0) *code = bt_code;
   if (*code == 0) *code = kw_code;
   if (*code == 0) *code = gm_code;
+  if (*code == 0) *code = pf_code;
+  if (*code == 0) *code = pr_code;
   return ok();
 }
 
@@ -709,6 +728,243 @@ int mla_gemm_fp8_form(int num_tokens, int n, int k, int num_experts, int grouped
   }
   mla::gemm_fp8_form(grouped != 0, num_tokens, n, k, num_experts, out, out_dtype == MLA_OUT_FP32, ldo, dev, clusters,
                      tile_tokens, k_parts, copied_results);
+  return ok();
+}
+
+int mla_rope_table(float* table, int64_t first_position, int64_t num_positions, int rotary_dim, double base,
+                   int scaling, double factor, int64_t original_max_position, double beta_fast, double beta_slow,
+                   double magnitude, void* stream) {
+  if (num_positions < 0 || first_position < 0 || first_position > ((int64_t)1 << 31) ||
+      num_positions > ((int64_t)1 << 31) - first_position)
+    return fail(MLA_ERR_ARG, "positions must be within [0, 2^31)");
+  if (rotary_dim < 2 || rotary_dim > MLA_ROPE_MAX_DIM || rotary_dim % 2 != 0)
+    return fail(MLA_ERR_ARG, "rotary_dim must be even and in [2, MLA_ROPE_MAX_DIM]");
+  if (!(base > 1.0) || !std::isfinite(base)) return fail(MLA_ERR_ARG, "base must be finite and > 1");
+  if (scaling != MLA_ROPE_PLAIN && scaling != MLA_ROPE_LINEAR && scaling != MLA_ROPE_YARN)
+    return fail(MLA_ERR_ARG, "scaling must be MLA_ROPE_PLAIN, MLA_ROPE_LINEAR or MLA_ROPE_YARN");
+  if (scaling != MLA_ROPE_PLAIN && (!(factor > 0.0) || !std::isfinite(factor)))
+    return fail(MLA_ERR_ARG, "factor must be finite and > 0");
+  if (scaling == MLA_ROPE_YARN &&
+      (original_max_position < 1 || !(beta_slow > 0.0) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast)))
+    return fail(MLA_ERR_ARG, "YaRN needs original_max_position >= 1 and finite beta_fast > beta_slow > 0");
+  if (!std::isfinite(magnitude) || !std::isfinite((float)magnitude)) return fail(MLA_ERR_ARG, "magnitude must be finite");
+  const int half = rotary_dim / 2;
+  if (num_positions * half > (int64_t)INT32_MAX * 256) return fail(MLA_ERR_ARG, "too many positions for one launch");
+  if (num_positions == 0) return ok();
+  if (!table || !aligned(table, 4)) return fail(MLA_ERR_ARG, "table must be a device pointer aligned to its elements");
+  int rc = check_device(nullptr);
+  if (rc != MLA_OK) return rc;
+  const double two_pi = 6.283185307179586476925;
+  double lo = 0.0, hi = 0.0;
+  if (scaling == MLA_ROPE_YARN) {
+    auto pair_that_turns = [&](double beta) {
+      return rotary_dim * std::log((double)original_max_position / (beta * two_pi)) / (2.0 * std::log(base));
+    };
+    lo = std::max(std::floor(pair_that_turns(beta_fast)), 0.0);
+    hi = std::min(std::ceil(pair_that_turns(beta_slow)), rotary_dim - 1.0);
+    if (hi == lo) hi += 0.001;
+  }
+  uint64_t turns[MLA_ROPE_MAX_DIM / 2];
+  for (int i = 0; i < half; ++i) {
+    double w = std::pow(base, -2.0 * i / rotary_dim);
+    if (scaling == MLA_ROPE_LINEAR) w /= factor;
+    if (scaling == MLA_ROPE_YARN) {
+      const double g = std::min(std::max((i - lo) / (hi - lo), 0.0), 1.0);
+      w = w / factor * g + w * (1.0 - g);
+    }
+    const double t = w / two_pi;  // turns of a position; whole ones do not matter
+    turns[i] = static_cast<uint64_t>(std::ldexp(t - std::floor(t), 64));
+  }
+  cudaError_t e = mla::launch_rope_table(table, first_position, num_positions, half, turns, (float)magnitude,
+                                         static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("rope table launch: ") + cudaGetErrorString(e));
+  return ok();
+}
+
+int mla_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
+             int num_tokens, int num_heads, int rotary_dim, const int64_t* positions, const float* cos_sin_cache,
+             int64_t max_position, int is_neox, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+             void* k_out, int64_t k_out_stride, void* stream) {
+  if (num_tokens < 0 || num_heads < 0 || num_heads > (1 << 16))
+    return fail(MLA_ERR_ARG, "num_tokens must be >= 0, num_heads in [0, 65536]");
+  if (rotary_dim < 2 || rotary_dim > MLA_ROPE_MAX_DIM || rotary_dim % 2 != 0)
+    return fail(MLA_ERR_ARG, "rotary_dim must be even and in [2, MLA_ROPE_MAX_DIM]");
+  if (max_position < 1) return fail(MLA_ERR_ARG, "max_position must be >= 1");
+  if (num_tokens == 0) return ok();
+  if (num_heads == 0 && !k) return fail(MLA_ERR_ARG, "neither a query nor a key is given");
+  if (!positions || !cos_sin_cache || (num_heads > 0 && (!q || !q_out)) || (!k != !k_out))
+    return fail(MLA_ERR_ARG, "a required device pointer is NULL");
+  if (num_heads > 0 && (q_token_stride < rotary_dim || q_out_token_stride < rotary_dim ||
+                        (num_heads > 1 && (q_head_stride < rotary_dim || q_out_head_stride < rotary_dim))))
+    return fail(MLA_ERR_ARG, "the query's strides must be >= rotary_dim");
+  if (k && (k_stride < rotary_dim || k_out_stride < rotary_dim)) return fail(MLA_ERR_ARG, "the key's strides must be >= rotary_dim");
+  if (!aligned(positions, 8) || !aligned(cos_sin_cache, 4) || !aligned(q, 2) || !aligned(q_out, 2) || !aligned(k, 2) ||
+      !aligned(k_out, 2))
+    return fail(MLA_ERR_ARG, "arrays must be aligned to their elements");
+  int rc = check_device(nullptr);
+  if (rc != MLA_OK) return rc;
+  if (num_heads == 0) q = q_out = nullptr;
+  if (num_heads <= 1) q_head_stride = q_out_head_stride = 0;
+  cudaError_t e = mla::launch_rope({q, q_token_stride, q_head_stride}, {k, k_stride, 0},
+                                   {q_out, q_out_token_stride, q_out_head_stride}, {k_out, k_out_stride, 0}, positions,
+                                   cos_sin_cache, max_position, num_tokens, num_heads, rotary_dim / 2, is_neox != 0,
+                                   static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("rope launch: ") + cudaGetErrorString(e));
+  return ok();
+}
+
+int mla_cache_gather(const void* kv_pages, int kv_dtype, int64_t num_pages, int page_size, const int32_t* block_table,
+                     int64_t bt_stride, const int32_t* starts, const int32_t* cu_seqlens, int batch, int num_tokens,
+                     float k_scale, void* latent, int latent_dtype, int64_t latent_stride, float* latent_scales,
+                     int64_t scale_stride, void* k_pe, int64_t k_pe_stride, void* stream) {
+  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_E4M3) return fail(MLA_ERR_ARG, "kv_dtype must be MLA_KV_BF16 or MLA_KV_E4M3");
+  if (latent_dtype != MLA_OUT_BF16 && latent_dtype != MLA_OUT_E4M3)
+    return fail(MLA_ERR_ARG, "latent_dtype must be MLA_OUT_BF16 or MLA_OUT_E4M3");
+  if (page_size != 32 && page_size != 64) return fail(MLA_ERR_ARG, "page_size must be 32 or 64");
+  if (num_pages <= 0 || num_pages > INT32_MAX / page_size)
+    return fail(MLA_ERR_ARG, "num_pages must be > 0 and num_pages * page_size < 2^31");
+  if (batch < 1 || batch > (1 << 24)) return fail(MLA_ERR_ARG, "batch must be in [1, 2^24]");
+  if (bt_stride < 1 || bt_stride > INT32_MAX) return fail(MLA_ERR_ARG, "bt_stride must be in [1, 2^31)");
+  if (num_tokens < 0) return fail(MLA_ERR_ARG, "num_tokens must be >= 0");
+  if (kv_dtype == MLA_KV_E4M3 && (!(k_scale > 0.f) || !std::isfinite(k_scale)))
+    return fail(MLA_ERR_ARG, "k_scale must be finite and > 0");
+  if (num_tokens == 0) return ok();
+  const bool e4m3 = latent_dtype == MLA_OUT_E4M3;
+  if (!kv_pages || !block_table || !cu_seqlens || !latent || !k_pe || (e4m3 && !latent_scales))
+    return fail(MLA_ERR_ARG, "a required device pointer is NULL");
+  if (latent_stride < MLA_KV_LORA_RANK || latent_stride % (e4m3 ? 16 : 8) != 0 || k_pe_stride < MLA_ROPE_DIM ||
+      k_pe_stride % 8 != 0)
+    return fail(MLA_ERR_ARG, "row pitches must be multiples of 16 bytes and cover a row");
+  if (e4m3 && scale_stride < num_tokens) return fail(MLA_ERR_ARG, "scale_stride must be >= num_tokens");
+  if (!aligned(kv_pages, 16) || !aligned(latent, 16) || !aligned(k_pe, 16) || !aligned(block_table, 4) ||
+      !aligned(starts, 4) || !aligned(cu_seqlens, 4) || !aligned(latent_scales, 4))
+    return fail(MLA_ERR_ARG, "rows must be 16-byte aligned (offsets and scales 4)");
+  int rc = check_device(nullptr);
+  if (rc != MLA_OK) return rc;
+  cudaError_t e = mla::launch_cache_gather(kv_pages, kv_dtype == MLA_KV_E4M3, num_pages, page_size, block_table, bt_stride,
+                                           starts, cu_seqlens, batch, num_tokens, kv_dtype == MLA_KV_E4M3 ? k_scale : 1.f,
+                                           latent, e4m3, latent_stride, latent_scales, scale_stride, k_pe, k_pe_stride,
+                                           static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("gather launch: ") + cudaGetErrorString(e));
+  return ok();
+}
+
+// The sizes of mla_prefill.
+static int check_prefill_sizes(int num_tokens_q, int num_tokens_k, int batch, int num_heads) {
+  if (num_tokens_q < 0 || num_tokens_k < 0) return fail(MLA_ERR_ARG, "token counts must be >= 0");
+  // rows are numbered in 32 bits, to the end of an item that begins with the last one
+  if (num_tokens_q > INT32_MAX - 1024 || num_tokens_k > INT32_MAX - 1024)
+    return fail(MLA_ERR_ARG, "token counts must be <= 2^31 - 1025");
+  if (batch < 1 || batch > (1 << 24)) return fail(MLA_ERR_ARG, "batch must be in [1, 2^24]");
+  if (num_heads < 1 || num_heads > (1 << 16)) return fail(MLA_ERR_ARG, "num_heads must be in [1, 65536]");
+  if ((int64_t)mla::prefill_items(num_tokens_q, batch) * num_heads > INT32_MAX)
+    return fail(MLA_ERR_ARG, "too many tokens x heads for one launch");
+  return MLA_OK;
+}
+
+int mla_prefill_workspace_bytes(int num_tokens_q, int num_tokens_k, int batch, int num_heads, size_t* bytes_out) {
+  if (!bytes_out) return fail(MLA_ERR_ARG, "bytes_out is NULL");
+  int rc = check_prefill_sizes(num_tokens_q, num_tokens_k, batch, num_heads);
+  if (rc != MLA_OK) return rc;
+  mla::Device dev{};
+  rc = check_device(&dev.sms, &dev.id);
+  if (rc != MLA_OK) return rc;
+  *bytes_out = mla::prefill_workspace(num_tokens_q, num_tokens_k, batch, num_heads, dev);
+  return ok();
+}
+
+int mla_prefill(const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_head_stride, const void* q_pe,
+                int64_t q_pe_token_stride, int64_t q_pe_head_stride, const void* k_nope, int64_t k_nope_token_stride,
+                int64_t k_nope_head_stride, const void* k_pe, int64_t k_pe_stride, const void* v,
+                int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_seqlens_q,
+                const int32_t* cu_seqlens_k, int batch, int num_tokens_q, int num_tokens_k, int num_heads, int causal,
+                float scale, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse, void* workspace,
+                size_t workspace_bytes, void* stream) {
+  int rc = check_prefill_sizes(num_tokens_q, num_tokens_k, batch, num_heads);
+  if (rc != MLA_OK) return rc;
+  // (the scale in units of log2 as well)
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.5f) || !std::isfinite(16.f / scale))
+    return fail(MLA_ERR_ARG, "scale must be finite and > 0");
+  if (num_tokens_q == 0) return ok();
+  if (!q_nope || !q_pe || !cu_seqlens_q || !cu_seqlens_k || !out || !lse || (num_tokens_k > 0 && (!k_nope || !k_pe || !v)))
+    return fail(MLA_ERR_ARG, "a required device pointer is NULL");
+  mla::PrefillCall p{};
+  p.q_nope = {q_nope, q_nope_token_stride, q_nope_head_stride};
+  p.q_pe = {q_pe, q_pe_token_stride, q_pe_head_stride};
+  p.k_nope = {k_nope, k_nope_token_stride, k_nope_head_stride};
+  p.v = {v, v_token_stride, v_head_stride};
+  p.k_pe = {k_pe, k_pe_stride, k_pe_stride};
+  p.out = {out, out_token_stride, out_head_stride};
+  struct Rule {
+    mla::HeadRows* rows;
+    int width;
+    bool used;
+  };
+  const Rule rules[] = {{&p.q_nope, 128, true},          {&p.q_pe, 64, true},          {&p.out, 128, true},
+                        {&p.k_nope, 128, num_tokens_k > 0}, {&p.k_pe, 64, num_tokens_k > 0}, {&p.v, 128, num_tokens_k > 0}};
+  for (const Rule& r : rules) {
+    if (!r.used) continue;
+    if (num_heads == 1) r.rows->head_stride = r.rows->token_stride;
+    // the copy engine's strides are 40 bits
+    for (int64_t s : {r.rows->token_stride, r.rows->head_stride})
+      if (s < r.width || s % 8 != 0 || s >= ((int64_t)1 << 39))
+        return fail(MLA_ERR_ARG, "strides must be multiples of 8, at least a head's width and < 2^39");
+    if (!aligned(r.rows->p, 16)) return fail(MLA_ERR_ARG, "arrays must be 16-byte aligned");
+  }
+  if (!aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4) || !aligned(lse, 4))
+    return fail(MLA_ERR_ARG, "offsets and lse must be 4-byte aligned");
+  mla::Device dev{};
+  rc = check_device(&dev.sms, &dev.id);
+  if (rc != MLA_OK) return rc;
+  const size_t need = mla::prefill_workspace(num_tokens_q, num_tokens_k, batch, num_heads, dev);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need)
+      return fail(MLA_ERR_WORKSPACE, "workspace is smaller than mla_prefill_workspace_bytes");
+    if (!aligned(workspace, 256)) return fail(MLA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  }
+  p.lse = lse;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.batch = batch;
+  p.num_heads = num_heads;
+  p.num_tokens_q = num_tokens_q;
+  p.num_tokens_k = num_tokens_k;
+  p.causal = causal != 0;
+  p.scale = scale;
+  p.workspace = workspace;
+  cudaError_t e = mla::launch_prefill(p, dev, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported)
+    return fail(MLA_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled unavailable or rejected the operands");
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("prefill launch: ") + cudaGetErrorString(e));
+  return ok();
+}
+
+int mla_merge_states(const void* out_a, int64_t a_token_stride, int64_t a_head_stride, const float* lse_a,
+                     const void* out_b, int64_t b_token_stride, int64_t b_head_stride, const float* lse_b,
+                     int num_tokens, int num_heads, int dim, void* out, int64_t out_token_stride,
+                     int64_t out_head_stride, float* lse, void* stream) {
+  if (num_tokens < 0 || num_heads < 1 || num_heads > (1 << 16))
+    return fail(MLA_ERR_ARG, "num_tokens must be >= 0, num_heads in [1, 65536]");
+  if (dim < 8 || dim > MLA_MERGE_MAX_DIM || dim % 8 != 0)
+    return fail(MLA_ERR_ARG, "dim must be a multiple of 8 in [8, MLA_MERGE_MAX_DIM]");
+  if ((int64_t)num_tokens * num_heads > INT32_MAX) return fail(MLA_ERR_ARG, "num_tokens * num_heads must be < 2^31");
+  if (num_tokens == 0) return ok();
+  if (!out_a || !out_b || !out || !lse_a || !lse_b || !lse) return fail(MLA_ERR_ARG, "a required device pointer is NULL");
+  for (int64_t s : {a_token_stride, b_token_stride, out_token_stride})
+    if (s < dim || s % 8 != 0) return fail(MLA_ERR_ARG, "strides must be multiples of 8 and >= dim");
+  if (num_heads > 1)
+    for (int64_t s : {a_head_stride, b_head_stride, out_head_stride})
+      if (s < dim || s % 8 != 0) return fail(MLA_ERR_ARG, "strides must be multiples of 8 and >= dim");
+  if (!aligned(out_a, 16) || !aligned(out_b, 16) || !aligned(out, 16) || !aligned(lse_a, 4) || !aligned(lse_b, 4) ||
+      !aligned(lse, 4))
+    return fail(MLA_ERR_ARG, "out arrays must be 16-byte aligned (lse 4)");
+  int rc = check_device(nullptr);
+  if (rc != MLA_OK) return rc;
+  cudaError_t e = mla::launch_merge_states({out_a, a_token_stride, a_head_stride}, lse_a,
+                                           {out_b, b_token_stride, b_head_stride}, lse_b,
+                                           {out, out_token_stride, out_head_stride}, lse, num_tokens, num_heads, dim,
+                                           static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("merge launch: ") + cudaGetErrorString(e));
   return ok();
 }
 
