@@ -857,7 +857,7 @@ static int check_prefill_sizes(int num_tokens_q, int num_tokens_k, int batch, in
     return fail(MLA_ERR_ARG, "token counts must be <= 2^31 - 1025");
   if (batch < 1 || batch > (1 << 24)) return fail(MLA_ERR_ARG, "batch must be in [1, 2^24]");
   if (num_heads < 1 || num_heads > (1 << 16)) return fail(MLA_ERR_ARG, "num_heads must be in [1, 65536]");
-  if ((int64_t)mla::prefill_items(num_tokens_q, batch) * num_heads > INT32_MAX)
+  if ((int64_t)mla::prefill_items(num_tokens_q, batch) * num_heads > INT32_MAX / 2)
     return fail(MLA_ERR_ARG, "too many tokens x heads for one launch");
   return MLA_OK;
 }

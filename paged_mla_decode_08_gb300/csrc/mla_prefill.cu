@@ -5,11 +5,12 @@
 //
 //   s_j = scale (q_nope . k_nope_j + q_pe . k_pe_j),   out = softmax(s) V,   lse = ln sum e^s
 //
-// One CTA per item: 256 query rows of one request and head, as two tiles of 128
-// rows whose products and softmax alternate.  Per 128 keys and tile
-//   S = Q K^T    (M = 128, N = 128, K = 192)  operands in shared memory -> TMEM
+// One item: 512 query rows of one request and head on a pair of CTAs
+// (cta_group::2), or 256 on one CTA; two tiles whose products and softmax
+// alternate, each with 128 rows in every CTA.  A step is 128 keys (64 on one CTA):
+//   S = Q K^T    (M = 128, N = 128, K = 192 a CTA)  operands in shared memory -> TMEM
 //   P = 2^(c S - m) in registers, bf16, written over S
-//   O += P V     (M = 128, N = 128, K = 128)  P from TMEM, V from shared memory
+//   O += P V     (M = 128, N = 128, K = 128 a CTA)  P from TMEM, V from shared memory
 // A thread of the softmax owns one query row, so its maximum and sum need no
 // exchange.  While one tile's softmax runs, the tensor core has the other
 // tile's products.  The running maximum only moves when a score exceeds it by
@@ -17,22 +18,28 @@
 // rescales its rows of O, which no product uses at that time: the products of a
 // tile run in order, so S(j) in TMEM means that P V (j - 1) is done.
 //
-// P enters the second product in bf16 (half a step: 2^-9 of each weight, of
+// Why pairs.  Q takes 96 KB of a CTA's shared memory.  One CTA reads 80 KB of keys
+// and values a 128 keys, twice what the rest of its memory can hold ahead, and its
+// products read 128 bytes of shared memory a cycle, all there is.  A pair's CTAs hold
+// half of the keys and half of the value columns each: half the loads, half the reads
+// of B, and three steps ahead.  19 heads, 2048 rows over 8192 keys: 125 us, 1628
+// TFLOP/s (one CTA per 256 rows: 220 us).
+//
+// P enters the second product in bf16 (half a step: 2^-8 of each weight at most, of
 // random sign, below the rounding of the bf16 output); row sums and lse use the
 // unrounded values.
 //
 // TMEM (512 columns): S / P of both tiles [0, 256), O of both tiles [256, 512).
-// Shared memory: Q (2 x 48 KB) and a ring of eight 16 KB slots, each 128 keys x
-// 64 columns in the 128-byte swizzle: a key tile takes three (two of k_nope, one
-// of k_pe), a value tile two.
+// Shared memory: Q (2 x 48 KB) and a ring of three steps of 40 KB: 64 keys x 192
+// columns, and 16 KB of values, in boxes of 64 columns in the 128-byte swizzle.
 //
 // Masked places.  Scores past a row's last key are replaced by -inf, so keys
 // there may hold anything.  Values there are multiplied by P = 0, which leaves
-// NaN of an infinity or a NaN; so two warps look through the value tiles that
-// some row does not see whole, and put zeros in the place of what is not finite.
+// NaN of an infinity or a NaN; so a warp looks through the value tiles that
+// some row does not see whole, and puts zeros in the place of what is not finite.
 // The rows that do see such a value get it in the epilogue.
 //
-// Warps: 0 TMA, 1 MMA, 2-3 value scan, 4-7 softmax of the first tile, 8-11 of
+// Warps: 0 TMA, 1 MMA, 2 value scan, 4-7 softmax of the first tile, 8-11 of
 // the second.  Waits are bounded: on timeout the error word is set, every role
 // stops, copies and products in flight are awaited, TMEM is freed.
 #include <cuda.h>
@@ -55,30 +62,41 @@ using namespace mla::ptx;
 
 __device__ int g_prefill_error;
 
-constexpr int kRows = 128;             // query rows of a tile
-constexpr int kItemRows = 2 * kRows;   // ... and of an item
-constexpr int kKeys = 128;             // keys of a step
-constexpr int kSlot = kKeys * 128;     // bytes of a ring slot, and of a Q box
-constexpr int kSlots = 8;
-constexpr int kKSlots = 3, kVSlots = 2, kStepSlots = kKSlots + kVSlots;
-constexpr int kQTile = 3 * kSlot;
+constexpr int kRows = 128;               // query rows of a tile in a CTA
+constexpr int kStages = 3;
+constexpr int kBox = 64 * 128;           // 64 keys x 64 columns
+constexpr int kQTile = 3 * 2 * kBox;     // 128 rows x 192 columns
+constexpr int kKBytes = 3 * kBox;        // 64 keys x 192 columns of keys
+constexpr int kVBytes = 2 * kBox;        // 64 keys x 128 or 128 keys x 64 columns of values
+constexpr int kStageBytes = kKBytes + kVBytes;
 constexpr int kOffQ = 0;
 constexpr int kOffRing = 2 * kQTile;
-constexpr int kOffBars = kOffRing + kSlots * kSlot;
+constexpr int kOffBars = kOffRing + kStages * kStageBytes;
 constexpr int kThreads = 384;
 constexpr int kRegsLoad = 56, kRegsSoftmax = 224;  // 128 x 56 + 256 x 224 = 384 x 168, the launch's registers
 constexpr float kRescaleLog2 = 8.0f;
 constexpr long long kTimeoutCycles = 2000000000LL;
 
+// kCtas: CTAs that share an item's keys
+template <int kCtas>
+struct Form {
+  static constexpr int kKeys = 64 * kCtas;             // keys of a step
+  static constexpr int kTileRows = kRows * kCtas;      // query rows of a tile
+  static constexpr int kItemRows = 2 * kTileRows;
+};
+
 enum Bar : int {
-  B_Q = 0,                    // [tile]
-  B_FULL = B_Q + 2,           // [slot]
-  B_EMPTY = B_FULL + kSlots,  // [slot]
-  B_S = B_EMPTY + kSlots,     // [tile] scores are in TMEM
-  B_P = B_S + 2,              // [tile] weights are in TMEM, O is rescaled
-  B_O = B_P + 2,              // [tile] the tile's products are done
-  B_RAW = B_O + 2,            // [2 w + step parity] half w of a value tile landed, for the scan
-  B_FIN = B_RAW + 4,          // every product is done
+  B_Q = 0,                        // [tile] Q landed (the leader's barrier)
+  B_QE = B_Q + 2,                 // [tile] Q is read
+  B_KF = B_QE + 2,                // [stage] keys landed (the leader's)
+  B_KE = B_KF + kStages,          // [stage] keys are read
+  B_VF = B_KE + kStages,          // [stage] values landed and, where masked, looked through (the leader's)
+  B_VE = B_VF + kStages,          // [stage] values are read
+  B_RAW = B_VE + kStages,         // [scan % 3] values landed, for the scan
+  B_S = B_RAW + kStages,          // [tile] scores are in TMEM
+  B_P = B_S + 2,                  // [tile] weights are in TMEM, O is rescaled (the leader's)
+  B_O = B_P + 2,                  // [tile] the tile's products are done
+  B_FIN = B_O + 2,                // every product is done
   B_COUNT
 };
 constexpr int kOffTmem = kOffBars + B_COUNT * 8;
@@ -108,34 +126,43 @@ struct Item {
   int head, row0;      // first query row of the item within the request
 };
 
-// What one tile (of 128 rows) of an item computes.
+// What a CTA does of one tile of an item.
 struct Tile {
-  int row0, rows;  // within the request
-  int steps;       // key tiles with a visible key
-  int masked;      // first of them that some row does not see whole
+  int row0, rows;  // this CTA's, within the request
+  int steps;       // of the tile: steps with a key that a row of it sees
+  int masked;      // first step that some row of this CTA does not see whole
 };
 
 __device__ __forceinline__ int visible(const Item& it, int causal, int row) {
   return causal ? max(0, min(it.lk, it.lk - it.lq + 1 + row)) : it.lk;
 }
-__device__ __forceinline__ Tile tile_of(const Item& it, int causal, int t) {
+template <int kCtas>
+__device__ __forceinline__ Tile tile_of(const Item& it, int causal, int t, int rank) {
+  using F = Form<kCtas>;
   Tile d;
-  d.row0 = it.row0 + t * kRows;
-  d.rows = min(kRows, it.lq - d.row0);
-  d.steps = d.masked = 0;
-  if (d.rows <= 0) {
-    d.rows = 0;
-  } else {
-    d.steps = (visible(it, causal, d.row0 + d.rows - 1) + kKeys - 1) / kKeys;
-    d.masked = visible(it, causal, d.row0) / kKeys;
-  }
+  const int first = it.row0 + t * F::kTileRows, last = min(first + F::kTileRows, it.lq) - 1;
+  d.row0 = first + rank * kRows;
+  d.rows = max(0, min(kRows, it.lq - d.row0));
+  d.steps = last >= first ? (visible(it, causal, last) + F::kKeys - 1) / F::kKeys : 0;
+  d.masked = visible(it, causal, min(d.row0, it.lq - 1)) / F::kKeys;
   return d;
 }
+// First step whose values are looked through: one that some row does not see whole.
+template <int kCtas>
+__device__ __forceinline__ int first_scan(const Item& it, int causal) {
+  int from = INT32_MAX;
+  for (int t = 0; t < 2; ++t) {
+    const Tile d = tile_of<kCtas>(it, causal, t, 0);
+    if (d.steps) from = min(from, d.masked);
+  }
+  return from;
+}
 
-// Item `idx` of a head: requests own ceil(rows / 256) items each, those with the
+// Item `idx` of a head: requests own ceil(rows / kItemRows) items each, those with the
 // most keys first.  Found by a warp over the offsets; false: there is no such item.
 // A request whose offsets break the rules, by themselves or by beginning before an
 // earlier one's end, owns none.
+template <int kItemRows>
 __device__ bool find_item(const Args& a, int idx, int lane, Item* it) {
   int items = 0, end = 0;  // of the requests so far
   bool bad_q = false, bad_k = false, found = false;
@@ -190,16 +217,20 @@ __device__ __forceinline__ void flag_store(uint32_t addr, uint32_t v) {
   asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// The leader of a pair waits for what its peer did as well.
+template <int kCtas>
 struct Ctx {
-  uint32_t sbase;
+  uint32_t sbase, leader;  // shared-memory windows of this CTA and (as a cluster address) of the leader
+  int rank;
+  __device__ __forceinline__ uint32_t leader_bar(int i) const { return leader + kOffBars + 8 * i; }
   __device__ __forceinline__ uint32_t bar(int i) const { return sbase + kOffBars + 8 * i; }
   // Bounded wait; false: gave up here or elsewhere in the CTA.
   __device__ __forceinline__ bool wait(int i, uint32_t parity, int code) const {
     const uint32_t b = bar(i);
-    if (mbar_try_wait(b, parity)) return true;
+    if (kCtas > 1 ? mbar_try_wait_cluster(b, parity) : mbar_try_wait(b, parity)) return true;
     const long long t0 = clock64();
     while (true) {
-      if (mbar_try_wait(b, parity)) return true;
+      if (kCtas > 1 ? mbar_try_wait_cluster(b, parity) : mbar_try_wait(b, parity)) return true;
       if (flag_load(sbase + kOffAbort)) return false;
       if (clock64() - t0 > kTimeoutCycles) {
         flag_store(sbase + kOffAbort, 1);
@@ -207,6 +238,31 @@ struct Ctx {
         return false;
       }
     }
+  }
+  // For the issuing warp: the first tries loop inside one statement and the verdict is
+  // a vote, so the compiler sees no divergence.
+  __device__ __forceinline__ bool wait_uniform(int i, uint32_t parity, int code) const {
+    uint32_t ok;
+    if (kCtas > 1)
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+          "TRY:\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+          "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 64;\n\t@q bra TRY;\n"
+          "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(bar(i)), "r"(parity)
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+          "TRY:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+          "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 64;\n\t@q bra TRY;\n"
+          "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(bar(i)), "r"(parity)
+          : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
+    return wait_warp(i, parity, code);
   }
   __device__ __forceinline__ bool wait_warp(int i, uint32_t parity, int code) const {
     return __all_sync(0xffffffffu, wait(i, parity, code));
@@ -219,11 +275,26 @@ struct Ctx {
   }
 };
 
+// Load a box into this CTA's shared memory, completing on a barrier of the leader.
+template <int kCtas>
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
+  if (kCtas > 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+// Announce this CTA's bytes on a barrier of the leader (cluster address).
+__device__ __forceinline__ void announce(uint32_t cluster_bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
+               : "memory");
 }
 
 struct Maps {
@@ -232,59 +303,57 @@ struct Maps {
 
 // ------------------------------------------------------------------ TMA
 
-// The value tiles from step scan_from on complete on barriers of the scan, which
-// then fills the slot's own: the products wait for one barrier a slot, and no one
-// waits for a phase that another may leave behind.
-__device__ __forceinline__ int raw_bar(int half, int scans) { return B_RAW + 2 * half + (scans & 1); }
-
-__device__ void load_item(const Ctx& c, const Maps& m, const Item& it, const Tile& ta, const Tile& tb, int scan_from) {
+// Every CTA loads its own rows of Q, its 64 of the step's keys, and its columns of
+// the step's values.  The values from step scan_from on complete on barriers of the
+// scan, which then fills the stage's own: the products wait for one barrier, and no
+// one waits for a phase that another may leave behind.
+template <int kCtas>
+__device__ void load_item(const Ctx<kCtas>& c, const Maps& m, const Item& it, const Tile& ta, const Tile& tb, int scan_from) {
+  using F = Form<kCtas>;
   const int steps = max(ta.steps, tb.steps);
-  int slot = 0, issued = 0;
-  uint32_t phase = 0;
+  int j = 0;
   bool ok = true;
   auto load_q = [&](int t, const Tile& d) {
     if (d.steps == 0) return;
-    const uint32_t dst = c.sbase + kOffQ + t * kQTile, bar = c.bar(B_Q + t);
+    const uint32_t dst = c.sbase + kOffQ + t * kQTile, bar = c.leader_bar(B_Q + t);
     const int row = it.q0 + d.row0;
-    mbar_arrive_expect_tx(bar, kQTile);
-    tma_3d(dst, &m.q_nope, bar, 0, it.head, row);
-    tma_3d(dst + kSlot, &m.q_nope, bar, 64, it.head, row);
-    tma_3d(dst + 2 * kSlot, &m.q_pe, bar, 0, it.head, row);
+    announce(bar, kQTile);
+    tma_3d<kCtas>(dst, &m.q_nope, bar, 0, it.head, row);
+    tma_3d<kCtas>(dst + 2 * kBox, &m.q_nope, bar, 64, it.head, row);
+    tma_3d<kCtas>(dst + 4 * kBox, &m.q_pe, bar, 0, it.head, row);
   };
   load_q(0, ta);
-  for (int j = 0; ok && j < steps; ++j) {
-    const int row = it.k0 + j * kKeys;
-    for (int i = 0; ok && i < kStepSlots; ++i) {
-      if (!(ok = c.wait(B_EMPTY + slot, phase ^ 1, 0xA11))) break;
-      const bool scan = i >= kKSlots && j >= scan_from;
-      const uint32_t dst = c.sbase + kOffRing + slot * kSlot;
-      const uint32_t bar = c.bar(scan ? raw_bar(i - kKSlots, j - scan_from) : B_FULL + slot);
-      mbar_arrive_expect_tx(bar, kSlot);
-      if (i < 2)
-        tma_3d(dst, &m.k_nope, bar, 64 * i, it.head, row);
-      else if (i == 2)
-        tma_3d(dst, &m.k_pe, bar, 0, 0, row);
-      else
-        tma_3d(dst, &m.v, bar, 64 * (i - 3), it.head, row);
-      ++issued;
-      if (++slot == kSlots) {
-        slot = 0;
-        phase ^= 1;
-      }
-      if (j == 0 && i == 2) load_q(1, tb);
+  for (; j < steps; ++j) {
+    const int stage = j % kStages;
+    const uint32_t parity = ((j / kStages) & 1) ^ 1, dst = c.sbase + kOffRing + stage * kStageBytes;
+    const int row = it.k0 + j * F::kKeys;
+    if (!(ok = c.wait(B_KE + stage, parity, 0xA11))) break;
+    {
+      const uint32_t bar = c.leader_bar(B_KF + stage);
+      announce(bar, kKBytes);
+      tma_3d<kCtas>(dst, &m.k_nope, bar, 0, it.head, row + 64 * c.rank);
+      tma_3d<kCtas>(dst + kBox, &m.k_nope, bar, 64, it.head, row + 64 * c.rank);
+      tma_3d<kCtas>(dst + 2 * kBox, &m.k_pe, bar, 0, 0, row + 64 * c.rank);
+    }
+    if (j == 0) load_q(1, tb);
+    if (!(ok = c.wait(B_VE + stage, parity, 0xA12))) break;
+    if (j < scan_from) {
+      const uint32_t bar = c.leader_bar(B_VF + stage);
+      announce(bar, kVBytes);
+      tma_3d<kCtas>(dst + kKBytes, &m.v, bar, 64 * c.rank, it.head, row);
+      if (kCtas == 1) tma_3d<kCtas>(dst + kKBytes + kBox, &m.v, bar, 64, it.head, row);
+    } else {
+      const uint32_t bar = c.bar(B_RAW + (j - scan_from) % kStages);
+      mbar_arrive_expect_tx(bar, kVBytes);
+      tma_3d<1>(dst + kKBytes, &m.v, bar, 64 * c.rank, it.head, row);
+      if (kCtas == 1) tma_3d<1>(dst + kKBytes + kBox, &m.v, bar, 64, it.head, row);
     }
   }
-  // every copy has landed before this CTA may leave
-  if (!ok) {
-    if (ta.steps) c.wait_limited(B_Q, 0);
-    if (tb.steps) c.wait_limited(B_Q + 1, 0);
-    for (int i = max(0, issued - kSlots); i < issued; ++i) {
-      const int scans = i / kStepSlots - scan_from, half = i % kStepSlots - kKSlots;
-      if (scans >= 0 && half >= 0)
-        c.wait_limited(raw_bar(half, scans), (scans >> 1) & 1);
-      else
-        c.wait_limited(B_FULL + i % kSlots, (i / kSlots) & 1);
-    }
+  // Every copy has landed, and every arrival that the products send here has come
+  // in, before this CTA may leave.  (The products follow the copies.)
+  for (int i = max(0, j - kStages); i < j; ++i) {
+    c.wait_limited(B_KE + i % kStages, (i / kStages) & 1);
+    c.wait_limited(B_VE + i % kStages, (i / kStages) & 1);
   }
 }
 
@@ -292,95 +361,154 @@ __device__ void load_item(const Ctx& c, const Maps& m, const Item& it, const Til
 
 // Operand descriptors differ in the start address alone (the low word).
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (kSwizzle128B << 29);
-__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lbo) {
-  const uint32_t low = ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
-  return static_cast<uint64_t>(kDescHigh) << 32 | low;
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); }
+
+// Four K = 16 products, D[tmem] (+)= A B^T, for a CTA or a pair: A in shared memory
+// (`a` a low word, a step 32 bytes) or in TMEM (`a` an address, a step 8 columns), B
+// in shared memory (a step 32 bytes of keys, or 16 keys of values).  The whole issuing
+// warp runs through, one lane (`go`) issues: with predicated instructions and no
+// divergence descriptors stay in uniform registers.  (One lane in a branch of its own
+// took 95 to 120 cycles a product, which the tensor core does in 64.)
+template <int kCtas>
+__device__ __forceinline__ void products_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate,
+                                            uint32_t go) {
+  if (kCtas == 1)
+    asm volatile(
+        "{\n\t.reg .pred g, p;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\tsetp.ne.b32 g, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t@g tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 da, {x, %6};\n\tmov.b64 db, {y, %6};\n\t@g tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 da, {x, %6};\n\tmov.b64 db, {y, %6};\n\t@g tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 da, {x, %6};\n\tmov.b64 db, {y, %6};\n\t@g tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(go), "r"(kDescHigh)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred g, p;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\tsetp.ne.b32 g, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t@g tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 da, {x, %6};\n\tmov.b64 db, {y, %6};\n\t@g tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 da, {x, %6};\n\tmov.b64 db, {y, %6};\n\t@g tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 da, {x, %6};\n\tmov.b64 db, {y, %6};\n\t@g tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t"
+        "}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(go), "r"(kDescHigh)
+        : "memory");
+}
+template <int kCtas>
+__device__ __forceinline__ void products_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate,
+                                            uint32_t go) {
+  if (kCtas == 1)
+    asm volatile(
+        "{\n\t.reg .pred g, p;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\tsetp.ne.b32 g, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %6};\n\t@g tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 db, {y, %6};\n\t@g tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 256;\n\tmov.b64 db, {y, %6};\n\t@g tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 384;\n\tmov.b64 db, {y, %6};\n\t@g tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(go), "r"(kDescHigh)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred g, p;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\tsetp.ne.b32 g, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %6};\n\t@g tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %3, p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 db, {y, %6};\n\t@g tcgen05.mma.cta_group::2.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 256;\n\tmov.b64 db, {y, %6};\n\t@g tcgen05.mma.cta_group::2.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 384;\n\tmov.b64 db, {y, %6};\n\t@g tcgen05.mma.cta_group::2.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(go), "r"(kDescHigh)
+        : "memory");
+}
+// Arrive on the barrier at this offset in every CTA when the products issued so far are done.
+template <int kCtas>
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t go) {
+  if (kCtas == 1)
+    asm volatile(
+        "{\n\t.reg .pred g;\n\tsetp.ne.b32 g, %1, 0;\n\t"
+        "@g tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(go)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred g;\n\tsetp.ne.b32 g, %1, 0;\n\t"
+        "@g tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(bar),
+        "r"(go), "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
 }
 
-__device__ void issue_products(const Ctx& c, uint32_t tmem, const Tile& ta, const Tile& tb) {
-  constexpr uint32_t kIdescS = idesc_f32acc(kRows, kKeys, 0, 0, 1), kIdescO = idesc_f32acc(kRows, 128, 0, 1, 1);
+// Run by a whole warp.
+template <int kCtas>
+__device__ void issue_products(const Ctx<kCtas>& c, uint32_t tmem, const Tile& ta, const Tile& tb) {
+  using F = Form<kCtas>;
+  constexpr uint32_t kIdescS = idesc_f32acc(F::kTileRows, F::kKeys, 0, 0, 1);
+  constexpr uint32_t kIdescO = idesc_f32acc(F::kTileRows, 128, 0, 1, 1);
   const int steps[2] = {ta.steps, tb.steps};
   const int total = max(ta.steps, tb.steps);
-  bool ok = true, q_here[2] = {false, false};
+  const uint32_t go = elect_one();
+  const uint32_t q0 = desc_low(c.sbase + kOffQ, 16), k0 = desc_low(c.sbase + kOffRing, 16);
+  const uint32_t v0 = desc_low(c.sbase + kOffRing + kKBytes, kBox);
+  bool ok = true;
+  int ks = 0, vs = 0;            // stages of step j's keys and of step j - 1's values
+  uint32_t kp = 0, vp = 0;       // ... and their parities
   for (int j = 0; ok && j <= total; ++j) {
-    bool k_here = false, v_here = false;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (!ok) break;
       if (j > 0 && j - 1 < steps[t]) {
         // ---- O += P V of step j - 1
-        const int first = (j - 1) * kStepSlots + kKSlots;
-        if (!v_here) {
-          for (int i = first; ok && i < first + kVSlots; ++i) ok = c.wait(B_FULL + i % kSlots, (i / kSlots) & 1, 0xA12);
-          v_here = true;
-        }
-        if (!ok || !(ok = c.wait(B_P + t, (j - 1) & 1, 0xA14))) break;
+        if ((t == 0 || j - 1 >= steps[0]) && !(ok = c.wait_uniform(B_VF + vs, vp, 0xA13))) break;
+        if (!(ok = c.wait_uniform(B_P + t, (j - 1) & 1, 0xA14))) break;
         tc_fence_after();
-        // the value tile's two slots are neighbours in the ring's numbering, not always in memory
-        const uint32_t v0 = c.sbase + kOffRing + (first % kSlots) * kSlot;
-        const uint32_t v1 = c.sbase + kOffRing + ((first + 1) % kSlots) * kSlot;
-        constexpr uint32_t kIdescHalf = idesc_f32acc(kRows, 64, 0, 1, 1);
-        if (v1 == v0 + kSlot) {
+        const uint32_t v = v0 + vs * (kStageBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + 8 * kk, desc(v0 + kk * 2048, kSlot), kIdescO,
-                   j > 1 || kk > 0);
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk) {
-            mma_ts(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + 8 * kk, desc(v0 + kk * 2048, kSlot), kIdescHalf,
-                   j > 1 || kk > 0);
-            mma_ts(tmem + TM_O + 128 * t + 64, tmem + TM_S + 128 * t + 8 * kk, desc(v1 + kk * 2048, kSlot), kIdescHalf,
-                   j > 1 || kk > 0);
-          }
-        }
-        if (j == steps[t]) mma_commit(c.bar(B_O + t));
-        if (t == 1 || j - 1 >= steps[1])  // its last reader
-          for (int i = first; i < first + kVSlots; ++i) mma_commit(c.bar(B_EMPTY + i % kSlots));
+        for (int kk = 0; kk < F::kKeys / 64; ++kk)  // 64 value columns of a key are 128 bytes
+          products_ts<kCtas>(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + 32 * kk, v + kk * 512, kIdescO, j > 1 || kk > 0, go);
+        if (j == steps[t]) commit<kCtas>(c.bar(B_O + t), go);
+        if (t == 1 || j - 1 >= steps[1]) commit<kCtas>(c.bar(B_VE + vs), go);  // its last reader
       }
       if (j < steps[t]) {
         // ---- S = Q K^T of step j
-        const int first = j * kStepSlots;
-        if (!k_here) {
-          for (int i = first; ok && i < first + kKSlots; ++i) ok = c.wait(B_FULL + i % kSlots, (i / kSlots) & 1, 0xA15);
-          k_here = true;
-        }
-        if (ok && !q_here[t]) {
-          ok = c.wait(B_Q + t, 0, 0xA16);
-          q_here[t] = true;
-        }
-        if (!ok) break;
+        if ((t == 0 || j >= steps[0]) && !(ok = c.wait_uniform(B_KF + ks, kp, 0xA15))) break;
+        if (j == 0 && !(ok = c.wait_uniform(B_Q + t, 0, 0xA16))) break;
         tc_fence_after();
-        const uint32_t qa = c.sbase + kOffQ + t * kQTile;
+        const uint32_t q = q0 + t * (kQTile >> 4), k = k0 + ks * (kStageBytes >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 12; ++kk) {
-          const uint32_t ka = c.sbase + kOffRing + ((first + kk / 4) % kSlots) * kSlot;
-          mma_ss(tmem + TM_S + 128 * t, desc(qa + (kk / 4) * kSlot + (kk % 4) * 32, 16), desc(ka + (kk % 4) * 32, 16),
-                 kIdescS, kk > 0);
-        }
-        mma_commit(c.bar(B_S + t));
-        if (t == 1 || j >= steps[1])
-          for (int i = first; i < first + kKSlots; ++i) mma_commit(c.bar(B_EMPTY + i % kSlots));
+        for (int kk = 0; kk < 3; ++kk)
+          products_ss<kCtas>(tmem + TM_S + 128 * t, q + kk * (2 * kBox >> 4), k + kk * (kBox >> 4), kIdescS, kk > 0, go);
+        commit<kCtas>(c.bar(B_S + t), go);
+        if (t == 1 || j >= steps[1]) commit<kCtas>(c.bar(B_KE + ks), go);
       }
+    }
+    if (j > 0 && ++vs == kStages) {
+      vs = 0;
+      vp ^= 1;
+    }
+    if (++ks == kStages) {
+      ks = 0;
+      kp ^= 1;
     }
   }
   // every product is done before TMEM is released
-  mma_commit(c.bar(B_FIN));
+  commit<kCtas>(c.bar(B_FIN), go);
   c.wait_limited(B_FIN, 0);
 }
 
 // ------------------------------------------------------------------ value scan
 
-// Zeros in the place of what is not finite, in the value tiles from step
-// scan_from on; warp w looks after the tile's columns 64 w .. 64 w + 63.
-__device__ void scan_values(const Ctx& c, const Item& it, int steps, int scan_from, int w, int lane) {
+// Zeros in the place of what is not finite, in this CTA's values from step
+// scan_from on.
+template <int kCtas>
+__device__ void scan_values(const Ctx<kCtas>& c, const Item& it, int steps, int scan_from, int lane) {
+  using F = Form<kCtas>;
   for (int j = scan_from; j < steps; ++j) {
-    const int slot = (j * kStepSlots + kKSlots + w) % kSlots, scans = j - scan_from;
-    if (!c.wait_warp(raw_bar(w, scans), (scans >> 1) & 1, 0xA13)) return;
-    const uint32_t base = c.sbase + kOffRing + slot * kSlot + lane * 16;
+    const int stage = j % kStages, scans = j - scan_from;
+    if (!c.wait_warp(B_RAW + scans % kStages, (scans / kStages) & 1, 0xA17)) return;
+    const uint32_t base = c.sbase + kOffRing + stage * kStageBytes + kKBytes + lane * 16;
     bool seen = false;
-#pragma unroll 4
-    for (int i = 0; i < kSlot / 512; ++i) {
+#pragma unroll 8
+    for (int i = 0; i < kVBytes / 512; ++i) {
       uint4 x = ld_shared_v4(base + i * 512);
       constexpr uint32_t kExp = 0x7F807F80u;
       const uint32_t b0 = __vcmpeq2(x.x & kExp, kExp), b1 = __vcmpeq2(x.y & kExp, kExp), b2 = __vcmpeq2(x.z & kExp, kExp),
@@ -391,13 +519,19 @@ __device__ void scan_values(const Ctx& c, const Item& it, int steps, int scan_fr
         x.z &= ~b2;
         x.w &= ~b3;
         st_shared_v4(base + i * 512, x);
-        seen |= j * kKeys + i * 4 + (lane >> 3) < it.lk;  // a slot's row is 128 bytes
+        // a key is 128 bytes; one CTA alone holds two boxes of 64 keys
+        seen |= j * F::kKeys + (i * 4 + (lane >> 3)) % F::kKeys < it.lk;
       }
     }
     if (seen) flag_store(c.sbase + kOffPoison, 1);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar(B_FULL + slot));
+    if (lane == 0) {
+      if (kCtas > 1)
+        mbar_arrive_remote(c.leader_bar(B_VF + stage));
+      else
+        mbar_arrive(c.bar(B_VF + stage));
+    }
   }
 }
 
@@ -441,38 +575,60 @@ __device__ __noinline__ float non_finite(const uint16_t* v, int64_t stride, int 
   return sum;
 }
 
-__device__ void softmax_tile(const Ctx& c, const Args& a, const Item& it, const Tile& d, int t, int scan_from, uint32_t tmem) {
+// (What it orders, TMEM, the tcgen05 fences order; a release at cluster scope would
+// wait for stores in flight.)
+template <int kCtas>
+__device__ __forceinline__ void arrive_leader(const Ctx<kCtas>& c, int bar) {
+  if (kCtas > 1)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(c.leader_bar(bar)) : "memory");
+  else
+    mbar_arrive(c.bar(bar));
+}
+
+template <int kCtas>
+__device__ void softmax_tile(const Ctx<kCtas>& c, const Args& a, const Item& it, const Tile& d, int t, int scan_from,
+                             uint32_t tmem) {
+  using F = Form<kCtas>;
+  constexpr int kParts = F::kKeys / 32;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
   const int row = d.row0 + quad * 32 + lane;  // within the request
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t ts = tmem + lanes + TM_S + 128 * t, to = tmem + lanes + TM_O + 128 * t;
+  if (d.rows == 0) {  // the tile's rows are the other CTA's
+    for (int j = 0; j < d.steps; ++j) {
+      if (!c.wait_warp(B_S + t, j & 1, 0xA18)) return;
+      if (lane == 0) arrive_leader(c, B_P + t);
+    }
+    return;
+  }
   const int seen = visible(it, a.causal, min(row, it.lq - 1));
   const float slack = kRescaleLog2 / a.scale_log2;
   float top = -CUDART_INF_F, sum = 0.f;  // the running maximum (of S) and sum
   for (int j = 0; j < d.steps; ++j) {
     if (!c.wait_warp(B_S + t, j & 1, 0xA18)) return;
     tc_fence_after();
-    uint32_t s[4][32];
+    uint32_t s[kParts][32];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) tmem_ld32_async(ts + 32 * q, s[q]);
+    for (int q = 0; q < kParts; ++q) tmem_ld32_async(ts + 32 * q, s[q]);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) tmem_wait_ld32(s[q]);
+    for (int q = 0; q < kParts; ++q) tmem_wait_ld32(s[q]);
     if (j >= d.masked) {
-      const int left = seen - j * kKeys;
+      const int left = seen - j * F::kKeys;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < kParts; ++q)
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (32 * q + i >= left) s[q][i] = 0xFF800000u;  // -inf
     }
-    float high[4];
+    float high[kParts];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kParts; ++q) {
       high[q] = __uint_as_float(s[q][0]);
 #pragma unroll
       for (int i = 1; i < 32; ++i) high[q] = fmaxf(high[q], __uint_as_float(s[q][i]));
     }
-    const float here = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
+    float here = fmaxf(high[0], high[1]);
+    if (kParts == 4) here = fmaxf(here, fmaxf(high[kParts - 2], high[kParts - 1]));
     const bool move = here > top + slack;
     if (__any_sync(0xffffffffu, move)) {
       const float factor = move ? ex2_approx((top - here) * a.scale_log2) : 1.f;
@@ -492,7 +648,7 @@ __device__ void softmax_tile(const Ctx& c, const Args& a, const Item& it, const 
     const float base = top == -CUDART_INF_F ? 0.f : top * a.scale_log2;
     float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kParts; ++q) {
       uint32_t p[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -507,7 +663,7 @@ __device__ void softmax_tile(const Ctx& c, const Args& a, const Item& it, const 
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar(B_P + t));
+    if (lane == 0) arrive_leader(c, B_P + t);
   }
   // ---- epilogue
   if (d.steps > 0) {
@@ -531,7 +687,7 @@ __device__ void softmax_tile(const Ctx& c, const Args& a, const Item& it, const 
     if (poison && mine && !none) {
       const uint16_t* v = a.v + it.k0 * a.v_ts + it.head * a.v_hs + 32 * q;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] += non_finite(v + i, a.v_ts, scan_from * kKeys, seen);
+      for (int i = 0; i < 32; ++i) o[i] += non_finite(v + i, a.v_ts, scan_from * F::kKeys, seen);
     }
     uint32_t p[16];
 #pragma unroll
@@ -547,17 +703,38 @@ __device__ void softmax_tile(const Ctx& c, const Args& a, const Item& it, const 
   }
 }
 
+template <int kCtas>
+__device__ __forceinline__ void tmem_alloc_of(uint32_t dst) {
+  if (kCtas == 1) {
+    tmem_alloc(dst, kTmemCols);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int kCtas>
+__device__ __forceinline__ void tmem_dealloc_of(uint32_t tmem) {
+  if (kCtas == 1)
+    tmem_dealloc(tmem, kTmemCols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+template <int kCtas>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ Maps maps, const Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Ctx c;
+  Ctx<kCtas> c;
   c.sbase = smem_u32(smem);
+  c.rank = kCtas > 1 ? (int)cluster_ctarank() : 0;
+  c.leader = kCtas > 1 ? mapa(c.sbase, 0) : c.sbase;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int index = (int)blockIdx.x / kCtas;
   volatile int* slot = reinterpret_cast<volatile int*>(smem + kOffItem);  // the item; [6]: whether there is one
   if (warp == 0) {
     Item it{};
-    const int idx = (int)(blockIdx.x % a.tiles);
-    const bool found = find_item(a, idx, lane, &it);
+    const bool found = find_item<Form<kCtas>::kItemRows>(a, index % a.tiles, lane, &it);
     if (lane == 0) {
       slot[0] = it.q0;
       slot[1] = it.lq;
@@ -568,16 +745,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       flag_store(c.sbase + kOffAbort, 0);
       flag_store(c.sbase + kOffPoison, 0);
       for (int t = 0; t < 2; ++t) {
-        mbar_init(c.bar(B_Q + t), 1);
+        mbar_init(c.bar(B_Q + t), kCtas);
+        mbar_init(c.bar(B_QE + t), 1);
         mbar_init(c.bar(B_S + t), 1);
-        mbar_init(c.bar(B_P + t), 4);
+        mbar_init(c.bar(B_P + t), 4 * kCtas);
         mbar_init(c.bar(B_O + t), 1);
       }
-      for (int i = 0; i < kSlots; ++i) {
-        mbar_init(c.bar(B_FULL + i), 1);
-        mbar_init(c.bar(B_EMPTY + i), 1);
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(c.bar(B_KF + i), kCtas);
+        mbar_init(c.bar(B_KE + i), 1);
+        mbar_init(c.bar(B_VF + i), kCtas);
+        mbar_init(c.bar(B_VE + i), 1);
+        mbar_init(c.bar(B_RAW + i), 1);
       }
-      for (int i = 0; i < 4; ++i) mbar_init(c.bar(B_RAW + i), 1);
       mbar_init(c.bar(B_FIN), 1);
       fence_mbar_init();
       prefetch_tensormap(&maps.q_nope);
@@ -588,11 +768,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
     __syncwarp();
   } else if (warp == 1) {
-    tmem_alloc(c.sbase + kOffTmem, kTmemCols);
-    tmem_relinquish();
+    tmem_alloc_of<kCtas>(c.sbase + kOffTmem);
   }
   tc_fence_before();
   __syncthreads();
+  if (kCtas > 1) cluster_sync();  // the peer's barriers are initialised before any arrival there
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem);
   Item it;
@@ -601,28 +781,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   it.k0 = slot[2];
   it.lk = slot[3];
   it.row0 = slot[4];
-  it.head = (int)(blockIdx.x / a.tiles);
+  it.head = index / a.tiles;
   if (slot[6]) {
-    const Tile ta = tile_of(it, a.causal, 0), tb = tile_of(it, a.causal, 1);
-    // steps whose values are looked through: those that some row does not see whole
-    const int scan_from = min(ta.steps ? ta.masked : INT32_MAX, tb.steps ? tb.masked : INT32_MAX);
+    const Tile ta = tile_of<kCtas>(it, a.causal, 0, c.rank), tb = tile_of<kCtas>(it, a.causal, 1, c.rank);
+    const int scan_from = first_scan<kCtas>(it, a.causal);
     if (warp < 4) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
       if (warp == 0 && lane == 0) load_item(c, maps, it, ta, tb, scan_from);
-      if (warp == 1 && lane == 0) issue_products(c, tmem, ta, tb);
-      if (warp >= 2) scan_values(c, it, max(ta.steps, tb.steps), scan_from, warp - 2, lane);
+      if (warp == 1) {
+        if (c.rank == 0)
+          issue_products(c, tmem, ta, tb);
+        else
+          c.wait_limited(B_FIN, 0);  // the leader's last arrival here
+      }
+      if (warp == 2) scan_values(c, it, max(ta.steps, tb.steps), scan_from, lane);
     } else {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
       const int t = (warp - 4) >> 2;
       const Tile d = t ? tb : ta;
-      if (d.rows > 0) softmax_tile(c, a, it, d, t, scan_from, tmem);
+      softmax_tile(c, a, it, d, t, scan_from, tmem);
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (kCtas > 1) cluster_sync();  // every product is read and no arrival is left on its way
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 1) tmem_dealloc_of<kCtas>(tmem);
+  if (kCtas > 1) cluster_sync();
 }
 
 // ------------------------------------------------------------------ host side
@@ -640,17 +826,56 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// bf16 [tokens, heads, cols] read in boxes of 128 tokens x 64 columns of one head
-static bool make_map(CUtensorMap* map, const HeadRows& x, int64_t cols, int64_t heads, int64_t tokens) {
+// bf16 [tokens, heads, cols] read in boxes of `box_rows` tokens x 64 columns of one head
+static bool make_map(CUtensorMap* map, const HeadRows& x, int64_t cols, int64_t heads, int64_t tokens, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)heads, (cuuint64_t)tokens};
   cuuint64_t strides[2] = {(cuuint64_t)x.head_stride * 2, (cuuint64_t)x.token_stride * 2};
-  cuuint32_t box[3] = {64, 1, kRows};
+  cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x.p), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Items of a head: one for each `item_rows` rows of a request, at most
+static int items_of_a_head(int num_tokens_q, int batch, int item_rows) {
+  return num_tokens_q / item_rows + (batch < num_tokens_q ? batch : num_tokens_q);
+}
+
+template <int kCtas>
+static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t stream) {
+  using F = Form<kCtas>;
+  constexpr auto kernel = prefill_kernel<kCtas>;
+  static OncePerDevice once;
+  const cudaError_t e =
+      once.run(dev.id, [] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
+  if (e != cudaSuccess) return e;
+  Maps m;
+  // without a key no box of the keys is ever loaded: any valid map will do
+  const bool keys = p.num_tokens_k > 0;
+  const int64_t tk = keys ? p.num_tokens_k : 1;
+  if (!make_map(&m.q_nope, p.q_nope, 128, p.num_heads, p.num_tokens_q, kRows) ||
+      !make_map(&m.q_pe, p.q_pe, 64, p.num_heads, p.num_tokens_q, kRows) ||
+      !make_map(&m.k_nope, keys ? p.k_nope : p.q_nope, 128, p.num_heads, tk, 64) ||
+      !make_map(&m.k_pe, keys ? p.k_pe : p.q_pe, 64, 1, tk, 64) ||
+      !make_map(&m.v, keys ? p.v : p.q_nope, 128, p.num_heads, tk, F::kKeys))
+    return cudaErrorNotSupported;
+  a.tiles = items_of_a_head(p.num_tokens_q, p.batch, F::kItemRows);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.tiles * a.heads * kCtas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, m, a);
 }
 
 }  // namespace prefill
@@ -659,21 +884,7 @@ static bool make_map(CUtensorMap* map, const HeadRows& x, int64_t cols, int64_t 
 // encoder is unavailable or rejected the operands.
 cudaError_t launch_prefill(const PrefillCall& p, Device dev, cudaStream_t stream) {
   using namespace prefill;
-  static OncePerDevice once;
-  const cudaError_t e = once.run(
-      dev.id, [] { return cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
-  if (e != cudaSuccess) return e;
-  Maps m;
-  // without a key no box of the keys is ever loaded: any valid map will do
-  const bool keys = p.num_tokens_k > 0;
-  const HeadRows k_pe{p.k_pe.p, p.k_pe.token_stride, p.k_pe.token_stride};
-  if (!make_map(&m.q_nope, p.q_nope, 128, p.num_heads, p.num_tokens_q) ||
-      !make_map(&m.q_pe, p.q_pe, 64, p.num_heads, p.num_tokens_q) ||
-      !make_map(&m.k_nope, keys ? p.k_nope : p.q_nope, 128, p.num_heads, keys ? p.num_tokens_k : 1) ||
-      !make_map(&m.k_pe, keys ? k_pe : p.q_pe, 64, 1, keys ? p.num_tokens_k : 1) ||
-      !make_map(&m.v, keys ? p.v : p.q_nope, 128, p.num_heads, keys ? p.num_tokens_k : 1))
-    return cudaErrorNotSupported;
-  Args a;
+  Args a{};
   a.cu_q = p.cu_q;
   a.cu_k = p.cu_k;
   a.v = static_cast<const uint16_t*>(p.v.p);
@@ -687,16 +898,15 @@ cudaError_t launch_prefill(const PrefillCall& p, Device dev, cudaStream_t stream
   a.heads = p.num_heads;
   a.tokens_q = p.num_tokens_q;
   a.tokens_k = p.num_tokens_k;
-  a.tiles = prefill_items(p.num_tokens_q, p.batch);
   a.causal = p.causal;
   a.scale_log2 = p.scale * 1.44269504088896340736f;
-  prefill_kernel<<<(unsigned)(a.tiles * a.heads), kThreads, kSmem, stream>>>(m, a);
-  return cudaGetLastError();
+  const bool pair = p.num_tokens_q / p.batch > 256;
+  return pair ? launch<2>(p, a, dev, stream) : launch<1>(p, a, dev, stream);
 }
 
-// Items of a head: one for each 256 rows of a request, at most
+// Launch bound: the small form's CTAs, at most
 int prefill_items(int num_tokens_q, int batch) {
-  return num_tokens_q / prefill::kItemRows + (batch < num_tokens_q ? batch : num_tokens_q);
+  return prefill::items_of_a_head(num_tokens_q, batch, prefill::Form<1>::kItemRows);
 }
 
 // Nothing is split over the keys: no workspace.
