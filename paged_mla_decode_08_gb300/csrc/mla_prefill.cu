@@ -39,8 +39,8 @@
 // some row does not see whole, and puts zeros in the place of what is not finite.
 // The rows that do see such a value get it in the epilogue.
 //
-// Warps: 0 TMA, 1 MMA, 2 value scan, 4-7 softmax of the first tile, 8-11 of
-// the second.  Waits are bounded: on timeout the error word is set, every role
+// Warps: 0 TMA, 1 MMA, 2 value scan, 3 items, 4-7 softmax of the first tile,
+// 8-11 of the second.  Waits are bounded: on timeout the error word is set, every role
 // stops, copies and products in flight are awaited, TMEM is freed.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -85,6 +85,7 @@ struct Form {
   static constexpr int kItemRows = 2 * kTileRows;
 };
 
+constexpr int kItemSlots = 2;
 enum Bar : int {
   B_Q = 0,                        // [tile] Q landed (the leader's barrier)
   B_QE = B_Q + 2,                 // [tile] Q is read
@@ -94,16 +95,23 @@ enum Bar : int {
   B_VE = B_VF + kStages,          // [stage] values are read
   B_RAW = B_VE + kStages,         // [scan % 3] values landed, for the scan
   B_S = B_RAW + kStages,          // [tile] scores are in TMEM
-  B_P = B_S + 2,                  // [tile] weights are in TMEM, O is rescaled (the leader's)
-  B_O = B_P + 2,                  // [tile] the tile's products are done
-  B_FIN = B_O + 2,                // every product is done
+  B_P = B_S + 2,                  // [2 tile + half] weights are in TMEM, O is rescaled (the leader's)
+  B_O = B_P + 4,                  // [tile] the tile's products are done
+  B_ITEM = B_O + 2,               // [slot] an item is there
+  B_TAKEN = B_ITEM + kItemSlots,  // [slot] every role of the item's CTAs has it (the leader's)
+  B_NEXT = B_TAKEN + kItemSlots,  // the item's copies are issued: time to ask for the next
+  B_ASKED,                        // the answer is there
+  B_FIN,                          // every product is done
   B_COUNT
 };
 constexpr int kOffTmem = kOffBars + B_COUNT * 8;
 constexpr int kOffAbort = kOffTmem + 4;
+constexpr int kPoisons = 8;
 constexpr int kOffPoison = kOffAbort + 4;
-constexpr int kOffItem = (kOffPoison + 4 + 15) / 16 * 16;
-constexpr int kSmem = kOffItem + 32 + 1024;  // + alignment slack
+constexpr int kOffItem = (kOffPoison + 4 * kPoisons + 15) / 16 * 16;
+constexpr int kItemBytes = 32;
+constexpr int kOffAnswer = kOffItem + kItemSlots * kItemBytes;
+constexpr int kSmem = kOffAnswer + 16 + 1024;  // + alignment slack
 static_assert(kSmem <= 232448, "shared memory budget");
 
 constexpr uint32_t TM_S = 0, TM_O = 256, kTmemCols = 512;
@@ -124,6 +132,7 @@ struct Args {
 struct Item {
   int q0, lq, k0, lk;  // the request's rows and keys
   int head, row0;      // first query row of the item within the request
+  int more;            // 0: there is no item, the work is done
 };
 
 // What a CTA does of one tile of an item.
@@ -227,10 +236,10 @@ struct Ctx {
   // Bounded wait; false: gave up here or elsewhere in the CTA.
   __device__ __forceinline__ bool wait(int i, uint32_t parity, int code) const {
     const uint32_t b = bar(i);
-    if (kCtas > 1 ? mbar_try_wait_cluster(b, parity) : mbar_try_wait(b, parity)) return true;
+    if (mbar_try_wait(b, parity)) return true;
     const long long t0 = clock64();
     while (true) {
-      if (kCtas > 1 ? mbar_try_wait_cluster(b, parity) : mbar_try_wait(b, parity)) return true;
+      if (mbar_try_wait(b, parity)) return true;
       if (flag_load(sbase + kOffAbort)) return false;
       if (clock64() - t0 > kTimeoutCycles) {
         flag_store(sbase + kOffAbort, 1);
@@ -239,28 +248,22 @@ struct Ctx {
       }
     }
   }
+  // Whether a phase is over, for a converged warp.
+  __device__ __forceinline__ bool ready(int i, uint32_t parity) const {
+    return __all_sync(0xffffffffu, mbar_test_wait(bar(i), parity));
+  }
   // For the issuing warp: the first tries loop inside one statement and the verdict is
   // a vote, so the compiler sees no divergence.
   __device__ __forceinline__ bool wait_uniform(int i, uint32_t parity, int code) const {
     uint32_t ok;
-    if (kCtas > 1)
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
-          "TRY:\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-          "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 64;\n\t@q bra TRY;\n"
-          "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(bar(i)), "r"(parity)
-          : "memory");
-    else
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
-          "TRY:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-          "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 64;\n\t@q bra TRY;\n"
-          "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(bar(i)), "r"(parity)
-          : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+        "TRY:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 64;\n\t@q bra TRY;\n"
+        "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar(i)), "r"(parity)
+        : "memory");
     if (__all_sync(0xffffffffu, ok)) return true;
     return wait_warp(i, parity, code);
   }
@@ -271,6 +274,132 @@ struct Ctx {
   __device__ __forceinline__ void wait_limited(int i, uint32_t parity) const {
     const long long t0 = clock64();
     while (!mbar_try_wait(bar(i), parity) && clock64() - t0 < kTimeoutCycles) {
+    }
+  }
+};
+
+// ------------------------------------------------------------------ items
+
+// The pair's CTAs take items together.  The leader asks the hardware for the next
+// one (a cluster of this grid that has not started, which then never does): work is
+// handed out as it gets done, and a CTA goes on to its next item without a launch,
+// with its first copies and products under the last one's epilogue.
+__device__ __forceinline__ void ask_for_cluster(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+               "r"(bar)
+               : "memory");
+}
+// The first CTA of the cluster that the answer gives, or -1.
+__device__ __forceinline__ int read_answer(uint32_t answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(answer)
+      : "memory");
+  fence_proxy_async_smem();  // the next answer is written by the asynchronous proxy
+  return got ? (int)x : -1;
+}
+
+// Run by a warp of the leader: finds items and hands them to both CTAs.
+template <int kCtas>
+__device__ void schedule(const Ctx<kCtas>& c, const Args& a, int lane) {
+  const uint32_t peer_items = kCtas > 1 ? mapa(c.sbase + kOffItem, 1) : 0;
+  const uint32_t peer_bars = kCtas > 1 ? mapa(c.bar(B_ITEM), 1) : 0;
+  int cta = (int)blockIdx.x, asked = 0;
+  auto answered = [&] {
+    const uint32_t parity = asked++ & 1;
+    if (c.wait_warp(B_ASKED, parity, 0xA1A)) return true;
+    c.wait_limited(B_ASKED, parity);  // it comes in a microsecond or so, whatever else went wrong
+    return false;
+  };
+  for (int n = 0;; ++n) {
+    Item it{};
+    while (cta >= 0) {
+      const int index = cta / kCtas;
+      it.head = index / a.tiles;
+      it.more = find_item<Form<kCtas>::kItemRows>(a, index - it.head * a.tiles, lane, &it);
+      if (it.more) break;
+      // fewer items than there could have been: on to the next one
+      if (lane == 0) {
+        mbar_arrive_expect_tx(c.bar(B_ASKED), 16);
+        ask_for_cluster(c.sbase + kOffAnswer, c.bar(B_ASKED));
+      }
+      __syncwarp();
+      if (!answered()) return;
+      cta = read_answer(c.sbase + kOffAnswer);
+    }
+    const int slot = n % kItemSlots;
+    if (n >= kItemSlots && !c.wait_warp(B_TAKEN + slot, (n / kItemSlots + 1) & 1, 0xA1B)) return;
+    if (lane == 0) {
+      const uint32_t dst = kOffItem + slot * kItemBytes;
+      st_shared_v4(c.sbase + dst, make_uint4(it.q0, it.lq, it.k0, it.lk));
+      st_shared_v4(c.sbase + dst + 16, make_uint4(it.head, it.row0, it.more, 0));
+      mbar_arrive(c.bar(B_ITEM + slot));
+      if (kCtas > 1) {
+        const uint32_t to = peer_items + slot * kItemBytes, bar = peer_bars + 8 * slot;
+        st_async_v4(to, it.q0, it.lq, it.k0, it.lk, bar);
+        st_async_v4(to + 16, it.head, it.row0, it.more, 0, bar);
+      }
+    }
+    __syncwarp();
+    if (!it.more) return;
+    if (!c.wait_warp(B_NEXT, n & 1, 0xA1C)) return;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(c.bar(B_ASKED), 16);
+      ask_for_cluster(c.sbase + kOffAnswer, c.bar(B_ASKED));
+    }
+    __syncwarp();
+    if (!answered()) return;
+    cta = read_answer(c.sbase + kOffAnswer);
+  }
+}
+// ... and by one of its peer, whose slots the leader fills.
+template <int kCtas>
+__device__ void receive(const Ctx<kCtas>& c, int lane) {
+  for (int n = 0;; ++n) {
+    const int slot = n % kItemSlots;
+    if (lane == 0) mbar_arrive_expect_tx(c.bar(B_ITEM + slot), kItemBytes);
+    __syncwarp();
+    if (!c.wait_warp(B_ITEM + slot, (n / kItemSlots) & 1, 0xA1E)) return;
+    if (flag_load(c.sbase + kOffItem + slot * kItemBytes + 24) == 0) return;
+  }
+}
+
+// Item n, for a converged warp; false: there is none, or a wait gave up.
+template <int kCtas>
+__device__ __forceinline__ bool take_item(const Ctx<kCtas>& c, int n, Item* it) {
+  const int slot = n % kItemSlots;
+  if (!c.wait_warp(B_ITEM + slot, (n / kItemSlots) & 1, 0xA1F)) return false;
+  const uint32_t src = c.sbase + kOffItem + slot * kItemBytes;
+  const uint4 x = ld_shared_v4(src), y = ld_shared_v4(src + 16);
+  it->q0 = x.x;
+  it->lq = x.y;
+  it->k0 = x.z;
+  it->lk = x.w;
+  it->head = y.x;
+  it->row0 = y.y;
+  it->more = y.z;
+  __syncwarp();
+  if (it->more && (threadIdx.x & 31) == 0) {
+    if (kCtas > 1)
+      mbar_arrive_remote(c.leader_bar(B_TAKEN + slot));
+    else
+      mbar_arrive(c.bar(B_TAKEN + slot));
+  }
+  return it->more != 0;
+}
+
+// A place in a ring: counts on through all items.
+template <int N>
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1;
     }
   }
 };
@@ -304,56 +433,79 @@ struct Maps {
 // ------------------------------------------------------------------ TMA
 
 // Every CTA loads its own rows of Q, its 64 of the step's keys, and its columns of
-// the step's values.  The values from step scan_from on complete on barriers of the
-// scan, which then fills the stage's own: the products wait for one barrier, and no
-// one waits for a phase that another may leave behind.
+// the step's values.  The values that are to be looked through complete on barriers
+// of the scan, which then fills the stage's own: the products wait for one barrier,
+// and no one waits for a phase that another may leave behind.
 template <int kCtas>
-__device__ void load_item(const Ctx<kCtas>& c, const Maps& m, const Item& it, const Tile& ta, const Tile& tb, int scan_from) {
+__device__ void load_items(const Ctx<kCtas>& c, const Args& a, const Maps& m, int lane) {
   using F = Form<kCtas>;
-  const int steps = max(ta.steps, tb.steps);
-  int j = 0;
+  Ring<kStages> ring, raw;
+  uint32_t qe[2] = {1, 1};  // parities of Q's release
+  int loaded = 0;           // stages used so far
   bool ok = true;
-  auto load_q = [&](int t, const Tile& d) {
-    if (d.steps == 0) return;
-    const uint32_t dst = c.sbase + kOffQ + t * kQTile, bar = c.leader_bar(B_Q + t);
-    const int row = it.q0 + d.row0;
-    announce(bar, kQTile);
-    tma_3d<kCtas>(dst, &m.q_nope, bar, 0, it.head, row);
-    tma_3d<kCtas>(dst + 2 * kBox, &m.q_nope, bar, 64, it.head, row);
-    tma_3d<kCtas>(dst + 4 * kBox, &m.q_pe, bar, 0, it.head, row);
-  };
-  load_q(0, ta);
-  for (; j < steps; ++j) {
-    const int stage = j % kStages;
-    const uint32_t parity = ((j / kStages) & 1) ^ 1, dst = c.sbase + kOffRing + stage * kStageBytes;
-    const int row = it.k0 + j * F::kKeys;
-    if (!(ok = c.wait(B_KE + stage, parity, 0xA11))) break;
-    {
-      const uint32_t bar = c.leader_bar(B_KF + stage);
-      announce(bar, kKBytes);
-      tma_3d<kCtas>(dst, &m.k_nope, bar, 0, it.head, row + 64 * c.rank);
-      tma_3d<kCtas>(dst + kBox, &m.k_nope, bar, 64, it.head, row + 64 * c.rank);
-      tma_3d<kCtas>(dst + 2 * kBox, &m.k_pe, bar, 0, 0, row + 64 * c.rank);
+  Item it;
+  for (int n = 0; ok && take_item(c, n, &it); ++n) {
+    const Tile tiles[2] = {tile_of<kCtas>(it, a.causal, 0, c.rank), tile_of<kCtas>(it, a.causal, 1, c.rank)};
+    const int steps = max(tiles[0].steps, tiles[1].steps), scan_from = first_scan<kCtas>(it, a.causal);
+    auto load_q = [&](int t) {
+      if (tiles[t].steps == 0) return true;
+      if (!c.wait_warp(B_QE + t, qe[t], 0xA10)) return false;
+      qe[t] ^= 1;
+      if (lane == 0) {
+        const uint32_t dst = c.sbase + kOffQ + t * kQTile, bar = c.leader_bar(B_Q + t);
+        const int row = it.q0 + tiles[t].row0;
+        announce(bar, kQTile);
+        tma_3d<kCtas>(dst, &m.q_nope, bar, 0, it.head, row);
+        tma_3d<kCtas>(dst + 2 * kBox, &m.q_nope, bar, 64, it.head, row);
+        tma_3d<kCtas>(dst + 4 * kBox, &m.q_pe, bar, 0, it.head, row);
+      }
+      __syncwarp();
+      return true;
+    };
+    ok = load_q(0);
+    for (int j = 0; ok && j < steps; ++j, ring.next()) {
+      const int stage = ring.slot;
+      const uint32_t dst = c.sbase + kOffRing + stage * kStageBytes;
+      const int row = it.k0 + j * F::kKeys;
+      if (!(ok = c.wait_warp(B_KE + stage, ring.phase ^ 1, 0xA11))) break;
+      if (lane == 0) {
+        const uint32_t bar = c.leader_bar(B_KF + stage);
+        announce(bar, kKBytes);
+        tma_3d<kCtas>(dst, &m.k_nope, bar, 0, it.head, row + 64 * c.rank);
+        tma_3d<kCtas>(dst + kBox, &m.k_nope, bar, 64, it.head, row + 64 * c.rank);
+        tma_3d<kCtas>(dst + 2 * kBox, &m.k_pe, bar, 0, 0, row + 64 * c.rank);
+      }
+      __syncwarp();
+      if (j == 0 && !(ok = load_q(1))) break;
+      if (!(ok = c.wait_warp(B_VE + stage, ring.phase ^ 1, 0xA12))) break;
+      ++loaded;
+      const bool scan = j >= scan_from;
+      if (lane == 0) {
+        const uint32_t bar = scan ? c.bar(B_RAW + raw.slot) : c.leader_bar(B_VF + stage);
+        if (scan)
+          mbar_arrive_expect_tx(bar, kVBytes);
+        else
+          announce(bar, kVBytes);
+        tma_3d<kCtas>(dst + kKBytes, &m.v, bar, 64 * c.rank, it.head, row);
+        if (kCtas == 1) tma_3d<kCtas>(dst + kKBytes + kBox, &m.v, bar, 64, it.head, row);
+      }
+      __syncwarp();
+      if (scan) raw.next();
     }
-    if (j == 0) load_q(1, tb);
-    if (!(ok = c.wait(B_VE + stage, parity, 0xA12))) break;
-    if (j < scan_from) {
-      const uint32_t bar = c.leader_bar(B_VF + stage);
-      announce(bar, kVBytes);
-      tma_3d<kCtas>(dst + kKBytes, &m.v, bar, 64 * c.rank, it.head, row);
-      if (kCtas == 1) tma_3d<kCtas>(dst + kKBytes + kBox, &m.v, bar, 64, it.head, row);
-    } else {
-      const uint32_t bar = c.bar(B_RAW + (j - scan_from) % kStages);
-      mbar_arrive_expect_tx(bar, kVBytes);
-      tma_3d<1>(dst + kKBytes, &m.v, bar, 64 * c.rank, it.head, row);
-      if (kCtas == 1) tma_3d<1>(dst + kKBytes + kBox, &m.v, bar, 64, it.head, row);
+    if (ok && c.rank == 0 && lane == 0) mbar_arrive(c.bar(B_NEXT));
+    __syncwarp();
+  }
+  if (!ok) {  // the copies in flight land within a few microseconds
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000) {
     }
   }
   // Every copy has landed, and every arrival that the products send here has come
   // in, before this CTA may leave.  (The products follow the copies.)
-  for (int i = max(0, j - kStages); i < j; ++i) {
-    c.wait_limited(B_KE + i % kStages, (i / kStages) & 1);
-    c.wait_limited(B_VE + i % kStages, (i / kStages) & 1);
+  for (int k = 0; k < kStages; ++k, ring.next()) {  // from the oldest stage on
+    if (k < kStages - loaded) continue;             // never used
+    c.wait_limited(B_KE + ring.slot, ring.phase ^ 1);
+    c.wait_limited(B_VE + ring.slot, ring.phase ^ 1);
   }
 }
 
@@ -439,55 +591,72 @@ __device__ __forceinline__ uint32_t elect_one() {
   return e;
 }
 
-// Run by a whole warp.
+// Run by a whole warp.  In turn: O += P V of a tile's last step and S = Q K^T of its
+// next one, then the same of the other tile, on through all items.
 template <int kCtas>
-__device__ void issue_products(const Ctx<kCtas>& c, uint32_t tmem, const Tile& ta, const Tile& tb) {
+__device__ void issue_products(const Ctx<kCtas>& c, const Args& a, uint32_t tmem) {
   using F = Form<kCtas>;
   constexpr uint32_t kIdescS = idesc_f32acc(F::kTileRows, F::kKeys, 0, 0, 1);
   constexpr uint32_t kIdescO = idesc_f32acc(F::kTileRows, 128, 0, 1, 1);
-  const int steps[2] = {ta.steps, tb.steps};
-  const int total = max(ta.steps, tb.steps);
   const uint32_t go = elect_one();
   const uint32_t q0 = desc_low(c.sbase + kOffQ, 16), k0 = desc_low(c.sbase + kOffRing, 16);
   const uint32_t v0 = desc_low(c.sbase + kOffRing + kKBytes, kBox);
-  bool ok = true;
-  int ks = 0, vs = 0;            // stages of step j's keys and of step j - 1's values
-  uint32_t kp = 0, vp = 0;       // ... and their parities
-  for (int j = 0; ok && j <= total; ++j) {
+  Ring<kStages> kr, vr;              // the next step's keys, the last step's values
+  uint32_t qp[2] = {0, 0}, pp[2] = {0, 0};  // parities of Q and of P
+  bool due[2] = {false, false};      // the last step's second product is still to come
+  bool first[2], last[2];            // ... of that step in its item
+  bool ok = true, more = true;
+  Item it;
+  for (int n = 0; ok && more;) {
+    // What is still to come is not held up by an item that is not there yet.
+    const bool take = !(due[0] || due[1]) || c.ready(B_ITEM + n % kItemSlots, (n / kItemSlots) & 1);
+    if (take) more = take_item(c, n++, &it);
+    const bool keys = take && more;
+    const int steps[2] = {keys ? tile_of<kCtas>(it, a.causal, 0, 0).steps : 0,
+                          keys ? tile_of<kCtas>(it, a.causal, 1, 0).steps : 0};
+    const int total = keys ? max(steps[0], steps[1]) : 1;
+    for (int j = 0; ok && j < total; ++j) {
+      const bool was[2] = {due[0], due[1]};
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      if (j > 0 && j - 1 < steps[t]) {
-        // ---- O += P V of step j - 1
-        if ((t == 0 || j - 1 >= steps[0]) && !(ok = c.wait_uniform(B_VF + vs, vp, 0xA13))) break;
-        if (!(ok = c.wait_uniform(B_P + t, (j - 1) & 1, 0xA14))) break;
-        tc_fence_after();
-        const uint32_t v = v0 + vs * (kStageBytes >> 4);
+      for (int t = 0; t < 2; ++t) {
+        if (was[t]) {
+          if ((t == 0 || !was[0]) && !(ok = c.wait_uniform(B_VF + vr.slot, vr.phase, 0xA13))) break;
+          const uint32_t v = v0 + vr.slot * (kStageBytes >> 4);
+          const uint32_t d = tmem + TM_O + 128 * t, p = tmem + TM_S + 128 * t;
 #pragma unroll
-        for (int kk = 0; kk < F::kKeys / 64; ++kk)  // 64 value columns of a key are 128 bytes
-          products_ts<kCtas>(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + 32 * kk, v + kk * 512, kIdescO, j > 1 || kk > 0, go);
-        if (j == steps[t]) commit<kCtas>(c.bar(B_O + t), go);
-        if (t == 1 || j - 1 >= steps[1]) commit<kCtas>(c.bar(B_VE + vs), go);  // its last reader
+          for (int half = 0; half < kCtas; ++half) {  // 64 keys each; 64 value columns of a key are 128 bytes
+            if (!(ok = c.wait_uniform(B_P + 2 * t + half, pp[t], 0xA14))) break;
+            tc_fence_after();
+            products_ts<kCtas>(d, p + 32 * half, v + 512 * half, kIdescO, !first[t] || half > 0, go);
+          }
+          if (!ok) break;
+          pp[t] ^= 1;
+          if (last[t]) commit<kCtas>(c.bar(B_O + t), go);
+          if (t == 1 || !was[1]) commit<kCtas>(c.bar(B_VE + vr.slot), go);  // its last reader
+        }
+        if (j < steps[t]) {
+          if ((t == 0 || j >= steps[0]) && !(ok = c.wait_uniform(B_KF + kr.slot, kr.phase, 0xA15))) break;
+          if (j == 0) {
+            if (!(ok = c.wait_uniform(B_Q + t, qp[t], 0xA16))) break;
+            qp[t] ^= 1;
+          }
+          tc_fence_after();
+          const uint32_t q = q0 + t * (kQTile >> 4), k = k0 + kr.slot * (kStageBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 3; ++kk)
+            products_ss<kCtas>(tmem + TM_S + 128 * t, q + kk * (2 * kBox >> 4), k + kk * (kBox >> 4), kIdescS, kk > 0, go);
+          commit<kCtas>(c.bar(B_S + t), go);
+          if (j == steps[t] - 1) commit<kCtas>(c.bar(B_QE + t), go);
+          if (t == 1 || j >= steps[1]) commit<kCtas>(c.bar(B_KE + kr.slot), go);
+          due[t] = true;
+          first[t] = j == 0;
+          last[t] = j == steps[t] - 1;
+        } else {
+          due[t] = false;
+        }
       }
-      if (j < steps[t]) {
-        // ---- S = Q K^T of step j
-        if ((t == 0 || j >= steps[0]) && !(ok = c.wait_uniform(B_KF + ks, kp, 0xA15))) break;
-        if (j == 0 && !(ok = c.wait_uniform(B_Q + t, 0, 0xA16))) break;
-        tc_fence_after();
-        const uint32_t q = q0 + t * (kQTile >> 4), k = k0 + ks * (kStageBytes >> 4);
-#pragma unroll
-        for (int kk = 0; kk < 3; ++kk)
-          products_ss<kCtas>(tmem + TM_S + 128 * t, q + kk * (2 * kBox >> 4), k + kk * (kBox >> 4), kIdescS, kk > 0, go);
-        commit<kCtas>(c.bar(B_S + t), go);
-        if (t == 1 || j >= steps[1]) commit<kCtas>(c.bar(B_KE + ks), go);
-      }
-    }
-    if (j > 0 && ++vs == kStages) {
-      vs = 0;
-      vp ^= 1;
-    }
-    if (++ks == kStages) {
-      ks = 0;
-      kp ^= 1;
+      if (was[0] || was[1]) vr.next();
+      if (keys) kr.next();
     }
   }
   // every product is done before TMEM is released
@@ -497,40 +666,49 @@ __device__ void issue_products(const Ctx<kCtas>& c, uint32_t tmem, const Tile& t
 
 // ------------------------------------------------------------------ value scan
 
-// Zeros in the place of what is not finite, in this CTA's values from step
-// scan_from on.
+// Zeros in the place of what is not finite, in this CTA's share of the values that
+// some row does not see whole.  An item whose own keys have such values is noted
+// (kPoisons flags: the scan is at most three items ahead of the epilogue).
 template <int kCtas>
-__device__ void scan_values(const Ctx<kCtas>& c, const Item& it, int steps, int scan_from, int lane) {
+__device__ void scan_values(const Ctx<kCtas>& c, const Args& a, int lane) {
   using F = Form<kCtas>;
-  for (int j = scan_from; j < steps; ++j) {
-    const int stage = j % kStages, scans = j - scan_from;
-    if (!c.wait_warp(B_RAW + scans % kStages, (scans / kStages) & 1, 0xA17)) return;
-    const uint32_t base = c.sbase + kOffRing + stage * kStageBytes + kKBytes + lane * 16;
-    bool seen = false;
+  Ring<kStages> ring, raw;
+  Item it;
+  for (int n = 0; take_item(c, n, &it); ++n) {
+    const int steps = max(tile_of<kCtas>(it, a.causal, 0, 0).steps, tile_of<kCtas>(it, a.causal, 1, 0).steps);
+    const int scan_from = first_scan<kCtas>(it, a.causal);
+    flag_store(c.sbase + kOffPoison + 4 * ((n + kPoisons / 2) % kPoisons), 0);
+    for (int j = 0; j < steps; ++j, ring.next()) {
+      if (j < scan_from) continue;
+      if (!c.wait_warp(B_RAW + raw.slot, raw.phase, 0xA17)) return;
+      raw.next();
+      const uint32_t base = c.sbase + kOffRing + ring.slot * kStageBytes + kKBytes + lane * 16;
+      bool seen = false;
 #pragma unroll 8
-    for (int i = 0; i < kVBytes / 512; ++i) {
-      uint4 x = ld_shared_v4(base + i * 512);
-      constexpr uint32_t kExp = 0x7F807F80u;
-      const uint32_t b0 = __vcmpeq2(x.x & kExp, kExp), b1 = __vcmpeq2(x.y & kExp, kExp), b2 = __vcmpeq2(x.z & kExp, kExp),
-                     b3 = __vcmpeq2(x.w & kExp, kExp);
-      if (b0 | b1 | b2 | b3) {
-        x.x &= ~b0;
-        x.y &= ~b1;
-        x.z &= ~b2;
-        x.w &= ~b3;
-        st_shared_v4(base + i * 512, x);
-        // a key is 128 bytes; one CTA alone holds two boxes of 64 keys
-        seen |= j * F::kKeys + (i * 4 + (lane >> 3)) % F::kKeys < it.lk;
+      for (int i = 0; i < kVBytes / 512; ++i) {
+        uint4 x = ld_shared_v4(base + i * 512);
+        constexpr uint32_t kExp = 0x7F807F80u;
+        const uint32_t b0 = __vcmpeq2(x.x & kExp, kExp), b1 = __vcmpeq2(x.y & kExp, kExp), b2 = __vcmpeq2(x.z & kExp, kExp),
+                       b3 = __vcmpeq2(x.w & kExp, kExp);
+        if (b0 | b1 | b2 | b3) {
+          x.x &= ~b0;
+          x.y &= ~b1;
+          x.z &= ~b2;
+          x.w &= ~b3;
+          st_shared_v4(base + i * 512, x);
+          // a key is 128 bytes; one CTA alone holds two boxes of 64 keys
+          seen |= j * F::kKeys + (i * 4 + (lane >> 3)) % F::kKeys < it.lk;
+        }
       }
-    }
-    if (seen) flag_store(c.sbase + kOffPoison, 1);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      if (kCtas > 1)
-        mbar_arrive_remote(c.leader_bar(B_VF + stage));
-      else
-        mbar_arrive(c.bar(B_VF + stage));
+      if (seen) flag_store(c.sbase + kOffPoison + 4 * (n % kPoisons), 1);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (kCtas > 1)
+          mbar_arrive_remote(c.leader_bar(B_VF + ring.slot));
+        else
+          mbar_arrive(c.bar(B_VF + ring.slot));
+      }
     }
   }
 }
@@ -543,7 +721,7 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 }
 #define MLA_I8(b) "r"(r[b + 0]), "r"(r[b + 1]), "r"(r[b + 2]), "r"(r[b + 3]), "r"(r[b + 4]), "r"(r[b + 5]), \
                   "r"(r[b + 6]), "r"(r[b + 7])
-__device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
       "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
@@ -585,121 +763,198 @@ __device__ __forceinline__ void arrive_leader(const Ctx<kCtas>& c, int bar) {
     mbar_arrive(c.bar(bar));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+union Pair {
+  float2 f;
+  uint64_t u;
+};
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  Pair x, y, z, d;
+  x.f = a; y.f = b; z.f = c;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.u) : "l"(x.u), "l"(y.u), "l"(z.u));
+  return d.f;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  Pair x, y, d;
+  x.f = a; y.f = b;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(x.u), "l"(y.u));
+  return d.f;
+}
+
+// Weights 2^(c s - base) of 32 scores, packed, and their sum onto two pairs.
+__device__ __forceinline__ void weights32(const uint32_t (&s)[32], float2 scale, float base, uint32_t* p, float2 (&sum)[2]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float2 x = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), scale, make_float2(-base, -base));
+    x.x = ex2_approx(x.x);
+    x.y = ex2_approx(x.y);
+    sum[i & 1] = add2(sum[i & 1], x);
+    p[i] = pack(x.x, x.y);
+  }
+}
+__device__ __forceinline__ void mask32(uint32_t (&s)[32], int left) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i >= left) s[i] = 0xFF800000u;  // -inf
+}
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+  float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
+#pragma unroll
+  for (int i = 2; i < 32; i += 4) {
+    a = max3(a, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+    if (i + 3 < 32) b = max3(b, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+  }
+  return fmaxf(a, b);
+}
+
+// The softmax and the epilogue of one tile, for every item: four warps, a row a
+// thread.  The weights of a step's first half are made with the running maximum as it
+// was, while the step's own is found (the exponentials' pipe and the comparisons' run
+// side by side); should it have to move, which is rare after the first step, they
+// are made again.  The first half is handed to the tensor core before the second one
+// is made.
 template <int kCtas>
-__device__ void softmax_tile(const Ctx<kCtas>& c, const Args& a, const Item& it, const Tile& d, int t, int scan_from,
-                             uint32_t tmem) {
+__device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_t tmem) {
   using F = Form<kCtas>;
   constexpr int kParts = F::kKeys / 32;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
-  const int row = d.row0 + quad * 32 + lane;  // within the request
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t ts = tmem + lanes + TM_S + 128 * t, to = tmem + lanes + TM_O + 128 * t;
-  if (d.rows == 0) {  // the tile's rows are the other CTA's
-    for (int j = 0; j < d.steps; ++j) {
-      if (!c.wait_warp(B_S + t, j & 1, 0xA18)) return;
-      if (lane == 0) arrive_leader(c, B_P + t);
-    }
-    return;
-  }
-  const int seen = visible(it, a.causal, min(row, it.lq - 1));
   const float slack = kRescaleLog2 / a.scale_log2;
-  float top = -CUDART_INF_F, sum = 0.f;  // the running maximum (of S) and sum
-  for (int j = 0; j < d.steps; ++j) {
-    if (!c.wait_warp(B_S + t, j & 1, 0xA18)) return;
-    tc_fence_after();
-    uint32_t s[kParts][32];
-#pragma unroll
-    for (int q = 0; q < kParts; ++q) tmem_ld32_async(ts + 32 * q, s[q]);
-#pragma unroll
-    for (int q = 0; q < kParts; ++q) tmem_wait_ld32(s[q]);
-    if (j >= d.masked) {
+  const float2 scale = make_float2(a.scale_log2, a.scale_log2);
+  uint32_t sp = 0, op = 0;  // parities of S and O
+  Item it;
+  for (int n = 0; take_item(c, n, &it); ++n) {
+    const Tile d = tile_of<kCtas>(it, a.causal, t, c.rank);
+    if (d.rows == 0) {  // the tile's rows are the other CTA's, or there are none
+      for (int j = 0; j < d.steps; ++j, sp ^= 1) {
+        if (!c.wait_warp(B_S + t, sp, 0xA18)) return;
+        if (lane == 0)
+          for (int half = 0; half < kCtas; ++half) arrive_leader(c, B_P + 2 * t + half);
+      }
+      if (d.steps > 0) op ^= 1;
+      continue;
+    }
+    const int row = d.row0 + quad * 32 + lane;  // within the request
+    const int seen = visible(it, a.causal, min(row, it.lq - 1));
+    float top = -CUDART_INF_F, base = 0.f;  // the running maximum of S, and of c S (0 while there is none)
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    for (int j = 0; j < d.steps; ++j, sp ^= 1) {
+      if (!c.wait_warp(B_S + t, sp, 0xA18)) return;
+      tc_fence_after();
+      constexpr int kHalf = kParts / 2;
+      const bool masked = j >= d.masked;
       const int left = seen - j * F::kKeys;
+      uint32_t s[kHalf][32], p[16 * kHalf];
+      float here;
+      {
+        uint32_t u[kHalf][32];  // the second half, for the maximum
 #pragma unroll
-      for (int q = 0; q < kParts; ++q)
+        for (int q = 0; q < kHalf; ++q) tmem_ld32_async(ts + 32 * q, s[q]);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (32 * q + i >= left) s[q][i] = 0xFF800000u;  // -inf
-    }
-    float high[kParts];
+        for (int q = 0; q < kHalf; ++q) tmem_ld32_async(ts + 32 * (kHalf + q), u[q]);
 #pragma unroll
-    for (int q = 0; q < kParts; ++q) {
-      high[q] = __uint_as_float(s[q][0]);
+        for (int q = 0; q < kHalf; ++q) {
+          tmem_wait_ld32(s[q]);
+          if (masked) mask32(s[q], left - 32 * q);
+        }
 #pragma unroll
-      for (int i = 1; i < 32; ++i) high[q] = fmaxf(high[q], __uint_as_float(s[q][i]));
-    }
-    float here = fmaxf(high[0], high[1]);
-    if (kParts == 4) here = fmaxf(here, fmaxf(high[kParts - 2], high[kParts - 1]));
-    const bool move = here > top + slack;
-    if (__any_sync(0xffffffffu, move)) {
-      const float factor = move ? ex2_approx((top - here) * a.scale_log2) : 1.f;
-      if (move) top = here;
-      sum *= factor;
-      if (j > 0) {
+        for (int q = 0; q < kHalf; ++q) {
+          tmem_wait_ld32(u[q]);
+          if (masked) mask32(u[q], left - 32 * (kHalf + q));
+        }
+        here = fmaxf(max32(s[0]), max32(u[0]));
+        if (kHalf == 2) here = max3(here, max32(s[kHalf - 1]), max32(u[kHalf - 1]));
+      }
+      float2 more[2] = {sum[0], sum[1]};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t o[32];
-          tmem_ld32(to + 32 * q, o);
+      for (int q = 0; q < kHalf; ++q) weights32(s[q], scale, base, p + 16 * q, more);
+      const bool move = here > top + slack;
+      if (__any_sync(0xffffffffu, move)) {
+        const float factor = move ? ex2_approx((top - here) * a.scale_log2) : 1.f;
+        if (move) {
+          top = here;
+          base = here * a.scale_log2;
+        }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-          tmem_st32(to + 32 * q, o);
+        for (int i = 0; i < 2; ++i) more[i] = sum[i] = make_float2(sum[i].x * factor, sum[i].y * factor);
+#pragma unroll
+        for (int q = 0; q < kHalf; ++q) weights32(s[q], scale, base, p + 16 * q, more);
+        if (j > 0) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[32];
+            tmem_ld32(to + 32 * q, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+            tmem_st32(to + 32 * q, o);
+          }
         }
       }
-    }
-    const float base = top == -CUDART_INF_F ? 0.f : top * a.scale_log2;
-    float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int q = 0; q < kParts; ++q) {
+      for (int q = 0; q < kHalf; ++q) tmem_st16_async(ts + 16 * q, p + 16 * q);
+#pragma unroll
+      for (int q = 0; q < kHalf; ++q) tmem_ld32_async(ts + 32 * (kHalf + q), s[q]);  // (P ends before)
+      if (kCtas > 1) {
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader(c, B_P + 2 * t);
+      }
+#pragma unroll
+      for (int q = 0; q < kHalf; ++q) {
+        tmem_wait_ld32(s[q]);
+        if (masked) mask32(s[q], left - 32 * (kHalf + q));
+        weights32(s[q], scale, base, p + 16 * q, more);
+        tmem_st16_async(ts + 16 * (kHalf + q), p + 16 * q);
+      }
+      sum[0] = more[0];
+      sum[1] = more[1];
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_leader(c, B_P + 2 * t + kCtas - 1);
+    }
+    // ---- epilogue
+    if (d.steps > 0) {
+      if (!c.wait_warp(B_O + t, op, 0xA19)) return;
+      op ^= 1;
+      tc_fence_after();
+    }
+    const float total = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    const bool mine = row < it.lq;
+    const bool none = total == 0.f;  // no key, or scores of -inf alone
+    const float inv = 1.f / total;
+    const bool poison = flag_load(c.sbase + kOffPoison + 4 * (n % kPoisons)) != 0;
+    const int64_t token = it.q0 + row;
+    uint16_t* out = a.out + token * a.out_ts + it.head * a.out_hs;
+    const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      uint32_t r[32];
+      if (d.steps > 0) tmem_ld32(to + 32 * q, r);
+      float o[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : __uint_as_float(r[i]) * inv;
+      if (poison && mine && !none) {
+        const uint16_t* v = a.v + it.k0 * a.v_ts + it.head * a.v_hs + 32 * q;
+        const int from = first_scan<kCtas>(it, a.causal) * F::kKeys;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] += non_finite(v + i, a.v_ts, from, seen);
+      }
       uint32_t p[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float x = ex2_approx(fmaf(__uint_as_float(s[q][2 * i]), a.scale_log2, -base));
-        const float y = ex2_approx(fmaf(__uint_as_float(s[q][2 * i + 1]), a.scale_log2, -base));
-        add[i & 3] += x + y;
-        p[i] = pack(x, y);
+      for (int i = 0; i < 16; ++i) p[i] = pack(o[2 * i], o[2 * i + 1]);
+      if (mine) {
+        store32(out + 32 * q, p, wide);
+        store32(out + 32 * q + 16, p + 8, wide);
       }
-      tmem_st16_async(ts + 16 * q, p);
     }
-    sum += (add[0] + add[1]) + (add[2] + add[3]);
-    tmem_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) arrive_leader(c, B_P + t);
-  }
-  // ---- epilogue
-  if (d.steps > 0) {
-    if (!c.wait_warp(B_O + t, 0, 0xA19)) return;
-    tc_fence_after();
-  }
-  const bool mine = row < it.lq;
-  const bool none = sum == 0.f;  // no key, or scores of -inf alone
-  const float inv = 1.f / sum;
-  const bool poison = flag_load(c.sbase + kOffPoison) != 0;
-  const int64_t token = it.q0 + row;
-  uint16_t* out = a.out + token * a.out_ts + it.head * a.out_hs;
-  const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
-#pragma unroll 1
-  for (int q = 0; q < 4; ++q) {
-    uint32_t r[32];
-    if (d.steps > 0) tmem_ld32(to + 32 * q, r);
-    float o[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : __uint_as_float(r[i]) * inv;
-    if (poison && mine && !none) {
-      const uint16_t* v = a.v + it.k0 * a.v_ts + it.head * a.v_hs + 32 * q;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] += non_finite(v + i, a.v_ts, scan_from * F::kKeys, seen);
-    }
-    uint32_t p[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) p[i] = pack(o[2 * i], o[2 * i + 1]);
-    if (mine) {
-      store32(out + 32 * q, p, wide);
-      store32(out + 32 * q + 16, p + 8, wide);
-    }
-  }
-  if (mine) {
-    const float base = top == -CUDART_INF_F ? 0.f : top * a.scale_log2;
-    a.lse[token * a.heads + it.head] = none ? -CUDART_INF_F : fmaf(base, CUDART_LN2_F, logf(sum));
+    if (mine) a.lse[token * a.heads + it.head] = none ? -CUDART_INF_F : fmaf(base, CUDART_LN2_F, logf(total));
   }
 }
 
@@ -730,25 +985,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   c.rank = kCtas > 1 ? (int)cluster_ctarank() : 0;
   c.leader = kCtas > 1 ? mapa(c.sbase, 0) : c.sbase;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int index = (int)blockIdx.x / kCtas;
-  volatile int* slot = reinterpret_cast<volatile int*>(smem + kOffItem);  // the item; [6]: whether there is one
   if (warp == 0) {
-    Item it{};
-    const bool found = find_item<Form<kCtas>::kItemRows>(a, index % a.tiles, lane, &it);
     if (lane == 0) {
-      slot[0] = it.q0;
-      slot[1] = it.lq;
-      slot[2] = it.k0;
-      slot[3] = it.lk;
-      slot[4] = it.row0;
-      slot[6] = found;
       flag_store(c.sbase + kOffAbort, 0);
-      flag_store(c.sbase + kOffPoison, 0);
+      for (int i = 0; i < kPoisons; ++i) flag_store(c.sbase + kOffPoison + 4 * i, 0);
       for (int t = 0; t < 2; ++t) {
         mbar_init(c.bar(B_Q + t), kCtas);
         mbar_init(c.bar(B_QE + t), 1);
         mbar_init(c.bar(B_S + t), 1);
-        mbar_init(c.bar(B_P + t), 4 * kCtas);
+        mbar_init(c.bar(B_P + 2 * t), 4 * kCtas);
+        mbar_init(c.bar(B_P + 2 * t + 1), 4 * kCtas);
         mbar_init(c.bar(B_O + t), 1);
       }
       for (int i = 0; i < kStages; ++i) {
@@ -758,6 +1004,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         mbar_init(c.bar(B_VE + i), 1);
         mbar_init(c.bar(B_RAW + i), 1);
       }
+      for (int i = 0; i < kItemSlots; ++i) {
+        mbar_init(c.bar(B_ITEM + i), 1);
+        mbar_init(c.bar(B_TAKEN + i), 10 * kCtas + 1);  // copies, scan, softmax; and the leader's products
+      }
+      mbar_init(c.bar(B_NEXT), 1);
+      mbar_init(c.bar(B_ASKED), 1);
       mbar_init(c.bar(B_FIN), 1);
       fence_mbar_init();
       prefetch_tensormap(&maps.q_nope);
@@ -775,32 +1027,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   if (kCtas > 1) cluster_sync();  // the peer's barriers are initialised before any arrival there
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem);
-  Item it;
-  it.q0 = slot[0];
-  it.lq = slot[1];
-  it.k0 = slot[2];
-  it.lk = slot[3];
-  it.row0 = slot[4];
-  it.head = index / a.tiles;
-  if (slot[6]) {
-    const Tile ta = tile_of<kCtas>(it, a.causal, 0, c.rank), tb = tile_of<kCtas>(it, a.causal, 1, c.rank);
-    const int scan_from = first_scan<kCtas>(it, a.causal);
-    if (warp < 4) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
-      if (warp == 0 && lane == 0) load_item(c, maps, it, ta, tb, scan_from);
-      if (warp == 1) {
-        if (c.rank == 0)
-          issue_products(c, tmem, ta, tb);
-        else
-          c.wait_limited(B_FIN, 0);  // the leader's last arrival here
-      }
-      if (warp == 2) scan_values(c, it, max(ta.steps, tb.steps), scan_from, lane);
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
+    if (warp == 0) {
+      load_items(c, a, maps, lane);
+    } else if (warp == 1) {
+      if (c.rank == 0)
+        issue_products(c, a, tmem);
+      else
+        c.wait_limited(B_FIN, 0);  // the leader's last arrival here
+    } else if (warp == 2) {
+      scan_values(c, a, lane);
+    } else if (c.rank == 0) {
+      schedule(c, a, lane);
     } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-      const int t = (warp - 4) >> 2;
-      const Tile d = t ? tb : ta;
-      softmax_tile(c, a, it, d, t, scan_from, tmem);
+      receive(c, lane);
     }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    softmax_items(c, a, (warp - 4) >> 2, tmem);
   }
   __syncwarp();
   tc_fence_before();
