@@ -35,11 +35,14 @@
 //
 // Masked places.  Scores past a row's last key are replaced by -inf, so keys
 // there may hold anything.  Values there are multiplied by P = 0, which leaves
-// NaN of an infinity or a NaN; so a warp looks through the value tiles that
-// some row does not see whole, and puts zeros in the place of what is not finite.
-// The rows that do see such a value get it in the epilogue.
+// NaN of an infinity or a NaN; so the value tiles that some row does not see whole
+// are looked through before they are used, and zeros put in the place of what is not
+// finite.  The rows that do see such a value get it in the epilogue.
 //
-// Warps: 0 TMA, 1 MMA, 2 value scan, 3 items, 4-7 softmax of the first tile,
+// Few row blocks and many keys: the keys of a block are cut into parts, each an item of
+// its own, whose results in fp32 a second kernel merges.
+//
+// Warps: 0 TMA, 1 MMA, 2 none, 3 items, 4-7 softmax of the first tile,
 // 8-11 of the second.  Waits are bounded: on timeout the error word is set, every role
 // stops, copies and products in flight are awaited, TMEM is freed.
 #include <cuda.h>
@@ -48,7 +51,9 @@
 #include <cudaTypedefs.h>
 #include <math_constants.h>
 
+#include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/mla_decode.h"
 #include "mla_internal.h"
@@ -91,9 +96,9 @@ enum Bar : int {
   B_QE = B_Q + 2,                 // [tile] Q is read
   B_KF = B_QE + 2,                // [stage] keys landed (the leader's)
   B_KE = B_KF + kStages,          // [stage] keys are read
-  B_VF = B_KE + kStages,          // [stage] values landed and, where masked, looked through (the leader's)
+  B_VF = B_KE + kStages,          // [stage] values landed (the leader's); not those to be looked through
   B_VE = B_VF + kStages,          // [stage] values are read
-  B_RAW = B_VE + kStages,         // [scan % 3] values landed, for the scan
+  B_RAW = B_VE + kStages,         // [look % 3] values to be looked through landed
   B_S = B_RAW + kStages,          // [tile] scores are in TMEM
   B_P = B_S + 2,                  // [2 tile + half] weights are in TMEM, O is rescaled (the leader's)
   B_O = B_P + 4,                  // [tile] the tile's products are done
@@ -124,7 +129,10 @@ struct Args {
   float* lse;
   int64_t v_ts, v_hs, out_ts, out_hs;  // strides of a token and a head, in elements
   int32_t batch, heads, tokens_q, tokens_k;
-  int32_t tiles;   // items of a head: at most this many exist
+  int32_t tiles;   // row blocks of a head: at most this many exist
+  int32_t parts;   // items of a row block: each has a part of the keys
+  float* part_out; // [part][token][head][128], [part][token][head]: what a part alone gives
+  float* part_lse;
   int32_t causal;
   float scale_log2;  // scale * log2(e)
 };
@@ -132,39 +140,55 @@ struct Args {
 struct Item {
   int q0, lq, k0, lk;  // the request's rows and keys
   int head, row0;      // first query row of the item within the request
+  int part;            // of the keys' steps
   int more;            // 0: there is no item, the work is done
 };
 
-// What a CTA does of one tile of an item.
+// What a CTA does of an item.
 struct Tile {
   int row0, rows;  // this CTA's, within the request
-  int steps;       // of the tile: steps with a key that a row of it sees
+  int steps;       // with a key that a row of the tile (of both CTAs) sees
   int masked;      // first step that some row of this CTA does not see whole
+};
+struct Work {
+  Tile tile[2];
+  int begin;   // first step of the item, in the request's keys; the others count from it
+  int steps;   // of the longer tile
+  int look;    // first step whose values are looked through: some row does not see it whole
 };
 
 __device__ __forceinline__ int visible(const Item& it, int causal, int row) {
   return causal ? max(0, min(it.lk, it.lk - it.lq + 1 + row)) : it.lk;
 }
 template <int kCtas>
-__device__ __forceinline__ Tile tile_of(const Item& it, int causal, int t, int rank) {
+__device__ __forceinline__ Work work_of(const Item& it, const Args& a, int rank) {
   using F = Form<kCtas>;
-  Tile d;
-  const int first = it.row0 + t * F::kTileRows, last = min(first + F::kTileRows, it.lq) - 1;
-  d.row0 = first + rank * kRows;
-  d.rows = max(0, min(kRows, it.lq - d.row0));
-  d.steps = last >= first ? (visible(it, causal, last) + F::kKeys - 1) / F::kKeys : 0;
-  d.masked = visible(it, causal, min(d.row0, it.lq - 1)) / F::kKeys;
-  return d;
-}
-// First step whose values are looked through: one that some row does not see whole.
-template <int kCtas>
-__device__ __forceinline__ int first_scan(const Item& it, int causal) {
-  int from = INT32_MAX;
+  Work w;
+  int all[2], total = 0;
+#pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const Tile d = tile_of<kCtas>(it, causal, t, 0);
-    if (d.steps) from = min(from, d.masked);
+    const int first = it.row0 + t * F::kTileRows, last = min(first + F::kTileRows, it.lq) - 1;
+    w.tile[t].row0 = first + rank * kRows;
+    w.tile[t].rows = max(0, min(kRows, it.lq - w.tile[t].row0));
+    all[t] = last >= first ? (visible(it, a.causal, last) + F::kKeys - 1) / F::kKeys : 0;
+    total = max(total, all[t]);
   }
-  return from;
+  w.begin = 0;
+  int end = total;
+  if (a.parts > 1) {
+    w.begin = (int)((int64_t)total * it.part / a.parts);
+    end = (int)((int64_t)total * (it.part + 1) / a.parts);
+  }
+  w.steps = end - w.begin;
+  w.look = w.steps;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    w.tile[t].steps = max(0, min(all[t], end) - w.begin);
+    w.tile[t].masked = visible(it, a.causal, min(w.tile[t].row0, it.lq - 1)) / F::kKeys - w.begin;
+    if (w.tile[t].steps > 0)
+      w.look = min(w.look, max(0, visible(it, a.causal, it.row0 + t * F::kTileRows) / F::kKeys - w.begin));
+  }
+  return w;
 }
 
 // Item `idx` of a head: requests own ceil(rows / kItemRows) items each, those with the
@@ -303,12 +327,21 @@ __device__ __forceinline__ int read_answer(uint32_t answer) {
   return got ? (int)x : -1;
 }
 
+// The item that the CTA of this number starts with, for a converged warp.
+template <int kCtas>
+__device__ __forceinline__ bool item_of(const Args& a, int cta, int lane, Item* it) {
+  const int index = cta / kCtas, rest = index / a.tiles;
+  it->head = rest / a.parts;
+  it->part = rest - it->head * a.parts;
+  return find_item<Form<kCtas>::kItemRows>(a, index - rest * a.tiles, lane, it);
+}
+
 // Run by a warp of the leader: finds items and hands them to both CTAs.
 template <int kCtas>
-__device__ void schedule(const Ctx<kCtas>& c, const Args& a, int lane) {
+__device__ void schedule(const Ctx<kCtas>& c, const Args& a, Item it, int lane) {
   const uint32_t peer_items = kCtas > 1 ? mapa(c.sbase + kOffItem, 1) : 0;
   const uint32_t peer_bars = kCtas > 1 ? mapa(c.bar(B_ITEM), 1) : 0;
-  int cta = (int)blockIdx.x, asked = 0;
+  int cta = (int)blockIdx.x, asked = 0;  // it: this CTA's own item, if there is one
   auto answered = [&] {
     const uint32_t parity = asked++ & 1;
     if (c.wait_warp(B_ASKED, parity, 0xA1A)) return true;
@@ -316,11 +349,8 @@ __device__ void schedule(const Ctx<kCtas>& c, const Args& a, int lane) {
     return false;
   };
   for (int n = 0;; ++n) {
-    Item it{};
-    while (cta >= 0) {
-      const int index = cta / kCtas;
-      it.head = index / a.tiles;
-      it.more = find_item<Form<kCtas>::kItemRows>(a, index - it.head * a.tiles, lane, &it);
+    for (bool known = n == 0; cta >= 0; known = false) {
+      if (!known) it.more = item_of<kCtas>(a, cta, lane, &it);
       if (it.more) break;
       // fewer items than there could have been: on to the next one
       if (lane == 0) {
@@ -331,17 +361,18 @@ __device__ void schedule(const Ctx<kCtas>& c, const Args& a, int lane) {
       if (!answered()) return;
       cta = read_answer(c.sbase + kOffAnswer);
     }
+    if (cta < 0) it.more = 0;
     const int slot = n % kItemSlots;
     if (n >= kItemSlots && !c.wait_warp(B_TAKEN + slot, (n / kItemSlots + 1) & 1, 0xA1B)) return;
     if (lane == 0) {
       const uint32_t dst = kOffItem + slot * kItemBytes;
       st_shared_v4(c.sbase + dst, make_uint4(it.q0, it.lq, it.k0, it.lk));
-      st_shared_v4(c.sbase + dst + 16, make_uint4(it.head, it.row0, it.more, 0));
+      st_shared_v4(c.sbase + dst + 16, make_uint4(it.head, it.row0, it.part, it.more));
       mbar_arrive(c.bar(B_ITEM + slot));
       if (kCtas > 1) {
         const uint32_t to = peer_items + slot * kItemBytes, bar = peer_bars + 8 * slot;
         st_async_v4(to, it.q0, it.lq, it.k0, it.lk, bar);
-        st_async_v4(to + 16, it.head, it.row0, it.more, 0, bar);
+        st_async_v4(to + 16, it.head, it.row0, it.part, it.more, bar);
       }
     }
     __syncwarp();
@@ -364,7 +395,7 @@ __device__ void receive(const Ctx<kCtas>& c, int lane) {
     if (lane == 0) mbar_arrive_expect_tx(c.bar(B_ITEM + slot), kItemBytes);
     __syncwarp();
     if (!c.wait_warp(B_ITEM + slot, (n / kItemSlots) & 1, 0xA1E)) return;
-    if (flag_load(c.sbase + kOffItem + slot * kItemBytes + 24) == 0) return;
+    if (flag_load(c.sbase + kOffItem + slot * kItemBytes + 28) == 0) return;
   }
 }
 
@@ -381,7 +412,8 @@ __device__ __forceinline__ bool take_item(const Ctx<kCtas>& c, int n, Item* it) 
   it->lk = x.w;
   it->head = y.x;
   it->row0 = y.y;
-  it->more = y.z;
+  it->part = y.z;
+  it->more = y.w;
   __syncwarp();
   if (it->more && (threadIdx.x & 31) == 0) {
     if (kCtas > 1)
@@ -433,9 +465,8 @@ struct Maps {
 // ------------------------------------------------------------------ TMA
 
 // Every CTA loads its own rows of Q, its 64 of the step's keys, and its columns of
-// the step's values.  The values that are to be looked through complete on barriers
-// of the scan, which then fills the stage's own: the products wait for one barrier,
-// and no one waits for a phase that another may leave behind.
+// the step's values.  Values that are to be looked through complete on barriers of this
+// CTA instead of the leader's.
 template <int kCtas>
 __device__ void load_items(const Ctx<kCtas>& c, const Args& a, const Maps& m, int lane) {
   using F = Form<kCtas>;
@@ -445,15 +476,14 @@ __device__ void load_items(const Ctx<kCtas>& c, const Args& a, const Maps& m, in
   bool ok = true;
   Item it;
   for (int n = 0; ok && take_item(c, n, &it); ++n) {
-    const Tile tiles[2] = {tile_of<kCtas>(it, a.causal, 0, c.rank), tile_of<kCtas>(it, a.causal, 1, c.rank)};
-    const int steps = max(tiles[0].steps, tiles[1].steps), scan_from = first_scan<kCtas>(it, a.causal);
+    const Work w = work_of<kCtas>(it, a, c.rank);
     auto load_q = [&](int t) {
-      if (tiles[t].steps == 0) return true;
+      if (w.tile[t].steps == 0) return true;
       if (!c.wait_warp(B_QE + t, qe[t], 0xA10)) return false;
       qe[t] ^= 1;
       if (lane == 0) {
         const uint32_t dst = c.sbase + kOffQ + t * kQTile, bar = c.leader_bar(B_Q + t);
-        const int row = it.q0 + tiles[t].row0;
+        const int row = it.q0 + w.tile[t].row0;
         announce(bar, kQTile);
         tma_3d<kCtas>(dst, &m.q_nope, bar, 0, it.head, row);
         tma_3d<kCtas>(dst + 2 * kBox, &m.q_nope, bar, 64, it.head, row);
@@ -463,10 +493,10 @@ __device__ void load_items(const Ctx<kCtas>& c, const Args& a, const Maps& m, in
       return true;
     };
     ok = load_q(0);
-    for (int j = 0; ok && j < steps; ++j, ring.next()) {
+    for (int j = 0; ok && j < w.steps; ++j, ring.next()) {
       const int stage = ring.slot;
       const uint32_t dst = c.sbase + kOffRing + stage * kStageBytes;
-      const int row = it.k0 + j * F::kKeys;
+      const int row = it.k0 + (w.begin + j) * F::kKeys;
       if (!(ok = c.wait_warp(B_KE + stage, ring.phase ^ 1, 0xA11))) break;
       if (lane == 0) {
         const uint32_t bar = c.leader_bar(B_KF + stage);
@@ -479,10 +509,10 @@ __device__ void load_items(const Ctx<kCtas>& c, const Args& a, const Maps& m, in
       if (j == 0 && !(ok = load_q(1))) break;
       if (!(ok = c.wait_warp(B_VE + stage, ring.phase ^ 1, 0xA12))) break;
       ++loaded;
-      const bool scan = j >= scan_from;
+      const bool look = j >= w.look;
       if (lane == 0) {
-        const uint32_t bar = scan ? c.bar(B_RAW + raw.slot) : c.leader_bar(B_VF + stage);
-        if (scan)
+        const uint32_t bar = look ? c.bar(B_RAW + raw.slot) : c.leader_bar(B_VF + stage);
+        if (look)
           mbar_arrive_expect_tx(bar, kVBytes);
         else
           announce(bar, kVBytes);
@@ -490,7 +520,7 @@ __device__ void load_items(const Ctx<kCtas>& c, const Args& a, const Maps& m, in
         if (kCtas == 1) tma_3d<kCtas>(dst + kKBytes + kBox, &m.v, bar, 64, it.head, row);
       }
       __syncwarp();
-      if (scan) raw.next();
+      if (look) raw.next();
     }
     if (ok && c.rank == 0 && lane == 0) mbar_arrive(c.bar(B_NEXT));
     __syncwarp();
@@ -603,6 +633,8 @@ __device__ void issue_products(const Ctx<kCtas>& c, const Args& a, uint32_t tmem
   const uint32_t v0 = desc_low(c.sbase + kOffRing + kKBytes, kBox);
   Ring<kStages> kr, vr;              // the next step's keys, the last step's values
   uint32_t qp[2] = {0, 0}, pp[2] = {0, 0};  // parities of Q and of P
+  uint32_t vp = 0;                   // [stage] of the values that are not looked through
+  bool looked = false;               // the last step's values are: with the weights comes the word that they can be used
   bool due[2] = {false, false};      // the last step's second product is still to come
   bool first[2], last[2];            // ... of that step in its item
   bool ok = true, more = true;
@@ -612,15 +644,23 @@ __device__ void issue_products(const Ctx<kCtas>& c, const Args& a, uint32_t tmem
     const bool take = !(due[0] || due[1]) || c.ready(B_ITEM + n % kItemSlots, (n / kItemSlots) & 1);
     if (take) more = take_item(c, n++, &it);
     const bool keys = take && more;
-    const int steps[2] = {keys ? tile_of<kCtas>(it, a.causal, 0, 0).steps : 0,
-                          keys ? tile_of<kCtas>(it, a.causal, 1, 0).steps : 0};
-    const int total = keys ? max(steps[0], steps[1]) : 1;
+    int steps[2] = {0, 0}, total = 1, look = 0;
+    if (keys) {
+      const Work w = work_of<kCtas>(it, a, 0);
+      steps[0] = w.tile[0].steps;
+      steps[1] = w.tile[1].steps;
+      total = w.steps;
+      look = w.look;
+    }
     for (int j = 0; ok && j < total; ++j) {
       const bool was[2] = {due[0], due[1]};
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (was[t]) {
-          if ((t == 0 || !was[0]) && !(ok = c.wait_uniform(B_VF + vr.slot, vr.phase, 0xA13))) break;
+          if ((t == 0 || !was[0]) && !looked) {
+            if (!(ok = c.wait_uniform(B_VF + vr.slot, (vp >> vr.slot) & 1, 0xA13))) break;
+            vp ^= 1u << vr.slot;
+          }
           const uint32_t v = v0 + vr.slot * (kStageBytes >> 4);
           const uint32_t d = tmem + TM_O + 128 * t, p = tmem + TM_S + 128 * t;
 #pragma unroll
@@ -656,7 +696,10 @@ __device__ void issue_products(const Ctx<kCtas>& c, const Args& a, uint32_t tmem
         }
       }
       if (was[0] || was[1]) vr.next();
-      if (keys) kr.next();
+      if (keys) {
+        kr.next();
+        looked = j >= look;
+      }
     }
   }
   // every product is done before TMEM is released
@@ -664,53 +707,38 @@ __device__ void issue_products(const Ctx<kCtas>& c, const Args& a, uint32_t tmem
   c.wait_limited(B_FIN, 0);
 }
 
-// ------------------------------------------------------------------ value scan
+// ------------------------------------------------------------------ masked values
 
-// Zeros in the place of what is not finite, in this CTA's share of the values that
-// some row does not see whole.  An item whose own keys have such values is noted
-// (kPoisons flags: the scan is at most three items ahead of the epilogue).
+// Zeros in the place of what is not finite, in a quarter (32 keys, or 16 of two boxes)
+// of this CTA's values of a step; `own`: keys of it that are the request's.  True: some
+// of those were not finite.
 template <int kCtas>
-__device__ void scan_values(const Ctx<kCtas>& c, const Args& a, int lane) {
+__device__ bool look_through(uint32_t values, int quarter, int lane, int own) {
   using F = Form<kCtas>;
-  Ring<kStages> ring, raw;
-  Item it;
-  for (int n = 0; take_item(c, n, &it); ++n) {
-    const int steps = max(tile_of<kCtas>(it, a.causal, 0, 0).steps, tile_of<kCtas>(it, a.causal, 1, 0).steps);
-    const int scan_from = first_scan<kCtas>(it, a.causal);
-    flag_store(c.sbase + kOffPoison + 4 * ((n + kPoisons / 2) % kPoisons), 0);
-    for (int j = 0; j < steps; ++j, ring.next()) {
-      if (j < scan_from) continue;
-      if (!c.wait_warp(B_RAW + raw.slot, raw.phase, 0xA17)) return;
-      raw.next();
-      const uint32_t base = c.sbase + kOffRing + ring.slot * kStageBytes + kKBytes + lane * 16;
-      bool seen = false;
-#pragma unroll 8
-      for (int i = 0; i < kVBytes / 512; ++i) {
-        uint4 x = ld_shared_v4(base + i * 512);
-        constexpr uint32_t kExp = 0x7F807F80u;
-        const uint32_t b0 = __vcmpeq2(x.x & kExp, kExp), b1 = __vcmpeq2(x.y & kExp, kExp), b2 = __vcmpeq2(x.z & kExp, kExp),
-                       b3 = __vcmpeq2(x.w & kExp, kExp);
-        if (b0 | b1 | b2 | b3) {
-          x.x &= ~b0;
-          x.y &= ~b1;
-          x.z &= ~b2;
-          x.w &= ~b3;
-          st_shared_v4(base + i * 512, x);
-          // a key is 128 bytes; one CTA alone holds two boxes of 64 keys
-          seen |= j * F::kKeys + (i * 4 + (lane >> 3)) % F::kKeys < it.lk;
-        }
-      }
-      if (seen) flag_store(c.sbase + kOffPoison + 4 * (n % kPoisons), 1);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        if (kCtas > 1)
-          mbar_arrive_remote(c.leader_bar(B_VF + ring.slot));
-        else
-          mbar_arrive(c.bar(B_VF + ring.slot));
+  const uint32_t base = values + quarter * (kVBytes / 4) + lane * 16;
+  constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u, kTop = 0x80008000u;  // an exponent of ones carries into the sign
+  uint4 x[8];
+  uint32_t found = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = ld_shared_v4(base + i * 512);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    found |= ((x[i].x & kExp) + kOne) | ((x[i].y & kExp) + kOne) | ((x[i].z & kExp) + kOne) | ((x[i].w & kExp) + kOne);
+  bool seen = false;
+  if (found & kTop) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      uint4 y = ld_shared_v4(base + i * 512);
+      const uint32_t b0 = __vcmpeq2(y.x & kExp, kExp), b1 = __vcmpeq2(y.y & kExp, kExp), b2 = __vcmpeq2(y.z & kExp, kExp),
+                     b3 = __vcmpeq2(y.w & kExp, kExp);
+      if (b0 | b1 | b2 | b3) {
+        st_shared_v4(base + i * 512, make_uint4(y.x & ~b0, y.y & ~b1, y.z & ~b2, y.w & ~b3));
+        // a key is 128 bytes; one CTA alone holds two boxes of 64 keys
+        seen |= (quarter * 32 + i * 4 + (lane >> 3)) % F::kKeys < own;
       }
     }
   }
+  return seen;
 }
 
 // ------------------------------------------------------------------ softmax
@@ -753,8 +781,8 @@ __device__ __noinline__ float non_finite(const uint16_t* v, int64_t stride, int 
   return sum;
 }
 
-// (What it orders, TMEM, the tcgen05 fences order; a release at cluster scope would
-// wait for stores in flight.)
+// (What it orders, this CTA's TMEM and, behind a proxy fence, its shared memory, is in
+// place by then; a release at cluster scope would wait a microsecond for it again.)
 template <int kCtas>
 __device__ __forceinline__ void arrive_leader(const Ctx<kCtas>& c, int bar) {
   if (kCtas > 1)
@@ -827,12 +855,31 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
   const float slack = kRescaleLog2 / a.scale_log2;
   const float2 scale = make_float2(a.scale_log2, a.scale_log2);
   uint32_t sp = 0, op = 0;  // parities of S and O
+  int vstep = 0, looks = 0;  // steps, and steps looked through, of the items before
   Item it;
   for (int n = 0; take_item(c, n, &it); ++n) {
-    const Tile d = tile_of<kCtas>(it, a.causal, t, c.rank);
+    const Work w = work_of<kCtas>(it, a, c.rank);
+    const Tile d = w.tile[t];
+    const int values = vstep, look0 = looks;
+    vstep = (vstep + w.steps) % kStages;
+    looks = (looks + w.steps - w.look) % (2 * kStages);
+    if (t == 0 && quad == 0) flag_store(c.sbase + kOffPoison + 4 * ((n + kPoisons / 2) % kPoisons), 0);
+    // The first active tile's warps look through a step's values, before its weights are handed over.
+    const int looker = t == 0 ? w.look : max(w.look, w.tile[0].steps);
+    auto look = [&](int j) {
+      const int k = look0 + j - w.look;
+      if (!c.wait_warp(B_RAW + k % kStages, (k / kStages) & 1, 0xA17)) return false;
+      const uint32_t at = c.sbase + kOffRing + (values + j) % kStages * kStageBytes + kKBytes;
+      if (look_through<kCtas>(at, quad, lane, it.lk - (w.begin + j) * F::kKeys))
+        flag_store(c.sbase + kOffPoison + 4 * (n % kPoisons), 1);
+      fence_proxy_async_smem();
+      return true;
+    };
     if (d.rows == 0) {  // the tile's rows are the other CTA's, or there are none
       for (int j = 0; j < d.steps; ++j, sp ^= 1) {
         if (!c.wait_warp(B_S + t, sp, 0xA18)) return;
+        if (j >= looker && !look(j)) return;
+        __syncwarp();
         if (lane == 0)
           for (int half = 0; half < kCtas; ++half) arrive_leader(c, B_P + 2 * t + half);
       }
@@ -843,12 +890,14 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
     const int seen = visible(it, a.causal, min(row, it.lq - 1));
     float top = -CUDART_INF_F, base = 0.f;  // the running maximum of S, and of c S (0 while there is none)
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    for (int j = 0; j < d.steps; ++j, sp ^= 1) {
-      if (!c.wait_warp(B_S + t, sp, 0xA18)) return;
+    // One step; kSome: there are keys that some row does not see, or values to look through.
+    auto step = [&](int j, auto some) {
+      constexpr bool kSome = decltype(some)::value;
+      if (!c.wait_warp(B_S + t, sp, 0xA18)) return false;
+      sp ^= 1;
       tc_fence_after();
       constexpr int kHalf = kParts / 2;
-      const bool masked = j >= d.masked;
-      const int left = seen - j * F::kKeys;
+            const int left = seen - (w.begin + j) * F::kKeys;
       uint32_t s[kHalf][32], p[16 * kHalf];
       float here;
       {
@@ -860,12 +909,12 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
 #pragma unroll
         for (int q = 0; q < kHalf; ++q) {
           tmem_wait_ld32(s[q]);
-          if (masked) mask32(s[q], left - 32 * q);
+          if (kSome) mask32(s[q], left - 32 * q);
         }
 #pragma unroll
         for (int q = 0; q < kHalf; ++q) {
           tmem_wait_ld32(u[q]);
-          if (masked) mask32(u[q], left - 32 * (kHalf + q));
+          if (kSome) mask32(u[q], left - 32 * (kHalf + q));
         }
         here = fmaxf(max32(s[0]), max32(u[0]));
         if (kHalf == 2) here = max3(here, max32(s[kHalf - 1]), max32(u[kHalf - 1]));
@@ -899,6 +948,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       for (int q = 0; q < kHalf; ++q) tmem_st16_async(ts + 16 * q, p + 16 * q);
 #pragma unroll
       for (int q = 0; q < kHalf; ++q) tmem_ld32_async(ts + 32 * (kHalf + q), s[q]);  // (P ends before)
+      if (kSome && j >= looker && !look(j)) return false;
       if (kCtas > 1) {
         tmem_wait_st();
         tc_fence_before();
@@ -908,7 +958,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
 #pragma unroll
       for (int q = 0; q < kHalf; ++q) {
         tmem_wait_ld32(s[q]);
-        if (masked) mask32(s[q], left - 32 * (kHalf + q));
+        if (kSome) mask32(s[q], left - 32 * (kHalf + q));
         weights32(s[q], scale, base, p + 16 * q, more);
         tmem_st16_async(ts + 16 * (kHalf + q), p + 16 * q);
       }
@@ -918,7 +968,14 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_leader(c, B_P + 2 * t + kCtas - 1);
-    }
+      return true;
+    };
+    const int whole = min(d.steps, max(0, min(d.masked, looker)));
+    int j = 0;
+    for (; j < whole; ++j)
+      if (!step(j, std::false_type())) return;
+    for (; j < d.steps; ++j)
+      if (!step(j, std::true_type())) return;
     // ---- epilogue
     if (d.steps > 0) {
       if (!c.wait_warp(B_O + t, op, 0xA19)) return;
@@ -930,7 +987,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
     const bool none = total == 0.f;  // no key, or scores of -inf alone
     const float inv = 1.f / total;
     const bool poison = flag_load(c.sbase + kOffPoison + 4 * (n % kPoisons)) != 0;
-    const int64_t token = it.q0 + row;
+    const int64_t token = it.q0 + row, part_row = (int64_t)it.part * a.tokens_q + token;
     uint16_t* out = a.out + token * a.out_ts + it.head * a.out_hs;
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
 #pragma unroll 1
@@ -942,9 +999,17 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : __uint_as_float(r[i]) * inv;
       if (poison && mine && !none) {
         const uint16_t* v = a.v + it.k0 * a.v_ts + it.head * a.v_hs + 32 * q;
-        const int from = first_scan<kCtas>(it, a.causal) * F::kKeys;
+        const int from = (w.begin + w.look) * F::kKeys, to = min(seen, (w.begin + w.steps) * F::kKeys);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] += non_finite(v + i, a.v_ts, from, seen);
+        for (int i = 0; i < 32; ++i) o[i] += non_finite(v + i, a.v_ts, from, to);
+      }
+      if (a.parts > 1) {
+        float4* to = reinterpret_cast<float4*>(a.part_out + (part_row * a.heads + it.head) * 128 + 32 * q);
+        if (mine && !none) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+        continue;
       }
       uint32_t p[16];
 #pragma unroll
@@ -954,7 +1019,8 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
         store32(out + 32 * q + 16, p + 8, wide);
       }
     }
-    if (mine) a.lse[token * a.heads + it.head] = none ? -CUDART_INF_F : fmaf(base, CUDART_LN2_F, logf(total));
+    float* lse = a.parts > 1 ? a.part_lse + part_row * a.heads : a.lse + token * a.heads;
+    if (mine) lse[it.head] = none ? -CUDART_INF_F : fmaf(base, CUDART_LN2_F, logf(total));
   }
 }
 
@@ -985,7 +1051,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   c.rank = kCtas > 1 ? (int)cluster_ctarank() : 0;
   c.leader = kCtas > 1 ? mapa(c.sbase, 0) : c.sbase;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  if (warp == 0) {
+  Item own{};
+  if (warp == 3 && c.rank == 0) {
+    own.more = item_of<kCtas>(a, (int)blockIdx.x, lane, &own);
+  } else if (warp == 0) {
     if (lane == 0) {
       flag_store(c.sbase + kOffAbort, 0);
       for (int i = 0; i < kPoisons; ++i) flag_store(c.sbase + kOffPoison + 4 * i, 0);
@@ -1006,7 +1075,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       for (int i = 0; i < kItemSlots; ++i) {
         mbar_init(c.bar(B_ITEM + i), 1);
-        mbar_init(c.bar(B_TAKEN + i), 10 * kCtas + 1);  // copies, scan, softmax; and the leader's products
+        mbar_init(c.bar(B_TAKEN + i), 9 * kCtas + 1);  // copies, softmax; and the leader's products
       }
       mbar_init(c.bar(B_NEXT), 1);
       mbar_init(c.bar(B_ASKED), 1);
@@ -1036,12 +1105,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         issue_products(c, a, tmem);
       else
         c.wait_limited(B_FIN, 0);  // the leader's last arrival here
-    } else if (warp == 2) {
-      scan_values(c, a, lane);
-    } else if (c.rank == 0) {
-      schedule(c, a, lane);
-    } else {
-      receive(c, lane);
+    } else if (warp == 3) {
+      if (c.rank == 0)
+        schedule(c, a, own, lane);
+      else
+        receive(c, lane);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -1054,6 +1122,46 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   tc_fence_after();
   if (warp == 1) tmem_dealloc_of<kCtas>(tmem);
   if (kCtas > 1) cluster_sync();
+}
+
+// ------------------------------------------------------------------ parts
+
+// lse = ln sum_k e^lse_k, out = sum_k e^(lse_k - lse) out_k over the parts of a row; a
+// warp a row, 64 rows a block.
+constexpr int kMergeRows = 64;
+template <int kItemRows>
+__global__ void __launch_bounds__(256) merge_parts_kernel(const Args a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = (int)blockIdx.x / a.tiles;
+  Item it;
+  if (!find_item<kItemRows>(a, (int)blockIdx.x - head * a.tiles, lane, &it)) return;
+  const int first = it.row0 + (int)blockIdx.y * kMergeRows;
+  const int end = min(first + kMergeRows, min(it.row0 + kItemRows, it.lq));
+  for (int row = first + warp; row < end; row += 8) {
+    const int64_t token = it.q0 + row, at = token * a.heads + head, stride = (int64_t)a.tokens_q * a.heads;
+    float mine = lane < a.parts ? __ldcg(a.part_lse + lane * stride + at) : -CUDART_INF_F;  // at most 32 parts
+    float top = mine;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float base = top == -CUDART_INF_F ? 0.f : top;
+    float w = expf(mine - base), sum = w;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    w = sum == 0.f ? 0.f : w / sum;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < a.parts; ++k) {
+      const float f = __shfl_sync(0xffffffffu, w, k);
+      if (f == 0.f) continue;  // (it may not have been written)
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_out + (k * stride + at) * 128) + lane);
+      o.x += f * x.x;
+      o.y += f * x.y;
+      o.z += f * x.z;
+      o.w += f * x.w;
+    }
+    *reinterpret_cast<uint2*>(a.out + token * a.out_ts + head * a.out_hs + 4 * lane) = make_uint2(pack(o.x, o.y), pack(o.z, o.w));
+    if (lane == 0) a.lse[at] = sum == 0.f ? -CUDART_INF_F : base + logf(sum);
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -1089,6 +1197,15 @@ static int items_of_a_head(int num_tokens_q, int batch, int item_rows) {
   return num_tokens_q / item_rows + (batch < num_tokens_q ? batch : num_tokens_q);
 }
 
+// Parts of the keys: enough to give every CTA an item, of 512 keys or more.
+template <int kCtas>
+static int parts_of(int num_tokens_q, int num_tokens_k, int batch, int num_heads, int sms) {
+  const int64_t items = (int64_t)items_of_a_head(num_tokens_q, batch, Form<kCtas>::kItemRows) * num_heads;
+  const int64_t room = sms / kCtas / std::max<int64_t>(1, items), most = num_tokens_k / batch / 512;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(room, most), 32));
+}
+static bool in_pairs(int num_tokens_q, int batch) { return num_tokens_q / batch > 256; }
+
 template <int kCtas>
 static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t stream) {
   using F = Form<kCtas>;
@@ -1108,8 +1225,11 @@ static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t
       !make_map(&m.v, keys ? p.v : p.q_nope, 128, p.num_heads, tk, F::kKeys))
     return cudaErrorNotSupported;
   a.tiles = items_of_a_head(p.num_tokens_q, p.batch, F::kItemRows);
+  a.parts = parts_of<kCtas>(p.num_tokens_q, p.num_tokens_k, p.batch, p.num_heads, dev.sms);
+  a.part_out = static_cast<float*>(p.workspace);
+  a.part_lse = a.part_out + (int64_t)a.parts * p.num_tokens_q * p.num_heads * 128;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.tiles * a.heads * kCtas));
+  cfg.gridDim = dim3((unsigned)(a.tiles * a.heads * a.parts * kCtas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
@@ -1120,7 +1240,14 @@ static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, m, a);
+  const cudaError_t main = cudaLaunchKernelEx(&cfg, kernel, m, a);
+  if (main != cudaSuccess || a.parts == 1) return main;
+  cfg.gridDim = dim3((unsigned)(a.tiles * a.heads), F::kItemRows / kMergeRows);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, merge_parts_kernel<F::kItemRows>, a);
 }
 
 }  // namespace prefill
@@ -1145,8 +1272,7 @@ cudaError_t launch_prefill(const PrefillCall& p, Device dev, cudaStream_t stream
   a.tokens_k = p.num_tokens_k;
   a.causal = p.causal;
   a.scale_log2 = p.scale * 1.44269504088896340736f;
-  const bool pair = p.num_tokens_q / p.batch > 256;
-  return pair ? launch<2>(p, a, dev, stream) : launch<1>(p, a, dev, stream);
+  return in_pairs(p.num_tokens_q, p.batch) ? launch<2>(p, a, dev, stream) : launch<1>(p, a, dev, stream);
 }
 
 // Launch bound: the small form's CTAs, at most
@@ -1154,8 +1280,13 @@ int prefill_items(int num_tokens_q, int batch) {
   return prefill::items_of_a_head(num_tokens_q, batch, prefill::Form<1>::kItemRows);
 }
 
-// Nothing is split over the keys: no workspace.
-size_t prefill_workspace(int, int, int, int, Device) { return 0; }
+// What the parts of a call write; 0: its keys are not cut.
+size_t prefill_workspace(int num_tokens_q, int num_tokens_k, int batch, int num_heads, Device dev) {
+  using namespace prefill;
+  const int parts = in_pairs(num_tokens_q, batch) ? parts_of<2>(num_tokens_q, num_tokens_k, batch, num_heads, dev.sms)
+                                                  : parts_of<1>(num_tokens_q, num_tokens_k, batch, num_heads, dev.sms);
+  return parts == 1 ? 0 : align256((size_t)parts * num_tokens_q * num_heads * (128 + 1) * 4);
+}
 
 cudaError_t prefill_read_error(int* code, bool reset) {
   cudaError_t e = cudaMemcpyFromSymbol(code, prefill::g_prefill_error, sizeof(int));

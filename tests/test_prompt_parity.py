@@ -88,6 +88,9 @@ CASES = [
     (1, [640], [640], True), (2, [500], [500], False), (1, [1], [1000], True), (1, [1], [1000], False),
     (3, [5, 0, 300, 1], [5, 9, 300, 640], True), (2, [130, 64, 0, 1, 257], [0, 400, 0, 1, 511], False),
     (1, [300], [100], True), (2, [300, 7], [0, 7], True), (5, [40] * 40, [40] * 40, True), (1, [1] * 70, [300] * 70, True),
+    # few rows and many keys: the keys are cut into parts
+    (2, [100], [5000], False), (1, [1], [20000], True), (3, [600], [4000], True), (2, [5, 0, 300], [3000, 2500, 0], True),
+    (2, [700, 3], [1100, 3500], True), (1, [40, 30, 1], [1500, 0, 9000], False),
     (16, [130], [130], True), (1, [513, 511], [513, 1025], True), (1, [2], [384], False), (1, [200], [256], False),
 ]
 
