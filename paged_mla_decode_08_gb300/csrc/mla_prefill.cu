@@ -90,7 +90,7 @@ struct Form {
   static constexpr int kItemRows = 2 * kTileRows;
 };
 
-constexpr int kItemSlots = 2;
+constexpr int kItemSlots = 4;
 enum Bar : int {
   B_Q = 0,                        // [tile] Q landed (the leader's barrier)
   B_QE = B_Q + 2,                 // [tile] Q is read
@@ -104,7 +104,9 @@ enum Bar : int {
   B_O = B_P + 4,                  // [tile] the tile's products are done
   B_ITEM = B_O + 2,               // [slot] an item is there
   B_TAKEN = B_ITEM + kItemSlots,  // [slot] every role of the item's CTAs has it (the leader's)
-  B_NEXT = B_TAKEN + kItemSlots,  // the item's copies are issued: time to ask for the next
+  B_STAT = B_TAKEN + kItemSlots,  // alone: the second tile's sums are there
+  B_READ,                         // ... and its part of the output is read
+  B_NEXT,                         // the item's copies are issued: time to ask for the next
   B_ASKED,                        // the answer is there
   B_FIN,                          // every product is done
   B_COUNT
@@ -116,7 +118,8 @@ constexpr int kOffPoison = kOffAbort + 4;
 constexpr int kOffItem = (kOffPoison + 4 * kPoisons + 15) / 16 * 16;
 constexpr int kItemBytes = 32;
 constexpr int kOffAnswer = kOffItem + kItemSlots * kItemBytes;
-constexpr int kSmem = kOffAnswer + 16 + 1024;  // + alignment slack
+constexpr int kOffStat = kOffAnswer + 16;  // [row] base and sum of the second tile
+constexpr int kSmem = kOffStat + kRows * 8 + 1024;  // + alignment slack
 static_assert(kSmem <= 232448, "shared memory budget");
 
 constexpr uint32_t TM_S = 0, TM_O = 256, kTmemCols = 512;
@@ -147,13 +150,14 @@ struct Item {
 // What a CTA does of an item.
 struct Tile {
   int row0, rows;  // this CTA's, within the request
-  int steps;       // with a key that a row of the tile (of both CTAs) sees
-  int masked;      // first step that some row of this CTA does not see whole
+  int steps;       // with a key that a row of the tile (of both CTAs) sees; this tile's share
+  int masked;      // first step of the item that some row of this CTA does not see whole
 };
 struct Work {
   Tile tile[2];
   int begin;   // first step of the item, in the request's keys; the others count from it
-  int steps;   // of the longer tile
+  int steps;   // of the item
+  bool alone;  // one tile's rows: the other tile takes them too, and every second step
   int look;    // first step whose values are looked through: some row does not see it whole
 };
 
@@ -187,6 +191,12 @@ __device__ __forceinline__ Work work_of(const Item& it, const Args& a, int rank)
     w.tile[t].masked = visible(it, a.causal, min(w.tile[t].row0, it.lq - 1)) / F::kKeys - w.begin;
     if (w.tile[t].steps > 0)
       w.look = min(w.look, max(0, visible(it, a.causal, it.row0 + t * F::kTileRows) / F::kKeys - w.begin));
+  }
+  w.alone = it.lq - it.row0 <= F::kTileRows && w.steps > 1;
+  if (w.alone) {
+    w.tile[1] = w.tile[0];
+    w.tile[0].steps = (w.steps + 1) / 2;
+    w.tile[1].steps = w.steps / 2;
   }
   return w;
 }
@@ -399,29 +409,37 @@ __device__ void receive(const Ctx<kCtas>& c, int lane) {
   }
 }
 
-// Item n, for a converged warp; false: there is none, or a wait gave up.
+// Item n, for a converged warp, while its slot is held.
 template <int kCtas>
-__device__ __forceinline__ bool take_item(const Ctx<kCtas>& c, int n, Item* it) {
+__device__ __forceinline__ Item read_item(const Ctx<kCtas>& c, int n) {
+  const uint32_t src = c.sbase + kOffItem + n % kItemSlots * kItemBytes;
+  const uint4 x = ld_shared_v4(src), y = ld_shared_v4(src + 16);
+  return Item{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+}
+// Wait for item n; false: there is none, or a wait gave up.
+template <int kCtas>
+__device__ __forceinline__ bool await_item(const Ctx<kCtas>& c, int n) {
   const int slot = n % kItemSlots;
   if (!c.wait_warp(B_ITEM + slot, (n / kItemSlots) & 1, 0xA1F)) return false;
-  const uint32_t src = c.sbase + kOffItem + slot * kItemBytes;
-  const uint4 x = ld_shared_v4(src), y = ld_shared_v4(src + 16);
-  it->q0 = x.x;
-  it->lq = x.y;
-  it->k0 = x.z;
-  it->lk = x.w;
-  it->head = y.x;
-  it->row0 = y.y;
-  it->part = y.z;
-  it->more = y.w;
+  return flag_load(c.sbase + kOffItem + slot * kItemBytes + 28) != 0;
+}
+// The warp has what it needs of item n.
+template <int kCtas>
+__device__ __forceinline__ void release_item(const Ctx<kCtas>& c, int n) {
   __syncwarp();
-  if (it->more && (threadIdx.x & 31) == 0) {
+  if ((threadIdx.x & 31) == 0) {
     if (kCtas > 1)
-      mbar_arrive_remote(c.leader_bar(B_TAKEN + slot));
+      mbar_arrive_remote(c.leader_bar(B_TAKEN + n % kItemSlots));
     else
-      mbar_arrive(c.bar(B_TAKEN + slot));
+      mbar_arrive(c.bar(B_TAKEN + n % kItemSlots));
   }
-  return it->more != 0;
+}
+template <int kCtas>
+__device__ __forceinline__ bool take_item(const Ctx<kCtas>& c, int n, Item* it) {
+  if (!await_item(c, n)) return false;
+  *it = read_item(c, n);
+  release_item(c, n);
+  return true;
 }
 
 // A place in a ring: counts on through all items.
@@ -634,7 +652,8 @@ __device__ void issue_products(const Ctx<kCtas>& c, const Args& a, uint32_t tmem
   Ring<kStages> kr, vr;              // the next step's keys, the last step's values
   uint32_t qp[2] = {0, 0}, pp[2] = {0, 0};  // parities of Q and of P
   uint32_t vp = 0;                   // [stage] of the values that are not looked through
-  bool looked = false;               // the last step's values are: with the weights comes the word that they can be used
+  bool looked[2];                    // the last step's values are: with the weights comes the word that they can be used
+  bool alone = false, was_alone = false;  // the tiles have steps of their own: of the next, of the last step
   bool due[2] = {false, false};      // the last step's second product is still to come
   bool first[2], last[2];            // ... of that step in its item
   bool ok = true, more = true;
@@ -649,15 +668,16 @@ __device__ void issue_products(const Ctx<kCtas>& c, const Args& a, uint32_t tmem
       const Work w = work_of<kCtas>(it, a, 0);
       steps[0] = w.tile[0].steps;
       steps[1] = w.tile[1].steps;
-      total = w.steps;
+      total = max(steps[0], steps[1]);
       look = w.look;
+      alone = w.alone;
     }
     for (int j = 0; ok && j < total; ++j) {
       const bool was[2] = {due[0], due[1]};
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (was[t]) {
-          if ((t == 0 || !was[0]) && !looked) {
+          if ((t == 0 || !was[0] || was_alone) && !looked[t]) {
             if (!(ok = c.wait_uniform(B_VF + vr.slot, (vp >> vr.slot) & 1, 0xA13))) break;
             vp ^= 1u << vr.slot;
           }
@@ -672,10 +692,13 @@ __device__ void issue_products(const Ctx<kCtas>& c, const Args& a, uint32_t tmem
           if (!ok) break;
           pp[t] ^= 1;
           if (last[t]) commit<kCtas>(c.bar(B_O + t), go);
-          if (t == 1 || !was[1]) commit<kCtas>(c.bar(B_VE + vr.slot), go);  // its last reader
+          if (t == 1 || !was[1] || was_alone) {  // its last reader
+            commit<kCtas>(c.bar(B_VE + vr.slot), go);
+            vr.next();
+          }
         }
         if (j < steps[t]) {
-          if ((t == 0 || j >= steps[0]) && !(ok = c.wait_uniform(B_KF + kr.slot, kr.phase, 0xA15))) break;
+          if ((t == 0 || j >= steps[0] || alone) && !(ok = c.wait_uniform(B_KF + kr.slot, kr.phase, 0xA15))) break;
           if (j == 0) {
             if (!(ok = c.wait_uniform(B_Q + t, qp[t], 0xA16))) break;
             qp[t] ^= 1;
@@ -687,19 +710,19 @@ __device__ void issue_products(const Ctx<kCtas>& c, const Args& a, uint32_t tmem
             products_ss<kCtas>(tmem + TM_S + 128 * t, q + kk * (2 * kBox >> 4), k + kk * (kBox >> 4), kIdescS, kk > 0, go);
           commit<kCtas>(c.bar(B_S + t), go);
           if (j == steps[t] - 1) commit<kCtas>(c.bar(B_QE + t), go);
-          if (t == 1 || j >= steps[1]) commit<kCtas>(c.bar(B_KE + kr.slot), go);
+          if (t == 1 || j >= steps[1] || alone) {
+            commit<kCtas>(c.bar(B_KE + kr.slot), go);
+            kr.next();
+          }
           due[t] = true;
           first[t] = j == 0;
           last[t] = j == steps[t] - 1;
+          looked[t] = (alone ? 2 * j + t : j) >= look;
         } else {
           due[t] = false;
         }
       }
-      if (was[0] || was[1]) vr.next();
-      if (keys) {
-        kr.next();
-        looked = j >= look;
-      }
+      was_alone = alone;
     }
   }
   // every product is done before TMEM is released
@@ -854,20 +877,124 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
   const uint32_t ts = tmem + lanes + TM_S + 128 * t, to = tmem + lanes + TM_O + 128 * t;
   const float slack = kRescaleLog2 / a.scale_log2;
   const float2 scale = make_float2(a.scale_log2, a.scale_log2);
-  uint32_t sp = 0, op = 0;  // parities of S and O
+  uint32_t sp = 0, op = 0, other_op = 0, ap = 0;  // parities of S, O, the other tile's O, and what passes between them
   int vstep = 0, looks = 0;  // steps, and steps looked through, of the items before
-  Item it;
-  for (int n = 0; take_item(c, n, &it); ++n) {
+  float top, base;           // the running maximum of S, and of c S (0 while there is none)
+  float2 sum[2];
+  // One step.  left: keys of it that this thread's row sees, where some row does not see them all
+  // (masks are left out where before_hand_over is the step's without any).
+  auto step = [&](bool fresh, int left, auto before_hand_over) {
+    constexpr bool kSome = !std::is_empty<decltype(before_hand_over)>::value;
+    if (!c.wait_warp(B_S + t, sp, 0xA18)) return false;
+    sp ^= 1;
+    tc_fence_after();
+    constexpr int kHalf = kParts / 2;
+    uint32_t s[kHalf][32], p[16 * kHalf];
+    float here;
+    {
+      uint32_t u[kHalf][32];  // the second half, for the maximum
+#pragma unroll
+      for (int q = 0; q < kHalf; ++q) tmem_ld32_async(ts + 32 * q, s[q]);
+#pragma unroll
+      for (int q = 0; q < kHalf; ++q) tmem_ld32_async(ts + 32 * (kHalf + q), u[q]);
+#pragma unroll
+      for (int q = 0; q < kHalf; ++q) {
+        tmem_wait_ld32(s[q]);
+        if (kSome) mask32(s[q], left - 32 * q);
+      }
+#pragma unroll
+      for (int q = 0; q < kHalf; ++q) {
+        tmem_wait_ld32(u[q]);
+        if (kSome) mask32(u[q], left - 32 * (kHalf + q));
+      }
+      here = fmaxf(max32(s[0]), max32(u[0]));
+      if (kHalf == 2) here = max3(here, max32(s[kHalf - 1]), max32(u[kHalf - 1]));
+    }
+    float2 more[2] = {sum[0], sum[1]};
+    if (!fresh) {
+#pragma unroll
+      for (int q = 0; q < kHalf; ++q) weights32(s[q], scale, base, p + 16 * q, more);
+    }
+    const bool move = here > top + slack;
+    if (fresh || __any_sync(0xffffffffu, move)) {
+      const float factor = move ? ex2_approx((top - here) * a.scale_log2) : 1.f;
+      if (move) {
+        top = here;
+        base = here * a.scale_log2;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) more[i] = sum[i] = make_float2(sum[i].x * factor, sum[i].y * factor);
+#pragma unroll
+      for (int q = 0; q < kHalf; ++q) weights32(s[q], scale, base, p + 16 * q, more);
+      if (!fresh) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[32];
+          tmem_ld32(to + 32 * q, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+          tmem_st32(to + 32 * q, o);
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kHalf; ++q) tmem_st16_async(ts + 16 * q, p + 16 * q);
+#pragma unroll
+    for (int q = 0; q < kHalf; ++q) tmem_ld32_async(ts + 32 * (kHalf + q), s[q]);  // (P ends before)
+    if (!before_hand_over()) return false;
+    if (kCtas > 1) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_leader(c, B_P + 2 * t);
+    }
+#pragma unroll
+    for (int q = 0; q < kHalf; ++q) {
+      tmem_wait_ld32(s[q]);
+      if (kSome) mask32(s[q], left - 32 * (kHalf + q));
+      weights32(s[q], scale, base, p + 16 * q, more);
+      tmem_st16_async(ts + 16 * (kHalf + q), p + 16 * q);
+    }
+    sum[0] = more[0];
+    sum[1] = more[1];
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) arrive_leader(c, B_P + 2 * t + kCtas - 1);
+    return true;
+  };
+  for (int n = 0; await_item(c, n); ++n) {
+    // Steps that every row sees whole need nothing of the item; what it is is read again
+    // behind them, so that it takes no registers meanwhile.
+    int whole;
+    {
+      const Item it = read_item(c, n);
+      const Work w = work_of<kCtas>(it, a, c.rank);
+      const Tile d = t ? w.tile[1] : w.tile[0];
+      const int stride = w.alone ? 2 : 1, shift = w.alone ? t : 0;
+      const int some = min(d.masked, t == 0 || w.alone ? w.look : max(w.look, w.tile[0].steps));
+      whole = d.rows == 0 ? 0 : min(d.steps, max(0, (some - shift + stride - 1) / stride));
+    }
+    top = -CUDART_INF_F;
+    base = 0.f;
+    sum[0] = sum[1] = make_float2(0.f, 0.f);
+    for (int j = 0; j < whole; ++j)
+      if (!step(j == 0, 0, [] { return true; })) return;
+
+    const Item it = read_item(c, n);
     const Work w = work_of<kCtas>(it, a, c.rank);
-    const Tile d = w.tile[t];
+    const Tile d = t ? w.tile[1] : w.tile[0];
     const int values = vstep, look0 = looks;
     vstep = (vstep + w.steps) % kStages;
     looks = (looks + w.steps - w.look) % (2 * kStages);
     if (t == 0 && quad == 0) flag_store(c.sbase + kOffPoison + 4 * ((n + kPoisons / 2) % kPoisons), 0);
+    // A tile's steps are every one of the item's, or every second one.
+    const int stride = w.alone ? 2 : 1, shift = w.alone ? t : 0;
+    auto own = [&](int step) { return max(0, (step - shift + stride - 1) / stride); };  // first of its steps from there on
     // The first active tile's warps look through a step's values, before its weights are handed over.
-    const int looker = t == 0 ? w.look : max(w.look, w.tile[0].steps);
-    auto look = [&](int j) {
-      const int k = look0 + j - w.look;
+    const int looker = own(t == 0 || w.alone ? w.look : max(w.look, w.tile[0].steps));
+    auto look = [&](int i) {
+      const int j = i * stride + shift, k = look0 + j - w.look;
       if (!c.wait_warp(B_RAW + k % kStages, (k / kStages) & 1, 0xA17)) return false;
       const uint32_t at = c.sbase + kOffRing + (values + j) % kStages * kStageBytes + kKBytes;
       if (look_through<kCtas>(at, quad, lane, it.lk - (w.begin + j) * F::kKeys))
@@ -884,108 +1011,49 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
           for (int half = 0; half < kCtas; ++half) arrive_leader(c, B_P + 2 * t + half);
       }
       if (d.steps > 0) op ^= 1;
+      if ((t ? w.tile[0] : w.tile[1]).steps > 0) other_op ^= 1;
+      release_item(c, n);
       continue;
     }
     const int row = d.row0 + quad * 32 + lane;  // within the request
     const int seen = visible(it, a.causal, min(row, it.lq - 1));
-    float top = -CUDART_INF_F, base = 0.f;  // the running maximum of S, and of c S (0 while there is none)
-    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    // One step; kSome: there are keys that some row does not see, or values to look through.
-    auto step = [&](int j, auto some) {
-      constexpr bool kSome = decltype(some)::value;
-      if (!c.wait_warp(B_S + t, sp, 0xA18)) return false;
-      sp ^= 1;
-      tc_fence_after();
-      constexpr int kHalf = kParts / 2;
-            const int left = seen - (w.begin + j) * F::kKeys;
-      uint32_t s[kHalf][32], p[16 * kHalf];
-      float here;
-      {
-        uint32_t u[kHalf][32];  // the second half, for the maximum
-#pragma unroll
-        for (int q = 0; q < kHalf; ++q) tmem_ld32_async(ts + 32 * q, s[q]);
-#pragma unroll
-        for (int q = 0; q < kHalf; ++q) tmem_ld32_async(ts + 32 * (kHalf + q), u[q]);
-#pragma unroll
-        for (int q = 0; q < kHalf; ++q) {
-          tmem_wait_ld32(s[q]);
-          if (kSome) mask32(s[q], left - 32 * q);
-        }
-#pragma unroll
-        for (int q = 0; q < kHalf; ++q) {
-          tmem_wait_ld32(u[q]);
-          if (kSome) mask32(u[q], left - 32 * (kHalf + q));
-        }
-        here = fmaxf(max32(s[0]), max32(u[0]));
-        if (kHalf == 2) here = max3(here, max32(s[kHalf - 1]), max32(u[kHalf - 1]));
-      }
-      float2 more[2] = {sum[0], sum[1]};
-#pragma unroll
-      for (int q = 0; q < kHalf; ++q) weights32(s[q], scale, base, p + 16 * q, more);
-      const bool move = here > top + slack;
-      if (__any_sync(0xffffffffu, move)) {
-        const float factor = move ? ex2_approx((top - here) * a.scale_log2) : 1.f;
-        if (move) {
-          top = here;
-          base = here * a.scale_log2;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) more[i] = sum[i] = make_float2(sum[i].x * factor, sum[i].y * factor);
-#pragma unroll
-        for (int q = 0; q < kHalf; ++q) weights32(s[q], scale, base, p + 16 * q, more);
-        if (j > 0) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t o[32];
-            tmem_ld32(to + 32 * q, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-            tmem_st32(to + 32 * q, o);
-          }
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < kHalf; ++q) tmem_st16_async(ts + 16 * q, p + 16 * q);
-#pragma unroll
-      for (int q = 0; q < kHalf; ++q) tmem_ld32_async(ts + 32 * (kHalf + q), s[q]);  // (P ends before)
-      if (kSome && j >= looker && !look(j)) return false;
-      if (kCtas > 1) {
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_leader(c, B_P + 2 * t);
-      }
-#pragma unroll
-      for (int q = 0; q < kHalf; ++q) {
-        tmem_wait_ld32(s[q]);
-        if (kSome) mask32(s[q], left - 32 * (kHalf + q));
-        weights32(s[q], scale, base, p + 16 * q, more);
-        tmem_st16_async(ts + 16 * (kHalf + q), p + 16 * q);
-      }
-      sum[0] = more[0];
-      sum[1] = more[1];
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_leader(c, B_P + 2 * t + kCtas - 1);
-      return true;
-    };
-    const int whole = min(d.steps, max(0, min(d.masked, looker)));
-    int j = 0;
-    for (; j < whole; ++j)
-      if (!step(j, std::false_type())) return;
-    for (; j < d.steps; ++j)
-      if (!step(j, std::true_type())) return;
+    for (int j = whole; j < d.steps; ++j)
+      if (!step(j == 0, seen - (w.begin + j * stride + shift) * F::kKeys, [&] { return j < looker || look(j); })) return;
     // ---- epilogue
+    float total = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y), mine_f = 1.f, other_f = 0.f;
+    const uint32_t stat = c.sbase + kOffStat + (quad * 32 + lane) * 8;
+    if (w.alone && t == 1) {
+      // the first tile's warps write both tiles' rows
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(stat), "f"(base), "f"(total) : "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c.bar(B_STAT));
+      if (!c.wait_warp(B_READ, ap, 0xA20)) return;
+      ap ^= 1;
+      op ^= 1;
+      other_op ^= 1;
+      release_item(c, n);
+      continue;
+    }
     if (d.steps > 0) {
       if (!c.wait_warp(B_O + t, op, 0xA19)) return;
       op ^= 1;
-      tc_fence_after();
     }
-    const float total = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    if (w.alone) {
+      if (!c.wait_warp(B_STAT, ap, 0xA1C) || !c.wait_warp(B_O + 1, other_op, 0xA1D)) return;
+      ap ^= 1;
+      float b, l;
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(b), "=f"(l) : "r"(stat) : "memory");
+      const float m = total == 0.f ? b : l == 0.f ? base : fmaxf(base, b);
+      mine_f = total == 0.f ? 0.f : ex2_approx(base - m);
+      other_f = l == 0.f ? 0.f : ex2_approx(b - m);
+      base = m;
+      total = total * mine_f + l * other_f;
+    }
+    if ((t ? w.tile[0] : w.tile[1]).steps > 0) other_op ^= 1;
+    tc_fence_after();
     const bool mine = row < it.lq;
     const bool none = total == 0.f;  // no key, or scores of -inf alone
-    const float inv = 1.f / total;
+    const float inv = mine_f / total, other_inv = other_f / total;
     const bool poison = flag_load(c.sbase + kOffPoison + 4 * (n % kPoisons)) != 0;
     const int64_t token = it.q0 + row, part_row = (int64_t)it.part * a.tokens_q + token;
     uint16_t* out = a.out + token * a.out_ts + it.head * a.out_hs;
@@ -996,7 +1064,17 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       if (d.steps > 0) tmem_ld32(to + 32 * q, r);
       float o[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : __uint_as_float(r[i]) * inv;
+      for (int i = 0; i < 32; ++i) o[i] = none || mine_f == 0.f ? 0.f : __uint_as_float(r[i]) * inv;
+      if (w.alone) {
+        tmem_ld32(tmem + lanes + TM_O + 128 + 32 * q, r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] += none || other_f == 0.f ? 0.f : __uint_as_float(r[i]) * other_inv;
+        if (q == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(c.bar(B_READ));
+        }
+      }
       if (poison && mine && !none) {
         const uint16_t* v = a.v + it.k0 * a.v_ts + it.head * a.v_hs + 32 * q;
         const int from = (w.begin + w.look) * F::kKeys, to = min(seen, (w.begin + w.steps) * F::kKeys);
@@ -1020,6 +1098,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       }
     }
     float* lse = a.parts > 1 ? a.part_lse + part_row * a.heads : a.lse + token * a.heads;
+    release_item(c, n);
     if (mine) lse[it.head] = none ? -CUDART_INF_F : fmaf(base, CUDART_LN2_F, logf(total));
   }
 }
@@ -1053,6 +1132,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   Item own{};
   if (warp == 3 && c.rank == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     own.more = item_of<kCtas>(a, (int)blockIdx.x, lane, &own);
   } else if (warp == 0) {
     if (lane == 0) {
@@ -1077,6 +1157,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         mbar_init(c.bar(B_ITEM + i), 1);
         mbar_init(c.bar(B_TAKEN + i), 9 * kCtas + 1);  // copies, softmax; and the leader's products
       }
+      mbar_init(c.bar(B_STAT), 4);
+      mbar_init(c.bar(B_READ), 4);
       mbar_init(c.bar(B_NEXT), 1);
       mbar_init(c.bar(B_ASKED), 1);
       mbar_init(c.bar(B_FIN), 1);
@@ -1091,6 +1173,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   } else if (warp == 1) {
     tmem_alloc_of<kCtas>(c.sbase + kOffTmem);
   }
+  // The work before this launch is complete before anything of it is read or replaced.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (kCtas > 1) cluster_sync();  // the peer's barriers are initialised before any arrival there
@@ -1233,20 +1318,21 @@ static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCtas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   const cudaError_t main = cudaLaunchKernelEx(&cfg, kernel, m, a);
   if (main != cudaSuccess || a.parts == 1) return main;
   cfg.gridDim = dim3((unsigned)(a.tiles * a.heads), F::kItemRows / kMergeRows);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, merge_parts_kernel<F::kItemRows>, a);
 }
 
