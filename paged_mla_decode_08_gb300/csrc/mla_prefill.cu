@@ -91,6 +91,7 @@ struct Form {
 };
 
 constexpr int kItemSlots = 4;
+constexpr int kAskAhead = 8;  // steps before an item's end at which its successor is asked for
 enum Bar : int {
   B_Q = 0,                        // [tile] Q landed (the leader's barrier)
   B_QE = B_Q + 2,                 // [tile] Q is read
@@ -106,7 +107,7 @@ enum Bar : int {
   B_TAKEN = B_ITEM + kItemSlots,  // [slot] every role of the item's CTAs has it (the leader's)
   B_STAT = B_TAKEN + kItemSlots,  // alone: the second tile's sums are there
   B_READ,                         // ... and its part of the output is read
-  B_NEXT,                         // the item's copies are issued: time to ask for the next
+  B_NEXT,                         // the item's copies come to their end: time to ask for the next
   B_ASKED,                        // the answer is there
   B_FIN,                          // every product is done
   B_COUNT
@@ -319,6 +320,8 @@ struct Ctx {
 // handed out as it gets done, and a CTA goes on to its next item without a launch,
 // with its first copies and products under the last one's epilogue.
 __device__ __forceinline__ void ask_for_cluster(uint32_t answer, uint32_t bar) {
+  fence_proxy_async_smem();  // the last answer is read
+  mbar_arrive_expect_tx(bar, 16);
   asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
                "r"(bar)
                : "memory");
@@ -333,7 +336,6 @@ __device__ __forceinline__ int read_answer(uint32_t answer) {
       : "=r"(got), "=r"(x)
       : "r"(answer)
       : "memory");
-  fence_proxy_async_smem();  // the next answer is written by the asynchronous proxy
   return got ? (int)x : -1;
 }
 
@@ -364,7 +366,6 @@ __device__ void schedule(const Ctx<kCtas>& c, const Args& a, Item it, int lane) 
       if (it.more) break;
       // fewer items than there could have been: on to the next one
       if (lane == 0) {
-        mbar_arrive_expect_tx(c.bar(B_ASKED), 16);
         ask_for_cluster(c.sbase + kOffAnswer, c.bar(B_ASKED));
       }
       __syncwarp();
@@ -389,7 +390,6 @@ __device__ void schedule(const Ctx<kCtas>& c, const Args& a, Item it, int lane) 
     if (!it.more) return;
     if (!c.wait_warp(B_NEXT, n & 1, 0xA1C)) return;
     if (lane == 0) {
-      mbar_arrive_expect_tx(c.bar(B_ASKED), 16);
       ask_for_cluster(c.sbase + kOffAnswer, c.bar(B_ASKED));
     }
     __syncwarp();
@@ -407,6 +407,17 @@ __device__ void receive(const Ctx<kCtas>& c, int lane) {
     if (!c.wait_warp(B_ITEM + slot, (n / kItemSlots) & 1, 0xA1E)) return;
     if (flag_load(c.sbase + kOffItem + slot * kItemBytes + 28) == 0) return;
   }
+}
+
+// Arrive on a barrier of the leader.  (What it orders is in place by then: this CTA's
+// TMEM behind the tcgen05 fence, its shared memory behind a proxy fence or read already;
+// a release at cluster scope would wait for all of it again, a thousand cycles.)
+template <int kCtas>
+__device__ __forceinline__ void arrive_leader(const Ctx<kCtas>& c, int bar) {
+  if (kCtas > 1)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(c.leader_bar(bar)) : "memory");
+  else
+    mbar_arrive(c.bar(bar));
 }
 
 // Item n, for a converged warp, while its slot is held.
@@ -427,12 +438,7 @@ __device__ __forceinline__ bool await_item(const Ctx<kCtas>& c, int n) {
 template <int kCtas>
 __device__ __forceinline__ void release_item(const Ctx<kCtas>& c, int n) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) {
-    if (kCtas > 1)
-      mbar_arrive_remote(c.leader_bar(B_TAKEN + n % kItemSlots));
-    else
-      mbar_arrive(c.bar(B_TAKEN + n % kItemSlots));
-  }
+  if ((threadIdx.x & 31) == 0) arrive_leader(c, B_TAKEN + n % kItemSlots);
 }
 template <int kCtas>
 __device__ __forceinline__ bool take_item(const Ctx<kCtas>& c, int n, Item* it) {
@@ -470,9 +476,10 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, uin
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
-// Announce this CTA's bytes on a barrier of the leader (cluster address).
+// Announce this CTA's bytes on a barrier of the leader (cluster address).  It orders
+// nothing; a release at cluster scope would take the producer a thousand cycles each.
 __device__ __forceinline__ void announce(uint32_t cluster_bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
                : "memory");
 }
 
@@ -525,6 +532,7 @@ __device__ void load_items(const Ctx<kCtas>& c, const Args& a, const Maps& m, in
       }
       __syncwarp();
       if (j == 0 && !(ok = load_q(1))) break;
+      if (j == max(0, w.steps - kAskAhead) && c.rank == 0 && lane == 0) mbar_arrive(c.bar(B_NEXT));
       if (!(ok = c.wait_warp(B_VE + stage, ring.phase ^ 1, 0xA12))) break;
       ++loaded;
       const bool look = j >= w.look;
@@ -540,7 +548,7 @@ __device__ void load_items(const Ctx<kCtas>& c, const Args& a, const Maps& m, in
       __syncwarp();
       if (look) raw.next();
     }
-    if (ok && c.rank == 0 && lane == 0) mbar_arrive(c.bar(B_NEXT));
+    if (ok && w.steps == 0 && c.rank == 0 && lane == 0) mbar_arrive(c.bar(B_NEXT));
     __syncwarp();
   }
   if (!ok) {  // the copies in flight land within a few microseconds
@@ -760,6 +768,7 @@ __device__ bool look_through(uint32_t values, int quarter, int lane, int own) {
         seen |= (quarter * 32 + i * 4 + (lane >> 3)) % F::kKeys < own;
       }
     }
+    fence_proxy_async_smem();
   }
   return seen;
 }
@@ -802,16 +811,6 @@ __device__ __noinline__ float non_finite(const uint16_t* v, int64_t stride, int 
     if ((bits & 0x7F80u) == 0x7F80u) sum += __uint_as_float(bits << 16);
   }
   return sum;
-}
-
-// (What it orders, this CTA's TMEM and, behind a proxy fence, its shared memory, is in
-// place by then; a release at cluster scope would wait a microsecond for it again.)
-template <int kCtas>
-__device__ __forceinline__ void arrive_leader(const Ctx<kCtas>& c, int bar) {
-  if (kCtas > 1)
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(c.leader_bar(bar)) : "memory");
-  else
-    mbar_arrive(c.bar(bar));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -999,7 +998,6 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       const uint32_t at = c.sbase + kOffRing + (values + j) % kStages * kStageBytes + kKBytes;
       if (look_through<kCtas>(at, quad, lane, it.lk - (w.begin + j) * F::kKeys))
         flag_store(c.sbase + kOffPoison + 4 * (n % kPoisons), 1);
-      fence_proxy_async_smem();
       return true;
     };
     if (d.rows == 0) {  // the tile's rows are the other CTA's, or there are none
