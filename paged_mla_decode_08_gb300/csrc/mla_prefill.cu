@@ -117,8 +117,7 @@ constexpr int kOffAbort = kOffTmem + 4;
 constexpr int kPoisons = 8;
 constexpr int kOffPoison = kOffAbort + 4;
 constexpr int kOffItem = (kOffPoison + 4 * kPoisons + 15) / 16 * 16;
-constexpr int kItemBytes = 32;
-constexpr int kOffAnswer = kOffItem + kItemSlots * kItemBytes;
+constexpr int kOffAnswer = kOffItem + kItemSlots * 64;
 constexpr int kOffStat = kOffAnswer + 16;  // [row] base and sum of the second tile
 constexpr int kSmem = kOffStat + kRows * 8 + 1024;  // + alignment slack
 static_assert(kSmem <= 232448, "shared memory budget");
@@ -141,65 +140,59 @@ struct Args {
   float scale_log2;  // scale * log2(e)
 };
 
+// An item, as the scheduler hands it out (four 16-byte pieces).
 struct Item {
-  int q0, lq, k0, lk;  // the request's rows and keys
-  int head, row0;      // first query row of the item within the request
-  int part;            // of the keys' steps
-  int more;            // 0: there is no item, the work is done
+  int q0, lq, k0, lk;   // the request's rows and keys
+  int head, row0;       // first query row of the item within the request
+  int part;             // of the keys' steps
+  int more;             // 0: there is no item, the work is done
+  // what it computes
+  int begin;            // first step, in the request's keys; the others count from it
+  int steps;
+  int look;             // first step whose values are looked through: some row does not see it whole
+  int alone;            // one tile's rows: the other tile takes them too, and every second step
+  int tile_steps[2];    // a tile's share: the steps with a key that a row of it sees
+  int unused[2];
 };
-
-// What a CTA does of an item.
-struct Tile {
-  int row0, rows;  // this CTA's, within the request
-  int steps;       // with a key that a row of the tile (of both CTAs) sees; this tile's share
-  int masked;      // first step of the item that some row of this CTA does not see whole
-};
-struct Work {
-  Tile tile[2];
-  int begin;   // first step of the item, in the request's keys; the others count from it
-  int steps;   // of the item
-  bool alone;  // one tile's rows: the other tile takes them too, and every second step
-  int look;    // first step whose values are looked through: some row does not see it whole
-};
+constexpr int kItemBytes = sizeof(Item);
+static_assert(kItemBytes == 64, "pieces of an item");
 
 __device__ __forceinline__ int visible(const Item& it, int causal, int row) {
   return causal ? max(0, min(it.lk, it.lk - it.lq + 1 + row)) : it.lk;
 }
 template <int kCtas>
-__device__ __forceinline__ Work work_of(const Item& it, const Args& a, int rank) {
+__device__ __forceinline__ void plan_item(Item* it, const Args& a) {
   using F = Form<kCtas>;
-  Work w;
   int all[2], total = 0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int first = it.row0 + t * F::kTileRows, last = min(first + F::kTileRows, it.lq) - 1;
-    w.tile[t].row0 = first + rank * kRows;
-    w.tile[t].rows = max(0, min(kRows, it.lq - w.tile[t].row0));
-    all[t] = last >= first ? (visible(it, a.causal, last) + F::kKeys - 1) / F::kKeys : 0;
+    const int first = it->row0 + t * F::kTileRows, last = min(first + F::kTileRows, it->lq) - 1;
+    all[t] = last >= first ? (visible(*it, a.causal, last) + F::kKeys - 1) / F::kKeys : 0;
     total = max(total, all[t]);
   }
-  w.begin = 0;
+  it->begin = 0;
   int end = total;
   if (a.parts > 1) {
-    w.begin = (int)((int64_t)total * it.part / a.parts);
-    end = (int)((int64_t)total * (it.part + 1) / a.parts);
+    it->begin = total * it->part / a.parts;  // (fewer than 2^25 steps, at most 32 parts)
+    end = total * (it->part + 1) / a.parts;
   }
-  w.steps = end - w.begin;
-  w.look = w.steps;
+  it->steps = it->look = end - it->begin;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    w.tile[t].steps = max(0, min(all[t], end) - w.begin);
-    w.tile[t].masked = visible(it, a.causal, min(w.tile[t].row0, it.lq - 1)) / F::kKeys - w.begin;
-    if (w.tile[t].steps > 0)
-      w.look = min(w.look, max(0, visible(it, a.causal, it.row0 + t * F::kTileRows) / F::kKeys - w.begin));
+    it->tile_steps[t] = max(0, min(all[t], end) - it->begin);
+    if (it->tile_steps[t] > 0)
+      it->look = min(it->look, max(0, visible(*it, a.causal, it->row0 + t * F::kTileRows) / F::kKeys - it->begin));
   }
-  w.alone = it.lq - it.row0 <= F::kTileRows && w.steps > 1;
-  if (w.alone) {
-    w.tile[1] = w.tile[0];
-    w.tile[0].steps = (w.steps + 1) / 2;
-    w.tile[1].steps = w.steps / 2;
+  it->alone = it->lq - it->row0 <= F::kTileRows && it->steps > 1;
+  if (it->alone) {
+    it->tile_steps[0] = (it->steps + 1) / 2;
+    it->tile_steps[1] = it->steps / 2;
   }
-  return w;
+}
+// First row of a CTA's share of a tile, within the request.
+template <int kCtas>
+__device__ __forceinline__ int first_row(const Item& it, int t, int rank) {
+  return it.row0 + (it.alone ? 0 : t * Form<kCtas>::kTileRows) + rank * kRows;
 }
 
 // Item `idx` of a head: requests own ceil(rows / kItemRows) items each, those with the
@@ -341,11 +334,14 @@ __device__ __forceinline__ int read_answer(uint32_t answer) {
 
 // The item that the CTA of this number starts with, for a converged warp.
 template <int kCtas>
-__device__ __forceinline__ bool item_of(const Args& a, int cta, int lane, Item* it) {
+__device__ __forceinline__ Item item_of(const Args& a, int cta, int lane) {
+  Item it;
   const int index = cta / kCtas, rest = index / a.tiles;
-  it->head = rest / a.parts;
-  it->part = rest - it->head * a.parts;
-  return find_item<Form<kCtas>::kItemRows>(a, index - rest * a.tiles, lane, it);
+  it.head = rest / a.parts;
+  it.part = rest - it.head * a.parts;
+  it.more = find_item<Form<kCtas>::kItemRows>(a, index - rest * a.tiles, lane, &it);
+  if (it.more) plan_item<kCtas>(&it, a);
+  return it;
 }
 
 // Run by a warp of the leader: finds items and hands them to both CTAs.
@@ -362,7 +358,7 @@ __device__ void schedule(const Ctx<kCtas>& c, const Args& a, Item it, int lane) 
   };
   for (int n = 0;; ++n) {
     for (bool known = n == 0; cta >= 0; known = false) {
-      if (!known) it.more = item_of<kCtas>(a, cta, lane, &it);
+      if (!known) it = item_of<kCtas>(a, cta, lane);
       if (it.more) break;
       // fewer items than there could have been: on to the next one
       if (lane == 0) {
@@ -377,14 +373,16 @@ __device__ void schedule(const Ctx<kCtas>& c, const Args& a, Item it, int lane) 
     if (n >= kItemSlots && !c.wait_warp(B_TAKEN + slot, (n / kItemSlots + 1) & 1, 0xA1B)) return;
     if (lane == 0) {
       const uint32_t dst = kOffItem + slot * kItemBytes;
-      st_shared_v4(c.sbase + dst, make_uint4(it.q0, it.lq, it.k0, it.lk));
-      st_shared_v4(c.sbase + dst + 16, make_uint4(it.head, it.row0, it.part, it.more));
-      mbar_arrive(c.bar(B_ITEM + slot));
-      if (kCtas > 1) {
-        const uint32_t to = peer_items + slot * kItemBytes, bar = peer_bars + 8 * slot;
-        st_async_v4(to, it.q0, it.lq, it.k0, it.lk, bar);
-        st_async_v4(to + 16, it.head, it.row0, it.part, it.more, bar);
+      const int piece[4][4] = {{it.q0, it.lq, it.k0, it.lk}, {it.head, it.row0, it.part, it.more},
+                               {it.begin, it.steps, it.look, it.alone}, {it.tile_steps[0], it.tile_steps[1], 0, 0}};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        st_shared_v4(c.sbase + dst + 16 * i, make_uint4(piece[i][0], piece[i][1], piece[i][2], piece[i][3]));
+        if (kCtas > 1)
+          st_async_v4(peer_items + slot * kItemBytes + 16 * i, piece[i][0], piece[i][1], piece[i][2], piece[i][3],
+                      peer_bars + 8 * slot);
       }
+      mbar_arrive(c.bar(B_ITEM + slot));
     }
     __syncwarp();
     if (!it.more) return;
@@ -424,8 +422,10 @@ __device__ __forceinline__ void arrive_leader(const Ctx<kCtas>& c, int bar) {
 template <int kCtas>
 __device__ __forceinline__ Item read_item(const Ctx<kCtas>& c, int n) {
   const uint32_t src = c.sbase + kOffItem + n % kItemSlots * kItemBytes;
-  const uint4 x = ld_shared_v4(src), y = ld_shared_v4(src + 16);
-  return Item{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+  const uint4 x = ld_shared_v4(src), y = ld_shared_v4(src + 16), z = ld_shared_v4(src + 32);
+  const uint2 w = ld_shared_v2(src + 48);
+  return Item{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w,
+              (int)z.x, (int)z.y, (int)z.z, (int)z.w, {(int)w.x, (int)w.y}, {0, 0}};
 }
 // Wait for item n; false: there is none, or a wait gave up.
 template <int kCtas>
@@ -501,14 +501,13 @@ __device__ void load_items(const Ctx<kCtas>& c, const Args& a, const Maps& m, in
   bool ok = true;
   Item it;
   for (int n = 0; ok && take_item(c, n, &it); ++n) {
-    const Work w = work_of<kCtas>(it, a, c.rank);
     auto load_q = [&](int t) {
-      if (w.tile[t].steps == 0) return true;
+      if (it.tile_steps[t] == 0) return true;
       if (!c.wait_warp(B_QE + t, qe[t], 0xA10)) return false;
       qe[t] ^= 1;
       if (lane == 0) {
         const uint32_t dst = c.sbase + kOffQ + t * kQTile, bar = c.leader_bar(B_Q + t);
-        const int row = it.q0 + w.tile[t].row0;
+        const int row = it.q0 + first_row<kCtas>(it, t, c.rank);
         announce(bar, kQTile);
         tma_3d<kCtas>(dst, &m.q_nope, bar, 0, it.head, row);
         tma_3d<kCtas>(dst + 2 * kBox, &m.q_nope, bar, 64, it.head, row);
@@ -518,10 +517,10 @@ __device__ void load_items(const Ctx<kCtas>& c, const Args& a, const Maps& m, in
       return true;
     };
     ok = load_q(0);
-    for (int j = 0; ok && j < w.steps; ++j, ring.next()) {
+    for (int j = 0; ok && j < it.steps; ++j, ring.next()) {
       const int stage = ring.slot;
       const uint32_t dst = c.sbase + kOffRing + stage * kStageBytes;
-      const int row = it.k0 + (w.begin + j) * F::kKeys;
+      const int row = it.k0 + (it.begin + j) * F::kKeys;
       if (!(ok = c.wait_warp(B_KE + stage, ring.phase ^ 1, 0xA11))) break;
       if (lane == 0) {
         const uint32_t bar = c.leader_bar(B_KF + stage);
@@ -532,10 +531,10 @@ __device__ void load_items(const Ctx<kCtas>& c, const Args& a, const Maps& m, in
       }
       __syncwarp();
       if (j == 0 && !(ok = load_q(1))) break;
-      if (j == max(0, w.steps - kAskAhead) && c.rank == 0 && lane == 0) mbar_arrive(c.bar(B_NEXT));
+      if (j == max(0, it.steps - kAskAhead) && c.rank == 0 && lane == 0) mbar_arrive(c.bar(B_NEXT));
       if (!(ok = c.wait_warp(B_VE + stage, ring.phase ^ 1, 0xA12))) break;
       ++loaded;
-      const bool look = j >= w.look;
+      const bool look = j >= it.look;
       if (lane == 0) {
         const uint32_t bar = look ? c.bar(B_RAW + raw.slot) : c.leader_bar(B_VF + stage);
         if (look)
@@ -548,7 +547,7 @@ __device__ void load_items(const Ctx<kCtas>& c, const Args& a, const Maps& m, in
       __syncwarp();
       if (look) raw.next();
     }
-    if (ok && w.steps == 0 && c.rank == 0 && lane == 0) mbar_arrive(c.bar(B_NEXT));
+    if (ok && it.steps == 0 && c.rank == 0 && lane == 0) mbar_arrive(c.bar(B_NEXT));
     __syncwarp();
   }
   if (!ok) {  // the copies in flight land within a few microseconds
@@ -658,76 +657,71 @@ __device__ void issue_products(const Ctx<kCtas>& c, const Args& a, uint32_t tmem
   const uint32_t q0 = desc_low(c.sbase + kOffQ, 16), k0 = desc_low(c.sbase + kOffRing, 16);
   const uint32_t v0 = desc_low(c.sbase + kOffRing + kKBytes, kBox);
   Ring<kStages> kr, vr;              // the next step's keys, the last step's values
-  uint32_t qp[2] = {0, 0}, pp[2] = {0, 0};  // parities of Q and of P
+  // of each tile a bit
+  uint32_t qp = 0, pp = 0;           // parities of Q and of P
+  uint32_t due = 0;                  // the last step's second product is still to come
+  uint32_t first = 0, last = 0;      // ... of that step in its item
+  uint32_t looked = 0;               // its values are looked through: with the weights comes the word that they can be used
   uint32_t vp = 0;                   // [stage] of the values that are not looked through
-  bool looked[2];                    // the last step's values are: with the weights comes the word that they can be used
   bool alone = false, was_alone = false;  // the tiles have steps of their own: of the next, of the last step
-  bool due[2] = {false, false};      // the last step's second product is still to come
-  bool first[2], last[2];            // ... of that step in its item
   bool ok = true, more = true;
   Item it;
   for (int n = 0; ok && more;) {
     // What is still to come is not held up by an item that is not there yet.
-    const bool take = !(due[0] || due[1]) || c.ready(B_ITEM + n % kItemSlots, (n / kItemSlots) & 1);
+    const bool take = !due || c.ready(B_ITEM + n % kItemSlots, (n / kItemSlots) & 1);
     if (take) more = take_item(c, n++, &it);
     const bool keys = take && more;
-    int steps[2] = {0, 0}, total = 1, look = 0;
-    if (keys) {
-      const Work w = work_of<kCtas>(it, a, 0);
-      steps[0] = w.tile[0].steps;
-      steps[1] = w.tile[1].steps;
-      total = max(steps[0], steps[1]);
-      look = w.look;
-      alone = w.alone;
-    }
+    const int steps0 = keys ? it.tile_steps[0] : 0, steps1 = keys ? it.tile_steps[1] : 0;
+    const int total = keys ? max(steps0, steps1) : 1, look = it.look;
+    if (keys) alone = it.alone;
     for (int j = 0; ok && j < total; ++j) {
-      const bool was[2] = {due[0], due[1]};
-#pragma unroll
+      const uint32_t was = due;
+#pragma unroll 1
       for (int t = 0; t < 2; ++t) {
-        if (was[t]) {
-          if ((t == 0 || !was[0] || was_alone) && !looked[t]) {
+        const uint32_t bit = 1u << t, d = tmem + TM_O + 128 * t, p = tmem + TM_S + 128 * t;
+        if (was & bit) {
+          if ((t == 0 || !(was & 1) || was_alone) && !(looked & bit)) {
             if (!(ok = c.wait_uniform(B_VF + vr.slot, (vp >> vr.slot) & 1, 0xA13))) break;
             vp ^= 1u << vr.slot;
           }
           const uint32_t v = v0 + vr.slot * (kStageBytes >> 4);
-          const uint32_t d = tmem + TM_O + 128 * t, p = tmem + TM_S + 128 * t;
 #pragma unroll
           for (int half = 0; half < kCtas; ++half) {  // 64 keys each; 64 value columns of a key are 128 bytes
-            if (!(ok = c.wait_uniform(B_P + 2 * t + half, pp[t], 0xA14))) break;
+            if (!(ok = c.wait_uniform(B_P + 2 * t + half, (pp >> t) & 1, 0xA14))) break;
             tc_fence_after();
-            products_ts<kCtas>(d, p + 32 * half, v + 512 * half, kIdescO, !first[t] || half > 0, go);
+            products_ts<kCtas>(d, p + 32 * half, v + 512 * half, kIdescO, !(first & bit) || half > 0, go);
           }
           if (!ok) break;
-          pp[t] ^= 1;
-          if (last[t]) commit<kCtas>(c.bar(B_O + t), go);
-          if (t == 1 || !was[1] || was_alone) {  // its last reader
+          pp ^= bit;
+          if (last & bit) commit<kCtas>(c.bar(B_O + t), go);
+          if (t == 1 || !(was & 2) || was_alone) {  // its last reader
             commit<kCtas>(c.bar(B_VE + vr.slot), go);
             vr.next();
           }
+          due &= ~bit;
         }
-        if (j < steps[t]) {
-          if ((t == 0 || j >= steps[0] || alone) && !(ok = c.wait_uniform(B_KF + kr.slot, kr.phase, 0xA15))) break;
+        const int steps = t ? steps1 : steps0;
+        if (j < steps) {
+          if ((t == 0 || j >= steps0 || alone) && !(ok = c.wait_uniform(B_KF + kr.slot, kr.phase, 0xA15))) break;
           if (j == 0) {
-            if (!(ok = c.wait_uniform(B_Q + t, qp[t], 0xA16))) break;
-            qp[t] ^= 1;
+            if (!(ok = c.wait_uniform(B_Q + t, (qp >> t) & 1, 0xA16))) break;
+            qp ^= bit;
           }
           tc_fence_after();
           const uint32_t q = q0 + t * (kQTile >> 4), k = k0 + kr.slot * (kStageBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < 3; ++kk)
-            products_ss<kCtas>(tmem + TM_S + 128 * t, q + kk * (2 * kBox >> 4), k + kk * (kBox >> 4), kIdescS, kk > 0, go);
+            products_ss<kCtas>(p, q + kk * (2 * kBox >> 4), k + kk * (kBox >> 4), kIdescS, kk > 0, go);
           commit<kCtas>(c.bar(B_S + t), go);
-          if (j == steps[t] - 1) commit<kCtas>(c.bar(B_QE + t), go);
-          if (t == 1 || j >= steps[1] || alone) {
+          if (j == steps - 1) commit<kCtas>(c.bar(B_QE + t), go);
+          if (t == 1 || j >= steps1 || alone) {
             commit<kCtas>(c.bar(B_KE + kr.slot), go);
             kr.next();
           }
-          due[t] = true;
-          first[t] = j == 0;
-          last[t] = j == steps[t] - 1;
-          looked[t] = (alone ? 2 * j + t : j) >= look;
-        } else {
-          due[t] = false;
+          due |= bit;
+          first = (first & ~bit) | (j == 0 ? bit : 0);
+          last = (last & ~bit) | (j == steps - 1 ? bit : 0);
+          looked = (looked & ~bit) | ((alone ? 2 * j + t : j) >= look ? bit : 0);
         }
       }
       was_alone = alone;
@@ -802,15 +796,23 @@ __device__ __forceinline__ void store32(uint16_t* p, const uint32_t* r, bool wid
   }
 }
 
-// Sum of what is not finite among the values of keys [from, to) in one column: they
-// weigh something, so an infinity or a NaN is what a row that sees them gets.
-__device__ __noinline__ float non_finite(const uint16_t* v, int64_t stride, int from, int to) {
-  float sum = 0.f;
-  for (int key = from; key < to; ++key) {
-    const uint32_t bits = v[key * stride];
-    if ((bits & 0x7F80u) == 0x7F80u) sum += __uint_as_float(bits << 16);
+// Adds to a row's written results what is not finite among the values of keys [from, to),
+// column by column: such a value weighs something, so an infinity or a NaN is what a
+// row that sees it gets.
+template <class T>
+__device__ __noinline__ void add_non_finite(const uint16_t* v, int64_t stride, int from, int to, T* out) {
+  for (int col = 0; col < 128; ++col) {
+    float sum = 0.f;
+    for (int key = from; key < to; ++key) {
+      const uint32_t bits = v[key * stride + col];
+      if ((bits & 0x7F80u) == 0x7F80u) sum += __uint_as_float(bits << 16);
+    }
+    if (sum == 0.f) continue;
+    if constexpr (sizeof(T) == 2)
+      out[col] = __float2bfloat16_rn(__bfloat162float(out[col]) + sum);
+    else
+      out[col] += sum;
   }
-  return sum;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -859,6 +861,17 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
     if (i + 3 < 32) b = max3(b, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
   }
   return fmaxf(a, b);
+}
+
+// A tile's first steps, of which every row of a CTA sees every key and no values are to
+// be looked through.
+template <int kCtas>
+__device__ __forceinline__ int whole_steps(const Item& it, int causal, int t, int rank) {
+  const int row = min(first_row<kCtas>(it, t, rank), it.lq - 1);
+  const int masked = visible(it, causal, row) / Form<kCtas>::kKeys - it.begin;
+  const int some = min(masked, t == 0 || it.alone ? it.look : max(it.look, it.tile_steps[0]));
+  const int mine = it.alone ? (some - t + 1) / 2 : some;  // of this tile's
+  return min(t ? it.tile_steps[1] : it.tile_steps[0], max(0, mine));
 }
 
 // The softmax and the epilogue of one tile, for every item: four warps, a row a
@@ -926,7 +939,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
 #pragma unroll
       for (int q = 0; q < kHalf; ++q) weights32(s[q], scale, base, p + 16 * q, more);
       if (!fresh) {
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           uint32_t o[32];
           tmem_ld32(to + 32 * q, o);
@@ -965,15 +978,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
   for (int n = 0; await_item(c, n); ++n) {
     // Steps that every row sees whole need nothing of the item; what it is is read again
     // behind them, so that it takes no registers meanwhile.
-    int whole;
-    {
-      const Item it = read_item(c, n);
-      const Work w = work_of<kCtas>(it, a, c.rank);
-      const Tile d = t ? w.tile[1] : w.tile[0];
-      const int stride = w.alone ? 2 : 1, shift = w.alone ? t : 0;
-      const int some = min(d.masked, t == 0 || w.alone ? w.look : max(w.look, w.tile[0].steps));
-      whole = d.rows == 0 ? 0 : min(d.steps, max(0, (some - shift + stride - 1) / stride));
-    }
+    const int whole = whole_steps<kCtas>(read_item(c, n), a.causal, t, c.rank);
     top = -CUDART_INF_F;
     base = 0.f;
     sum[0] = sum[1] = make_float2(0.f, 0.f);
@@ -981,46 +986,34 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       if (!step(j == 0, 0, [] { return true; })) return;
 
     const Item it = read_item(c, n);
-    const Work w = work_of<kCtas>(it, a, c.rank);
-    const Tile d = t ? w.tile[1] : w.tile[0];
+    const int mine_steps = t ? it.tile_steps[1] : it.tile_steps[0], other_steps = t ? it.tile_steps[0] : it.tile_steps[1];
     const int values = vstep, look0 = looks;
-    vstep = (vstep + w.steps) % kStages;
-    looks = (looks + w.steps - w.look) % (2 * kStages);
+    vstep = (vstep + it.steps) % kStages;
+    looks = (looks + it.steps - it.look) % (2 * kStages);
     if (t == 0 && quad == 0) flag_store(c.sbase + kOffPoison + 4 * ((n + kPoisons / 2) % kPoisons), 0);
     // A tile's steps are every one of the item's, or every second one.
-    const int stride = w.alone ? 2 : 1, shift = w.alone ? t : 0;
-    auto own = [&](int step) { return max(0, (step - shift + stride - 1) / stride); };  // first of its steps from there on
+    const int stride = it.alone ? 2 : 1, shift = it.alone ? t : 0;
     // The first active tile's warps look through a step's values, before its weights are handed over.
-    const int looker = own(t == 0 || w.alone ? w.look : max(w.look, w.tile[0].steps));
-    auto look = [&](int i) {
-      const int j = i * stride + shift, k = look0 + j - w.look;
+    const int looker = t == 0 || it.alone ? it.look : max(it.look, it.tile_steps[0]);
+    auto look = [&](int j) {
+      if (j < looker) return true;
+      const int k = look0 + j - it.look;
       if (!c.wait_warp(B_RAW + k % kStages, (k / kStages) & 1, 0xA17)) return false;
       const uint32_t at = c.sbase + kOffRing + (values + j) % kStages * kStageBytes + kKBytes;
-      if (look_through<kCtas>(at, quad, lane, it.lk - (w.begin + j) * F::kKeys))
+      if (look_through<kCtas>(at, quad, lane, it.lk - (it.begin + j) * F::kKeys))
         flag_store(c.sbase + kOffPoison + 4 * (n % kPoisons), 1);
       return true;
     };
-    if (d.rows == 0) {  // the tile's rows are the other CTA's, or there are none
-      for (int j = 0; j < d.steps; ++j, sp ^= 1) {
-        if (!c.wait_warp(B_S + t, sp, 0xA18)) return;
-        if (j >= looker && !look(j)) return;
-        __syncwarp();
-        if (lane == 0)
-          for (int half = 0; half < kCtas; ++half) arrive_leader(c, B_P + 2 * t + half);
-      }
-      if (d.steps > 0) op ^= 1;
-      if ((t ? w.tile[0] : w.tile[1]).steps > 0) other_op ^= 1;
-      release_item(c, n);
-      continue;
-    }
-    const int row = d.row0 + quad * 32 + lane;  // within the request
+    const int row = first_row<kCtas>(it, t, c.rank) + quad * 32 + lane;  // within the request
     const int seen = visible(it, a.causal, min(row, it.lq - 1));
-    for (int j = whole; j < d.steps; ++j)
-      if (!step(j == 0, seen - (w.begin + j * stride + shift) * F::kKeys, [&] { return j < looker || look(j); })) return;
+    for (int i = whole; i < mine_steps; ++i) {
+      const int j = i * stride + shift;
+      if (!step(i == 0, seen - (it.begin + j) * F::kKeys, [&] { return look(j); })) return;
+    }
     // ---- epilogue
     float total = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y), mine_f = 1.f, other_f = 0.f;
     const uint32_t stat = c.sbase + kOffStat + (quad * 32 + lane) * 8;
-    if (w.alone && t == 1) {
+    if (it.alone && t == 1) {
       // the first tile's warps write both tiles' rows
       asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(stat), "f"(base), "f"(total) : "memory");
       __syncwarp();
@@ -1032,11 +1025,11 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       release_item(c, n);
       continue;
     }
-    if (d.steps > 0) {
+    if (mine_steps > 0) {
       if (!c.wait_warp(B_O + t, op, 0xA19)) return;
       op ^= 1;
     }
-    if (w.alone) {
+    if (it.alone) {
       if (!c.wait_warp(B_STAT, ap, 0xA1C) || !c.wait_warp(B_O + 1, other_op, 0xA1D)) return;
       ap ^= 1;
       float b, l;
@@ -1047,7 +1040,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       base = m;
       total = total * mine_f + l * other_f;
     }
-    if ((t ? w.tile[0] : w.tile[1]).steps > 0) other_op ^= 1;
+    if (other_steps > 0) other_op ^= 1;
     tc_fence_after();
     const bool mine = row < it.lq;
     const bool none = total == 0.f;  // no key, or scores of -inf alone
@@ -1059,11 +1052,11 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       uint32_t r[32];
-      if (d.steps > 0) tmem_ld32(to + 32 * q, r);
+      if (mine_steps > 0) tmem_ld32(to + 32 * q, r);
       float o[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] = none || mine_f == 0.f ? 0.f : __uint_as_float(r[i]) * inv;
-      if (w.alone) {
+      if (it.alone) {
         tmem_ld32(tmem + lanes + TM_O + 128 + 32 * q, r);
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] += none || other_f == 0.f ? 0.f : __uint_as_float(r[i]) * other_inv;
@@ -1072,12 +1065,6 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
           __syncwarp();
           if (lane == 0) mbar_arrive(c.bar(B_READ));
         }
-      }
-      if (poison && mine && !none) {
-        const uint16_t* v = a.v + it.k0 * a.v_ts + it.head * a.v_hs + 32 * q;
-        const int from = (w.begin + w.look) * F::kKeys, to = min(seen, (w.begin + w.steps) * F::kKeys);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] += non_finite(v + i, a.v_ts, from, to);
       }
       if (a.parts > 1) {
         float4* to = reinterpret_cast<float4*>(a.part_out + (part_row * a.heads + it.head) * 128 + 32 * q);
@@ -1096,6 +1083,14 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       }
     }
     float* lse = a.parts > 1 ? a.part_lse + part_row * a.heads : a.lse + token * a.heads;
+    if (poison && mine && !none) {
+      const uint16_t* v = a.v + it.k0 * a.v_ts + it.head * a.v_hs;
+      const int from = (it.begin + it.look) * F::kKeys, to = min(seen, (it.begin + it.steps) * F::kKeys);
+      if (a.parts > 1)
+        add_non_finite(v, a.v_ts, from, to, a.part_out + (part_row * a.heads + it.head) * 128);
+      else
+        add_non_finite(v, a.v_ts, from, to, reinterpret_cast<__nv_bfloat16*>(out));
+    }
     release_item(c, n);
     if (mine) lse[it.head] = none ? -CUDART_INF_F : fmaf(base, CUDART_LN2_F, logf(total));
   }
@@ -1128,10 +1123,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   c.rank = kCtas > 1 ? (int)cluster_ctarank() : 0;
   c.leader = kCtas > 1 ? mapa(c.sbase, 0) : c.sbase;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  Item own{};
+  Item own;
   if (warp == 3 && c.rank == 0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    own.more = item_of<kCtas>(a, (int)blockIdx.x, lane, &own);
+    own = item_of<kCtas>(a, (int)blockIdx.x, lane);
   } else if (warp == 0) {
     if (lane == 0) {
       flag_store(c.sbase + kOffAbort, 0);
