@@ -893,11 +893,12 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
   int vstep = 0, looks = 0;  // steps, and steps looked through, of the items before
   float top, base;           // the running maximum of S, and of c S (0 while there is none)
   float2 sum[2];
-  // One step.  left: keys of it that this thread's row sees, where some row does not see them all
-  // (masks are left out where before_hand_over is the step's without any).
-  auto step = [&](bool fresh, int left, auto before_hand_over) {
-    constexpr bool kSome = !std::is_empty<decltype(before_hand_over)>::value;
-    if (!c.wait_warp(B_S + t, sp, 0xA18)) return false;
+  // One step.  left: keys of it that this thread's row sees, where some row does not see them
+  // all; before(): what is to be done while the scores are computed.  (A before() that keeps
+  // nothing stands for a step without masks.)
+  auto step = [&](bool fresh, int left, auto before) {
+    constexpr bool kSome = !std::is_empty<decltype(before)>::value;
+    if (!before() || !c.wait_warp(B_S + t, sp, 0xA18)) return false;
     sp ^= 1;
     tc_fence_after();
     constexpr int kHalf = kParts / 2;
@@ -953,7 +954,6 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
     for (int q = 0; q < kHalf; ++q) tmem_st16_async(ts + 16 * q, p + 16 * q);
 #pragma unroll
     for (int q = 0; q < kHalf; ++q) tmem_ld32_async(ts + 32 * (kHalf + q), s[q]);  // (P ends before)
-    if (!before_hand_over()) return false;
     if (kCtas > 1) {
       tmem_wait_st();
       tc_fence_before();
@@ -1282,7 +1282,14 @@ static int parts_of(int num_tokens_q, int num_tokens_k, int batch, int num_heads
   const int64_t room = sms / kCtas / std::max<int64_t>(1, items), most = num_tokens_k / batch / 512;
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(room, most), 32));
 }
-static bool in_pairs(int num_tokens_q, int batch) { return num_tokens_q / batch > 256; }
+// Pairs of CTAs, or one CTA an item: by the rows and keys of a request, on average.
+// Measured (128 heads; one CTA, pair): 8 requests of 512 rows 183 and 165 us, 16 of 300
+// rows 248 and 268, 16 of 200 rows 114 and 154; with 1000 keys each 8 of 200 rows 161 and
+// 143, 16 of 64 rows 206 and 259 (half of a pair has no row of a request of 128 or fewer).
+static bool in_pairs(int num_tokens_q, int num_tokens_k, int batch) {
+  const int rows = num_tokens_q / batch, keys = num_tokens_k / batch;
+  return rows > 384 || (rows > kRows && keys / 3 >= rows);
+}
 
 template <int kCtas>
 static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t stream) {
@@ -1351,7 +1358,7 @@ cudaError_t launch_prefill(const PrefillCall& p, Device dev, cudaStream_t stream
   a.tokens_k = p.num_tokens_k;
   a.causal = p.causal;
   a.scale_log2 = p.scale * 1.44269504088896340736f;
-  return in_pairs(p.num_tokens_q, p.batch) ? launch<2>(p, a, dev, stream) : launch<1>(p, a, dev, stream);
+  return in_pairs(p.num_tokens_q, p.num_tokens_k, p.batch) ? launch<2>(p, a, dev, stream) : launch<1>(p, a, dev, stream);
 }
 
 // Launch bound: the small form's CTAs, at most
@@ -1362,7 +1369,7 @@ int prefill_items(int num_tokens_q, int batch) {
 // What the parts of a call write; 0: its keys are not cut.
 size_t prefill_workspace(int num_tokens_q, int num_tokens_k, int batch, int num_heads, Device dev) {
   using namespace prefill;
-  const int parts = in_pairs(num_tokens_q, batch) ? parts_of<2>(num_tokens_q, num_tokens_k, batch, num_heads, dev.sms)
+  const int parts = in_pairs(num_tokens_q, num_tokens_k, batch) ? parts_of<2>(num_tokens_q, num_tokens_k, batch, num_heads, dev.sms)
                                                   : parts_of<1>(num_tokens_q, num_tokens_k, batch, num_heads, dev.sms);
   return parts == 1 ? 0 : align256((size_t)parts * num_tokens_q * num_heads * (128 + 1) * 4);
 }
