@@ -424,15 +424,8 @@ def mla_rope_table(table, first_position: int = 0, base: float = 10000.0, scalin
     """Fill ``table`` (fp32 CUDA [positions, rotary_dim], contiguous) with the
     cosines, then the sines, of positions first_position, first_position + 1, ...:
     the cos_sin_cache of ``mla_rope`` and ``mla_rope_quantize_cache_write``."""
-    import torch
-    if table.dim() != 2 or table.dtype != torch.float32 or not table.is_contiguous() or not table.is_cuda:
-        raise MlaError(MLA_ERR_ARG, "table must be a contiguous fp32 CUDA tensor [positions, rotary_dim]")
-    if table.device.index != torch.cuda.current_device():
-        raise MlaError(MLA_ERR_ARG, "table is on another device than the current one")
-    rows, dim = table.shape
-    _check(load().mla_rope_table(_ptr(table), int(first_position), int(rows), int(dim), float(base), int(scaling),
-                                 float(factor), int(original_max_position), float(beta_fast), float(beta_slow),
-                                 float(magnitude), _stream(stream)))
+    (_calls or _load_calls()).rope_table(table, first_position, base, scaling, factor, original_max_position, beta_fast,
+                                         beta_slow, magnitude, None if stream is None else _stream(stream))
 
 
 def mla_rope(q, k, positions, cos_sin_cache, is_neox: bool, q_out, k_out, stream=None):

@@ -43,49 +43,64 @@ constexpr int kThreads = 256;
 
 // cos and sin of position * frequency.  A position's angle is a whole number times
 // a fixed fraction of a turn, and whole turns do not matter: the fraction is held
-// in 64 bits and the product taken modulo 2^64, so the reduction costs one integer
-// product and is exact to 2^-64 of a turn a position, however far (double
-// precision, at this GPU's rate, would be what bounds the kernel).  The upper 24
-// bits of the reduced turn are exact in fp32 and go through sincospif; the rest d
-// enters as cos - d sin, sin + d cos.
+// in 64 bits and the product taken modulo 2^64, so the reduction costs two integer
+// products and is exact to 2^-33 of a turn, however far (double precision, at this
+// GPU's rate, would be what bounds the kernel).  The nearest quarter turn goes, and the
+// rest, at most pi / 4, through the Taylor polynomials of degree 9 and 10 (their next
+// terms are below 2e-9 there); the sum is off by about one unit of 2^-24.
+// 163840 positions of 64 columns: 42 MB.
 struct TableArgs {
   float* table;
   int64_t first, positions;
-  int32_t half;  // pairs of a row
+  int32_t half;        // pairs of a row
+  int32_t block_rows;  // rows of a block at a time
   float magnitude;
   uint64_t turns[MLA_ROPE_MAX_DIM / 2];  // of a position, in 2^-64 of a turn
 };
 
-__device__ __forceinline__ void cos_sin(uint64_t turn, float magnitude, float* c, float* s) {
-  const int64_t t = static_cast<int64_t>(turn);  // [-1/2, 1/2) of a turn
-  const float low = static_cast<float>(static_cast<uint32_t>(turn >> 8)) * (2.f * CUDART_PI_F * 0x1p-56f);
-  float c0, s0;
-  sincospif(static_cast<float>(static_cast<int32_t>(t >> 40)) * 0x1p-23f, &s0, &c0);
-  *c = fmaf(-low, s0, c0) * magnitude;
-  *s = fmaf(low, c0, s0) * magnitude;
+__device__ __forceinline__ void cos_sin(uint32_t turn, float magnitude, float* c, float* s) {
+  const uint32_t quarter = (turn + 0x20000000u) >> 30;
+  const float y = static_cast<float>(static_cast<int32_t>(turn - (quarter << 30))) * (2.f * CUDART_PI_F * 0x1p-32f);
+  const float z = y * y;
+  const float sy = fmaf(y * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), y);
+  const float cy =
+      fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
+  const float c0 = quarter & 1 ? sy : cy, s0 = quarter & 1 ? cy : sy;
+  *c = __uint_as_float(__float_as_uint(c0) ^ (((quarter + 1) & 2) << 30)) * magnitude;
+  *s = __uint_as_float(__float_as_uint(s0) ^ ((quarter & 2) << 30)) * magnitude;
 }
 
-// kWide: four pairs a thread (half % 4 == 0, 16-byte rows); else one
+constexpr int kTableRows = 4;  // of a thread
+
+// kWide: four pairs a thread and row (half % 4 == 0, 16-byte rows); else one
 template <bool kWide>
 __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_constant__ TableArgs a) {
   grid_dependency();
   constexpr int kPairs = kWide ? 4 : 1;
-  const int per_row = a.half / kPairs;
-  const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (item >= a.positions * per_row) return;
-  const int64_t p = item / per_row;
-  const int i = (int)(item - p * per_row) * kPairs;
-  float c[kPairs], s[kPairs];
+  const int per_row = a.half / kPairs, sub = threadIdx.x / per_row, i = (threadIdx.x - sub * per_row) * kPairs;
+  if (sub >= a.block_rows) return;
+  uint32_t high[kPairs], low[kPairs];
 #pragma unroll
-  for (int k = 0; k < kPairs; ++k)
-    cos_sin(static_cast<uint64_t>(a.first + p) * a.turns[i + k], a.magnitude, c + k, s + k);
-  float* row = a.table + p * 2 * a.half + i;
-  if (kWide) {
-    *reinterpret_cast<float4*>(row) = make_float4(c[0], c[1 % kPairs], c[2 % kPairs], c[3 % kPairs]);
-    *reinterpret_cast<float4*>(row + a.half) = make_float4(s[0], s[1 % kPairs], s[2 % kPairs], s[3 % kPairs]);
-  } else {
-    row[0] = c[0];
-    row[a.half] = s[0];
+  for (int k = 0; k < kPairs; ++k) {
+    high[k] = static_cast<uint32_t>(a.turns[i + k] >> 32);
+    low[k] = static_cast<uint32_t>(a.turns[i + k]);
+  }
+#pragma unroll
+  for (int r = 0; r < kTableRows; ++r) {
+    const int64_t p = ((int64_t)blockIdx.x * kTableRows + r) * a.block_rows + sub;
+    if (p >= a.positions) return;
+    const uint32_t position = static_cast<uint32_t>(a.first + p);
+    float c[kPairs], s[kPairs];
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) cos_sin(position * high[k] + __umulhi(position, low[k]), a.magnitude, c + k, s + k);
+    float* row = a.table + p * 2 * a.half + i;
+    if (kWide) {
+      *reinterpret_cast<float4*>(row) = make_float4(c[0], c[1 % kPairs], c[2 % kPairs], c[3 % kPairs]);
+      *reinterpret_cast<float4*>(row + a.half) = make_float4(s[0], s[1 % kPairs], s[2 % kPairs], s[3 % kPairs]);
+    } else {
+      row[0] = c[0];
+      row[a.half] = s[0];
+    }
   }
 }
 
@@ -100,89 +115,104 @@ struct RopeArgs {
   const int64_t* positions;
   const float* table;
   int64_t max_position;
-  int32_t tokens, heads;  // heads: query heads; the key is one row more
-  int32_t rows;           // of a token: heads, and the key if there is one
-  int32_t half, neox;
+  int32_t tokens, heads;  // query heads; k may be NULL
+  int32_t half;
   int32_t chunks;         // of a row: threads that share it
-  int32_t lanes;          // rows of a token at a time
+  int32_t lanes;          // heads of a token at a time
   int32_t block_tokens;   // tokens of a block
 };
 
-__device__ __forceinline__ const uint16_t* rope_src(const RopeArgs& a, int64_t t, int h) {
-  return h < a.heads ? a.q + t * a.q_ts + h * a.q_hs : a.k + t * a.k_ts;
+constexpr int kRopeRows = 4;       // that a thread has in flight
+constexpr int kRopeThreads = 128;  // 8192 tokens of 128 heads: 41.3 us (99% of a measured copy), of 256 43.3, of 512 62
+
+// Four pairs of a row.
+template <bool kNeox>
+__device__ __forceinline__ uint4 load_pairs(const uint16_t* row, int chunk, int half) {
+  if (!kNeox) return *reinterpret_cast<const uint4*>(row + 8 * chunk);
+  const uint2 lo = *reinterpret_cast<const uint2*>(row + 4 * chunk), hi = *reinterpret_cast<const uint2*>(row + half + 4 * chunk);
+  return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
-__device__ __forceinline__ uint16_t* rope_dst(const RopeArgs& a, int64_t t, int h) {
-  return h < a.heads ? a.q_out + t * a.qo_ts + h * a.qo_hs : a.k_out + t * a.ko_ts;
+// ... rotated.
+template <bool kNeox>
+__device__ __forceinline__ void rotate_pairs(uint4 v, float4 c, float4 s, uint16_t* row, int chunk, int half) {
+  float x[4], y[4], p[4], q[4];
+  if (kNeox) {
+    x[0] = bf_lo(v.x); x[1] = bf_hi(v.x); x[2] = bf_lo(v.y); x[3] = bf_hi(v.y);
+    y[0] = bf_lo(v.z); y[1] = bf_hi(v.z); y[2] = bf_lo(v.w); y[3] = bf_hi(v.w);
+  } else {
+    x[0] = bf_lo(v.x); y[0] = bf_hi(v.x); x[1] = bf_lo(v.y); y[1] = bf_hi(v.y);
+    x[2] = bf_lo(v.z); y[2] = bf_hi(v.z); x[3] = bf_lo(v.w); y[3] = bf_hi(v.w);
+  }
+  const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p[i] = __fsub_rn(__fmul_rn(x[i], cs[i]), __fmul_rn(y[i], sn[i]));
+    q[i] = __fadd_rn(__fmul_rn(y[i], cs[i]), __fmul_rn(x[i], sn[i]));
+  }
+  if (kNeox) {
+    *reinterpret_cast<uint2*>(row + 4 * chunk) = make_uint2(bf16x2(p[0], p[1]), bf16x2(p[2], p[3]));
+    *reinterpret_cast<uint2*>(row + half + 4 * chunk) = make_uint2(bf16x2(q[0], q[1]), bf16x2(q[2], q[3]));
+  } else {
+    *reinterpret_cast<uint4*>(row + 8 * chunk) =
+        make_uint4(bf16x2(p[0], q[0]), bf16x2(p[1], q[1]), bf16x2(p[2], q[2]), bf16x2(p[3], q[3]));
+  }
 }
 
 // A thread keeps the cosines and sines of its pairs (four, or one where rows are
-// not made of 16-byte pieces) and rotates them in several heads of its token.  Each
+// not made of 16-byte pieces) and rotates them in several heads of its token; the
+// first rows are on their way while the position and its cosines are found.  Each
 // product and sum is rounded to fp32 on its own, as in the cache write's rotation.
-template <bool kWide>
+template <bool kWide, bool kNeox>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
   grid_dependency();
   const int chunk = threadIdx.x % a.chunks, slot = threadIdx.x / a.chunks;
   const int sub = slot / a.lanes, lane = slot - sub * a.lanes;
   const int64_t t = (int64_t)blockIdx.x * a.block_tokens + sub;
   if (sub >= a.block_tokens || t >= a.tokens) return;
+  const bool key = a.k != nullptr && lane == a.lanes - 1;  // the last lane has the key as well
+  const int64_t step = a.lanes * a.q_hs, out_step = a.lanes * a.qo_hs;
+  const uint16_t* src = a.q + t * a.q_ts + lane * a.q_hs;
+  const uint16_t* key_src = a.k + t * a.k_ts;
+  uint4 v[kRopeRows], kv = make_uint4(0, 0, 0, 0);
+  auto fetch = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < kRopeRows; ++i)
+      if (h + i * a.lanes < a.heads) v[i] = load_pairs<kNeox>(src + i * step, chunk, a.half);
+  };
+  if (kWide) {
+    fetch(lane);
+    if (key) kv = load_pairs<kNeox>(key_src, chunk, a.half);
+  }
   const int64_t pos = a.positions[t];
   if (pos < 0 || pos >= a.max_position) {
     if (chunk == 0 && lane == 0) record(0x801);
     return;  // nothing of this token is written
   }
   const float* row = a.table + pos * 2 * a.half;
+  uint16_t* dst = a.q_out + t * a.qo_ts + lane * a.qo_hs;
+  uint16_t* key_dst = a.k_out + t * a.ko_ts;
   if (kWide) {
     const float4 c = *reinterpret_cast<const float4*>(row + 4 * chunk);
     const float4 s = *reinterpret_cast<const float4*>(row + a.half + 4 * chunk);
-    const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-    auto load = [&](int h) {
-      const uint16_t* x = rope_src(a, t, h);
-      if (!a.neox) return *reinterpret_cast<const uint4*>(x + 8 * chunk);
-      const uint2 lo = *reinterpret_cast<const uint2*>(x + 4 * chunk), hi = *reinterpret_cast<const uint2*>(x + a.half + 4 * chunk);
-      return make_uint4(lo.x, lo.y, hi.x, hi.y);
-    };
-    auto rotate = [&](int h, uint4 v) {
-      float x[4], y[4], p[4], q[4];
-      if (a.neox) {
-        x[0] = bf_lo(v.x); x[1] = bf_hi(v.x); x[2] = bf_lo(v.y); x[3] = bf_hi(v.y);
-        y[0] = bf_lo(v.z); y[1] = bf_hi(v.z); y[2] = bf_lo(v.w); y[3] = bf_hi(v.w);
-      } else {
-        x[0] = bf_lo(v.x); y[0] = bf_hi(v.x); x[1] = bf_lo(v.y); y[1] = bf_hi(v.y);
-        x[2] = bf_lo(v.z); y[2] = bf_hi(v.z); x[3] = bf_lo(v.w); y[3] = bf_hi(v.w);
-      }
+    if (key) rotate_pairs<kNeox>(kv, c, s, key_dst, chunk, a.half);
+    for (int h = lane; h < a.heads; h += kRopeRows * a.lanes) {
+      if (h > lane) fetch(h);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[i] = __fsub_rn(__fmul_rn(x[i], cs[i]), __fmul_rn(y[i], sn[i]));
-        q[i] = __fadd_rn(__fmul_rn(y[i], cs[i]), __fmul_rn(x[i], sn[i]));
-      }
-      uint16_t* o = rope_dst(a, t, h);
-      if (a.neox) {
-        *reinterpret_cast<uint2*>(o + 4 * chunk) = make_uint2(bf16x2(p[0], p[1]), bf16x2(p[2], p[3]));
-        *reinterpret_cast<uint2*>(o + a.half + 4 * chunk) = make_uint2(bf16x2(q[0], q[1]), bf16x2(q[2], q[3]));
-      } else {
-        *reinterpret_cast<uint4*>(o + 8 * chunk) =
-            make_uint4(bf16x2(p[0], q[0]), bf16x2(p[1], q[1]), bf16x2(p[2], q[2]), bf16x2(p[3], q[3]));
-      }
-    };
-    int h = lane;
-    for (; h + 3 * a.lanes < a.rows; h += 4 * a.lanes) {
-      uint4 v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = load(h + i * a.lanes);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) rotate(h + i * a.lanes, v[i]);
+      for (int i = 0; i < kRopeRows; ++i)
+        if (h + i * a.lanes < a.heads) rotate_pairs<kNeox>(v[i], c, s, dst + i * out_step, chunk, a.half);
+      src += kRopeRows * step;
+      dst += kRopeRows * out_step;
     }
-    for (; h < a.rows; h += a.lanes) rotate(h, load(h));
   } else {
     const float c = row[chunk], s = row[a.half + chunk];
-    const int at0 = a.neox ? chunk : 2 * chunk, at1 = a.neox ? a.half + chunk : 2 * chunk + 1;
-    for (int h = lane; h < a.rows; h += a.lanes) {
-      const uint16_t* x = rope_src(a, t, h);
+    const int at0 = kNeox ? chunk : 2 * chunk, at1 = kNeox ? a.half + chunk : 2 * chunk + 1;
+    auto one = [&](const uint16_t* x, uint16_t* o) {
       const float u = bf(x[at0]), v = bf(x[at1]);
-      uint16_t* o = rope_dst(a, t, h);
       o[at0] = to_bf16(__fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s)));
       o[at1] = to_bf16(__fadd_rn(__fmul_rn(v, c), __fmul_rn(u, s)));
-    }
+    };
+    if (key) one(key_src, key_dst);
+    for (int h = lane; h < a.heads; h += a.lanes, src += step, dst += out_step) one(src, dst);
   }
 }
 
@@ -201,8 +231,12 @@ struct GatherArgs {
   float k_scale;
 };
 
-constexpr int kGatherRows = 4;  // of a warp
-
+// A warp copies four rows: it looks them up at once, a lane each (a chain: offsets, block
+// table, row), then has all of them on their way, and their rotary parts and scales in
+// one access for the four.  65536 rows of e4m3: 4 rows a warp 15.9 us, 2 rows 16.8, 8 and 16
+// rows four at a time 18.5 and 19.4 (fewer warps, the chain shows), before the accesses
+// were joined.
+constexpr int kGatherRows = 4;
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
   uint32_t d;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(d) : "r"(v));
@@ -237,10 +271,43 @@ __device__ __forceinline__ int owner(const GatherArgs& a, int r, int lane) {
   return lo;
 }
 
-// A warp copies four consecutive rows; a lane 16 latent columns and, the first
-// ones, a piece of the rotary ones.
+// 16 codes into 16 bf16 of their values times the scale
+__device__ __forceinline__ void store_widened(uint4* out, uint4 v, float scale) {
+  const uint2 p0 = widen(v.x, scale), p1 = widen(v.y, scale), p2 = widen(v.z, scale), p3 = widen(v.w, scale);
+  out[0] = make_uint4(p0.x, p0.y, p1.x, p1.y);
+  out[1] = make_uint4(p2.x, p2.y, p3.x, p3.y);
+}
+// A lane's 16 columns of a row through the quantiser (8 lanes share a block of 128).
+__device__ __forceinline__ uint4 quantize16(const uint4 (&x)[2], float* scale) {
+  float v[16];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[8 * k + 2 * e] = bf_lo(u[e]);
+      v[8 * k + 2 * e + 1] = bf_hi(u[e]);
+    }
+  }
+  uint32_t top = 0;  // magnitudes order as integers, NaN above all
+#pragma unroll
+  for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int d = 1; d < 8; d *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float amax = __uint_as_float(top);
+  *scale = __fdiv_rn(amax < 1e-10f ? 1e-10f : amax, 448.f);
+  const float inv = __frcp_rn(*scale);
+  uint32_t code[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    code[e] = e4m3x2(__fmul_rn(v[4 * e], inv), __fmul_rn(v[4 * e + 1], inv)) |
+              (uint32_t)e4m3x2(__fmul_rn(v[4 * e + 2], inv), __fmul_rn(v[4 * e + 3], inv)) << 16;
+  return make_uint4(code[0], code[1], code[2], code[3]);
+}
+
 template <bool kCacheE4m3, bool kOutE4m3>
 __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const GatherArgs a) {
+  constexpr int kRowBytes = kCacheE4m3 ? 576 : 1152;
   grid_dependency();
   const int lane = threadIdx.x & 31;
   const int64_t row0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kGatherRows;
@@ -253,17 +320,16 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const GatherArgs
     if (bad) record(0x903);
   }
   if (row0 >= a.tokens) return;
-  constexpr int kRowBytes = kCacheE4m3 ? 576 : 1152, kLaneBytes = kCacheE4m3 ? 16 : 32;
-  const int my_row = (int)row0 + min(lane, kGatherRows - 1);
-  const uint8_t* src_mine = nullptr;
+  const uint8_t* mine = nullptr;  // lane i: where row row0 + i comes from
   {
+    const int row = (int)row0 + min(lane, kGatherRows - 1);
     int b = owner(a, (int)row0, lane);
-    if (lane < kGatherRows && my_row < a.tokens) {
-      while (b < a.batch && __ldg(a.cu + b + 1) <= my_row) ++b;
+    if (lane < kGatherRows && row < a.tokens) {
+      while (b < a.batch && __ldg(a.cu + b + 1) <= row) ++b;
       if (b < a.batch) {
         const int begin = __ldg(a.cu + b);
-        const int64_t token = (a.starts ? (int64_t)__ldg(a.starts + b) : 0) + my_row - begin;
-        if (my_row >= begin) {
+        const int64_t token = (a.starts ? (int64_t)__ldg(a.starts + b) : 0) + row - begin;
+        if (row >= begin) {
           const int64_t block = token >> a.page_shift;
           if (token < 0 || block >= a.bt_stride) {
             record(0x901);
@@ -272,83 +338,69 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const GatherArgs
             if (page < 0 || page >= a.num_pages)
               record(0x902);
             else
-              src_mine = a.kv + ((page << a.page_shift) + (token & ((1 << a.page_shift) - 1))) * kRowBytes;
+              mine = a.kv + ((page << a.page_shift) + (token & ((1 << a.page_shift) - 1))) * kRowBytes;
           }
         }
       }
     }
   }
+  // the rotary parts: a lane a 16-byte piece of row `pe_row`
+  constexpr int kPieces = kCacheE4m3 ? 4 : 8;
+  const int pe_row = lane / kPieces, piece = lane % kPieces;
+  const auto address = reinterpret_cast<unsigned long long>(mine);
+  const uint8_t* pe_src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, address, pe_row & (kGatherRows - 1)));
+  const bool pe_live = pe_row < kGatherRows && pe_src;
   const uint8_t* src[kGatherRows];
-  uint4 x[kGatherRows][kLaneBytes / 16], pe[kGatherRows];
+  uint4 x[kGatherRows][kCacheE4m3 ? 1 : 2], pe;
 #pragma unroll
   for (int i = 0; i < kGatherRows; ++i) {
-    src[i] = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src_mine), i));
-    if (src[i]) {
+    src[i] = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, address, i));
+    if (!src[i]) continue;
 #pragma unroll
-      for (int k = 0; k < kLaneBytes / 16; ++k) x[i][k] = *reinterpret_cast<const uint4*>(src[i] + lane * kLaneBytes + 16 * k);
-      if (lane < kRowBytes / 144) pe[i] = *reinterpret_cast<const uint4*>(src[i] + 32 * kLaneBytes + 16 * lane);
-    }
+    for (int k = 0; k < (kCacheE4m3 ? 1 : 2); ++k)
+      x[i][k] = *reinterpret_cast<const uint4*>(src[i] + ((kCacheE4m3 ? 1 : 2) * lane + k) * 16);
   }
+  if (pe_live) pe = *reinterpret_cast<const uint4*>(pe_src + (kRowBytes - 16 * kPieces) + 16 * piece);
+
+  float scales[kGatherRows];
 #pragma unroll
   for (int i = 0; i < kGatherRows; ++i) {
     if (!src[i]) continue;
     const int64_t r = row0 + i;
-    uint16_t* pe_out = a.k_pe + r * a.k_pe_stride;
-    if (kCacheE4m3) {
-      if (lane < 4) {
-        const uint2 p0 = widen(pe[i].x, a.k_scale), p1 = widen(pe[i].y, a.k_scale), p2 = widen(pe[i].z, a.k_scale),
-                    p3 = widen(pe[i].w, a.k_scale);
-        reinterpret_cast<uint4*>(pe_out)[2 * lane] = make_uint4(p0.x, p0.y, p1.x, p1.y);
-        reinterpret_cast<uint4*>(pe_out)[2 * lane + 1] = make_uint4(p2.x, p2.y, p3.x, p3.y);
-      }
-    } else if (lane < 8) {
-      reinterpret_cast<uint4*>(pe_out)[lane] = pe[i];
-    }
-    if (kOutE4m3) {
+    if constexpr (kOutE4m3) {
       uint4* out = reinterpret_cast<uint4*>(a.latent + r * a.latent_stride) + lane;
-      float scale = a.k_scale;
-      if (kCacheE4m3) {
+      if constexpr (kCacheE4m3)
         *out = x[i][0];  // the codes as they are, with the cache's scale
-      } else {
-        float v[16];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint4 w = x[i][k % (kLaneBytes / 16)];
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[8 * k + 2 * e] = bf_lo(u[e]);
-            v[8 * k + 2 * e + 1] = bf_hi(u[e]);
-          }
-        }
-        uint32_t top = 0;  // magnitudes order as integers, NaN above all
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int d = 1; d < 8; d *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));  // a block of 128: 8 lanes
-        const float amax = __uint_as_float(top);
-        scale = __fdiv_rn(amax < 1e-10f ? 1e-10f : amax, 448.f);
-        const float inv = __frcp_rn(scale);
-        uint32_t code[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          code[e] = e4m3x2(__fmul_rn(v[4 * e], inv), __fmul_rn(v[4 * e + 1], inv)) |
-                    (uint32_t)e4m3x2(__fmul_rn(v[4 * e + 2], inv), __fmul_rn(v[4 * e + 3], inv)) << 16;
-        *out = make_uint4(code[0], code[1], code[2], code[3]);
-      }
-      if (lane % 8 == 0) a.scales[(lane / 8) * a.scale_stride + r] = scale;
+      else
+        *out = quantize16(x[i], &scales[i]);
     } else {
       uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.latent) + r * a.latent_stride) + 2 * lane;
-      if (kCacheE4m3) {
-        const uint2 p0 = widen(x[i][0].x, a.k_scale), p1 = widen(x[i][0].y, a.k_scale), p2 = widen(x[i][0].z, a.k_scale),
-                    p3 = widen(x[i][0].w, a.k_scale);
-        out[0] = make_uint4(p0.x, p0.y, p1.x, p1.y);
-        out[1] = make_uint4(p2.x, p2.y, p3.x, p3.y);
+      if constexpr (kCacheE4m3) {
+        store_widened(out, x[i][0], a.k_scale);
       } else {
         out[0] = x[i][0];
-        out[1] = x[i][kLaneBytes / 16 - 1];
+        out[1] = x[i][1];
       }
     }
+  }
+  if (pe_live) {
+    uint4* out = reinterpret_cast<uint4*>(a.k_pe + (row0 + pe_row) * a.k_pe_stride);
+    if (kCacheE4m3)
+      store_widened(out + 2 * piece, pe, a.k_scale);
+    else
+      out[piece] = pe;
+  }
+  if constexpr (kOutE4m3) {  // lane 8 b + i: block b of row i
+    const int i = lane % 8;
+    float scale = a.k_scale;
+    bool live = false;
+#pragma unroll
+    for (int k = 0; k < kGatherRows; ++k)
+      if (i == k) {
+        live = src[k] != nullptr;
+        if (!kCacheE4m3) scale = scales[k];
+      }
+    if (live) a.scales[(lane / 8) * a.scale_stride + row0 + i] = scale;
   }
 }
 
@@ -404,10 +456,10 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const MergeArgs m) {
 }
 
 template <class Kernel, class A>
-static cudaError_t launch_pdl(Kernel kernel, int64_t blocks, cudaStream_t stream, const A& a) {
+static cudaError_t launch_pdl(Kernel kernel, int64_t blocks, int threads, cudaStream_t stream, const A& a) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -435,8 +487,9 @@ cudaError_t launch_rope_table(float* table, int64_t first, int64_t positions, in
   a.magnitude = magnitude;
   std::copy(turns, turns + half, a.turns);
   const bool wide = half % 4 == 0 && multiple(table, 16);
-  const int64_t items = positions * (wide ? half / 4 : half), blocks = (items + kThreads - 1) / kThreads;
-  return wide ? launch_pdl(rope_table_kernel<true>, blocks, stream, a) : launch_pdl(rope_table_kernel<false>, blocks, stream, a);
+  a.block_rows = kThreads / (wide ? half / 4 : half);
+  const int64_t block = (int64_t)kTableRows * a.block_rows, blocks = (positions + block - 1) / block;
+  return wide ? launch_pdl(rope_table_kernel<true>, blocks, kThreads, stream, a) : launch_pdl(rope_table_kernel<false>, blocks, kThreads, stream, a);
 }
 
 cudaError_t launch_rope(HeadRows q, HeadRows k, HeadRows q_out, HeadRows k_out, const int64_t* positions,
@@ -459,19 +512,20 @@ cudaError_t launch_rope(HeadRows q, HeadRows k, HeadRows q_out, HeadRows k_out, 
   a.max_position = max_position;
   a.tokens = tokens;
   a.heads = heads;
-  a.rows = heads + (k.p ? 1 : 0);
   a.half = half;
-  a.neox = neox;
   auto in_pieces = [](const HeadRows& r) {
     return !r.p || (multiple(r.p, 16) && r.token_stride % 8 == 0 && r.head_stride % 8 == 0);
   };
   const bool wide = half % 4 == 0 && multiple(table, 16) && in_pieces(q) && in_pieces(k) && in_pieces(q_out) && in_pieces(k_out);
   a.chunks = wide ? half / 4 : half;
-  const int slots = kThreads / a.chunks;
-  a.lanes = std::min(slots, a.rows);
+  const int threads = a.chunks <= kRopeThreads ? kRopeThreads : kThreads;  // (a chunk each at least)
+  const int slots = threads / a.chunks;
+  a.lanes = std::max(1, std::min(slots, heads));
   a.block_tokens = slots / a.lanes;
   const int64_t blocks = ((int64_t)tokens + a.block_tokens - 1) / a.block_tokens;
-  return wide ? launch_pdl(rope_kernel<true>, blocks, stream, a) : launch_pdl(rope_kernel<false>, blocks, stream, a);
+  if (neox)
+    return wide ? launch_pdl(rope_kernel<true, true>, blocks, threads, stream, a) : launch_pdl(rope_kernel<false, true>, blocks, threads, stream, a);
+  return wide ? launch_pdl(rope_kernel<true, false>, blocks, threads, stream, a) : launch_pdl(rope_kernel<false, false>, blocks, threads, stream, a);
 }
 
 cudaError_t launch_cache_gather(const void* kv, bool kv_e4m3, int64_t num_pages, int page_size, const int32_t* block_table,
@@ -499,10 +553,10 @@ cudaError_t launch_cache_gather(const void* kv, bool kv_e4m3, int64_t num_pages,
   constexpr int kBlockRows = kThreads / 32 * kGatherRows;
   const int64_t blocks = ((int64_t)tokens + kBlockRows - 1) / kBlockRows;
   if (kv_e4m3)
-    return latent_e4m3 ? launch_pdl(cache_gather_kernel<true, true>, blocks, stream, a)
-                       : launch_pdl(cache_gather_kernel<true, false>, blocks, stream, a);
-  return latent_e4m3 ? launch_pdl(cache_gather_kernel<false, true>, blocks, stream, a)
-                     : launch_pdl(cache_gather_kernel<false, false>, blocks, stream, a);
+    return latent_e4m3 ? launch_pdl(cache_gather_kernel<true, true>, blocks, kThreads, stream, a)
+                       : launch_pdl(cache_gather_kernel<true, false>, blocks, kThreads, stream, a);
+  return latent_e4m3 ? launch_pdl(cache_gather_kernel<false, true>, blocks, kThreads, stream, a)
+                     : launch_pdl(cache_gather_kernel<false, false>, blocks, kThreads, stream, a);
 }
 
 cudaError_t launch_merge_states(HeadRows x, const float* lse_x, HeadRows y, const float* lse_y, HeadRows out, float* lse,
@@ -525,7 +579,7 @@ cudaError_t launch_merge_states(HeadRows x, const float* lse_x, HeadRows y, cons
   m.heads = heads;
   m.chunks = dim / 8;
   m.block_rows = kThreads / m.chunks;
-  return launch_pdl(merge_kernel, (m.rows + m.block_rows - 1) / m.block_rows, stream, m);
+  return launch_pdl(merge_kernel, (m.rows + m.block_rows - 1) / m.block_rows, kThreads, stream, m);
 }
 
 cudaError_t prompt_rows_read_error(int* code, bool reset) {

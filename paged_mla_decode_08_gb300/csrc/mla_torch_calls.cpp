@@ -287,10 +287,27 @@ double as_double(PyObject* o) {
   return v;
 }
 
+int64_t as_int64(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw std::exception();
+  return v;
+}
+
 bool as_bool(PyObject* o) {
   const int v = PyObject_IsTrue(o);
   if (v < 0) throw std::exception();
   return v != 0;
+}
+
+// (table, first_position, base, scaling, factor, original_max_position, beta_fast, beta_slow, magnitude, stream)
+PyObject* rope_table(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 10, [&] {
+    const at::Tensor& t = tensor(a[0], "table", 2, kFp32);
+    packed(t, "table");
+    check(mla_rope_table(static_cast<float*>(t.data_ptr()), as_int64(a[1]), t.size(0), size32(t.size(1), "rotary_dim"),
+                         as_double(a[2]), as_int(a[3]), as_double(a[4]), as_int64(a[5]), as_double(a[6]), as_double(a[7]),
+                         as_double(a[8]), as_stream(a[9])));
+  });
 }
 
 // (q, k, positions, cos_sin_cache, is_neox, q_out, k_out, stream)
@@ -418,6 +435,7 @@ PyMethodDef methods[] = {fast<add_rmsnorm>("add_rmsnorm"),
                          fast<act_quantize>("act_quantize"),
                          fast<gemm_fp8>("gemm_fp8"),
                          fast<grouped_gemm_fp8>("grouped_gemm_fp8"),
+                         fast<rope_table>("rope_table"),
                          fast<rope>("rope"),
                          fast<cache_gather>("cache_gather"),
                          fast<prefill>("prefill"),
