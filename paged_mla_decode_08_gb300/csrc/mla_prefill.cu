@@ -1205,41 +1205,46 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 // ------------------------------------------------------------------ parts
 
 // lse = ln sum_k e^lse_k, out = sum_k e^(lse_k - lse) out_k over the parts of a row; a
-// warp a row, 64 rows a block.
-constexpr int kMergeRows = 64;
+// warp a row, so that all rows' loads are on their way at once, four parts at a time.
+constexpr int kMergeRows = 8;  // of a block
 template <int kItemRows>
-__global__ void __launch_bounds__(256) merge_parts_kernel(const Args a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = (int)blockIdx.x / a.tiles;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   Item it;
   if (!find_item<kItemRows>(a, (int)blockIdx.x - head * a.tiles, lane, &it)) return;
-  const int first = it.row0 + (int)blockIdx.y * kMergeRows;
-  const int end = min(first + kMergeRows, min(it.row0 + kItemRows, it.lq));
-  for (int row = first + warp; row < end; row += 8) {
-    const int64_t token = it.q0 + row, at = token * a.heads + head, stride = (int64_t)a.tokens_q * a.heads;
-    float mine = lane < a.parts ? __ldcg(a.part_lse + lane * stride + at) : -CUDART_INF_F;  // at most 32 parts
-    float top = mine;
+  const int row = it.row0 + (int)blockIdx.y * kMergeRows + warp;
+  if (row >= it.lq) return;
+  const int64_t token = it.q0 + row, at = token * a.heads + head, stride = (int64_t)a.tokens_q * a.heads;
+  const float mine = lane < a.parts ? __ldcg(a.part_lse + lane * stride + at) : -CUDART_INF_F;  // at most 32 parts
+  const float4* x = reinterpret_cast<const float4*>(a.part_out + at * 128) + lane;
+  float top = mine;
 #pragma unroll
-    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float base = top == -CUDART_INF_F ? 0.f : top;
-    float w = expf(mine - base), sum = w;
+  for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float base = top == -CUDART_INF_F ? 0.f : top;
+  float w = expf(mine - base), sum = w;
 #pragma unroll
-    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    w = sum == 0.f ? 0.f : w / sum;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < a.parts; ++k) {
-      const float f = __shfl_sync(0xffffffffu, w, k);
-      if (f == 0.f) continue;  // (it may not have been written)
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_out + (k * stride + at) * 128) + lane);
-      o.x += f * x.x;
-      o.y += f * x.y;
-      o.z += f * x.z;
-      o.w += f * x.w;
+  for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  w = sum == 0.f ? 0.f : w / sum;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < a.parts; k0 += 4) {
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k0 + k < a.parts) v[k] = __ldcg(x + (k0 + k) * stride * 32);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+      if (k0 + k >= a.parts || f == 0.f) continue;  // (it may not have been written)
+      o.x += f * v[k].x;
+      o.y += f * v[k].y;
+      o.z += f * v[k].z;
+      o.w += f * v[k].w;
     }
-    *reinterpret_cast<uint2*>(a.out + token * a.out_ts + head * a.out_hs + 4 * lane) = make_uint2(pack(o.x, o.y), pack(o.z, o.w));
-    if (lane == 0) a.lse[at] = sum == 0.f ? -CUDART_INF_F : base + logf(sum);
   }
+  *reinterpret_cast<uint2*>(a.out + token * a.out_ts + head * a.out_hs + 4 * lane) = make_uint2(pack(o.x, o.y), pack(o.z, o.w));
+  if (lane == 0) a.lse[at] = sum == 0.f ? -CUDART_INF_F : base + logf(sum);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1330,7 +1335,7 @@ static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t
   const cudaError_t main = cudaLaunchKernelEx(&cfg, kernel, m, a);
   if (main != cudaSuccess || a.parts == 1) return main;
   cfg.gridDim = dim3((unsigned)(a.tiles * a.heads), F::kItemRows / kMergeRows);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(32 * kMergeRows);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, merge_parts_kernel<F::kItemRows>, a);
