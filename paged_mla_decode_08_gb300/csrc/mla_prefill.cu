@@ -91,7 +91,7 @@ struct Form {
 };
 
 constexpr int kItemSlots = 4;
-constexpr int kAskAhead = 8;  // steps before an item's end at which its successor is asked for
+constexpr int kAskAhead = 4;  // steps before an item's end at which its successor is asked for
 enum Bar : int {
   B_Q = 0,                        // [tile] Q landed (the leader's barrier)
   B_QE = B_Q + 2,                 // [tile] Q is read
@@ -134,6 +134,7 @@ struct Args {
   int32_t batch, heads, tokens_q, tokens_k;
   int32_t tiles;   // row blocks of a head: at most this many exist
   int32_t parts;   // items of a row block: each has a part of the keys
+  int32_t group;   // heads whose items are mixed
   float* part_out; // [part][token][head][128], [part][token][head]: what a part alone gives
   float* part_lse;
   int32_t causal;
@@ -332,14 +333,19 @@ __device__ __forceinline__ int read_answer(uint32_t answer) {
   return got ? (int)x : -1;
 }
 
-// The item that the CTA of this number starts with, for a converged warp.
+// The item that the CTA of this number starts with, for a converged warp.  Items come
+// a row block at a time, a request's last and longest first, for a group of heads whose
+// keys and values stay in L2; then the next group's.
 template <int kCtas>
 __device__ __forceinline__ Item item_of(const Args& a, int cta, int lane) {
   Item it;
-  const int index = cta / kCtas, rest = index / a.tiles;
-  it.head = rest / a.parts;
-  it.part = rest - it.head * a.parts;
-  it.more = find_item<Form<kCtas>::kItemRows>(a, index - rest * a.tiles, lane, &it);
+  const int index = cta / kCtas, group = index / (a.group * a.tiles * a.parts);
+  const int rest = index - group * (a.group * a.tiles * a.parts);
+  const int of_tile = min(a.group, a.heads - group * a.group) * a.parts;  // items of a row block, of the group's heads
+  const int tile = rest / of_tile, within = rest - tile * of_tile;
+  it.head = group * a.group + within / a.parts;
+  it.part = within % a.parts;
+  it.more = find_item<Form<kCtas>::kItemRows>(a, tile, lane, &it);
   if (it.more) plan_item<kCtas>(&it, a);
   return it;
 }
@@ -863,6 +869,18 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
   return fmaxf(a, b);
 }
 
+// Item n has values of its own that are not finite: told to both CTAs, since each looks
+// through half of the columns.
+template <int kCtas>
+__device__ __forceinline__ void note_non_finite(const Ctx<kCtas>& c, int n) {
+  const uint32_t at = c.sbase + kOffPoison + 4 * (n % kPoisons);
+  flag_store(at, 1);
+  if (kCtas > 1) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa(at, c.rank ^ 1)), "r"(1) : "memory");
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  }
+}
+
 // A tile's first steps, of which every row of a CTA sees every key and no values are to
 // be looked through.
 template <int kCtas>
@@ -1001,7 +1019,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       if (!c.wait_warp(B_RAW + k % kStages, (k / kStages) & 1, 0xA17)) return false;
       const uint32_t at = c.sbase + kOffRing + (values + j) % kStages * kStageBytes + kKBytes;
       if (look_through<kCtas>(at, quad, lane, it.lk - (it.begin + j) * F::kKeys))
-        flag_store(c.sbase + kOffPoison + 4 * (n % kPoisons), 1);
+        note_non_finite(c, n);
       return true;
     };
     const int row = first_row<kCtas>(it, t, c.rank) + quad * 32 + lane;  // within the request
@@ -1296,6 +1314,11 @@ static bool in_pairs(int num_tokens_q, int num_tokens_k, int batch) {
   return rows > 384 || (rows > kRows && keys / 3 >= rows);
 }
 
+// Keys and values of a group of heads (a request's, on average).  16 and 128 heads of one
+// prompt of 8192: 24 MB 229 and 1494 us, 32 MB 193 and 1460, 48 MB 194 and 1578; one head
+// after the other 237 and 1598.
+constexpr int64_t kGroupBytes = 32 << 20;
+
 template <int kCtas>
 static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t stream) {
   using F = Form<kCtas>;
@@ -1316,6 +1339,8 @@ static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t
     return cudaErrorNotSupported;
   a.tiles = items_of_a_head(p.num_tokens_q, p.batch, F::kItemRows);
   a.parts = parts_of<kCtas>(p.num_tokens_q, p.num_tokens_k, p.batch, p.num_heads, dev.sms);
+  const int64_t groups = std::max<int64_t>(1, (512 * (tk / p.batch) * p.num_heads + kGroupBytes - 1) / kGroupBytes);
+  a.group = (int)((p.num_heads + groups - 1) / groups);
   a.part_out = static_cast<float*>(p.workspace);
   a.part_lse = a.part_out + (int64_t)a.parts * p.num_tokens_q * p.num_heads * 128;
   cudaLaunchConfig_t cfg = {};

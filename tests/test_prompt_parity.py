@@ -300,3 +300,139 @@ def test_merge_of_parts_that_weigh_nothing():
     la[0], lb[0] = nan, 1.0
     B.mla_merge_states(a, la, b, lb, out, lse)
     assert lse[0].isnan() and out[0].isnan().all()
+
+
+# ---- attention: masked places, offsets, strides
+
+
+@pytest.mark.parametrize("h", [1, 3])
+@pytest.mark.parametrize("q_lens,k_lens", [([40], [40]), ([300], [300]), ([700], [900]), ([5, 130, 260], [400, 130, 700]), ([90], [3000])])
+@pytest.mark.parametrize("where", ["k_nope", "k_pe", "v"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_masked_places_may_hold_anything(h, q_lens, k_lens, where, bad):
+    """A key or value that is not finite changes the rows that see it and no other."""
+    a = Attn(h, q_lens, k_lens, True, seed=3)
+    clean = [x.clone() for x in a.run()]
+    x = getattr(a, where)
+    ends = np.cumsum(k_lens)
+    for end, n in zip(ends, q_lens):
+        x[end - n // 2, ..., 5] = bad  # the second half of the request's rows see it
+    a.run()
+    row = 0
+    for n in q_lens:
+        first = n - n // 2
+        assert torch.equal(a.out[row:row + first], clean[0][row:row + first])
+        assert torch.equal(a.lse[row:row + first], clean[1][row:row + first])
+        part = a.out[row + first:row + n].float()
+        if where == "v":
+            assert torch.equal(part[..., :5], clean[0][row + first:row + n, :, :5].float())
+            assert torch.equal(part[..., 6:], clean[0][row + first:row + n, :, 6:].float())
+            assert torch.equal(a.lse[row + first:row + n], clean[1][row + first:row + n])
+            assert part[..., 5].isnan().all() if bad != bad else torch.all(part[..., 5] == bad)
+        elif bad != bad:
+            assert part.isnan().all() and a.lse[row + first:row + n].isnan().all()
+        row += n
+
+
+def test_values_of_both_infinities():
+    a = Attn(2, [200], [200], True, seed=4)
+    a.v[50, :, 7], a.v[150, :, 7] = float("inf"), -float("inf")
+    a.run()
+    col = a.out[:, :, 7].float()
+    assert torch.all(col[:50].isfinite()) and torch.all(col[50:150] == float("inf")) and col[150:].isnan().all()
+
+
+def test_rows_behind_the_last_key_and_rows_without_an_owner():
+    """Rows past the last request, and the gaps that offsets leave, are not touched; keys there are not read."""
+    a = Attn(2, [100, 50], [100, 50], True, seed=5)
+    a.cu_q = torch.tensor([0, 60, 120], dtype=torch.int32, device="cuda")     # 30 rows at the end are no one's
+    a.cu_k = torch.tensor([0, 60, 120], dtype=torch.int32, device="cuda")
+    a.k_nope[120:], a.v[120:], a.k_pe[120:] = float("nan"), float("nan"), float("nan")
+    a.run()
+    assert torch.all(a.out[120:] == 7) and torch.all(a.lse[120:] == 7)
+    a.k_nope[120:], a.v[120:], a.k_pe[120:] = 0, 0, 0
+    a.check(rows=slice(0, 120))
+
+
+@pytest.mark.parametrize("cq,ck,code,owned", [
+    ([0, 30, 20, 60], [0, 30, 60, 90], 0xA01, [(0, 30)]),            # decreasing; then before an earlier one's end
+    ([0, 30, 60, 500], [0, 30, 60, 90], 0xA01, [(0, 60)]),
+    ([-5, 30, 60, 90], [0, 30, 60, 90], 0xA01, [(30, 90)]),
+    ([0, 30, 60, 90], [0, 30, 20, 90], 0xA02, [(0, 30), (60, 90)]),
+    ([0, 30, 60, 90], [0, 30, 60, 1000], 0xA02, [(0, 60)]),
+    ([0, 30, 60, 90], [-1, 30, 60, 90], 0xA02, [(30, 90)]),
+])
+def test_offsets_that_break_the_rules(cq, ck, code, owned):
+    a = Attn(2, [100], [100], False, seed=6)
+    a.cu_q, a.cu_k = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (cq, ck))
+    a.run()
+    assert B.mla_decode_device_error() == code
+    done = torch.zeros(100, dtype=torch.bool, device="cuda")
+    for lo, hi in owned:
+        done[lo:hi] = True
+    assert torch.equal((a.lse != 7).all(1), done) and torch.equal((a.out != 7).any(2).all(1), done)
+    assert torch.equal((a.lse != 7).any(1), done)
+
+
+def test_no_key_at_all():
+    a = Attn(4, [5, 0, 300], [0, 0, 0], False)
+    a.run()
+    assert not a.out.any() and torch.all(a.lse == -float("inf"))
+
+
+def test_scores_of_minus_infinity():
+    a = Attn(1, [3], [200], False, seed=7)
+    a.q_nope[1] = 0
+    a.q_nope[1, :, 0] = 1
+    a.k_nope[..., 0] = -float("inf")
+    a.q_pe[1] = 0
+    a.q_nope[0, :, 0], a.q_nope[2, :, 0] = 0, 0    # 0 times an infinity
+    a.run()
+    assert not a.out[1].any() and torch.all(a.lse[1] == -float("inf"))
+    assert a.out[[0, 2]].isnan().all()
+
+
+def test_large_scores():
+    """Maxima that climb by far more than the running one is allowed to lag."""
+    a = Attn(2, [300], [900], False, seed=8)
+    step = torch.arange(900, device="cuda").float()
+    a.q_nope[:], a.k_nope[:] = 0, 0
+    a.q_nope[..., 0] = 16.0
+    a.k_nope[..., 0] = (step[:, None] * 0.25).to(BF)
+    a.run()
+    a.check()
+    a.k_nope[..., 0] = (step.flip(0)[:, None] * 0.25).to(BF)
+    a.run()
+    a.check()
+    a.k_nope[..., 0] = torch.where(step[:, None] % 130 == 129, 300.0, -200.0).to(BF)
+    a.run()
+    a.check()
+
+
+def test_strides():
+    """Heads before tokens, wide gaps, a single head of many."""
+    a = Attn(3, [70, 200], [70, 333], True, seed=9)
+    want = [x.clone() for x in a.run()]
+    gaps = lambda x, pad: torch.nn.functional.pad(x, (0, pad))[..., :x.shape[2]]  # noqa: E731
+    a.q_nope, a.q_pe, a.k_nope = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (a.q_nope, a.q_pe, a.k_nope))
+    a.v, a.k_pe = gaps(a.v, 24), torch.nn.functional.pad(a.k_pe, (0, 8))[:, :64]
+    a.out = torch.full((3, 270, 136), 7.0, dtype=BF, device="cuda")[..., :128].transpose(0, 1)
+    a.run()
+    assert torch.equal(a.out, want[0]) and torch.equal(a.lse, want[1])
+    for h in range(3):
+        one = Attn(1, [70, 200], [70, 333], True, seed=9)
+        one.q_nope, one.q_pe, one.k_nope, one.v = (x[:, h:h + 1] for x in (a.q_nope, a.q_pe, a.k_nope, a.v))
+        one.k_pe = a.k_pe
+        one.run()
+        assert torch.equal(one.out, want[0][:, h:h + 1]) and torch.equal(one.lse, want[1][:, h:h + 1])
+
+
+def test_workspace_is_asked_for():
+    need = B.mla_prefill_workspace_bytes(100, 50000, 1, 2)
+    assert need > 0
+    a = Attn(2, [100], [50000], False)
+    for ws in (None, a.ws[:need - 256], a.ws[128:]):
+        with pytest.raises(B.MlaError) as e:
+            B.mla_prefill(a.q_nope, a.q_pe, a.k_nope, a.k_pe, a.v, a.cu_q, a.cu_k, False, SCALE, a.out, a.lse, ws)
+        assert e.value.code == B.MLA_ERR_WORKSPACE
+    assert torch.all(a.out == 7)
