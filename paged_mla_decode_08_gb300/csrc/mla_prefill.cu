@@ -911,12 +911,37 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
   int vstep = 0, looks = 0;  // steps, and steps looked through, of the items before
   float top, base;           // the running maximum of S, and of c S (0 while there is none)
   float2 sum[2];
-  // One step.  left: keys of it that this thread's row sees, where some row does not see them
-  // all; before(): what is to be done while the scores are computed.  (A before() that keeps
-  // nothing stands for a step without masks.)
-  auto step = [&](bool fresh, int left, auto before) {
-    constexpr bool kSome = !std::is_empty<decltype(before)>::value;
-    if (!before() || !c.wait_warp(B_S + t, sp, 0xA18)) return false;
+  // The running maximum moves to `here` where that is too far above it; `fresh`: there
+  // is no output yet, which else is rescaled.
+  auto move_to = [&](float here, bool fresh) {
+    const bool up = here > top + slack;
+    const float factor = up ? ex2_approx((top - here) * a.scale_log2) : 1.f;
+    if (up) {
+      top = here;
+      base = here * a.scale_log2;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sum[i] = make_float2(sum[i].x * factor, sum[i].y * factor);
+    if (fresh) return;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      uint32_t o[32];
+      tmem_ld32(to + 32 * q, o);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+      tmem_st32(to + 32 * q, o);
+    }
+  };
+  // The weights stored so far are in TMEM: hand them over.
+  auto hand_over = [&](int half) {
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) arrive_leader(c, B_P + 2 * t + half);
+  };
+  // A step that every row sees whole.
+  auto whole_step = [&](bool fresh) {
+    if (!c.wait_warp(B_S + t, sp, 0xA18)) return false;
     sp ^= 1;
     tc_fence_after();
     constexpr int kHalf = kParts / 2;
@@ -929,15 +954,9 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
 #pragma unroll
       for (int q = 0; q < kHalf; ++q) tmem_ld32_async(ts + 32 * (kHalf + q), u[q]);
 #pragma unroll
-      for (int q = 0; q < kHalf; ++q) {
-        tmem_wait_ld32(s[q]);
-        if (kSome) mask32(s[q], left - 32 * q);
-      }
+      for (int q = 0; q < kHalf; ++q) tmem_wait_ld32(s[q]);
 #pragma unroll
-      for (int q = 0; q < kHalf; ++q) {
-        tmem_wait_ld32(u[q]);
-        if (kSome) mask32(u[q], left - 32 * (kHalf + q));
-      }
+      for (int q = 0; q < kHalf; ++q) tmem_wait_ld32(u[q]);
       here = fmaxf(max32(s[0]), max32(u[0]));
       if (kHalf == 2) here = max3(here, max32(s[kHalf - 1]), max32(u[kHalf - 1]));
     }
@@ -946,51 +965,61 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
 #pragma unroll
       for (int q = 0; q < kHalf; ++q) weights32(s[q], scale, base, p + 16 * q, more);
     }
-    const bool move = here > top + slack;
-    if (fresh || __any_sync(0xffffffffu, move)) {
-      const float factor = move ? ex2_approx((top - here) * a.scale_log2) : 1.f;
-      if (move) {
-        top = here;
-        base = here * a.scale_log2;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) more[i] = sum[i] = make_float2(sum[i].x * factor, sum[i].y * factor);
+    if (fresh || __any_sync(0xffffffffu, here > top + slack)) {
+      move_to(here, fresh);
+      more[0] = sum[0];
+      more[1] = sum[1];
 #pragma unroll
       for (int q = 0; q < kHalf; ++q) weights32(s[q], scale, base, p + 16 * q, more);
-      if (!fresh) {
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t o[32];
-          tmem_ld32(to + 32 * q, o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-          tmem_st32(to + 32 * q, o);
-        }
-      }
     }
 #pragma unroll
     for (int q = 0; q < kHalf; ++q) tmem_st16_async(ts + 16 * q, p + 16 * q);
 #pragma unroll
     for (int q = 0; q < kHalf; ++q) tmem_ld32_async(ts + 32 * (kHalf + q), s[q]);  // (P ends before)
-    if (kCtas > 1) {
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_leader(c, B_P + 2 * t);
-    }
+    if (kCtas > 1) hand_over(0);
 #pragma unroll
     for (int q = 0; q < kHalf; ++q) {
       tmem_wait_ld32(s[q]);
-      if (kSome) mask32(s[q], left - 32 * (kHalf + q));
       weights32(s[q], scale, base, p + 16 * q, more);
       tmem_st16_async(ts + 16 * (kHalf + q), p + 16 * q);
     }
     sum[0] = more[0];
     sum[1] = more[1];
-    tmem_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) arrive_leader(c, B_P + 2 * t + kCtas - 1);
+    hand_over(kCtas - 1);
+    return true;
+  };
+  // A step of which this thread's row sees `left` keys, 32 at a time in loops: it comes a few
+  // times an item, and what it costs is to fetch its instructions (unrolled it took
+  // 3000 to 3500 cycles where a whole step takes 1400).
+  auto edge_step = [&](bool fresh, int left) {
+    if (!c.wait_warp(B_S + t, sp, 0xA18)) return false;
+    sp ^= 1;
+    tc_fence_after();
+    const int most = __shfl_sync(0xffffffffu, left, 31);  // rows see more and more
+    uint32_t s[32];
+    float here = -CUDART_INF_F;
+#pragma unroll 1
+    for (int q = 0; q < kParts && 32 * q < most; ++q) {
+      tmem_ld32(ts + 32 * q, s);
+      mask32(s, left - 32 * q);
+      here = fmaxf(here, max32(s));
+    }
+    if (fresh || __any_sync(0xffffffffu, here > top + slack)) move_to(here, fresh);
+#pragma unroll 1
+    for (int q = 0; q < kParts; ++q) {
+      uint32_t p[16];
+      if (32 * q < most) {
+        tmem_ld32(ts + 32 * q, s);
+        mask32(s, left - 32 * q);
+        weights32(s, scale, base, p, sum);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[i] = 0;
+      }
+      tmem_st16_async(ts + 16 * q, p);  // (over scores that are read)
+      if (kCtas > 1 && q == kParts / 2 - 1) hand_over(0);
+    }
+    hand_over(kCtas - 1);
     return true;
   };
   for (int n = 0; await_item(c, n); ++n) {
@@ -1001,7 +1030,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
     base = 0.f;
     sum[0] = sum[1] = make_float2(0.f, 0.f);
     for (int j = 0; j < whole; ++j)
-      if (!step(j == 0, 0, [] { return true; })) return;
+      if (!whole_step(j == 0)) return;
 
     const Item it = read_item(c, n);
     const int mine_steps = t ? it.tile_steps[1] : it.tile_steps[0], other_steps = t ? it.tile_steps[0] : it.tile_steps[1];
@@ -1026,7 +1055,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
     const int seen = visible(it, a.causal, min(row, it.lq - 1));
     for (int i = whole; i < mine_steps; ++i) {
       const int j = i * stride + shift;
-      if (!step(i == 0, seen - (it.begin + j) * F::kKeys, [&] { return look(j); })) return;
+      if (!look(j) || !edge_step(i == 0, seen - (it.begin + j) * F::kKeys)) return;
     }
     // ---- epilogue
     float total = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y), mine_f = 1.f, other_f = 0.f;
