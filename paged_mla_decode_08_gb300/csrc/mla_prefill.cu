@@ -1072,12 +1072,8 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       release_item(c, n);
       continue;
     }
-    if (mine_steps > 0) {
-      if (!c.wait_warp(B_O + t, op, 0xA19)) return;
-      op ^= 1;
-    }
     if (it.alone) {
-      if (!c.wait_warp(B_STAT, ap, 0xA1C) || !c.wait_warp(B_O + 1, other_op, 0xA1D)) return;
+      if (!c.wait_warp(B_STAT, ap, 0xA1C)) return;
       ap ^= 1;
       float b, l;
       asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(b), "=f"(l) : "r"(stat) : "memory");
@@ -1087,26 +1083,37 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       base = m;
       total = total * mine_f + l * other_f;
     }
-    if (other_steps > 0) other_op ^= 1;
-    tc_fence_after();
     const bool mine = row < it.lq;
     const bool none = total == 0.f;  // no key, or scores of -inf alone
-    const float inv = mine_f / total, other_inv = other_f / total;
-    const bool poison = flag_load(c.sbase + kOffPoison + 4 * (n % kPoisons)) != 0;
+    // a share of no weight may hold anything
+    const uint32_t keep = none || mine_f == 0.f ? 0 : ~0u, keep_other = none || other_f == 0.f ? 0 : ~0u;
+    const float inv = __fdividef(mine_f, total), other_inv = __fdividef(other_f, total);
     const int64_t token = it.q0 + row, part_row = (int64_t)it.part * a.tokens_q + token;
     uint16_t* out = a.out + token * a.out_ts + it.head * a.out_hs;
+    float* part_out = a.part_out + (part_row * a.heads + it.head) * 128;
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+    // The first turn reads and writes nothing: it has the loop's instructions fetched
+    // while the last products run (900 cycles an item).
 #pragma unroll 1
-    for (int q = 0; q < 4; ++q) {
+    for (int q = -1; q < 4; ++q) {
+      if (q == 0 && mine_steps > 0) {
+        if (!c.wait_warp(B_O + t, op, 0xA19) || (it.alone && !c.wait_warp(B_O + 1, other_op, 0xA1D))) return;
+        tc_fence_after();
+      }
       uint32_t r[32];
-      if (mine_steps > 0) tmem_ld32(to + 32 * q, r);
-      float o[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = none || mine_f == 0.f ? 0.f : __uint_as_float(r[i]) * inv;
+      for (int i = 0; i < 32; ++i) r[i] = 0;
+      if (q >= 0 && mine_steps > 0) tmem_ld32(to + 32 * q, r);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i] & keep) * inv);
       if (it.alone) {
-        tmem_ld32(tmem + lanes + TM_O + 128 + 32 * q, r);
+        uint32_t u[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] += none || other_f == 0.f ? 0.f : __uint_as_float(r[i]) * other_inv;
+        for (int i = 0; i < 32; ++i) u[i] = 0;
+        if (q >= 0) tmem_ld32(tmem + lanes + TM_O + 128 + 32 * q, u);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          r[i] = __float_as_uint(fmaf(__uint_as_float(u[i] & keep_other), other_inv, __uint_as_float(r[i])));
         if (q == 3) {
           tc_fence_before();
           __syncwarp();
@@ -1114,27 +1121,34 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
         }
       }
       if (a.parts > 1) {
-        float4* to = reinterpret_cast<float4*>(a.part_out + (part_row * a.heads + it.head) * 128 + 32 * q);
-        if (mine && !none) {
+        if (mine && !none && q >= 0) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 8; ++i)
+            reinterpret_cast<uint4*>(part_out + 32 * q)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
         }
         continue;
       }
       uint32_t p[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) p[i] = pack(o[2 * i], o[2 * i + 1]);
-      if (mine) {
+      for (int i = 0; i < 16; ++i) p[i] = pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+      if (none) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[i] = 0;
+      }
+      if (mine && q >= 0) {
         store32(out + 32 * q, p, wide);
         store32(out + 32 * q + 16, p + 8, wide);
       }
     }
+    if (mine_steps > 0) op ^= 1;
+    if (other_steps > 0) other_op ^= 1;
+    const bool poison = flag_load(c.sbase + kOffPoison + 4 * (n % kPoisons)) != 0;
     float* lse = a.parts > 1 ? a.part_lse + part_row * a.heads : a.lse + token * a.heads;
     if (poison && mine && !none) {
       const uint16_t* v = a.v + it.k0 * a.v_ts + it.head * a.v_hs;
       const int from = (it.begin + it.look) * F::kKeys, to = min(seen, (it.begin + it.steps) * F::kKeys);
       if (a.parts > 1)
-        add_non_finite(v, a.v_ts, from, to, a.part_out + (part_row * a.heads + it.head) * 128);
+        add_non_finite(v, a.v_ts, from, to, part_out);
       else
         add_non_finite(v, a.v_ts, from, to, reinterpret_cast<__nv_bfloat16*>(out));
     }
