@@ -1349,18 +1349,13 @@ static int parts_of(int num_tokens_q, int num_tokens_k, int batch, int num_heads
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(room, most), 32));
 }
 // Pairs of CTAs, or one CTA an item: by the rows and keys of a request, on average.
-// Measured (128 heads; one CTA, pair): 8 requests of 512 rows 183 and 165 us, 16 of 300
-// rows 248 and 268, 16 of 200 rows 114 and 154; with 1000 keys each 8 of 200 rows 161 and
-// 143, 16 of 64 rows 206 and 259 (half of a pair has no row of a request of 128 or fewer).
+// Measured in us (128 heads; one CTA, pair): 8 requests of 512 rows 131 and 138, 16 of 300
+// rows 178 and 208, one of 1024 rows 57 and 57, of 1537 116 and 111, of 2048 163 and 137; with
+// a prefix, 8 of 200 rows and 1000 keys 150 and 145, one of 512 and 2800 112 and 85; 16 of
+// 64 rows and 1000 keys 200 and 262 (half of a pair has no row of 128 or fewer).
 static bool in_pairs(int num_tokens_q, int num_tokens_k, int batch) {
-  const int rows = num_tokens_q / batch, keys = num_tokens_k / batch;
-  return rows > 384 || (rows > kRows && keys / 3 >= rows);
+  return num_tokens_q / batch > kRows && num_tokens_k / batch > 600;
 }
-
-// Keys and values of a group of heads (a request's, on average).  16 and 128 heads of one
-// prompt of 8192: 24 MB 229 and 1494 us, 32 MB 193 and 1460, 48 MB 194 and 1578; one head
-// after the other 237 and 1598.
-constexpr int64_t kGroupBytes = 32 << 20;
 
 template <int kCtas>
 static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t stream) {
