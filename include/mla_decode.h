@@ -630,8 +630,8 @@ int mla_gemm_fp8_form(int num_tokens, int n, int k, int num_experts, int grouped
  *                    pairs that turn more than beta_fast times within the original
  *                    context keep their frequency, those that turn less than
  *                    beta_slow times are stretched.
- * Angles are reduced exactly (to 2^-64 of a turn a position), so far positions
- * lose nothing: the error is that of one fp32 sine, cosine and product.
+ * Angles are reduced in whole numbers, to 2^-31 of a turn, so far positions lose
+ * nothing: the error is about that of one fp32 sine, cosine and product.
  *
  *   table           device fp32 [num_positions, rotary_dim], contiguous.
  *   first_position  >= 0, first_position + num_positions <= 2^31.
@@ -725,18 +725,20 @@ int mla_cache_gather(const void* kv_pages, int kv_dtype, int64_t num_pages, int 
  *                 query row.  Rows that no request owns are not written.
  *   out           device bf16 [num_tokens_q, num_heads, 128].
  *   lse           device fp32 [num_tokens_q, num_heads], contiguous.
- *   scale         softmax scale, finite, > 0 (1/sqrt(192) for DeepSeek-V3 shapes).
+ *   scale         softmax scale, > 0, itself and 16 / scale finite in fp32
+ *                 (1/sqrt(192) for DeepSeek-V3 shapes); scores are held in fp32.
  *   workspace     device scratch of mla_prefill_workspace_bytes (same sizes), 256-byte
  *                 aligned; may be NULL when that is 0.  No initial contents are needed
  *                 and none are kept; calls that overlap on the GPU must not share it.
- * Strides are multiples of 8 elements and at least the width, all pointers 16-byte
- * aligned (offsets and lse 4), num_heads of a one-headed array any stride.
+ * Strides are multiples of 8 elements, at least the width and below 2^39 (the head
+ * stride of a single head is not looked at); pointers are 16-byte aligned (offsets and
+ * lse 4).
  * Products run on the tensor cores with bf16 operands and fp32 accumulation;
  * probabilities enter the second one as bf16, row sums and lse use them unrounded.
  * Masked keys and values may hold anything (NaN, infinities); a value that is not
  * finite reaches the rows that see it and no other.
  * Errors: MLA_ERR_ARG, MLA_ERR_WORKSPACE, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.  A wait
- * that timed out inside the kernel reads 0xA1x.
+ * that timed out inside the kernel reads 0xA1x or 0xA2x.
  */
 int mla_prefill(const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_head_stride, const void* q_pe,
                 int64_t q_pe_token_stride, int64_t q_pe_head_stride, const void* k_nope, int64_t k_nope_token_stride,
@@ -796,7 +798,7 @@ void mla_planner_constants(int* tile_tokens, int* segment_overhead_tiles, int* m
  * that, the first out-of-range lookup of a block-table builder (0x30x) or of
  * the RoPE / cache-write step (0x60x), or a malformed expert offset (0x701) or
  * a timed-out wait (0x71x, 0x72x, 0x73x) of a product, or malformed offsets (0xA0x)
- * or a timed-out wait (0xA1x) of mla_prefill, or an out-of-range lookup of
+ * or a timed-out wait (0xA1x, 0xA2x) of mla_prefill, or an out-of-range lookup of
  * mla_rope (0x801) or mla_cache_gather (0x90x).  Reading it
  * synchronises with the device; reset != 0 clears it.  Errors: MLA_ERR_ARG,
  * MLA_ERR_CUDA. */

@@ -2,8 +2,9 @@
 
 Argument marshalling only: every step of the decode runs in the library's
 CUDA kernels.  (The tensors of the FP8 layer's and the prompt's operators are
-checked and passed on by the native module _mla_calls instead of ctypes.)  Torch tensors are accepted for convenience and are only used
-for their device pointers and the current CUDA stream.  There is no fallback:
+checked and passed on by the native module _mla_calls instead of ctypes.)  Torch
+tensors are accepted for convenience and are only used for their device pointers
+and the current CUDA stream.  There is no fallback:
 if the library is missing, loading fails loudly.
 """
 

@@ -1073,7 +1073,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       continue;
     }
     if (it.alone) {
-      if (!c.wait_warp(B_STAT, ap, 0xA1C)) return;
+      if (!c.wait_warp(B_STAT, ap, 0xA21)) return;
       ap ^= 1;
       float b, l;
       asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(b), "=f"(l) : "r"(stat) : "memory");
@@ -1240,10 +1240,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     if (warp == 0) {
       load_items(c, a, maps, lane);
     } else if (warp == 1) {
-      if (c.rank == 0)
-        issue_products(c, a, tmem);
-      else
-        c.wait_limited(B_FIN, 0);  // the leader's last arrival here
+      if (c.rank == 0) issue_products(c, a, tmem);
     } else if (warp == 3) {
       if (c.rank == 0)
         schedule(c, a, own, lane);
@@ -1257,8 +1254,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (kCtas > 1) cluster_sync();  // every product is read and no arrival is left on its way
+  if (kCtas > 1) cluster_sync();  // every product is read
   tc_fence_after();
+  if (kCtas > 1 && c.rank > 0 && warp == 1) c.wait_limited(B_FIN, 0);  // the leader's last arrival here
+  __syncwarp();
   if (warp == 1) tmem_dealloc_of<kCtas>(tmem);
   if (kCtas > 1) cluster_sync();
 }
@@ -1297,7 +1296,8 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float f = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
-      if (k0 + k >= a.parts || f == 0.f) continue;  // (it may not have been written)
+      const float l = __shfl_sync(0xffffffffu, mine, (k0 + k) & 31);
+      if (l == -CUDART_INF_F) continue;  // it has not been written
       o.x += f * v[k].x;
       o.y += f * v[k].y;
       o.z += f * v[k].z;

@@ -44,7 +44,7 @@ constexpr int kThreads = 256;
 // cos and sin of position * frequency.  A position's angle is a whole number times
 // a fixed fraction of a turn, and whole turns do not matter: the fraction is held
 // in 64 bits and the product taken modulo 2^64, so the reduction costs two integer
-// products and is exact to 2^-33 of a turn, however far (double precision, at this
+// products and is good to 2^-31 of a turn, however far (double precision, at this
 // GPU's rate, would be what bounds the kernel).  The nearest quarter turn goes, and the
 // rest, at most pi / 4, through the Taylor polynomials of degree 9 and 10 (their next
 // terms are below 2e-9 there); the sum is off by about one unit of 2^-24.
@@ -324,8 +324,14 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const GatherArgs
   {
     const int row = (int)row0 + min(lane, kGatherRows - 1);
     int b = owner(a, (int)row0, lane);
+    if (b < a.batch && __ldg(a.cu + b + 1) < row0 + kGatherRows) {  // the rows are not all of one request
+#pragma unroll 1
+      for (int i = 1; i < kGatherRows; ++i) {
+        const int other = owner(a, (int)row0 + i, lane);
+        if (lane >= i) b = other;
+      }
+    }
     if (lane < kGatherRows && row < a.tokens) {
-      while (b < a.batch && __ldg(a.cu + b + 1) <= row) ++b;
       if (b < a.batch) {
         const int begin = __ldg(a.cu + b);
         const int64_t token = (a.starts ? (int64_t)__ldg(a.starts + b) : 0) + row - begin;
@@ -434,6 +440,7 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const MergeArgs m) {
     const uint4 xb = *reinterpret_cast<const uint4*>(m.b + t * m.b_ts + h * m.b_hs + 8 * chunk);
     const float la = m.lse_a[row], lb = m.lse_b[row];
     const float top = fmaxf(la, lb), base = top == -CUDART_INF_F ? 0.f : top;
+    const bool no_a = la == -CUDART_INF_F, no_b = lb == -CUDART_INF_F;
     float wa = __expf(la - base), wb = __expf(lb - base);
     const float sum = wa + wb;
     lse = sum == 0.f ? -CUDART_INF_F : base + logf(sum);
@@ -444,9 +451,9 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const MergeArgs m) {
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // a part that weighs nothing may hold anything
-      const float a0 = wa == 0.f ? 0.f : wa * bf_lo(ua[i]), a1 = wa == 0.f ? 0.f : wa * bf_hi(ua[i]);
-      const float b0 = wb == 0.f ? 0.f : wb * bf_lo(ub[i]), b1 = wb == 0.f ? 0.f : wb * bf_hi(ub[i]);
+      // a part without a key may hold anything
+      const float a0 = no_a ? 0.f : wa * bf_lo(ua[i]), a1 = no_a ? 0.f : wa * bf_hi(ua[i]);
+      const float b0 = no_b ? 0.f : wb * bf_lo(ub[i]), b1 = no_b ? 0.f : wb * bf_hi(ub[i]);
       o[i] = bf16x2(a0 + b0, a1 + b1);
     }
     *reinterpret_cast<uint4*>(m.out + t * m.o_ts + h * m.o_hs + 8 * chunk) = make_uint4(o[0], o[1], o[2], o[3]);

@@ -1,7 +1,7 @@
-// The way in from Python of the FP8 layer's and the prompt's operators: checks torch tensors and calls the
-// C ABI.  A small call's kernel takes two microseconds; the same checks made in
-// Python (shapes, types, strides and pointers of up to seven tensors, then
-// ctypes) took seven, this module about one.  No arithmetic happens here.
+// The way in from Python of the FP8 layer's and the prompt's operators: checks torch
+// tensors and calls the C ABI.  A small call's kernel takes two microseconds; the same
+// checks made in Python (shapes, types, strides and pointers of up to seven tensors,
+// then ctypes) took seven, this module about one.  No arithmetic happens here.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
