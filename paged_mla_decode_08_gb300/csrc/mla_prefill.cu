@@ -132,7 +132,7 @@ struct Args {
   float* lse;
   int64_t v_ts, v_hs, out_ts, out_hs;  // strides of a token and a head, in elements
   int32_t batch, heads, tokens_q, tokens_k;
-  int32_t tiles;   // row blocks of a head: at most this many exist
+  int32_t tiles;   // row blocks: at most this many exist
   int32_t parts;   // items of a row block: each has a part of the keys
   int32_t group;   // heads whose items are mixed
   float* part_out; // [part][token][head][128], [part][token][head]: what a part alone gives
@@ -196,54 +196,80 @@ __device__ __forceinline__ int first_row(const Item& it, int t, int rank) {
   return it.row0 + (it.alone ? 0 : t * Form<kCtas>::kTileRows) + rank * kRows;
 }
 
-// Item `idx` of a head: requests own ceil(rows / kItemRows) items each, those with the
-// most keys first.  Found by a warp over the offsets; false: there is no such item.
-// A request whose offsets break the rules, by themselves or by beginning before an
-// earlier one's end, owns none.
+// Row blocks: requests own ceil(rows / kItemRows) each, in their order; a request's
+// come with the most keys first.  A request whose offsets break the rules, by
+// themselves or by beginning before an earlier one's end, owns none.  Found by a warp
+// that walks over the offsets, 32 requests at a time.
+struct Walk {
+  int base = 0;    // the next 32 requests
+  int blocks = 0;  // row blocks of those before
+  int end = 0;     // ... and the latest end of their rows
+};
+// A lane's request of the next 32, and how many row blocks there are up to it.
+struct Request {
+  int q0, q1, k0, k1, upto;
+  bool bad_q, bad_k;
+};
 template <int kItemRows>
-__device__ bool find_item(const Args& a, int idx, int lane, Item* it) {
-  int items = 0, end = 0;  // of the requests so far
-  bool bad_q = false, bad_k = false, found = false;
-  for (int base = 0; base < a.batch; base += 32) {
-    const int b = base + lane;
-    int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-    if (b < a.batch) {
-      q0 = __ldg(a.cu_q + b);
-      q1 = __ldg(a.cu_q + b + 1);
-      k0 = __ldg(a.cu_k + b);
-      k1 = __ldg(a.cu_k + b + 1);
-    }
-    int before = q1;  // the latest end of the requests before this one
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) before = max(before, __shfl_up_sync(0xffffffffu, before, d) * (lane >= d));
-    const int last = max(end, __shfl_sync(0xffffffffu, before, 31));
-    before = __shfl_up_sync(0xffffffffu, before, 1);
-    before = max(end, lane ? before : 0);
-    end = last;
-    const bool ok_q = q0 >= before && q0 <= q1 && q1 <= a.tokens_q, ok_k = k0 >= 0 && k0 <= k1 && k1 <= a.tokens_k;
-    if (b < a.batch) {
-      bad_q |= !ok_q;
-      bad_k |= !ok_k;
-    }
-    int upto = ok_q && ok_k ? (q1 - q0 + kItemRows - 1) / kItemRows : 0;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) upto += __shfl_up_sync(0xffffffffu, upto, d) * (lane >= d);
-    upto += items;
-    const unsigned hit = __ballot_sync(0xffffffffu, upto > idx);
-    if (hit && !found) {
-      found = true;
-      const int src = __ffs(hit) - 1;
-      it->q0 = __shfl_sync(0xffffffffu, q0, src);
-      it->lq = __shfl_sync(0xffffffffu, q1, src) - it->q0;
-      it->k0 = __shfl_sync(0xffffffffu, k0, src);
-      it->lk = __shfl_sync(0xffffffffu, k1, src) - it->k0;
-      it->row0 = (__shfl_sync(0xffffffffu, upto, src) - 1 - idx) * kItemRows;
-    }
-    items = __shfl_sync(0xffffffffu, upto, 31);
-    if (found && idx != 0) break;  // the first item's finder looks at every request
+__device__ __forceinline__ Request walk_on(const Args& a, Walk& w, int lane) {
+  Request r{};
+  const int b = w.base + lane;
+  if (b < a.batch) {
+    r.q0 = __ldg(a.cu_q + b);
+    r.q1 = __ldg(a.cu_q + b + 1);
+    r.k0 = __ldg(a.cu_k + b);
+    r.k1 = __ldg(a.cu_k + b + 1);
   }
-  if (idx == 0 && (bad_q || bad_k)) atomicCAS(&g_prefill_error, 0, bad_q ? 0xA01 : 0xA02);
-  return found;
+  int before = r.q1;  // the latest end of the requests before this one
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) before = max(before, __shfl_up_sync(0xffffffffu, before, d) * (lane >= d));
+  const int last = max(w.end, __shfl_sync(0xffffffffu, before, 31));
+  before = __shfl_up_sync(0xffffffffu, before, 1);
+  before = max(w.end, lane ? before : 0);
+  const bool ok_q = r.q0 >= before && r.q0 <= r.q1 && r.q1 <= a.tokens_q, ok_k = r.k0 >= 0 && r.k0 <= r.k1 && r.k1 <= a.tokens_k;
+  r.bad_q = b < a.batch && !ok_q;
+  r.bad_k = b < a.batch && !ok_k;
+  r.upto = b < a.batch && ok_q && ok_k ? (r.q1 - r.q0 + kItemRows - 1) / kItemRows : 0;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) r.upto += __shfl_up_sync(0xffffffffu, r.upto, d) * (lane >= d);
+  r.upto += w.blocks;
+  w = Walk{w.base + 32, __shfl_sync(0xffffffffu, r.upto, 31), last};
+  return r;
+}
+// All of them; `report`: offsets that break the rules go to the error word.
+template <int kItemRows>
+__device__ __forceinline__ int count_blocks(const Args& a, int lane, bool report) {
+  Walk w;
+  bool bad_q = false, bad_k = false;
+  while (w.base < a.batch) {
+    const Request r = walk_on<kItemRows>(a, w, lane);
+    bad_q |= r.bad_q;
+    bad_k |= r.bad_k;
+  }
+  if (report && (bad_q || bad_k)) atomicCAS(&g_prefill_error, 0, bad_q ? 0xA01 : 0xA02);
+  return w.blocks;
+}
+// Number `idx`; false: there is none.  The walk goes on from where the last one ended,
+// if that is not too far.
+template <int kItemRows>
+__device__ __forceinline__ bool find_block(const Args& a, int idx, Walk& from, int lane, Item* it) {
+  Walk w;
+  if (from.blocks <= idx) w = from;
+  while (w.base < a.batch) {
+    from = w;
+    const Request r = walk_on<kItemRows>(a, w, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, r.upto > idx);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      it->q0 = __shfl_sync(0xffffffffu, r.q0, src);
+      it->lq = __shfl_sync(0xffffffffu, r.q1, src) - it->q0;
+      it->k0 = __shfl_sync(0xffffffffu, r.k0, src);
+      it->lk = __shfl_sync(0xffffffffu, r.k1, src) - it->k0;
+      it->row0 = (__shfl_sync(0xffffffffu, r.upto, src) - 1 - idx) * kItemRows;
+      return true;
+    }
+  }
+  return false;
 }
 
 __device__ __forceinline__ uint32_t flag_load(uint32_t addr) {
@@ -333,48 +359,64 @@ __device__ __forceinline__ int read_answer(uint32_t answer) {
   return got ? (int)x : -1;
 }
 
-// The item that the CTA of this number starts with, for a converged warp.  Items come
-// a row block at a time, a request's last and longest first, for a group of heads whose
-// keys and values stay in L2; then the next group's.
+// What there is to do, and where a cluster stands: item `index`, then every
+// `clusters`-th after it, then those of the cluster that the hardware gives.
+struct Work {
+  int blocks;    // row blocks
+  int items;     // ... of all heads and parts
+  int clusters;  // of the grid
+  int index;     // -1: nothing is left
+  Walk walk;
+};
 template <int kCtas>
-__device__ __forceinline__ Item item_of(const Args& a, int cta, int lane) {
+__device__ __forceinline__ Work work_of(const Args& a, int blocks) {
+  return Work{blocks, blocks * a.heads * a.parts, (int)gridDim.x / kCtas, (int)blockIdx.x / kCtas, Walk()};
+}
+// Item `index`, for a converged warp.  Items come a row block at a time, a request's last
+// and longest first, for a group of heads whose keys and values stay in L2; then
+// the next group's.
+template <int kCtas>
+__device__ __forceinline__ Item item_of(const Args& a, Work& w, int lane) {
   Item it;
-  const int index = cta / kCtas, group = index / (a.group * a.tiles * a.parts);
-  const int rest = index - group * (a.group * a.tiles * a.parts);
-  const int of_tile = min(a.group, a.heads - group * a.group) * a.parts;  // items of a row block, of the group's heads
-  const int tile = rest / of_tile, within = rest - tile * of_tile;
+  const int of_group = a.group * w.blocks * a.parts, group = w.index / of_group, rest = w.index - group * of_group;
+  const int of_block = min(a.group, a.heads - group * a.group) * a.parts;  // items of a row block, of the group's heads
+  const int block = rest / of_block, within = rest - block * of_block;
   it.head = group * a.group + within / a.parts;
   it.part = within % a.parts;
-  it.more = find_item<Form<kCtas>::kItemRows>(a, tile, lane, &it);
+  it.more = find_block<Form<kCtas>::kItemRows>(a, block, w.walk, lane, &it);
   if (it.more) plan_item<kCtas>(&it, a);
   return it;
 }
 
 // Run by a warp of the leader: finds items and hands them to both CTAs.
 template <int kCtas>
-__device__ void schedule(const Ctx<kCtas>& c, const Args& a, Item it, int lane) {
+__device__ void schedule(const Ctx<kCtas>& c, const Args& a, Work w, Item it, int lane) {
   const uint32_t peer_items = kCtas > 1 ? mapa(c.sbase + kOffItem, 1) : 0;
   const uint32_t peer_bars = kCtas > 1 ? mapa(c.bar(B_ITEM), 1) : 0;
-  int cta = (int)blockIdx.x, asked = 0;  // it: this CTA's own item, if there is one
-  auto answered = [&] {
+  int asked = 0;
+  // The next index; false: a wait gave up.
+  auto ask = [&] {
+    if (lane == 0) ask_for_cluster(c.sbase + kOffAnswer, c.bar(B_ASKED));
+    __syncwarp();
     const uint32_t parity = asked++ & 1;
-    if (c.wait_warp(B_ASKED, parity, 0xA1A)) return true;
-    c.wait_limited(B_ASKED, parity);  // it comes in a microsecond or so, whatever else went wrong
-    return false;
+    if (!c.wait_warp(B_ASKED, parity, 0xA1A)) {
+      c.wait_limited(B_ASKED, parity);  // it comes in a microsecond or so, whatever else went wrong
+      return false;
+    }
+    const int cta = read_answer(c.sbase + kOffAnswer);
+    w.index = cta < 0 ? -1 : cta / kCtas;
+    return true;
   };
   for (int n = 0;; ++n) {
-    for (bool known = n == 0; cta >= 0; known = false) {
-      if (!known) it = item_of<kCtas>(a, cta, lane);
-      if (it.more) break;
-      // fewer items than there could have been: on to the next one
-      if (lane == 0) {
-        ask_for_cluster(c.sbase + kOffAnswer, c.bar(B_ASKED));
-      }
-      __syncwarp();
-      if (!answered()) return;
-      cta = read_answer(c.sbase + kOffAnswer);
+    bool known = n == 0;  // the first item, if there is one
+    while (w.index >= w.items) {  // fewer items than clusters: on to the next one
+      if (!ask()) return;
+      known = false;
     }
-    if (cta < 0) it.more = 0;
+    if (w.index < 0)
+      it.more = 0;
+    else if (!known)
+      it = item_of<kCtas>(a, w, lane);
     const int slot = n % kItemSlots;
     if (n >= kItemSlots && !c.wait_warp(B_TAKEN + slot, (n / kItemSlots + 1) & 1, 0xA1B)) return;
     if (lane == 0) {
@@ -393,12 +435,10 @@ __device__ void schedule(const Ctx<kCtas>& c, const Args& a, Item it, int lane) 
     __syncwarp();
     if (!it.more) return;
     if (!c.wait_warp(B_NEXT, n & 1, 0xA1C)) return;
-    if (lane == 0) {
-      ask_for_cluster(c.sbase + kOffAnswer, c.bar(B_ASKED));
-    }
-    __syncwarp();
-    if (!answered()) return;
-    cta = read_answer(c.sbase + kOffAnswer);
+    if (w.index < w.items - w.clusters)
+      w.index += w.clusters;
+    else if (!ask())
+      return;
   }
 }
 // ... and by one of its peer, whose slots the leader fills.
@@ -1184,10 +1224,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   c.rank = kCtas > 1 ? (int)cluster_ctarank() : 0;
   c.leader = kCtas > 1 ? mapa(c.sbase, 0) : c.sbase;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  int blocks = 0;
   Item own;
   if (warp == 3 && c.rank == 0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    own = item_of<kCtas>(a, (int)blockIdx.x, lane);
+    blocks = count_blocks<Form<kCtas>::kItemRows>(a, lane, blockIdx.x == 0);
+    Work work = work_of<kCtas>(a, blocks);
+    if (work.index < work.items) own = item_of<kCtas>(a, work, lane);
   } else if (warp == 0) {
     if (lane == 0) {
       flag_store(c.sbase + kOffAbort, 0);
@@ -1243,7 +1286,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (c.rank == 0) issue_products(c, a, tmem);
     } else if (warp == 3) {
       if (c.rank == 0)
-        schedule(c, a, own, lane);
+        schedule(c, a, work_of<kCtas>(a, blocks), own, lane);
       else
         receive(c, lane);
     }
@@ -1273,7 +1316,8 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args
   const int head = (int)blockIdx.x / a.tiles;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Item it;
-  if (!find_item<kItemRows>(a, (int)blockIdx.x - head * a.tiles, lane, &it)) return;
+  Walk walk;
+  if (!find_block<kItemRows>(a, (int)blockIdx.x - head * a.tiles, walk, lane, &it)) return;
   const int row = it.row0 + (int)blockIdx.y * kMergeRows + warp;
   if (row >= it.lq) return;
   const int64_t token = it.q0 + row, at = token * a.heads + head, stride = (int64_t)a.tokens_q * a.heads;
@@ -1362,6 +1406,15 @@ static bool in_pairs(int num_tokens_q, int num_tokens_k, int batch) {
 // after the other 237 and 1598.
 constexpr int64_t kGroupBytes = 32 << 20;
 
+// Clusters: one for each item that there can be, and no more than twice those that there
+// are if the rows are few requests'.  (A batch padded with empty requests would
+// else start many for nothing.)  With more items than clusters each takes several.
+template <int kCtas>
+static int64_t clusters_of(const PrefillCall& p, const Args& a, int sms) {
+  const int64_t full = ((int64_t)p.num_tokens_q + Form<kCtas>::kItemRows - 1) / Form<kCtas>::kItemRows * a.heads * a.parts;
+  return std::min<int64_t>((int64_t)a.tiles * a.heads * a.parts, std::max<int64_t>(2 * full, 2 * sms / kCtas));
+}
+
 template <int kCtas>
 static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t stream) {
   using F = Form<kCtas>;
@@ -1387,7 +1440,7 @@ static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t
   a.part_out = static_cast<float*>(p.workspace);
   a.part_lse = a.part_out + (int64_t)a.parts * p.num_tokens_q * p.num_heads * 128;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.tiles * a.heads * a.parts * kCtas));
+  cfg.gridDim = dim3((unsigned)(clusters_of<kCtas>(p, a, dev.sms) * kCtas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;

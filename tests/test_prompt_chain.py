@@ -293,3 +293,66 @@ def test_a_cache_past_32_bits():
     rows, pe = new(128, 512), new(128, 64)
     B.mla_cache_gather(kv, B.MLA_KV_BF16, bt, None, cu([128]), 1.0, rows, B.MLA_OUT_BF16, None, pe)
     assert torch.equal(rows, kv[-1, :, :512].repeat(2, 1)) and torch.equal(pe, kv[-1, :, 512:].repeat(2, 1))
+
+
+def lens_of(batch, active, seed, most):
+    g = np.random.default_rng(seed)
+    lens = np.zeros(batch, dtype=int)
+    lens[g.choice(batch, active, replace=False)] = g.integers(1, most + 1, active)
+    return lens
+
+
+@pytest.mark.parametrize("batch, active, most, h", [(500, 3, 700, 16), (300, 290, 5, 16), (129, 40, 300, 24), (4097, 2, 9, 2)])
+def test_batches_padded_with_empty_requests(batch, active, most, h):
+    """Every row of every request, wherever it lies among empty ones, whether clusters
+    find one item, several or none."""
+    lens = lens_of(batch, active, 1, most)
+    extra = np.random.default_rng(2).integers(0, 200, batch) * (lens > 0)  # keys ahead of the new ones
+    t, tk = int(lens.sum()), int((lens + extra).sum())
+    q, kv, k_pe = randn(t + 3, h, 192, seed=1), randn(tk, h, 256, seed=2), randn(tk, 64, seed=3)
+    out, lse = torch.full((t + 3, h, 128), 7, dtype=BF, device="cuda"), torch.full((t + 3, h), 7.0, device="cuda")
+    prefill(q[..., :128], q[..., 128:], kv[..., :128], k_pe, kv[..., 128:], cu(lens), cu(lens + extra), True, out, lse)
+    k = torch.cat([kv[..., :128], k_pe[:, None].expand(-1, h, -1)], -1).double()
+    q0 = k0 = 0
+    for n, m in zip(lens, lens + extra):
+        if n:
+            s = SCALE * torch.einsum("qhd,khd->hqk", q[q0:q0 + n].double(), k[k0:k0 + m])
+            s.masked_fill_(torch.arange(m, device="cuda") > torch.arange(m - n, m, device="cuda")[:, None], -float("inf"))
+            w, v = torch.softmax(s, -1), kv[k0:k0 + m, :, 128:].double()
+            want, mass = torch.einsum("hqk,khd->qhd", w, v), torch.einsum("hqk,khd->qhd", w, v.abs())
+            assert torch.all((out[q0:q0 + n].double() - want).abs() <= 2.0 ** -7 * mass + 2.0 ** -8 * want.abs())
+            assert torch.all((lse[q0:q0 + n].double() - torch.logsumexp(s, -1).T).abs() <= 1e-4)
+        q0, k0 = q0 + n, k0 + m
+    assert torch.all(out[t:] == 7) and torch.all(lse[t:] == 7)
+
+
+def test_gather_among_empty_requests():
+    lens = lens_of(500, 30, 4, 3)
+    t = int(lens.sum())
+    kv = randn(70, 64, 576, seed=1)
+    bt = torch.randint(0, 70, (500, 2), generator=torch.Generator().manual_seed(1), dtype=torch.int32).cuda()
+    starts = torch.randint(0, 120, (500,), generator=torch.Generator().manual_seed(2), dtype=torch.int32).cuda()
+    rows, pe = torch.full((t + 5, 512), 7, dtype=BF, device="cuda"), torch.full((t + 5, 64), 7, dtype=BF, device="cuda")
+    B.mla_cache_gather(kv, B.MLA_KV_BF16, bt, starts, cu(lens), 1.0, rows, B.MLA_OUT_BF16, None, pe)
+    owner = torch.repeat_interleave(torch.arange(500), torch.tensor(lens)).cuda()
+    token = starts[owner] + torch.tensor(np.concatenate([np.arange(n) for n in lens])).cuda()
+    want = kv[bt[owner, token // 64].long(), token % 64]
+    assert torch.equal(rows[:t], want[:, :512]) and torch.equal(pe[:t], want[:, 512:])
+    assert torch.all(rows[t:] == 7) and torch.all(pe[t:] == 7)
+
+
+def test_an_infinity_in_a_part_of_little_weight():
+    """Its part weighs less than fp32 holds, but something: the row does not look finite."""
+    a, b = torch.ones(1, 1, 8, dtype=BF, device="cuda"), torch.ones(1, 1, 8, dtype=BF, device="cuda")
+    b[0, 0, 3] = float("inf")
+    la, lb, out, lse = (torch.full((1, 1), x, device="cuda") for x in (0.0, -200.0, 0.0, 0.0))
+    B.mla_merge_states(a, la, b, lb, out := new(1, 1, 8), lse)
+    assert torch.isfinite(out).flatten().tolist() == [True] * 3 + [False] + [True] * 4 and float(lse) == 0.0
+    # within one call, whose keys are cut into parts
+    n = 20000
+    q, k, k_pe, v = new(1, 1, 192).fill_(1), new(n, 1, 128).fill_(-8), new(n, 64).fill_(0), new(n, 1, 128).fill_(1)
+    k[0] = 8
+    v[n - 1, 0, 5] = float("inf")
+    out, lse = new(1, 1, 128), torch.empty(1, 1, device="cuda")
+    prefill(q[..., :128], q[..., 128:], k, k_pe, v, cu([1]), cu([n]), False, out, lse)
+    assert not torch.isfinite(out[0, 0, 5]) and torch.all(out[0, 0, :5] == 1) and torch.all(out[0, 0, 6:] == 1)
