@@ -16,14 +16,26 @@
 // tile's products.  The running maximum only moves when a score exceeds it by
 // 2^8 (P stays below 256, which bf16 and the fp32 sums hold); then that warp
 // rescales its rows of O, which no product uses at that time: the products of a
-// tile run in order, so S(j) in TMEM means that P V (j - 1) is done.
+// tile run in order, so S(j) in TMEM means that P V (j - 1) is done.  An item whose rows
+// fill one tile or less has them in both, each with every second step ("alone"); the
+// epilogue joins the two sums.
 //
 // Why pairs.  Q takes 96 KB of a CTA's shared memory.  One CTA reads 80 KB of keys
 // and values a 128 keys, twice what the rest of its memory can hold ahead, and its
 // products read 128 bytes of shared memory a cycle, all there is.  A pair's CTAs hold
 // half of the keys and half of the value columns each: half the loads, half the reads
-// of B, and three steps ahead.  19 heads, 2048 rows over 8192 keys: 125 us, 1628
-// TFLOP/s (one CTA per 256 rows: 220 us).
+// of B, and three steps ahead.  19 heads, 2048 rows over 8192 keys: 108 us, 1880
+// TFLOP/s (one CTA per 256 rows: 220 us).  One CTA an item has finer steps, rows and
+// keys, for short requests.
+//
+// What bounds it.  Long prompts: the tensor core.  8192 tokens of 128 heads, causal: 1460
+// to 1580 us (the products' floor at a library's burst rate is 1460), 1650 us in a
+// loop of seconds under the power cap (98% of a library product's rate there).  Few rows
+// over many keys: the bytes of keys and values; 8 requests of a row over 1000 to 4500 keys,
+// 128 heads: 258 us, 5.6 TB/s.  Between them, what an item takes beside its steps: the
+// first scores, the last weights' products and the epilogue come one after the other
+// (a request of 130 tokens, 16 heads: 10 us with the launch, of which the data's
+// floor is 0.4).
 //
 // P enters the second product in bf16 (half a step: 2^-8 of each weight at most, of
 // random sign, below the rounding of the bf16 output); row sums and lse use the
@@ -1385,11 +1397,14 @@ static int items_of_a_head(int num_tokens_q, int batch, int item_rows) {
   return num_tokens_q / item_rows + (batch < num_tokens_q ? batch : num_tokens_q);
 }
 
-// Parts of the keys: enough to give every CTA an item, of 512 keys or more.
+// Parts of the keys: enough to give every CTA an item, of 256 keys or more.  In us, not
+// cut, of 1024, 512 and 256 keys at least: a row over 2000 keys, 16 heads, 26.6, 26.6, 17.8,
+// 16.9; over 16000 165, 36, 36, 36; 16 rows over 2000 keys, 4 heads, 26.4, 26.4, 16.7, 14.1;
+// 300 rows over 20000 keys, 19 heads, 228, 79, 79, 78.
 template <int kCtas>
 static int parts_of(int num_tokens_q, int num_tokens_k, int batch, int num_heads, int sms) {
   const int64_t items = (int64_t)items_of_a_head(num_tokens_q, batch, Form<kCtas>::kItemRows) * num_heads;
-  const int64_t room = sms / kCtas / std::max<int64_t>(1, items), most = num_tokens_k / batch / 512;
+  const int64_t room = sms / kCtas / std::max<int64_t>(1, items), most = num_tokens_k / batch / 256;
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(room, most), 32));
 }
 // Pairs of CTAs, or one CTA an item: by the rows and keys of a request, on average.
@@ -1406,13 +1421,15 @@ static bool in_pairs(int num_tokens_q, int num_tokens_k, int batch) {
 // after the other 237 and 1598.
 constexpr int64_t kGroupBytes = 32 << 20;
 
-// Clusters: one for each item that there can be, and no more than twice those that there
-// are if the rows are few requests'.  (A batch padded with empty requests would
-// else start many for nothing.)  With more items than clusters each takes several.
+// Clusters: one for each item that there can be, but no more than twice those of rows that
+// are all one request's, or eight an SM.  With more items than clusters each takes several.
+// (A batch padded with empty requests would else start many for nothing: 2048 rows of 4
+// requests among 512, 128 heads, took 2166 us, now 83, as a batch of 4 takes 79.  Two an
+// SM left 4 requests of 64 rows over 1000 to 4000 keys at 149 us, eight 138.)
 template <int kCtas>
 static int64_t clusters_of(const PrefillCall& p, const Args& a, int sms) {
   const int64_t full = ((int64_t)p.num_tokens_q + Form<kCtas>::kItemRows - 1) / Form<kCtas>::kItemRows * a.heads * a.parts;
-  return std::min<int64_t>((int64_t)a.tiles * a.heads * a.parts, std::max<int64_t>(2 * full, 2 * sms / kCtas));
+  return std::min<int64_t>((int64_t)a.tiles * a.heads * a.parts, std::max<int64_t>(2 * full, 8 * sms / kCtas));
 }
 
 template <int kCtas>
