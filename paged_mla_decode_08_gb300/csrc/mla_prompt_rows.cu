@@ -426,7 +426,9 @@ struct MergeArgs {
 };
 
 // A thread merges 8 columns of a row; a block owns whole rows, whose old lse every
-// thread reads before the new one is written (they may be the same array).
+// thread reads before the new one is written (they may be the same array).  Bound by
+// its bytes: 8192 rows of 128 heads and 128 columns, 818 MB, 129 us (95% of a
+// measured copy's rate).
 __global__ void __launch_bounds__(kThreads) merge_kernel(const MergeArgs m) {
   grid_dependency();
   const int sub = threadIdx.x / m.chunks, chunk = threadIdx.x - sub * m.chunks;
@@ -440,7 +442,9 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const MergeArgs m) {
     const uint4 xb = *reinterpret_cast<const uint4*>(m.b + t * m.b_ts + h * m.b_hs + 8 * chunk);
     const float la = m.lse_a[row], lb = m.lse_b[row];
     const float top = fmaxf(la, lb), base = top == -CUDART_INF_F ? 0.f : top;
-    const bool no_a = la == -CUDART_INF_F, no_b = lb == -CUDART_INF_F;
+    // a part without a key may hold anything (its bits are cleared: a branch would put its
+    // load behind that of its lse, 142 us for 129)
+    const uint32_t keep_a = la == -CUDART_INF_F ? 0u : ~0u, keep_b = lb == -CUDART_INF_F ? 0u : ~0u;
     float wa = __expf(la - base), wb = __expf(lb - base);
     const float sum = wa + wb;
     lse = sum == 0.f ? -CUDART_INF_F : base + logf(sum);
@@ -451,10 +455,8 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const MergeArgs m) {
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // a part without a key may hold anything
-      const float a0 = no_a ? 0.f : wa * bf_lo(ua[i]), a1 = no_a ? 0.f : wa * bf_hi(ua[i]);
-      const float b0 = no_b ? 0.f : wb * bf_lo(ub[i]), b1 = no_b ? 0.f : wb * bf_hi(ub[i]);
-      o[i] = bf16x2(a0 + b0, a1 + b1);
+      const uint32_t x = ua[i] & keep_a, y = ub[i] & keep_b;
+      o[i] = bf16x2(wa * bf_lo(x) + wb * bf_lo(y), wa * bf_hi(x) + wb * bf_hi(y));
     }
     *reinterpret_cast<uint4*>(m.out + t * m.o_ts + h * m.o_hs + 8 * chunk) = make_uint4(o[0], o[1], o[2], o[3]);
   }
