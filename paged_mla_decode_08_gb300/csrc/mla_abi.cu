@@ -52,7 +52,7 @@ void gemm_fp8_form(bool grouped, int m, int n, int k, int experts, const void* o
                    const int32_t* clusters, int* tile_tokens, int* k_parts, int* copied);
 cudaError_t gemm_read_error(int* code, bool reset);
 cudaError_t launch_rope_table(float* table, int64_t first, int64_t positions, int half, const uint64_t* turns,
-                              float magnitude, cudaStream_t stream);
+                              float magnitude, Device dev, cudaStream_t stream);
 cudaError_t launch_rope(HeadRows q, HeadRows k, HeadRows q_out, HeadRows k_out, const int64_t* positions,
                         const float* table, int64_t max_position, int tokens, int heads, int half, bool neox,
                         cudaStream_t stream);
@@ -752,7 +752,8 @@ int mla_rope_table(float* table, int64_t first_position, int64_t num_positions, 
   if (num_positions * half > (int64_t)INT32_MAX * 256) return fail(MLA_ERR_ARG, "too many positions for one launch");
   if (num_positions == 0) return ok();
   if (!table || !aligned(table, 4)) return fail(MLA_ERR_ARG, "table must be a device pointer aligned to its elements");
-  int rc = check_device(nullptr);
+  mla::Device dev{};
+  int rc = check_device(&dev.sms, &dev.id);
   if (rc != MLA_OK) return rc;
   const double two_pi = 6.283185307179586476925;
   double lo = 0.0, hi = 0.0;
@@ -775,7 +776,7 @@ int mla_rope_table(float* table, int64_t first_position, int64_t num_positions, 
     const double t = w / two_pi;  // turns of a position; whole ones do not matter
     turns[i] = static_cast<uint64_t>(std::ldexp(t - std::floor(t), 64));
   }
-  cudaError_t e = mla::launch_rope_table(table, first_position, num_positions, half, turns, (float)magnitude,
+  cudaError_t e = mla::launch_rope_table(table, first_position, num_positions, half, turns, (float)magnitude, dev,
                                          static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("rope table launch: ") + cudaGetErrorString(e));
   return ok();

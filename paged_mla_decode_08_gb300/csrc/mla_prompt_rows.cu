@@ -70,10 +70,10 @@ __device__ __forceinline__ void cos_sin(uint32_t turn, float magnitude, float* c
   *s = __uint_as_float(__float_as_uint(s0) ^ ((quarter & 2) << 30)) * magnitude;
 }
 
-constexpr int kTableRows = 4;  // of a thread
-
-// kWide: four pairs a thread and row (half % 4 == 0, 16-byte rows); else one
-template <bool kWide>
+// kWide: four pairs a thread and row (half % 4 == 0, 16-byte rows); else one.  kRows: rows
+// of a thread, four where that fills the GPU (163840 positions: 1 row 12.5 us, 4 rows 7.3;
+// 4096: 3.7 and 3.9).
+template <bool kWide, int kRows>
 __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_constant__ TableArgs a) {
   grid_dependency();
   constexpr int kPairs = kWide ? 4 : 1;
@@ -86,8 +86,8 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
     low[k] = static_cast<uint32_t>(a.turns[i + k]);
   }
 #pragma unroll
-  for (int r = 0; r < kTableRows; ++r) {
-    const int64_t p = ((int64_t)blockIdx.x * kTableRows + r) * a.block_rows + sub;
+  for (int r = 0; r < kRows; ++r) {
+    const int64_t p = ((int64_t)blockIdx.x * kRows + r) * a.block_rows + sub;
     if (p >= a.positions) return;
     const uint32_t position = static_cast<uint32_t>(a.first + p);
     float c[kPairs], s[kPairs];
@@ -486,7 +486,7 @@ static bool multiple(const void* p, size_t a) { return reinterpret_cast<uintptr_
 namespace mla {
 
 cudaError_t launch_rope_table(float* table, int64_t first, int64_t positions, int half, const uint64_t* turns,
-                              float magnitude, cudaStream_t stream) {
+                              float magnitude, Device dev, cudaStream_t stream) {
   using namespace mla_pr;
   TableArgs a{};
   a.table = table;
@@ -497,8 +497,12 @@ cudaError_t launch_rope_table(float* table, int64_t first, int64_t positions, in
   std::copy(turns, turns + half, a.turns);
   const bool wide = half % 4 == 0 && multiple(table, 16);
   a.block_rows = kThreads / (wide ? half / 4 : half);
-  const int64_t block = (int64_t)kTableRows * a.block_rows, blocks = (positions + block - 1) / block;
-  return wide ? launch_pdl(rope_table_kernel<true>, blocks, kThreads, stream, a) : launch_pdl(rope_table_kernel<false>, blocks, kThreads, stream, a);
+  const int64_t singles = (positions + a.block_rows - 1) / a.block_rows, fours = (positions + 4 * a.block_rows - 1) / (4 * a.block_rows);
+  if (fours >= dev.sms)
+    return wide ? launch_pdl(rope_table_kernel<true, 4>, fours, kThreads, stream, a)
+                : launch_pdl(rope_table_kernel<false, 4>, fours, kThreads, stream, a);
+  return wide ? launch_pdl(rope_table_kernel<true, 1>, singles, kThreads, stream, a)
+              : launch_pdl(rope_table_kernel<false, 1>, singles, kThreads, stream, a);
 }
 
 cudaError_t launch_rope(HeadRows q, HeadRows k, HeadRows q_out, HeadRows k_out, const int64_t* positions,
