@@ -595,7 +595,7 @@ int mla_gemm_fp8_form(int num_tokens, int n, int k, int num_experts, int grouped
  * gather of cached rows for the expansion of a prefix, and the merge of the
  * prefix's and the new tokens' results.  (sglang trtllm_mla_backend.py,
  * forward_extend: ragged attention of head dims 192 / 128 with lse, prefix chunks
- * attended without a mask and merged; tokenspeed trtllm_mla.py, forward_extend.)
+ * attended without a mask and merged; tokenspeed trtllm_mla.py, TRTLLMMLABackend.)
  * Every call is asynchronous on `stream`, allocates nothing and may be captured in
  * a CUDA graph.
  *

@@ -1,7 +1,7 @@
 // Latent attention in its expanded form, for prompts: every head has its own
 // 128-wide keys and values, and the 64 rotary key columns are one row shared by
 // all heads (sglang trtllm_mla_backend.py, forward_extend: ragged attention of
-// head dims 192 / 128 with lse; tokenspeed trtllm_mla.py, forward_extend).
+// head dims 192 / 128 with lse; tokenspeed trtllm_mla.py, TRTLLMMLABackend).
 //
 //   s_j = scale (q_nope . k_nope_j + q_pe . k_pe_j),   out = softmax(s) V,   lse = ln sum e^s
 //
