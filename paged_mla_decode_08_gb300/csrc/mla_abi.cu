@@ -13,6 +13,7 @@
 
 #include "../../include/mla_decode.h"
 #include "mla_internal.h"
+#include "mla_prompt.h"
 #include "per_device.h"
 
 namespace mla {

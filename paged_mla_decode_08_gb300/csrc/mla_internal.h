@@ -106,25 +106,6 @@ struct GemmForm {
   int give_up_warp;  // epilogue warp that gives up, -1: none
 };
 
-// Rows [token][head] of a tensor: strides in elements, columns contiguous.
-struct HeadRows {
-  const void* p;
-  int64_t token_stride, head_stride;
-};
-
-// One call of the expanded attention.
-struct PrefillCall {
-  HeadRows q_nope, q_pe, k_nope, k_pe, v, out;
-  float* lse;
-  const int32_t* cu_q;
-  const int32_t* cu_k;
-  int batch, num_heads, num_tokens_q, num_tokens_k;
-  bool causal;
-  float scale;
-  void* workspace;
-};
-int prefill_items(int num_tokens_q, int batch);
-
 #ifdef __CUDACC__
 // First query token and query-token count of request b: (b * q_len, q_len)
 // for a uniform batch; (cu_q[b], cu_q[b+1] - cu_q[b]) for a ragged one.  A

@@ -69,6 +69,7 @@
 
 #include "../../include/mla_decode.h"
 #include "mla_internal.h"
+#include "mla_prompt.h"
 #include "per_device.h"
 #include "sm103_ptx.cuh"
 

@@ -12,6 +12,7 @@
 
 #include "../../include/mla_decode.h"
 #include "mla_internal.h"
+#include "mla_prompt.h"
 
 namespace mla_pr {
 
