@@ -356,3 +356,36 @@ def test_an_infinity_in_a_part_of_little_weight():
     out, lse = new(1, 1, 128), torch.empty(1, 1, device="cuda")
     prefill(q[..., :128], q[..., 128:], k, k_pe, v, cu([1]), cu([n]), False, out, lse)
     assert not torch.isfinite(out[0, 0, 5]) and torch.all(out[0, 0, :5] == 1) and torch.all(out[0, 0, 6:] == 1)
+
+
+def test_many_heads():
+    t, h = 3, 2999
+    q, kv, k_pe = randn(t, h, 192, seed=1), randn(t, h, 256, seed=2), randn(t, 64, seed=3)
+    out, lse = new(t, h, 128), torch.empty(t, h, device="cuda")
+    prefill(q[..., :128], q[..., 128:], kv[..., :128], k_pe, kv[..., 128:], cu([t]), cu([t]), True, out, lse)
+    k = torch.cat([kv[..., :128], k_pe[:, None].expand(-1, h, -1)], -1).double()
+    s = SCALE * torch.einsum("qhd,khd->hqk", q.double(), k)
+    s.masked_fill_(torch.ones(t, t, dtype=torch.bool, device="cuda").triu(1), -float("inf"))
+    w, v = torch.softmax(s, -1), kv[..., 128:].double()
+    want, mass = torch.einsum("hqk,khd->qhd", w, v), torch.einsum("hqk,khd->qhd", w, v.abs())
+    assert torch.all((out.double() - want).abs() <= 2.0 ** -7 * mass + 2.0 ** -8 * want.abs())
+    assert torch.equal(out[0], kv[0, :, 128:])  # one key
+
+
+def test_offsets_that_begin_behind_the_first_row():
+    """Rows ahead of the first request's and behind the last one's belong to no one."""
+    q, kv, k_pe = randn(50, 2, 192, seed=1), randn(80, 2, 256, seed=2), randn(80, 64, seed=3)
+    kv[:9], kv[70:], k_pe[:9], k_pe[70:], q[:11], q[40:] = (float("nan"),) * 6
+    out, lse = torch.full((50, 2, 128), 7, dtype=BF, device="cuda"), torch.full((50, 2), 7.0, device="cuda")
+    prefill(q[..., :128], q[..., 128:], kv[..., :128], k_pe, kv[..., 128:], cu([20, 9]) + 11, cu([50, 11]) + 9, True, out, lse)
+    alone, alone_lse = new(29, 2, 128), torch.empty(29, 2, device="cuda")
+    prefill(q[11:40, :, :128], q[11:40, :, 128:], kv[9:70, :, :128], k_pe[9:70], kv[9:70, :, 128:], cu([20, 9]), cu([50, 11]),
+            True, alone, alone_lse)
+    assert torch.equal(out[11:40], alone) and torch.equal(lse[11:40], alone_lse) and torch.isfinite(alone).all()
+    assert torch.all(out[:11] == 7) and torch.all(out[40:] == 7) and torch.all(lse[:11] == 7) and torch.all(lse[40:] == 7)
+    pages = randn(3, 64, 576, seed=4)
+    rows, pe = torch.full((20, 512), 7, dtype=BF, device="cuda"), torch.full((20, 64), 7, dtype=BF, device="cuda")
+    bt = torch.tensor([[2], [2]], dtype=torch.int32, device="cuda")  # a page of two requests
+    B.mla_cache_gather(pages, B.MLA_KV_BF16, bt, None, cu([5, 7]) + 4, 1.0, rows, B.MLA_OUT_BF16, None, pe)
+    assert torch.equal(rows[4:9], pages[2, :5, :512]) and torch.equal(rows[9:16], pages[2, :7, :512])
+    assert torch.all(rows[:4] == 7) and torch.all(rows[16:] == 7) and torch.all(pe[:4] == 7) and torch.all(pe[16:] == 7)
