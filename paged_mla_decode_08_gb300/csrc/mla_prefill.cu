@@ -166,7 +166,8 @@ struct Item {
   int look;             // first step whose values are looked through: some row does not see it whole
   int alone;            // one tile's rows: the other tile takes them too, and every second step
   int tile_steps[2];    // a tile's share: the steps with a key that a row of it sees
-  int unused[2];
+  int end;              // behind the item's last row within the request
+  int unused;
 };
 constexpr int kItemBytes = sizeof(Item);
 static_assert(kItemBytes == 64, "pieces of an item");
@@ -180,7 +181,7 @@ __device__ __forceinline__ void plan_item(Item* it, const Args& a) {
   int all[2], total = 0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int first = it->row0 + t * F::kTileRows, last = min(first + F::kTileRows, it->lq) - 1;
+    const int first = it->row0 + t * F::kTileRows, last = min(first + F::kTileRows, it->end) - 1;
     all[t] = last >= first ? (visible(*it, a.causal, last) + F::kKeys - 1) / F::kKeys : 0;
     total = max(total, all[t]);
   }
@@ -197,7 +198,7 @@ __device__ __forceinline__ void plan_item(Item* it, const Args& a) {
     if (it->tile_steps[t] > 0)
       it->look = min(it->look, max(0, visible(*it, a.causal, it->row0 + t * F::kTileRows) / F::kKeys - it->begin));
   }
-  it->alone = it->lq - it->row0 <= F::kTileRows && it->steps > 1;
+  it->alone = it->end - it->row0 <= F::kTileRows && it->steps > 1;
   if (it->alone) {
     it->tile_steps[0] = (it->steps + 1) / 2;
     it->tile_steps[1] = it->steps / 2;
@@ -210,7 +211,9 @@ __device__ __forceinline__ int first_row(const Item& it, int t, int rank) {
 }
 
 // Row blocks: requests own ceil(rows / kItemRows) each, in their order; a request's
-// come with the most keys first.  A request whose offsets break the rules, by
+// come with the most keys first.  A request's first block takes what its rows leave over,
+// for those see the fewest keys (128 heads, causal: 1537 rows 111 us with the last one taking
+// it, 100 so; 16 requests of 300 rows 179 and 156).  A request whose offsets break the rules, by
 // themselves or by beginning before an earlier one's end, owns none.  Found by a warp
 // that walks over the offsets, 32 requests at a time.
 struct Walk {
@@ -278,7 +281,9 @@ __device__ __forceinline__ bool find_block(const Args& a, int idx, Walk& from, i
       it->lq = __shfl_sync(0xffffffffu, r.q1, src) - it->q0;
       it->k0 = __shfl_sync(0xffffffffu, r.k0, src);
       it->lk = __shfl_sync(0xffffffffu, r.k1, src) - it->k0;
-      it->row0 = (__shfl_sync(0xffffffffu, r.upto, src) - 1 - idx) * kItemRows;
+      const int block = __shfl_sync(0xffffffffu, r.upto, src) - 1 - idx;  // of the request
+      it->end = it->lq - ((it->lq - 1) / kItemRows - block) * kItemRows;
+      it->row0 = max(0, it->end - kItemRows);
       return true;
     }
   }
@@ -435,7 +440,7 @@ __device__ void schedule(const Ctx<kCtas>& c, const Args& a, Work w, Item it, in
     if (lane == 0) {
       const uint32_t dst = kOffItem + slot * kItemBytes;
       const int piece[4][4] = {{it.q0, it.lq, it.k0, it.lk}, {it.head, it.row0, it.part, it.more},
-                               {it.begin, it.steps, it.look, it.alone}, {it.tile_steps[0], it.tile_steps[1], 0, 0}};
+                               {it.begin, it.steps, it.look, it.alone}, {it.tile_steps[0], it.tile_steps[1], it.end, 0}};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         st_shared_v4(c.sbase + dst + 16 * i, make_uint4(piece[i][0], piece[i][1], piece[i][2], piece[i][3]));
@@ -482,9 +487,9 @@ template <int kCtas>
 __device__ __forceinline__ Item read_item(const Ctx<kCtas>& c, int n) {
   const uint32_t src = c.sbase + kOffItem + n % kItemSlots * kItemBytes;
   const uint4 x = ld_shared_v4(src), y = ld_shared_v4(src + 16), z = ld_shared_v4(src + 32);
-  const uint2 w = ld_shared_v2(src + 48);
+  const uint4 w = ld_shared_v4(src + 48);
   return Item{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w,
-              (int)z.x, (int)z.y, (int)z.z, (int)z.w, {(int)w.x, (int)w.y}, {0, 0}};
+              (int)z.x, (int)z.y, (int)z.z, (int)z.w, {(int)w.x, (int)w.y}, (int)w.z, 0};
 }
 // Wait for item n; false: there is none, or a wait gave up.
 template <int kCtas>
@@ -938,7 +943,7 @@ __device__ __forceinline__ void note_non_finite(const Ctx<kCtas>& c, int n) {
 // be looked through.
 template <int kCtas>
 __device__ __forceinline__ int whole_steps(const Item& it, int causal, int t, int rank) {
-  const int row = min(first_row<kCtas>(it, t, rank), it.lq - 1);
+  const int row = min(first_row<kCtas>(it, t, rank), it.end - 1);
   const int masked = visible(it, causal, row) / Form<kCtas>::kKeys - it.begin;
   const int some = min(masked, t == 0 || it.alone ? it.look : max(it.look, it.tile_steps[0]));
   const int mine = it.alone ? (some - t + 1) / 2 : some;  // of this tile's
@@ -1105,7 +1110,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       return true;
     };
     const int row = first_row<kCtas>(it, t, c.rank) + quad * 32 + lane;  // within the request
-    const int seen = visible(it, a.causal, min(row, it.lq - 1));
+    const int seen = visible(it, a.causal, min(row, it.end - 1));
     for (int i = whole; i < mine_steps; ++i) {
       const int j = i * stride + shift;
       if (!look(j) || !edge_step(i == 0, seen - (it.begin + j) * F::kKeys)) return;
@@ -1136,7 +1141,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
       base = m;
       total = total * mine_f + l * other_f;
     }
-    const bool mine = row < it.lq;
+    const bool mine = row < it.end;
     const bool none = total == 0.f;  // no key, or scores of -inf alone
     // a share of no weight may hold anything
     const uint32_t keep = none || mine_f == 0.f ? 0 : ~0u, keep_other = none || other_f == 0.f ? 0 : ~0u;
@@ -1332,7 +1337,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args
   Walk walk;
   if (!find_block<kItemRows>(a, (int)blockIdx.x - head * a.tiles, walk, lane, &it)) return;
   const int row = it.row0 + (int)blockIdx.y * kMergeRows + warp;
-  if (row >= it.lq) return;
+  if (row >= it.end) return;
   const int64_t token = it.q0 + row, at = token * a.heads + head, stride = (int64_t)a.tokens_q * a.heads;
   const float mine = lane < a.parts ? __ldcg(a.part_lse + lane * stride + at) : -CUDART_INF_F;  // at most 32 parts
   const float4* x = reinterpret_cast<const float4*>(a.part_out + at * 128) + lane;
