@@ -252,11 +252,13 @@ __device__ __forceinline__ Request walk_on(const Args& a, Walk& w, int lane) {
   w = Walk{w.base + 32, __shfl_sync(0xffffffffu, r.upto, 31), last};
   return r;
 }
-// All of them; `report`: offsets that break the rules go to the error word.
+// All of them, and the first 32 requests; `report`: offsets that break the rules go to the
+// error word.
 template <int kItemRows>
-__device__ __forceinline__ int count_blocks(const Args& a, int lane, bool report) {
+__device__ __forceinline__ int count_blocks(const Args& a, int lane, bool report, Request* first) {
   Walk w;
-  bool bad_q = false, bad_k = false;
+  *first = walk_on<kItemRows>(a, w, lane);
+  bool bad_q = first->bad_q, bad_k = first->bad_k;
   while (w.base < a.batch) {
     const Request r = walk_on<kItemRows>(a, w, lane);
     bad_q |= r.bad_q;
@@ -264,6 +266,21 @@ __device__ __forceinline__ int count_blocks(const Args& a, int lane, bool report
   }
   if (report && (bad_q || bad_k)) atomicCAS(&g_prefill_error, 0, bad_q ? 0xA01 : 0xA02);
   return w.blocks;
+}
+// Number `idx`, if it is one of these requests'.
+template <int kItemRows>
+__device__ __forceinline__ bool pick_block(const Request& r, int idx, Item* it) {
+  const unsigned hit = __ballot_sync(0xffffffffu, r.upto > idx);
+  if (!hit) return false;
+  const int src = __ffs(hit) - 1;
+  it->q0 = __shfl_sync(0xffffffffu, r.q0, src);
+  it->lq = __shfl_sync(0xffffffffu, r.q1, src) - it->q0;
+  it->k0 = __shfl_sync(0xffffffffu, r.k0, src);
+  it->lk = __shfl_sync(0xffffffffu, r.k1, src) - it->k0;
+  const int block = __shfl_sync(0xffffffffu, r.upto, src) - 1 - idx;  // of the request
+  it->end = it->lq - ((it->lq - 1) / kItemRows - block) * kItemRows;
+  it->row0 = max(0, it->end - kItemRows);
+  return true;
 }
 // Number `idx`; false: there is none.  The walk goes on from where the last one ended,
 // if that is not too far.
@@ -273,19 +290,7 @@ __device__ __forceinline__ bool find_block(const Args& a, int idx, Walk& from, i
   if (from.blocks <= idx) w = from;
   while (w.base < a.batch) {
     from = w;
-    const Request r = walk_on<kItemRows>(a, w, lane);
-    const unsigned hit = __ballot_sync(0xffffffffu, r.upto > idx);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      it->q0 = __shfl_sync(0xffffffffu, r.q0, src);
-      it->lq = __shfl_sync(0xffffffffu, r.q1, src) - it->q0;
-      it->k0 = __shfl_sync(0xffffffffu, r.k0, src);
-      it->lk = __shfl_sync(0xffffffffu, r.k1, src) - it->k0;
-      const int block = __shfl_sync(0xffffffffu, r.upto, src) - 1 - idx;  // of the request
-      it->end = it->lq - ((it->lq - 1) / kItemRows - block) * kItemRows;
-      it->row0 = max(0, it->end - kItemRows);
-      return true;
-    }
+    if (pick_block<kItemRows>(walk_on<kItemRows>(a, w, lane), idx, it)) return true;
   }
   return false;
 }
@@ -392,16 +397,17 @@ __device__ __forceinline__ Work work_of(const Args& a, int blocks) {
 }
 // Item `index`, for a converged warp.  Items come a row block at a time, a request's last
 // and longest first, for a group of heads whose keys and values stay in L2; then
-// the next group's.
+// the next group's.  `first`: the first requests, if they are at hand.
 template <int kCtas>
-__device__ __forceinline__ Item item_of(const Args& a, Work& w, int lane) {
+__device__ __forceinline__ Item item_of(const Args& a, Work& w, int lane, const Request* first = nullptr) {
   Item it;
   const int of_group = a.group * w.blocks * a.parts, group = w.index / of_group, rest = w.index - group * of_group;
   const int of_block = min(a.group, a.heads - group * a.group) * a.parts;  // items of a row block, of the group's heads
   const int block = rest / of_block, within = rest - block * of_block;
   it.head = group * a.group + within / a.parts;
   it.part = within % a.parts;
-  it.more = find_block<Form<kCtas>::kItemRows>(a, block, w.walk, lane, &it);
+  constexpr int kRowsOf = Form<kCtas>::kItemRows;
+  it.more = (first && pick_block<kRowsOf>(*first, block, &it)) || find_block<kRowsOf>(a, block, w.walk, lane, &it);
   if (it.more) plan_item<kCtas>(&it, a);
   return it;
 }
@@ -1246,9 +1252,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   Item own;
   if (warp == 3 && c.rank == 0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    blocks = count_blocks<Form<kCtas>::kItemRows>(a, lane, blockIdx.x == 0);
+    Request first;
+    blocks = count_blocks<Form<kCtas>::kItemRows>(a, lane, blockIdx.x == 0, &first);
     Work work = work_of<kCtas>(a, blocks);
-    if (work.index < work.items) own = item_of<kCtas>(a, work, lane);
+    if (work.index < work.items) own = item_of<kCtas>(a, work, lane, &first);
   } else if (warp == 0) {
     if (lane == 0) {
       flag_store(c.sbase + kOffAbort, 0);
