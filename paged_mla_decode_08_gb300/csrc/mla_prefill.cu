@@ -227,10 +227,10 @@ struct Request {
   bool bad_q, bad_k;
 };
 template <int kItemRows>
-__device__ __forceinline__ Request walk_on(const Args& a, Walk& w, int lane) {
+__device__ __forceinline__ Request walk_on(const Args& a, int batch, Walk& w, int lane) {
   Request r{};
   const int b = w.base + lane;
-  if (b < a.batch) {
+  if (b < batch) {
     r.q0 = __ldg(a.cu_q + b);
     r.q1 = __ldg(a.cu_q + b + 1);
     r.k0 = __ldg(a.cu_k + b);
@@ -243,9 +243,9 @@ __device__ __forceinline__ Request walk_on(const Args& a, Walk& w, int lane) {
   before = __shfl_up_sync(0xffffffffu, before, 1);
   before = max(w.end, lane ? before : 0);
   const bool ok_q = r.q0 >= before && r.q0 <= r.q1 && r.q1 <= a.tokens_q, ok_k = r.k0 >= 0 && r.k0 <= r.k1 && r.k1 <= a.tokens_k;
-  r.bad_q = b < a.batch && !ok_q;
-  r.bad_k = b < a.batch && !ok_k;
-  r.upto = b < a.batch && ok_q && ok_k ? (r.q1 - r.q0 + kItemRows - 1) / kItemRows : 0;
+  r.bad_q = b < batch && !ok_q;
+  r.bad_k = b < batch && !ok_k;
+  r.upto = b < batch && ok_q && ok_k ? (r.q1 - r.q0 + kItemRows - 1) / kItemRows : 0;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) r.upto += __shfl_up_sync(0xffffffffu, r.upto, d) * (lane >= d);
   r.upto += w.blocks;
@@ -255,12 +255,12 @@ __device__ __forceinline__ Request walk_on(const Args& a, Walk& w, int lane) {
 // All of them, and the first 32 requests; `report`: offsets that break the rules go to the
 // error word.
 template <int kItemRows>
-__device__ __forceinline__ int count_blocks(const Args& a, int lane, bool report, Request* first) {
+__device__ __forceinline__ int count_blocks(const Args& a, int batch, int lane, bool report, Request* first) {
   Walk w;
-  *first = walk_on<kItemRows>(a, w, lane);
+  *first = walk_on<kItemRows>(a, batch, w, lane);
   bool bad_q = first->bad_q, bad_k = first->bad_k;
-  while (w.base < a.batch) {
-    const Request r = walk_on<kItemRows>(a, w, lane);
+  while (w.base < batch) {
+    const Request r = walk_on<kItemRows>(a, batch, w, lane);
     bad_q |= r.bad_q;
     bad_k |= r.bad_k;
   }
@@ -285,12 +285,12 @@ __device__ __forceinline__ bool pick_block(const Request& r, int idx, Item* it) 
 // Number `idx`; false: there is none.  The walk goes on from where the last one ended,
 // if that is not too far.
 template <int kItemRows>
-__device__ __forceinline__ bool find_block(const Args& a, int idx, Walk& from, int lane, Item* it) {
+__device__ __forceinline__ bool find_block(const Args& a, int batch, int idx, Walk& from, int lane, Item* it) {
   Walk w;
   if (from.blocks <= idx) w = from;
-  while (w.base < a.batch) {
+  while (w.base < batch) {
     from = w;
-    if (pick_block<kItemRows>(walk_on<kItemRows>(a, w, lane), idx, it)) return true;
+    if (pick_block<kItemRows>(walk_on<kItemRows>(a, batch, w, lane), idx, it)) return true;
   }
   return false;
 }
@@ -399,17 +399,26 @@ __device__ __forceinline__ Work work_of(const Args& a, int blocks) {
 // and longest first, for a group of heads whose keys and values stay in L2; then
 // the next group's.  `first`: the first requests, if they are at hand.
 template <int kCtas>
-__device__ __forceinline__ Item item_of(const Args& a, Work& w, int lane, const Request* first = nullptr) {
-  Item it;
+__device__ __forceinline__ Item item_of(const Args& a, Work& w, int lane, int batch, const Request* first = nullptr) {
+  Item it{};
   const int of_group = a.group * w.blocks * a.parts, group = w.index / of_group, rest = w.index - group * of_group;
   const int of_block = min(a.group, a.heads - group * a.group) * a.parts;  // items of a row block, of the group's heads
   const int block = rest / of_block, within = rest - block * of_block;
   it.head = group * a.group + within / a.parts;
   it.part = within % a.parts;
   constexpr int kRowsOf = Form<kCtas>::kItemRows;
-  it.more = (first && pick_block<kRowsOf>(*first, block, &it)) || find_block<kRowsOf>(a, block, w.walk, lane, &it);
-  if (it.more) plan_item<kCtas>(&it, a);
+  it.more = (first && pick_block<kRowsOf>(*first, block, &it)) || find_block<kRowsOf>(a, batch, block, w.walk, lane, &it);
+  plan_item<kCtas>(&it, a);
   return it;
+}
+
+template <int kCtas>
+__device__ __forceinline__ void put_item(const Ctx<kCtas>& c, int slot, const Item& it) {
+  const uint32_t dst = c.sbase + kOffItem + slot * kItemBytes;
+  st_shared_v4(dst, make_uint4(it.q0, it.lq, it.k0, it.lk));
+  st_shared_v4(dst + 16, make_uint4(it.head, it.row0, it.part, it.more));
+  st_shared_v4(dst + 32, make_uint4(it.begin, it.steps, it.look, it.alone));
+  st_shared_v4(dst + 48, make_uint4(it.tile_steps[0], it.tile_steps[1], it.end, 0));
 }
 
 // Run by a warp of the leader: finds items and hands them to both CTAs.
@@ -432,7 +441,7 @@ __device__ void schedule(const Ctx<kCtas>& c, const Args& a, Work w, Item it, in
     return true;
   };
   for (int n = 0;; ++n) {
-    bool known = n == 0;  // the first item, if there is one
+    bool known = n == 0;  // the first item, if there is one, is in its slot
     while (w.index >= w.items) {  // fewer items than clusters: on to the next one
       if (!ask()) return;
       known = false;
@@ -440,19 +449,17 @@ __device__ void schedule(const Ctx<kCtas>& c, const Args& a, Work w, Item it, in
     if (w.index < 0)
       it.more = 0;
     else if (!known)
-      it = item_of<kCtas>(a, w, lane);
+      it = item_of<kCtas>(a, w, lane, a.batch);
     const int slot = n % kItemSlots;
     if (n >= kItemSlots && !c.wait_warp(B_TAKEN + slot, (n / kItemSlots + 1) & 1, 0xA1B)) return;
     if (lane == 0) {
-      const uint32_t dst = kOffItem + slot * kItemBytes;
-      const int piece[4][4] = {{it.q0, it.lq, it.k0, it.lk}, {it.head, it.row0, it.part, it.more},
-                               {it.begin, it.steps, it.look, it.alone}, {it.tile_steps[0], it.tile_steps[1], it.end, 0}};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        st_shared_v4(c.sbase + dst + 16 * i, make_uint4(piece[i][0], piece[i][1], piece[i][2], piece[i][3]));
-        if (kCtas > 1)
-          st_async_v4(peer_items + slot * kItemBytes + 16 * i, piece[i][0], piece[i][1], piece[i][2], piece[i][3],
-                      peer_bars + 8 * slot);
+      if (!known) put_item(c, slot, it);  // (a first item is there)
+      if (kCtas > 1) {
+        const uint32_t dst = peer_items + slot * kItemBytes, bar = peer_bars + 8 * slot;
+        st_async_v4(dst, it.q0, it.lq, it.k0, it.lk, bar);
+        st_async_v4(dst + 16, it.head, it.row0, it.part, it.more, bar);
+        st_async_v4(dst + 32, it.begin, it.steps, it.look, it.alone, bar);
+        st_async_v4(dst + 48, it.tile_steps[0], it.tile_steps[1], it.end, 0, bar);
       }
       mbar_arrive(c.bar(B_ITEM + slot));
     }
@@ -1251,11 +1258,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   int blocks = 0;
   Item own;
   if (warp == 3 && c.rank == 0) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    Request first;
-    blocks = count_blocks<Form<kCtas>::kItemRows>(a, lane, blockIdx.x == 0, &first);
-    Work work = work_of<kCtas>(a, blocks);
-    if (work.index < work.items) own = item_of<kCtas>(a, work, lane, &first);
+    // A first turn on nothing has the instructions fetched while the work before this
+    // launch is not done.
+#pragma unroll 1
+    for (int turn = 0; turn < 2; ++turn) {
+      if (turn) asm volatile("griddepcontrol.wait;" ::: "memory");
+      Request first;
+      blocks = count_blocks<Form<kCtas>::kItemRows>(a, turn ? a.batch : 0, lane, blockIdx.x == 0, &first);
+      Work work = work_of<kCtas>(a, turn ? blocks : 1);
+      if (turn == 0 || work.index < work.items) own = item_of<kCtas>(a, work, lane, turn ? a.batch : 0, &first);
+      if (lane == 0) put_item(c, 0, own);
+    }
   } else if (warp == 0) {
     if (lane == 0) {
       flag_store(c.sbase + kOffAbort, 0);
@@ -1342,7 +1355,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Item it;
   Walk walk;
-  if (!find_block<kItemRows>(a, (int)blockIdx.x - head * a.tiles, walk, lane, &it)) return;
+  if (!find_block<kItemRows>(a, a.batch, (int)blockIdx.x - head * a.tiles, walk, lane, &it)) return;
   const int row = it.row0 + (int)blockIdx.y * kMergeRows + warp;
   if (row >= it.end) return;
   const int64_t token = it.q0 + row, at = token * a.heads + head, stride = (int64_t)a.tokens_q * a.heads;
