@@ -32,9 +32,9 @@
 // to 1580 us (the products' floor at a library's burst rate is 1460), 1650 us in a
 // loop of seconds under the power cap (98% of a library product's rate there).  Few rows
 // over many keys: the bytes of keys and values; 8 requests of a row over 1000 to 4500 keys,
-// 128 heads: 258 us, 5.6 TB/s.  Between them, what an item takes beside its steps: the
+// 128 heads: 241 us, 6.0 TB/s.  Between them, what an item takes beside its steps: the
 // first scores, the last weights' products and the epilogue come one after the other
-// (a request of 130 tokens, 16 heads: 10 us with the launch, of which the data's
+// (a request of 130 tokens, 16 heads: 9 us with the launch, of which the data's
 // floor is 0.4).
 //
 // P enters the second product in bf16 (half a step: 2^-8 of each weight at most, of
@@ -132,7 +132,8 @@ constexpr int kOffPoison = kOffAbort + 4;
 constexpr int kOffItem = (kOffPoison + 4 * kPoisons + 15) / 16 * 16;
 constexpr int kOffAnswer = kOffItem + kItemSlots * 64;
 constexpr int kOffStat = kOffAnswer + 16;  // [row] base and sum of the second tile
-constexpr int kSmem = kOffStat + kRows * 8 + 1024;  // + alignment slack
+constexpr int kOffFirst = kOffStat + kRows * 8;  // the first 32 requests: offsets, then counts
+constexpr int kSmem = kOffFirst + 32 * 24 + 1024;  // + alignment slack
 static_assert(kSmem <= 232448, "shared memory budget");
 
 constexpr uint32_t TM_S = 0, TM_O = 256, kTmemCols = 512;
@@ -213,17 +214,19 @@ __device__ __forceinline__ int first_row(const Item& it, int t, int rank) {
 // Row blocks: requests own ceil(rows / kItemRows) each, in their order; a request's
 // come with the most keys first.  A request's first block takes what its rows leave over,
 // for those see the fewest keys (128 heads, causal: 1537 rows 111 us with the last one taking
-// it, 100 so; 16 requests of 300 rows 179 and 156).  A request whose offsets break the rules, by
-// themselves or by beginning before an earlier one's end, owns none.  Found by a warp
-// that walks over the offsets, 32 requests at a time.
+// it, 100 so; 16 requests of 300 rows 179 and 156).  Up to 32 requests come with the most
+// keys first (8 requests of a row over 1000 to 4500 keys, 128 heads, 257 and 241 us; 10 of 1
+// to 900 rows over 20 to 4512 keys, 16 heads, 79 and 65).  A request whose offsets break the
+// rules, by themselves or by beginning before an earlier one's end, owns none.  Found by
+// a warp that walks over the offsets, 32 requests at a time.
 struct Walk {
   int base = 0;    // the next 32 requests
   int blocks = 0;  // row blocks of those before
   int end = 0;     // ... and the latest end of their rows
 };
-// A lane's request of the next 32, and how many row blocks there are up to it.
+// A lane's request of the next 32, its row blocks, and how many there are up to it.
 struct Request {
-  int q0, q1, k0, k1, upto;
+  int q0, q1, k0, k1, blocks, upto;
   bool bad_q, bad_k;
 };
 template <int kItemRows>
@@ -245,11 +248,25 @@ __device__ __forceinline__ Request walk_on(const Args& a, int batch, Walk& w, in
   const bool ok_q = r.q0 >= before && r.q0 <= r.q1 && r.q1 <= a.tokens_q, ok_k = r.k0 >= 0 && r.k0 <= r.k1 && r.k1 <= a.tokens_k;
   r.bad_q = b < batch && !ok_q;
   r.bad_k = b < batch && !ok_k;
-  r.upto = b < batch && ok_q && ok_k ? (r.q1 - r.q0 + kItemRows - 1) / kItemRows : 0;
+  r.blocks = b < batch && ok_q && ok_k ? (r.q1 - r.q0 + kItemRows - 1) / kItemRows : 0;
+  r.upto = r.blocks;
+  int all;
+  if (batch <= 32) {
+    const int keys = r.k1 - r.k0;
+    all = r.upto = 0;
+#pragma unroll 1
+    for (int i = 0; i < batch; ++i) {
+      const int other = __shfl_sync(0xffffffffu, keys, i), blocks = __shfl_sync(0xffffffffu, r.blocks, i);
+      all += blocks;
+      if (other > keys || (other == keys && i <= lane)) r.upto += blocks;
+    }
+  } else {
 #pragma unroll
-  for (int d = 1; d < 32; d *= 2) r.upto += __shfl_up_sync(0xffffffffu, r.upto, d) * (lane >= d);
+    for (int d = 1; d < 32; d *= 2) r.upto += __shfl_up_sync(0xffffffffu, r.upto, d) * (lane >= d);
+    all = __shfl_sync(0xffffffffu, r.upto, 31);
+  }
   r.upto += w.blocks;
-  w = Walk{w.base + 32, __shfl_sync(0xffffffffu, r.upto, 31), last};
+  w = Walk{w.base + 32, w.blocks + all, last};
   return r;
 }
 // All of them, and the first 32 requests; `report`: offsets that break the rules go to the
@@ -270,7 +287,7 @@ __device__ __forceinline__ int count_blocks(const Args& a, int batch, int lane, 
 // Number `idx`, if it is one of these requests'.
 template <int kItemRows>
 __device__ __forceinline__ bool pick_block(const Request& r, int idx, Item* it) {
-  const unsigned hit = __ballot_sync(0xffffffffu, r.upto > idx);
+  const unsigned hit = __ballot_sync(0xffffffffu, r.upto > idx && r.upto - r.blocks <= idx);
   if (!hit) return false;
   const int src = __ffs(hit) - 1;
   it->q0 = __shfl_sync(0xffffffffu, r.q0, src);
@@ -397,9 +414,9 @@ __device__ __forceinline__ Work work_of(const Args& a, int blocks) {
 }
 // Item `index`, for a converged warp.  Items come a row block at a time, a request's last
 // and longest first, for a group of heads whose keys and values stay in L2; then
-// the next group's.  `first`: the first requests, if they are at hand.
+// the next group's.
 template <int kCtas>
-__device__ __forceinline__ Item item_of(const Args& a, Work& w, int lane, int batch, const Request* first = nullptr) {
+__device__ __forceinline__ Item item_of(const Args& a, Work& w, int lane, int batch, const Request& first) {
   Item it{};
   const int of_group = a.group * w.blocks * a.parts, group = w.index / of_group, rest = w.index - group * of_group;
   const int of_block = min(a.group, a.heads - group * a.group) * a.parts;  // items of a row block, of the group's heads
@@ -407,7 +424,7 @@ __device__ __forceinline__ Item item_of(const Args& a, Work& w, int lane, int ba
   it.head = group * a.group + within / a.parts;
   it.part = within % a.parts;
   constexpr int kRowsOf = Form<kCtas>::kItemRows;
-  it.more = (first && pick_block<kRowsOf>(*first, block, &it)) || find_block<kRowsOf>(a, batch, block, w.walk, lane, &it);
+  it.more = pick_block<kRowsOf>(first, block, &it) || find_block<kRowsOf>(a, batch, block, w.walk, lane, &it);
   plan_item<kCtas>(&it, a);
   return it;
 }
@@ -419,6 +436,19 @@ __device__ __forceinline__ void put_item(const Ctx<kCtas>& c, int slot, const It
   st_shared_v4(dst + 16, make_uint4(it.head, it.row0, it.part, it.more));
   st_shared_v4(dst + 32, make_uint4(it.begin, it.steps, it.look, it.alone));
   st_shared_v4(dst + 48, make_uint4(it.tile_steps[0], it.tile_steps[1], it.end, 0));
+}
+
+// The first 32 requests, kept for the items to come.
+template <int kCtas>
+__device__ __forceinline__ void put_requests(const Ctx<kCtas>& c, int lane, const Request& r) {
+  st_shared_v4(c.sbase + kOffFirst + 16 * lane, make_uint4(r.q0, r.q1, r.k0, r.k1));
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(c.sbase + kOffFirst + 512 + 8 * lane), "r"(r.blocks), "r"(r.upto) : "memory");
+}
+template <int kCtas>
+__device__ __forceinline__ Request get_requests(const Ctx<kCtas>& c, int lane) {
+  const uint4 x = ld_shared_v4(c.sbase + kOffFirst + 16 * lane);
+  const uint2 y = ld_shared_v2(c.sbase + kOffFirst + 512 + 8 * lane);
+  return Request{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, false, false};
 }
 
 // Run by a warp of the leader: finds items and hands them to both CTAs.
@@ -449,7 +479,7 @@ __device__ void schedule(const Ctx<kCtas>& c, const Args& a, Work w, Item it, in
     if (w.index < 0)
       it.more = 0;
     else if (!known)
-      it = item_of<kCtas>(a, w, lane, a.batch);
+      it = item_of<kCtas>(a, w, lane, a.batch, get_requests(c, lane));
     const int slot = n % kItemSlots;
     if (n >= kItemSlots && !c.wait_warp(B_TAKEN + slot, (n / kItemSlots + 1) & 1, 0xA1B)) return;
     if (lane == 0) {
@@ -1266,7 +1296,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       Request first;
       blocks = count_blocks<Form<kCtas>::kItemRows>(a, turn ? a.batch : 0, lane, blockIdx.x == 0, &first);
       Work work = work_of<kCtas>(a, turn ? blocks : 1);
-      if (turn == 0 || work.index < work.items) own = item_of<kCtas>(a, work, lane, turn ? a.batch : 0, &first);
+      if (turn == 0 || work.index < work.items) own = item_of<kCtas>(a, work, lane, turn ? a.batch : 0, first);
+      put_requests(c, lane, first);
       if (lane == 0) put_item(c, 0, own);
     }
   } else if (warp == 0) {
@@ -1450,7 +1481,7 @@ constexpr int64_t kGroupBytes = 32 << 20;
 // Clusters: one for each item that there can be, but no more than twice those of rows that
 // are all one request's, or eight an SM.  With more items than clusters each takes several.
 // (A batch padded with empty requests would else start many for nothing: 2048 rows of 4
-// requests among 512, 128 heads, took 2166 us, now 83, as a batch of 4 takes 79.  Two an
+// requests among 512, 128 heads, took 2166 us, now 83 to 87, as a batch of 4 takes 79.  Two an
 // SM left 4 requests of 64 rows over 1000 to 4000 keys at 149 us, eight 138.)
 template <int kCtas>
 static int64_t clusters_of(const PrefillCall& p, const Args& a, int sms) {
