@@ -630,8 +630,9 @@ int mla_gemm_fp8_form(int num_tokens, int n, int k, int num_experts, int grouped
  *                    pairs that turn more than beta_fast times within the original
  *                    context keep their frequency, those that turn less than
  *                    beta_slow times are stretched.
- * Angles are reduced in whole numbers, to 2^-31 of a turn, so far positions lose
- * nothing: the error is about that of one fp32 sine, cosine and product.
+ * Frequencies are computed in double precision (2^-52 of w_i) and angles reduced in
+ * whole numbers, to 2^-31 of a turn: far positions lose no more than those two, beside
+ * the error of one fp32 sine, cosine and product.
  *
  *   table           device fp32 [num_positions, rotary_dim], contiguous.
  *   first_position  >= 0, first_position + num_positions <= 2^31.

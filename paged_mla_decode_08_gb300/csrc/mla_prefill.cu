@@ -32,7 +32,7 @@
 // to 1580 us (the products' floor at a library's burst rate is 1460), 1650 us in a
 // loop of seconds under the power cap (98% of a library product's rate there).  Few rows
 // over many keys: the bytes of keys and values; 8 requests of a row over 1000 to 4500 keys,
-// 128 heads: 241 us, 6.0 TB/s.  Between them, what an item takes beside its steps: the
+// 128 heads: 241 to 246 us, 5.9 TB/s.  Between them, what an item takes beside its steps: the
 // first scores, the last weights' products and the epilogue come one after the other
 // (a request of 130 tokens, 16 heads: 9 us with the launch, of which the data's
 // floor is 0.4).
