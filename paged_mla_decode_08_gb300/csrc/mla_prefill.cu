@@ -103,6 +103,7 @@ struct Form {
   static constexpr int kItemRows = 2 * kTileRows;
 };
 
+constexpr int kPartKeys = 256;  // of a part, at least
 constexpr int kItemSlots = 4;
 constexpr int kAskAhead = 4;  // steps before an item's end at which its successor is asked for
 enum Bar : int {
@@ -133,7 +134,7 @@ constexpr int kOffItem = (kOffPoison + 4 * kPoisons + 15) / 16 * 16;
 constexpr int kOffAnswer = kOffItem + kItemSlots * 64;
 constexpr int kOffStat = kOffAnswer + 16;  // [row] base and sum of the second tile
 constexpr int kOffFirst = kOffStat + kRows * 8;  // the first 32 requests: offsets, then counts
-constexpr int kSmem = kOffFirst + 32 * 24 + 1024;  // + alignment slack
+constexpr int kSmem = kOffFirst + 32 * 32 + 1024;  // + alignment slack
 static_assert(kSmem <= 232448, "shared memory budget");
 
 constexpr uint32_t TM_S = 0, TM_O = 256, kTmemCols = 512;
@@ -147,7 +148,8 @@ struct Args {
   int64_t v_ts, v_hs, out_ts, out_hs;  // strides of a token and a head, in elements
   int32_t batch, heads, tokens_q, tokens_k;
   int32_t tiles;   // row blocks: at most this many exist
-  int32_t parts;   // items of a row block: each has a part of the keys
+  int32_t parts;   // of a row block's keys, at most: each is an item of its own
+  int32_t slots;   // CTAs, or pairs, that the GPU has room for
   int32_t group;   // heads whose items are mixed
   float* part_out; // [part][token][head][128], [part][token][head]: what a part alone gives
   float* part_lse;
@@ -168,7 +170,7 @@ struct Item {
   int alone;            // one tile's rows: the other tile takes them too, and every second step
   int tile_steps[2];    // a tile's share: the steps with a key that a row of it sees
   int end;              // behind the item's last row within the request
-  int unused;
+  int parts;            // of its keys
 };
 constexpr int kItemBytes = sizeof(Item);
 static_assert(kItemBytes == 64, "pieces of an item");
@@ -188,9 +190,9 @@ __device__ __forceinline__ void plan_item(Item* it, const Args& a) {
   }
   it->begin = 0;
   int end = total;
-  if (a.parts > 1) {
-    it->begin = total * it->part / a.parts;  // (fewer than 2^25 steps, at most 32 parts)
-    end = total * (it->part + 1) / a.parts;
+  if (it->parts > 1) {
+    it->begin = total * it->part / it->parts;  // (fewer than 2^25 steps, at most 32 parts)
+    end = total * (it->part + 1) / it->parts;
   }
   it->steps = it->look = end - it->begin;
 #pragma unroll
@@ -211,7 +213,7 @@ __device__ __forceinline__ int first_row(const Item& it, int t, int rank) {
   return it.row0 + (it.alone ? 0 : t * Form<kCtas>::kTileRows) + rank * kRows;
 }
 
-// Row blocks: requests own ceil(rows / kItemRows) each, in their order; a request's
+// Row blocks, or the parts of their keys, one after the other: requests own ceil(rows / kItemRows) each, in their order; a request's
 // come with the most keys first.  A request's first block takes what its rows leave over,
 // for those see the fewest keys (128 heads, causal: 1537 rows 111 us with the last one taking
 // it, 100 so; 16 requests of 300 rows 179 and 156).  Up to 32 requests come with the most
@@ -221,15 +223,19 @@ __device__ __forceinline__ int first_row(const Item& it, int t, int rank) {
 // a warp that walks over the offsets, 32 requests at a time.
 struct Walk {
   int base = 0;    // the next 32 requests
-  int blocks = 0;  // row blocks of those before
+  int blocks = 0;  // row blocks, or parts, of those before
   int end = 0;     // ... and the latest end of their rows
 };
-// A lane's request of the next 32, its row blocks, and how many there are up to it.
+// A lane's request of the next 32, its row blocks (or parts), how many there are up to
+// it, and the parts of a block.
 struct Request {
-  int q0, q1, k0, k1, blocks, upto;
+  int q0, q1, k0, k1, blocks, upto, parts;
   bool bad_q, bad_k;
 };
-template <int kItemRows>
+// Up to 32 requests: a request's keys are cut so that no part is twice as long as all
+// keys and row blocks, spread evenly, would make them (4 requests of 64 rows, 32 heads, three
+// over 500 keys and one over 8000, 88 us uncut, 50 so).  More requests: all alike.
+template <int kItemRows, bool kCut>
 __device__ __forceinline__ Request walk_on(const Args& a, int batch, Walk& w, int lane) {
   Request r{};
   const int b = w.base + lane;
@@ -249,10 +255,18 @@ __device__ __forceinline__ Request walk_on(const Args& a, int batch, Walk& w, in
   r.bad_q = b < batch && !ok_q;
   r.bad_k = b < batch && !ok_k;
   r.blocks = b < batch && ok_q && ok_k ? (r.q1 - r.q0 + kItemRows - 1) / kItemRows : 0;
-  r.upto = r.blocks;
   int all;
+  r.parts = a.parts;
   if (batch <= 32) {
-    const int keys = r.k1 - r.k0;
+    const int keys = r.blocks > 0 ? r.k1 - r.k0 : 0;
+    if (a.parts > 1) {
+      float load = static_cast<float>(r.blocks) * static_cast<float>(keys);
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) load += __shfl_xor_sync(0xffffffffu, load, d);
+      const float share = fmaxf(static_cast<float>(kPartKeys), load * static_cast<float>(a.heads) / static_cast<float>(a.slots));
+      r.parts = max(1, min(a.parts, static_cast<int>(static_cast<float>(keys) / share)));
+    }
+    if (kCut) r.blocks *= r.parts;
     all = r.upto = 0;
 #pragma unroll 1
     for (int i = 0; i < batch; ++i) {
@@ -261,6 +275,8 @@ __device__ __forceinline__ Request walk_on(const Args& a, int batch, Walk& w, in
       if (other > keys || (other == keys && i <= lane)) r.upto += blocks;
     }
   } else {
+    if (kCut) r.blocks *= r.parts;
+    r.upto = r.blocks;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) r.upto += __shfl_up_sync(0xffffffffu, r.upto, d) * (lane >= d);
     all = __shfl_sync(0xffffffffu, r.upto, 31);
@@ -271,21 +287,21 @@ __device__ __forceinline__ Request walk_on(const Args& a, int batch, Walk& w, in
 }
 // All of them, and the first 32 requests; `report`: offsets that break the rules go to the
 // error word.
-template <int kItemRows>
+template <int kItemRows, bool kCut>
 __device__ __forceinline__ int count_blocks(const Args& a, int batch, int lane, bool report, Request* first) {
   Walk w;
-  *first = walk_on<kItemRows>(a, batch, w, lane);
+  *first = walk_on<kItemRows, kCut>(a, batch, w, lane);
   bool bad_q = first->bad_q, bad_k = first->bad_k;
   while (w.base < batch) {
-    const Request r = walk_on<kItemRows>(a, batch, w, lane);
+    const Request r = walk_on<kItemRows, kCut>(a, batch, w, lane);
     bad_q |= r.bad_q;
     bad_k |= r.bad_k;
   }
   if (report && (bad_q || bad_k)) atomicCAS(&g_prefill_error, 0, bad_q ? 0xA01 : 0xA02);
   return w.blocks;
 }
-// Number `idx`, if it is one of these requests'.
-template <int kItemRows>
+// Row block, or part, number `idx`, if it is one of these requests'.
+template <int kItemRows, bool kCut>
 __device__ __forceinline__ bool pick_block(const Request& r, int idx, Item* it) {
   const unsigned hit = __ballot_sync(0xffffffffu, r.upto > idx && r.upto - r.blocks <= idx);
   if (!hit) return false;
@@ -294,20 +310,27 @@ __device__ __forceinline__ bool pick_block(const Request& r, int idx, Item* it) 
   it->lq = __shfl_sync(0xffffffffu, r.q1, src) - it->q0;
   it->k0 = __shfl_sync(0xffffffffu, r.k0, src);
   it->lk = __shfl_sync(0xffffffffu, r.k1, src) - it->k0;
-  const int block = __shfl_sync(0xffffffffu, r.upto, src) - 1 - idx;  // of the request
+  it->parts = __shfl_sync(0xffffffffu, r.parts, src);
+  int block = __shfl_sync(0xffffffffu, r.upto, src) - 1 - idx;  // of the request
+  it->part = 0;
+  if (kCut && it->parts > 1) {
+    const int at = block;
+    block = at / it->parts;
+    it->part = at - block * it->parts;
+  }
   it->end = it->lq - ((it->lq - 1) / kItemRows - block) * kItemRows;
   it->row0 = max(0, it->end - kItemRows);
   return true;
 }
 // Number `idx`; false: there is none.  The walk goes on from where the last one ended,
 // if that is not too far.
-template <int kItemRows>
+template <int kItemRows, bool kCut>
 __device__ __forceinline__ bool find_block(const Args& a, int batch, int idx, Walk& from, int lane, Item* it) {
   Walk w;
   if (from.blocks <= idx) w = from;
   while (w.base < batch) {
     from = w;
-    if (pick_block<kItemRows>(walk_on<kItemRows>(a, batch, w, lane), idx, it)) return true;
+    if (pick_block<kItemRows, kCut>(walk_on<kItemRows, kCut>(a, batch, w, lane), idx, it)) return true;
   }
   return false;
 }
@@ -402,15 +425,15 @@ __device__ __forceinline__ int read_answer(uint32_t answer) {
 // What there is to do, and where a cluster stands: item `index`, then every
 // `clusters`-th after it, then those of the cluster that the hardware gives.
 struct Work {
-  int blocks;    // row blocks
-  int items;     // ... of all heads and parts
+  int blocks;    // parts of row blocks
+  int items;     // ... of all heads
   int clusters;  // of the grid
   int index;     // -1: nothing is left
   Walk walk;
 };
 template <int kCtas>
 __device__ __forceinline__ Work work_of(const Args& a, int blocks) {
-  return Work{blocks, blocks * a.heads * a.parts, (int)gridDim.x / kCtas, (int)blockIdx.x / kCtas, Walk()};
+  return Work{blocks, blocks * a.heads, (int)gridDim.x / kCtas, (int)blockIdx.x / kCtas, Walk()};
 }
 // Item `index`, for a converged warp.  Items come a row block at a time, a request's last
 // and longest first, for a group of heads whose keys and values stay in L2; then
@@ -418,13 +441,12 @@ __device__ __forceinline__ Work work_of(const Args& a, int blocks) {
 template <int kCtas>
 __device__ __forceinline__ Item item_of(const Args& a, Work& w, int lane, int batch, const Request& first) {
   Item it{};
-  const int of_group = a.group * w.blocks * a.parts, group = w.index / of_group, rest = w.index - group * of_group;
-  const int of_block = min(a.group, a.heads - group * a.group) * a.parts;  // items of a row block, of the group's heads
-  const int block = rest / of_block, within = rest - block * of_block;
-  it.head = group * a.group + within / a.parts;
-  it.part = within % a.parts;
+  const int of_group = a.group * w.blocks, group = w.index / of_group, rest = w.index - group * of_group;
+  const int heads = min(a.group, a.heads - group * a.group);
+  const int block = rest / heads;
+  it.head = group * a.group + rest - block * heads;
   constexpr int kRowsOf = Form<kCtas>::kItemRows;
-  it.more = pick_block<kRowsOf>(first, block, &it) || find_block<kRowsOf>(a, batch, block, w.walk, lane, &it);
+  it.more = pick_block<kRowsOf, true>(first, block, &it) || find_block<kRowsOf, true>(a, batch, block, w.walk, lane, &it);
   plan_item<kCtas>(&it, a);
   return it;
 }
@@ -435,20 +457,19 @@ __device__ __forceinline__ void put_item(const Ctx<kCtas>& c, int slot, const It
   st_shared_v4(dst, make_uint4(it.q0, it.lq, it.k0, it.lk));
   st_shared_v4(dst + 16, make_uint4(it.head, it.row0, it.part, it.more));
   st_shared_v4(dst + 32, make_uint4(it.begin, it.steps, it.look, it.alone));
-  st_shared_v4(dst + 48, make_uint4(it.tile_steps[0], it.tile_steps[1], it.end, 0));
+  st_shared_v4(dst + 48, make_uint4(it.tile_steps[0], it.tile_steps[1], it.end, it.parts));
 }
 
 // The first 32 requests, kept for the items to come.
 template <int kCtas>
 __device__ __forceinline__ void put_requests(const Ctx<kCtas>& c, int lane, const Request& r) {
   st_shared_v4(c.sbase + kOffFirst + 16 * lane, make_uint4(r.q0, r.q1, r.k0, r.k1));
-  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(c.sbase + kOffFirst + 512 + 8 * lane), "r"(r.blocks), "r"(r.upto) : "memory");
+  st_shared_v4(c.sbase + kOffFirst + 512 + 16 * lane, make_uint4(r.blocks, r.upto, r.parts, 0));
 }
 template <int kCtas>
 __device__ __forceinline__ Request get_requests(const Ctx<kCtas>& c, int lane) {
-  const uint4 x = ld_shared_v4(c.sbase + kOffFirst + 16 * lane);
-  const uint2 y = ld_shared_v2(c.sbase + kOffFirst + 512 + 8 * lane);
-  return Request{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, false, false};
+  const uint4 x = ld_shared_v4(c.sbase + kOffFirst + 16 * lane), y = ld_shared_v4(c.sbase + kOffFirst + 512 + 16 * lane);
+  return Request{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, false, false};
 }
 
 // Run by a warp of the leader: finds items and hands them to both CTAs.
@@ -489,7 +510,7 @@ __device__ void schedule(const Ctx<kCtas>& c, const Args& a, Work w, Item it, in
         st_async_v4(dst, it.q0, it.lq, it.k0, it.lk, bar);
         st_async_v4(dst + 16, it.head, it.row0, it.part, it.more, bar);
         st_async_v4(dst + 32, it.begin, it.steps, it.look, it.alone, bar);
-        st_async_v4(dst + 48, it.tile_steps[0], it.tile_steps[1], it.end, 0, bar);
+        st_async_v4(dst + 48, it.tile_steps[0], it.tile_steps[1], it.end, it.parts, bar);
       }
       mbar_arrive(c.bar(B_ITEM + slot));
     }
@@ -532,7 +553,7 @@ __device__ __forceinline__ Item read_item(const Ctx<kCtas>& c, int n) {
   const uint4 x = ld_shared_v4(src), y = ld_shared_v4(src + 16), z = ld_shared_v4(src + 32);
   const uint4 w = ld_shared_v4(src + 48);
   return Item{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w,
-              (int)z.x, (int)z.y, (int)z.z, (int)z.w, {(int)w.x, (int)w.y}, (int)w.z, 0};
+              (int)z.x, (int)z.y, (int)z.z, (int)z.w, {(int)w.x, (int)w.y}, (int)w.z, (int)w.w};
 }
 // Wait for item n; false: there is none, or a wait gave up.
 template <int kCtas>
@@ -1221,7 +1242,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
           if (lane == 0) mbar_arrive(c.bar(B_READ));
         }
       }
-      if (a.parts > 1) {
+      if (it.parts > 1) {
         if (mine && !none && q >= 0) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -1244,11 +1265,11 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
     if (mine_steps > 0) op ^= 1;
     if (other_steps > 0) other_op ^= 1;
     const bool poison = flag_load(c.sbase + kOffPoison + 4 * (n % kPoisons)) != 0;
-    float* lse = a.parts > 1 ? a.part_lse + part_row * a.heads : a.lse + token * a.heads;
+    float* lse = it.parts > 1 ? a.part_lse + part_row * a.heads : a.lse + token * a.heads;
     if (poison && mine && !none) {
       const uint16_t* v = a.v + it.k0 * a.v_ts + it.head * a.v_hs;
       const int from = (it.begin + it.look) * F::kKeys, to = min(seen, (it.begin + it.steps) * F::kKeys);
-      if (a.parts > 1)
+      if (it.parts > 1)
         add_non_finite(v, a.v_ts, from, to, part_out);
       else
         add_non_finite(v, a.v_ts, from, to, reinterpret_cast<__nv_bfloat16*>(out));
@@ -1294,7 +1315,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     for (int turn = 0; turn < 2; ++turn) {
       if (turn) asm volatile("griddepcontrol.wait;" ::: "memory");
       Request first;
-      blocks = count_blocks<Form<kCtas>::kItemRows>(a, turn ? a.batch : 0, lane, blockIdx.x == 0, &first);
+      blocks = count_blocks<Form<kCtas>::kItemRows, true>(a, turn ? a.batch : 0, lane, blockIdx.x == 0, &first);
       Work work = work_of<kCtas>(a, turn ? blocks : 1);
       if (turn == 0 || work.index < work.items) own = item_of<kCtas>(a, work, lane, turn ? a.batch : 0, first);
       put_requests(c, lane, first);
@@ -1386,11 +1407,12 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Item it;
   Walk walk;
-  if (!find_block<kItemRows>(a, a.batch, (int)blockIdx.x - head * a.tiles, walk, lane, &it)) return;
+  if (!find_block<kItemRows, false>(a, a.batch, (int)blockIdx.x - head * a.tiles, walk, lane, &it)) return;
+  if (it.parts == 1) return;  // its results are there
   const int row = it.row0 + (int)blockIdx.y * kMergeRows + warp;
   if (row >= it.end) return;
   const int64_t token = it.q0 + row, at = token * a.heads + head, stride = (int64_t)a.tokens_q * a.heads;
-  const float mine = lane < a.parts ? __ldcg(a.part_lse + lane * stride + at) : -CUDART_INF_F;  // at most 32 parts
+  const float mine = lane < it.parts ? __ldcg(a.part_lse + lane * stride + at) : -CUDART_INF_F;  // at most 32 parts
   const float4* x = reinterpret_cast<const float4*>(a.part_out + at * 128) + lane;
   float top = mine;
 #pragma unroll
@@ -1401,11 +1423,11 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args
   for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   w = sum == 0.f ? 0.f : w / sum;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < a.parts; k0 += 4) {
+  for (int k0 = 0; k0 < it.parts; k0 += 4) {
     float4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (k0 + k < a.parts) v[k] = __ldcg(x + (k0 + k) * stride * 32);
+      if (k0 + k < it.parts) v[k] = __ldcg(x + (k0 + k) * stride * 32);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float f = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
@@ -1449,20 +1471,27 @@ static bool make_map(CUtensorMap* map, const HeadRows& x, int64_t cols, int64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Items of a head: one for each `item_rows` rows of a request, at most
+// Row blocks: at most this many exist
 static int items_of_a_head(int num_tokens_q, int batch, int item_rows) {
-  return num_tokens_q / item_rows + (batch < num_tokens_q ? batch : num_tokens_q);
+  const int owners = std::min(batch, num_tokens_q);  // requests with a row, at most
+  return (num_tokens_q - owners) / item_rows + owners;
 }
 
-// Parts of the keys: enough to give every CTA an item, of 256 keys or more.  In us, not
-// cut, of 1024, 512 and 256 keys at least: a row over 2000 keys, 16 heads, 26.6, 26.6, 17.8,
-// 16.9; over 16000 165, 36, 36, 36; 16 rows over 2000 keys, 4 heads, 26.4, 26.4, 16.7, 14.1;
-// 300 rows over 20000 keys, 19 heads, 228, 79, 79, 78.
+// Parts of a row block's keys, at most: enough to give every CTA an item, of 256 keys or
+// more.  In us, not cut, of 1024, 512 and 256 keys at least: a row over 2000 keys, 16 heads,
+// 26.6, 26.6, 17.8, 16.9; over 16000 165, 36, 36, 36; 16 rows over 2000 keys, 4 heads, 26.4,
+// 26.4, 16.7, 14.1; 300 rows over 20000 keys, 19 heads, 228, 79, 79, 78.  The keys may be
+// one request's: where few requests give few items they are cut as their lengths ask for
+// (on the device), within 64 MB of results.
 template <int kCtas>
 static int parts_of(int num_tokens_q, int num_tokens_k, int batch, int num_heads, int sms) {
-  const int64_t items = (int64_t)items_of_a_head(num_tokens_q, batch, Form<kCtas>::kItemRows) * num_heads;
-  const int64_t room = sms / kCtas / std::max<int64_t>(1, items), most = num_tokens_k / batch / 256;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(room, most), 32));
+  const int64_t items = std::max<int64_t>(1, (int64_t)items_of_a_head(num_tokens_q, batch, Form<kCtas>::kItemRows) * num_heads);
+  int64_t parts = std::min<int64_t>(sms / kCtas / items, num_tokens_k / batch / kPartKeys);
+  if (batch > 1 && batch <= 32 && items <= 2 * sms / kCtas) {
+    const int64_t bytes = (int64_t)std::max(1, num_tokens_q) * num_heads * (128 + 1) * 4;
+    parts = std::max(parts, std::min<int64_t>(num_tokens_k / kPartKeys, (64 << 20) / bytes));
+  }
+  return (int)std::max<int64_t>(1, std::min<int64_t>(parts, 32));
 }
 // Pairs of CTAs, or one CTA an item: by the rows and keys of a request, on average.
 // Measured in us (128 heads; one CTA, pair): 8 requests of 512 rows 131 and 138, 16 of 300
@@ -1508,6 +1537,7 @@ static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t
       !make_map(&m.v, keys ? p.v : p.q_nope, 128, p.num_heads, tk, F::kKeys))
     return cudaErrorNotSupported;
   a.tiles = items_of_a_head(p.num_tokens_q, p.batch, F::kItemRows);
+  a.slots = dev.sms / kCtas;
   a.parts = parts_of<kCtas>(p.num_tokens_q, p.num_tokens_k, p.batch, p.num_heads, dev.sms);
   const int64_t groups = std::max<int64_t>(1, (512 * (tk / p.batch) * p.num_heads + kGroupBytes - 1) / kGroupBytes);
   a.group = (int)((p.num_heads + groups - 1) / groups);

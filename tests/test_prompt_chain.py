@@ -389,3 +389,31 @@ def test_offsets_that_begin_behind_the_first_row():
     B.mla_cache_gather(pages, B.MLA_KV_BF16, bt, None, cu([5, 7]) + 4, 1.0, rows, B.MLA_OUT_BF16, None, pe)
     assert torch.equal(rows[4:9], pages[2, :5, :512]) and torch.equal(rows[9:16], pages[2, :7, :512])
     assert torch.all(rows[:4] == 7) and torch.all(rows[16:] == 7) and torch.all(pe[:4] == 7) and torch.all(pe[16:] == 7)
+
+
+@pytest.mark.parametrize("h, lens, ahead", [(3, [64, 5, 0, 64], [436, 0, 9, 7936]), (16, [1, 1, 1], [300, 9000, 300]), (2, [700, 3, 40], [5000, 100, 0]),
+                                            (1, [2] * 31 + [1], [40] * 31 + [6000])])
+def test_one_long_request_among_short_ones(h, lens, ahead):
+    """Its keys are cut, theirs are not; an infinity reaches the rows that see it."""
+    q, kv = randn(sum(lens), h, 192, seed=1), randn(sum(lens) + sum(ahead), h, 256, seed=2)
+    k_pe = randn(kv.shape[0], 64, seed=3)
+    keys = [a + n for a, n in zip(ahead, lens)]
+    out, lse = new(sum(lens), h, 128), torch.empty(sum(lens), h, device="cuda")
+    prefill(q[..., :128], q[..., 128:], kv[..., :128], k_pe, kv[..., 128:], cu(lens), cu(keys), True, out, lse)
+    k = torch.cat([kv[..., :128], k_pe[:, None].expand(-1, h, -1)], -1).double()
+    q0 = k0 = 0
+    for n, m in zip(lens, keys):
+        s = SCALE * torch.einsum("qhd,khd->hqk", q[q0:q0 + n].double(), k[k0:k0 + m])
+        s.masked_fill_(torch.arange(m, device="cuda") > torch.arange(m - n, m, device="cuda")[:, None], -float("inf"))
+        w, v = torch.softmax(s, -1), kv[k0:k0 + m, :, 128:].double()
+        want, mass = torch.einsum("hqk,khd->qhd", w, v), torch.einsum("hqk,khd->qhd", w, v.abs())
+        assert torch.all((out[q0:q0 + n].double() - want).abs() <= 2.0 ** -7 * mass + 2.0 ** -8 * want.abs())
+        assert torch.all((lse[q0:q0 + n].double() - torch.logsumexp(s, -1).T).abs() <= 1e-4)
+        q0, k0 = q0 + n, k0 + m
+    again, again_lse = torch.empty_like(out), torch.empty_like(lse)
+    kv[-1, :, 130] = float("inf")  # the last request's last key: seen by its last row
+    prefill(q[..., :128], q[..., 128:], kv[..., :128], k_pe, kv[..., 128:], cu(lens), cu(keys), True, again, again_lse)
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    if lens[-1]:
+        bad[-1, :, 2] = True
+    assert torch.equal(~torch.isfinite(again), bad) and torch.equal(again[~bad], out[~bad]) and torch.equal(again_lse, lse)
