@@ -65,7 +65,6 @@
 
 #include <algorithm>
 #include <mutex>
-#include <type_traits>
 
 #include "../../include/mla_decode.h"
 #include "mla_internal.h"

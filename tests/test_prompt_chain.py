@@ -243,7 +243,12 @@ def test_a_stream_given_by_name():
 
 
 def exact_rows(q, k, v):
-    """fp64 attention of a few rows over all keys: q [n, 192], k [m, 192], v [m, 128]."""
+    """fp64 attention of a few rows over all keys: q [n, 192], k [m, 192], v [m, 128].
+
+    What the tests below allow, in units of the weights' mass sum w |v|: 2^-8 for weights
+    rounded to bf16 (half a step), and as much again for scores off by up to 2^-9 (a sum
+    of 192 fp32 products is off by 24 roundings of 2^-22 of sum |q k| scale < 60, which is
+    below 2^-11) and for fp32 sums; and 2^-8 of the result for its own rounding."""
     w = torch.softmax(SCALE * (q.double() @ k.double().T), 1)
     return w @ v.double(), w @ v.double().abs()
 
@@ -417,3 +422,32 @@ def test_one_long_request_among_short_ones(h, lens, ahead):
     if lens[-1]:
         bad[-1, :, 2] = True
     assert torch.equal(~torch.isfinite(again), bad) and torch.equal(again[~bad], out[~bad]) and torch.equal(again_lse, lse)
+
+
+def test_calls_in_a_row_share_a_workspace_and_feed_each_other():
+    """Each call begins where the one before it ends: it reads that one's results, and
+    replaces what it left in the workspace."""
+    h, n = 4, 6000
+    q, kv, k_pe = randn(64, h, 192, seed=1), randn(n, h, 256, seed=2), randn(n, 64, seed=3)
+    need = max(B.mla_prefill_workspace_bytes(64, n, 1, h), B.mla_prefill_workspace_bytes(64, n, 2, h))
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def steps(wait):
+        x, outs = q.clone(), []
+        for i in range(6):
+            out, lse = new(64, h, 128), torch.empty(64, h, device="cuda")
+            cq, ck = (cu([64]), cu([n])) if i % 2 else (cu([30, 34]), cu([n - 1000, 1000]))
+            B.mla_prefill(x[..., :128], x[..., 128:], kv[..., :128], k_pe, kv[..., 128:], cq, ck, False, SCALE, out, lse, ws)
+            if wait:
+                torch.cuda.synchronize()
+            x = torch.cat([out, q[..., 128:]], -1) if i % 3 == 2 else x
+            B.mla_merge_states(out, lse, out, lse, x[..., :128], torch.empty_like(lse))
+            if wait:
+                torch.cuda.synchronize()
+            outs += [out, lse]
+        return outs
+
+    want = steps(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(want, steps(False)))
