@@ -1397,13 +1397,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 // ------------------------------------------------------------------ parts
 
 // lse = ln sum_k e^lse_k, out = sum_k e^(lse_k - lse) out_k over the parts of a row; a
-// warp a row, so that all rows' loads are on their way at once, four parts at a time.
-constexpr int kMergeRows = 8;  // of a block
+// warp a row, so that all rows' loads are on their way at once, four parts at a time.  500
+// rows of 16 heads in 4 parts over 20000 keys: 79 us, 73 without the merge.
+constexpr int kMergeRows = 8;  // of a CTA
 template <int kItemRows>
 __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = (int)blockIdx.x / a.tiles;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Item it;
   Walk walk;
   if (!find_block<kItemRows, false>(a, a.batch, (int)blockIdx.x - head * a.tiles, walk, lane, &it)) return;
@@ -1413,6 +1415,13 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args
   const int64_t token = it.q0 + row, at = token * a.heads + head, stride = (int64_t)a.tokens_q * a.heads;
   const float mine = lane < it.parts ? __ldcg(a.part_lse + lane * stride + at) : -CUDART_INF_F;  // at most 32 parts
   const float4* x = reinterpret_cast<const float4*>(a.part_out + at * 128) + lane;
+  float4 v[4];  // the first ones are on their way with the lse
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k0 + k < it.parts) v[k] = __ldcg(x + (k0 + k) * stride * 32);
+  };
+  fetch(0);
   float top = mine;
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -1423,10 +1432,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args
   w = sum == 0.f ? 0.f : w / sum;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k0 = 0; k0 < it.parts; k0 += 4) {
-    float4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k0 + k < it.parts) v[k] = __ldcg(x + (k0 + k) * stride * 32);
+    if (k0 > 0) fetch(k0);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float f = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
@@ -1478,8 +1484,9 @@ static int items_of_a_head(int num_tokens_q, int batch, int item_rows) {
 
 // Parts of a row block's keys, at most: enough to give every CTA an item, of 256 keys or
 // more.  In us, not cut, of 1024, 512 and 256 keys at least: a row over 2000 keys, 16 heads,
-// 26.6, 26.6, 17.8, 16.9; over 16000 165, 36, 36, 36; 16 rows over 2000 keys, 4 heads, 26.4,
-// 26.4, 16.7, 14.1; 300 rows over 20000 keys, 19 heads, 228, 79, 79, 78.  The keys may be
+// 26.6, 26.6, 17.8, 16.9 (16.0 since the merge starts earlier); over 16000 165, 36, 36, 36; 16
+// rows over 2000 keys, 4 heads, 26.4, 26.4, 16.7, 14.1 (13.5); 300 rows over 20000 keys, 19
+// heads, 228, 79, 79, 78.  The keys may be
 // one request's: where few requests give few items they are cut as their lengths ask for
 // (on the device), within 64 MB of results.
 template <int kCtas>
@@ -1558,7 +1565,7 @@ static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t
   cfg.numAttrs = 2;
   const cudaError_t main = cudaLaunchKernelEx(&cfg, kernel, m, a);
   if (main != cudaSuccess || a.parts == 1) return main;
-  cfg.gridDim = dim3((unsigned)(a.tiles * a.heads), F::kItemRows / kMergeRows);
+  cfg.gridDim = dim3((unsigned)(a.tiles * a.heads), (unsigned)((std::min(F::kItemRows, p.num_tokens_q) + kMergeRows - 1) / kMergeRows));
   cfg.blockDim = dim3(32 * kMergeRows);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
