@@ -259,11 +259,13 @@ __device__ __forceinline__ Request walk_on(const Args& a, int batch, Walk& w, in
   if (batch <= 32) {
     const int keys = r.blocks > 0 ? r.k1 - r.k0 : 0;
     if (a.parts > 1) {
-      float load = static_cast<float>(r.blocks) * static_cast<float>(keys);
+      // each operation rounded by itself: both kernels come to the same numbers
+      float load = __fmul_rn(static_cast<float>(r.blocks), static_cast<float>(keys));
 #pragma unroll
-      for (int d = 1; d < 32; d *= 2) load += __shfl_xor_sync(0xffffffffu, load, d);
-      const float share = fmaxf(static_cast<float>(kPartKeys), load * static_cast<float>(a.heads) / static_cast<float>(a.slots));
-      r.parts = max(1, min(a.parts, static_cast<int>(static_cast<float>(keys) / share)));
+      for (int d = 1; d < 32; d *= 2) load = __fadd_rn(load, __shfl_xor_sync(0xffffffffu, load, d));
+      const float even = __fdiv_rn(__fmul_rn(load, static_cast<float>(a.heads)), static_cast<float>(a.slots));
+      const float share = fmaxf(static_cast<float>(kPartKeys), even);
+      r.parts = max(1, min(a.parts, static_cast<int>(__fdiv_rn(static_cast<float>(keys), share))));
     }
     if (kCut) r.blocks *= r.parts;
     all = r.upto = 0;
