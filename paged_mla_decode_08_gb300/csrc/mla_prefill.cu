@@ -104,6 +104,13 @@ struct Form {
 
 constexpr int kPartKeys = 256;  // of a part, at least
 constexpr int kItemSlots = 4;
+// Steps whose values are looked through: an item has at most five (its rows span four
+// steps of keys), and a tile's warps, which may have nothing to do in an item, are at most
+// kItemSlots items ahead of the other tile's.  With a barrier for each of those, the one
+// that a warp comes to is behind in no phase, so a wait for either parity is not passed
+// early.
+constexpr int kLookBars = 32;
+static_assert(kLookBars >= 5 * kItemSlots && kLookBars == 32, "every step in flight has its own; a lane sets one up");
 constexpr int kAskAhead = 4;  // steps before an item's end at which its successor is asked for
 enum Bar : int {
   B_Q = 0,                        // [tile] Q landed (the leader's barrier)
@@ -112,8 +119,8 @@ enum Bar : int {
   B_KE = B_KF + kStages,          // [stage] keys are read
   B_VF = B_KE + kStages,          // [stage] values landed (the leader's); not those to be looked through
   B_VE = B_VF + kStages,          // [stage] values are read
-  B_RAW = B_VE + kStages,         // [look % 3] values to be looked through landed
-  B_S = B_RAW + kStages,          // [tile] scores are in TMEM
+  B_RAW = B_VE + kStages,         // [look % kLookBars] values to be looked through landed
+  B_S = B_RAW + kLookBars,        // [tile] scores are in TMEM
   B_P = B_S + 2,                  // [2 tile + half] weights are in TMEM, O is rescaled (the leader's)
   B_O = B_P + 4,                  // [tile] the tile's products are done
   B_ITEM = B_O + 2,               // [slot] an item is there
@@ -624,7 +631,8 @@ struct Maps {
 template <int kCtas>
 __device__ void load_items(const Ctx<kCtas>& c, const Args& a, const Maps& m, int lane) {
   using F = Form<kCtas>;
-  Ring<kStages> ring, raw;
+  Ring<kStages> ring;
+  Ring<kLookBars> raw;
   uint32_t qe[2] = {1, 1};  // parities of Q's release
   int loaded = 0;           // stages used so far
   bool ok = true;
@@ -1159,7 +1167,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
     const int mine_steps = t ? it.tile_steps[1] : it.tile_steps[0], other_steps = t ? it.tile_steps[0] : it.tile_steps[1];
     const int values = vstep, look0 = looks;
     vstep = (vstep + it.steps) % kStages;
-    looks = (looks + it.steps - it.look) % (2 * kStages);
+    looks = (looks + it.steps - it.look) % (2 * kLookBars);
     if (t == 0 && quad == 0) flag_store(c.sbase + kOffPoison + 4 * ((n + kPoisons / 2) % kPoisons), 0);
     // A tile's steps are every one of the item's, or every second one.
     const int stride = it.alone ? 2 : 1, shift = it.alone ? t : 0;
@@ -1168,7 +1176,7 @@ __device__ void softmax_items(const Ctx<kCtas>& c, const Args& a, int t, uint32_
     auto look = [&](int j) {
       if (j < looker) return true;
       const int k = look0 + j - it.look;
-      if (!c.wait_warp(B_RAW + k % kStages, (k / kStages) & 1, 0xA17)) return false;
+      if (!c.wait_warp(B_RAW + k % kLookBars, (k / kLookBars) & 1, 0xA17)) return false;
       const uint32_t at = c.sbase + kOffRing + (values + j) % kStages * kStageBytes + kKBytes;
       if (look_through<kCtas>(at, quad, lane, it.lk - (it.begin + j) * F::kKeys))
         note_non_finite(c, n);
@@ -1323,6 +1331,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (lane == 0) put_item(c, 0, own);
     }
   } else if (warp == 0) {
+    mbar_init(c.bar(B_RAW + lane), 1);
+    fence_mbar_init();
     if (lane == 0) {
       flag_store(c.sbase + kOffAbort, 0);
       for (int i = 0; i < kPoisons; ++i) flag_store(c.sbase + kOffPoison + 4 * i, 0);
@@ -1339,7 +1349,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         mbar_init(c.bar(B_KE + i), 1);
         mbar_init(c.bar(B_VF + i), kCtas);
         mbar_init(c.bar(B_VE + i), 1);
-        mbar_init(c.bar(B_RAW + i), 1);
       }
       for (int i = 0; i < kItemSlots; ++i) {
         mbar_init(c.bar(B_ITEM + i), 1);
