@@ -246,10 +246,11 @@ __device__ __forceinline__ Request walk_on(const Args& a, int batch, Walk& w, in
   Request r{};
   const int b = w.base + lane;
   if (b < batch) {
-    r.q0 = __ldg(a.cu_q + b);
-    r.q1 = __ldg(a.cu_q + b + 1);
-    r.k0 = __ldg(a.cu_k + b);
-    r.k1 = __ldg(a.cu_k + b + 1);
+    // plain loads: the kernel before may write them while this one is resident
+    r.q0 = a.cu_q[b];
+    r.q1 = a.cu_q[b + 1];
+    r.k0 = a.cu_k[b];
+    r.k1 = a.cu_k[b + 1];
   }
   int before = r.q1;  // the latest end of the requests before this one
 #pragma unroll

@@ -234,11 +234,13 @@ struct GatherArgs {
 
 // A warp copies four rows: it looks them up at once, a lane each (a chain: offsets, block
 // table, row), then has all of them on their way, and their rotary parts and scales in
-// one access for the four.  65536 rows of e4m3: 4 rows a warp 15.9 us, 2 rows 16.8, 8 and 16
-// rows four at a time 18.5 and 19.4 (fewer warps, the chain shows), before the accesses
-// were joined.  65536 rows now, in a loop over more data than L2 holds, by blocks of 128 and
-// 256 threads: bf16 25.8 us and 26.3, bf16 to codes 22.9 and 23.9, e4m3 to bf16 22.0 and 22.4,
-// codes 16.1 and 16.4 (75 to 88% of a measured copy's rate).
+// one access for the four.  Offsets, starts and block table are read by plain loads: the
+// kernel before may write them while this one is resident.  65536 rows of e4m3: 4 rows a
+// warp 15.9 us, 2 rows 16.8, 8 and 16 rows four at a time 18.5 and 19.4 (fewer warps, the
+// chain shows), before the accesses were joined.  65536 rows now, in a loop over more data
+// than L2 holds, by blocks of 128 and 256 threads: bf16 25.8 us and 26.3, bf16 to codes 22.9
+// and 23.9, e4m3 to bf16 22.0 and 22.4, codes 16.1 and 16.4 (75 to 88% of a measured copy's
+// rate).
 constexpr int kGatherRows = 4, kGatherThreads = 128;
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
   uint32_t d;
@@ -264,7 +266,7 @@ __device__ __forceinline__ int owner(const GatherArgs& a, int r, int lane) {
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int at = lo + lane * step;
-    const bool le = lane * step < n && __ldg(a.cu + at) <= r;
+    const bool le = lane * step < n && a.cu[at] <= r;
     const unsigned m = __ballot_sync(0xffffffffu, le);
     const int last = m ? 31 - __clz(m) : 0;
     const int end = min(lo + n, lo + (last + 1) * step);
@@ -317,8 +319,8 @@ __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const Gath
   if (blockIdx.x == 0 && threadIdx.x < 32) {  // the offsets' rules, looked at once
     bool bad = false;
     for (int b = lane; b <= a.batch; b += 32) {
-      const int c = __ldg(a.cu + b);
-      bad |= c < 0 || c > a.tokens || (b > 0 && c < __ldg(a.cu + b - 1));
+      const int c = a.cu[b];
+      bad |= c < 0 || c > a.tokens || (b > 0 && c < a.cu[b - 1]);
     }
     if (bad) record(0x903);
   }
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const Gath
   {
     const int row = (int)row0 + min(lane, kGatherRows - 1);
     int b = owner(a, (int)row0, lane);
-    if (b < a.batch && __ldg(a.cu + b + 1) < row0 + kGatherRows) {  // the rows are not all of one request
+    if (b < a.batch && a.cu[b + 1] < row0 + kGatherRows) {  // the rows are not all of one request
 #pragma unroll 1
       for (int i = 1; i < kGatherRows; ++i) {
         const int other = owner(a, (int)row0 + i, lane);
@@ -336,14 +338,14 @@ __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const Gath
     }
     if (lane < kGatherRows && row < a.tokens) {
       if (b < a.batch) {
-        const int begin = __ldg(a.cu + b);
-        const int64_t token = (a.starts ? (int64_t)__ldg(a.starts + b) : 0) + row - begin;
+        const int begin = a.cu[b];
+        const int64_t token = (a.starts ? (int64_t)a.starts[b] : 0) + row - begin;
         if (row >= begin) {
           const int64_t block = token >> a.page_shift;
           if (token < 0 || block >= a.bt_stride) {
             record(0x901);
           } else {
-            const int64_t page = __ldg(a.block_table + b * a.bt_stride + block);
+            const int64_t page = a.block_table[b * a.bt_stride + block];
             if (page < 0 || page >= a.num_pages)
               record(0x902);
             else
