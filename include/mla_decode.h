@@ -728,9 +728,10 @@ int mla_cache_gather(const void* kv_pages, int kv_dtype, int64_t num_pages, int 
  *   lse           device fp32 [num_tokens_q, num_heads], contiguous.
  *   scale         softmax scale, > 0, itself and 16 / scale finite in fp32
  *                 (1/sqrt(192) for DeepSeek-V3 shapes); scores are held in fp32.
- *   workspace     device scratch of mla_prefill_workspace_bytes (same sizes), 256-byte
- *                 aligned; may be NULL when that is 0.  No initial contents are needed
- *                 and none are kept; calls that overlap on the GPU must not share it.
+ *   workspace     device scratch of mla_prefill_workspace_bytes (of these sizes, or of
+ *                 larger ones), 256-byte aligned; may be NULL when that is 0.  No initial
+ *                 contents are needed and none are kept; calls that overlap on the GPU must
+ *                 not share it.
  * Strides are multiples of 8 elements, at least the width and below 2^39 (the head
  * stride of a single head is not looked at); pointers are 16-byte aligned (offsets and
  * lse 4).
@@ -749,9 +750,23 @@ int mla_prefill(const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_
                 float scale, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse, void* workspace,
                 size_t workspace_bytes, void* stream);
 
-/* Device workspace that mla_prefill needs for these sizes on the current device
- * (0: none).  Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA. */
+/* Device workspace that is enough, on the current device, for every call of mla_prefill
+ * with no more query rows, keys, requests and heads than these (0: none of them needs
+ * any).  A single call may use less, also none where a smaller one uses some: whether and
+ * how its keys are cut goes by all four.  It does not exceed 64 MB, or 129 KB an SM if
+ * that is more.  Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA. */
 int mla_prefill_workspace_bytes(int num_tokens_q, int num_tokens_k, int batch, int num_heads, size_t* bytes_out);
+
+/*
+ * How mla_prefill cuts up a call of these sizes (host only, nothing is launched; used by
+ * tests and tools): query rows of an item (512 on a pair of CTAs, 256 on one), parts
+ * that a row block's keys are cut into at most, heads whose items are mixed, the bytes of
+ * workspace that the call itself needs, and mla_prefill_workspace_bytes.  num_sms 0: on
+ * the current device; else on one of num_sms SMs.
+ * Errors: MLA_ERR_ARG, and for the current device MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
+ */
+int mla_prefill_form(int num_tokens_q, int num_tokens_k, int batch, int num_heads, int num_sms, int* item_rows,
+                     int* parts, int* group_heads, size_t* used_bytes, size_t* workspace_bytes);
 
 /*
  * Merge two partial attention results of the same rows (over disjoint keys):

@@ -77,6 +77,8 @@ SIGNATURES = {
                              _c_int, _c_int, _c_int, _c_int, _c_int, ctypes.c_float, _vp, _i64, _i64, _vp, _vp, _c_size,
                              _vp]),
     "mla_prefill_workspace_bytes": (_c_int, [_c_int, _c_int, _c_int, _c_int, ctypes.POINTER(_c_size)]),
+    "mla_prefill_form": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, ctypes.POINTER(_c_size),
+                                  ctypes.POINTER(_c_size)]),
     "mla_merge_states": (_c_int, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _c_int, _c_int, _c_int, _vp, _i64, _i64, _vp,
                                   _vp]),
     "mla_plan_workspace_bytes": (_c_size, [_vp]),
@@ -448,7 +450,8 @@ def mla_cache_gather(kv_pages, kv_dtype: int, block_table, starts, cu_seqlens, k
 
 
 def mla_prefill_workspace_bytes(num_tokens_q: int, num_tokens_k: int, batch: int, num_heads: int) -> int:
-    """Device workspace that ``mla_prefill`` needs for these sizes (0: none)."""
+    """Device workspace that is enough for every ``mla_prefill`` with no more query rows,
+    keys, requests and heads than these (0: none of them needs any)."""
     need = _c_size()
     _check(load().mla_prefill_workspace_bytes(num_tokens_q, num_tokens_k, batch, num_heads, ctypes.byref(need)))
     return need.value

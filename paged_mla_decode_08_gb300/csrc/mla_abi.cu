@@ -65,7 +65,6 @@ cudaError_t launch_merge_states(HeadRows x, const float* lse_x, HeadRows y, cons
                                 int tokens, int heads, int dim, cudaStream_t stream);
 cudaError_t prompt_rows_read_error(int* code, bool reset);
 cudaError_t launch_prefill(const PrefillCall& p, Device dev, cudaStream_t stream);
-size_t prefill_workspace(int num_tokens_q, int num_tokens_k, int batch, int num_heads, Device dev);
 cudaError_t prefill_read_error(int* code, bool reset);
 }  // namespace mla
 
@@ -871,7 +870,27 @@ int mla_prefill_workspace_bytes(int num_tokens_q, int num_tokens_k, int batch, i
   mla::Device dev{};
   rc = check_device(&dev.sms, &dev.id);
   if (rc != MLA_OK) return rc;
-  *bytes_out = mla::prefill_workspace(num_tokens_q, num_tokens_k, batch, num_heads, dev);
+  *bytes_out = mla::prefill_workspace(num_tokens_q, num_tokens_k, batch, num_heads, dev.sms);
+  return ok();
+}
+
+int mla_prefill_form(int num_tokens_q, int num_tokens_k, int batch, int num_heads, int num_sms, int* item_rows,
+                     int* parts, int* group_heads, size_t* used_bytes, size_t* workspace_bytes) {
+  if (!item_rows || !parts || !group_heads || !used_bytes || !workspace_bytes) return fail(MLA_ERR_ARG, "a result pointer is NULL");
+  int rc = check_prefill_sizes(num_tokens_q, num_tokens_k, batch, num_heads);
+  if (rc != MLA_OK) return rc;
+  if (num_sms < 0 || num_sms > (1 << 16)) return fail(MLA_ERR_ARG, "num_sms must be in [0, 65536]");
+  mla::Device dev{0, num_sms};
+  if (num_sms == 0) {
+    rc = check_device(&dev.sms, &dev.id);
+    if (rc != MLA_OK) return rc;
+  }
+  const mla::PrefillForm f = mla::prefill_form(num_tokens_q, num_tokens_k, batch, num_heads, dev.sms);
+  *item_rows = f.item_rows;
+  *parts = f.parts;
+  *group_heads = f.group;
+  *used_bytes = f.workspace;
+  *workspace_bytes = mla::prefill_workspace(num_tokens_q, num_tokens_k, batch, num_heads, dev.sms);
   return ok();
 }
 
@@ -918,7 +937,7 @@ int mla_prefill(const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_
   mla::Device dev{};
   rc = check_device(&dev.sms, &dev.id);
   if (rc != MLA_OK) return rc;
-  const size_t need = mla::prefill_workspace(num_tokens_q, num_tokens_k, batch, num_heads, dev);
+  const size_t need = mla::prefill_form(num_tokens_q, num_tokens_k, batch, num_heads, dev.sms).workspace;
   if (need > 0) {
     if (!workspace || workspace_bytes < need)
       return fail(MLA_ERR_WORKSPACE, "workspace is smaller than mla_prefill_workspace_bytes");

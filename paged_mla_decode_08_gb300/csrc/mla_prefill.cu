@@ -1494,6 +1494,9 @@ static int items_of_a_head(int num_tokens_q, int batch, int item_rows) {
   return (num_tokens_q - owners) / item_rows + owners;
 }
 
+constexpr int kMostParts = 32;
+constexpr int64_t kPartRowBytes = (128 + 1) * 4, kPartBytes = 64 << 20;
+
 // Parts of a row block's keys, at most: enough to give every CTA an item, of 256 keys or
 // more.  In us, not cut, of 1024, 512 and 256 keys at least: a row over 2000 keys, 16 heads,
 // 26.6, 26.6, 17.8, 16.9 (16.0 since the merge starts earlier); over 16000 165, 36, 36, 36; 16
@@ -1506,10 +1509,10 @@ static int parts_of(int num_tokens_q, int num_tokens_k, int batch, int num_heads
   const int64_t items = std::max<int64_t>(1, (int64_t)items_of_a_head(num_tokens_q, batch, Form<kCtas>::kItemRows) * num_heads);
   int64_t parts = std::min<int64_t>(sms / kCtas / items, num_tokens_k / batch / kPartKeys);
   if (batch > 1 && batch <= 32 && items <= 2 * sms / kCtas) {
-    const int64_t bytes = (int64_t)std::max(1, num_tokens_q) * num_heads * (128 + 1) * 4;
-    parts = std::max(parts, std::min<int64_t>(num_tokens_k / kPartKeys, (64 << 20) / bytes));
+    const int64_t bytes = (int64_t)std::max(1, num_tokens_q) * num_heads * kPartRowBytes;
+    parts = std::max(parts, std::min<int64_t>(num_tokens_k / kPartKeys, kPartBytes / bytes));
   }
-  return (int)std::max<int64_t>(1, std::min<int64_t>(parts, 32));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(parts, kMostParts));
 }
 // Pairs of CTAs, or one CTA an item: by the rows and keys of a request, on average.
 // Measured in us (128 heads; one CTA, pair): 8 requests of 512 rows 131 and 138, 16 of 300
@@ -1524,6 +1527,11 @@ static bool in_pairs(int num_tokens_q, int num_tokens_k, int batch) {
 // prompt of 8192: 24 MB 229 and 1494 us, 32 MB 193 and 1460, 48 MB 194 and 1578; one head
 // after the other 237 and 1598.
 constexpr int64_t kGroupBytes = 32 << 20;
+static int group_of(int num_tokens_k, int batch, int num_heads) {
+  const int64_t bytes = 512 * ((int64_t)std::max(1, num_tokens_k) / batch) * num_heads;
+  const int64_t groups = std::max<int64_t>(1, (bytes + kGroupBytes - 1) / kGroupBytes);
+  return (int)((num_heads + groups - 1) / groups);
+}
 
 // Clusters: one for each item that there can be, but no more than twice those of rows that
 // are all one request's, or eight an SM.  With more items than clusters each takes several.
@@ -1557,8 +1565,7 @@ static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t
   a.tiles = items_of_a_head(p.num_tokens_q, p.batch, F::kItemRows);
   a.slots = dev.sms / kCtas;
   a.parts = parts_of<kCtas>(p.num_tokens_q, p.num_tokens_k, p.batch, p.num_heads, dev.sms);
-  const int64_t groups = std::max<int64_t>(1, (512 * (tk / p.batch) * p.num_heads + kGroupBytes - 1) / kGroupBytes);
-  a.group = (int)((p.num_heads + groups - 1) / groups);
+  a.group = group_of(p.num_tokens_k, p.batch, p.num_heads);
   a.part_out = static_cast<float*>(p.workspace);
   a.part_lse = a.part_out + (int64_t)a.parts * p.num_tokens_q * p.num_heads * 128;
   cudaLaunchConfig_t cfg = {};
@@ -1614,12 +1621,30 @@ int prefill_items(int num_tokens_q, int batch) {
   return prefill::items_of_a_head(num_tokens_q, batch, prefill::Form<1>::kItemRows);
 }
 
-// What the parts of a call write; 0: its keys are not cut.
-size_t prefill_workspace(int num_tokens_q, int num_tokens_k, int batch, int num_heads, Device dev) {
+PrefillForm prefill_form(int num_tokens_q, int num_tokens_k, int batch, int num_heads, int sms) {
   using namespace prefill;
-  const int parts = in_pairs(num_tokens_q, num_tokens_k, batch) ? parts_of<2>(num_tokens_q, num_tokens_k, batch, num_heads, dev.sms)
-                                                  : parts_of<1>(num_tokens_q, num_tokens_k, batch, num_heads, dev.sms);
-  return parts == 1 ? 0 : align256((size_t)parts * num_tokens_q * num_heads * (128 + 1) * 4);
+  const bool pairs = in_pairs(num_tokens_q, num_tokens_k, batch);
+  PrefillForm f;
+  f.item_rows = pairs ? Form<2>::kItemRows : Form<1>::kItemRows;
+  f.parts = pairs ? parts_of<2>(num_tokens_q, num_tokens_k, batch, num_heads, sms)
+                  : parts_of<1>(num_tokens_q, num_tokens_k, batch, num_heads, sms);
+  f.group = group_of(num_tokens_k, batch, num_heads);
+  // what the parts write; 0: the keys are not cut
+  f.workspace = f.parts == 1 ? 0 : align256((size_t)f.parts * num_tokens_q * num_heads * kPartRowBytes);
+  return f;
+}
+
+// Enough for every call of up to these sizes (one call's need does not grow with each of
+// them): no call has more parts than kMostParts or the pieces of kPartKeys in all keys, and
+// parts that are there to occupy the SMs write no more than their rows at a time, parts of
+// uneven requests no more than kPartBytes.
+size_t prefill_workspace(int num_tokens_q, int num_tokens_k, int batch, int num_heads, int sms) {
+  using namespace prefill;
+  const int64_t parts = std::min(kMostParts, num_tokens_k / kPartKeys);
+  if (parts < 2) return 0;
+  const int64_t busy = (int64_t)sms * Form<1>::kItemRows * kPartRowBytes;
+  const int64_t most = batch > 1 ? std::max(busy, kPartBytes) : busy;
+  return align256((size_t)std::min(parts * num_tokens_q * num_heads * kPartRowBytes, most));
 }
 
 cudaError_t prefill_read_error(int* code, bool reset) {

@@ -25,4 +25,14 @@ struct PrefillCall {
 };
 int prefill_items(int num_tokens_q, int batch);
 
+// How a call is cut up.
+struct PrefillForm {
+  int item_rows;  // query rows of an item: 512 on a pair of CTAs, 256 on one
+  int parts;      // of a row block's keys, at most
+  int group;      // heads whose items are mixed
+  size_t workspace;
+};
+PrefillForm prefill_form(int num_tokens_q, int num_tokens_k, int batch, int num_heads, int sms);
+size_t prefill_workspace(int num_tokens_q, int num_tokens_k, int batch, int num_heads, int sms);
+
 }  // namespace mla
