@@ -629,7 +629,8 @@ int mla_gemm_fp8_form(int num_tokens, int n, int k, int num_experts, int grouped
  *                    d(beta) = rotary_dim * ln(original_max_position / (2 pi beta)) / (2 ln base):
  *                    pairs that turn more than beta_fast times within the original
  *                    context keep their frequency, those that turn less than
- *                    beta_slow times are stretched.
+ *                    beta_slow times are stretched (where lo < hi; contexts so short or
+ *                    bases so small that it is not go by the formula as it stands).
  * Frequencies are computed in double precision (2^-52 of w_i) and angles reduced in
  * whole numbers, to 2^-31 of a turn: far positions lose no more than those two, beside
  * the error of one fp32 sine, cosine and product.
@@ -637,7 +638,8 @@ int mla_gemm_fp8_form(int num_tokens, int n, int k, int num_experts, int grouped
  *   table           device fp32 [num_positions, rotary_dim], contiguous.
  *   first_position  >= 0, first_position + num_positions <= 2^31.
  *   rotary_dim      even, 2 .. MLA_ROPE_MAX_DIM.
- *   base            finite, > 1.  factor: finite, > 0 (unused with PLAIN).
+ *   base            finite, > 1.  factor: finite, > 0 (unused with PLAIN), and no frequency
+ *                   overflows by it.
  *   original_max_position >= 1, beta_fast > beta_slow > 0, finite (YARN only).
  *   magnitude       finite.
  * Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.

@@ -752,9 +752,6 @@ int mla_rope_table(float* table, int64_t first_position, int64_t num_positions, 
   if (num_positions * half > (int64_t)INT32_MAX * 256) return fail(MLA_ERR_ARG, "too many positions for one launch");
   if (num_positions == 0) return ok();
   if (!table || !aligned(table, 4)) return fail(MLA_ERR_ARG, "table must be a device pointer aligned to its elements");
-  mla::Device dev{};
-  int rc = check_device(&dev.sms, &dev.id);
-  if (rc != MLA_OK) return rc;
   const double two_pi = 6.283185307179586476925;
   double lo = 0.0, hi = 0.0;
   if (scaling == MLA_ROPE_YARN) {
@@ -774,8 +771,12 @@ int mla_rope_table(float* table, int64_t first_position, int64_t num_positions, 
       w = w / factor * g + w * (1.0 - g);
     }
     const double t = w / two_pi;  // turns of a position; whole ones do not matter
+    if (!std::isfinite(t)) return fail(MLA_ERR_ARG, "factor is so small that a frequency is not finite");
     turns[i] = static_cast<uint64_t>(std::ldexp(t - std::floor(t), 64));
   }
+  mla::Device dev{};
+  int rc = check_device(&dev.sms, &dev.id);
+  if (rc != MLA_OK) return rc;
   cudaError_t e = mla::launch_rope_table(table, first_position, num_positions, half, turns, (float)magnitude, dev,
                                          static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, std::string("rope table launch: ") + cudaGetErrorString(e));
