@@ -1,5 +1,8 @@
 """Expanded attention where a CTA takes many items whose tiles are uneven: rows that
-see no key, requests of one step among longer ones, requests without a row between."""
+see no key, requests of one step among longer ones, requests without a row between;
+heads in groups; more items than clusters."""
+
+import ctypes
 
 import numpy as np
 import pytest
@@ -20,7 +23,7 @@ def no_device_error():
 
 
 def randn(*shape, seed=0):
-    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(BF).cuda()
+    return torch.randn(*shape, generator=torch.Generator("cuda").manual_seed(seed), device="cuda").to(BF)
 
 
 def cu(lens):
@@ -97,6 +100,7 @@ def test_tiles_that_run_ahead(name):
     CTA is at: the results keep their bits, run after run."""
     h, q_lens, k_lens = UNEVEN[name]
     c = Call(h, *between(q_lens, k_lens, 70), True)
+    assert (form(c)[0] == 512) == (name == "in pairs")
     clean = c.run()
     c.check(*clean, heads=[0, h // 2, h - 1])
     ends = c.ck.tolist()
@@ -106,3 +110,47 @@ def test_tiles_that_run_ahead(name):
     for _ in range(20):
         again = c.run()
         assert torch.equal(again[0], clean[0]) and torch.equal(again[1], clean[1])
+
+
+def form(c):
+    out = [ctypes.c_int() for _ in range(3)] + [ctypes.c_size_t() for _ in range(2)]
+    assert B.load().mla_prefill_form(c.tq, c.tk, len(c.q_lens), c.h, 0, *map(ctypes.byref, out)) == B.MLA_OK
+    return [x.value for x in out[:3]]
+
+
+def blocks(lens, item_rows):
+    return sum(-(-n // item_rows) for n in lens)
+
+
+GROUPS = [  # heads, rows, keys, item rows, whether the keys are cut
+    (19, [1000], [8192], 512, True), (19, [100], [8192], 256, True), (37, [3000], [3000], 512, False),
+    (71, [60, 90, 256, 31], [4000, 4100, 256, 9000], 256, False), (151, [40] * 40, [1500, 600] * 20, 256, False),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("h, q_lens, k_lens, item_rows, cut", GROUPS)
+def test_heads_in_groups(h, q_lens, k_lens, item_rows, cut, causal):
+    """Heads whose number their group's does not divide, in both forms, in parts and
+    with more requests than a warp has lanes."""
+    c = Call(h, q_lens, k_lens, causal)
+    rows, parts, group = form(c)
+    assert rows == item_rows and (parts > 1) == cut and group < h and h % group
+    c.check(*c.run(), heads=sorted({0, group - 1, group, h - 1}))
+
+
+def test_pairs_of_more_requests_than_lanes():
+    c = Call(3, [140] * 40, [700 + 5 * i for i in range(40)], True)
+    assert form(c)[0] == 512
+    c.check(*c.run())
+
+
+def test_pairs_with_more_items_than_clusters():
+    """Clusters go on by their number before they ask for another's items."""
+    rng = np.random.default_rng(5)
+    q_lens = np.where(rng.random(170) < 0.1, 0, rng.integers(140, 230, 170))
+    c = Call(8, q_lens, rng.integers(610, 760, 170), True)
+    rows, parts, _ = form(c)
+    clusters = max(2 * -(-c.tq // rows) * c.h * parts, 8 * torch.cuda.get_device_properties(0).multi_processor_count // 2)
+    assert rows == 512 and blocks(c.q_lens, rows) * c.h > clusters
+    c.check(*c.run(), heads=[0, 5, 7])
