@@ -1,5 +1,6 @@
 """What the prompt's operators read may be results of the kernel before, which can still
-run while they are resident: offsets, first tokens and block tables among them."""
+run while they are resident: offsets, first tokens and block tables among them.  The
+combine stands to the main kernel, whose partials it reads, in the same way."""
 
 import os
 import re
@@ -15,7 +16,7 @@ BF = torch.bfloat16
 SCALE = 1 / np.sqrt(192)
 
 
-@pytest.mark.parametrize("source", ["mla_prefill.cu", "mla_prompt_rows.cu"])
+@pytest.mark.parametrize("source", ["mla_prefill.cu", "mla_prompt_rows.cu", "mla_combine.cu"])
 def test_no_read_only_loads(source):
     """They promise that nobody writes the data in the kernel's lifetime, which begins
     before the kernel before it has ended."""
