@@ -1410,8 +1410,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
 // lse = ln sum_k e^lse_k, out = sum_k e^(lse_k - lse) out_k over the parts of a row; a
 // warp a row, so that all rows' loads are on their way at once, four parts at a time.  500
-// rows of 16 heads in 4 parts over 20000 keys: 79 us, 73 without the merge.
-constexpr int kMergeRows = 8;  // of a CTA
+// rows of 16 heads in 4 parts over 20000 keys: 79 us, 73 without the merge.  No more CTAs
+// than the SMs hold, for each looks its rows' request up, which takes longer than a row
+// (130 rows each of 4 requests over 130 keys, 16 heads, none in parts: 17.8 us with a CTA
+// for every 8 rows that there can be, 13.9 so, 9.1 without the launch; a long request
+// among those of 64 rows, 32 heads, 49.1 and 43.5).
+constexpr int kMergeRows = 8;  // of a CTA at a time
+constexpr int kMergeCtas = 8;  // of an SM
 template <int kItemRows>
 __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1422,42 +1427,43 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args
   Walk walk;
   if (!find_block<kItemRows, false>(a, a.batch, (int)blockIdx.x - head * a.tiles, walk, lane, &it)) return;
   if (it.parts == 1) return;  // its results are there
-  const int row = it.row0 + (int)blockIdx.y * kMergeRows + warp;
-  if (row >= it.end) return;
-  const int64_t token = it.q0 + row, at = token * a.heads + head, stride = (int64_t)a.tokens_q * a.heads;
-  const float mine = lane < it.parts ? __ldcg(a.part_lse + lane * stride + at) : -CUDART_INF_F;  // at most 32 parts
-  const float4* x = reinterpret_cast<const float4*>(a.part_out + at * 128) + lane;
-  float4 v[4];  // the first ones are on their way with the lse
-  auto fetch = [&](int k0) {
+  for (int row = it.row0 + (int)blockIdx.y * kMergeRows + warp; row < it.end; row += (int)gridDim.y * kMergeRows) {
+    const int64_t token = it.q0 + row, at = token * a.heads + head, stride = (int64_t)a.tokens_q * a.heads;
+    const float mine = lane < it.parts ? __ldcg(a.part_lse + lane * stride + at) : -CUDART_INF_F;  // at most 32 parts
+    const float4* x = reinterpret_cast<const float4*>(a.part_out + at * 128) + lane;
+    float4 v[4];  // the first ones are on their way with the lse
+    auto fetch = [&](int k0) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k0 + k < it.parts) v[k] = __ldcg(x + (k0 + k) * stride * 32);
-  };
-  fetch(0);
-  float top = mine;
+      for (int k = 0; k < 4; ++k)
+        if (k0 + k < it.parts) v[k] = __ldcg(x + (k0 + k) * stride * 32);
+    };
+    fetch(0);
+    float top = mine;
 #pragma unroll
-  for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  const float base = top == -CUDART_INF_F ? 0.f : top;
-  float w = expf(mine - base), sum = w;
+    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float base = top == -CUDART_INF_F ? 0.f : top;
+    float w = expf(mine - base), sum = w;
 #pragma unroll
-  for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  w = sum == 0.f ? 0.f : w / sum;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < it.parts; k0 += 4) {
-    if (k0 > 0) fetch(k0);
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    w = sum == 0.f ? 0.f : w / sum;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < it.parts; k0 += 4) {
+      if (k0 > 0) fetch(k0);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float f = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
-      const float l = __shfl_sync(0xffffffffu, mine, (k0 + k) & 31);
-      if (l == -CUDART_INF_F) continue;  // it has not been written
-      o.x += f * v[k].x;
-      o.y += f * v[k].y;
-      o.z += f * v[k].z;
-      o.w += f * v[k].w;
+      for (int k = 0; k < 4; ++k) {
+        const float f = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+        const float l = __shfl_sync(0xffffffffu, mine, (k0 + k) & 31);
+        if (l == -CUDART_INF_F) continue;  // it has not been written
+        o.x += f * v[k].x;
+        o.y += f * v[k].y;
+        o.z += f * v[k].z;
+        o.w += f * v[k].w;
+      }
     }
+    uint16_t* out = a.out + token * a.out_ts + head * a.out_hs + 4 * lane;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack(o.x, o.y), pack(o.z, o.w));
+    if (lane == 0) a.lse[at] = sum == 0.f ? -CUDART_INF_F : base + logf(sum);
   }
-  *reinterpret_cast<uint2*>(a.out + token * a.out_ts + head * a.out_hs + 4 * lane) = make_uint2(pack(o.x, o.y), pack(o.z, o.w));
-  if (lane == 0) a.lse[at] = sum == 0.f ? -CUDART_INF_F : base + logf(sum);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1501,14 +1507,17 @@ constexpr int64_t kPartRowBytes = (128 + 1) * 4, kPartBytes = 64 << 20;
 // more.  In us, not cut, of 1024, 512 and 256 keys at least: a row over 2000 keys, 16 heads,
 // 26.6, 26.6, 17.8, 16.9 (16.0 since the merge starts earlier); over 16000 165, 36, 36, 36; 16
 // rows over 2000 keys, 4 heads, 26.4, 26.4, 16.7, 14.1 (13.5); 300 rows over 20000 keys, 19
-// heads, 228, 79, 79, 78.  The keys may be
-// one request's: where few requests give few items they are cut as their lengths ask for
-// (on the device), within 64 MB of results.
+// heads, 228, 79, 79, 78.
+// The keys may be one request's: where few requests give few items they are cut as their
+// lengths ask for (on the device), within 64 MB of results, from kUnevenKeys on.  Even
+// requests pay 5 us for a merge of nothing; one that has nearly all of 1000 keys gains 2
+// (8 of a row, 16 heads, 17.8 to 15.5), of 1700 5 (4 of 64 rows, 21.0 to 15.9), of 4200 13.
+constexpr int kUnevenKeys = 6 * kPartKeys;
 template <int kCtas>
 static int parts_of(int num_tokens_q, int num_tokens_k, int batch, int num_heads, int sms) {
   const int64_t items = std::max<int64_t>(1, (int64_t)items_of_a_head(num_tokens_q, batch, Form<kCtas>::kItemRows) * num_heads);
   int64_t parts = std::min<int64_t>(sms / kCtas / items, num_tokens_k / batch / kPartKeys);
-  if (batch > 1 && batch <= 32 && items <= 2 * sms / kCtas) {
+  if (batch > 1 && batch <= 32 && items <= 2 * sms / kCtas && num_tokens_k >= kUnevenKeys) {
     const int64_t bytes = (int64_t)std::max(1, num_tokens_q) * num_heads * kPartRowBytes;
     parts = std::max(parts, std::min<int64_t>(num_tokens_k / kPartKeys, kPartBytes / bytes));
   }
@@ -1584,7 +1593,8 @@ static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t
   cfg.numAttrs = 2;
   const cudaError_t main = cudaLaunchKernelEx(&cfg, kernel, m, a);
   if (main != cudaSuccess || a.parts == 1) return main;
-  cfg.gridDim = dim3((unsigned)(a.tiles * a.heads), (unsigned)((std::min(F::kItemRows, p.num_tokens_q) + kMergeRows - 1) / kMergeRows));
+  const int row_blocks = a.tiles * a.heads, row_groups = (std::min(F::kItemRows, p.num_tokens_q) + kMergeRows - 1) / kMergeRows;
+  cfg.gridDim = dim3((unsigned)row_blocks, (unsigned)std::min(row_groups, std::max(1, kMergeCtas * dev.sms / row_blocks)));
   cfg.blockDim = dim3(32 * kMergeRows);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;

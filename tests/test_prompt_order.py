@@ -154,3 +154,22 @@ def test_pairs_with_more_items_than_clusters():
     clusters = max(2 * -(-c.tq // rows) * c.h * parts, 8 * torch.cuda.get_device_properties(0).multi_processor_count // 2)
     assert rows == 512 and blocks(c.q_lens, rows) * c.h > clusters
     c.check(*c.run(), heads=[0, 5, 7])
+
+
+@pytest.mark.parametrize("h, q_lens, k_lens, item_rows", [
+    (16, [120] * 4, [130, 4000, 130, 140], 256), (16, [200] * 4, [6000, 700, 300, 1000], 512), (50, [1, 255, 2, 100], [3000, 300, 1, 90], 256)])
+def test_parts_of_more_rows_than_the_merge_takes_at_once(h, q_lens, k_lens, item_rows):
+    """Its CTAs go on to their block's next rows; requests that are not cut lie between."""
+    c = Call(h, q_lens, k_lens, True)
+    rows, parts, _ = form(c)
+    groups, at_once = rows // 8, 8 * torch.cuda.get_device_properties(0).multi_processor_count
+    assert rows == item_rows and parts > 1 and blocks(q_lens, rows) * h * groups > at_once
+    out, lse = c.run()
+    c.check(out, lse, heads=[0, 1, h - 1])
+    assert all(torch.equal(a, b) for a, b in zip(c.run(), (out, lse)))
+
+
+def test_few_keys_are_not_cut_for_one_request_alone():
+    """Even requests of few keys have no second launch."""
+    assert form(Call(16, [130] * 4, [130] * 4, True))[1] == 1
+    assert form(Call(16, [130] * 4, [130, 1200, 130, 130], True))[1] > 1
