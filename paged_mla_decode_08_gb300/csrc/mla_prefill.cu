@@ -1527,7 +1527,9 @@ static int parts_of(int num_tokens_q, int num_tokens_k, int batch, int num_heads
 // Measured in us (128 heads; one CTA, pair): 8 requests of 512 rows 131 and 138, 16 of 300
 // rows 178 and 208, one of 1024 rows 57 and 57, of 1537 116 and 111, of 2048 163 and 137; with
 // a prefix, 8 of 200 rows and 1000 keys 150 and 145, one of 512 and 2800 112 and 85; 16 of
-// 64 rows and 1000 keys 200 and 262 (half of a pair has no row of 128 or fewer).
+// 64 rows and 1000 keys 200 and 262 (half of a pair has no row of 128 or fewer).  The host
+// knows the totals alone, so a prompt among empty or short requests is taken for short ones:
+// 8192 rows alone 1600, padded to 64 requests 2190; 4 of 2048 531, padded to 64 628.
 static bool in_pairs(int num_tokens_q, int num_tokens_k, int batch) {
   return num_tokens_q / batch > kRows && num_tokens_k / batch > 600;
 }
@@ -1545,8 +1547,8 @@ static int group_of(int num_tokens_k, int batch, int num_heads) {
 // Clusters: one for each item that there can be, but no more than twice those of rows that
 // are all one request's, or eight an SM.  With more items than clusters each takes several.
 // (A batch padded with empty requests would else start many for nothing: 2048 rows of 4
-// requests among 512, 128 heads, took 2166 us, now 83 to 87, as a batch of 4 takes 79.  Two an
-// SM left 4 requests of 64 rows over 1000 to 4000 keys at 149 us, eight 138.)
+// requests among 512, 128 heads, took 2166 us, now 82; as a batch of 4, in the same form, they
+// take 71.  Two an SM left 4 requests of 64 rows over 1000 to 4000 keys at 149 us, eight 138.)
 template <int kCtas>
 static int64_t clusters_of(const PrefillCall& p, const Args& a, int sms) {
   const int64_t full = ((int64_t)p.num_tokens_q + Form<kCtas>::kItemRows - 1) / Form<kCtas>::kItemRows * a.heads * a.parts;

@@ -73,7 +73,7 @@ __device__ __forceinline__ void cos_sin(uint32_t turn, float magnitude, float* c
 
 // kWide: four pairs a thread and row (half % 4 == 0, 16-byte rows); else one.  kRows: rows
 // of a thread, four where that fills the GPU (163840 positions: 1 row 12.5 us, 4 rows 7.3;
-// 4096: 3.7 and 3.9).
+// 4096, in a graph: 1.5 and 1.9).
 template <bool kWide, int kRows>
 __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_constant__ TableArgs a) {
   grid_dependency();
@@ -237,10 +237,10 @@ struct GatherArgs {
 // one access for the four.  Offsets, starts and block table are read by plain loads: the
 // kernel before may write them while this one is resident.  65536 rows of e4m3: 4 rows a
 // warp 15.9 us, 2 rows 16.8, 8 and 16 rows four at a time 18.5 and 19.4 (fewer warps, the
-// chain shows), before the accesses were joined.  65536 rows now, in a loop over more data
-// than L2 holds, by blocks of 128 and 256 threads: bf16 25.8 us and 26.3, bf16 to codes 22.9
-// and 23.9, e4m3 to bf16 22.0 and 22.4, codes 16.1 and 16.4 (75 to 88% of a measured copy's
-// rate).
+// chain shows), before the accesses were joined.  Now, in a graph, by blocks of 128 and 256
+// threads: 65536 rows over more data than L2 holds, bf16 25.9 us and 26.8, bf16 to codes 22.5
+// and 23.3, codes 15.6 and 15.7 (77 to 88% of a measured copy's rate; e4m3 to bf16 21.6);
+// 300 rows 2.5 and 3.1.
 constexpr int kGatherRows = 4, kGatherThreads = 128;
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
   uint32_t d;
@@ -432,7 +432,7 @@ struct MergeArgs {
 
 // A thread merges 8 columns of a row; a block owns whole rows, whose old lse every
 // thread reads before the new one is written (they may be the same array).  Bound by
-// its bytes: 8192 rows of 128 heads and 128 columns, 818 MB, 129 us (95% of a
+// its bytes: 8192 rows of 128 heads and 128 columns, 818 MB, 125 us (98% of a
 // measured copy's rate).
 __global__ void __launch_bounds__(kThreads) merge_kernel(const MergeArgs m) {
   grid_dependency();
