@@ -1410,14 +1410,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
 // lse = ln sum_k e^lse_k, out = sum_k e^(lse_k - lse) out_k over the parts of a row; a
 // warp a row, so that all rows' loads are on their way at once, four parts at a time.  500
-// rows of 16 heads in 4 parts over 20000 keys: 79 us, 73 without the merge.  No more CTAs
-// than the SMs hold, for each looks its rows' request up, which takes longer than a row
-// (130 rows each of 4 requests over 130 keys, 16 heads, none in parts: 17.8 us with a CTA
-// for every 8 rows that there can be, 13.9 so, 9.1 without the launch; a long request
-// among those of 64 rows, 32 heads, 49.1 and 43.5).
+// rows of 16 heads in 4 parts over 20000 keys: 79 us, 73 without the merge.  No more than
+// eight CTAs an SM, which go on to further rows (kOn) where there can be more: each looks
+// its rows' request up, which takes longer than a row (130 rows each of 4 requests over 130
+// keys, 16 heads, none in parts: 17.8 us with a CTA for every 8 rows that there can be, 13.9
+// so, 9.1 without the launch; a long request among those of 64 rows, 32 heads, 49.1 and
+// 43.5).  Without the loop where it is not needed: 300 rows of 19 heads over 20000 keys 77.2,
+// with it 78.2; 16 rows of 4 heads over 2000 11.9 and 12.1.
 constexpr int kMergeRows = 8;  // of a CTA at a time
 constexpr int kMergeCtas = 8;  // of an SM
-template <int kItemRows>
+template <int kItemRows, bool kOn>
 __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = (int)blockIdx.x / a.tiles;
@@ -1427,7 +1429,9 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args
   Walk walk;
   if (!find_block<kItemRows, false>(a, a.batch, (int)blockIdx.x - head * a.tiles, walk, lane, &it)) return;
   if (it.parts == 1) return;  // its results are there
-  for (int row = it.row0 + (int)blockIdx.y * kMergeRows + warp; row < it.end; row += (int)gridDim.y * kMergeRows) {
+  int row = it.row0 + (int)blockIdx.y * kMergeRows + warp;
+  if (row >= it.end) return;
+  do {
     const int64_t token = it.q0 + row, at = token * a.heads + head, stride = (int64_t)a.tokens_q * a.heads;
     const float mine = lane < it.parts ? __ldcg(a.part_lse + lane * stride + at) : -CUDART_INF_F;  // at most 32 parts
     const float4* x = reinterpret_cast<const float4*>(a.part_out + at * 128) + lane;
@@ -1463,7 +1467,8 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_parts_kernel(const Args
     uint16_t* out = a.out + token * a.out_ts + head * a.out_hs + 4 * lane;
     *reinterpret_cast<uint2*>(out) = make_uint2(pack(o.x, o.y), pack(o.z, o.w));
     if (lane == 0) a.lse[at] = sum == 0.f ? -CUDART_INF_F : base + logf(sum);
-  }
+    row += (int)gridDim.y * kMergeRows;
+  } while (kOn && row < it.end);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1596,11 +1601,13 @@ static cudaError_t launch(const PrefillCall& p, Args a, Device dev, cudaStream_t
   const cudaError_t main = cudaLaunchKernelEx(&cfg, kernel, m, a);
   if (main != cudaSuccess || a.parts == 1) return main;
   const int row_blocks = a.tiles * a.heads, row_groups = (std::min(F::kItemRows, p.num_tokens_q) + kMergeRows - 1) / kMergeRows;
-  cfg.gridDim = dim3((unsigned)row_blocks, (unsigned)std::min(row_groups, std::max(1, kMergeCtas * dev.sms / row_blocks)));
+  const int at_once = std::min(row_groups, std::max(1, kMergeCtas * dev.sms / row_blocks));
+  cfg.gridDim = dim3((unsigned)row_blocks, (unsigned)at_once);
   cfg.blockDim = dim3(32 * kMergeRows);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_parts_kernel<F::kItemRows>, a);
+  if (at_once < row_groups) return cudaLaunchKernelEx(&cfg, merge_parts_kernel<F::kItemRows, true>, a);
+  return cudaLaunchKernelEx(&cfg, merge_parts_kernel<F::kItemRows, false>, a);
 }
 
 }  // namespace prefill
